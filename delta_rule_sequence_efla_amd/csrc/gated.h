@@ -1,0 +1,43 @@
+// gated.h -- what the kernels of the gated delta rule share.
+//
+// The recurrence (per value head; a from beta and lambda = ||k||^2 under either
+// rule, common.h; g the log-decay):
+//     S_t = e^{g_t} (I - a_t k_t k_t^T) S_{t-1} + a_t k_t v_t^T,   o_t = S_t^T q_t.
+// With u_t = a_t (v_t - e^{g_t} S_{t-1}^T k_t) it is S_t = e^{g_t} S_{t-1} + k_t u_t^T.
+// Over a chunk with G_i = g_1 + .. + g_i and Gam_ij = e^{G_i - G_j} (i >= j, so
+// no exponent of a decaying gate is positive):
+//     A  = tril(diag(a) (Gam * K K^T), -1),   T = (I + A)^{-1} diag(a)
+//     U  = T (V - diag(e^G) K S)
+//     O  = diag(e^G) Q S + (Gam * tril(Q K^T)) U
+//     S <- e^{G_C} S + K^T diag(e^{G_C - G_j}) U
+// Query and key heads may be fewer than value heads: value head h reads query
+// and key head h / (H / Hk).
+#pragma once
+
+#include "common.h"
+
+namespace efla {
+
+// Log-decays below -128 act as -128: e^{-128} is zero in fp32 already, and
+// sums of a chunk's gates stay finite (G_i - G_j of two infinities would be
+// NaN), so g = -inf resets the state.  NaN passes through.
+__device__ __forceinline__ float gate_floor(float g) { return g < -128.0f ? -128.0f : g; }
+
+// Sum over the 16 lanes of a DPP row, in every lane.
+__device__ __forceinline__ float row_sum16(float s) {
+  s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x128, 0xF, 0xF, false));
+  s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x124, 0xF, 0xF, false));
+  s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x122, 0xF, 0xF, false));
+  s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x121, 0xF, 0xF, false));
+  return s;
+}
+
+// State a sequence starts from and ends in: row `seq` of the state tensor, or
+// row slots[seq] of a pool of P states; -1 (no row) for an entry outside it.
+__device__ __forceinline__ int64_t state_row(const int32_t* __restrict__ slots, int seq, int P) {
+  if (slots == nullptr) return seq;
+  const int s = slots[seq];
+  return s >= 0 && s < P ? s : -1;
+}
+
+}  // namespace efla

@@ -1,0 +1,147 @@
+// gated_api.hip -- the C entry points of the gated delta rule and of the plan
+// of a packed batch (include/efla.h): validation, workspace sizing, launches on
+// the caller's stream.  Nothing here allocates device memory or synchronizes.
+#include "checks.h"
+#include "launchers.h"
+
+namespace {
+
+// Shapes of a gated call over `units` sequences of `L` tokens.
+efla_status check_gated_shape(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk, efla_dtype dt,
+                              efla_rule rule) {
+  if (!valid_rule(rule) || Hk < 1) return EFLA_ERR_INVALID_ARG;
+  const efla_status st = check_chunk_shape(B, H, L, d_k, d_v, chunk, dt);
+  if (st != EFLA_OK) return st;
+  return H % Hk == 0 ? EFLA_OK : EFLA_ERR_INVALID_ARG;
+}
+
+template <typename F>
+efla_status by_type(efla_dtype dt, F&& f) {
+  return from_hip(dt == EFLA_BF16 ? f(uint16_t{}) : f(float{}));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t efla_gated_chunk_fwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
+                                           efla_dtype dtype) {
+  if (check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK) return 0;
+  return 0;
+}
+
+efla_status efla_gated_chunk_fwd(const void* q, const void* k, const void* v, const void* beta, const float* g,
+                                 const float* s0, void* o, float* s_final, int B, int H, int Hk, int64_t L, int d_k,
+                                 int d_v, int chunk, efla_dtype dtype, efla_rule rule, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  const efla_status st = check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, rule);
+  if (st != EFLA_OK) return st;
+  if (L > 0) {
+    if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || o == nullptr)
+      return EFLA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return EFLA_ERR_INVALID_ARG;
+  }
+  const size_t need = efla_gated_chunk_fwd_workspace_size(B, H, Hk, L, d_k, d_v, chunk, dtype);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
+  if (L == 0 && s_final == nullptr) return EFLA_OK;
+  const efla::GatedFwd a{q,       k,       v,       beta, g, s0, o,  s_final, nullptr,   nullptr,
+                         nullptr, B,       0,       B,    H, Hk, d_k, d_v,     int(rule), L};
+  return by_type(dtype, [&](auto t) {
+    return efla::launch_gated_recurrent<decltype(t)>(a, nullptr, chunk, static_cast<hipStream_t>(stream));
+  });
+}
+
+size_t efla_gated_chunk_fwd_varlen_workspace_size(int N, int H, int Hk, int64_t T, int d_k, int d_v, int chunk,
+                                                  efla_dtype dtype) {
+  if (check_gated_shape(N, H, Hk, T, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK) return 0;
+  return 0;
+}
+
+efla_status efla_gated_chunk_fwd_varlen(const void* q, const void* k, const void* v, const void* beta, const float* g,
+                                        const int32_t* cu_seqlens, const int32_t* slots, const int32_t* order, int N,
+                                        int P, const float* s0, void* o, float* s_final, int H, int Hk, int64_t T,
+                                        int d_k, int d_v, int chunk, efla_dtype dtype, efla_rule rule,
+                                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (N < 0 || P < 0 || T > INT32_MAX) return EFLA_ERR_INVALID_ARG;
+  const efla_status st = check_gated_shape(N < 1 ? 1 : N, H, Hk, T, d_k, d_v, chunk, dtype, rule);
+  if (st != EFLA_OK) return st;
+  if (slots == nullptr && P < N) return EFLA_ERR_INVALID_ARG;
+  if (N == 0) return EFLA_OK;
+  if (int64_t(H) * (T / chunk + N) > kMaxGrid) return EFLA_ERR_UNSUPPORTED;
+  if (cu_seqlens == nullptr) return EFLA_ERR_INVALID_ARG;
+  if (T > 0) {
+    if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || o == nullptr)
+      return EFLA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o)) return EFLA_ERR_INVALID_ARG;
+  }
+  const size_t need = efla_gated_chunk_fwd_varlen_workspace_size(N, H, Hk, T, d_k, d_v, chunk, dtype);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
+  if (T == 0 && s_final == nullptr) return EFLA_OK;
+  const efla::GatedFwd a{q,     k, v, beta, g, s0, o,   s_final, cu_seqlens, slots,
+                         order, 0, N, P,    H, Hk, d_k, d_v,     int(rule),  T};
+  return by_type(dtype, [&](auto t) {
+    return efla::launch_gated_recurrent<decltype(t)>(a, nullptr, chunk, static_cast<hipStream_t>(stream));
+  });
+}
+
+size_t efla_gated_chunk_bwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
+                                           efla_dtype dtype) {
+  if (check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || L == 0) return 0;
+  return efla::gated_bwd_workspace(B, H, Hk, L, d_k, d_v, chunk, elem_bytes(dtype));
+}
+
+efla_status efla_gated_chunk_bwd(const void* q, const void* k, const void* v, const void* beta, const float* g,
+                                 const float* s0, const void* d_o, const float* ds_final, void* dq, void* dk, void* dv,
+                                 void* dbeta, void* dg, float* ds0, int B, int H, int Hk, int64_t L, int d_k, int d_v,
+                                 int chunk, efla_dtype dtype, efla_rule rule, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  const efla_status st = check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, rule);
+  if (st != EFLA_OK) return st;
+  if (L == 0 && ds0 == nullptr) return EFLA_OK;
+  if (L > 0) {
+    if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || d_o == nullptr ||
+        dq == nullptr || dk == nullptr || dv == nullptr || dbeta == nullptr || dg == nullptr)
+      return EFLA_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(d_o) || !aligned16(dq) || !aligned16(dk) ||
+        !aligned16(dv))
+      return EFLA_ERR_INVALID_ARG;
+    const size_t need = efla_gated_chunk_bwd_workspace_size(B, H, Hk, L, d_k, d_v, chunk, dtype);
+    if (workspace == nullptr || workspace_bytes < need) return EFLA_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
+  }
+  const efla::GatedBwd b{q, k, v, beta, d_o, g, s0, ds_final, dq, dk, dv, dbeta, dg, ds0, B, H, Hk, d_k, d_v,
+                         int(rule), L};
+  return by_type(dtype, [&](auto t) {
+    return efla::launch_gated_bwd<decltype(t)>(b, chunk, workspace, static_cast<hipStream_t>(stream));
+  });
+}
+
+efla_status efla_gated_step(const void* q, const void* k, const void* v, const void* beta, const float* g,
+                            float* state, const int32_t* slots, void* o, int N, int P, int H, int Hk, int d_k, int d_v,
+                            efla_dtype dtype, efla_rule rule, void* stream) {
+  if (!valid_rule(rule) || !valid_dtype(dtype) || N < 0 || P < 0 || H < 1 || Hk < 1 || H % Hk != 0)
+    return EFLA_ERR_INVALID_ARG;
+  if (!valid_dim(d_k) || !valid_dim(d_v) || int64_t(N) * H * (d_v / 16) > kMaxGrid) return EFLA_ERR_UNSUPPORTED;
+  if (slots == nullptr && P < N) return EFLA_ERR_INVALID_ARG;
+  if (N == 0 || P == 0) return EFLA_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || state == nullptr ||
+      o == nullptr)
+    return EFLA_ERR_INVALID_ARG;
+  if (!aligned16(state)) return EFLA_ERR_INVALID_ARG;
+  const efla::GatedStep a{q, k, v, beta, g, state, slots, o, N, P, H, Hk, d_k, d_v, int(rule)};
+  return by_type(dtype,
+                 [&](auto t) { return efla::launch_gated_step<decltype(t)>(a, static_cast<hipStream_t>(stream)); });
+}
+
+efla_status efla_pack_plan(const int32_t* lengths, const int32_t* starts, int N, int64_t T, int chunk,
+                           int32_t* cu_seqlens, int32_t* order, int32_t* token_seq, int32_t* token_pos, void* stream) {
+  if (N < 0 || T < 0 || T > INT32_MAX || cu_seqlens == nullptr || (N > 0 && lengths == nullptr))
+    return EFLA_ERR_INVALID_ARG;
+  if (!valid_chunk(chunk)) return EFLA_ERR_UNSUPPORTED;
+  return from_hip(efla::launch_plan(lengths, starts, N, int(T), chunk, cu_seqlens, order, token_seq, token_pos,
+                                    static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

@@ -137,4 +137,47 @@ hipError_t launch_seg_offsets(int32_t* cu, int B, int G, int64_t L, int64_t Ls, 
 hipError_t launch_seg_combine(const float* M, const float* N, const float* s0, float* sin, float* sfin, int B, int H,
                               int G, int DK, int DV, hipStream_t s);
 
+// The gated delta rule (gated.h).  Pointers as in include/efla.h; element type
+// by the launcher's template argument.
+struct GatedStep {
+  const void *q, *k, *v, *beta;
+  const float* g;
+  float* state;
+  const int32_t* slots;  // rows of the state pool, null: row n
+  void* o;
+  int N, P, H, Hk, DK, DV, rule;
+};
+template <typename T>
+hipError_t launch_gated_step(const GatedStep& a, hipStream_t s);
+
+struct GatedFwd {
+  const void *q, *k, *v, *beta;
+  const float *g, *s0;
+  void* o;
+  float* sfin;
+  const int32_t *cu, *slots, *order;  // packed batch: offsets, rows of the states, schedule
+  int B, N, P, H, Hk, DK, DV, rule;   // P: rows of s0 and sfin
+  int64_t L;                          // tokens a sequence, or of the packed batch
+};
+// Token by token in fp32, any d_k / d_v; o may be null; states (dense batches):
+// the state before every C-th token, [chunk slot][d_k][d_v].
+template <typename T>
+hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipStream_t s);
+
+struct GatedBwd {
+  const void *q, *k, *v, *beta, *d_o;
+  const float *g, *s0, *dsf;
+  void *dq, *dk, *dv, *dbeta, *dg;
+  float* ds0;
+  int B, H, Hk, DK, DV, rule;
+  int64_t L;
+};
+size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t esz);
+template <typename T>
+hipError_t launch_gated_bwd(const GatedBwd& b, int C, void* ws, hipStream_t s);
+
+// Tables of a packed batch (plan.hip); order, seq, pos and starts nullable.
+hipError_t launch_plan(const int32_t* lengths, const int32_t* starts, int N, int T, int C, int32_t* cu,
+                       int32_t* order, int32_t* seq, int32_t* pos, hipStream_t s);
+
 }  // namespace efla

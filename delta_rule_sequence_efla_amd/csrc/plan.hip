@@ -1,0 +1,153 @@
+// plan.hip -- the tables of a packed batch, from the requests' lengths in
+// device memory: offsets, the longest-first order of the recurrence, and the
+// sequence and position of every packed row.
+//
+// With l_u = max(lengths[u], 0): cu[u] = min(l_0 + .. + l_{u-1}, T); order by
+// chunk count as rank_sequences (common.h) writes it; a row t belongs to the
+// first sequence that ends after it (sequences without tokens own no row), at
+// position t - cu[u] + starts[u].
+//
+// Up to kPlanSeqs sequences one launch does it all: every workgroup sums the
+// lengths for itself into LDS (16 KiB at most, read from L2) rather than wait
+// for another launch's sums, then fills its rows by binary search there; the
+// first N / 16 workgroups also rank 16 sequences each.  At these sizes the time
+// is launch and load latency.  More sequences take a launch for the offsets
+// (order is then the index order) and one for the rows.
+#include "gated.h"
+#include "launchers.h"
+
+namespace efla {
+
+namespace {
+constexpr int kPlanSeqs = 4096;   // sequences whose offsets fit the LDS copy
+constexpr int kPlanRows = 1024;   // packed rows per workgroup
+constexpr int kPlanRank = 16;     // sequences ranked per workgroup, 16 lanes each
+
+// Sums are clamped at T as they grow: with T < 2^31 and partial sums clamped
+// to T, min(a + b, T) needs a + b < 2^32, so it is formed unsigned.
+__device__ __forceinline__ int sat_add(int a, int b, int T) {
+  const uint32_t s = uint32_t(a) + uint32_t(b);
+  return s > uint32_t(T) ? T : int(s);
+}
+__device__ __forceinline__ int wave_scan_sat(int x, int lane, int T) {
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x = sat_add(x, y, T);
+  }
+  return x;
+}
+__device__ __forceinline__ int plan_length(const int32_t* __restrict__ lengths, int u, int T) {
+  const int l = lengths[u];
+  return l < 0 ? 0 : (l > T ? T : l);
+}
+
+// end[u] (u < N) = min(l_0 + .. + l_u, T), by all kThreads threads; wsum: kThreads / 64 ints of LDS.
+__device__ __forceinline__ void plan_ends(const int32_t* __restrict__ lengths, int N, int T, int32_t* end, int* wsum) {
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  int carry = 0;
+  for (int base = 0; base < N; base += kThreads) {
+    const int u = base + tid;
+    const int x = wave_scan_sat(u < N ? plan_length(lengths, u, T) : 0, lane, T);
+    __syncthreads();  // the last round's wsum is read
+    if (lane == kWave - 1) wsum[w] = x;
+    __syncthreads();
+    int before = carry;
+    for (int j = 0; j < kThreads / kWave; ++j) {
+      if (j < w) before = sat_add(before, wsum[j], T);
+      carry = sat_add(carry, wsum[j], T);
+    }
+    if (u < N) end[u] = sat_add(before, x, T);
+  }
+  __syncthreads();
+}
+
+// sequence of row t: the first u with end[u] > t; N past the last
+__device__ __forceinline__ int plan_seq(const int32_t* end, int N, int t) {
+  int lo = 0, hi = N;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (end[mid] > t) hi = mid;
+    else lo = mid + 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int plan_chunks(const int32_t* end, int u, int C) {
+  return (end[u] - (u > 0 ? end[u - 1] : 0) + C - 1) / C;
+}
+
+__device__ __forceinline__ void plan_rows(const int32_t* end, int N, int T, const int32_t* __restrict__ starts,
+                                          int32_t* __restrict__ seq, int32_t* __restrict__ pos) {
+  for (int i = 0; i < kPlanRows / kThreads; ++i) {
+    const int64_t t = int64_t(blockIdx.x) * kPlanRows + i * kThreads + threadIdx.x;
+    if (t >= T) return;
+    const int u = plan_seq(end, N, int(t));
+    const bool in = u < N;
+    if (seq != nullptr) seq[t] = in ? u : -1;
+    if (pos != nullptr)
+      pos[t] = in ? int(uint32_t(t) - uint32_t(u > 0 ? end[u - 1] : 0) + uint32_t(starts != nullptr ? starts[u] : 0)) : -1;
+  }
+}
+}  // namespace
+
+__global__ __launch_bounds__(kThreads) void plan_kernel(const int32_t* __restrict__ lengths,
+                                                        const int32_t* __restrict__ starts, int N, int T, int C,
+                                                        int32_t* __restrict__ cu, int32_t* __restrict__ order,
+                                                        int32_t* __restrict__ seq, int32_t* __restrict__ pos) {
+  __shared__ int32_t end[kPlanSeqs];
+  __shared__ int wsum[kThreads / kWave];
+  plan_ends(lengths, N, T, end, wsum);
+  const int tid = threadIdx.x;
+  if (blockIdx.x == 0) {
+    for (int u = tid; u <= N; u += kThreads) cu[u] = u > 0 ? end[u - 1] : 0;
+  }
+  // rank(u) = #{v : n(v) > n(u)} + #{v < u : n(v) = n(u)}
+  const int u = int(blockIdx.x) * kPlanRank + (tid >> 4);
+  if (order != nullptr && int(blockIdx.x) * kPlanRank < N) {
+    const int nu = u < N ? plan_chunks(end, u, C) : 0;
+    int rank = 0;
+    for (int x = tid & 15; x < N; x += 16) {
+      const int nv = plan_chunks(end, x, C);
+      rank += (nv > nu || (nv == nu && x < u)) ? 1 : 0;
+    }
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1) rank += __shfl_xor(rank, d);
+    if ((tid & 15) == 0 && u < N) order[rank] = u;
+  }
+  if (seq != nullptr || pos != nullptr) plan_rows(end, N, T, starts, seq, pos);
+}
+
+__global__ __launch_bounds__(kThreads) void plan_offsets_kernel(const int32_t* __restrict__ lengths, int N, int T,
+                                                                int32_t* __restrict__ cu, int32_t* __restrict__ order) {
+  __shared__ int wsum[kThreads / kWave];
+  if (threadIdx.x == 0) cu[0] = 0;
+  plan_ends(lengths, N, T, cu + 1, wsum);
+  if (order != nullptr)
+    for (int u = threadIdx.x; u < N; u += kThreads) order[u] = u;
+}
+
+__global__ __launch_bounds__(kThreads) void plan_rows_kernel(const int32_t* __restrict__ cu,
+                                                             const int32_t* __restrict__ starts, int N, int T,
+                                                             int32_t* __restrict__ seq, int32_t* __restrict__ pos) {
+  plan_rows(cu + 1, N, T, starts, seq, pos);
+}
+
+hipError_t launch_plan(const int32_t* lengths, const int32_t* starts, int N, int T, int C, int32_t* cu,
+                       int32_t* order, int32_t* seq, int32_t* pos, hipStream_t s) {
+  const int row_wgs = seq != nullptr || pos != nullptr ? int((int64_t(T) + kPlanRows - 1) / kPlanRows) : 0;
+  if (N <= kPlanSeqs) {
+    const int rank_wgs = order != nullptr ? (N + kPlanRank - 1) / kPlanRank : 0;
+    int nwg = row_wgs > rank_wgs ? row_wgs : rank_wgs;
+    if (nwg < 1) nwg = 1;
+    hipLaunchKernelGGL(plan_kernel, dim3(unsigned(nwg)), dim3(kThreads), 0, s, lengths, starts, N, T, C, cu, order,
+                       seq, pos);
+    return hipGetLastError();
+  }
+  hipLaunchKernelGGL(plan_offsets_kernel, dim3(1), dim3(kThreads), 0, s, lengths, N, T, cu, order);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  if (row_wgs > 0)
+    hipLaunchKernelGGL(plan_rows_kernel, dim3(unsigned(row_wgs)), dim3(kThreads), 0, s, cu, starts, N, T, seq, pos);
+  return hipGetLastError();
+}
+
+}  // namespace efla

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -93,6 +94,23 @@ def lib() -> ctypes.CDLL:
         L.efla_chunk_fwd_varlen.restype = _i
         L.efla_chunk_fwd_varlen.argtypes = [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _i, _i64, _i, _i,
                                             _i, _i, _i, _vp, _sz, _vp]
+        L.efla_gated_chunk_fwd_workspace_size.restype = _sz
+        L.efla_gated_chunk_fwd_workspace_size.argtypes = [_i, _i, _i, _i64, _i, _i, _i, _i]
+        L.efla_gated_chunk_fwd.restype = _i
+        L.efla_gated_chunk_fwd.argtypes = [_vp] * 8 + [_i, _i, _i, _i64, _i, _i, _i, _i, _i, _vp, _sz, _vp]
+        L.efla_gated_chunk_fwd_varlen_workspace_size.restype = _sz
+        L.efla_gated_chunk_fwd_varlen_workspace_size.argtypes = [_i, _i, _i, _i64, _i, _i, _i, _i]
+        L.efla_gated_chunk_fwd_varlen.restype = _i
+        L.efla_gated_chunk_fwd_varlen.argtypes = [_vp] * 8 + [_i, _i, _vp, _vp, _vp, _i, _i, _i64, _i, _i, _i, _i, _i,
+                                                              _vp, _sz, _vp]
+        L.efla_gated_chunk_bwd_workspace_size.restype = _sz
+        L.efla_gated_chunk_bwd_workspace_size.argtypes = [_i, _i, _i, _i64, _i, _i, _i, _i]
+        L.efla_gated_chunk_bwd.restype = _i
+        L.efla_gated_chunk_bwd.argtypes = [_vp] * 14 + [_i, _i, _i, _i64, _i, _i, _i, _i, _i, _vp, _sz, _vp]
+        L.efla_gated_step.restype = _i
+        L.efla_gated_step.argtypes = [_vp] * 8 + [_i, _i, _i, _i, _i, _i, _i, _i, _vp]
+        L.efla_pack_plan.restype = _i
+        L.efla_pack_plan.argtypes = [_vp, _vp, _i, _i64, _i, _vp, _vp, _vp, _vp, _vp]
         _lib = L
     return _lib
 
@@ -526,6 +544,181 @@ def efla_step(q, k, v, beta, state, o=None, rule: str = "exact"):
         _check(lib().efla_step_rule(_p(q), _p(k), _p(v), _p(beta), _p(state), _p(o), N, H, dk, dv,
                                     _code(q.dtype), _rule(rule), _stream(dev)), "efla_step")
     return o
+
+
+# ---------------------------------------------------------------------------
+# The gated delta rule: S_t = e^{g_t} (I - a_t k_t k_t^T) S_{t-1} + a_t k_t v_t^T,
+# o_t = S_t^T q_t.  g is float32 for every dtype; q and k may have fewer heads
+# (Hk) than v, beta, g and the states (H): value head h reads head h // (H // Hk).
+
+def _gated_shapes(q, k, v, beta, g, lead: int):
+    """(device, leading dims, H, Hk, dk, dv) of a gated call's inputs, checked."""
+    dt = q.dtype
+    dev = _dev(q, k, v, beta, dtype=dt)
+    _dev(q, g)
+    if k.dim() != lead + 2 or v.dim() != lead + 2 or q.shape != k.shape or v.shape[:lead] != k.shape[:lead] \
+            or beta.shape != v.shape[:-1] or g.shape != v.shape[:-1] or g.dtype != torch.float32:
+        dims = {1: "N" , 2: "B,L"}[lead]
+        raise ValueError(f"expected q, k [{dims},Hk,dk], v [{dims},H,dv], beta [{dims},H] of one type, "
+                         f"g float32 [{dims},H]")
+    H, Hk = v.shape[-2], k.shape[-2]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"the {H} value heads must be a multiple of the {Hk} query and key heads")
+    return dev, H, Hk, k.shape[-1], v.shape[-1]
+
+
+def efla_gated_chunk_fwd_workspace_size(B, H, Hk, L, d_k, d_v, chunk, dtype) -> int:
+    return int(lib().efla_gated_chunk_fwd_workspace_size(B, H, Hk, L, d_k, d_v, chunk, _code(dtype)))
+
+
+def efla_gated_chunk_fwd(q, k, v, beta, g, s0=None, chunk: int = 64, o=None, s_final=None, workspace=None,
+                         want_final: bool = True, rule: str = "exact"):
+    """Gated forward pass over a dense batch: q, k [B,L,Hk,dk], v [B,L,H,dv],
+    beta [B,L,H] in one type, g float32 [B,L,H].  Returns (o [B,L,H,dv] in q's
+    dtype, S_L float32 [B,H,dk,dv] or None)."""
+    dev, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
+    B, L = k.shape[:2]
+    _dev(q, s0, o, s_final, workspace)
+    _want(s0, (B, H, dk, dv), "s0", torch.float32)
+    _want(o, v.shape, "o", q.dtype)
+    _want(s_final, (B, H, dk, dv), "s_final", torch.float32)
+    if o is None:
+        o = torch.empty_like(v)
+    if s_final is None and want_final:
+        s_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    code = _code(q.dtype)
+    if workspace is None:
+        n = lib().efla_gated_chunk_fwd_workspace_size(B, H, Hk, L, dk, dv, chunk, code)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    with torch.cuda.device(dev):
+        _check(lib().efla_gated_chunk_fwd(_p(q), _p(k), _p(v), _p(beta), _p(g), _p(s0), _p(o), _p(s_final), B, H, Hk,
+                                          L, dk, dv, chunk, code, _rule(rule), _p(workspace), _ws(workspace, dev),
+                                          _stream(dev)), "efla_gated_chunk_fwd")
+    return o, s_final
+
+
+def efla_gated_chunk_fwd_varlen_workspace_size(N, H, Hk, T, d_k, d_v, chunk, dtype) -> int:
+    return int(lib().efla_gated_chunk_fwd_varlen_workspace_size(N, H, Hk, T, d_k, d_v, chunk, _code(dtype)))
+
+
+def efla_gated_chunk_fwd_varlen(q, k, v, beta, g, cu_seqlens, s0=None, chunk: int = 64, slots=None, order=None,
+                                o=None, s_final=None, workspace=None, want_final: bool = True, rule: str = "exact"):
+    """Gated forward pass over a packed batch: q, k [T,Hk,dk], v [T,H,dv],
+    beta, g [T,H], int32 device offsets cu_seqlens [N+1].  s0 and s_final are
+    [N,H,dk,dv], or with int32 slots [N] pools [P,H,dk,dv] whose row slots[i]
+    sequence i starts from and ends in (an entry outside the pool: from zero,
+    final state not written).  order: a schedule as efla_pack_plan returns it.
+    Returns (o shaped like v, s_final)."""
+    dev, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1)
+    T = k.shape[0]
+    _dev(q, s0, o, s_final, workspace, cu_seqlens, slots, order)
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor of N+1 offsets")
+    N = cu_seqlens.numel() - 1
+    _want(slots, (N,), "slots", torch.int32)
+    _want(order, (N,), "order", torch.int32)
+    _want(o, v.shape, "o", q.dtype)
+    P = N
+    if slots is not None:
+        if s0 is None and s_final is None:
+            raise ValueError("slots need a pool: s0, s_final or both")
+        P = (s0 if s0 is not None else s_final).shape[0]
+    _want(s0, (P, H, dk, dv), "s0", torch.float32)
+    _want(s_final, (P, H, dk, dv), "s_final", torch.float32)
+    if o is None:
+        o = torch.empty_like(v)
+    if s_final is None and want_final:
+        if slots is not None:
+            raise ValueError("with slots the final states need a pool: pass s_final (it may be s0), or want_final=False")
+        s_final = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
+    code = _code(q.dtype)
+    if workspace is None:
+        n = lib().efla_gated_chunk_fwd_varlen_workspace_size(N, H, Hk, T, dk, dv, chunk, code)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    with torch.cuda.device(dev):
+        _check(lib().efla_gated_chunk_fwd_varlen(_p(q), _p(k), _p(v), _p(beta), _p(g), _p(cu_seqlens), _p(slots),
+                                                 _p(order), N, P, _p(s0), _p(o), _p(s_final), H, Hk, T, dk, dv, chunk,
+                                                 code, _rule(rule), _p(workspace), _ws(workspace, dev), _stream(dev)),
+               "efla_gated_chunk_fwd_varlen")
+    return o, s_final
+
+
+def efla_gated_chunk_bwd_workspace_size(B, H, Hk, L, d_k, d_v, chunk, dtype) -> int:
+    return int(lib().efla_gated_chunk_bwd_workspace_size(B, H, Hk, L, d_k, d_v, chunk, _code(dtype)))
+
+
+def efla_gated_chunk_bwd(q, k, v, beta, g, d_o, s0=None, ds_final=None, chunk: int = 64, rule: str = "exact",
+                         want_ds0: bool = True, workspace=None):
+    """Gradients through efla_gated_chunk_fwd for dLoss/do = d_o and dLoss/dS_L
+    = ds_final (None: zero).  Returns (dq, dk, dv, dbeta, dg, ds0): the first
+    five in q's dtype (dq and dk summed over the value heads that share a
+    head), ds0 float32 [B,H,dk,dv] or None when want_ds0 is False."""
+    dev, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
+    B, L = k.shape[:2]
+    _dev(q, d_o, s0, ds_final, workspace)
+    _want(d_o, v.shape, "d_o", q.dtype)
+    _want(s0, (B, H, dk, dv), "s0", torch.float32)
+    _want(ds_final, (B, H, dk, dv), "ds_final", torch.float32)
+    gq, gk, gv, gb, gg = (torch.empty_like(x) for x in (q, k, v, beta, beta))
+    gs0 = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if want_ds0 else None
+    code = _code(q.dtype)
+    if workspace is None:
+        n = lib().efla_gated_chunk_bwd_workspace_size(B, H, Hk, L, dk, dv, chunk, code)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    with torch.cuda.device(dev):
+        _check(lib().efla_gated_chunk_bwd(_p(q), _p(k), _p(v), _p(beta), _p(g), _p(s0), _p(d_o), _p(ds_final), _p(gq),
+                                          _p(gk), _p(gv), _p(gb), _p(gg), _p(gs0), B, H, Hk, L, dk, dv, chunk, code,
+                                          _rule(rule), _p(workspace), _ws(workspace, dev), _stream(dev)),
+               "efla_gated_chunk_bwd")
+    return gq, gk, gv, gb, gg, gs0
+
+
+def efla_gated_step(q, k, v, beta, g, state, slots=None, o=None, rule: str = "exact"):
+    """One gated decode step, in place on a pool of states [P,H,dk,dv] (fp32):
+    q, k [N,Hk,dk], v [N,H,dv], beta [N,H] in one type, g float32 [N,H].  Row n
+    updates state slots[n] (int32 [N]; None: state n); a slot outside the pool
+    skips the row and leaves its row of o as it was.  Returns o [N,H,dv]."""
+    dev, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1)
+    N = k.shape[0]
+    _dev(q, state, slots, o)
+    if state.dim() != 4 or state.shape[1:] != (H, dk, dv) or state.dtype != torch.float32 \
+            or (slots is None and state.shape[0] != N):
+        raise ValueError("state must be float32 [P,H,dk,dv], with P = N where no slots are given")
+    _want(slots, (N,), "slots", torch.int32)
+    _want(o, v.shape, "o", q.dtype)
+    if o is None:
+        o = torch.empty_like(v)
+    with torch.cuda.device(dev):
+        _check(lib().efla_gated_step(_p(q), _p(k), _p(v), _p(beta), _p(g), _p(state), _p(slots), _p(o), N,
+                                     state.shape[0], H, Hk, dk, dv, _code(q.dtype), _rule(rule), _stream(dev)),
+               "efla_gated_step")
+    return o
+
+
+class PackPlan(NamedTuple):
+    """Tables of a packed batch (efla_pack_plan), int32 on the device."""
+    cu_seqlens: torch.Tensor  # [N+1] offsets
+    order: torch.Tensor       # [N] requests, longest first
+    token_seq: torch.Tensor   # [T] request of every packed row, -1 behind the last
+    token_pos: torch.Tensor   # [T] its position, -1 behind the last
+
+
+def efla_pack_plan(lengths, tokens: int, starts=None, chunk: int = 64) -> PackPlan:
+    """Tables of a packed batch of ``tokens`` rows from the requests' new-token
+    counts ``lengths`` (int32 [N] on the device; nothing is copied to the host).
+    starts: int32 [N], the position of each request's first new token."""
+    dev = _dev(lengths, starts)
+    if lengths.dim() != 1 or lengths.dtype != torch.int32:
+        raise ValueError("lengths must be a 1-D int32 tensor")
+    N, T = lengths.numel(), int(tokens)
+    _want(starts, (N,), "starts", torch.int32)
+    if not 0 <= T < 2 ** 31:
+        raise ValueError("tokens must be in [0, 2^31)")
+    cu, order, seq, pos = torch.empty(2 * N + 1 + 2 * T, dtype=torch.int32, device=dev).split([N + 1, N, T, T])
+    with torch.cuda.device(dev):
+        _check(lib().efla_pack_plan(_p(lengths), _p(starts), N, T, chunk, _p(cu), _p(order), _p(seq), _p(pos),
+                                    _stream(dev)), "efla_pack_plan")
+    return PackPlan(cu, order, seq, pos)
 
 
 class PreparedCall:

@@ -333,6 +333,109 @@ efla_status efla_step_rule(const void *q, const void *k, const void *v, const vo
                            float *state, void *o, int N, int H, int d_k, int d_v,
                            efla_dtype dtype, efla_rule rule, void *stream);
 
+/*
+ * The gated delta rule: the recurrence above with a decay of the state before
+ * every update,
+ *     S_t = exp(g_t) (I - alpha_t k_t k_t^T) S_{t-1} + alpha_t k_t v_t^T,
+ *     o_t = S_t^T q_t,
+ * alpha under either rule (EFLA_RULE_EULER: the gated delta rule of a gated
+ * DeltaNet layer; EFLA_RULE_EXACT: the exact flow with the same decay).
+ *
+ *   - g is float32 for every dtype: a log-decay, one per token and value head;
+ *     it may have any sign, and values below -128 act as -128, whose decay is
+ *     zero in float32 (so -inf resets the state).
+ *   - Query and key heads may be shared: q, k have Hk heads, v, beta, g, o and
+ *     the states H, with H a multiple of Hk; value head h reads query and key
+ *     head h / (H / Hk).  H % Hk != 0 or Hk < 1 is EFLA_ERR_INVALID_ARG.
+ *   - States are float32 and carried in float32.  bf16 matrix-core products
+ *     that feed a state take each float32 operand as the sum of two bf16
+ *     values (16 significant bits), so a state is good to about 1e-5 whatever
+ *     the inputs' type; products that only feed o round such operands once.
+ *   - Layouts, alignment, streams, workspaces and errors as above otherwise.
+ *
+ * efla_gated_chunk_fwd -- dense batch.  q, k [B, L, Hk, d_k], v, o
+ * [B, L, H, d_v], beta [B, L, H] in dtype, g [B, L, H] float32, s0 and s_final
+ * [B, H, d_k, d_v] float32 (each nullable; s_final may alias s0).
+ */
+size_t efla_gated_chunk_fwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
+                                           efla_dtype dtype);
+efla_status efla_gated_chunk_fwd(const void *q, const void *k, const void *v, const void *beta,
+                                 const float *g, const float *s0, void *o, float *s_final, int B, int H,
+                                 int Hk, int64_t L, int d_k, int d_v, int chunk, efla_dtype dtype,
+                                 efla_rule rule, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * efla_gated_chunk_fwd_varlen -- packed batch (layouts and offsets as
+ * efla_chunk_fwd_varlen, q and k with Hk heads, g [T, H]), with the states in a
+ * pool:
+ *   slots [N] int32, DEVICE memory, nullable: sequence i starts from row
+ *       slots[i] of s0 and leaves its final state in row slots[i] of s_final
+ *       (NULL: row i).  s0 and s_final are [P, H, d_k, d_v] float32 and may be
+ *       one tensor.  An entry outside [0, P) stands for no row: the sequence
+ *       starts from zero and its final state is not written.  Rows that no
+ *       sequence names are left as they were.  The entries are read on the
+ *       device and cannot be checked here: a row named by two sequences holds
+ *       the final state of one of them, and with s0 and s_final one tensor both
+ *       sequences' results are unspecified.
+ *   order [N] int32, DEVICE memory, nullable: the sequences in the order in
+ *       which they are handed to workgroups, a permutation of 0 .. N-1 (as
+ *       efla_pack_plan writes it; NULL: ranked by the call itself for N <=
+ *       4096, else index order).  It does not change any result.
+ * P >= N where slots is NULL.  A sequence without tokens copies its state.
+ */
+size_t efla_gated_chunk_fwd_varlen_workspace_size(int N, int H, int Hk, int64_t T, int d_k, int d_v,
+                                                  int chunk, efla_dtype dtype);
+efla_status efla_gated_chunk_fwd_varlen(const void *q, const void *k, const void *v, const void *beta,
+                                        const float *g, const int32_t *cu_seqlens, const int32_t *slots,
+                                        const int32_t *order, int N, int P, const float *s0, void *o,
+                                        float *s_final, int H, int Hk, int64_t T, int d_k, int d_v,
+                                        int chunk, efla_dtype dtype, efla_rule rule, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
+/*
+ * efla_gated_chunk_bwd -- gradients through efla_gated_chunk_fwd (dense batch;
+ * arguments as efla_chunk_bwd, with g and Hk).  Writes dq, dk [B, L, Hk, d_k]
+ * (summed over the value heads that share a head, in a fixed order), dv
+ * [B, L, H, d_v], dbeta and dg [B, L, H], all in dtype, and ds0 float32
+ * (NULL: not written).  Results do not depend on timing.
+ */
+size_t efla_gated_chunk_bwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
+                                           efla_dtype dtype);
+efla_status efla_gated_chunk_bwd(const void *q, const void *k, const void *v, const void *beta,
+                                 const float *g, const float *s0, const void *d_o, const float *ds_final,
+                                 void *dq, void *dk, void *dv, void *dbeta, void *dg, float *ds0, int B,
+                                 int H, int Hk, int64_t L, int d_k, int d_v, int chunk, efla_dtype dtype,
+                                 efla_rule rule, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * efla_gated_step -- one token per request, its state updated in place in a
+ * pool: q, k [N, Hk, d_k], v, o [N, H, d_v], beta [N, H] in dtype, g [N, H]
+ * float32, state [P, H, d_k, d_v] float32, slots as above (NULL: row n, P >= N).
+ * A row of the batch whose slot lies outside [0, P) is skipped: its row of o
+ * is left as it was (rows that pad a batch to a fixed size).  A slot named
+ * twice is unspecified.  state must be 16-byte aligned.
+ */
+efla_status efla_gated_step(const void *q, const void *k, const void *v, const void *beta, const float *g,
+                            float *state, const int32_t *slots, void *o, int N, int P, int H, int Hk,
+                            int d_k, int d_v, efla_dtype dtype, efla_rule rule, void *stream);
+
+/*
+ * efla_pack_plan -- the tables of a packed batch from lengths in DEVICE memory
+ * (no copy to the host):
+ *   lengths [N] int32: new tokens of each request (negative counts as 0)
+ *   starts  [N] int32, nullable: position of each request's first new token
+ *   cu_seqlens [N + 1] int32 out: offsets, clamped at T (rows the batch holds)
+ *   order [N] int32 out, nullable: the requests by chunk count, longest first
+ *       (ties by index) for N <= 4096, else by index
+ *   token_seq, token_pos [T] int32 out, each nullable: the request of every
+ *       packed row and its position, t - cu_seqlens[i] + starts[i]; -1 in the
+ *       rows behind the last request
+ * N may be 0, T < 2^31.
+ */
+efla_status efla_pack_plan(const int32_t *lengths, const int32_t *starts, int N, int64_t T, int chunk,
+                           int32_t *cu_seqlens, int32_t *order, int32_t *token_seq, int32_t *token_pos,
+                           void *stream);
+
 #ifdef __cplusplus
 }
 #endif
