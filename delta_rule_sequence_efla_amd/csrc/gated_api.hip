@@ -15,9 +15,20 @@ efla_status check_gated_shape(int B, int H, int Hk, int64_t L, int d_k, int d_v,
   return H % Hk == 0 ? EFLA_OK : EFLA_ERR_INVALID_ARG;
 }
 
+// Which forward kernels run: the chunked matrix-core pass where its shapes and
+// type allow, else token by token in float32.
+bool gated_chunked(int d_k, int d_v, int chunk, efla_dtype dt) {
+  return dt == EFLA_BF16 && efla::gated_chunk_supported(d_k, d_v, chunk);
+}
+
 template <typename F>
 efla_status by_type(efla_dtype dt, F&& f) {
   return from_hip(dt == EFLA_BF16 ? f(uint16_t{}) : f(float{}));
+}
+
+efla_status gated_forward(const efla::GatedFwd& a, int chunk, efla_dtype dt, void* workspace, hipStream_t s) {
+  if (a.L > 0 && gated_chunked(a.DK, a.DV, chunk, dt)) return from_hip(efla::launch_gated_chunk(a, workspace, s));
+  return by_type(dt, [&](auto t) { return efla::launch_gated_recurrent<decltype(t)>(a, nullptr, chunk, s); });
 }
 
 }  // namespace
@@ -26,8 +37,8 @@ extern "C" {
 
 size_t efla_gated_chunk_fwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
                                            efla_dtype dtype) {
-  if (check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK) return 0;
-  return 0;
+  if (check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || L == 0) return 0;
+  return gated_chunked(d_k, d_v, chunk, dtype) ? efla::gated_fwd_layout(B, 0, H, L, false).total : 0;
 }
 
 efla_status efla_gated_chunk_fwd(const void* q, const void* k, const void* v, const void* beta, const float* g,
@@ -47,15 +58,13 @@ efla_status efla_gated_chunk_fwd(const void* q, const void* k, const void* v, co
   if (L == 0 && s_final == nullptr) return EFLA_OK;
   const efla::GatedFwd a{q,       k,       v,       beta, g, s0, o,  s_final, nullptr,   nullptr,
                          nullptr, B,       0,       B,    H, Hk, d_k, d_v,     int(rule), L};
-  return by_type(dtype, [&](auto t) {
-    return efla::launch_gated_recurrent<decltype(t)>(a, nullptr, chunk, static_cast<hipStream_t>(stream));
-  });
+  return gated_forward(a, chunk, dtype, workspace, static_cast<hipStream_t>(stream));
 }
 
 size_t efla_gated_chunk_fwd_varlen_workspace_size(int N, int H, int Hk, int64_t T, int d_k, int d_v, int chunk,
                                                   efla_dtype dtype) {
-  if (check_gated_shape(N, H, Hk, T, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK) return 0;
-  return 0;
+  if (check_gated_shape(N, H, Hk, T, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || T == 0) return 0;
+  return gated_chunked(d_k, d_v, chunk, dtype) ? efla::gated_fwd_layout(0, N, H, T, true).total : 0;
 }
 
 efla_status efla_gated_chunk_fwd_varlen(const void* q, const void* k, const void* v, const void* beta, const float* g,
@@ -81,9 +90,7 @@ efla_status efla_gated_chunk_fwd_varlen(const void* q, const void* k, const void
   if (T == 0 && s_final == nullptr) return EFLA_OK;
   const efla::GatedFwd a{q,     k, v, beta, g, s0, o,   s_final, cu_seqlens, slots,
                          order, 0, N, P,    H, Hk, d_k, d_v,     int(rule),  T};
-  return by_type(dtype, [&](auto t) {
-    return efla::launch_gated_recurrent<decltype(t)>(a, nullptr, chunk, static_cast<hipStream_t>(stream));
-  });
+  return gated_forward(a, chunk, dtype, workspace, static_cast<hipStream_t>(stream));
 }
 
 size_t efla_gated_chunk_bwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,

@@ -1,0 +1,83 @@
+// gated_fwd.hip -- launches of the chunked gated forward pass for bf16 inputs:
+// the UT transform (gated_ut.h), then the recurrence (gated_split.h).
+// Workspace, regions 256-byte aligned: T fragments [slots][12 KiB], gate blocks
+// [slots][1 KiB], and for packed batches the schedule (int32 per sequence).
+#include "gated_split.h"
+
+namespace efla {
+
+namespace {
+size_t align256(size_t x) { return (x + 255) / 256 * 256; }
+constexpr int kGatedChunk = 64;
+// Packed batches of at most this many sequences run longest first (the ranking
+// compares every pair of sequences).
+constexpr int kGatedOrderedSeqs = 4096;
+
+template <int DK, bool BWD>
+hipError_t ut_impl(const GatedFwd& a, uint16_t* tfr, float* gws, float* xws, int32_t* order, hipStream_t s) {
+  const int NC = a.cu == nullptr ? int((a.L + kGatedChunk - 1) / kGatedChunk) : int(a.L / kGatedChunk) + a.N;
+  const int64_t nchunks = int64_t(a.cu == nullptr ? a.B : 1) * a.H * NC;
+  constexpr int W = UtWaveShape<DK, kGatedChunk>::WAVES;
+  static_assert(64 * W == kThreads && W * UtWaveShape<DK, kGatedChunk>::SCRATCH >= int(kRankSeqs * sizeof(int)),
+                "ranking workgroups reuse the kernel's shape and LDS");
+  const int64_t nwg = (nchunks + W - 1) / W;
+  const int64_t nrank = order != nullptr ? (a.N + kRankSeqs - 1) / kRankSeqs : 0;
+  if (nwg + nrank == 0) return hipSuccess;
+  hipLaunchKernelGGL((gated_ut_wave_kernel<DK, BWD>), dim3(unsigned(nwg + nrank)), dim3(kThreads), 0, s,
+                     static_cast<const uint16_t*>(a.k), static_cast<const uint16_t*>(a.beta), a.g, tfr, gws, a.H, a.Hk,
+                     a.L, NC, nchunks, a.rule, a.cu, a.N, nwg, order, xws);
+  return hipGetLastError();
+}
+
+template <int DK, bool SAVE>
+hipError_t split_impl(const GatedFwd& a, const uint16_t* tfr, const float* gws, const int32_t* order,
+                      uint16_t* statesT, hipStream_t s) {
+  const int NC = a.cu == nullptr ? int((a.L + kGatedChunk - 1) / kGatedChunk) : int(a.L / kGatedChunk) + a.N;
+  const int64_t bh = int64_t(a.cu == nullptr ? a.B : a.N) * a.H;
+  const int NVB = a.DV / 32;
+  hipLaunchKernelGGL((gated_split_kernel<DK, SAVE>), dim3(unsigned(bh * NVB)), dim3(GatedSplitShape<DK>::THREADS), 0, s,
+                     a, tfr, gws, order, NC, NVB, bh % 8 == 0 ? 1 : 0, statesT);
+  return hipGetLastError();
+}
+}  // namespace
+
+bool gated_chunk_supported(int DK, int DV, int C) {
+  return C == kGatedChunk && (DK == 64 || DK == 128) && DV % 32 == 0;
+}
+
+GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed) {
+  const size_t slots = packed ? size_t(H) * (L / kGatedChunk + N) : size_t(B) * H * ((L + kGatedChunk - 1) / kGatedChunk);
+  GatedFwdLayout w{};
+  w.t = 0;
+  w.g = align256(slots * kGatedT * 2);
+  w.order = w.g + align256(slots * kGatedG * 4);
+  w.total = w.order + (packed ? align256(size_t(N) * 4) : 0);
+  return w;
+}
+
+hipError_t launch_gated_ut(const GatedFwd& a, uint16_t* tfr, float* gws, float* xws, int32_t* order, hipStream_t s) {
+  if (a.DK == 64) return xws == nullptr ? ut_impl<64, false>(a, tfr, gws, xws, order, s) : ut_impl<64, true>(a, tfr, gws, xws, order, s);
+  return xws == nullptr ? ut_impl<128, false>(a, tfr, gws, xws, order, s) : ut_impl<128, true>(a, tfr, gws, xws, order, s);
+}
+
+hipError_t launch_gated_split(const GatedFwd& a, const uint16_t* tfr, const float* gws, const int32_t* order,
+                              uint16_t* statesT, hipStream_t s) {
+  if (int64_t(a.cu == nullptr ? a.B : a.N) * a.H == 0) return hipSuccess;
+  if (a.DK == 64)
+    return statesT == nullptr ? split_impl<64, false>(a, tfr, gws, order, statesT, s) : split_impl<64, true>(a, tfr, gws, order, statesT, s);
+  return statesT == nullptr ? split_impl<128, false>(a, tfr, gws, order, statesT, s) : split_impl<128, true>(a, tfr, gws, order, statesT, s);
+}
+
+hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s) {
+  const bool packed = a.cu != nullptr;
+  const GatedFwdLayout lay = gated_fwd_layout(a.B, a.N, a.H, a.L, packed);
+  auto* ws = static_cast<unsigned char*>(workspace);
+  auto* tfr = reinterpret_cast<uint16_t*>(ws + lay.t);
+  auto* gws = reinterpret_cast<float*>(ws + lay.g);
+  // packed: the caller's schedule, or one ranked by workgroups of the UT launch
+  int32_t* mine = packed && a.order == nullptr && a.N <= kGatedOrderedSeqs ? reinterpret_cast<int32_t*>(ws + lay.order) : nullptr;
+  if (hipError_t e = launch_gated_ut(a, tfr, gws, nullptr, mine, s); e != hipSuccess) return e;
+  return launch_gated_split(a, tfr, gws, mine != nullptr ? mine : a.order, nullptr, s);
+}
+
+}  // namespace efla

@@ -1,0 +1,254 @@
+// gated_ut.h -- the UT transform of the gated delta rule (gated.h) for bf16
+// inputs, one wavefront per chunk of 64 tokens.
+//
+// For a chunk with key rows K, coefficients a and gate sums G_i:
+//     A = tril(diag(a) (Gam * K K^T), -1),  Gam_ij = e^{G_i - G_j},
+//     X = (I + A)^{-1},  T = X diag(a).
+// The work is laid out as in ut_wave.h (K as row fragments straight from
+// memory, the four diagonal 16x16 blocks of X by forward substitution, the
+// blocks below by fp32 16x16x4 products out of registers), with the tiles of
+// K K^T scaled by Gam before they are used; Gam_ii = 1, so lambda still is
+// their diagonal.  Gates are kept as base-2 logarithms: e^{G_i - G_j} is one
+// v_exp_f32.
+//
+// Written per chunk slot:
+//   tfr  T as the recurrence's operand fragments, in two bf16 parts (T = hi +
+//        lo to 2^-16): [12][64 lanes][8], fragments (rt, ku) of the lower
+//        triangle as pf_index numbers them, high parts first.  A lane's tile
+//        of X_ij^T is half a fragment of row tile i, so T leaves the registers
+//        in that order, 1 KiB coalesced, and the recurrence loads it the same
+//        way, past the LDS.
+//   gws  [4][64] fp32: G log2(e), e^{G_i}, e^{G_C - G_i}, a.  Tokens past the
+//        end have a = 0 and G = G_C.
+//   BWD: also X as fp32 rows ([64][64], zeros above the diagonal).
+// Bound by HBM like ut_wave_kernel: 16 KiB of K read and 13 KiB written a chunk
+// at d_k 128.
+#pragma once
+
+#include "gated.h"
+#include "launchers.h"
+#include "lds_ring.h"
+#include "ut_wave.h"
+
+namespace efla {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kGatedT = 12 * 64 * 8;  // bf16 values of T per chunk slot
+constexpr int kGatedG = 4 * 64;       // floats of the gate block per chunk slot
+
+// e^{x} for x in base-2 logarithms
+__device__ __forceinline__ float exp2_gate(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// High and low bf16 parts of eight fp32 values (two accumulator tiles), x = hi + lo to 2^-16.
+__device__ __forceinline__ void split_frag(const f32x4& lo4, const f32x4& hi4, Frag<uint16_t>& h, Frag<uint16_t>& l) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float x = e < 4 ? lo4[e & 3] : hi4[e & 3];
+    h.v[e] = static_cast<__bf16>(x);
+    l.v[e] = static_cast<__bf16>(x - static_cast<float>(h.v[e]));
+  }
+}
+
+template <int DK, bool BWD = false>
+__global__ __launch_bounds__(256) void gated_ut_wave_kernel(const uint16_t* __restrict__ k,
+                                                            const uint16_t* __restrict__ beta,
+                                                            const float* __restrict__ gate, uint16_t* __restrict__ tfr,
+                                                            float* __restrict__ gws, int H, int Hk, int64_t L, int NC,
+                                                            int64_t nchunks, int rule, const int32_t* __restrict__ cu,
+                                                            int N, int64_t nwg_ut, int32_t* __restrict__ order,
+                                                            float* __restrict__ xws) {
+  constexpr int C = 64;
+  using S = UtWaveShape<DK, C>;
+  constexpr int NRT = S::NRT, NKU = S::NKU, GBLK = S::GBLK, XP = S::XP, XBLK = S::XBLK;
+  __shared__ __align__(16) unsigned char scratch_all[S::WAVES][S::SCRATCH];
+  __shared__ __align__(16) float a_all[S::WAVES][64];
+  __shared__ __align__(16) float g_all[S::WAVES][64];
+
+  if (order != nullptr && int64_t(blockIdx.x) >= nwg_ut) {  // packed batch: the workgroups after the chunks rank the sequences
+    rank_sequences<C>(cu, N, L, int(blockIdx.x - nwg_ut), order, reinterpret_cast<int*>(scratch_all));
+    return;
+  }
+  const int lane = threadIdx.x & 63, w = wave_id(), li = lane & 15, g = lane >> 4;
+  const int64_t id = int64_t(blockIdx.x) * S::WAVES + w;
+  if (id >= nchunks) return;  // no workgroup barriers below
+  SeqSpan sp;
+  int chunk;
+  const int64_t h = cu == nullptr ? (id / NC) % H : id / NC;
+  if (cu == nullptr) {
+    chunk = int(id % NC);
+    sp = seq_span<C>(nullptr, int(id / NC / H), h, H, L, NC);
+  } else if (!slot_chunk<C>(cu, N, id % NC, h, H, L, NC, sp, chunk)) {
+    return;  // a slot no chunk of the packed batch uses
+  }
+  const int64_t t0 = int64_t(chunk) * C;
+  const int valid = int(sp.len - t0 < C ? sp.len - t0 : C);
+  const int64_t tok0 = sp.bos + t0, row0 = tok0 * H + h;
+  const int64_t hk = h / (H / Hk);
+  float* Gs = reinterpret_cast<float*>(scratch_all[w]);  // [4][GBLK] diagonal blocks of Gam * K K^T, row-major
+  float* Xs = Gs + 4 * GBLK;                             // [4][XBLK] diagonal X blocks, column-major
+  float* as = a_all[w];
+  float* gs = g_all[w];
+
+  Frag<uint16_t> Kf[NRT][NKU];
+#pragma unroll
+  for (int rt = 0; rt < NRT; ++rt) {
+    const int t = 16 * rt + li;
+    const uint16_t* src = k + ((tok0 + t) * Hk + hk) * DK + 8 * g;
+#pragma unroll
+    for (int ku = 0; ku < NKU; ++ku) {
+      if (t < valid) Kf[rt][ku].v = *reinterpret_cast<const bf16x8*>(src + 32 * ku);
+      else Kf[rt][ku].v = bf16x8{};
+    }
+  }
+  float bt = 0.0f, G = 0.0f;
+  if (lane < valid) {
+    bt = to_f32(beta[row0 + int64_t(lane) * H]);
+    G = gate_floor(gate[row0 + int64_t(lane) * H]);
+  }
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {  // inclusive sum over the chunk's tokens
+    const float y = __shfl_up(G, d);
+    if (lane >= d) G += y;
+  }
+  G *= kLog2e;
+  gs[lane] = G;
+  const float Gend = __shfl(G, 63);
+  float* gdst = gws + id * kGatedG;
+  gdst[lane] = G;
+  gdst[64 + lane] = exp2_gate(G);
+  gdst[128 + lane] = exp2_gate(Gend - G);
+  wave_lds_order();
+
+  // Gam * K K^T: Gd[b] holds rows li, columns 4g.. of diagonal block b (K K^T
+  // is symmetric), Gu[i][m] the tile of block (i, m) transposed, m < i
+  f32x4 Gd[NRT];
+  f32x4 Gu[NRT][NRT];
+  float gr[NRT];
+  f32x4 gc[NRT];
+#pragma unroll
+  for (int b = 0; b < NRT; ++b) {
+    gr[b] = gs[16 * b + li];
+    gc[b] = *reinterpret_cast<const f32x4*>(gs + 16 * b + 4 * g);
+  }
+#pragma unroll
+  for (int bb = 0; bb < NRT; ++bb) {
+    Gd[bb] = zero4();
+#pragma unroll
+    for (int ku = 0; ku < NKU; ++ku) mma(Gd[bb], Kf[bb][ku], Kf[bb][ku]);
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) Gd[bb][qq] = 4 * g + qq <= li ? Gd[bb][qq] * exp2_gate(gr[bb] - gc[bb][qq]) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 1; i < NRT; ++i)
+#pragma unroll
+    for (int m = 0; m < i; ++m) {
+      Gu[i][m] = zero4();
+#pragma unroll
+      for (int ku = 0; ku < NKU; ++ku) mma(Gu[i][m], Kf[m][ku], Kf[i][ku]);
+#pragma unroll
+      for (int qq = 0; qq < 4; ++qq) Gu[i][m][qq] *= exp2_gate(gr[i] - gc[m][qq]);
+    }
+#pragma unroll
+  for (int bb = 0; bb < NRT; ++bb) *reinterpret_cast<f32x4*>(Gs + bb * GBLK + li * 16 + 4 * g) = Gd[bb];
+  wave_lds_order();
+  {
+    const float lam = Gs[(lane >> 4) * GBLK + (lane & 15) * 17];
+    const float a = (lane < valid) ? efla_alpha_rule(bt, lam, rule) : 0.0f;
+    as[lane] = a;
+    gdst[192 + lane] = a;
+  }
+  wave_lds_order();
+
+  // diagonal blocks of X by forward substitution, lane = (block, column)
+  {
+    const int bb = lane >> 4, c = lane & 15;
+    const float* Gb = Gs + bb * GBLK;
+    f32x4 ab[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) ab[j] = *reinterpret_cast<const f32x4*>(as + 16 * bb + 4 * j);
+    float x[16];
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+      for (int j = 0; 4 * j < r; ++j) {
+        const f32x4 grow = *reinterpret_cast<const f32x4*>(Gb + r * 16 + 4 * j);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int m = 4 * j + e;
+          if (m < r) {
+            if (e & 1) s1 = fmaf(grow[e], x[m], s1);
+            else s0 = fmaf(grow[e], x[m], s0);
+          }
+        }
+      }
+      x[r] = (r == c ? 1.0f : 0.0f) - ab[r / 4][r % 4] * (s0 + s1);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      *reinterpret_cast<f32x4*>(Xs + bb * XBLK + c * XP + 4 * j) = f32x4{x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]};
+  }
+  wave_lds_order();
+  // XTo[i][j] is the tile of X_ij^T (element qq of lane (li, g) = X[16 i + li][16 j + 4 g + qq])
+  f32x4 X[NRT][NRT], XTo[NRT][NRT];
+#pragma unroll
+  for (int bb = 0; bb < NRT; ++bb) {
+    X[bb][bb] = *reinterpret_cast<const f32x4*>(Xs + bb * XBLK + li * XP + 4 * g);
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) XTo[bb][bb][qq] = Xs[bb * XBLK + (4 * g + qq) * XP + li];
+  }
+  f32x4 arow[NRT];
+#pragma unroll
+  for (int i = 0; i < NRT; ++i) arow[i] = *reinterpret_cast<const f32x4*>(as + 16 * i + 4 * g);
+  wave_lds_order();
+#pragma unroll
+  for (int i = 1; i < NRT; ++i)
+#pragma unroll
+    for (int j = 0; j < i; ++j) {
+      f32x4 R = zero4();
+#pragma unroll
+      for (int m = j; m < i; ++m) mma16_f32(R, Gu[i][m], X[m][j]);
+#pragma unroll
+      for (int qq = 0; qq < 4; ++qq) R[qq] *= arow[i][qq];
+      f32x4 Y = zero4(), YT = zero4();
+      mma16_f32(Y, XTo[i][i], R);
+      mma16_f32(YT, R, XTo[i][i]);
+#pragma unroll
+      for (int qq = 0; qq < 4; ++qq) {
+        X[i][j][qq] = -Y[qq];
+        XTo[i][j][qq] = -YT[qq];
+      }
+    }
+  if constexpr (BWD) {  // X as rows, 16-byte pieces: a lane holds four columns of a row
+    float* xdst = xws + id * int64_t(C) * C;
+#pragma unroll
+    for (int i = 0; i < NRT; ++i)
+#pragma unroll
+      for (int j = 0; j < NRT; ++j) {
+        f32x4 x;
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) x[qq] = (j < i || (j == i && 4 * g + qq <= li)) ? XTo[i][j < i ? j : i][qq] : 0.0f;
+        __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(xdst + (16 * i + li) * C + 16 * j + 4 * g));
+      }
+  }
+  bf16x8* tdst = reinterpret_cast<bf16x8*>(tfr + id * kGatedT) + lane;
+#pragma unroll
+  for (int i = 0; i < NRT; ++i)
+#pragma unroll
+    for (int ku = 0; 32 * ku <= 16 * i + 15; ++ku) {
+      f32x4 t[2];
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int j = 2 * ku + p;
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq)
+          t[p][qq] = (j < i || (j == i && 4 * g + qq <= li)) ? XTo[i][j < i ? j : i][qq] * arow[j][qq] : 0.0f;
+      }
+      Frag<uint16_t> hi, lo;
+      split_frag(t[0], t[1], hi, lo);
+      tdst[pf_index(i, ku) * 64] = hi.v;
+      tdst[(6 + pf_index(i, ku)) * 64] = lo.v;
+    }
+}
+
+}  // namespace efla

@@ -164,6 +164,19 @@ struct GatedFwd {
 template <typename T>
 hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipStream_t s);
 
+// Chunked forward of bf16 inputs (gated_ut.h, gated_split.h): chunk 64, d_k 64
+// or 128, d_v a multiple of 32.  xws: X of every chunk, fp32, for the backward;
+// statesT: every chunk's start state, [slots][DV][DK] bf16.
+struct GatedFwdLayout {
+  size_t t, g, order, total;
+};
+bool gated_chunk_supported(int DK, int DV, int C);
+GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed);
+hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s);
+hipError_t launch_gated_ut(const GatedFwd& a, uint16_t* tfr, float* gws, float* xws, int32_t* order, hipStream_t s);
+hipError_t launch_gated_split(const GatedFwd& a, const uint16_t* tfr, const float* gws, const int32_t* order,
+                              uint16_t* statesT, hipStream_t s);
+
 struct GatedBwd {
   const void *q, *k, *v, *beta, *d_o;
   const float *g, *s0, *dsf;
