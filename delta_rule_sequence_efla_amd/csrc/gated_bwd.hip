@@ -1,7 +1,12 @@
-// gated_bwd.hip -- launches of the gated backward pass (gated_bwd.h).
-// Workspace, every region 256-byte aligned, per chunk slot ((b H + h) NC + n),
-// all fp32: T, X, P [C][C]; a, G [C]; S, dS [d_k][d_v]; and where key heads are
-// shared dq and dk per value head, [B L][H][d_k].
+// gated_bwd.hip -- the gated backward pass: which kernels run, and its
+// workspace, every region 256-byte aligned, per chunk slot ((b H + h) NC + n).
+//   fp32 arithmetic (gated_bwd.h; every type and size), all fp32:
+//     T, X, P [C][C]; a, G [C]; S, dS [d_k][d_v]
+//   bf16 matrix cores (bf16 inputs, chunk 64, d_k 64 or 128, d_v % 32 == 0):
+//     T fragments (12 KiB) and gate block (1 KiB) as the forward's, X fp32,
+//     T and P bf16 [C][C], Qe bf16 [C][d_k], S and dS bf16 [d_v][d_k]
+// and for both, where key heads are shared, dq and dk per value head in fp32,
+// [B L][H][d_k].
 #include "gated_bwd.h"
 
 namespace efla {
@@ -10,53 +15,99 @@ namespace {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
-static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, int DV, int C) {
+static bool gated_bwd_fast(int DK, int DV, int C, size_t esz) { return esz == 2 && gated_chunk_supported(DK, DV, C); }
+
+static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t esz) {
   const size_t slots = size_t(B) * H * ((L + C - 1) / C);
+  size_t at = 0;
+  auto region = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
   GatedBwdLayout w{};
-  w.t = 0;
-  w.x = w.t + align256(slots * C * C * 4);
-  w.p = w.x + align256(slots * C * C * 4);
-  w.a = w.p + align256(slots * C * C * 4);
-  w.gc = w.a + align256(slots * C * 4);
-  w.s = w.gc + align256(slots * C * 4);
-  w.ds = w.s + align256(slots * size_t(DK) * DV * 4);
-  w.dqh = w.ds + align256(slots * size_t(DK) * DV * 4);
-  const size_t heads = Hk < H ? align256(size_t(B) * L * H * DK * 4) : 0;
-  w.dkh = w.dqh + heads;
-  w.total = w.dkh + heads;
+  const bool fast = gated_bwd_fast(DK, DV, C, esz);
+  const size_t e = fast ? 2 : 4;
+  w.x = region(slots * C * C * 4);
+  w.t = region(slots * C * C * e);
+  w.p = region(slots * C * C * e);
+  w.s = region(slots * size_t(DK) * DV * e);
+  w.ds = region(slots * size_t(DK) * DV * e);
+  if (fast) {
+    w.tfr = region(slots * 12 * 1024);
+    w.gc = region(slots * 1024);
+    w.qe = region(slots * size_t(C) * DK * 2);
+  } else {
+    w.a = region(slots * C * 4);
+    w.gc = region(slots * C * 4);
+  }
+  const size_t heads = Hk < H ? size_t(B) * L * H * DK * 4 : 0;
+  w.dqh = region(heads);
+  w.dkh = region(heads);
+  w.total = at;
   return w;
 }
 
-size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t) {
-  return gated_bwd_layout(B, H, Hk, L, DK, DV, C).total;
+size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t esz) {
+  return gated_bwd_layout(B, H, Hk, L, DK, DV, C, esz).total;
+}
+
+// The forward's inputs, for the backward's recomputation.
+static GatedFwd forward_of(const GatedBwd& b) {
+  GatedFwd a{};
+  a.q = b.q;
+  a.k = b.k;
+  a.v = b.v;
+  a.beta = b.beta;
+  a.g = b.g;
+  a.s0 = b.s0;
+  a.B = b.B;
+  a.H = b.H;
+  a.Hk = b.Hk;
+  a.P = b.B;
+  a.L = b.L;
+  a.DK = b.DK;
+  a.DV = b.DV;
+  a.rule = b.rule;
+  return a;
+}
+
+// dq and dk of shared key heads from those of their value heads.
+template <typename T>
+static hipError_t sum_heads(const GatedBwd& b, const float* dqh, const float* dkh, hipStream_t s) {
+  const int64_t rows = int64_t(b.B) * b.L * b.Hk, n = rows * (b.DK / 4);
+  hipLaunchKernelGGL((gated_head_sum_kernel<T>), dim3(unsigned((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
+                     dqh, dkh, static_cast<T*>(b.dq), static_cast<T*>(b.dk), rows, b.H / b.Hk, b.DK);
+  return hipGetLastError();
+}
+
+static hipError_t gated_bwd_bf16(const GatedBwd& b, unsigned char* ws, hipStream_t s) {
+  const GatedBwdLayout lay = gated_bwd_layout(b.B, b.H, b.Hk, b.L, b.DK, b.DV, 64, 2);
+  auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
+  auto u = [&](size_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
+  const GatedFwd a = forward_of(b);
+  const bool shared = b.Hk < b.H;
+  hipError_t e = launch_gated_ut_bwd(a, u(lay.tfr), f(lay.gc), f(lay.x), u(lay.t), u(lay.p), u(lay.qe), s);
+  if (e == hipSuccess) e = launch_gated_states(a, u(lay.tfr), f(lay.gc), u(lay.s), s);
+  if (e == hipSuccess) e = launch_gated_reverse(b, u(lay.t), u(lay.qe), f(lay.gc), u(lay.ds), s);
+  if (e == hipSuccess)
+    e = launch_gated_bwd_chunk(b, u(lay.t), u(lay.p), f(lay.x), f(lay.gc), u(lay.s), u(lay.ds),
+                               shared ? f(lay.dqh) : nullptr, shared ? f(lay.dkh) : nullptr, s);
+  if (e == hipSuccess && shared) e = sum_heads<uint16_t>(b, f(lay.dqh), f(lay.dkh), s);
+  return e;
 }
 
 template <typename T, int DK, int C>
 static hipError_t gated_bwd_impl(const GatedBwd& b, unsigned char* ws, hipStream_t s) {
   const int NC = int((b.L + C - 1) / C);
   const int64_t bh = int64_t(b.B) * b.H, slots = bh * NC;
-  const GatedBwdLayout lay = gated_bwd_layout(b.B, b.H, b.Hk, b.L, DK, b.DV, C);
+  const GatedBwdLayout lay = gated_bwd_layout(b.B, b.H, b.Hk, b.L, DK, b.DV, C, sizeof(T));
   auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
   if (slots > 0) {
     hipLaunchKernelGGL((gated_ut_kernel<T, DK, C>), dim3(unsigned(slots)), dim3(kThreads), 0, s, b, f(lay.t), f(lay.x),
                        f(lay.p), f(lay.a), f(lay.gc), NC);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    GatedFwd a{};
-    a.q = b.q;
-    a.k = b.k;
-    a.v = b.v;
-    a.beta = b.beta;
-    a.g = b.g;
-    a.s0 = b.s0;
-    a.B = b.B;
-    a.H = b.H;
-    a.Hk = b.Hk;
-    a.P = b.B;
-    a.L = b.L;
-    a.DK = DK;
-    a.DV = b.DV;
-    a.rule = b.rule;
-    if (hipError_t e = launch_gated_recurrent<T>(a, f(lay.s), C, s); e != hipSuccess) return e;
+    if (hipError_t e = launch_gated_recurrent<T>(forward_of(b), f(lay.s), C, s); e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((gated_bwd_state_kernel<T, DK, C>), dim3(unsigned(bh * (b.DV / 16))), dim3(kThreads), 0, s, b,
                      f(lay.t), f(lay.p), f(lay.gc), f(lay.ds), NC, b.DV / 16);
@@ -67,12 +118,7 @@ static hipError_t gated_bwd_impl(const GatedBwd& b, unsigned char* ws, hipStream
                      f(lay.x), f(lay.p), f(lay.a), f(lay.gc), f(lay.s), f(lay.ds), shared ? f(lay.dqh) : nullptr,
                      shared ? f(lay.dkh) : nullptr, NC);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-  if (shared) {
-    const int64_t rows = int64_t(b.B) * b.L * b.Hk, n = rows * (DK / 4);
-    hipLaunchKernelGGL((gated_head_sum_kernel<T>), dim3(unsigned((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
-                       f(lay.dqh), f(lay.dkh), static_cast<T*>(b.dq), static_cast<T*>(b.dk), rows, b.H / b.Hk, DK);
-  }
-  return hipGetLastError();
+  return shared ? sum_heads<T>(b, f(lay.dqh), f(lay.dkh), s) : hipSuccess;
 }
 
 template <typename T, int DK>
@@ -88,6 +134,8 @@ static hipError_t gated_bwd_c(const GatedBwd& b, int C, unsigned char* ws, hipSt
 template <typename T>
 hipError_t launch_gated_bwd(const GatedBwd& b, int C, void* workspace, hipStream_t s) {
   auto* ws = static_cast<unsigned char*>(workspace);
+  // no chunk: only the state's gradient passes through, which the reverse pass of either does
+  if (b.L > 0 && gated_bwd_fast(b.DK, b.DV, C, sizeof(T))) return gated_bwd_bf16(b, ws, s);
   switch (b.DK) {
     case 16: return gated_bwd_c<T, 16>(b, C, ws, s);
     case 32: return gated_bwd_c<T, 32>(b, C, ws, s);

@@ -1,0 +1,563 @@
+// gated_bwd_chunk.h -- the per-chunk gradients of the gated backward for bf16
+// inputs, two workgroups per compute unit, in the form of bwd_chunk_tr.h (every
+// operand held once as a swizzled bf16 tile, read as rows or by transposing
+// reads; value blocks of 32 columns by direct transfers; eight wavefronts at
+// 128 VGPRs).
+//
+// The formulas are gated_bwd.h's.  What the gates add, and where it fits:
+//   * D = V - diag(e) K S and dU = P^T dO + diag(w) K dS' scale accumulator rows.
+//   * dK = diag(w) U dS'^T - diag(e) dD S^T: U and dD are needed unscaled too (for
+//     dP and dv), so the scaled operands are tiles of their own, rounded from the
+//     accumulators like the unscaled ones; diag(w) U takes V's place, which is
+//     read in the block's first phase alone, and V of the next block is fetched
+//     with the block's other operands.
+//   * Row sums for dg.  k_i . Y3_i = sum_c dD_ic (e K S)_ic and k_j . Y2_j = sum_c
+//     U_jc (w K dS')_jc: both factors sit in the same wavefront's accumulators
+//     one phase apart, so no product is added; q_i . Y1_i comes from dQ's
+//     accumulators before dP K is added.  <dS', S> is summed from the tiles.
+//   * M = dP0 * P + diag(a) N of gated_bwd.h: Q K^T is formed once more in fp32
+//     at the end (P itself was rounded to bf16), on the tiles that hold dP.
+// Shared key heads (SHARED): dq and dk of every value head leave in fp32, staged
+// as whole rows one after the other, and gated_head_sum_kernel adds them up.
+// 79 KiB of LDS; bound as bwd_chunk_tr_kernel by the latency of its loads.
+#pragma once
+
+#include <type_traits>
+
+#include "bwd_chunk_tr.h"
+#include "gated.h"
+#include "gated_ut.h"
+
+namespace efla {
+
+template <int DK>
+struct GatedTrShape : BwdTrShape<DK, 64> {
+  using B = BwdTrShape<DK, 64>;
+  static constexpr int C = 64;
+  static constexpr int EDT = B::LOOP_END;               // diag(e) dD (negated) [C][BV]
+  static constexpr int LOOP_END = EDT + C * B::BV * 2;
+  // row and column sums of M: behind dA in the region that held Q and dX, or
+  // (d_k 64) behind the tail's arrays
+  static constexpr int MSUM_BYTES = 2 * B::NRT * C * 4;
+  static constexpr bool MSUM_IN = B::TT + C * B::CPF * 4 + MSUM_BYTES <= B::A0;
+  static constexpr int MSUM = MSUM_IN ? B::TT + C * B::CPF * 4 : B::TAIL_END;
+  static constexpr int TAIL_END = MSUM_IN ? B::TAIL_END : B::TAIL_END + MSUM_BYTES;
+  static constexpr int FP = DK + 4;                     // pitch of fp32 rows staged for the stores
+  static_assert(B::TT + C * FP * 4 <= B::RED, "an fp32 tile of dq or dk fits over the tail's arrays");
+  static constexpr int BYTES = LOOP_END > TAIL_END ? LOOP_END : TAIL_END;
+};
+
+template <int DK, bool SHARED>
+__global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_tr_kernel(
+    GatedBwd b, const uint16_t* __restrict__ tws, const uint16_t* __restrict__ pws, const float* __restrict__ xws,
+    const float* __restrict__ gws, const uint16_t* __restrict__ states, const uint16_t* __restrict__ dstates,
+    float* __restrict__ dqh, float* __restrict__ dkh, int NC) {
+  using S = GatedTrShape<DK>;
+  constexpr int C = 64, BV = S::BV, NRT = S::NRT, NDT = S::NDT, NKU_D = S::NKU_D, NKU_C = S::NKU_C, NWV = S::NWV;
+  constexpr int NTH = S::NTH, NQ = S::NQ, NP = S::NP, CPF = S::CPF;
+  __shared__ __align__(1024) unsigned char lds[S::BYTES];
+  __shared__ __align__(16) float as[C], das[C], dls[C], lam[C];
+  __shared__ __align__(16) float gs[C], es[C], ws[C], ys[C];
+  __shared__ __align__(16) float xw[4][C];  // row sums: dD.(e K S) and U.(w K dS'), by tile column of the block
+  __shared__ float c0s[NWV];
+  auto b16 = [&](int off) { return reinterpret_cast<uint16_t*>(lds + off); };
+  auto f32p = [&](int off) { return reinterpret_cast<float*>(lds + off); };
+  uint16_t *Kt = b16(S::KT), *Tt = b16(S::TT), *Pt = b16(S::PT), *St = b16(S::ST), *dSt = b16(S::DST);
+  uint16_t *Vt = b16(S::VT), *dOt = b16(S::DOT), *Dt = b16(S::DT), *dUt = b16(S::DUT), *Ut = b16(S::UT);
+  uint16_t *dDt = b16(S::DDT), *eDt = b16(S::EDT), *Wt = Vt;
+
+  const int H = b.H, Hk = b.Hk, DV = b.DV;
+  const int64_t slot = blockIdx.x;
+  const int n = int(slot % NC);
+  const int64_t bh = slot / NC, h = bh % H, hk = h / (H / Hk);
+  const int64_t left = b.L - int64_t(n) * C;
+  const int valid = int(left < C ? left : C);
+  const int64_t tok0 = (bh / H) * b.L + int64_t(n) * C;
+  const int64_t row0 = tok0 * H + h, krow0 = tok0 * Hk + hk;
+  const int tid = threadIdx.x, lane0 = tid & 63, w = wave_id(), li0 = lane0 & 15, g0 = lane0 >> 4;
+  const int64_t k_stride = int64_t(Hk) * DK, v_stride = int64_t(H) * DV;
+  const auto* q = static_cast<const uint16_t*>(b.q);
+  const auto* k = static_cast<const uint16_t*>(b.k);
+  const auto* v = static_cast<const uint16_t*>(b.v);
+  const auto* dout = static_cast<const uint16_t*>(b.d_o);
+  auto* dv = static_cast<uint16_t*>(b.dv);
+  auto st16 = [](uint16_t* p, const u32x4& x) { *reinterpret_cast<u32x4*>(p) = x; };
+  constexpr u32x4 Z{0u, 0u, 0u, 0u};
+
+  // the chunk's K, T, P: direct transfers (rows of K past the end re-read row 0
+  // and are cleared with the first block's)
+  constexpr int UK = C * DK / 8;
+  static_assert(UK % NTH == 0, "whole units per thread");
+  typename S::TK dma_k;
+  typename S::TC dma_c;
+  dma_k.init(k_stride, lane0, w);
+  dma_c.init(C, lane0, w);
+  {
+    const auto* ks = static_cast<const uint16_t*>(uniform_ptr(k + krow0 * DK));
+    const auto* ts = static_cast<const uint16_t*>(uniform_ptr(tws + slot * C * C));
+    const auto* ps = static_cast<const uint16_t*>(uniform_ptr(pws + slot * C * C));
+#pragma unroll
+    for (int i = 0; i < S::TK::PER_WAVE; ++i) {
+      if (valid == C) dma_k.template issue<false>(i, lds_addr_of(Kt), ks, C);
+      else dma_k.template issue<true>(i, lds_addr_of(Kt), ks, valid);
+    }
+#pragma unroll
+    for (int i = 0; i < S::TC::PER_WAVE; ++i) {
+      dma_c.template issue<false>(i, lds_addr_of(Tt), ts, C);
+      dma_c.template issue<false>(i, lds_addr_of(Pt), ps, C);
+    }
+  }
+  if (tid < 4 * C) {
+    const float x = gws[slot * kGatedG + tid];
+    float* const to = tid < C ? gs : tid < 2 * C ? es : tid < 3 * C ? ws : as;
+    to[tid & (C - 1)] = x;
+    xw[tid >> 6][tid & 63] = 0.0f;
+  }
+
+  typename S::TS dma_s;
+  typename S::TV dma_v;
+  dma_s.init(DK, lane0, w);
+  dma_v.init(v_stride, lane0, w);
+  auto dma_rows = [&](uint16_t* dst, const uint16_t* src, int v0) {
+    const auto* sp_ = static_cast<const uint16_t*>(uniform_ptr(src + row0 * DV + v0));
+#pragma unroll
+    for (int i = 0; i < S::TV::PER_WAVE; ++i) {
+      if (valid == C) dma_v.template issue<false>(i, lds_addr_of(dst), sp_, C);
+      else dma_v.template issue<true>(i, lds_addr_of(dst), sp_, valid);
+    }
+  };
+  auto dma_block = [&](int v0) {
+    const auto* sb = static_cast<const uint16_t*>(uniform_ptr(states + (slot * DV + v0) * DK));
+    const auto* db = static_cast<const uint16_t*>(uniform_ptr(dstates + (slot * DV + v0) * DK));
+    dma_rows(Vt, v, v0);
+#pragma unroll
+    for (int i = 0; i < S::TS::PER_WAVE; ++i) {
+      dma_s.template issue<false>(i, lds_addr_of(St), sb, BV);
+      dma_s.template issue<false>(i, lds_addr_of(dSt), db, BV);
+    }
+    dma_rows(dOt, dout, v0);
+  };
+  auto put = [&](uint16_t* X, const f32x4& a, int rt, int c, int li, int g) {
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) X[swz_off<BV>(16 * rt + 4 * g + qq, 16 * c + li)] = from_f32<uint16_t>(a[qq]);
+  };
+
+  f32x4 dQa[NQ], dKa[NQ], dPa[NP], dTa[NP];
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) dQa[i] = dKa[i] = zero4();
+#pragma unroll
+  for (int i = 0; i < NP; ++i) dPa[i] = dTa[i] = zero4();
+  float c0 = 0.0f;  // this thread's part of <dS', S>
+
+  constexpr int UX = C * C / 4;  // 16-byte units of fp32 X
+  u32x4 rx[UX / NTH];
+  static_assert(UX % NTH == 0, "whole units per thread");
+
+  dma_block(0);
+  auto block = [&](const int v0, auto lastc) {
+    constexpr bool LAST = decltype(lastc)::value;
+    // lane indices the compiler cannot see through, so that fragment addresses
+    // are formed here rather than held across the loop
+    int li = li0, g = g0, lane = lane0, tidv = tid;
+    asm volatile("" : "+v"(li), "+v"(g), "+v"(lane), "+v"(tidv));
+    wait_vmcnt<0>();  // this wavefront's transfers of the block
+    if (valid < C) {
+      __syncthreads();  // every wavefront's transfers landed
+      for (int i = tidv; i < 2 * (C - valid) * (BV / 8); i += NTH) {
+        const int r = valid + (i >> 1) / (BV / 8), ch = (i >> 1) % (BV / 8);
+        st16(((i & 1) ? dOt : Vt) + swz_off<BV>(r, 8 * ch), Z);
+      }
+      if (v0 == 0)
+        for (int i = tidv; i < (C - valid) * (DK / 8); i += NTH)
+          st16(Kt + swzw_off<DK>(valid + i / (DK / 8), 8 * (i % (DK / 8))), Z);
+    }
+    __syncthreads();  // the block's operands in place (and the chunk's K, T, P, gates)
+    const int rt = w >> 1, c = w & 1;  // this wavefront's tile of the [C][BV] products
+    // D = V - diag(e) K S and dU = P^T dO + diag(w) K dS'
+    f32x4 d = zero4(), du = zero4(), eks, wkd;
+    {
+#pragma unroll
+      for (int ku = 0; ku < NKU_D; ++ku) {
+        const Frag<uint16_t> a = wide_frag<DK>(Kt, 16 * rt + li, ku, g);
+        mma(d, a, wide_frag<DK>(St, 16 * c + li, ku, g));
+        mma(du, a, wide_frag<DK>(dSt, 16 * c + li, ku, g));
+      }
+      const f32x4 e4 = *reinterpret_cast<const f32x4*>(es + 16 * rt + 4 * g);
+      const f32x4 w4 = *reinterpret_cast<const f32x4*>(ws + 16 * rt + 4 * g);
+#pragma unroll
+      for (int qq = 0; qq < 4; ++qq) {
+        eks[qq] = e4[qq] * d[qq];
+        wkd[qq] = w4[qq] * du[qq];
+      }
+      du = wkd;
+#pragma unroll
+      for (int ku = 0; ku < NKU_C; ++ku)
+        if (32 * ku + 31 >= 16 * rt) mma(du, sw_frag_tr<C>(Pt, 16 * rt, ku, lane), sw_frag_tr<BV>(dOt, 16 * c, ku, lane));
+      const bf16x4 vv = lds_read_tr(Vt + swz_off<BV>(16 * rt + 4 * g + (li >> 2), 16 * c + 4 * (li & 3)));
+#pragma unroll
+      for (int qq = 0; qq < 4; ++qq) d[qq] = static_cast<float>(vv[qq]) - eks[qq];
+      put(Dt, d, rt, c, li, g);
+      put(dUt, du, rt, c, li, g);
+      // <dS', S>: both tiles have one layout, eight elements a thread
+      if (tidv < BV * DK / 8) {
+        const bf16x8 sv = *reinterpret_cast<const bf16x8*>(St + 8 * tidv), dsv = *reinterpret_cast<const bf16x8*>(dSt + 8 * tidv);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) c0 = fmaf(static_cast<float>(sv[e]), static_cast<float>(dsv[e]), c0);
+      }
+    }
+    __syncthreads();
+    if constexpr (LAST) {
+#pragma unroll
+      for (int i = 0; i < UX / NTH; ++i) {
+        const int u = tidv + NTH * i, r = u / (C / 4), ch = u % (C / 4);
+        rx[i] = *reinterpret_cast<const u32x4*>(xws + slot * C * C + r * C + 4 * ch);
+      }
+    }
+    // U = T D and dD = T^T dU (= dV), and both scaled for dK
+    {
+      f32x4 u = zero4(), dd = zero4();
+#pragma unroll
+      for (int ku = 0; ku < NKU_C; ++ku) {
+        if (32 * ku <= 16 * rt + 15) mma(u, sw_frag<C>(Tt, 16 * rt + li, ku, g), sw_frag_tr<BV>(Dt, 16 * c, ku, lane));
+        if (32 * ku + 31 >= 16 * rt)
+          mma(dd, sw_frag_tr<C>(Tt, 16 * rt, ku, lane), sw_frag_tr<BV>(dUt, 16 * c, ku, lane));
+      }
+      put(Ut, u, rt, c, li, g);
+      put(dDt, dd, rt, c, li, g);
+      const f32x4 e4 = *reinterpret_cast<const f32x4*>(es + 16 * rt + 4 * g);
+      const f32x4 w4 = *reinterpret_cast<const f32x4*>(ws + 16 * rt + 4 * g);
+      float xs[4], wk[4];
+#pragma unroll
+      for (int qq = 0; qq < 4; ++qq) {
+        xs[qq] = row_sum16(dd[qq] * eks[qq]);
+        wk[qq] = row_sum16(u[qq] * wkd[qq]);
+        u[qq] *= w4[qq];
+        dd[qq] *= -e4[qq];
+      }
+      put(Wt, u, rt, c, li, g);
+      put(eDt, dd, rt, c, li, g);
+      if (li == 0) {  // one lane per row and tile column: its own place
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) {
+          xw[c][16 * rt + 4 * g + qq] += xs[qq];
+          xw[2 + c][16 * rt + 4 * g + qq] += wk[qq];
+        }
+      }
+    }
+    __syncthreads();
+    // dv = dD from its staged tile, as whole 64-byte row pieces
+    if (tidv < 4 * C) {
+      const int r = tidv >> 2, p = tidv & 3;
+      if (r < valid) {
+        const u32x4 x = *reinterpret_cast<const u32x4*>(dDt + r * BV + 8 * (p ^ swz_row<BV / 8>(r)));
+        __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(dv + row0 * DV + r * v_stride + v0 + 8 * p));
+      }
+    }
+    if (v0 + BV >= DV) {  // the tail's Q, during the last block (over T and P, done with)
+      const auto* qs = static_cast<const uint16_t*>(uniform_ptr(q + krow0 * DK));
+#pragma unroll
+      for (int i = 0; i < S::TK::PER_WAVE; ++i) {
+        if (valid == C) dma_k.template issue<false>(i, lds_addr_of(b16(S::QT)), qs, C);
+        else dma_k.template issue<true>(i, lds_addr_of(b16(S::QT)), qs, valid);
+      }
+    }
+    // dQ += dO S^T (unscaled);  dK += (w U) dS'^T + (-e dD) S^T;  dP0 += dO U^T;  dT += dU D^T
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
+      const Frag<uint16_t> bS = wide_frag_tr<DK>(St, dt, 0, lane);
+      mma(dQa[i], sw_frag<BV>(dOt, 16 * rr + li, 0, g), bS);
+      mma(dKa[i], sw_frag<BV>(Wt, 16 * rr + li, 0, g), wide_frag_tr<DK>(dSt, dt, 0, lane));
+      mma(dKa[i], sw_frag<BV>(eDt, 16 * rr + li, 0, g), bS);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int t = w + NWV * i, rr = t / NRT, jt = t % NRT;
+      if (jt <= rr) {
+        mma(dPa[i], sw_frag<BV>(dOt, 16 * rr + li, 0, g), sw_frag<BV>(Ut, 16 * jt + li, 0, g));
+        mma(dTa[i], sw_frag<BV>(dUt, 16 * rr + li, 0, g), sw_frag<BV>(Dt, 16 * jt + li, 0, g));
+      }
+    }
+    if (v0 + BV < DV) {
+      __syncthreads();  // every read of this block's operands done
+      dma_block(v0 + BV);
+    }
+  };
+  for (int v0 = 0; v0 + BV < DV; v0 += BV) block(v0, std::false_type{});
+  block(DV - BV, std::true_type{});
+  wait_vmcnt<0>();  // Q's transfers and X
+  __syncthreads();  // done with the loop's arrays (K stays); Q in place
+
+  // ---- the UT-transform part (bwd_chunk_tr.h), with the gates -----------------
+  const int li = li0, g = g0, lane = lane0;
+  uint16_t *Qt = b16(S::QT), *dPt = b16(S::DPT), *dXh = b16(S::DXH), *dXl = b16(S::DXL);
+  uint16_t *Wh = b16(S::WH), *Wl = b16(S::WL), *Xh = b16(S::XH), *Xl = b16(S::XL), *Eb = b16(S::EB);
+  uint16_t *dQs = b16(S::DQS), *dKs = b16(S::DKS);
+  float *A0 = f32p(S::A0), *dAf = f32p(S::DAF), *red = f32p(S::RED), *msum = f32p(S::MSUM);
+  constexpr int CPG = S::CPG;
+  constexpr int NPART = NTH / C, RPP = C / NPART;
+  const int cr = tid % C, prt = tid / C;
+  auto split = [](float x, uint16_t& hi, uint16_t& lo) {
+    hi = from_f32<uint16_t>(x);
+    lo = from_f32<uint16_t>(x - to_f32(hi));
+  };
+  auto mma3 = [](f32x4& acc, const Frag<uint16_t>& ah, const Frag<uint16_t>& al, const Frag<uint16_t>& bh_,
+                 const Frag<uint16_t>& bl) {
+    mma(acc, ah, bh_);
+    mma(acc, ah, bl);
+    mma(acc, al, bh_);
+  };
+#pragma unroll
+  for (int d = 32; d > 0; d >>= 1) c0 += __shfl_xor(c0, d);
+  if (lane == 0) c0s[w] = c0;
+  // rows of Q past the end re-read row 0: cleared before they are read
+  if (valid < C) {
+    for (int i = tid; i < (C - valid) * (DK / 8); i += NTH)
+      st16(Qt + swzw_off<DK>(valid + i / (DK / 8), 8 * (i % (DK / 8))), Z);
+    __syncthreads();
+  }
+  // Y1 = diag(e) dO S^T, and q . Y1 row by row (a wavefront's tiles lie in one
+  // or two columns dt: partial sums by dt)
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
+    const int cp = key_phys(16 * dt + li);
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) {
+      const int r = 16 * rr + 4 * g + qq;
+      dQa[i][qq] *= es[r];
+      const float s = row_sum16(dQa[i][qq] * to_f32(Qt[swzw_off<DK>(r, cp)]));
+      if (li == 0) red[dt * C + r] = s;
+    }
+  }
+  // dP = Gam * dP0 as bf16, dT fp32, X as high and low parts; the first part of
+  // M (strictly lower), dP * Q K^T, stays in registers
+  f32x4 M[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int t = w + NWV * i, rr = t / NRT, jt = t % NRT;
+    f32x4 qk = zero4();
+    if (jt <= rr) {
+#pragma unroll
+      for (int ku = 0; ku < NKU_D; ++ku)
+        mma(qk, wide_frag<DK>(Qt, 16 * rr + li, ku, g), wide_frag<DK>(Kt, 16 * jt + li, ku, g));
+    }
+    const float gj = gs[16 * jt + li];
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) {
+      const int r = 16 * rr + 4 * g + qq, c = 16 * jt + li;
+      const float p = c <= r ? dPa[i][qq] * exp2_gate(gs[r] - gj) : 0.0f;
+      M[i][qq] = c < r ? p * qk[qq] : 0.0f;
+      dPt[swz_off<C>(r, c)] = from_f32<uint16_t>(p);
+      A0[r * CPF + c] = c <= r ? dTa[i][qq] : 0.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < UX / NTH; ++i) {
+    const int u = tid + NTH * i, r = u / (C / 4), ch = u % (C / 4);
+    union {
+      u32x4 u;
+      float f[4];
+    } x;
+    x.u = rx[i];
+    uint16_t hi[4], lo[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split(x.f[e], hi[e], lo[e]);
+    *reinterpret_cast<uint2*>(Xh + swz_off<C>(r, 4 * ch)) = *reinterpret_cast<const uint2*>(hi);
+    *reinterpret_cast<uint2*>(Xl + swz_off<C>(r, 4 * ch)) = *reinterpret_cast<const uint2*>(lo);
+  }
+  __syncthreads();
+  if (tid < C) {  // y_i so far
+    float s = -(xw[0][tid] + xw[1][tid]);
+#pragma unroll
+    for (int j = 0; j < NDT; ++j) s += red[j * C + tid];
+    ys[tid] = s;
+  }
+  // dQ += dP K;  dK += dP^T Q
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
+#pragma unroll
+    for (int ku = 0; ku < NKU_C; ++ku) {
+      if (32 * ku <= 16 * rr + 15)
+        mma(dQa[i], sw_frag<C>(dPt, 16 * rr + li, ku, g), wide_frag_tr<DK>(Kt, dt, ku, lane));
+      if (32 * ku + 31 >= 16 * rr)
+        mma(dKa[i], sw_frag_tr<C>(dPt, 16 * rr, ku, lane), wide_frag_tr<DK>(Qt, dt, ku, lane));
+    }
+  }
+  __syncthreads();  // red is read, Q and dP are done with
+  // da_j = sum_i dT_ij X_ij (partial sums);  dX = dT diag(a), as high and low parts (over Q)
+  {
+    float s = 0.0f;
+#pragma unroll
+    for (int r = prt * RPP; r < (prt + 1) * RPP; ++r)
+      s = fmaf(A0[r * CPF + cr], to_f32(Xh[swz_off<C>(r, cr)]) + to_f32(Xl[swz_off<C>(r, cr)]), s);
+    red[prt * C + cr] = s;
+  }
+  for (int i = tid; i < C * C; i += NTH) {
+    const int r = i / C, c = i % C;
+    uint16_t hi, lo;
+    split(A0[r * CPF + c] * as[c], hi, lo);
+    dXh[swz_off<C>(r, c)] = hi;
+    dXl[swz_off<C>(r, c)] = lo;
+  }
+  __syncthreads();
+  if (tid < C) {
+    float s = 0.0f;
+#pragma unroll
+    for (int p = 0; p < NPART; ++p) s += red[p * C + tid];
+    das[tid] = s;
+  }
+  // W = X^T dX, as high and low parts (over dT)
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int t = w + NWV * i, rr = t / NRT, jt = t % NRT;
+    f32x4 acc = zero4();
+#pragma unroll
+    for (int ku = 0; ku < NKU_C; ++ku)
+      if (32 * ku + 31 >= 16 * rr && 32 * ku + 31 >= 16 * jt)  // X and dT are lower triangular
+        mma3(acc, sw_frag_tr<C>(Xh, 16 * rr, ku, lane), sw_frag_tr<C>(Xl, 16 * rr, ku, lane),
+             sw_frag_tr<C>(dXh, 16 * jt, ku, lane), sw_frag_tr<C>(dXl, 16 * jt, ku, lane));
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) {
+      const int r = 16 * rr + 4 * g + qq, c = 16 * jt + li;
+      uint16_t hi, lo;
+      split(acc[qq], hi, lo);
+      Wh[swz_off<C>(r, c)] = hi;
+      Wl[swz_off<C>(r, c)] = lo;
+    }
+  }
+  __syncthreads();
+  // Gam dA = -Gam * (W X^T) (strictly lower, fp32, over dX);  K K^T on the lower
+  // tiles: lambda, N = Gam dA * K K^T and M += diag(a) N, with their sums
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int t = w + NWV * i, rr = t / NRT, jt = t % NRT;
+    f32x4 acc = zero4(), gg = zero4();
+    if (jt <= rr) {
+#pragma unroll
+      for (int ku = 0; ku < NKU_C; ++ku)
+        if (32 * ku <= 16 * jt + 15)  // X^T's rows of this tile are zero past column 16 jt + 15
+          mma3(acc, sw_frag<C>(Wh, 16 * rr + li, ku, g), sw_frag<C>(Wl, 16 * rr + li, ku, g),
+               sw_frag<C>(Xh, 16 * jt + li, ku, g), sw_frag<C>(Xl, 16 * jt + li, ku, g));
+#pragma unroll
+      for (int ku = 0; ku < NKU_D; ++ku)
+        mma(gg, wide_frag<DK>(Kt, 16 * rr + li, ku, g), wide_frag<DK>(Kt, 16 * jt + li, ku, g));
+    }
+    const float gj = gs[16 * jt + li];
+    float cs = 0.0f;
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) {
+      const int r = 16 * rr + 4 * g + qq, c = 16 * jt + li;
+      const float da = c < r ? -acc[qq] * exp2_gate(gs[r] - gj) : 0.0f;
+      dAf[r * CPF + c] = da;
+      if (c == r) lam[r] = gg[qq];
+      const float nn = da * gg[qq];
+      const float m = fmaf(as[r], nn, M[i][qq]);
+      cs += m;
+      const float s = row_sum16(nn), sm = row_sum16(m);
+      if (li == 0) {
+        red[jt * C + r] = s;
+        msum[jt * C + r] = sm;
+      }
+    }
+    cs += __shfl_xor(cs, 16);
+    cs += __shfl_xor(cs, 32);
+    if (g == 0) msum[(NRT + rr) * C + 16 * jt + li] = cs;
+  }
+  __syncthreads();
+  // da_i += sum_j N_ij, then dbeta and dlambda;  dg;  dG + dG^T as bf16 (over X)
+  if (tid < C) {
+    float s = das[tid], y = ys[tid];
+#pragma unroll
+    for (int jt = 0; jt < NRT; ++jt) {
+      s += red[jt * C + tid];
+      y += msum[jt * C + tid] - msum[(NRT + jt) * C + tid];
+    }
+    float dl = 0.0f;
+    if (tid < valid) {
+      const float bt = to_f32(static_cast<const uint16_t*>(b.beta)[row0 + int64_t(tid) * H]);
+      float da_db, da_dl;
+      efla_alpha_grad(bt, lam[tid], b.rule, da_db, da_dl);
+      dl = s * da_dl;
+      static_cast<uint16_t*>(b.dbeta)[row0 + int64_t(tid) * H] = from_f32<uint16_t>(s * da_db);
+    }
+    dls[tid] = dl;
+    // dg_t = e^{G_C} <dS', S> + sum_{j<t} k_j . Y2_j + sum_{i>=t} y_i  (tid < C: one wavefront)
+    const float wj = xw[2][tid] + xw[3][tid];
+    float before = wj, after = y, all = 0.0f;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const float p = __shfl_up(before, d), z = __shfl_down(after, d);
+      if (tid >= d) before += p;
+      if (tid + d < kWave) after += z;
+    }
+#pragma unroll
+    for (int j = 0; j < NWV; ++j) all += c0s[j];
+    if (tid < valid)
+      static_cast<uint16_t*>(b.dg)[row0 + int64_t(tid) * H] = from_f32<uint16_t>(fmaf(es[C - 1], all, before - wj + after));
+  }
+  for (int i = tid; i < C * C; i += NTH) {
+    const int r = i / C, c = i % C;
+    Eb[swz_off<C>(r, c)] = from_f32<uint16_t>(as[r] * dAf[r * CPF + c] + as[c] * dAf[c * CPF + r]);
+  }
+  __syncthreads();
+  // dK += (dG + dG^T) K + 2 diag(dlambda) K
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
+#pragma unroll
+    for (int ku = 0; ku < NKU_C; ++ku)
+      mma(dKa[i], sw_frag<C>(Eb, 16 * rr + li, ku, g), wide_frag_tr<DK>(Kt, dt, ku, lane));
+    const int cp = key_phys(16 * dt + li);
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) {
+      const int r = 16 * rr + 4 * g + qq;
+      dKa[i][qq] = fmaf(2.0f * dls[r], to_f32(Kt[swzw_off<DK>(r, cp)]), dKa[i][qq]);
+      if constexpr (!SHARED) {  // dQ and dK staged as bf16 rows (physical key columns) over W and dA
+        dQs[r * CPG + cp] = from_f32<uint16_t>(dQa[i][qq]);
+        dKs[r * CPG + cp] = from_f32<uint16_t>(dKa[i][qq]);
+      }
+    }
+  }
+  __syncthreads();
+  if constexpr (!SHARED) {
+    auto* dq = static_cast<uint16_t*>(b.dq);
+    auto* dk = static_cast<uint16_t*>(b.dk);
+#pragma unroll
+    for (int i = 0; i < UK / NTH; ++i) {
+      const int u = tid + NTH * i, r = u / (DK / 8), ch = u % (DK / 8);
+      if (r < valid) {
+        __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(dQs + r * CPG + 8 * ch),
+                                    reinterpret_cast<u32x4*>(dq + krow0 * DK + r * k_stride + 8 * ch));
+        __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(dKs + r * CPG + 8 * ch),
+                                    reinterpret_cast<u32x4*>(dk + krow0 * DK + r * k_stride + 8 * ch));
+      }
+    }
+  } else {  // fp32 rows of this value head, dq then dk through one staging tile
+    float* F = f32p(S::TT);
+    constexpr int FP = S::FP, UF = C * DK / 4;
+    auto leave = [&](const f32x4 (&acc)[NQ], float* dst) {
+#pragma unroll
+      for (int i = 0; i < NQ; ++i) {
+        const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
+        const int cp = key_phys(16 * dt + li);
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) F[(16 * rr + 4 * g + qq) * FP + cp] = acc[i][qq];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < UF / NTH; ++i) {
+        const int u = tid + NTH * i, r = u / (DK / 4), ch = u % (DK / 4);
+        if (r < valid)
+          *reinterpret_cast<f32x4*>(dst + (row0 + int64_t(r) * H) * DK + 4 * ch) =
+              *reinterpret_cast<const f32x4*>(F + r * FP + 4 * ch);
+      }
+    };
+    leave(dQa, dqh);
+    __syncthreads();
+    leave(dKa, dkh);
+  }
+}
+
+}  // namespace efla

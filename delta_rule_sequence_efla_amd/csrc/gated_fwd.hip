@@ -14,7 +14,7 @@ constexpr int kGatedChunk = 64;
 constexpr int kGatedOrderedSeqs = 4096;
 
 template <int DK, bool BWD>
-hipError_t ut_impl(const GatedFwd& a, uint16_t* tfr, float* gws, float* xws, int32_t* order, hipStream_t s) {
+hipError_t ut_impl(const GatedFwd& a, uint16_t* tfr, float* gws, const GatedUtBwd& b, int32_t* order, hipStream_t s) {
   const int NC = a.cu == nullptr ? int((a.L + kGatedChunk - 1) / kGatedChunk) : int(a.L / kGatedChunk) + a.N;
   const int64_t nchunks = int64_t(a.cu == nullptr ? a.B : 1) * a.H * NC;
   constexpr int W = UtWaveShape<DK, kGatedChunk>::WAVES;
@@ -25,17 +25,17 @@ hipError_t ut_impl(const GatedFwd& a, uint16_t* tfr, float* gws, float* xws, int
   if (nwg + nrank == 0) return hipSuccess;
   hipLaunchKernelGGL((gated_ut_wave_kernel<DK, BWD>), dim3(unsigned(nwg + nrank)), dim3(kThreads), 0, s,
                      static_cast<const uint16_t*>(a.k), static_cast<const uint16_t*>(a.beta), a.g, tfr, gws, a.H, a.Hk,
-                     a.L, NC, nchunks, a.rule, a.cu, a.N, nwg, order, xws);
+                     a.L, NC, nchunks, a.rule, a.cu, a.N, nwg, order, b);
   return hipGetLastError();
 }
 
-template <int DK, bool SAVE>
+template <int DK, bool OUT>
 hipError_t split_impl(const GatedFwd& a, const uint16_t* tfr, const float* gws, const int32_t* order,
                       uint16_t* statesT, hipStream_t s) {
   const int NC = a.cu == nullptr ? int((a.L + kGatedChunk - 1) / kGatedChunk) : int(a.L / kGatedChunk) + a.N;
   const int64_t bh = int64_t(a.cu == nullptr ? a.B : a.N) * a.H;
   const int NVB = a.DV / 32;
-  hipLaunchKernelGGL((gated_split_kernel<DK, SAVE>), dim3(unsigned(bh * NVB)), dim3(GatedSplitShape<DK>::THREADS), 0, s,
+  hipLaunchKernelGGL((gated_split_kernel<DK, OUT>), dim3(unsigned(bh * NVB)), dim3(GatedSplitShape<DK>::THREADS), 0, s,
                      a, tfr, gws, order, NC, NVB, bh % 8 == 0 ? 1 : 0, statesT);
   return hipGetLastError();
 }
@@ -55,17 +55,16 @@ GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed) {
   return w;
 }
 
-hipError_t launch_gated_ut(const GatedFwd& a, uint16_t* tfr, float* gws, float* xws, int32_t* order, hipStream_t s) {
-  if (a.DK == 64) return xws == nullptr ? ut_impl<64, false>(a, tfr, gws, xws, order, s) : ut_impl<64, true>(a, tfr, gws, xws, order, s);
-  return xws == nullptr ? ut_impl<128, false>(a, tfr, gws, xws, order, s) : ut_impl<128, true>(a, tfr, gws, xws, order, s);
+hipError_t launch_gated_ut_bwd(const GatedFwd& a, uint16_t* tfr, float* gws, float* x, uint16_t* t, uint16_t* p,
+                               uint16_t* qe, hipStream_t s) {
+  const GatedUtBwd b{static_cast<const uint16_t*>(a.q), x, t, p, qe};
+  return a.DK == 64 ? ut_impl<64, true>(a, tfr, gws, b, nullptr, s) : ut_impl<128, true>(a, tfr, gws, b, nullptr, s);
 }
 
-hipError_t launch_gated_split(const GatedFwd& a, const uint16_t* tfr, const float* gws, const int32_t* order,
-                              uint16_t* statesT, hipStream_t s) {
-  if (int64_t(a.cu == nullptr ? a.B : a.N) * a.H == 0) return hipSuccess;
-  if (a.DK == 64)
-    return statesT == nullptr ? split_impl<64, false>(a, tfr, gws, order, statesT, s) : split_impl<64, true>(a, tfr, gws, order, statesT, s);
-  return statesT == nullptr ? split_impl<128, false>(a, tfr, gws, order, statesT, s) : split_impl<128, true>(a, tfr, gws, order, statesT, s);
+hipError_t launch_gated_states(const GatedFwd& a, const uint16_t* tfr, const float* gws, uint16_t* statesT,
+                               hipStream_t s) {
+  return a.DK == 64 ? split_impl<64, false>(a, tfr, gws, nullptr, statesT, s)
+                    : split_impl<128, false>(a, tfr, gws, nullptr, statesT, s);
 }
 
 hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s) {
@@ -76,8 +75,11 @@ hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s)
   auto* gws = reinterpret_cast<float*>(ws + lay.g);
   // packed: the caller's schedule, or one ranked by workgroups of the UT launch
   int32_t* mine = packed && a.order == nullptr && a.N <= kGatedOrderedSeqs ? reinterpret_cast<int32_t*>(ws + lay.order) : nullptr;
-  if (hipError_t e = launch_gated_ut(a, tfr, gws, nullptr, mine, s); e != hipSuccess) return e;
-  return launch_gated_split(a, tfr, gws, mine != nullptr ? mine : a.order, nullptr, s);
+  const GatedUtBwd none{};
+  const hipError_t e = a.DK == 64 ? ut_impl<64, false>(a, tfr, gws, none, mine, s) : ut_impl<128, false>(a, tfr, gws, none, mine, s);
+  if (e != hipSuccess) return e;
+  const int32_t* order = mine != nullptr ? mine : a.order;
+  return a.DK == 64 ? split_impl<64, true>(a, tfr, gws, order, nullptr, s) : split_impl<128, true>(a, tfr, gws, order, nullptr, s);
 }
 
 }  // namespace efla

@@ -56,9 +56,11 @@ struct GatedSplitShape {
   static constexpr int THREADS = 8 * kWave;
 };
 
-// SAVE: also the state at the start of every chunk as the high operand parts,
-// transposed, [slots][DV][DK] (the layout of recurrence_split.h).
-template <int DK, bool SAVE>
+// OUT: writes o and the final state.  Else (the backward's recomputation) the
+// state at the start of every chunk instead, as the high operand parts,
+// transposed, [slots][DV][DK] (the layout of recurrence_split.h); the O and P
+// waves idle and Q is not brought in.
+template <int DK, bool OUT>
 __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint16_t* __restrict__ tfr,
                                                           const float* __restrict__ gws,
                                                           const int32_t* __restrict__ order, int NC, int NVB, int remap,
@@ -129,7 +131,7 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
     // The schedule of recurrence_split.h: chunk n+3 goes into chunk n's slot
     // half after barrier B of step n and half after barrier A of step n+1; a
     // wait is for all but one chunk's transfers.
-    constexpr int D = S::COUNT;
+    constexpr int D = OUT ? S::COUNT : S::COUNT - S::PQ;  // Q comes last
     static_assert(D < 64, "one chunk's transfers fit the vmcnt counter");
     typename S::TQ tq;
     typename S::TV tv;
@@ -247,7 +249,7 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
       }
 #pragma unroll
       for (int ku = 0; ku < NKU_C; ++ku) {
-        bU_buf[ct][ku][lane] = acc_frag<uint16_t>(U[2 * ku], U[2 * ku + 1]).v;
+        if constexpr (OUT) bU_buf[ct][ku][lane] = acc_frag<uint16_t>(U[2 * ku], U[2 * ku + 1]).v;
 #pragma unroll
         for (int qq = 0; qq < 4; ++qq) {
           U[2 * ku][qq] *= wg[2 * ku][qq];
@@ -312,7 +314,7 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
       for (int d = 0; d < 2 * KH; ++d)
 #pragma unroll
         for (int kt = 0; kt < NKU_C; ++kt) KT[d][kt] = wide_frag_tr<DK>(cur + S::KOFF, dt0 + d, kt, lane);
-      if constexpr (SAVE) save(n);
+      if constexpr (!OUT) save(n);
 #pragma unroll
       for (int d = 0; d < 2 * KH; ++d)
 #pragma unroll
@@ -334,7 +336,7 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
         }
       publish();
     });
-    if (a.sfin != nullptr && srow >= 0) {
+    if (OUT && a.sfin != nullptr && srow >= 0) {
       float* sf = a.sfin + (srow * H + h) * DK * DV + v0 + li;
 #pragma unroll
       for (int d = 0; d < 2 * KH; ++d)
@@ -343,6 +345,11 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
 #pragma unroll
           for (int qq = 0; qq < 4; ++qq)
             sf[int64_t(key_phys(16 * (dt0 + d) + 4 * g + qq)) * DV + 16 * c] = St[d][c][qq];
+    }
+  } else if (!OUT) {
+    for (int n = 0; n < nc; ++n) {
+      barrier_nowait();
+      barrier_nowait();
     }
   } else if (role == S::kO0 || role == S::kO1) {
     // ------------------------------------------------------------- output

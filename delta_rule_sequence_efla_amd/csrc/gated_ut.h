@@ -20,7 +20,11 @@
 //        way, past the LDS.
 //   gws  [4][64] fp32: G log2(e), e^{G_i}, e^{G_C - G_i}, a.  Tokens past the
 //        end have a = 0 and G = G_C.
-//   BWD: also X as fp32 rows ([64][64], zeros above the diagonal).
+//   BWD: also what the backward's passes read, as rows: X fp32 and T bf16
+//        ([64][64], zeros above the diagonal), P = Gam * tril(Q K^T) bf16, and
+//        the effective queries Qe = diag(e^G) Q - P T diag(e^G) K, bf16
+//        [64][d_k], through which the output reads the chunk's start state
+//        (O = Qe S + P T V), formed from registers as in ut_wave.h.
 // Bound by HBM like ut_wave_kernel: 16 KiB of K read and 13 KiB written a chunk
 // at d_k 128.
 #pragma once
@@ -31,6 +35,13 @@
 #include "ut_wave.h"
 
 namespace efla {
+
+// What the backward instance reads and writes besides (null otherwise).
+struct GatedUtBwd {
+  const uint16_t* q;
+  float* x;
+  uint16_t *t, *p, *qe;
+};
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kGatedT = 12 * 64 * 8;  // bf16 values of T per chunk slot
@@ -56,7 +67,7 @@ __global__ __launch_bounds__(256) void gated_ut_wave_kernel(const uint16_t* __re
                                                             float* __restrict__ gws, int H, int Hk, int64_t L, int NC,
                                                             int64_t nchunks, int rule, const int32_t* __restrict__ cu,
                                                             int N, int64_t nwg_ut, int32_t* __restrict__ order,
-                                                            float* __restrict__ xws) {
+                                                            GatedUtBwd b) {
   constexpr int C = 64;
   using S = UtWaveShape<DK, C>;
   constexpr int NRT = S::NRT, NKU = S::NKU, GBLK = S::GBLK, XP = S::XP, XBLK = S::XBLK;
@@ -219,18 +230,6 @@ __global__ __launch_bounds__(256) void gated_ut_wave_kernel(const uint16_t* __re
         XTo[i][j][qq] = -YT[qq];
       }
     }
-  if constexpr (BWD) {  // X as rows, 16-byte pieces: a lane holds four columns of a row
-    float* xdst = xws + id * int64_t(C) * C;
-#pragma unroll
-    for (int i = 0; i < NRT; ++i)
-#pragma unroll
-      for (int j = 0; j < NRT; ++j) {
-        f32x4 x;
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq) x[qq] = (j < i || (j == i && 4 * g + qq <= li)) ? XTo[i][j < i ? j : i][qq] : 0.0f;
-        __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(xdst + (16 * i + li) * C + 16 * j + 4 * g));
-      }
-  }
   bf16x8* tdst = reinterpret_cast<bf16x8*>(tfr + id * kGatedT) + lane;
 #pragma unroll
   for (int i = 0; i < NRT; ++i)
@@ -249,6 +248,150 @@ __global__ __launch_bounds__(256) void gated_ut_wave_kernel(const uint16_t* __re
       tdst[pf_index(i, ku) * 64] = hi.v;
       tdst[(6 + pf_index(i, ku)) * 64] = lo.v;
     }
+  if constexpr (BWD) {
+    constexpr int TP = S::TP, NKC = C / 32;
+    uint16_t* Ts = reinterpret_cast<uint16_t*>(scratch_all[w]);  // [C][TP] staging
+    float* xdst = b.x + id * int64_t(C) * C;
+    float e_row[NRT];
+#pragma unroll
+    for (int i = 0; i < NRT; ++i) e_row[i] = exp2_gate(gr[i]);
+    // X as rows, a lane's four columns a piece; T staged as bf16 rows
+#pragma unroll
+    for (int i = 0; i < NRT; ++i)
+#pragma unroll
+      for (int j = 0; j < NRT; ++j) {
+        f32x4 x;
+        bf16x4 tv;
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) {
+          x[qq] = (j < i || (j == i && 4 * g + qq <= li)) ? XTo[i][j < i ? j : i][qq] : 0.0f;
+          tv[qq] = static_cast<__bf16>(x[qq] * arow[j][qq]);
+        }
+        __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(xdst + (16 * i + li) * C + 16 * j + 4 * g));
+        *reinterpret_cast<bf16x4*>(Ts + (16 * i + li) * TP + 16 * j + 4 * g) = tv;
+      }
+    auto store_rows = [&](uint16_t* dst) {  // the staging tile as 16-byte row pieces
+      wave_lds_order();
+#pragma unroll
+      for (int idx = lane; idx < C * (C / 8); idx += 64) {
+        const int r = idx / (C / 8), c0 = (idx % (C / 8)) * 8;
+        __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(Ts + r * TP + c0),
+                                    reinterpret_cast<u32x4*>(dst + r * C + c0));
+      }
+      wave_lds_order();
+    };
+    store_rows(b.t + id * int64_t(C) * C);
+    Frag<uint16_t> Qr[NRT][NKU];
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt) {
+      const int t = 16 * rt + li;
+#pragma unroll
+      for (int ku = 0; ku < NKU; ++ku) {
+        Qr[rt][ku].v = bf16x8{};
+        if (t < valid)
+          Qr[rt][ku].v = *reinterpret_cast<const bf16x8*>(b.q + ((tok0 + t) * Hk + hk) * DK + 32 * ku + 8 * g);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NRT; ++r)
+#pragma unroll
+      for (int c = 0; c < NRT; ++c) {
+        f32x4 acc = zero4();
+        if (c <= r) {
+#pragma unroll
+          for (int ku = 0; ku < NKU; ++ku) mma(acc, Qr[r][ku], Kf[c][ku]);
+        }
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) {
+          const int ii = 16 * r + 4 * g + qq, jj = 16 * c + li;
+          Ts[ii * TP + jj] = from_f32<uint16_t>(jj <= ii ? acc[qq] * exp2_gate(gc[r][qq] - gr[c]) : 0.0f);
+        }
+      }
+    store_rows(b.p + id * int64_t(C) * C);
+    // P^T as B operand fragments, ku <= rt / 2 (P is lower triangular)
+    Frag<uint16_t> PtB[NRT][NKC];
+#pragma unroll
+    for (int rt = 0; rt < NRT; ++rt)
+#pragma unroll
+      for (int ku = 0; ku < NKC; ++ku)
+        if (2 * ku <= rt) {
+          const bf16x4 lo = *reinterpret_cast<const bf16x4*>(Ts + (16 * rt + li) * TP + 32 * ku + 4 * g);
+          const bf16x4 hi = *reinterpret_cast<const bf16x4*>(Ts + (16 * rt + li) * TP + 32 * ku + 16 + 4 * g);
+          PtB[rt][ku].v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        }
+    float acol[NRT];
+#pragma unroll
+    for (int j = 0; j < NRT; ++j) acol[j] = as[16 * j + li];
+    f32x4 PTt[NRT][NRT];  // [j][rt]: (P T)^T[16 j + 4 g + qq][16 rt + li]
+#pragma unroll
+    for (int j = 0; j < NRT; ++j)
+#pragma unroll
+      for (int rt = 0; rt < NRT; ++rt) {
+        PTt[j][rt] = zero4();
+        if (j > rt) continue;
+#pragma unroll
+        for (int ku = j / 2; ku <= rt / 2; ++ku) {
+          f32x4 lo = zero4(), hi = zero4();
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq) {
+            if (j <= 2 * ku) lo[qq] = X[2 * ku][j][qq] * acol[j];
+            if (j <= 2 * ku + 1) hi[qq] = X[2 * ku + 1][j][qq] * acol[j];
+          }
+          mma(PTt[j][rt], acc_frag<uint16_t>(lo, hi), PtB[rt][ku]);
+        }
+      }
+    // rows (tokens) scaled by e^G: (P T diag(e^G))^T
+#pragma unroll
+    for (int j = 0; j < NRT; ++j) {
+      f32x4 ej;
+#pragma unroll
+      for (int qq = 0; qq < 4; ++qq) ej[qq] = exp2_gate(gc[j][qq]);
+#pragma unroll
+      for (int rt = j; rt < NRT; ++rt)
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) PTt[j][rt][qq] *= ej[qq];
+    }
+    Frag<uint16_t> PTB[NKC][NRT];
+#pragma unroll
+    for (int ku = 0; ku < NKC; ++ku)
+#pragma unroll
+      for (int rt = 0; rt < NRT; ++rt)
+        if (2 * ku <= rt) PTB[ku][rt] = acc_frag<uint16_t>(PTt[2 * ku][rt], PTt[2 * ku + 1][rt]);
+    uint16_t* qdst = b.qe + id * int64_t(C) * DK;
+#pragma unroll
+    for (int ku2 = 0; ku2 < NKU; ++ku2) {
+      f32x4 Cq[2][NRT];  // [h][rt]: (P T diag(e^G) K)[16 rt + li][32 ku2 + 8 g + 4 h + qq]
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        Frag<uint16_t> sel;  // picks dim 32 ku2 + 8 (li / 4) + 4 hh + li % 4 for column li
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          sel.v[e] = static_cast<__bf16>((g == (li >> 2) && e == 4 * hh + (li & 3)) ? 1.0f : 0.0f);
+        f32x4 ZK[NRT];
+#pragma unroll
+        for (int tb = 0; tb < NRT; ++tb) {
+          ZK[tb] = zero4();
+          mma(ZK[tb], Kf[tb][ku2], sel);
+        }
+#pragma unroll
+        for (int rt = 0; rt < NRT; ++rt) {
+          Cq[hh][rt] = zero4();
+#pragma unroll
+          for (int ku = 0; 2 * ku <= rt; ++ku)
+            mma(Cq[hh][rt], acc_frag<uint16_t>(ZK[2 * ku], ZK[2 * ku + 1]), PTB[ku][rt]);
+        }
+      }
+#pragma unroll
+      for (int rt = 0; rt < NRT; ++rt) {
+        const bf16x8 qv = Qr[rt][ku2].v;
+        bf16x8 o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          o[e] = static_cast<__bf16>(fmaf(e_row[rt], static_cast<float>(qv[e]), -Cq[e / 4][rt][e % 4]));
+        __builtin_nontemporal_store(o, reinterpret_cast<bf16x8*>(qdst + (16 * rt + li) * DK + 32 * ku2 + 8 * g));
+      }
+    }
+  }
 }
 
 }  // namespace efla

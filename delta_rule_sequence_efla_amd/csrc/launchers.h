@@ -165,17 +165,20 @@ template <typename T>
 hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipStream_t s);
 
 // Chunked forward of bf16 inputs (gated_ut.h, gated_split.h): chunk 64, d_k 64
-// or 128, d_v a multiple of 32.  xws: X of every chunk, fp32, for the backward;
-// statesT: every chunk's start state, [slots][DV][DK] bf16.
+// or 128, d_v a multiple of 32.
 struct GatedFwdLayout {
   size_t t, g, order, total;
 };
 bool gated_chunk_supported(int DK, int DV, int C);
 GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed);
 hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s);
-hipError_t launch_gated_ut(const GatedFwd& a, uint16_t* tfr, float* gws, float* xws, int32_t* order, hipStream_t s);
-hipError_t launch_gated_split(const GatedFwd& a, const uint16_t* tfr, const float* gws, const int32_t* order,
-                              uint16_t* statesT, hipStream_t s);
+// Its two launches as the backward runs them over a dense batch: T fragments and
+// gate blocks as the forward's, X (fp32), T, P and Qe as rows; then every
+// chunk's start state, [slots][DV][DK] bf16.
+hipError_t launch_gated_ut_bwd(const GatedFwd& a, uint16_t* tfr, float* gws, float* x, uint16_t* t, uint16_t* p,
+                               uint16_t* qe, hipStream_t s);
+hipError_t launch_gated_states(const GatedFwd& a, const uint16_t* tfr, const float* gws, uint16_t* statesT,
+                               hipStream_t s);
 
 struct GatedBwd {
   const void *q, *k, *v, *beta, *d_o;
@@ -188,6 +191,15 @@ struct GatedBwd {
 size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t esz);
 template <typename T>
 hipError_t launch_gated_bwd(const GatedBwd& b, int C, void* ws, hipStream_t s);
+// The backward's passes for bf16 inputs at the chunked forward's shapes: the
+// reverse pass over the chunks (gated_reverse.h), dS' of every chunk as
+// [slots][DV][DK] bf16, and the per-chunk gradients (gated_bwd_chunk.h); dqh,
+// dkh as in gated_bwd.h.
+hipError_t launch_gated_reverse(const GatedBwd& b, const uint16_t* t, const uint16_t* qe, const float* gws,
+                                uint16_t* dstatesT, hipStream_t s);
+hipError_t launch_gated_bwd_chunk(const GatedBwd& b, const uint16_t* t, const uint16_t* p, const float* x,
+                                  const float* gws, const uint16_t* statesT, const uint16_t* dstatesT, float* dqh,
+                                  float* dkh, hipStream_t s);
 
 // Tables of a packed batch (plan.hip); order, seq, pos and starts nullable.
 hipError_t launch_plan(const int32_t* lengths, const int32_t* starts, int N, int T, int C, int32_t* cu,
