@@ -15,9 +15,21 @@ namespace {
 size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
-static bool gated_bwd_fast(int DK, int DV, int C, size_t esz) { return esz == 2 && gated_chunk_supported(DK, DV, C); }
+// Sequences this short run in fp32 (chunk 16) for bf16 inputs too: dq and dk of
+// a few tokens are keys and queries times single scalar products dO_i . U_j,
+// which cancel by chance, so the bf16 rounding of U shows in them (8e-3 of dq
+// at two tokens and two key heads; from some tens of scalars on, 4e-3 at most).
+// Either way the call is four or five launches of a few microseconds.
+constexpr int64_t kShort = 16;
+static bool gated_bwd_fast(int64_t L, int DK, int DV, int C, size_t esz) {
+  return esz == 2 && L > kShort && gated_chunk_supported(DK, DV, C);
+}
+// chunk of the fp32 kernels (the result does not depend on it)
+static int fp32_chunk(int64_t L, int C) { return L <= kShort ? 16 : C; }
 
 static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t esz) {
+  const bool fast = gated_bwd_fast(L, DK, DV, C, esz);
+  if (!fast) C = fp32_chunk(L, C);
   const size_t slots = size_t(B) * H * ((L + C - 1) / C);
   size_t at = 0;
   auto region = [&](size_t bytes) {
@@ -26,7 +38,6 @@ static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, 
     return here;
   };
   GatedBwdLayout w{};
-  const bool fast = gated_bwd_fast(DK, DV, C, esz);
   const size_t e = fast ? 2 : 4;
   w.x = region(slots * C * C * 4);
   w.t = region(slots * C * C * e);
@@ -134,8 +145,8 @@ static hipError_t gated_bwd_c(const GatedBwd& b, int C, unsigned char* ws, hipSt
 template <typename T>
 hipError_t launch_gated_bwd(const GatedBwd& b, int C, void* workspace, hipStream_t s) {
   auto* ws = static_cast<unsigned char*>(workspace);
-  // no chunk: only the state's gradient passes through, which the reverse pass of either does
-  if (b.L > 0 && gated_bwd_fast(b.DK, b.DV, C, sizeof(T))) return gated_bwd_bf16(b, ws, s);
+  if (gated_bwd_fast(b.L, b.DK, b.DV, C, sizeof(T))) return gated_bwd_bf16(b, ws, s);
+  C = fp32_chunk(b.L, C);
   switch (b.DK) {
     case 16: return gated_bwd_c<T, 16>(b, C, ws, s);
     case 32: return gated_bwd_c<T, 32>(b, C, ws, s);

@@ -184,13 +184,12 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
     const int ct = role == S::kY1 ? 1 : 0;
     Frag<uint16_t> Kf[NRT][NKU_D];
     bf16x4 Vt[NRT];
-    f32x4 eg[NRT], wg[NRT];
+    f32x4 eg[NRT];
     struct TFrag {
       Frag<uint16_t> h[6], l[6];
-    };
-    TFrag T0, T1;
-    auto load_t = [&](TFrag& T, int m) {
-      const bf16x8* src = reinterpret_cast<const bf16x8*>(tfr + (sp.slot0 + m) * kGatedT) + lane;
+    } T;
+    auto load_t = [&](int m) {
+      const bf16x8* src = reinterpret_cast<const bf16x8*>(tfr + (sp.slot0 + (m < nc ? m : nc - 1)) * kGatedT) + lane;
 #pragma unroll
       for (int f = 0; f < 6; ++f) {
         T.h[f].v = src[f * 64];
@@ -205,28 +204,30 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
       for (int rt = 0; rt < NRT; ++rt) {
         Vt[rt] = lds_read_tr(Vs + swz_off<BV>(16 * rt + 4 * g + (li >> 2), 16 * ct + 4 * (li & 3)));
         eg[rt] = *reinterpret_cast<const f32x4*>(gt + 64 + 16 * rt + 4 * g);
-        wg[rt] = *reinterpret_cast<const f32x4*>(gt + 128 + 16 * rt + 4 * g);
       }
 #pragma unroll
       for (int ku = 0; ku < NKU_D; ++ku)
 #pragma unroll
         for (int rt = 0; rt < NRT; ++rt) Kf[rt][ku] = wide_frag<DK>(Ks, 16 * rt + li, ku, g);
     };
-    auto step = [&](TFrag& T, int n) {
+    auto step = [&](int n) {
       sync();  // A
       if (n == 0) load(ring);
+      Frag<uint16_t> sh[NKU_D], sl[NKU_D];
+#pragma unroll
+      for (int ku = 0; ku < NKU_D; ++ku) {
+        sh[ku].v = bS_buf[0][ct][ku][lane];
+        sl[ku].v = bS_buf[1][ct][ku][lane];
+      }
       f32x4 Y[NRT];
 #pragma unroll
       for (int rt = 0; rt < NRT; ++rt) Y[rt] = zero4();
 #pragma unroll
       for (int ku = 0; ku < NKU_D; ++ku) {
-        Frag<uint16_t> sh, sl;
-        sh.v = bS_buf[0][ct][ku][lane];
-        sl.v = bS_buf[1][ct][ku][lane];
 #pragma unroll
-        for (int rt = 0; rt < NRT; ++rt) mma(Y[rt], Kf[rt][ku], sh);
+        for (int rt = 0; rt < NRT; ++rt) mma(Y[rt], Kf[rt][ku], sh[ku]);
 #pragma unroll
-        for (int rt = 0; rt < NRT; ++rt) mma(Y[rt], Kf[rt][ku], sl);
+        for (int rt = 0; rt < NRT; ++rt) mma(Y[rt], Kf[rt][ku], sl[ku]);
       }
 #pragma unroll
       for (int rt = 0; rt < NRT; ++rt)
@@ -235,9 +236,12 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
       Frag<uint16_t> dh[NKU_C], dl[NKU_C];
 #pragma unroll
       for (int ku = 0; ku < NKU_C; ++ku) split_frag(Y[2 * ku], Y[2 * ku + 1], dh[ku], dl[ku]);
-      f32x4 U[NRT];
+      f32x4 U[NRT], wg[NRT];  // w read here: held from load() on, the registers would spill
 #pragma unroll
-      for (int rt = 0; rt < NRT; ++rt) U[rt] = zero4();
+      for (int rt = 0; rt < NRT; ++rt) {
+        U[rt] = zero4();
+        wg[rt] = *reinterpret_cast<const f32x4*>(gates(ring + (n % 3) * S::SLOT) + 128 + 16 * rt + 4 * g);
+      }
 #pragma unroll
       for (int kk = 0; kk < NKU_C; ++kk) {
 #pragma unroll
@@ -261,15 +265,15 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
         bW_buf[1][ct][ku][lane] = wl.v;
       }
       sync();  // B
-      if (n + 2 < nc) load_t(T, n + 2);
-      if (n + 1 < nc) load(ring + ((n + 1) % 3) * S::SLOT);
+      // Past the last chunk the loads go on, from the last chunk's slot and
+      // whatever the ring holds, and nothing reads what they bring: behind a
+      // branch, the loaded registers would be merged with the old ones, with a
+      // wait there.
+      load_t(n + 1);
+      load(ring + ((n + 1) % 3) * S::SLOT);
     };
-    if (nc > 0) load_t(T0, 0);
-    if (nc > 1) load_t(T1, 1);
-    for (int n = 0; n < nc; n += 2) {
-      step(T0, n);
-      if (n + 1 < nc) step(T1, n + 1);
-    }
+    if (nc > 0) load_t(0);
+    for (int n = 0; n < nc; ++n) step(n);
   } else if (role == S::kS0 || role == S::kS1) {
     // ----------------------------------------------------------------- S
     // rows: logical key dims 64 hh .. (k-units KH hh .. KH hh + KH - 1)
@@ -306,8 +310,17 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
       }
     };
     publish();
+    // T of a later chunk touched line by line, 6 KiB by each S wave in its idle
+    // phase, so that the Y waves' loads half a chunk ahead find it in L2
+    uint32_t warm = 0, seen = 0;
     run([&](const uint16_t* __restrict__ cur, const uint16_t*, int n) {
       sync();  // A
+      seen |= warm;
+      {
+        const int m = n + 3 < nc ? n + 3 : nc - 1;
+        const auto* line = reinterpret_cast<const uint32_t*>(tfr + (sp.slot0 + m) * kGatedT) + 32 * (48 * hh + (lane < 48 ? lane : 47));
+        warm = *line;
+      }
       Frag<uint16_t> KT[2 * KH][NKU_C];
       const float end = gates(cur)[64 + 63];
 #pragma unroll
@@ -320,7 +333,10 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
 #pragma unroll
         for (int c = 0; c < NT; ++c)
 #pragma unroll
-          for (int qq = 0; qq < 4; ++qq) St[d][c][qq] *= end;
+          for (int qq = 0; qq < 4; ++qq) {
+            St[d][c][qq] *= end;
+            asm volatile("" : "+v"(St[d][c][qq]));  // here, not past the barrier, where S is the chunk's critical work
+          }
       sync();  // B
 #pragma unroll
       for (int c = 0; c < NT; ++c)
@@ -336,6 +352,7 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
         }
       publish();
     });
+    if (seen == 0x7fc1a5e3u && lane == 64) ring[0] = 1;  // never: keeps the loads above
     if (OUT && a.sfin != nullptr && srow >= 0) {
       float* sf = a.sfin + (srow * H + h) * DK * DV + v0 + li;
 #pragma unroll

@@ -13,6 +13,11 @@ namespace efla {
 // step is bound by HBM (8 d_k d_v bytes a head).  One workgroup per request,
 // head and DVW value columns; thread (rg, cq) keeps columns 4 cq .. 4 cq + 3 of
 // rows rg, rg + NRG, .. in registers, and r and p are summed through LDS.
+// States are read and written past the caches (nontemporal): a step touches
+// each once, and a model's other layers run before the next one.  256 requests
+// of 16 heads, d 128 (541 MB, three pools in turn): 106.7 us with ordinary
+// accesses and whole states per workgroup, 99.4 us nontemporal, 96.3 us with 64
+// columns a workgroup, 98.2 us with 32 (a large in-place copy's rate: 89 us).
 // A row of the batch whose slot lies outside the pool has no request: its
 // state does not exist and its row of o is left as it was.
 template <typename T, int DK, int DVW>
@@ -35,13 +40,14 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(
   if (row < 0) return;
   const int64_t uk = int64_t(n) * Hk + h / (H / Hk);
   const int tid = threadIdx.x, cq = tid % NCQ, rg = tid / NCQ;
-  const bool on = rg < NRG;
+  const bool on = NRG * NCQ == kThreads || rg < NRG;
   float* Su = state + (row * H + h) * DK * DV + v0;
 
   f32x4 S[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
-    S[i] = on ? *reinterpret_cast<const f32x4*>(Su + int64_t(rg + i * NRG) * DV + 4 * cq) : zero4();
+    S[i] = on ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(Su + int64_t(rg + i * NRG) * DV + 4 * cq))
+              : zero4();
   if (tid < DK) {
     ks[tid] = to_f32(k[uk * DK + tid]);
     qs[tid] = to_f32(q[uk * DK + tid]);
@@ -96,7 +102,7 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(
       f32x4 x;
 #pragma unroll
       for (int c = 0; c < 4; ++c) x[c] = fmaf(kk, uq[c], e * S[i][c]);
-      *reinterpret_cast<f32x4*>(Su + int64_t(rg + i * NRG) * DV + 4 * cq) = x;
+      __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(Su + int64_t(rg + i * NRG) * DV + 4 * cq));
     }
   }
 }
@@ -114,14 +120,14 @@ static hipError_t gated_step_impl(const GatedStep& a, hipStream_t s) {
 
 template <typename T, int DK>
 static hipError_t gated_step_dv(const GatedStep& a, hipStream_t s) {
-  // Whole states per workgroup; few heads in all are cut into blocks of 32
-  // value columns so that more compute units share the loads.
-  const bool cut = int64_t(a.N) * a.H < 512;
+  // 64 value columns a workgroup (above); where that gives the compute units
+  // less than four workgroups each, 32, so that more of them share the loads.
+  const bool cut = int64_t(a.N) * a.H * (a.DV / 64) < 1024;
   switch (a.DV) {
     case 16: return gated_step_impl<T, DK, 16>(a, s);
     case 32: return gated_step_impl<T, DK, 32>(a, s);
     case 64: return cut ? gated_step_impl<T, DK, 32>(a, s) : gated_step_impl<T, DK, 64>(a, s);
-    case 128: return cut ? gated_step_impl<T, DK, 32>(a, s) : gated_step_impl<T, DK, 128>(a, s);
+    case 128: return cut ? gated_step_impl<T, DK, 32>(a, s) : gated_step_impl<T, DK, 64>(a, s);
   }
   return hipErrorInvalidValue;
 }
@@ -151,6 +157,9 @@ template hipError_t launch_gated_step<uint16_t>(const GatedStep&, hipStream_t);
 // r -> u -> S alone.  With `states`, the state before every C-th token is
 // stored, [chunk slot][d_k][d_v] fp32 (the backward's chunk starts; C % 16 == 0).
 template <typename T, int N> struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Piece { T e[N]; };
+template <int NK> struct Token {
+  float k[NK], q[NK], v, a, e;
+};
 
 template <typename T, int DK>
 __global__ __launch_bounds__(kThreads) void gated_recurrent_kernel(GatedFwd a, float* __restrict__ states, int C,
@@ -224,13 +233,54 @@ __global__ __launch_bounds__(kThreads) void gated_recurrent_kernel(GatedFwd a, f
     if (o != nullptr && t < len) o[t * H * DV + pc] = from_f32<T>(oS[b][tok][pc]);
   };
 
+  auto fetch = [&](Token<NK>& x, int b, int j) {
+#pragma unroll
+    for (int e = 0; e < NK; ++e) {
+      x.k[e] = kS[b][j][li * NK + e];
+      x.q[e] = qS[b][j][li * NK + e];
+    }
+    x.v = vS[b][j][col];
+    x.a = aS[b][j];
+    x.e = eS[b][j];
+  };
+  auto token = [&](const Token<NK>& x, int b, int j) {
+    float r0 = 0.0f, r1 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < NK; ++e) {
+      if (e & 1) r1 = fmaf(x.k[e], S[e], r1);
+      else r0 = fmaf(x.k[e], S[e], r0);
+    }
+    const float r = row_sum16(r0 + r1);
+    const float u = x.a * fmaf(-x.e, r, x.v);
+    float p0 = 0.0f, p1 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < NK; ++e) {
+      S[e] = fmaf(x.k[e], u, x.e * S[e]);
+      if (e & 1) p1 = fmaf(x.q[e], S[e], p1);
+      else p0 = fmaf(x.q[e], S[e], p0);
+    }
+    const float p = row_sum16(p0 + p1);
+    if (li == 0) oS[b][j][col] = p;
+  };
+
   const int64_t slot0 = int64_t(unit) * NC;  // dense batches only
-  if (len > 0) {
-    load(0);
-    stage(0);
-    if (TB < len) load(TB);
-    __syncthreads();
+  auto finish = [&]() {
+    if (a.sfin == nullptr || row < 0) return;
+    float* sf = a.sfin + (row * H + h) * DK * DV + v0 + col;
+#pragma unroll
+    for (int e = 0; e < NK; ++e) sf[int64_t(li * NK + e) * DV] = S[e];
+  };
+  if (len <= 0) {
+    finish();
+    return;
   }
+  // (staging waits for the first block's loads and, in order, for S before
+  // them: were the loop reachable with S in flight, every block would wait for
+  // the next block's loads at its first token)
+  load(0);
+  stage(0);
+  if (TB < len) load(TB);
+  __syncthreads();
   for (int64_t t0 = 0; t0 < len; t0 += TB) {
     const int b = int(t0 / TB) & 1;
     if (states != nullptr && t0 % C == 0) {
@@ -239,31 +289,15 @@ __global__ __launch_bounds__(kThreads) void gated_recurrent_kernel(GatedFwd a, f
       for (int e = 0; e < NK; ++e) dst[int64_t(li * NK + e) * DV] = S[e];
     }
     const int cnt = int(len - t0 < TB ? len - t0 : TB);
-    for (int j = 0; j < cnt; ++j) {
-      float kk[NK], qq[NK];
-#pragma unroll
-      for (int e = 0; e < NK; ++e) {
-        kk[e] = kS[b][j][li * NK + e];
-        qq[e] = qS[b][j][li * NK + e];
-      }
-      const float eg = eS[b][j];
-      float r0 = 0.0f, r1 = 0.0f;
-#pragma unroll
-      for (int e = 0; e < NK; ++e) {
-        if (e & 1) r1 = fmaf(kk[e], S[e], r1);
-        else r0 = fmaf(kk[e], S[e], r0);
-      }
-      const float r = row_sum16(r0 + r1);
-      const float u = aS[b][j] * fmaf(-eg, r, vS[b][j][col]);
-      float p0 = 0.0f, p1 = 0.0f;
-#pragma unroll
-      for (int e = 0; e < NK; ++e) {
-        S[e] = fmaf(kk[e], u, eg * S[e]);
-        if (e & 1) p1 = fmaf(qq[e], S[e], p1);
-        else p0 = fmaf(qq[e], S[e], p0);
-      }
-      const float p = row_sum16(p0 + p1);
-      if (li == 0) oS[b][j][col] = p;
+    // a token's values are read from the LDS while the one before is worked on
+    Token<NK> now, next;
+    fetch(now, b, 0);
+    for (int j = 0; j < cnt; j += 2) {
+      fetch(next, b, j + 1 < TB ? j + 1 : j);
+      token(now, b, j);
+      if (j + 1 >= cnt) break;
+      fetch(now, b, j + 2 < TB ? j + 2 : j);
+      token(next, b, j + 1);
     }
     if (t0 + TB < len) {
       stage(b ^ 1);  // last read two blocks ago, before the barrier below
@@ -272,11 +306,7 @@ __global__ __launch_bounds__(kThreads) void gated_recurrent_kernel(GatedFwd a, f
     __syncthreads();
     store(t0, b);  // oS[b] is written again two blocks on, after the next barrier
   }
-  if (a.sfin != nullptr && row >= 0) {
-    float* sf = a.sfin + (row * H + h) * DK * DV + v0 + col;
-#pragma unroll
-    for (int e = 0; e < NK; ++e) sf[int64_t(li * NK + e) * DV] = S[e];
-  }
+  finish();
 }
 
 template <typename T>

@@ -50,14 +50,25 @@ constexpr int kGatedG = 4 * 64;       // floats of the gate block per chunk slot
 // e^{x} for x in base-2 logarithms
 __device__ __forceinline__ float exp2_gate(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// High and low bf16 parts of eight fp32 values (two accumulator tiles), x = hi + lo to 2^-16.
+// High and low bf16 parts of eight fp32 values (two accumulator tiles), x = hi +
+// lo to 2^-16, two values at a time: one packed conversion, the high parts back
+// as floats by a shift and a mask, and one packed conversion of what is left
+// (element by element the compiler converts every high part twice).
 __device__ __forceinline__ void split_frag(const f32x4& lo4, const f32x4& hi4, Frag<uint16_t>& h, Frag<uint16_t>& l) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  u32x4 hp, lp;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float x = e < 4 ? lo4[e & 3] : hi4[e & 3];
-    h.v[e] = static_cast<__bf16>(x);
-    l.v[e] = static_cast<__bf16>(x - static_cast<float>(h.v[e]));
+  for (int e = 0; e < 4; ++e) {
+    const f32x4& src = e < 2 ? lo4 : hi4;
+    const f32x2 x{src[2 * (e & 1)], src[2 * (e & 1) + 1]};
+    const uint32_t p = __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
+    const f32x2 rest{x[0] - __uint_as_float(p << 16), x[1] - __uint_as_float(p & 0xffff0000u)};
+    hp[e] = p;
+    lp[e] = __builtin_bit_cast(uint32_t, __builtin_convertvector(rest, bf16x2));
   }
+  h.v = __builtin_bit_cast(bf16x8, hp);
+  l.v = __builtin_bit_cast(bf16x8, lp);
 }
 
 template <int DK, bool BWD = false>

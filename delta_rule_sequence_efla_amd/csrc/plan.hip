@@ -42,23 +42,21 @@ __device__ __forceinline__ int plan_length(const int32_t* __restrict__ lengths, 
   return l < 0 ? 0 : (l > T ? T : l);
 }
 
-// end[u] (u < N) = min(l_0 + .. + l_u, T), by all kThreads threads; wsum: kThreads / 64 ints of LDS.
-__device__ __forceinline__ void plan_ends(const int32_t* __restrict__ lengths, int N, int T, int32_t* end, int* wsum) {
+// end[u] (u < N) = min(l_0 + .. + l_u, T) in place of l_u, by all kThreads
+// threads, thread t on `per` consecutive entries; end: LDS; wsum: kThreads / 64
+// ints of LDS.
+__device__ __forceinline__ void scan_lds(int N, int T, int32_t* end, int* wsum) {
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-  int carry = 0;
-  for (int base = 0; base < N; base += kThreads) {
-    const int u = base + tid;
-    const int x = wave_scan_sat(u < N ? plan_length(lengths, u, T) : 0, lane, T);
-    __syncthreads();  // the last round's wsum is read
-    if (lane == kWave - 1) wsum[w] = x;
-    __syncthreads();
-    int before = carry;
-    for (int j = 0; j < kThreads / kWave; ++j) {
-      if (j < w) before = sat_add(before, wsum[j], T);
-      carry = sat_add(carry, wsum[j], T);
-    }
-    if (u < N) end[u] = sat_add(before, x, T);
-  }
+  const int per = (N + kThreads - 1) / kThreads, a = tid * per, z = a + per < N ? a + per : N;
+  int sum = 0;
+  for (int u = a; u < z; ++u) end[u] = sum = sat_add(sum, end[u], T);
+  const int x = wave_scan_sat(sum, lane, T);
+  if (lane == kWave - 1) wsum[w] = x;
+  __syncthreads();
+  int before = __shfl_up(x, 1);
+  if (lane == 0) before = 0;
+  for (int j = 0; j < w; ++j) before = sat_add(before, wsum[j], T);
+  for (int u = a; u < z; ++u) end[u] = sat_add(before, end[u], T);
   __syncthreads();
 }
 
@@ -72,8 +70,9 @@ __device__ __forceinline__ int plan_seq(const int32_t* end, int N, int t) {
   }
   return lo;
 }
-__device__ __forceinline__ int plan_chunks(const int32_t* end, int u, int C) {
-  return (end[u] - (u > 0 ? end[u - 1] : 0) + C - 1) / C;
+// chunks of 2^shift tokens
+__device__ __forceinline__ int plan_chunks(const int32_t* end, int u, int shift) {
+  return (end[u] - (u > 0 ? end[u - 1] : 0) + (1 << shift) - 1) >> shift;
 }
 
 __device__ __forceinline__ void plan_rows(const int32_t* end, int N, int T, const int32_t* __restrict__ starts,
@@ -91,23 +90,26 @@ __device__ __forceinline__ void plan_rows(const int32_t* end, int N, int T, cons
 }  // namespace
 
 __global__ __launch_bounds__(kThreads) void plan_kernel(const int32_t* __restrict__ lengths,
-                                                        const int32_t* __restrict__ starts, int N, int T, int C,
-                                                        int32_t* __restrict__ cu, int32_t* __restrict__ order,
+                                                        const int32_t* __restrict__ starts, int N, int T,
+                                                        int shift, int32_t* __restrict__ cu, int32_t* __restrict__ order,
                                                         int32_t* __restrict__ seq, int32_t* __restrict__ pos) {
   __shared__ int32_t end[kPlanSeqs];
   __shared__ int wsum[kThreads / kWave];
-  plan_ends(lengths, N, T, end, wsum);
   const int tid = threadIdx.x;
+  for (int u = tid; u < N; u += kThreads) end[u] = plan_length(lengths, u, T);
+  __syncthreads();
+  scan_lds(N, T, end, wsum);
   if (blockIdx.x == 0) {
     for (int u = tid; u <= N; u += kThreads) cu[u] = u > 0 ? end[u - 1] : 0;
   }
   // rank(u) = #{v : n(v) > n(u)} + #{v < u : n(v) = n(u)}
   const int u = int(blockIdx.x) * kPlanRank + (tid >> 4);
   if (order != nullptr && int(blockIdx.x) * kPlanRank < N) {
-    const int nu = u < N ? plan_chunks(end, u, C) : 0;
+    const int nu = u < N ? plan_chunks(end, u, shift) : 0;
     int rank = 0;
+#pragma unroll 4
     for (int x = tid & 15; x < N; x += 16) {
-      const int nv = plan_chunks(end, x, C);
+      const int nv = plan_chunks(end, x, shift);
       rank += (nv > nu || (nv == nu && x < u)) ? 1 : 0;
     }
 #pragma unroll
@@ -119,9 +121,19 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const int32_t* __restric
 
 __global__ __launch_bounds__(kThreads) void plan_offsets_kernel(const int32_t* __restrict__ lengths, int N, int T,
                                                                 int32_t* __restrict__ cu, int32_t* __restrict__ order) {
+  __shared__ int32_t end[kPlanSeqs];
   __shared__ int wsum[kThreads / kWave];
   if (threadIdx.x == 0) cu[0] = 0;
-  plan_ends(lengths, N, T, cu + 1, wsum);
+  int carry = 0;  // the same in every thread
+  for (int base = 0; base < N; base += kPlanSeqs) {
+    const int n = N - base < kPlanSeqs ? N - base : kPlanSeqs;
+    for (int u = threadIdx.x; u < n; u += kThreads) end[u] = plan_length(lengths, base + u, T);
+    __syncthreads();
+    scan_lds(n, T, end, wsum);
+    for (int u = threadIdx.x; u < n; u += kThreads) cu[1 + base + u] = sat_add(carry, end[u], T);
+    carry = sat_add(carry, end[n - 1], T);
+    __syncthreads();
+  }
   if (order != nullptr)
     for (int u = threadIdx.x; u < N; u += kThreads) order[u] = u;
 }
@@ -134,13 +146,14 @@ __global__ __launch_bounds__(kThreads) void plan_rows_kernel(const int32_t* __re
 
 hipError_t launch_plan(const int32_t* lengths, const int32_t* starts, int N, int T, int C, int32_t* cu,
                        int32_t* order, int32_t* seq, int32_t* pos, hipStream_t s) {
+  const int shift = C == 64 ? 6 : C == 32 ? 5 : 4;
   const int row_wgs = seq != nullptr || pos != nullptr ? int((int64_t(T) + kPlanRows - 1) / kPlanRows) : 0;
   if (N <= kPlanSeqs) {
     const int rank_wgs = order != nullptr ? (N + kPlanRank - 1) / kPlanRank : 0;
     int nwg = row_wgs > rank_wgs ? row_wgs : rank_wgs;
     if (nwg < 1) nwg = 1;
-    hipLaunchKernelGGL(plan_kernel, dim3(unsigned(nwg)), dim3(kThreads), 0, s, lengths, starts, N, T, C, cu, order,
-                       seq, pos);
+    hipLaunchKernelGGL(plan_kernel, dim3(unsigned(nwg)), dim3(kThreads), 0, s, lengths, starts, N, T, shift, cu,
+                       order, seq, pos);
     return hipGetLastError();
   }
   hipLaunchKernelGGL(plan_offsets_kernel, dim3(1), dim3(kThreads), 0, s, lengths, N, T, cu, order);

@@ -551,20 +551,57 @@ def efla_step(q, k, v, beta, state, o=None, rule: str = "exact"):
 # o_t = S_t^T q_t.  g is float32 for every dtype; q and k may have fewer heads
 # (Hk) than v, beta, g and the states (H): value head h reads head h // (H // Hk).
 
+def _at(t) -> int:
+    """A tensor's address, 0 for None."""
+    return 0 if t is None else t.data_ptr()
+
+
+def _call(fn, index: int, where: str, *args) -> None:
+    """fn(*args, stream) on torch's current stream of device ``index``, with
+    that device current.  A call of a decode step costs more on the host than
+    on the GPU, so the device is switched only where it is another one."""
+    stream = torch.cuda.current_stream(index).cuda_stream
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status:
+        raise EflaError(status, where)
+
+
 def _gated_shapes(q, k, v, beta, g, lead: int):
-    """(device, leading dims, H, Hk, dk, dv) of a gated call's inputs, checked."""
-    dt = q.dtype
-    dev = _dev(q, k, v, beta, dtype=dt)
-    _dev(q, g)
-    if k.dim() != lead + 2 or v.dim() != lead + 2 or q.shape != k.shape or v.shape[:lead] != k.shape[:lead] \
-            or beta.shape != v.shape[:-1] or g.shape != v.shape[:-1] or g.dtype != torch.float32:
-        dims = {1: "N" , 2: "B,L"}[lead]
+    """(device index, H, Hk, dk, dv) of a gated call's inputs, checked."""
+    dt, ks, vs = q.dtype, k.shape, v.shape
+    if len(ks) != lead + 2 or len(vs) != lead + 2 or q.shape != ks or vs[:lead] != ks[:lead] \
+            or beta.shape != vs[:-1] or g.shape != vs[:-1] or k.dtype != dt or v.dtype != dt or beta.dtype != dt \
+            or g.dtype != torch.float32:
+        dims = {1: "N", 2: "B,L"}[lead]
         raise ValueError(f"expected q, k [{dims},Hk,dk], v [{dims},H,dv], beta [{dims},H] of one type, "
                          f"g float32 [{dims},H]")
-    H, Hk = v.shape[-2], k.shape[-2]
+    H, Hk = vs[-2], ks[-2]
     if Hk < 1 or H % Hk:
         raise ValueError(f"the {H} value heads must be a multiple of the {Hk} query and key heads")
-    return dev, H, Hk, k.shape[-1], v.shape[-1]
+    index = q.get_device()
+    _same(index, q, k, v, beta, g)
+    return index, H, Hk, ks[-1], vs[-1]
+
+
+def _same(index: int, *ts) -> None:
+    """Every tensor given must be contiguous and live on GPU ``index``."""
+    for t in ts:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("EFLA tensors must live on the GPU")
+        if not t.is_contiguous():
+            raise ValueError("EFLA tensors must be contiguous")
+        if t.get_device() != index:
+            raise ValueError("EFLA tensors must share one device")
+
+
+def _nbytes(t) -> int:
+    return 0 if t is None else t.numel() * t.element_size()
 
 
 def efla_gated_chunk_fwd_workspace_size(B, H, Hk, L, d_k, d_v, chunk, dtype) -> int:
@@ -576,24 +613,22 @@ def efla_gated_chunk_fwd(q, k, v, beta, g, s0=None, chunk: int = 64, o=None, s_f
     """Gated forward pass over a dense batch: q, k [B,L,Hk,dk], v [B,L,H,dv],
     beta [B,L,H] in one type, g float32 [B,L,H].  Returns (o [B,L,H,dv] in q's
     dtype, S_L float32 [B,H,dk,dv] or None)."""
-    dev, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
+    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
     B, L = k.shape[:2]
-    _dev(q, s0, o, s_final, workspace)
+    _same(index, s0, o, s_final, workspace)
     _want(s0, (B, H, dk, dv), "s0", torch.float32)
     _want(o, v.shape, "o", q.dtype)
     _want(s_final, (B, H, dk, dv), "s_final", torch.float32)
     if o is None:
         o = torch.empty_like(v)
     if s_final is None and want_final:
-        s_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
-    code = _code(q.dtype)
+        s_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+    code, r = _code(q.dtype), _rule(rule)
     if workspace is None:
         n = lib().efla_gated_chunk_fwd_workspace_size(B, H, Hk, L, dk, dv, chunk, code)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    with torch.cuda.device(dev):
-        _check(lib().efla_gated_chunk_fwd(_p(q), _p(k), _p(v), _p(beta), _p(g), _p(s0), _p(o), _p(s_final), B, H, Hk,
-                                          L, dk, dv, chunk, code, _rule(rule), _p(workspace), _ws(workspace, dev),
-                                          _stream(dev)), "efla_gated_chunk_fwd")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    _call(lib().efla_gated_chunk_fwd, index, "efla_gated_chunk_fwd", _at(q), _at(k), _at(v), _at(beta), _at(g), _at(s0),
+          _at(o), _at(s_final), B, H, Hk, L, dk, dv, chunk, code, r, _at(workspace), _nbytes(workspace))
     return o, s_final
 
 
@@ -609,9 +644,9 @@ def efla_gated_chunk_fwd_varlen(q, k, v, beta, g, cu_seqlens, s0=None, chunk: in
     sequence i starts from and ends in (an entry outside the pool: from zero,
     final state not written).  order: a schedule as efla_pack_plan returns it.
     Returns (o shaped like v, s_final)."""
-    dev, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1)
+    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1)
     T = k.shape[0]
-    _dev(q, s0, o, s_final, workspace, cu_seqlens, slots, order)
+    _same(index, s0, o, s_final, workspace, cu_seqlens, slots, order)
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be a 1-D int32 tensor of N+1 offsets")
     N = cu_seqlens.numel() - 1
@@ -630,16 +665,14 @@ def efla_gated_chunk_fwd_varlen(q, k, v, beta, g, cu_seqlens, s0=None, chunk: in
     if s_final is None and want_final:
         if slots is not None:
             raise ValueError("with slots the final states need a pool: pass s_final (it may be s0), or want_final=False")
-        s_final = torch.empty((N, H, dk, dv), dtype=torch.float32, device=dev)
-    code = _code(q.dtype)
+        s_final = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+    code, r = _code(q.dtype), _rule(rule)
     if workspace is None:
         n = lib().efla_gated_chunk_fwd_varlen_workspace_size(N, H, Hk, T, dk, dv, chunk, code)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    with torch.cuda.device(dev):
-        _check(lib().efla_gated_chunk_fwd_varlen(_p(q), _p(k), _p(v), _p(beta), _p(g), _p(cu_seqlens), _p(slots),
-                                                 _p(order), N, P, _p(s0), _p(o), _p(s_final), H, Hk, T, dk, dv, chunk,
-                                                 code, _rule(rule), _p(workspace), _ws(workspace, dev), _stream(dev)),
-               "efla_gated_chunk_fwd_varlen")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    _call(lib().efla_gated_chunk_fwd_varlen, index, "efla_gated_chunk_fwd_varlen", _at(q), _at(k), _at(v), _at(beta),
+          _at(g), _at(cu_seqlens), _at(slots), _at(order), N, P, _at(s0), _at(o), _at(s_final), H, Hk, T, dk, dv, chunk,
+          code, r, _at(workspace), _nbytes(workspace))
     return o, s_final
 
 
@@ -653,23 +686,21 @@ def efla_gated_chunk_bwd(q, k, v, beta, g, d_o, s0=None, ds_final=None, chunk: i
     = ds_final (None: zero).  Returns (dq, dk, dv, dbeta, dg, ds0): the first
     five in q's dtype (dq and dk summed over the value heads that share a
     head), ds0 float32 [B,H,dk,dv] or None when want_ds0 is False."""
-    dev, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
+    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
     B, L = k.shape[:2]
-    _dev(q, d_o, s0, ds_final, workspace)
+    _same(index, d_o, s0, ds_final, workspace)
     _want(d_o, v.shape, "d_o", q.dtype)
     _want(s0, (B, H, dk, dv), "s0", torch.float32)
     _want(ds_final, (B, H, dk, dv), "ds_final", torch.float32)
     gq, gk, gv, gb, gg = (torch.empty_like(x) for x in (q, k, v, beta, beta))
-    gs0 = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev) if want_ds0 else None
-    code = _code(q.dtype)
+    gs0 = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device) if want_ds0 else None
+    code, r = _code(q.dtype), _rule(rule)
     if workspace is None:
         n = lib().efla_gated_chunk_bwd_workspace_size(B, H, Hk, L, dk, dv, chunk, code)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    with torch.cuda.device(dev):
-        _check(lib().efla_gated_chunk_bwd(_p(q), _p(k), _p(v), _p(beta), _p(g), _p(s0), _p(d_o), _p(ds_final), _p(gq),
-                                          _p(gk), _p(gv), _p(gb), _p(gg), _p(gs0), B, H, Hk, L, dk, dv, chunk, code,
-                                          _rule(rule), _p(workspace), _ws(workspace, dev), _stream(dev)),
-               "efla_gated_chunk_bwd")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    _call(lib().efla_gated_chunk_bwd, index, "efla_gated_chunk_bwd", _at(q), _at(k), _at(v), _at(beta), _at(g), _at(s0),
+          _at(d_o), _at(ds_final), _at(gq), _at(gk), _at(gv), _at(gb), _at(gg), _at(gs0), B, H, Hk, L, dk, dv, chunk,
+          code, r, _at(workspace), _nbytes(workspace))
     return gq, gk, gv, gb, gg, gs0
 
 
@@ -678,9 +709,9 @@ def efla_gated_step(q, k, v, beta, g, state, slots=None, o=None, rule: str = "ex
     q, k [N,Hk,dk], v [N,H,dv], beta [N,H] in one type, g float32 [N,H].  Row n
     updates state slots[n] (int32 [N]; None: state n); a slot outside the pool
     skips the row and leaves its row of o as it was.  Returns o [N,H,dv]."""
-    dev, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1)
+    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1)
     N = k.shape[0]
-    _dev(q, state, slots, o)
+    _same(index, state, slots, o)
     if state.dim() != 4 or state.shape[1:] != (H, dk, dv) or state.dtype != torch.float32 \
             or (slots is None and state.shape[0] != N):
         raise ValueError("state must be float32 [P,H,dk,dv], with P = N where no slots are given")
@@ -688,10 +719,8 @@ def efla_gated_step(q, k, v, beta, g, state, slots=None, o=None, rule: str = "ex
     _want(o, v.shape, "o", q.dtype)
     if o is None:
         o = torch.empty_like(v)
-    with torch.cuda.device(dev):
-        _check(lib().efla_gated_step(_p(q), _p(k), _p(v), _p(beta), _p(g), _p(state), _p(slots), _p(o), N,
-                                     state.shape[0], H, Hk, dk, dv, _code(q.dtype), _rule(rule), _stream(dev)),
-               "efla_gated_step")
+    _call(lib().efla_gated_step, index, "efla_gated_step", _at(q), _at(k), _at(v), _at(beta), _at(g), _at(state),
+          _at(slots), _at(o), N, state.shape[0], H, Hk, dk, dv, _code(q.dtype), _rule(rule))
     return o
 
 
@@ -707,17 +736,18 @@ def efla_pack_plan(lengths, tokens: int, starts=None, chunk: int = 64) -> PackPl
     """Tables of a packed batch of ``tokens`` rows from the requests' new-token
     counts ``lengths`` (int32 [N] on the device; nothing is copied to the host).
     starts: int32 [N], the position of each request's first new token."""
-    dev = _dev(lengths, starts)
+    index = lengths.get_device()
+    _same(index, lengths, starts)
     if lengths.dim() != 1 or lengths.dtype != torch.int32:
         raise ValueError("lengths must be a 1-D int32 tensor")
     N, T = lengths.numel(), int(tokens)
     _want(starts, (N,), "starts", torch.int32)
     if not 0 <= T < 2 ** 31:
         raise ValueError("tokens must be in [0, 2^31)")
-    cu, order, seq, pos = torch.empty(2 * N + 1 + 2 * T, dtype=torch.int32, device=dev).split([N + 1, N, T, T])
-    with torch.cuda.device(dev):
-        _check(lib().efla_pack_plan(_p(lengths), _p(starts), N, T, chunk, _p(cu), _p(order), _p(seq), _p(pos),
-                                    _stream(dev)), "efla_pack_plan")
+    cu, order, seq, pos = torch.empty(2 * N + 1 + 2 * T, dtype=torch.int32, device=lengths.device).split([N + 1, N, T, T])
+    at = cu.data_ptr()
+    _call(lib().efla_pack_plan, index, "efla_pack_plan", _at(lengths), _at(starts), N, T, chunk, at, at + 4 * (N + 1),
+          at + 4 * (2 * N + 1), at + 4 * (2 * N + 1 + T))
     return PackPlan(cu, order, seq, pos)
 
 
