@@ -35,7 +35,7 @@ hipError_t split_impl(const GatedFwd& a, const uint16_t* tfr, const float* gws, 
   const int NC = a.cu == nullptr ? int((a.L + kGatedChunk - 1) / kGatedChunk) : int(a.L / kGatedChunk) + a.N;
   const int64_t bh = int64_t(a.cu == nullptr ? a.B : a.N) * a.H;
   const int NVB = a.DV / 32;
-  hipLaunchKernelGGL((gated_split_kernel<DK, OUT>), dim3(unsigned(bh * NVB)), dim3(GatedSplitShape<DK>::THREADS), 0, s,
+  hipLaunchKernelGGL((gated_split_kernel<DK, OUT>), dim3(unsigned(bh * NVB)), dim3(OUT ? GatedSplitShape<DK>::THREADS : GatedSplitShape<DK>::STATE_THREADS), 0, s,
                      a, tfr, gws, order, NC, NVB, bh % 8 == 0 ? 1 : 0, statesT);
   return hipGetLastError();
 }

@@ -1,5 +1,5 @@
 // gated_split.h -- the sequential chunk pass of the gated delta rule for bf16
-// inputs, each chunk's work spread over eight wavefronts, with the state good
+// inputs, each chunk's work spread over fourteen wavefronts, with the state good
 // to 16 significant bits or more.
 //
 // Per chunk (start state S, T from gated_ut.h; e = e^G, w = e^{G_C - G}):
@@ -13,25 +13,30 @@
 // parts alone go in.
 //
 // A workgroup owns 32 value columns (two 16-column tiles) of one (sequence,
-// head).  The roles are those of recurrence_split.h:
-//   Y wave per tile      Y = K S, D, U = T D; publishes U (for O) and
-//                        diag(w) U in two parts (for S)
-//   S wave per half of   S <- e^{G_C} S + K^T (diag(w) U) in fp32 registers;
-//   the key dimension    publishes S in two parts
-//   O wave per half of   Z^T = S^T Q^T, then O^T = diag(e) Z^T + U^T P^T, staged
-//   the chunk's rows     in LDS and stored a chunk later
-//   P wave               Gam * tril(Q K^T), half of the key dimension a phase
-//   DMA wave             Q, K, V and the chunk's gates into a three-slot ring
+// head).  A wavefront's time is close to the sum of its matrix instructions (16
+// cycles), vector instructions (4) and LDS round trips, so the chain S -> D -> U
+// -> S is cut into as many wavefronts as the registers allow:
+//   Y wave per tile and   D = V - diag(e) K S for its 32 tokens; after barrier M
+//   half of the tokens    U = T D for them (the later half reads the earlier
+//                         half's D); publishes U (for O) and diag(w) U in two
+//                         parts (for S)
+//   S wave per 32 key     S <- e^{G_C} S + K^T (diag(w) U) in fp32 registers;
+//   dims                  publishes S in two parts
+//   O wave per half of    Z^T = S^T Q^T, then O^T = diag(e) Z^T + U^T P^T, staged
+//   the tokens            in LDS and stored a chunk later
+//   three P waves         Gam * tril(Q K^T), half of the key dimension a phase
+//   DMA wave              Q, K, V and the chunk's gates into a three-slot ring
 // T does not pass the LDS: it comes in fragment order, 12 KiB a chunk, and the
-// Y waves load it into registers two chunks ahead.  That is what makes eight
-// wavefronts (two a SIMD, 256 VGPRs) the right number here: the Y waves hold
-// two chunks' T besides the chunk's K.
-// Two barriers a chunk, every exchange buffer written in one phase and read in
-// the other:
+// Y waves load it into registers half a chunk ahead; the S waves, idle then,
+// touch a later chunk's T so that those loads are served by the L2.
+// Three barriers a chunk, every exchange buffer written in one phase and read in
+// another:
 //   A (chunk n in LDS, S_n published)
-//     Y: products -> publish U | S: read K^T | O: Z^T | P: finish -> publish | DMA: half of chunk n+2
+//     Y: K S, D -> publish | S: read K^T | O: Z^T | P: finish P_n | DMA: half of chunk n+2
+//   M (D published)
+//     Y: T D -> publish U | P: gates -> publish
 //   B (U and P published, chunk n+1 in LDS)
-//     Y: read K, V of n+1, load T of n+2 | S: update -> publish | O: O^T, read Q of n+1 | P: start n+1 | DMA
+//     Y: load K, V, T of n+1 | S: update -> publish | O: O^T | P: start n+1 | DMA
 #pragma once
 
 #include <type_traits>
@@ -51,17 +56,18 @@ struct GatedSplitShape {
   using TQ = DmaTile<C, DK, 1, true>;
   using TV = DmaTile<C, BV, 1>;
   static constexpr int PQ = TQ::PER_WAVE, PV = TV::PER_WAVE, COUNT = 2 * PQ + PV + 1;
-  // by wavefront index (SIMD = index % 4): the chain's four on a SIMD each
-  static constexpr int kS0 = 0, kY0 = 1, kY1 = 2, kS1 = 3, kP = 4, kO0 = 5, kO1 = 6, kDma = 7;
-  static constexpr int THREADS = 8 * kWave;
+  // wavefronts by index (SIMD = index % 4)
+  static constexpr int NSW = NKU_D;  // S waves, 32 key dims each
+  static constexpr int kY = 0, kS = 4, kDma = kS + NSW, kP = kDma + 1, kO = kP + 3;
+  static constexpr int THREADS = (kO + 2) * kWave, STATE_THREADS = (kDma + 1) * kWave;
 };
 
 // OUT: writes o and the final state.  Else (the backward's recomputation) the
 // state at the start of every chunk instead, as the high operand parts,
-// transposed, [slots][DV][DK] (the layout of recurrence_split.h); the O and P
-// waves idle and Q is not brought in.
+// transposed, [slots][DV][DK] (the layout of recurrence_split.h), without the O
+// and P waves and Q.
 template <int DK, bool OUT>
-__global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint16_t* __restrict__ tfr,
+__global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitShape<DK>::STATE_THREADS)) void gated_split_kernel(GatedFwd a, const uint16_t* __restrict__ tfr,
                                                           const float* __restrict__ gws,
                                                           const int32_t* __restrict__ order, int NC, int NVB, int remap,
                                                           uint16_t* __restrict__ statesT) {
@@ -74,6 +80,7 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
   __shared__ __align__(16) bf16x8 bS_buf[2][NT][NKU_D][kWave];  // S_n, high and low parts
   __shared__ __align__(16) bf16x8 bU_buf[NT][NKU_C][kWave];     // U_n, high parts
   __shared__ __align__(16) bf16x8 bW_buf[2][NT][NKU_C][kWave];  // diag(w) U_n, high and low parts
+  __shared__ __align__(16) bf16x8 bD_buf[2][NT][kWave];         // D_n of tokens 0-31, high and low parts
   __shared__ __align__(16) bf16x8 P_buf[S::NPF][kWave];
   __shared__ __align__(16) uint16_t O_st[C][S::OP];
 
@@ -171,165 +178,171 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
       barrier_nowait();  // A
       if (n + 2 < nc) {
         issue(n + 2, 1, 2);
-        wait_vmcnt<D>();  // chunk n+1 complete: only chunk n+2's transfers remain
+        barrier_nowait();  // M
+        wait_vmcnt<D>();   // chunk n+1 complete: only chunk n+2's transfers remain
       } else {
+        barrier_nowait();  // M
         wait_vmcnt<0>();
       }
       barrier_nowait();  // B
       if (n + 3 < nc) issue(n + 3, 0, 2);
     }
     wait_vmcnt<0>();
-  } else if (role == S::kY0 || role == S::kY1) {
+  } else if (role < S::kS) {
     // ----------------------------------------------------------------- Y
-    const int ct = role == S::kY1 ? 1 : 0;
-    Frag<uint16_t> Kf[NRT][NKU_D];
-    bf16x4 Vt[NRT];
-    f32x4 eg[NRT];
-    struct TFrag {
-      Frag<uint16_t> h[6], l[6];
-    } T;
-    auto load_t = [&](int m) {
-      const bf16x8* src = reinterpret_cast<const bf16x8*>(tfr + (sp.slot0 + (m < nc ? m : nc - 1)) * kGatedT) + lane;
+    const int ct = role & 1;  // the later half's waves, with twice the products after M, on SIMDs 2 and 3
+    auto y_role = [&](auto halfc) {
+      constexpr int Y = decltype(halfc)::value, RT0 = 2 * Y;
+      Frag<uint16_t> Kf[2][NKU_D], Th[2][Y + 1], Tl[2][Y + 1];
+      bf16x4 Vt[2];
+      auto load_t = [&](int m) {
+        const bf16x8* src = reinterpret_cast<const bf16x8*>(tfr + (sp.slot0 + (m < nc ? m : nc - 1)) * kGatedT) + lane;
 #pragma unroll
-      for (int f = 0; f < 6; ++f) {
-        T.h[f].v = src[f * 64];
-        T.l[f].v = src[(6 + f) * 64];
-      }
-    };
-    auto load = [&](const uint16_t* __restrict__ cur) {  // this chunk's K, gates and this tile's V
-      const uint16_t* Ks = cur + S::KOFF;
-      const uint16_t* Vs = cur + S::VOFF;
-      const float* gt = gates(cur);
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-      for (int rt = 0; rt < NRT; ++rt) {
-        Vt[rt] = lds_read_tr(Vs + swz_off<BV>(16 * rt + 4 * g + (li >> 2), 16 * ct + 4 * (li & 3)));
-        eg[rt] = *reinterpret_cast<const f32x4*>(gt + 64 + 16 * rt + 4 * g);
-      }
+          for (int kk = 0; kk <= Y; ++kk) {
+            Th[r][kk].v = src[pf_index(RT0 + r, kk) * 64];
+            Tl[r][kk].v = src[(6 + pf_index(RT0 + r, kk)) * 64];
+          }
+      };
+      auto load = [&](const uint16_t* __restrict__ cur) {  // this chunk's K and this tile's V
 #pragma unroll
-      for (int ku = 0; ku < NKU_D; ++ku)
+        for (int r = 0; r < 2; ++r)
+          Vt[r] = lds_read_tr(cur + S::VOFF + swz_off<BV>(16 * (RT0 + r) + 4 * g + (li >> 2), 16 * ct + 4 * (li & 3)));
 #pragma unroll
-        for (int rt = 0; rt < NRT; ++rt) Kf[rt][ku] = wide_frag<DK>(Ks, 16 * rt + li, ku, g);
-    };
-    auto step = [&](int n) {
-      sync();  // A
-      if (n == 0) load(ring);
-      Frag<uint16_t> sh[NKU_D], sl[NKU_D];
+        for (int ku = 0; ku < NKU_D; ++ku)
 #pragma unroll
-      for (int ku = 0; ku < NKU_D; ++ku) {
-        sh[ku].v = bS_buf[0][ct][ku][lane];
-        sl[ku].v = bS_buf[1][ct][ku][lane];
-      }
-      f32x4 Y[NRT];
+          for (int r = 0; r < 2; ++r) Kf[r][ku] = wide_frag<DK>(cur + S::KOFF, 16 * (RT0 + r) + li, ku, g);
+      };
+      auto step = [&](int n) {
+        sync();  // A
+        if (n == 0) load(ring);
+        const float* gt = gates(ring + (n % 3) * S::SLOT) + 16 * RT0 + 4 * g;
+        Frag<uint16_t> sh[NKU_D], sl[NKU_D];
 #pragma unroll
-      for (int rt = 0; rt < NRT; ++rt) Y[rt] = zero4();
-#pragma unroll
-      for (int ku = 0; ku < NKU_D; ++ku) {
-#pragma unroll
-        for (int rt = 0; rt < NRT; ++rt) mma(Y[rt], Kf[rt][ku], sh[ku]);
-#pragma unroll
-        for (int rt = 0; rt < NRT; ++rt) mma(Y[rt], Kf[rt][ku], sl[ku]);
-      }
-#pragma unroll
-      for (int rt = 0; rt < NRT; ++rt)
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq) Y[rt][qq] = fmaf(-eg[rt][qq], Y[rt][qq], static_cast<float>(Vt[rt][qq]));
-      Frag<uint16_t> dh[NKU_C], dl[NKU_C];
-#pragma unroll
-      for (int ku = 0; ku < NKU_C; ++ku) split_frag(Y[2 * ku], Y[2 * ku + 1], dh[ku], dl[ku]);
-      f32x4 U[NRT], wg[NRT];  // w read here: held from load() on, the registers would spill
-#pragma unroll
-      for (int rt = 0; rt < NRT; ++rt) {
-        U[rt] = zero4();
-        wg[rt] = *reinterpret_cast<const f32x4*>(gates(ring + (n % 3) * S::SLOT) + 128 + 16 * rt + 4 * g);
-      }
-#pragma unroll
-      for (int kk = 0; kk < NKU_C; ++kk) {
-#pragma unroll
-        for (int rt = 2 * kk; rt < NRT; ++rt) mma(U[rt], T.l[pf_index(rt, kk)], dh[kk]);
-#pragma unroll
-        for (int rt = 2 * kk; rt < NRT; ++rt) mma(U[rt], T.h[pf_index(rt, kk)], dl[kk]);
-#pragma unroll
-        for (int rt = 2 * kk; rt < NRT; ++rt) mma(U[rt], T.h[pf_index(rt, kk)], dh[kk]);
-      }
-#pragma unroll
-      for (int ku = 0; ku < NKU_C; ++ku) {
-        if constexpr (OUT) bU_buf[ct][ku][lane] = acc_frag<uint16_t>(U[2 * ku], U[2 * ku + 1]).v;
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq) {
-          U[2 * ku][qq] *= wg[2 * ku][qq];
-          U[2 * ku + 1][qq] *= wg[2 * ku + 1][qq];
+        for (int ku = 0; ku < NKU_D; ++ku) {
+          sh[ku].v = bS_buf[0][ct][ku][lane];
+          sl[ku].v = bS_buf[1][ct][ku][lane];
         }
+        f32x4 D[2], lo[2], eg[2], wg[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          D[r] = lo[r] = zero4();
+          eg[r] = *reinterpret_cast<const f32x4*>(gt + 64 + 16 * r);
+          wg[r] = *reinterpret_cast<const f32x4*>(gt + 128 + 16 * r);
+        }
+#pragma unroll
+        for (int ku = 0; ku < NKU_D; ++ku) {  // high and low parts in sums of their own: four chains
+#pragma unroll
+          for (int r = 0; r < 2; ++r) mma(D[r], Kf[r][ku], sh[ku]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) mma(lo[r], Kf[r][ku], sl[ku]);
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq)
+            D[r][qq] = fmaf(-eg[r][qq], D[r][qq] + lo[r][qq], static_cast<float>(Vt[r][qq]));
+        Frag<uint16_t> dh[Y + 1], dl[Y + 1];
+        split_frag(D[0], D[1], dh[Y], dl[Y]);
+        if constexpr (Y == 0) {
+          bD_buf[0][ct][lane] = dh[0].v;
+          bD_buf[1][ct][lane] = dl[0].v;
+        }
+        sync();  // M
+        if constexpr (Y == 1) {
+          dh[0].v = bD_buf[0][ct][lane];
+          dl[0].v = bD_buf[1][ct][lane];
+        }
+        f32x4 U[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) U[r] = zero4();
+#pragma unroll
+        for (int kk = Y; kk >= 0; --kk) {  // this wave's own D first, while the other half's arrives
+#pragma unroll
+          for (int r = 0; r < 2; ++r) mma(U[r], Tl[r][kk], dh[kk]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) mma(U[r], Th[r][kk], dl[kk]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) mma(U[r], Th[r][kk], dh[kk]);
+        }
+        if constexpr (OUT) bU_buf[ct][Y][lane] = acc_frag<uint16_t>(U[0], U[1]).v;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq) U[r][qq] *= wg[r][qq];
         Frag<uint16_t> wh, wl;
-        split_frag(U[2 * ku], U[2 * ku + 1], wh, wl);
-        bW_buf[0][ct][ku][lane] = wh.v;
-        bW_buf[1][ct][ku][lane] = wl.v;
-      }
-      sync();  // B
-      // Past the last chunk the loads go on, from the last chunk's slot and
-      // whatever the ring holds, and nothing reads what they bring: behind a
-      // branch, the loaded registers would be merged with the old ones, with a
-      // wait there.
-      load_t(n + 1);
-      load(ring + ((n + 1) % 3) * S::SLOT);
+        split_frag(U[0], U[1], wh, wl);
+        bW_buf[0][ct][Y][lane] = wh.v;
+        bW_buf[1][ct][Y][lane] = wl.v;
+        sync();  // B
+        // Past the last chunk the loads go on, from the last chunk's slot and
+        // whatever the ring holds, and nothing reads what they bring: behind a
+        // branch, the loaded registers would be merged with the old ones, with
+        // a wait there.
+        load_t(n + 1);
+        load(ring + ((n + 1) % 3) * S::SLOT);
+      };
+      if (nc > 0) load_t(0);
+      for (int n = 0; n < nc; ++n) step(n);
     };
-    if (nc > 0) load_t(0);
-    for (int n = 0; n < nc; ++n) step(n);
-  } else if (role == S::kS0 || role == S::kS1) {
+    if (role < 2) y_role(std::integral_constant<int, 0>{});
+    else y_role(std::integral_constant<int, 1>{});
+  } else if (role < S::kDma) {
     // ----------------------------------------------------------------- S
-    // rows: logical key dims 64 hh .. (k-units KH hh .. KH hh + KH - 1)
-    const int hh = role == S::kS1 ? 1 : 0, dt0 = 2 * KH * hh, ku0 = KH * hh;
-    f32x4 St[2 * KH][NT];  // St[d][c][qq] = S[key_phys(16 (dt0 + d) + 4 g + qq)][v0 + 16 c + li]
+    // rows: logical key dims 32 sw .. 32 sw + 31 (one k-unit)
+    const int sw = role - S::kS;
+    f32x4 St[2][NT];  // St[d][c][qq] = S[key_phys(16 (2 sw + d) + 4 g + qq)][v0 + 16 c + li]
     const float* s0 = a.s0 == nullptr || srow < 0 ? nullptr : a.s0 + (srow * H + h) * DK * DV + v0 + li;
 #pragma unroll
-    for (int d = 0; d < 2 * KH; ++d)
+    for (int d = 0; d < 2; ++d)
 #pragma unroll
       for (int c = 0; c < NT; ++c)
 #pragma unroll
         for (int qq = 0; qq < 4; ++qq)
-          St[d][c][qq] = s0 != nullptr ? s0[int64_t(key_phys(16 * (dt0 + d) + 4 * g + qq)) * DV + 16 * c] : 0.0f;
+          St[d][c][qq] = s0 != nullptr ? s0[int64_t(key_phys(16 * (2 * sw + d) + 4 * g + qq)) * DV + 16 * c] : 0.0f;
     auto publish = [&]() {
 #pragma unroll
-      for (int u = 0; u < KH; ++u)
-#pragma unroll
-        for (int c = 0; c < NT; ++c) {
-          Frag<uint16_t> sh, sl;
-          split_frag(St[2 * u][c], St[2 * u + 1][c], sh, sl);
-          bS_buf[0][c][ku0 + u][lane] = sh.v;
-          bS_buf[1][c][ku0 + u][lane] = sl.v;
-        }
+      for (int c = 0; c < NT; ++c) {
+        Frag<uint16_t> sh, sl;
+        split_frag(St[0][c], St[1][c], sh, sl);
+        bS_buf[0][c][sw][lane] = sh.v;
+        bS_buf[1][c][sw][lane] = sl.v;
+      }
     };
     auto save = [&](int n) {  // chunk n's start state, whole rows of S^T (recurrence_split.h)
-      constexpr int PR = DK / 8;
+      constexpr int PR = DK / 8, RW = BV / NKU_D;  // 16-byte pieces per row, rows per S wave
 #pragma unroll
-      for (int j = 0; j < PR / 4; ++j) {
-        const int rr = 8 * (j / (PR / 8)) + (lane & 7);
-        const int p = 8 * (j % (PR / 8)) + 2 * (lane >> 4) + ((lane >> 3) & 1);
-        const bf16x8 f = bS_buf[0][hh][p >> 2][16 * (p & 3) + rr];
+      for (int j = 0; j < 2; ++j) {
+        const int r = RW * sw + 8 * (PR == 16 ? 0 : j) + (lane & 7);
+        const int p = 8 * (PR == 16 ? j : 0) + 2 * (lane >> 4) + ((lane >> 3) & 1);
+        const bf16x8 f = bS_buf[0][r >> 4][p >> 2][16 * (p & 3) + (r & 15)];
         __builtin_nontemporal_store(
-            f, reinterpret_cast<bf16x8*>(statesT + ((sp.slot0 + n) * DV + v0 + 16 * hh + rr) * DK + 8 * p));
+            f, reinterpret_cast<bf16x8*>(statesT + ((sp.slot0 + n) * DV + v0 + r) * DK + 8 * p));
       }
     };
     publish();
-    // T of a later chunk touched line by line, 6 KiB by each S wave in its idle
+    // T of a later chunk touched line by line, a share by each S wave in its idle
     // phase, so that the Y waves' loads half a chunk ahead find it in L2
     uint32_t warm = 0, seen = 0;
     run([&](const uint16_t* __restrict__ cur, const uint16_t*, int n) {
       sync();  // A
       seen |= warm;
       {
+        constexpr int LINES = kGatedT * 2 / 128 / S::NSW;
         const int m = n + 3 < nc ? n + 3 : nc - 1;
-        const auto* line = reinterpret_cast<const uint32_t*>(tfr + (sp.slot0 + m) * kGatedT) + 32 * (48 * hh + (lane < 48 ? lane : 47));
+        const auto* line = reinterpret_cast<const uint32_t*>(tfr + (sp.slot0 + m) * kGatedT) + 32 * (LINES * sw + (lane < LINES ? lane : LINES - 1));
         warm = *line;
       }
-      Frag<uint16_t> KT[2 * KH][NKU_C];
+      Frag<uint16_t> KT[2][NKU_C];
       const float end = gates(cur)[64 + 63];
 #pragma unroll
-      for (int d = 0; d < 2 * KH; ++d)
+      for (int d = 0; d < 2; ++d)
 #pragma unroll
-        for (int kt = 0; kt < NKU_C; ++kt) KT[d][kt] = wide_frag_tr<DK>(cur + S::KOFF, dt0 + d, kt, lane);
+        for (int kt = 0; kt < NKU_C; ++kt) KT[d][kt] = wide_frag_tr<DK>(cur + S::KOFF, 2 * sw + d, kt, lane);
       if constexpr (!OUT) save(n);
 #pragma unroll
-      for (int d = 0; d < 2 * KH; ++d)
+      for (int d = 0; d < 2; ++d)
 #pragma unroll
         for (int c = 0; c < NT; ++c)
 #pragma unroll
@@ -337,6 +350,7 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
             St[d][c][qq] *= end;
             asm volatile("" : "+v"(St[d][c][qq]));  // here, not past the barrier, where S is the chunk's critical work
           }
+      sync();  // M
       sync();  // B
 #pragma unroll
       for (int c = 0; c < NT; ++c)
@@ -346,9 +360,9 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
           wh.v = bW_buf[0][c][kt][lane];
           wl.v = bW_buf[1][c][kt][lane];
 #pragma unroll
-          for (int d = 0; d < 2 * KH; ++d) mma(St[d][c], KT[d][kt], wl);
+          for (int d = 0; d < 2; ++d) mma(St[d][c], KT[d][kt], wl);
 #pragma unroll
-          for (int d = 0; d < 2 * KH; ++d) mma(St[d][c], KT[d][kt], wh);
+          for (int d = 0; d < 2; ++d) mma(St[d][c], KT[d][kt], wh);
         }
       publish();
     });
@@ -356,21 +370,16 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
     if (OUT && a.sfin != nullptr && srow >= 0) {
       float* sf = a.sfin + (srow * H + h) * DK * DV + v0 + li;
 #pragma unroll
-      for (int d = 0; d < 2 * KH; ++d)
+      for (int d = 0; d < 2; ++d)
 #pragma unroll
         for (int c = 0; c < NT; ++c)
 #pragma unroll
           for (int qq = 0; qq < 4; ++qq)
-            sf[int64_t(key_phys(16 * (dt0 + d) + 4 * g + qq)) * DV + 16 * c] = St[d][c][qq];
+            sf[int64_t(key_phys(16 * (2 * sw + d) + 4 * g + qq)) * DV + 16 * c] = St[d][c][qq];
     }
-  } else if (!OUT) {
-    for (int n = 0; n < nc; ++n) {
-      barrier_nowait();
-      barrier_nowait();
-    }
-  } else if (role == S::kO0 || role == S::kO1) {
+  } else if (role >= S::kO) {
     // ------------------------------------------------------------- output
-    const int o_rh = role == S::kO1 ? 1 : 0, rt0 = 2 * o_rh;
+    const int o_rh = role - S::kO, rt0 = 2 * o_rh;
     Frag<uint16_t> Qf[2][NKU_D];
     float eg[2];
     auto load = [&](const uint16_t* __restrict__ cur) {
@@ -381,10 +390,10 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
 #pragma unroll
         for (int r = 0; r < 2; ++r) Qf[r][ku] = wide_frag<DK>(cur + S::QOFF, 16 * (rt0 + r) + li, ku, g);
     };
-    run([&](const uint16_t* __restrict__ cur, const uint16_t* __restrict__ nxt, int n) {
+    run([&](const uint16_t* __restrict__ cur, const uint16_t*, int n) {
       sync();  // A
-      if (n == 0) load(cur);
-      else store_staged(n - 1, o_rh);
+      load(cur);
+      if (n > 0) store_staged(n - 1, o_rh);
       f32x4 Zt[NT][2];  // Zt[c][r][qq] = Z[16 (rt0 + r) + li][16 c + 4 g + qq]
 #pragma unroll
       for (int c = 0; c < NT; ++c)
@@ -405,6 +414,7 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int qq = 0; qq < 4; ++qq) Zt[c][r][qq] *= eg[r];
+      sync();  // M
       sync();  // B
       Frag<uint16_t> bUo[NT][NKU_C];
 #pragma unroll
@@ -430,7 +440,6 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
           *reinterpret_cast<bf16x4*>(&O_st[16 * rt + li][16 * c + 4 * g]) = ov;
         }
       }
-      if (n + 1 < nc) load(nxt);
     });
     // the last chunk's output: staged by both output waves before this barrier
     sync();
@@ -438,57 +447,66 @@ __global__ __launch_bounds__(512) void gated_split_kernel(GatedFwd a, const uint
     return;
   } else {
     // ----------------------------------------------------------------- P
-    f32x4 Pt[NRT][NRT];  // Pt[r][c][qq] = P[16 r + li][16 c + 4 g + qq], c <= r
-    auto clear = [&]() {
+    // row tiles R0 .. R1 - 1 of P: 0-1, 2 and 3
+    auto p_role = [&](auto r0c, auto r1c) {
+      constexpr int R0 = decltype(r0c)::value, R1 = decltype(r1c)::value;
+      f32x4 Pt[R1 - R0][R1];  // Pt[r - R0][c][qq] = P[16 r + li][16 c + 4 g + qq], c <= r
+      auto clear = [&]() {
 #pragma unroll
-      for (int r = 0; r < NRT; ++r)
+        for (int r = R0; r < R1; ++r)
 #pragma unroll
-        for (int c = 0; c <= r; ++c) Pt[r][c] = zero4();
-    };
-    auto accumulate = [&](const uint16_t* __restrict__ cur, int ku0, int ku1) {
+          for (int c = 0; c <= r; ++c) Pt[r - R0][c] = zero4();
+      };
+      auto accumulate = [&](const uint16_t* __restrict__ cur, int k0, int k1) {
 #pragma unroll
-      for (int ku = 0; ku < NKU_D; ++ku) {
-        if (ku < ku0 || ku >= ku1) continue;
-        Frag<uint16_t> Qf[NRT], Kf[NRT];
+        for (int ku = 0; ku < NKU_D; ++ku) {
+          if (ku < k0 || ku >= k1) continue;
+          Frag<uint16_t> Qf[R1 - R0], Kf[R1];
 #pragma unroll
-        for (int r = 0; r < NRT; ++r) {
-          Qf[r] = wide_frag<DK>(cur + S::QOFF, 16 * r + li, ku, g);
-          Kf[r] = wide_frag<DK>(cur + S::KOFF, 16 * r + li, ku, g);
+          for (int r = R0; r < R1; ++r) Qf[r - R0] = wide_frag<DK>(cur + S::QOFF, 16 * r + li, ku, g);
+#pragma unroll
+          for (int c = 0; c < R1; ++c) Kf[c] = wide_frag<DK>(cur + S::KOFF, 16 * c + li, ku, g);
+#pragma unroll
+          for (int r = R0; r < R1; ++r)
+#pragma unroll
+            for (int c = 0; c <= r; ++c) mma(Pt[r - R0][c], Kf[c], Qf[r - R0]);
         }
-#pragma unroll
-        for (int r = 0; r < NRT; ++r)
-#pragma unroll
-          for (int c = 0; c <= r; ++c) mma(Pt[r][c], Kf[c], Qf[r]);
-      }
-    };
-    clear();
-    run([&](const uint16_t* __restrict__ cur, const uint16_t* __restrict__ nxt, int n) {
-      sync();  // A
-      if (n == 0) accumulate(cur, 0, KH);
-      accumulate(cur, KH, NKU_D);
-      const float* gt = gates(cur);
-      f32x4 gc[NRT];
-#pragma unroll
-      for (int c = 0; c < NRT; ++c) gc[c] = *reinterpret_cast<const f32x4*>(gt + 16 * c + 4 * g);
-#pragma unroll
-      for (int r = 0; r < NRT; ++r) {
-        const float gr = gt[16 * r + li];
-#pragma unroll
-        for (int c = 0; c <= r; ++c)
-#pragma unroll
-          for (int qq = 0; qq < 4; ++qq)
-            Pt[r][c][qq] = (c < r || 4 * g + qq <= li) ? Pt[r][c][qq] * exp2_gate(gr - gc[c][qq]) : 0.0f;
-#pragma unroll
-        for (int ku = 0; ku < NKU_C; ++ku)
-          if (32 * ku <= 16 * r + 15) {
-            const f32x4 phi = (2 * ku + 1 <= r) ? Pt[r][2 * ku + 1] : zero4();
-            P_buf[pf_index(r, ku)][lane] = acc_frag<uint16_t>(Pt[r][2 * ku], phi).v;
-          }
-      }
-      sync();  // B
+      };
       clear();
-      if (n + 1 < nc) accumulate(nxt, 0, KH);
-    });
+      run([&](const uint16_t* __restrict__ cur, const uint16_t* __restrict__ nxt, int n) {
+        sync();  // A
+        if (n == 0) accumulate(cur, 0, KH);
+        accumulate(cur, KH, NKU_D);
+        sync();  // M
+        const float* gt = gates(cur);
+        f32x4 gc[R1];
+#pragma unroll
+        for (int c = 0; c < R1; ++c) gc[c] = *reinterpret_cast<const f32x4*>(gt + 16 * c + 4 * g);
+#pragma unroll
+        for (int r = R0; r < R1; ++r) {
+          const float gr = gt[16 * r + li];
+#pragma unroll
+          for (int c = 0; c <= r; ++c)
+#pragma unroll
+            for (int qq = 0; qq < 4; ++qq)
+              Pt[r - R0][c][qq] =
+                  (c < r || 4 * g + qq <= li) ? Pt[r - R0][c][qq] * exp2_gate(gr - gc[c][qq]) : 0.0f;
+#pragma unroll
+          for (int ku = 0; ku < NKU_C; ++ku)
+            if (32 * ku <= 16 * r + 15) {
+              const f32x4 phi = (2 * ku + 1 <= r) ? Pt[r - R0][2 * ku + 1] : zero4();
+              P_buf[pf_index(r, ku)][lane] = acc_frag<uint16_t>(Pt[r - R0][2 * ku], phi).v;
+            }
+        }
+        sync();  // B
+        clear();
+        if (n + 1 < nc) accumulate(nxt, 0, KH);
+      });
+    };
+    using std::integral_constant;
+    if (role == S::kP) p_role(integral_constant<int, 0>{}, integral_constant<int, 2>{});
+    else if (role == S::kP + 1) p_role(integral_constant<int, 2>{}, integral_constant<int, 3>{});
+    else p_role(integral_constant<int, 3>{}, integral_constant<int, 4>{});
   }
   sync();  // with the output waves' last barrier
 }

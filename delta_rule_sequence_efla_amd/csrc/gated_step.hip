@@ -1,4 +1,4 @@
-// gated_step.hip -- the gated delta rule token by token (gated.h): one decode
+// gated_step.hip -- the gated delta rule without chunks (gated.h): one decode
 // token per request, and whole sequences for the inputs that the chunked
 // kernels do not take.  All arithmetic is fp32.
 #include "gated.h"
@@ -147,26 +147,39 @@ template hipError_t launch_gated_step<float>(const GatedStep&, hipStream_t);
 template hipError_t launch_gated_step<uint16_t>(const GatedStep&, hipStream_t);
 
 // ---------------------------------------------------------------------------
-// Whole sequences token by token, fp32 throughout: one workgroup per sequence,
-// head and 16 value columns.  The 16 lanes of a DPP row share one column and
-// split the key dims, NK each, so r = S^T k and o = S^T q are sums over a row
-// (four DPP adds, no LDS); a wavefront carries four columns.  Blocks of 16
-// tokens of q, k, v, beta and g are loaded into registers a block ahead (16
-// threads per token), widened into one of two LDS buffers, with a and e^g
-// formed on the way, so that a token costs LDS reads and the chain
-// r -> u -> S alone.  With `states`, the state before every C-th token is
-// stored, [chunk slot][d_k][d_v] fp32 (the backward's chunk starts; C % 16 == 0).
+// Whole sequences in fp32 throughout, two tokens at a time: one workgroup per
+// sequence, head and 16 value columns.  The 16 lanes of a DPP row share one
+// column and split the key dims, NK each, so a product of a key or query with S
+// is a sum over a row (four DPP adds, no LDS); a wavefront carries four columns.
+// With S the state before tokens 0 and 1 of a pair and r = k^T S, p = q^T S:
+//     u_0 = a_0 (v_0 - e_0 r_0)
+//     u_1 = a_1 (v_1 - e_1 (e_0 r_1 + (k_1.k_0) u_0))
+//     o_0 = e_0 p_0 + (q_0.k_0) u_0
+//     o_1 = e_1 (e_0 p_1 + (q_1.k_0) u_0) + (q_1.k_1) u_1
+//     S <- e_1 e_0 S + e_1 k_0 u_0 + k_1 u_1
+// so the four sums over rows, each a chain of DPP adds with two wait states in
+// between, run side by side.  Four more wavefronts stage blocks of 16 tokens, 16
+// threads a token: they load two blocks ahead into registers, form a, e and the
+// products of keys and queries among themselves, widen into one of two LDS
+// buffers, and store the outputs of the block before.
+// 777 tokens, 16 heads, d 64, fp32: 142 us token by token with the staging in
+// the same wavefronts, 111 us by pairs, 82 us with wavefronts for each.
+// With `states`, the state before every C-th token is stored, [chunk
+// slot][d_k][d_v] fp32 (the backward's chunk starts; C % 16 == 0).
 template <typename T, int N> struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Piece { T e[N]; };
-template <int NK> struct Token {
-  float k[NK], q[NK], v, a, e;
+template <int NK> struct TokenPair {
+  float k0[NK], k1[NK], q0[NK], q1[NK], v0, v1;
+  f32x4 c, d;  // a_0, e_0, a_1, e_1; k_1.k_0, q_0.k_0, q_1.k_0, q_1.k_1
 };
 
 template <typename T, int DK>
-__global__ __launch_bounds__(kThreads) void gated_recurrent_kernel(GatedFwd a, float* __restrict__ states, int C,
+__global__ __launch_bounds__(2 * kThreads) void gated_recurrent_kernel(GatedFwd a, float* __restrict__ states, int C,
                                                                    int NC) {
   constexpr int NK = DK / 16, TB = 16;
   __shared__ __align__(16) float kS[2][TB][DK], qS[2][TB][DK];
-  __shared__ float vS[2][TB][16], aS[2][TB], eS[2][TB], oS[2][TB][17];
+  __shared__ __align__(16) float cS[2][TB / 2][4], dS[2][TB / 2][4];  // per pair: TokenPair's c and d
+  __shared__ float vS[2][TB][16];
+  __shared__ float oS[2][TB * 17 + kThreads];  // behind the tile: where lanes without an output write
 
   const int NVB = a.DV / 16, H = a.H, DV = a.DV;
   const int64_t unit = blockIdx.x / NVB;
@@ -188,82 +201,92 @@ __global__ __launch_bounds__(kThreads) void gated_recurrent_kernel(GatedFwd a, f
   const float* g = a.g + bos * H + h;
   T* o = a.o == nullptr ? nullptr : static_cast<T*>(a.o) + (bos * H + h) * DV + v0;
 
-  const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), li = lane & 15, grp = lane >> 4;
+  const int tid = threadIdx.x & (kThreads - 1), lane = tid & 63, w = wave_id() & 3, li = lane & 15, grp = lane >> 4;
+  const bool stager = wave_id() >= 4;
   const int col = 4 * w + grp;            // this lane's value column of the block
   const int tok = tid >> 4, pc = tid & 15;  // staging: token of the block, piece of its row
+  const int blocks = int((len + TB - 1) / TB);
+
+  if (stager) {
+    if (len <= 0) return;
+    struct Regs {
+      Piece<T, NK> k, q;
+      float v, b, g;
+    } X, Y;
+    auto load = [&](Regs& x, int n) {  // tokens past the end: zeros, which change nothing
+      const int64_t t = int64_t(n) * TB + tok;
+#pragma unroll
+      for (int e = 0; e < NK; ++e) x.k.e[e] = x.q.e[e] = T(0);
+      x.v = x.b = x.g = 0.0f;
+      if (t < len) {
+        x.k = *reinterpret_cast<const Piece<T, NK>*>(k + t * a.Hk * DK + pc * NK);
+        x.q = *reinterpret_cast<const Piece<T, NK>*>(q + t * a.Hk * DK + pc * NK);
+        x.v = to_f32(v[t * H * DV + pc]);
+        x.b = to_f32(beta[t * H]);
+        x.g = g[t * H];
+      }
+    };
+    auto stage = [&](const Regs& r, int b) {
+      float lam = 0.0f, qk = 0.0f, kk1 = 0.0f, qk1 = 0.0f;
+#pragma unroll
+      for (int e = 0; e < NK; ++e) {
+        const float x = to_f32(r.k.e[e]), y = to_f32(r.q.e[e]);
+        const float other = __shfl_xor(x, 16);  // the key of the pair's other token
+        lam = fmaf(x, x, lam);
+        qk = fmaf(y, x, qk);
+        kk1 = fmaf(x, other, kk1);
+        qk1 = fmaf(y, other, qk1);
+        kS[b][tok][pc * NK + e] = x;
+        qS[b][tok][pc * NK + e] = y;
+      }
+      lam = row_sum16(lam);
+      qk = row_sum16(qk);
+      kk1 = row_sum16(kk1);
+      qk1 = row_sum16(qk1);
+      vS[b][tok][pc] = r.v;
+      if (pc == 0) {
+        cS[b][tok >> 1][2 * (tok & 1)] = efla_alpha_rule(r.b, lam, a.rule);
+        cS[b][tok >> 1][2 * (tok & 1) + 1] = expf(gate_floor(r.g));
+        if (tok & 1) {
+          dS[b][tok >> 1][0] = kk1;
+          dS[b][tok >> 1][2] = qk1;
+          dS[b][tok >> 1][3] = qk;
+        } else {
+          dS[b][tok >> 1][1] = qk;
+        }
+      }
+    };
+    auto store = [&](int n) {
+      const int64_t t = int64_t(n) * TB + tok;
+      if (o != nullptr && t < len) o[t * H * DV + pc] = from_f32<T>(oS[n & 1][tok * 17 + pc]);
+    };
+    // iteration n (block n is worked on): block n + 1 goes into the other
+    // buffer, block n - 1's outputs leave; loads past the end bring zeros
+    load(X, 0);
+    load(Y, 1);
+    stage(X, 0);
+    load(X, 2);
+    __syncthreads();
+    auto step = [&](Regs& r, int n) {
+      stage(r, (n + 1) & 1);
+      load(r, n + 3);
+      if (n > 0) store(n - 1);
+      __syncthreads();
+    };
+    for (int n = 0;;) {
+      step(Y, n);
+      if (++n >= blocks) break;
+      step(X, n);
+      if (++n >= blocks) break;
+    }
+    store(blocks - 1);
+    return;
+  }
 
   float S[NK];
   const float* s0 = a.s0 == nullptr || row < 0 ? nullptr : a.s0 + (row * H + h) * DK * DV + v0 + col;
 #pragma unroll
   for (int e = 0; e < NK; ++e) S[e] = s0 == nullptr ? 0.0f : s0[int64_t(li * NK + e) * DV];
-
-  Piece<T, NK> pk, pq;
-  float pv = 0.0f, pb = 0.0f, pg = 0.0f;
-  auto load = [&](int64_t t0) {
-    const int64_t t = t0 + tok;
-#pragma unroll
-    for (int e = 0; e < NK; ++e) pk.e[e] = pq.e[e] = T(0);
-    pv = pb = pg = 0.0f;
-    if (t < len) {
-      pk = *reinterpret_cast<const Piece<T, NK>*>(k + t * a.Hk * DK + pc * NK);
-      pq = *reinterpret_cast<const Piece<T, NK>*>(q + t * a.Hk * DK + pc * NK);
-      pv = to_f32(v[t * H * DV + pc]);
-      pb = to_f32(beta[t * H]);
-      pg = g[t * H];
-    }
-  };
-  auto stage = [&](int b) {
-    float lam = 0.0f;
-#pragma unroll
-    for (int e = 0; e < NK; ++e) {
-      const float x = to_f32(pk.e[e]);
-      lam = fmaf(x, x, lam);
-      kS[b][tok][pc * NK + e] = x;
-      qS[b][tok][pc * NK + e] = to_f32(pq.e[e]);
-    }
-    lam = row_sum16(lam);
-    vS[b][tok][pc] = pv;
-    if (pc == 0) {
-      aS[b][tok] = efla_alpha_rule(pb, lam, a.rule);
-      eS[b][tok] = expf(gate_floor(pg));
-    }
-  };
-  auto store = [&](int64_t t0, int b) {
-    const int64_t t = t0 + tok;
-    if (o != nullptr && t < len) o[t * H * DV + pc] = from_f32<T>(oS[b][tok][pc]);
-  };
-
-  auto fetch = [&](Token<NK>& x, int b, int j) {
-#pragma unroll
-    for (int e = 0; e < NK; ++e) {
-      x.k[e] = kS[b][j][li * NK + e];
-      x.q[e] = qS[b][j][li * NK + e];
-    }
-    x.v = vS[b][j][col];
-    x.a = aS[b][j];
-    x.e = eS[b][j];
-  };
-  auto token = [&](const Token<NK>& x, int b, int j) {
-    float r0 = 0.0f, r1 = 0.0f;
-#pragma unroll
-    for (int e = 0; e < NK; ++e) {
-      if (e & 1) r1 = fmaf(x.k[e], S[e], r1);
-      else r0 = fmaf(x.k[e], S[e], r0);
-    }
-    const float r = row_sum16(r0 + r1);
-    const float u = x.a * fmaf(-x.e, r, x.v);
-    float p0 = 0.0f, p1 = 0.0f;
-#pragma unroll
-    for (int e = 0; e < NK; ++e) {
-      S[e] = fmaf(x.k[e], u, x.e * S[e]);
-      if (e & 1) p1 = fmaf(x.q[e], S[e], p1);
-      else p0 = fmaf(x.q[e], S[e], p0);
-    }
-    const float p = row_sum16(p0 + p1);
-    if (li == 0) oS[b][j][col] = p;
-  };
-
-  const int64_t slot0 = int64_t(unit) * NC;  // dense batches only
   auto finish = [&]() {
     if (a.sfin == nullptr || row < 0) return;
     float* sf = a.sfin + (row * H + h) * DK * DV + v0 + col;
@@ -274,12 +297,48 @@ __global__ __launch_bounds__(kThreads) void gated_recurrent_kernel(GatedFwd a, f
     finish();
     return;
   }
-  // (staging waits for the first block's loads and, in order, for S before
-  // them: were the loop reachable with S in flight, every block would wait for
-  // the next block's loads at its first token)
-  load(0);
-  stage(0);
-  if (TB < len) load(TB);
+
+  auto fetch = [&](TokenPair<NK>& x, int b, int j) {
+#pragma unroll
+    for (int e = 0; e < NK; ++e) {
+      x.k0[e] = kS[b][j][li * NK + e];
+      x.k1[e] = kS[b][j + 1][li * NK + e];
+      x.q0[e] = qS[b][j][li * NK + e];
+      x.q1[e] = qS[b][j + 1][li * NK + e];
+    }
+    x.v0 = vS[b][j][col];
+    x.v1 = vS[b][j + 1][col];
+    x.c = *reinterpret_cast<const f32x4*>(cS[b][j >> 1]);
+    x.d = *reinterpret_cast<const f32x4*>(dS[b][j >> 1]);
+  };
+  // lane 0 of a row writes o of the pair's first token, lane 1 of its second,
+  // the others a place of their own
+  const int o_at = li < 2 ? li * 17 + col : TB * 17 + tid, o_step = li < 2 ? 17 : 0;
+  auto pair = [&](const TokenPair<NK>& x, int b, int j) {
+    float r0 = 0.0f, r1 = 0.0f, p0 = 0.0f, p1 = 0.0f;
+#pragma unroll
+    for (int e = 0; e < NK; ++e) {
+      r0 = fmaf(x.k0[e], S[e], r0);
+      r1 = fmaf(x.k1[e], S[e], r1);
+      p0 = fmaf(x.q0[e], S[e], p0);
+      p1 = fmaf(x.q1[e], S[e], p1);
+    }
+    r0 = row_sum16(r0);
+    r1 = row_sum16(r1);
+    p0 = row_sum16(p0);
+    p1 = row_sum16(p1);
+    const float e0 = x.c[1], e1 = x.c[3];
+    const float u0 = x.c[0] * fmaf(-e0, r0, x.v0);
+    const float u1 = x.c[2] * fmaf(-e1, fmaf(x.d[0], u0, e0 * r1), x.v1);
+    const float o0 = fmaf(x.d[1], u0, e0 * p0);
+    const float o1 = fmaf(x.d[3], u1, e1 * fmaf(x.d[2], u0, e0 * p1));
+    const float e01 = e0 * e1, w0 = e1 * u0;
+#pragma unroll
+    for (int e = 0; e < NK; ++e) S[e] = fmaf(x.k1[e], u1, fmaf(x.k0[e], w0, e01 * S[e]));
+    oS[b][o_at + j * o_step] = li == 0 ? o0 : o1;
+  };
+
+  const int64_t slot0 = int64_t(unit) * NC;  // dense batches only
   __syncthreads();
   for (int64_t t0 = 0; t0 < len; t0 += TB) {
     const int b = int(t0 / TB) & 1;
@@ -289,22 +348,17 @@ __global__ __launch_bounds__(kThreads) void gated_recurrent_kernel(GatedFwd a, f
       for (int e = 0; e < NK; ++e) dst[int64_t(li * NK + e) * DV] = S[e];
     }
     const int cnt = int(len - t0 < TB ? len - t0 : TB);
-    // a token's values are read from the LDS while the one before is worked on
-    Token<NK> now, next;
+    // a pair's values are read from the LDS while the pair before is worked on
+    TokenPair<NK> now, next;
     fetch(now, b, 0);
-    for (int j = 0; j < cnt; j += 2) {
-      fetch(next, b, j + 1 < TB ? j + 1 : j);
-      token(now, b, j);
-      if (j + 1 >= cnt) break;
-      fetch(now, b, j + 2 < TB ? j + 2 : j);
-      token(next, b, j + 1);
-    }
-    if (t0 + TB < len) {
-      stage(b ^ 1);  // last read two blocks ago, before the barrier below
-      if (t0 + 2 * TB < len) load(t0 + 2 * TB);
+    for (int j = 0; j < cnt; j += 4) {
+      fetch(next, b, j + 2 < TB ? j + 2 : j);
+      pair(now, b, j);
+      if (j + 2 >= cnt) break;
+      fetch(now, b, j + 4 < TB ? j + 4 : j);
+      pair(next, b, j + 2);
     }
     __syncthreads();
-    store(t0, b);  // oS[b] is written again two blocks on, after the next barrier
   }
   finish();
 }
@@ -315,7 +369,7 @@ hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipSt
   const int64_t nwg = units * (a.DV / 16);
   if (nwg == 0) return hipSuccess;
   const int NC = int((a.L + C - 1) / C);
-  const dim3 grid{unsigned(nwg)}, wg{kThreads};
+  const dim3 grid{unsigned(nwg)}, wg{2 * kThreads};
   switch (a.DK) {
     case 16: hipLaunchKernelGGL((gated_recurrent_kernel<T, 16>), grid, wg, 0, s, a, states, C, NC); break;
     case 32: hipLaunchKernelGGL((gated_recurrent_kernel<T, 32>), grid, wg, 0, s, a, states, C, NC); break;
