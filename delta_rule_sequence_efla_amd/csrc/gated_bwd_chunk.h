@@ -17,8 +17,8 @@
 //     accumulators before dP K is added.  <dS', S> is summed from the tiles.
 //   * M = dP0 * P + diag(a) N of gated_bwd.h: Q K^T is formed once more in fp32
 //     at the end (P itself was rounded to bf16), on the tiles that hold dP.
-// Shared key heads (SHARED): dq and dk of every value head leave in fp32, staged
-// as whole rows one after the other, and gated_head_sum_kernel adds them up.
+// Shared key heads (SHARED): dq and dk of every value head leave in fp32, and
+// gated_head_sum_kernel adds them up.
 // 79 KiB of LDS; bound as bwd_chunk_tr_kernel by the latency of its loads.
 #pragma once
 
@@ -42,8 +42,6 @@ struct GatedTrShape : BwdTrShape<DK, 64> {
   static constexpr bool MSUM_IN = B::TT + C * B::CPF * 4 + MSUM_BYTES <= B::A0;
   static constexpr int MSUM = MSUM_IN ? B::TT + C * B::CPF * 4 : B::TAIL_END;
   static constexpr int TAIL_END = MSUM_IN ? B::TAIL_END : B::TAIL_END + MSUM_BYTES;
-  static constexpr int FP = DK + 4;                     // pitch of fp32 rows staged for the stores
-  static_assert(B::TT + C * FP * 4 <= B::RED, "an fp32 tile of dq or dk fits over the tail's arrays");
   static constexpr int BYTES = LOOP_END > TAIL_END ? LOOP_END : TAIL_END;
 };
 
@@ -289,7 +287,11 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
   __syncthreads();  // done with the loop's arrays (K stays); Q in place
 
   // ---- the UT-transform part (bwd_chunk_tr.h), with the gates -----------------
-  const int li = li0, g = g0, lane = lane0;
+  int li = li0, g = g0, lane = lane0;
+  // As in a value block: between the stages the compiler may not carry addresses
+  // over (it kept a dozen for the last stage in scratch, whose reloads one by one
+  // took 10,000 of a chunk's 95,000 cycles)
+  auto fresh = [&]() { asm volatile("" : "+v"(li), "+v"(g), "+v"(lane)); };
   uint16_t *Qt = b16(S::QT), *dPt = b16(S::DPT), *dXh = b16(S::DXH), *dXl = b16(S::DXL);
   uint16_t *Wh = b16(S::WH), *Wl = b16(S::WL), *Xh = b16(S::XH), *Xl = b16(S::XL), *Eb = b16(S::EB);
   uint16_t *dQs = b16(S::DQS), *dKs = b16(S::DKS);
@@ -330,6 +332,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       if (li == 0) red[dt * C + r] = s;
     }
   }
+  fresh();
   // dP = Gam * dP0 as bf16, dT fp32, X as high and low parts; the first part of
   // M (strictly lower), dP * Q K^T, stays in registers
   f32x4 M[NP];
@@ -373,6 +376,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     for (int j = 0; j < NDT; ++j) s += red[j * C + tid];
     ys[tid] = s;
   }
+  fresh();
   // dQ += dP K;  dK += dP^T Q
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
@@ -383,6 +387,28 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
         mma(dQa[i], sw_frag<C>(dPt, 16 * rr + li, ku, g), wide_frag_tr<DK>(Kt, dt, ku, lane));
       if (32 * ku + 31 >= 16 * rr)
         mma(dKa[i], sw_frag_tr<C>(dPt, 16 * rr, ku, lane), wide_frag_tr<DK>(Qt, dt, ku, lane));
+    }
+  }
+  // dQ is complete: it waits for its place in the LDS as packed bf16 (half the
+  // registers), or, of a shared head, leaves in fp32 (pieces of 16 bytes, which
+  // the L2 joins)
+  uint32_t dQp[NQ][2];
+  auto leave = [&](const f32x4& x, float* dst, int rr, int dt) {
+    const int cp = key_phys(16 * dt + li);
+#pragma unroll
+    for (int qq = 0; qq < 4; ++qq) {
+      const int r = 16 * rr + 4 * g + qq;
+      if (r < valid) dst[(row0 + int64_t(r) * H) * DK + cp] = x[qq];
+    }
+  };
+#pragma unroll
+  for (int i = 0; i < NQ; ++i) {
+    const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
+    if constexpr (SHARED) leave(dQa[i], dqh, rr, dt);
+    else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        dQp[i][j] = uint32_t(from_f32<uint16_t>(dQa[i][2 * j])) | uint32_t(from_f32<uint16_t>(dQa[i][2 * j + 1])) << 16;
     }
   }
   __syncthreads();  // red is read, Q and dP are done with
@@ -408,6 +434,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     for (int p = 0; p < NPART; ++p) s += red[p * C + tid];
     das[tid] = s;
   }
+  fresh();
   // W = X^T dX, as high and low parts (over dT)
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
@@ -428,6 +455,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     }
   }
   __syncthreads();
+  fresh();
   // Gam dA = -Gam * (W X^T) (strictly lower, fp32, over dX);  K K^T on the lower
   // tiles: lambda, N = Gam dA * K K^T and M += diag(a) N, with their sums
 #pragma unroll
@@ -502,6 +530,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     Eb[swz_off<C>(r, c)] = from_f32<uint16_t>(as[r] * dAf[r * CPF + c] + as[c] * dAf[c * CPF + r]);
   }
   __syncthreads();
+  fresh();
   // dK += (dG + dG^T) K + 2 diag(dlambda) K
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
@@ -515,13 +544,16 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       const int r = 16 * rr + 4 * g + qq;
       dKa[i][qq] = fmaf(2.0f * dls[r], to_f32(Kt[swzw_off<DK>(r, cp)]), dKa[i][qq]);
       if constexpr (!SHARED) {  // dQ and dK staged as bf16 rows (physical key columns) over W and dA
-        dQs[r * CPG + cp] = from_f32<uint16_t>(dQa[i][qq]);
+        dQs[r * CPG + cp] = uint16_t(dQp[i][qq >> 1] >> (16 * (qq & 1)));
         dKs[r * CPG + cp] = from_f32<uint16_t>(dKa[i][qq]);
       }
     }
   }
-  __syncthreads();
-  if constexpr (!SHARED) {
+  if constexpr (SHARED) {
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) leave(dKa[i], dkh, (w + NWV * i) / NDT, (w + NWV * i) % NDT);
+  } else {
+    __syncthreads();
     auto* dq = static_cast<uint16_t*>(b.dq);
     auto* dk = static_cast<uint16_t*>(b.dk);
 #pragma unroll
@@ -534,29 +566,6 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
                                     reinterpret_cast<u32x4*>(dk + krow0 * DK + r * k_stride + 8 * ch));
       }
     }
-  } else {  // fp32 rows of this value head, dq then dk through one staging tile
-    float* F = f32p(S::TT);
-    constexpr int FP = S::FP, UF = C * DK / 4;
-    auto leave = [&](const f32x4 (&acc)[NQ], float* dst) {
-#pragma unroll
-      for (int i = 0; i < NQ; ++i) {
-        const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
-        const int cp = key_phys(16 * dt + li);
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq) F[(16 * rr + 4 * g + qq) * FP + cp] = acc[i][qq];
-      }
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < UF / NTH; ++i) {
-        const int u = tid + NTH * i, r = u / (DK / 4), ch = u % (DK / 4);
-        if (r < valid)
-          *reinterpret_cast<f32x4*>(dst + (row0 + int64_t(r) * H) * DK + 4 * ch) =
-              *reinterpret_cast<const f32x4*>(F + r * FP + 4 * ch);
-      }
-    };
-    leave(dQa, dqh);
-    __syncthreads();
-    leave(dKa, dkh);
   }
 }
 
