@@ -17,6 +17,11 @@
 //     accumulators before dP K is added.  <dS', S> is summed from the tiles.
 //   * M = dP0 * P + diag(a) N of gated_bwd.h: Q K^T is formed once more in fp32
 //     at the end (P itself was rounded to bf16), on the tiles that hold dP.
+// Every product is formed transposed: an accumulator tile then holds, in one lane,
+// four consecutive columns of one row (token), so tiles are written to the LDS
+// and rows of K and Q read beside them as 8-byte pieces (4 elements) instead of
+// one by one, a row's gate is one value a lane, and a row sum is three adds and
+// two lane exchanges.
 // Shared key heads (SHARED): dq and dk of every value head leave in fp32, and
 // gated_head_sum_kernel adds them up.
 // 79 KiB of LDS; bound as bwd_chunk_tr_kernel by the latency of its loads.
@@ -135,11 +140,22 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     }
     dma_rows(dOt, dout, v0);
   };
+  // tile (rt, c) of a [C][BV] array: lane (li, g) holds row 16 rt + li, columns 16 c + 4 g ..
   auto put = [&](uint16_t* X, const f32x4& a, int rt, int c, int li, int g) {
-#pragma unroll
-    for (int qq = 0; qq < 4; ++qq) X[swz_off<BV>(16 * rt + 4 * g + qq, 16 * c + li)] = from_f32<uint16_t>(a[qq]);
+    st4(X + swz_off<BV>(16 * rt + li, 16 * c + 4 * g), a);
+  };
+  auto rows4 = [](float s) {  // sum over the four lanes of a row
+    s += __shfl_xor(s, 16);
+    return s + __shfl_xor(s, 32);
+  };
+  auto sum4 = [](const f32x4& a, const f32x4& b_) {
+    return fmaf(a[0], b_[0], fmaf(a[1], b_[1], fmaf(a[2], b_[2], a[3] * b_[3])));
   };
 
+  // The [C][DK] tiles of a wavefront: two rows by two (d_k 64: one) columns, so
+  // that fragments serve two products; reading them is what the LDS is busiest with.
+  auto q_row = [&](int i) { return 2 * (w >> 2) + (i & 1); };
+  auto q_col = [&](int i) { return NQ / 2 * (w & 3) + (i >> 1); };
   f32x4 dQa[NQ], dKa[NQ], dPa[NP], dTa[NP];
 #pragma unroll
   for (int i = 0; i < NQ; ++i) dQa[i] = dKa[i] = zero4();
@@ -177,21 +193,16 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
 #pragma unroll
       for (int ku = 0; ku < NKU_D; ++ku) {
         const Frag<uint16_t> a = wide_frag<DK>(Kt, 16 * rt + li, ku, g);
-        mma(d, a, wide_frag<DK>(St, 16 * c + li, ku, g));
-        mma(du, a, wide_frag<DK>(dSt, 16 * c + li, ku, g));
+        mma(d, wide_frag<DK>(St, 16 * c + li, ku, g), a);
+        mma(du, wide_frag<DK>(dSt, 16 * c + li, ku, g), a);
       }
-      const f32x4 e4 = *reinterpret_cast<const f32x4*>(es + 16 * rt + 4 * g);
-      const f32x4 w4 = *reinterpret_cast<const f32x4*>(ws + 16 * rt + 4 * g);
-#pragma unroll
-      for (int qq = 0; qq < 4; ++qq) {
-        eks[qq] = e4[qq] * d[qq];
-        wkd[qq] = w4[qq] * du[qq];
-      }
+      eks = es[16 * rt + li] * d;
+      wkd = ws[16 * rt + li] * du;
       du = wkd;
 #pragma unroll
       for (int ku = 0; ku < NKU_C; ++ku)
-        if (32 * ku + 31 >= 16 * rt) mma(du, sw_frag_tr<C>(Pt, 16 * rt, ku, lane), sw_frag_tr<BV>(dOt, 16 * c, ku, lane));
-      const bf16x4 vv = lds_read_tr(Vt + swz_off<BV>(16 * rt + 4 * g + (li >> 2), 16 * c + 4 * (li & 3)));
+        if (32 * ku + 31 >= 16 * rt) mma(du, sw_frag_tr<BV>(dOt, 16 * c, ku, lane), sw_frag_tr<C>(Pt, 16 * rt, ku, lane));
+      const bf16x4 vv = *reinterpret_cast<const bf16x4*>(Vt + swz_off<BV>(16 * rt + li, 16 * c + 4 * g));
 #pragma unroll
       for (int qq = 0; qq < 4; ++qq) d[qq] = static_cast<float>(vv[qq]) - eks[qq];
       put(Dt, d, rt, c, li, g);
@@ -216,30 +227,18 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       f32x4 u = zero4(), dd = zero4();
 #pragma unroll
       for (int ku = 0; ku < NKU_C; ++ku) {
-        if (32 * ku <= 16 * rt + 15) mma(u, sw_frag<C>(Tt, 16 * rt + li, ku, g), sw_frag_tr<BV>(Dt, 16 * c, ku, lane));
+        if (32 * ku <= 16 * rt + 15) mma(u, sw_frag_tr<BV>(Dt, 16 * c, ku, lane), sw_frag<C>(Tt, 16 * rt + li, ku, g));
         if (32 * ku + 31 >= 16 * rt)
-          mma(dd, sw_frag_tr<C>(Tt, 16 * rt, ku, lane), sw_frag_tr<BV>(dUt, 16 * c, ku, lane));
+          mma(dd, sw_frag_tr<BV>(dUt, 16 * c, ku, lane), sw_frag_tr<C>(Tt, 16 * rt, ku, lane));
       }
       put(Ut, u, rt, c, li, g);
       put(dDt, dd, rt, c, li, g);
-      const f32x4 e4 = *reinterpret_cast<const f32x4*>(es + 16 * rt + 4 * g);
-      const f32x4 w4 = *reinterpret_cast<const f32x4*>(ws + 16 * rt + 4 * g);
-      float xs[4], wk[4];
-#pragma unroll
-      for (int qq = 0; qq < 4; ++qq) {
-        xs[qq] = row_sum16(dd[qq] * eks[qq]);
-        wk[qq] = row_sum16(u[qq] * wkd[qq]);
-        u[qq] *= w4[qq];
-        dd[qq] *= -e4[qq];
-      }
-      put(Wt, u, rt, c, li, g);
-      put(eDt, dd, rt, c, li, g);
-      if (li == 0) {  // one lane per row and tile column: its own place
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq) {
-          xw[c][16 * rt + 4 * g + qq] += xs[qq];
-          xw[2 + c][16 * rt + 4 * g + qq] += wk[qq];
-        }
+      const float xs = rows4(sum4(dd, eks)), wk = rows4(sum4(u, wkd));
+      put(Wt, ws[16 * rt + li] * u, rt, c, li, g);
+      put(eDt, -es[16 * rt + li] * dd, rt, c, li, g);
+      if (g == 0) {  // one lane per row and tile column: its own place
+        xw[c][16 * rt + li] += xs;
+        xw[2 + c][16 * rt + li] += wk;
       }
     }
     __syncthreads();
@@ -262,18 +261,18 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     // dQ += dO S^T (unscaled);  dK += (w U) dS'^T + (-e dD) S^T;  dP0 += dO U^T;  dT += dU D^T
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
-      const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
+      const int rr = q_row(i), dt = q_col(i);
       const Frag<uint16_t> bS = wide_frag_tr<DK>(St, dt, 0, lane);
-      mma(dQa[i], sw_frag<BV>(dOt, 16 * rr + li, 0, g), bS);
-      mma(dKa[i], sw_frag<BV>(Wt, 16 * rr + li, 0, g), wide_frag_tr<DK>(dSt, dt, 0, lane));
-      mma(dKa[i], sw_frag<BV>(eDt, 16 * rr + li, 0, g), bS);
+      mma(dQa[i], bS, sw_frag<BV>(dOt, 16 * rr + li, 0, g));
+      mma(dKa[i], wide_frag_tr<DK>(dSt, dt, 0, lane), sw_frag<BV>(Wt, 16 * rr + li, 0, g));
+      mma(dKa[i], bS, sw_frag<BV>(eDt, 16 * rr + li, 0, g));
     }
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int t = w + NWV * i, rr = t / NRT, jt = t % NRT;
       if (jt <= rr) {
-        mma(dPa[i], sw_frag<BV>(dOt, 16 * rr + li, 0, g), sw_frag<BV>(Ut, 16 * jt + li, 0, g));
-        mma(dTa[i], sw_frag<BV>(dUt, 16 * rr + li, 0, g), sw_frag<BV>(Dt, 16 * jt + li, 0, g));
+        mma(dPa[i], sw_frag<BV>(Ut, 16 * jt + li, 0, g), sw_frag<BV>(dOt, 16 * rr + li, 0, g));
+        mma(dTa[i], sw_frag<BV>(Dt, 16 * jt + li, 0, g), sw_frag<BV>(dUt, 16 * rr + li, 0, g));
       }
     }
     if (v0 + BV < DV) {
@@ -303,6 +302,15 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     hi = from_f32<uint16_t>(x);
     lo = from_f32<uint16_t>(x - to_f32(hi));
   };
+  auto split4 = [&](const f32x4& x, uint16_t* hi, uint16_t* lo) {  // four values, 8 bytes of each part
+    uint16_t h4[4], l4[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) split(x[e], h4[e], l4[e]);
+    *reinterpret_cast<uint2*>(hi) = *reinterpret_cast<const uint2*>(h4);
+    *reinterpret_cast<uint2*>(lo) = *reinterpret_cast<const uint2*>(l4);
+  };
+  // key columns of the four values a lane holds of tile column dt, as stored
+  auto key4 = [&](int dt) { return key_phys(16 * dt + 4 * g); };
   auto mma3 = [](f32x4& acc, const Frag<uint16_t>& ah, const Frag<uint16_t>& al, const Frag<uint16_t>& bh_,
                  const Frag<uint16_t>& bl) {
     mma(acc, ah, bh_);
@@ -318,19 +326,18 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       st16(Qt + swzw_off<DK>(valid + i / (DK / 8), 8 * (i % (DK / 8))), Z);
     __syncthreads();
   }
-  // Y1 = diag(e) dO S^T, and q . Y1 row by row (a wavefront's tiles lie in one
-  // or two columns dt: partial sums by dt)
+  // Y1 = diag(e) dO S^T, and q . Y1 row by row (partial sums by dt)
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
-    const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
-    const int cp = key_phys(16 * dt + li);
+    const int rr = q_row(i), dt = q_col(i);
+    const int r = 16 * rr + li;
+    dQa[i] *= es[r];
+    const bf16x4 qv = *reinterpret_cast<const bf16x4*>(Qt + swzw_off<DK>(r, key4(dt)));
+    f32x4 qf;
 #pragma unroll
-    for (int qq = 0; qq < 4; ++qq) {
-      const int r = 16 * rr + 4 * g + qq;
-      dQa[i][qq] *= es[r];
-      const float s = row_sum16(dQa[i][qq] * to_f32(Qt[swzw_off<DK>(r, cp)]));
-      if (li == 0) red[dt * C + r] = s;
-    }
+    for (int qq = 0; qq < 4; ++qq) qf[qq] = static_cast<float>(qv[qq]);
+    const float s = rows4(sum4(dQa[i], qf));
+    if (g == 0) red[dt * C + r] = s;
   }
   fresh();
   // dP = Gam * dP0 as bf16, dT fp32, X as high and low parts; the first part of
@@ -339,35 +346,29 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int t = w + NWV * i, rr = t / NRT, jt = t % NRT;
+    const int r = 16 * rr + li, c = 16 * jt + 4 * g;
     f32x4 qk = zero4();
     if (jt <= rr) {
 #pragma unroll
       for (int ku = 0; ku < NKU_D; ++ku)
-        mma(qk, wide_frag<DK>(Qt, 16 * rr + li, ku, g), wide_frag<DK>(Kt, 16 * jt + li, ku, g));
+        mma(qk, wide_frag<DK>(Kt, 16 * jt + li, ku, g), wide_frag<DK>(Qt, 16 * rr + li, ku, g));
     }
-    const float gj = gs[16 * jt + li];
+    const float gr = gs[r];
+    const f32x4 gj = *reinterpret_cast<const f32x4*>(gs + c);
+    f32x4 p, dt_;
 #pragma unroll
     for (int qq = 0; qq < 4; ++qq) {
-      const int r = 16 * rr + 4 * g + qq, c = 16 * jt + li;
-      const float p = c <= r ? dPa[i][qq] * exp2_gate(gs[r] - gj) : 0.0f;
-      M[i][qq] = c < r ? p * qk[qq] : 0.0f;
-      dPt[swz_off<C>(r, c)] = from_f32<uint16_t>(p);
-      A0[r * CPF + c] = c <= r ? dTa[i][qq] : 0.0f;
+      p[qq] = c + qq <= r ? dPa[i][qq] * exp2_gate(gr - gj[qq]) : 0.0f;
+      M[i][qq] = c + qq < r ? p[qq] * qk[qq] : 0.0f;
+      dt_[qq] = c + qq <= r ? dTa[i][qq] : 0.0f;
     }
+    st4(dPt + swz_off<C>(r, c), p);
+    st4(A0 + r * CPF + c, dt_);
   }
 #pragma unroll
   for (int i = 0; i < UX / NTH; ++i) {
     const int u = tid + NTH * i, r = u / (C / 4), ch = u % (C / 4);
-    union {
-      u32x4 u;
-      float f[4];
-    } x;
-    x.u = rx[i];
-    uint16_t hi[4], lo[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) split(x.f[e], hi[e], lo[e]);
-    *reinterpret_cast<uint2*>(Xh + swz_off<C>(r, 4 * ch)) = *reinterpret_cast<const uint2*>(hi);
-    *reinterpret_cast<uint2*>(Xl + swz_off<C>(r, 4 * ch)) = *reinterpret_cast<const uint2*>(lo);
+    split4(__builtin_bit_cast(f32x4, rx[i]), Xh + swz_off<C>(r, 4 * ch), Xl + swz_off<C>(r, 4 * ch));
   }
   __syncthreads();
   if (tid < C) {  // y_i so far
@@ -380,35 +381,30 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
   // dQ += dP K;  dK += dP^T Q
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
-    const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
+    const int rr = q_row(i), dt = q_col(i);
 #pragma unroll
     for (int ku = 0; ku < NKU_C; ++ku) {
       if (32 * ku <= 16 * rr + 15)
-        mma(dQa[i], sw_frag<C>(dPt, 16 * rr + li, ku, g), wide_frag_tr<DK>(Kt, dt, ku, lane));
+        mma(dQa[i], wide_frag_tr<DK>(Kt, dt, ku, lane), sw_frag<C>(dPt, 16 * rr + li, ku, g));
       if (32 * ku + 31 >= 16 * rr)
-        mma(dKa[i], sw_frag_tr<C>(dPt, 16 * rr, ku, lane), wide_frag_tr<DK>(Qt, dt, ku, lane));
+        mma(dKa[i], wide_frag_tr<DK>(Qt, dt, ku, lane), sw_frag_tr<C>(dPt, 16 * rr, ku, lane));
     }
   }
   // dQ is complete: it waits for its place in the LDS as packed bf16 (half the
-  // registers), or, of a shared head, leaves in fp32 (pieces of 16 bytes, which
-  // the L2 joins)
-  uint32_t dQp[NQ][2];
+  // registers), or, of a shared head, leaves in fp32
+  uint2 dQp[NQ];
   auto leave = [&](const f32x4& x, float* dst, int rr, int dt) {
-    const int cp = key_phys(16 * dt + li);
-#pragma unroll
-    for (int qq = 0; qq < 4; ++qq) {
-      const int r = 16 * rr + 4 * g + qq;
-      if (r < valid) dst[(row0 + int64_t(r) * H) * DK + cp] = x[qq];
-    }
+    const int r = 16 * rr + li;
+    if (r < valid) *reinterpret_cast<f32x4*>(dst + (row0 + int64_t(r) * H) * DK + key4(dt)) = x;
   };
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
-    const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
-    if constexpr (SHARED) leave(dQa[i], dqh, rr, dt);
+    if constexpr (SHARED) leave(dQa[i], dqh, q_row(i), q_col(i));
     else {
+      bf16x4 x;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        dQp[i][j] = uint32_t(from_f32<uint16_t>(dQa[i][2 * j])) | uint32_t(from_f32<uint16_t>(dQa[i][2 * j + 1])) << 16;
+      for (int qq = 0; qq < 4; ++qq) x[qq] = static_cast<__bf16>(dQa[i][qq]);
+      dQp[i] = __builtin_bit_cast(uint2, x);
     }
   }
   __syncthreads();  // red is read, Q and dP are done with
@@ -420,12 +416,11 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       s = fmaf(A0[r * CPF + cr], to_f32(Xh[swz_off<C>(r, cr)]) + to_f32(Xl[swz_off<C>(r, cr)]), s);
     red[prt * C + cr] = s;
   }
-  for (int i = tid; i < C * C; i += NTH) {
-    const int r = i / C, c = i % C;
-    uint16_t hi, lo;
-    split(A0[r * CPF + c] * as[c], hi, lo);
-    dXh[swz_off<C>(r, c)] = hi;
-    dXl[swz_off<C>(r, c)] = lo;
+#pragma unroll
+  for (int i = 0; i < C * C / 4 / NTH; ++i) {
+    const int u = tid + NTH * i, r = u / (C / 4), c = 4 * (u % (C / 4));
+    split4(*reinterpret_cast<const f32x4*>(A0 + r * CPF + c) * *reinterpret_cast<const f32x4*>(as + c),
+           dXh + swz_off<C>(r, c), dXl + swz_off<C>(r, c));
   }
   __syncthreads();
   if (tid < C) {
@@ -443,16 +438,10 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
 #pragma unroll
     for (int ku = 0; ku < NKU_C; ++ku)
       if (32 * ku + 31 >= 16 * rr && 32 * ku + 31 >= 16 * jt)  // X and dT are lower triangular
-        mma3(acc, sw_frag_tr<C>(Xh, 16 * rr, ku, lane), sw_frag_tr<C>(Xl, 16 * rr, ku, lane),
-             sw_frag_tr<C>(dXh, 16 * jt, ku, lane), sw_frag_tr<C>(dXl, 16 * jt, ku, lane));
-#pragma unroll
-    for (int qq = 0; qq < 4; ++qq) {
-      const int r = 16 * rr + 4 * g + qq, c = 16 * jt + li;
-      uint16_t hi, lo;
-      split(acc[qq], hi, lo);
-      Wh[swz_off<C>(r, c)] = hi;
-      Wl[swz_off<C>(r, c)] = lo;
-    }
+        mma3(acc, sw_frag_tr<C>(dXh, 16 * jt, ku, lane), sw_frag_tr<C>(dXl, 16 * jt, ku, lane),
+             sw_frag_tr<C>(Xh, 16 * rr, ku, lane), sw_frag_tr<C>(Xl, 16 * rr, ku, lane));
+    const int at = swz_off<C>(16 * rr + li, 16 * jt + 4 * g);
+    split4(acc, Wh + at, Wl + at);
   }
   __syncthreads();
   fresh();
@@ -466,32 +455,34 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
 #pragma unroll
       for (int ku = 0; ku < NKU_C; ++ku)
         if (32 * ku <= 16 * jt + 15)  // X^T's rows of this tile are zero past column 16 jt + 15
-          mma3(acc, sw_frag<C>(Wh, 16 * rr + li, ku, g), sw_frag<C>(Wl, 16 * rr + li, ku, g),
-               sw_frag<C>(Xh, 16 * jt + li, ku, g), sw_frag<C>(Xl, 16 * jt + li, ku, g));
+          mma3(acc, sw_frag<C>(Xh, 16 * jt + li, ku, g), sw_frag<C>(Xl, 16 * jt + li, ku, g),
+               sw_frag<C>(Wh, 16 * rr + li, ku, g), sw_frag<C>(Wl, 16 * rr + li, ku, g));
 #pragma unroll
       for (int ku = 0; ku < NKU_D; ++ku)
-        mma(gg, wide_frag<DK>(Kt, 16 * rr + li, ku, g), wide_frag<DK>(Kt, 16 * jt + li, ku, g));
+        mma(gg, wide_frag<DK>(Kt, 16 * jt + li, ku, g), wide_frag<DK>(Kt, 16 * rr + li, ku, g));
     }
-    const float gj = gs[16 * jt + li];
-    float cs = 0.0f;
+    const int r = 16 * rr + li, c = 16 * jt + 4 * g;
+    const float gr = gs[r], ar = as[r];
+    const f32x4 gj = *reinterpret_cast<const f32x4*>(gs + c);
+    f32x4 da;
+    float s = 0.0f, sm = 0.0f;
 #pragma unroll
     for (int qq = 0; qq < 4; ++qq) {
-      const int r = 16 * rr + 4 * g + qq, c = 16 * jt + li;
-      const float da = c < r ? -acc[qq] * exp2_gate(gs[r] - gj) : 0.0f;
-      dAf[r * CPF + c] = da;
-      if (c == r) lam[r] = gg[qq];
-      const float nn = da * gg[qq];
-      const float m = fmaf(as[r], nn, M[i][qq]);
-      cs += m;
-      const float s = row_sum16(nn), sm = row_sum16(m);
-      if (li == 0) {
-        red[jt * C + r] = s;
-        msum[jt * C + r] = sm;
-      }
+      da[qq] = c + qq < r ? -acc[qq] * exp2_gate(gr - gj[qq]) : 0.0f;
+      if (c + qq == r) lam[r] = gg[qq];
+      const float nn = da[qq] * gg[qq], m = fmaf(ar, nn, M[i][qq]);
+      s += nn;
+      sm += m;
+      const float cs = row_sum16(m);  // over the tile's rows
+      if (li == 0) msum[(NRT + rr) * C + c + qq] = cs;
     }
-    cs += __shfl_xor(cs, 16);
-    cs += __shfl_xor(cs, 32);
-    if (g == 0) msum[(NRT + rr) * C + 16 * jt + li] = cs;
+    *reinterpret_cast<f32x4*>(dAf + r * CPF + c) = da;
+    s = rows4(s);
+    sm = rows4(sm);
+    if (g == 0) {
+      red[jt * C + r] = s;
+      msum[jt * C + r] = sm;
+    }
   }
   __syncthreads();
   // da_i += sum_j N_ij, then dbeta and dlambda;  dg;  dG + dG^T as bf16 (over X)
@@ -525,33 +516,36 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     if (tid < valid)
       static_cast<uint16_t*>(b.dg)[row0 + int64_t(tid) * H] = from_f32<uint16_t>(fmaf(es[C - 1], all, before - wj + after));
   }
-  for (int i = tid; i < C * C; i += NTH) {
-    const int r = i / C, c = i % C;
-    Eb[swz_off<C>(r, c)] = from_f32<uint16_t>(as[r] * dAf[r * CPF + c] + as[c] * dAf[c * CPF + r]);
+#pragma unroll
+  for (int i = 0; i < C * C / 4 / NTH; ++i) {
+    const int u = tid + NTH * i, r = u / (C / 4), c = 4 * (u % (C / 4));
+    f32x4 x = as[r] * *reinterpret_cast<const f32x4*>(dAf + r * CPF + c);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = fmaf(as[c + e], dAf[(c + e) * CPF + r], x[e]);
+    st4(Eb + swz_off<C>(r, c), x);
   }
   __syncthreads();
   fresh();
   // dK += (dG + dG^T) K + 2 diag(dlambda) K
 #pragma unroll
   for (int i = 0; i < NQ; ++i) {
-    const int t = w + NWV * i, rr = t / NDT, dt = t % NDT;
+    const int rr = q_row(i), dt = q_col(i);
 #pragma unroll
     for (int ku = 0; ku < NKU_C; ++ku)
-      mma(dKa[i], sw_frag<C>(Eb, 16 * rr + li, ku, g), wide_frag_tr<DK>(Kt, dt, ku, lane));
-    const int cp = key_phys(16 * dt + li);
+      mma(dKa[i], wide_frag_tr<DK>(Kt, dt, ku, lane), sw_frag<C>(Eb, 16 * rr + li, ku, g));
+    const int r = 16 * rr + li, cp = key4(dt);
+    const float dl = 2.0f * dls[r];
+    const bf16x4 kv = *reinterpret_cast<const bf16x4*>(Kt + swzw_off<DK>(r, cp));
 #pragma unroll
-    for (int qq = 0; qq < 4; ++qq) {
-      const int r = 16 * rr + 4 * g + qq;
-      dKa[i][qq] = fmaf(2.0f * dls[r], to_f32(Kt[swzw_off<DK>(r, cp)]), dKa[i][qq]);
-      if constexpr (!SHARED) {  // dQ and dK staged as bf16 rows (physical key columns) over W and dA
-        dQs[r * CPG + cp] = uint16_t(dQp[i][qq >> 1] >> (16 * (qq & 1)));
-        dKs[r * CPG + cp] = from_f32<uint16_t>(dKa[i][qq]);
-      }
+    for (int qq = 0; qq < 4; ++qq) dKa[i][qq] = fmaf(dl, static_cast<float>(kv[qq]), dKa[i][qq]);
+    if constexpr (!SHARED) {  // dQ and dK staged as bf16 rows over W and dA
+      *reinterpret_cast<uint2*>(dQs + r * CPG + cp) = dQp[i];
+      st4(dKs + r * CPG + cp, dKa[i]);
     }
   }
   if constexpr (SHARED) {
 #pragma unroll
-    for (int i = 0; i < NQ; ++i) leave(dKa[i], dkh, (w + NWV * i) / NDT, (w + NWV * i) % NDT);
+    for (int i = 0; i < NQ; ++i) leave(dKa[i], dkh, q_row(i), q_col(i));
   } else {
     __syncthreads();
     auto* dq = static_cast<uint16_t*>(b.dq);
