@@ -13,11 +13,13 @@ namespace efla {
 // step is bound by HBM (8 d_k d_v bytes a head).  One workgroup per request,
 // head and DVW value columns; thread (rg, cq) keeps columns 4 cq .. 4 cq + 3 of
 // rows rg, rg + NRG, .. in registers, and r and p are summed through LDS.
-// States are read and written past the caches (nontemporal): a step touches
-// each once, and a model's other layers run before the next one.  256 requests
-// of 16 heads, d 128 (541 MB, three pools in turn): 106.7 us with ordinary
-// accesses and whole states per workgroup, 99.4 us nontemporal, 96.3 us with 64
-// columns a workgroup, 98.2 us with 32 (a large in-place copy's rate: 89 us).
+// States are written past the caches (nontemporal): a step touches each once,
+// and a model's other layers run before the next one.  Measured with three pools
+// in turn, bf16, 16 heads, d 128, ordinary / nontemporal loads / stores / both:
+// 256 requests (541 MB) 106.0 / 103.1 / 97.6 / 96.3 us (whole states per
+// workgroup, ordinary: 106.7; a large in-place scale's rate: 89 us), 84 requests
+// (177 MB) 31.6 / 30.8 / 30.5 / 33.6 us: part of a smaller pool stays in the
+// last-level cache and is lost to nontemporal loads.
 // A row of the batch whose slot lies outside the pool has no request: its
 // state does not exist and its row of o is left as it was.
 template <typename T, int DK, int DVW>
@@ -46,8 +48,7 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(
   f32x4 S[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
-    S[i] = on ? __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(Su + int64_t(rg + i * NRG) * DV + 4 * cq))
-              : zero4();
+    S[i] = on ? *reinterpret_cast<const f32x4*>(Su + int64_t(rg + i * NRG) * DV + 4 * cq) : zero4();
   if (tid < DK) {
     ks[tid] = to_f32(k[uk * DK + tid]);
     qs[tid] = to_f32(q[uk * DK + tid]);

@@ -556,11 +556,17 @@ def _at(t) -> int:
     return 0 if t is None else t.data_ptr()
 
 
+# A stream's handle without the Python object around it (2 us of a decode call's
+# 10 on the host), where this torch has that function.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn, index: int, where: str, *args) -> None:
     """fn(*args, stream) on torch's current stream of device ``index``, with
     that device current.  A call of a decode step costs more on the host than
     on the GPU, so the device is switched only where it is another one."""
-    stream = torch.cuda.current_stream(index).cuda_stream
+    stream = _raw_stream(index)
     if torch.cuda.current_device() == index:
         status = fn(*args, stream)
     else:
