@@ -15,10 +15,20 @@ efla_status check_gated_shape(int B, int H, int Hk, int64_t L, int d_k, int d_v,
   return H % Hk == 0 ? EFLA_OK : EFLA_ERR_INVALID_ARG;
 }
 
-// Which forward kernels run: the chunked matrix-core pass where its shapes and
-// type allow, else token by token in float32.
-bool gated_chunked(int d_k, int d_v, int chunk, efla_dtype dt) {
-  return dt == EFLA_BF16 && efla::gated_chunk_supported(d_k, d_v, chunk);
+// Which forward kernels run over `seqs` sequences of at most L tokens: the
+// chunked matrix-core passes for bf16 at their shapes (whatever chunk the caller
+// names: it does not change the result), else the fp32 recurrence.  The latter
+// also where it is the faster of the two, short sequences and few workgroups:
+// one launch against two, but time per token.  Measured (bf16, us, recurrence /
+// chunks; workgroups = seqs H d_v / 16):
+//   d 128,  128 workgroups: L 16  7.3 / 12.4, 48 12.4 / 13.2, 64 14.8 / 13.6
+//   d 128, 1024:            L 8  15.5 / 18.2, 16 19.2 / 18.2, 24 24.1 / 18.5
+//   d 64,   512:            L 16  7.0 / 12.7, 48 12.3 / 13.1, 64 15.1 / 13.4
+//   d 64,  4096:            L 8  31.7 / 46.0, 24 51.2 / 45.8
+bool gated_chunked(int64_t seqs, int H, int64_t L, int d_k, int d_v, efla_dtype dt) {
+  if (dt != EFLA_BF16 || !efla::gated_chunk_supported(d_k, d_v)) return false;
+  const int64_t wgs = seqs * H * (d_v / 16);
+  return L > 48 || wgs > 4096 || L * wgs * d_k > 1500000;
 }
 
 template <typename F>
@@ -27,7 +37,7 @@ efla_status by_type(efla_dtype dt, F&& f) {
 }
 
 efla_status gated_forward(const efla::GatedFwd& a, int chunk, efla_dtype dt, void* workspace, hipStream_t s) {
-  if (a.L > 0 && gated_chunked(a.DK, a.DV, chunk, dt)) return from_hip(efla::launch_gated_chunk(a, workspace, s));
+  if (a.L > 0 && gated_chunked(a.cu == nullptr ? a.B : a.N, a.H, a.L, a.DK, a.DV, dt)) return from_hip(efla::launch_gated_chunk(a, workspace, s));
   return by_type(dt, [&](auto t) { return efla::launch_gated_recurrent<decltype(t)>(a, nullptr, chunk, s); });
 }
 
@@ -38,7 +48,7 @@ extern "C" {
 size_t efla_gated_chunk_fwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
                                            efla_dtype dtype) {
   if (check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || L == 0) return 0;
-  return gated_chunked(d_k, d_v, chunk, dtype) ? efla::gated_fwd_layout(B, 0, H, L, false).total : 0;
+  return gated_chunked(B, H, L, d_k, d_v, dtype) ? efla::gated_fwd_layout(B, 0, H, L, false).total : 0;
 }
 
 efla_status efla_gated_chunk_fwd(const void* q, const void* k, const void* v, const void* beta, const float* g,
@@ -64,7 +74,7 @@ efla_status efla_gated_chunk_fwd(const void* q, const void* k, const void* v, co
 size_t efla_gated_chunk_fwd_varlen_workspace_size(int N, int H, int Hk, int64_t T, int d_k, int d_v, int chunk,
                                                   efla_dtype dtype) {
   if (check_gated_shape(N, H, Hk, T, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || T == 0) return 0;
-  return gated_chunked(d_k, d_v, chunk, dtype) ? efla::gated_fwd_layout(0, N, H, T, true).total : 0;
+  return gated_chunked(N, H, T, d_k, d_v, dtype) ? efla::gated_fwd_layout(0, N, H, T, true).total : 0;
 }
 
 efla_status efla_gated_chunk_fwd_varlen(const void* q, const void* k, const void* v, const void* beta, const float* g,
@@ -77,7 +87,7 @@ efla_status efla_gated_chunk_fwd_varlen(const void* q, const void* k, const void
   if (st != EFLA_OK) return st;
   if (slots == nullptr && P < N) return EFLA_ERR_INVALID_ARG;
   if (N == 0) return EFLA_OK;
-  if (int64_t(H) * (T / chunk + N) > kMaxGrid) return EFLA_ERR_UNSUPPORTED;
+  if (int64_t(H) * (T / 16 + N) > kMaxGrid) return EFLA_ERR_UNSUPPORTED;
   if (cu_seqlens == nullptr) return EFLA_ERR_INVALID_ARG;
   if (T > 0) {
     if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || o == nullptr)

@@ -48,7 +48,11 @@ __device__ __forceinline__ float wave_scan_f32(float x, int lane) {
 }
 
 // ---------------------------------------------------------------------------
-// T, X, P, a and G of every chunk, fp32, one workgroup per chunk.
+// T, X, P, a and G of every chunk, fp32, one workgroup per chunk.  X by blocks of
+// 16 rows: the rows above contribute by matrix products, spread over the
+// wavefronts, then a thread per column solves the diagonal block out of
+// registers (row by row over the whole chunk, one wavefront took 35 us of a
+// chunk's 40).
 // ---------------------------------------------------------------------------
 template <typename T, int DK, int C>
 __global__ __launch_bounds__(kThreads) void gated_ut_kernel(GatedBwd b, float* __restrict__ tws,
@@ -59,6 +63,7 @@ __global__ __launch_bounds__(kThreads) void gated_ut_kernel(GatedBwd b, float* _
   __shared__ __align__(16) float Ks[CP * QP];
   __shared__ __align__(16) float Am[CP * CPP];
   __shared__ __align__(16) float Xm[CP * CPP];
+  __shared__ __align__(16) float Rm[16 * CPP];
   __shared__ float as[CP], gs[CP];
   const int64_t slot = blockIdx.x;
   const int n = int(slot % NC);
@@ -109,15 +114,28 @@ __global__ __launch_bounds__(kThreads) void gated_ut_kernel(GatedBwd b, float* _
     if (tid < C) aws[slot * C + tid] = a;
   }
   __syncthreads();
-  // forward substitution, thread c on column c: x_r = delta_rc - a_r sum_{m<r} (Gam * G)_rm x_m
-  if (tid < CP) {
-    for (int r = 0; r < CP; ++r) {
-      float s = 0.0f;
-      for (int m = 0; m < r; ++m) s = fmaf(Am[r * CPP + m], Xm[m * CPP + tid], s);
-      Xm[r * CPP + tid] = (r == tid ? 1.0f : 0.0f) - as[r] * s;
+  // x_r = delta_rc - a_r sum_{m<r} (Gam * G)_rm x_m
+  for (int b0 = 0; b0 < CP; b0 += 16) {
+    for (int jt = w; 16 * jt < b0; jt += 4) {
+      f32x4 acc = zero4();
+      tile_mma16<false, false>(acc, Am, CPP, Xm, CPP, b0, 16 * jt, b0, li, g);
+#pragma unroll
+      for (int qq = 0; qq < 4; ++qq) Rm[(4 * g + qq) * CPP + 16 * jt + li] = acc[qq];
     }
+    __syncthreads();
+    if (tid < CP) {
+      float x[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        float s = tid < b0 ? Rm[r * CPP + tid] : 0.0f;
+#pragma unroll
+        for (int m = 0; m < r; ++m) s = fmaf(Am[(b0 + r) * CPP + b0 + m], x[m], s);
+        x[r] = (b0 + r == tid ? 1.0f : 0.0f) - as[b0 + r] * s;
+        Xm[(b0 + r) * CPP + tid] = x[r];
+      }
+    }
+    __syncthreads();
   }
-  __syncthreads();
   for (int i = tid; i < C * C; i += kThreads) {
     const int r = i / C, c = i % C;
     const float x = Xm[r * CPP + c];

@@ -2,7 +2,8 @@
 // workspace, every region 256-byte aligned, per chunk slot ((b H + h) NC + n).
 //   fp32 arithmetic (gated_bwd.h; every type and size), all fp32:
 //     T, X, P [C][C]; a, G [C]; S, dS [d_k][d_v]
-//   bf16 matrix cores (bf16 inputs, chunk 64, d_k 64 or 128, d_v % 32 == 0):
+//   bf16 matrix cores (bf16 inputs, d_k 64 or 128, d_v % 32 == 0; chunks of 64
+//   whatever chunk the caller names):
 //     T fragments (12 KiB) and gate block (1 KiB) as the forward's, X fp32,
 //     T and P bf16 [C][C], Qe bf16 [C][d_k], S and dS bf16 [d_v][d_k]
 // and for both, where key heads are shared, dq and dk per value head in fp32,
@@ -21,15 +22,15 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 // at two tokens and two key heads; from some tens of scalars on, 4e-3 at most).
 // Either way the call is four or five launches of a few microseconds.
 constexpr int64_t kShort = 16;
-static bool gated_bwd_fast(int64_t L, int DK, int DV, int C, size_t esz) {
-  return esz == 2 && L > kShort && gated_chunk_supported(DK, DV, C);
+static bool gated_bwd_fast(int64_t L, int DK, int DV, size_t esz) {
+  return esz == 2 && L > kShort && gated_chunk_supported(DK, DV);
 }
 // chunk of the fp32 kernels (the result does not depend on it)
 static int fp32_chunk(int64_t L, int C) { return L <= kShort ? 16 : C; }
 
 static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t esz) {
-  const bool fast = gated_bwd_fast(L, DK, DV, C, esz);
-  if (!fast) C = fp32_chunk(L, C);
+  const bool fast = gated_bwd_fast(L, DK, DV, esz);
+  C = fast ? 64 : fp32_chunk(L, C);
   const size_t slots = size_t(B) * H * ((L + C - 1) / C);
   size_t at = 0;
   auto region = [&](size_t bytes) {
@@ -145,7 +146,7 @@ static hipError_t gated_bwd_c(const GatedBwd& b, int C, unsigned char* ws, hipSt
 template <typename T>
 hipError_t launch_gated_bwd(const GatedBwd& b, int C, void* workspace, hipStream_t s) {
   auto* ws = static_cast<unsigned char*>(workspace);
-  if (gated_bwd_fast(b.L, b.DK, b.DV, C, sizeof(T))) return gated_bwd_bf16(b, ws, s);
+  if (gated_bwd_fast(b.L, b.DK, b.DV, sizeof(T))) return gated_bwd_bf16(b, ws, s);
   C = fp32_chunk(b.L, C);
   switch (b.DK) {
     case 16: return gated_bwd_c<T, 16>(b, C, ws, s);

@@ -41,9 +41,7 @@ hipError_t split_impl(const GatedFwd& a, const uint16_t* tfr, const float* gws, 
 }
 }  // namespace
 
-bool gated_chunk_supported(int DK, int DV, int C) {
-  return C == kGatedChunk && (DK == 64 || DK == 128) && DV % 32 == 0;
-}
+bool gated_chunk_supported(int DK, int DV) { return (DK == 64 || DK == 128) && DV % 32 == 0; }
 
 GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed) {
   const size_t slots = packed ? size_t(H) * (L / kGatedChunk + N) : size_t(B) * H * ((L + kGatedChunk - 1) / kGatedChunk);

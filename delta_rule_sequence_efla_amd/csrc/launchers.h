@@ -164,12 +164,12 @@ struct GatedFwd {
 template <typename T>
 hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipStream_t s);
 
-// Chunked forward of bf16 inputs (gated_ut.h, gated_split.h): chunk 64, d_k 64
-// or 128, d_v a multiple of 32.
+// Chunked forward of bf16 inputs (gated_ut.h, gated_split.h): d_k 64 or 128, d_v
+// a multiple of 32, in chunks of 64.
 struct GatedFwdLayout {
   size_t t, g, order, total;
 };
-bool gated_chunk_supported(int DK, int DV, int C);
+bool gated_chunk_supported(int DK, int DV);
 GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed);
 hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s);
 // Its two launches as the backward runs them over a dense batch: T fragments and

@@ -9,8 +9,8 @@
 //
 // Up to kPlanSeqs sequences one launch does it all: every workgroup sums the
 // lengths for itself into LDS (16 KiB at most, read from L2) rather than wait
-// for another launch's sums, then fills its rows by binary search there; the
-// first N / 16 workgroups also rank 16 sequences each.  At these sizes the time
+// for another launch's sums; the first N / 16 then rank 16 sequences each, the
+// others fill their rows by binary search there.  At these sizes the time
 // is launch and load latency.  More sequences take a launch for the offsets
 // (order is then the index order) and one for the rows.
 #include "gated.h"
@@ -70,17 +70,20 @@ __device__ __forceinline__ int plan_seq(const int32_t* end, int N, int t) {
   }
   return lo;
 }
-// chunks of 2^shift tokens
-__device__ __forceinline__ int plan_chunks(const int32_t* end, int u, int shift) {
-  return (end[u] - (u > 0 ? end[u - 1] : 0) + (1 << shift) - 1) >> shift;
-}
-
-__device__ __forceinline__ void plan_rows(const int32_t* end, int N, int T, const int32_t* __restrict__ starts,
-                                          int32_t* __restrict__ seq, int32_t* __restrict__ pos) {
-  for (int i = 0; i < kPlanRows / kThreads; ++i) {
-    const int64_t t = int64_t(blockIdx.x) * kPlanRows + i * kThreads + threadIdx.x;
+// Rows blk * kPlanRows ..: a thread's four rows follow each other, so the search
+// is made for the first, and again where a row lies past the next sequence too.
+__device__ __forceinline__ void plan_rows(const int32_t* end, int N, int T, int64_t blk,
+                                          const int32_t* __restrict__ starts, int32_t* __restrict__ seq,
+                                          int32_t* __restrict__ pos) {
+  static_assert(kPlanRows == 4 * kThreads, "four rows a thread");
+  const int64_t t0 = blk * kPlanRows + 4 * threadIdx.x;
+  if (t0 >= T) return;
+  int u = plan_seq(end, N, int(t0));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t t = t0 + i;
     if (t >= T) return;
-    const int u = plan_seq(end, N, int(t));
+    if (u < N && end[u] <= t && ++u < N && end[u] <= t) u = plan_seq(end, N, int(t));
     const bool in = u < N;
     if (seq != nullptr) seq[t] = in ? u : -1;
     if (pos != nullptr)
@@ -89,34 +92,46 @@ __device__ __forceinline__ void plan_rows(const int32_t* end, int N, int T, cons
 }
 }  // namespace
 
+// The first rank_wgs workgroups rank kPlanRank sequences each (the very first
+// also writes the offsets), the others fill kPlanRows rows each.
 __global__ __launch_bounds__(kThreads) void plan_kernel(const int32_t* __restrict__ lengths,
-                                                        const int32_t* __restrict__ starts, int N, int T,
-                                                        int shift, int32_t* __restrict__ cu, int32_t* __restrict__ order,
-                                                        int32_t* __restrict__ seq, int32_t* __restrict__ pos) {
-  __shared__ int32_t end[kPlanSeqs];
+                                                        const int32_t* __restrict__ starts, int N, int T, int shift,
+                                                        int rank_wgs, int32_t* __restrict__ cu,
+                                                        int32_t* __restrict__ order, int32_t* __restrict__ seq,
+                                                        int32_t* __restrict__ pos) {
+  __shared__ __align__(16) int32_t end[kPlanSeqs];
+  __shared__ __align__(16) int32_t chunks[kPlanSeqs];
   __shared__ int wsum[kThreads / kWave];
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, blk = blockIdx.x;
   for (int u = tid; u < N; u += kThreads) end[u] = plan_length(lengths, u, T);
   __syncthreads();
   scan_lds(N, T, end, wsum);
-  if (blockIdx.x == 0) {
+  if (blk >= rank_wgs) {
+    if (seq != nullptr || pos != nullptr) plan_rows(end, N, T, blk - rank_wgs, starts, seq, pos);
+    return;
+  }
+  if (blk == 0)
     for (int u = tid; u <= N; u += kThreads) cu[u] = u > 0 ? end[u - 1] : 0;
-  }
-  // rank(u) = #{v : n(v) > n(u)} + #{v < u : n(v) = n(u)}
-  const int u = int(blockIdx.x) * kPlanRank + (tid >> 4);
-  if (order != nullptr && int(blockIdx.x) * kPlanRank < N) {
-    const int nu = u < N ? plan_chunks(end, u, shift) : 0;
-    int rank = 0;
+  if (order == nullptr) return;
+  // chunk counts, padded with -1 (below every count) to whole steps of 64
+  const int padded = (N + 63) / 64 * 64;
+  for (int u = tid; u < padded; u += kThreads)
+    chunks[u] = u < N ? (end[u] - (u > 0 ? end[u - 1] : 0) + (1 << shift) - 1) >> shift : -1;
+  __syncthreads();
+  // rank(u) = #{v : n(v) > n(u)} + #{v < u : n(v) = n(u)}, 16 lanes a sequence, four v a step
+  typedef int i32x4 __attribute__((ext_vector_type(4)));
+  const int u = blk * kPlanRank + (tid >> 4);
+  const int nu = u < N ? chunks[u] : 0;
+  int rank = 0;
 #pragma unroll 4
-    for (int x = tid & 15; x < N; x += 16) {
-      const int nv = plan_chunks(end, x, shift);
-      rank += (nv > nu || (nv == nu && x < u)) ? 1 : 0;
-    }
+  for (int x = 4 * (tid & 15); x < padded; x += 64) {
+    const i32x4 nv = *reinterpret_cast<const i32x4*>(chunks + x);
 #pragma unroll
-    for (int d = 8; d > 0; d >>= 1) rank += __shfl_xor(rank, d);
-    if ((tid & 15) == 0 && u < N) order[rank] = u;
+    for (int i = 0; i < 4; ++i) rank += nv[i] + (x + i < u ? 1 : 0) > nu ? 1 : 0;
   }
-  if (seq != nullptr || pos != nullptr) plan_rows(end, N, T, starts, seq, pos);
+#pragma unroll
+  for (int d = 8; d > 0; d >>= 1) rank += __shfl_xor(rank, d);
+  if ((tid & 15) == 0 && u < N) order[rank] = u;
 }
 
 __global__ __launch_bounds__(kThreads) void plan_offsets_kernel(const int32_t* __restrict__ lengths, int N, int T,
@@ -141,7 +156,7 @@ __global__ __launch_bounds__(kThreads) void plan_offsets_kernel(const int32_t* _
 __global__ __launch_bounds__(kThreads) void plan_rows_kernel(const int32_t* __restrict__ cu,
                                                              const int32_t* __restrict__ starts, int N, int T,
                                                              int32_t* __restrict__ seq, int32_t* __restrict__ pos) {
-  plan_rows(cu + 1, N, T, starts, seq, pos);
+  plan_rows(cu + 1, N, T, blockIdx.x, starts, seq, pos);
 }
 
 hipError_t launch_plan(const int32_t* lengths, const int32_t* starts, int N, int T, int C, int32_t* cu,
@@ -149,11 +164,9 @@ hipError_t launch_plan(const int32_t* lengths, const int32_t* starts, int N, int
   const int shift = C == 64 ? 6 : C == 32 ? 5 : 4;
   const int row_wgs = seq != nullptr || pos != nullptr ? int((int64_t(T) + kPlanRows - 1) / kPlanRows) : 0;
   if (N <= kPlanSeqs) {
-    const int rank_wgs = order != nullptr ? (N + kPlanRank - 1) / kPlanRank : 0;
-    int nwg = row_wgs > rank_wgs ? row_wgs : rank_wgs;
-    if (nwg < 1) nwg = 1;
-    hipLaunchKernelGGL(plan_kernel, dim3(unsigned(nwg)), dim3(kThreads), 0, s, lengths, starts, N, T, shift, cu,
-                       order, seq, pos);
+    const int rank_wgs = order != nullptr && N > 0 ? (N + kPlanRank - 1) / kPlanRank : 1;
+    hipLaunchKernelGGL(plan_kernel, dim3(unsigned(rank_wgs + row_wgs)), dim3(kThreads), 0, s, lengths, starts, N, T,
+                       shift, rank_wgs, cu, order, seq, pos);
     return hipGetLastError();
   }
   hipLaunchKernelGGL(plan_offsets_kernel, dim3(1), dim3(kThreads), 0, s, lengths, N, T, cu, order);
