@@ -23,6 +23,20 @@ namespace efla {
 // NaN), so g = -inf resets the state.  NaN passes through.
 __device__ __forceinline__ float gate_floor(float g) { return g < -128.0f ? -128.0f : g; }
 
+// G of a chunk's tokens, lane by lane: the inclusive sum of their gates in 64
+// bits.  What is needed of G are differences, and after a reset (-128) or much
+// decay the float sum is too coarse for them: 1.5e-5 apart behind one reset,
+// 1e-3 behind a chunk of them.
+__device__ __forceinline__ double wave_scan_gate(float g, int lane) {
+  double x = double(g);
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const double y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  return x;
+}
+
 // Sum over the 16 lanes of a DPP row, in every lane.
 __device__ __forceinline__ float row_sum16(float s) {
   s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x128, 0xF, 0xF, false));

@@ -57,14 +57,15 @@ __device__ __forceinline__ float wave_scan_f32(float x, int lane) {
 template <typename T, int DK, int C>
 __global__ __launch_bounds__(kThreads) void gated_ut_kernel(GatedBwd b, float* __restrict__ tws,
                                                             float* __restrict__ xws, float* __restrict__ pws,
-                                                            float* __restrict__ aws, float* __restrict__ gws, int NC) {
+                                                            float* __restrict__ aws, double* __restrict__ gws, int NC) {
   constexpr int DKP = round_up(DK, 32), CP = round_up(C, 32), QP = DKP + 4, CPP = CP + 4, NCP = CP / 16;
   __shared__ __align__(16) float Qs[CP * QP];
   __shared__ __align__(16) float Ks[CP * QP];
   __shared__ __align__(16) float Am[CP * CPP];
   __shared__ __align__(16) float Xm[CP * CPP];
   __shared__ __align__(16) float Rm[16 * CPP];
-  __shared__ float as[CP], gs[CP];
+  __shared__ float as[CP];
+  __shared__ double gs[CP];
   const int64_t slot = blockIdx.x;
   const int n = int(slot % NC);
   const int64_t bh = slot / NC;
@@ -85,7 +86,7 @@ __global__ __launch_bounds__(kThreads) void gated_ut_kernel(GatedBwd b, float* _
   }
   if (w == 0) {
     const float gg = lane < valid ? gate_floor(b.g[(t0 + lane) * b.H + h]) : 0.0f;
-    const float G = wave_scan_f32(gg, lane);
+    const double G = wave_scan_gate(gg, lane);
     if (lane < CP) gs[lane] = G;
     if (lane < C) gws[slot * C + lane] = G;
   }
@@ -100,7 +101,7 @@ __global__ __launch_bounds__(kThreads) void gated_ut_kernel(GatedBwd b, float* _
 #pragma unroll
     for (int qq = 0; qq < 4; ++qq) {
       const int r = r0 + 4 * g + qq, c = c0 + li;
-      const float gam = c <= r ? expf(gs[r] - gs[c]) : 0.0f;
+      const float gam = c <= r ? expf(float(gs[r] - gs[c])) : 0.0f;
       if (r == c) as[r] = acc[qq];
       Am[r * CPP + c] = c < r ? gam * acc[qq] : 0.0f;
       if (r < C && c < C) pws[slot * C * C + r * C + c] = c <= r ? gam * pp[qq] : 0.0f;
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(kThreads) void gated_ut_kernel(GatedBwd b, float* _
 template <typename T, int DK, int C>
 __global__ __launch_bounds__(kThreads) void gated_bwd_state_kernel(GatedBwd b, const float* __restrict__ tws,
                                                                    const float* __restrict__ pws,
-                                                                   const float* __restrict__ gws,
+                                                                   const double* __restrict__ gws,
                                                                    float* __restrict__ dstates, int NC, int NVB) {
   constexpr int DKP = round_up(DK, 32), CP = round_up(C, 32);
   constexpr int QP = DKP + 4, CPP = CP + 4, VP = 16 + 4;
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_state_kernel(GatedBwd b, c
   F32Stager<T, C, DK> sq, sk;
   F32Stager<float, C, C> st, spp;
   F32Stager<T, C, 16> sdo;
-  float G = 0.0f, GC = 0.0f;
+  double G = 0.0, GC = 0.0;
   auto load = [&](int n) {
     const int64_t t0 = bos + int64_t(n) * C;
     const int64_t left = b.L - int64_t(n) * C;
@@ -193,7 +194,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_state_kernel(GatedBwd b, c
     sdo.load(static_cast<const T*>(b.d_o) + (t0 * b.H + h) * DV + v0, int64_t(b.H) * DV, valid, tid);
     st.load(tws + (slot0 + n) * C * C, C, C, tid);
     spp.load(pws + (slot0 + n) * C * C, C, C, tid);
-    if (tid < CP) G = tid < C ? gws[(slot0 + n) * C + tid] : 0.0f;
+    if (tid < CP) G = tid < C ? gws[(slot0 + n) * C + tid] : 0.0;
     GC = gws[(slot0 + n) * C + C - 1];
   };
   if (NC > 0) load(NC - 1);
@@ -210,10 +211,10 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_state_kernel(GatedBwd b, c
     st.store(Ts, CPP, tid);
     spp.store(Ps, CPP, tid);
     if (tid < CP) {
-      es[tid] = expf(G);
-      ws[tid] = expf(GC - G);
+      es[tid] = expf(float(G));
+      ws[tid] = expf(float(GC - G));
     }
-    const float end = expf(GC);
+    const float end = expf(float(GC));
     if (n > 0) load(n - 1);  // in flight during this chunk
     __syncthreads();
     for (int rt = w; rt < CP / 16; rt += 4) {
@@ -266,7 +267,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_state_kernel(GatedBwd b, c
 template <typename T, int DK, int C>
 __global__ __launch_bounds__(kThreads) void gated_bwd_chunk_kernel(
     GatedBwd b, const float* __restrict__ tws, const float* __restrict__ xws, const float* __restrict__ pws,
-    const float* __restrict__ aws, const float* __restrict__ gws, const float* __restrict__ states,
+    const float* __restrict__ aws, const double* __restrict__ gws, const float* __restrict__ states,
     const float* __restrict__ dstates, float* __restrict__ dqh, float* __restrict__ dkh, int NC) {
   using S = BwdChunkShape<T, DK, C>;
   constexpr int DKP = S::DKP, CP = S::CP, QP = S::QP, CPP = S::CPP, VP = S::VP, NQ = S::NQ, NP = S::NP;
@@ -277,7 +278,8 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_chunk_kernel(
   __shared__ __align__(16) float M1[CP * CPP];  // P, then dP, then X^T dX
   __shared__ __align__(16) float R[S::RBUF];
   __shared__ float rx[NCQ * CP], rw[NCQ * CP];  // row sums by tile column
-  __shared__ float as[CP], das[CP], dls[CP], gs[CP], es[CP], ws[CP], ys[CP], c0s[kThreads / kWave];
+  __shared__ float as[CP], das[CP], dls[CP], es[CP], ws[CP], ys[CP], c0s[kThreads / kWave];
+  __shared__ double gs[CP];
 
   const int64_t slot = blockIdx.x;
   const int n = int(slot % NC), H = b.H, Hk = b.Hk, DV = b.DV;
@@ -308,13 +310,14 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_chunk_kernel(
     st.store(M0, CPP, tid);
     spp.store(M1, CPP, tid);
   }
-  const float GC = gws[slot * C + C - 1], end = expf(GC);
+  const double GC = gws[slot * C + C - 1];
+  const float end = expf(float(GC));
   if (tid < CP) {
-    const float G = tid < C ? gws[slot * C + tid] : GC;
+    const double G = tid < C ? gws[slot * C + tid] : GC;
     as[tid] = tid < C ? aws[slot * C + tid] : 0.0f;
     gs[tid] = G;
-    es[tid] = expf(G);
-    ws[tid] = expf(GC - G);
+    es[tid] = expf(float(G));
+    ws[tid] = expf(float(GC - G));
   }
   float* Sv = R;               // S[:, block]      DKP x 16
   float* dSv = Sv + DKP * VP;  // dS'[:, block]
@@ -446,7 +449,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_chunk_kernel(
     for (int qq = 0; qq < 4; ++qq) {
       const int r = r0 + 4 * g + qq, c = cc + li;
       R2[r * CPP + c] = c < r ? dPa[i][qq] * M1[r * CPP + c] : 0.0f;
-      M1[r * CPP + c] = c <= r ? expf(gs[r] - gs[c]) * dPa[i][qq] : 0.0f;
+      M1[r * CPP + c] = c <= r ? expf(float(gs[r] - gs[c])) * dPa[i][qq] : 0.0f;
       M0[r * CPP + c] = c <= r ? dTa[i][qq] : 0.0f;
     }
   }
@@ -502,7 +505,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_chunk_kernel(
 #pragma unroll
     for (int qq = 0; qq < 4; ++qq) {
       const int r = r0 + 4 * g + qq, c = cc + li;
-      R2[r * CPP + c] = c < r ? -expf(gs[r] - gs[c]) * acc[qq] : 0.0f;
+      R2[r * CPP + c] = c < r ? -expf(float(gs[r] - gs[c])) * acc[qq] : 0.0f;
       R1[r * CPP + c] = gg[qq];
     }
   }

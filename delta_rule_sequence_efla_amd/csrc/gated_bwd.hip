@@ -1,7 +1,7 @@
 // gated_bwd.hip -- the gated backward pass: which kernels run, and its
 // workspace, every region 256-byte aligned, per chunk slot ((b H + h) NC + n).
 //   fp32 arithmetic (gated_bwd.h; every type and size), all fp32:
-//     T, X, P [C][C]; a, G [C]; S, dS [d_k][d_v]
+//     T, X, P [C][C]; a [C], G [C] in 64 bits; S, dS [d_k][d_v]
 //   bf16 matrix cores (bf16 inputs, d_k 64 or 128, d_v % 32 == 0; chunks of 64
 //   whatever chunk the caller names):
 //     T fragments (12 KiB) and gate block (1 KiB) as the forward's, X fp32,
@@ -51,7 +51,7 @@ static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, 
     w.qe = region(slots * size_t(C) * DK * 2);
   } else {
     w.a = region(slots * C * 4);
-    w.gc = region(slots * C * 4);
+    w.gc = region(slots * C * 8);
   }
   const size_t heads = Hk < H ? size_t(B) * L * H * DK * 4 : 0;
   w.dqh = region(heads);
@@ -117,17 +117,17 @@ static hipError_t gated_bwd_impl(const GatedBwd& b, unsigned char* ws, hipStream
   auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
   if (slots > 0) {
     hipLaunchKernelGGL((gated_ut_kernel<T, DK, C>), dim3(unsigned(slots)), dim3(kThreads), 0, s, b, f(lay.t), f(lay.x),
-                       f(lay.p), f(lay.a), f(lay.gc), NC);
+                       f(lay.p), f(lay.a), reinterpret_cast<double*>(ws + lay.gc), NC);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (hipError_t e = launch_gated_recurrent<T>(forward_of(b), f(lay.s), C, s); e != hipSuccess) return e;
   }
   hipLaunchKernelGGL((gated_bwd_state_kernel<T, DK, C>), dim3(unsigned(bh * (b.DV / 16))), dim3(kThreads), 0, s, b,
-                     f(lay.t), f(lay.p), f(lay.gc), f(lay.ds), NC, b.DV / 16);
+                     f(lay.t), f(lay.p), reinterpret_cast<double*>(ws + lay.gc), f(lay.ds), NC, b.DV / 16);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   if (slots == 0) return hipSuccess;
   const bool shared = b.Hk < b.H;
   hipLaunchKernelGGL((gated_bwd_chunk_kernel<T, DK, C>), dim3(unsigned(slots)), dim3(kThreads), 0, s, b, f(lay.t),
-                     f(lay.x), f(lay.p), f(lay.a), f(lay.gc), f(lay.s), f(lay.ds), shared ? f(lay.dqh) : nullptr,
+                     f(lay.x), f(lay.p), f(lay.a), reinterpret_cast<double*>(ws + lay.gc), f(lay.s), f(lay.ds), shared ? f(lay.dqh) : nullptr,
                      shared ? f(lay.dkh) : nullptr, NC);
   if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   return shared ? sum_heads<T>(b, f(lay.dqh), f(lay.dkh), s) : hipSuccess;

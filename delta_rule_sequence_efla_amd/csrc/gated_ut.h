@@ -43,7 +43,7 @@ struct GatedUtBwd {
   uint16_t *t, *p, *qe;
 };
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr double kLog2e = 1.4426950408889634;
 constexpr int kGatedT = 12 * 64 * 8;  // bf16 values of T per chunk slot
 constexpr int kGatedG = 4 * 64;       // floats of the gate block per chunk slot
 
@@ -72,7 +72,7 @@ __device__ __forceinline__ void split_frag(const f32x4& lo4, const f32x4& hi4, F
 }
 
 template <int DK, bool BWD = false>
-__global__ __launch_bounds__(256) void gated_ut_wave_kernel(const uint16_t* __restrict__ k,
+__global__ __launch_bounds__(256, BWD ? 2 : 4) void gated_ut_wave_kernel(const uint16_t* __restrict__ k,
                                                             const uint16_t* __restrict__ beta,
                                                             const float* __restrict__ gate, uint16_t* __restrict__ tfr,
                                                             float* __restrict__ gws, int H, int Hk, int64_t L, int NC,
@@ -110,6 +110,7 @@ __global__ __launch_bounds__(256) void gated_ut_wave_kernel(const uint16_t* __re
   float* Xs = Gs + 4 * GBLK;                             // [4][XBLK] diagonal X blocks, column-major
   float* as = a_all[w];
   float* gs = g_all[w];
+  float* gl = a_all[w];  // the sums' second floats, until a takes their place
 
   Frag<uint16_t> Kf[NRT][NKU];
 #pragma unroll
@@ -122,23 +123,22 @@ __global__ __launch_bounds__(256) void gated_ut_wave_kernel(const uint16_t* __re
       else Kf[rt][ku].v = bf16x8{};
     }
   }
-  float bt = 0.0f, G = 0.0f;
+  float bt = 0.0f, gt = 0.0f;
   if (lane < valid) {
     bt = to_f32(beta[row0 + int64_t(lane) * H]);
-    G = gate_floor(gate[row0 + int64_t(lane) * H]);
+    gt = gate_floor(gate[row0 + int64_t(lane) * H]);
   }
-#pragma unroll
-  for (int d = 1; d < kWave; d <<= 1) {  // inclusive sum over the chunk's tokens
-    const float y = __shfl_up(G, d);
-    if (lane >= d) G += y;
-  }
-  G *= kLog2e;
+  // G in two floats, so that differences behind a reset are as good as before
+  // it.  The block in gws holds the first: it serves P, which is rounded to bf16.
+  // Against float sums: 0.3 us of a 135 us forward (4096 tokens, 16 heads, d 128).
+  const double Gd64 = wave_scan_gate(gt, lane) * kLog2e;
+  const float G = float(Gd64);
   gs[lane] = G;
-  const float Gend = __shfl(G, 63);
+  gl[lane] = float(Gd64 - double(G));
   float* gdst = gws + id * kGatedG;
   gdst[lane] = G;
   gdst[64 + lane] = exp2_gate(G);
-  gdst[128 + lane] = exp2_gate(Gend - G);
+  gdst[128 + lane] = exp2_gate(float(__shfl(Gd64, 63) - Gd64));
   wave_lds_order();
 
   // Gam * K K^T: Gd[b] holds rows li, columns 4g.. of diagonal block b (K K^T
@@ -152,13 +152,16 @@ __global__ __launch_bounds__(256) void gated_ut_wave_kernel(const uint16_t* __re
     gr[b] = gs[16 * b + li];
     gc[b] = *reinterpret_cast<const f32x4*>(gs + 16 * b + 4 * g);
   }
+  auto gam = [&](int r, int c, int qq) {
+    return exp2_gate((gr[r] - gc[c][qq]) + (gl[16 * r + li] - gl[16 * c + 4 * g + qq]));
+  };
 #pragma unroll
   for (int bb = 0; bb < NRT; ++bb) {
     Gd[bb] = zero4();
 #pragma unroll
     for (int ku = 0; ku < NKU; ++ku) mma(Gd[bb], Kf[bb][ku], Kf[bb][ku]);
 #pragma unroll
-    for (int qq = 0; qq < 4; ++qq) Gd[bb][qq] = 4 * g + qq <= li ? Gd[bb][qq] * exp2_gate(gr[bb] - gc[bb][qq]) : 0.0f;
+    for (int qq = 0; qq < 4; ++qq) Gd[bb][qq] = 4 * g + qq <= li ? Gd[bb][qq] * gam(bb, bb, qq) : 0.0f;
   }
 #pragma unroll
   for (int i = 1; i < NRT; ++i)
@@ -168,7 +171,7 @@ __global__ __launch_bounds__(256) void gated_ut_wave_kernel(const uint16_t* __re
 #pragma unroll
       for (int ku = 0; ku < NKU; ++ku) mma(Gu[i][m], Kf[m][ku], Kf[i][ku]);
 #pragma unroll
-      for (int qq = 0; qq < 4; ++qq) Gu[i][m][qq] *= exp2_gate(gr[i] - gc[m][qq]);
+      for (int qq = 0; qq < 4; ++qq) Gu[i][m][qq] *= gam(i, m, qq);
     }
 #pragma unroll
   for (int bb = 0; bb < NRT; ++bb) *reinterpret_cast<f32x4*>(Gs + bb * GBLK + li * 16 + 4 * g) = Gd[bb];
