@@ -46,6 +46,27 @@ __device__ __forceinline__ float row_sum16(float s) {
   return s;
 }
 
+// slot_chunk (common.h) by all 64 lanes, uniform arguments but for the lane:
+// each step of the search tests 64 sequences, one load's latency instead of six.
+template <int C>
+__device__ __forceinline__ bool gated_slot_chunk(const int32_t* __restrict__ cu, int N, int64_t j, int64_t h, int H,
+                                                 int64_t L, int NC, int lane, SeqSpan& sp, int& n) {
+  int lo = 0, left = N;
+  while (left > 1) {
+    const int step = (left + kWave - 1) / kWave, u = lane * step;
+    const bool before = u < left && clamp_offset(cu[lo + u], 0, L) / C + lo + u <= j;
+    const int cnt = __popcll(__ballot(before));
+    const int at = cnt > 1 ? (cnt - 1) * step : 0;
+    lo += at;
+    left = left - at < step ? left - at : step;
+  }
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  sp = seq_span<C>(cu, lo, h, H, L, NC);
+  const int64_t nn = h * NC + j - sp.slot0;
+  n = int(nn);
+  return nn >= 0 && nn < sp.nc;
+}
+
 // State a sequence starts from and ends in: row `seq` of the state tensor, or
 // row slots[seq] of a pool of P states; -1 (no row) for an entry outside it.
 __device__ __forceinline__ int64_t state_row(const int32_t* __restrict__ slots, int seq, int P) {

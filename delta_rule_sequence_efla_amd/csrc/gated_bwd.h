@@ -67,10 +67,10 @@ __global__ __launch_bounds__(kThreads) void gated_ut_kernel(GatedBwd b, float* _
   __shared__ float as[CP];
   __shared__ double gs[CP];
   const int64_t slot = blockIdx.x;
-  const int n = int(slot % NC);
-  const int64_t bh = slot / NC;
-  const int h = int(bh % b.H), hk = h / (b.H / b.Hk);
-  const int64_t t0 = (bh / b.H) * b.L + int64_t(n) * C;
+  const uint32_t bh = blockIdx.x / uint32_t(NC);
+  const int n = int(blockIdx.x - bh * uint32_t(NC));
+  const int h = int(bh % uint32_t(b.H)), hk = h / (b.H / b.Hk);
+  const int64_t t0 = bh / uint32_t(b.H) * b.L + int64_t(n) * C;
   const int valid = int(b.L - int64_t(n) * C < C ? b.L - int64_t(n) * C : C);
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), li = lane & 15, g = lane >> 4;
   {
@@ -282,12 +282,12 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_chunk_kernel(
   __shared__ double gs[CP];
 
   const int64_t slot = blockIdx.x;
-  const int n = int(slot % NC), H = b.H, Hk = b.Hk, DV = b.DV;
-  const int64_t bh = slot / NC;
-  const int h = int(bh % H), hk = h / (H / Hk);
+  const uint32_t bh = blockIdx.x / uint32_t(NC);
+  const int n = int(blockIdx.x - bh * uint32_t(NC)), H = b.H, Hk = b.Hk, DV = b.DV;
+  const int h = int(bh % uint32_t(H)), hk = h / (H / Hk);
   const int64_t left = b.L - int64_t(n) * C;
   const int valid = int(left < C ? left : C);
-  const int64_t t0 = (bh / H) * b.L + int64_t(n) * C, row0 = t0 * H + h, krow0 = t0 * Hk + hk;
+  const int64_t t0 = bh / uint32_t(H) * b.L + int64_t(n) * C, row0 = t0 * H + h, krow0 = t0 * Hk + hk;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), li = lane & 15, g = lane >> 4;
   const int64_t k_stride = int64_t(Hk) * DK, v_stride = int64_t(H) * DV;
   const T* v = static_cast<const T*>(b.v);
@@ -580,10 +580,10 @@ __global__ __launch_bounds__(kThreads) void gated_head_sum_kernel(const float* _
                                                                   const float* __restrict__ dkh, T* __restrict__ dq,
                                                                   T* __restrict__ dk, int64_t rows, int R, int DK) {
   const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;  // (token, key head), four values
-  const int n4 = DK / 4;
-  if (i >= rows * n4) return;
-  const int64_t row = i / n4;
-  const int c = int(i % n4) * 4;
+  const int shift = __builtin_ctz(unsigned(DK)) - 2;  // d_k / 4 threads a row, a power of two
+  const int64_t row = i >> shift;
+  if (row >= rows) return;
+  const int c = int(i & ((1 << shift) - 1)) * 4;
   f32x4 x = zero4(), y = zero4();
   for (int r = 0; r < R; ++r) {
     x += *reinterpret_cast<const f32x4*>(dqh + (row * R + r) * DK + c);

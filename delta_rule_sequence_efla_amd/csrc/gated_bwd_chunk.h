@@ -71,11 +71,12 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
 
   const int H = b.H, Hk = b.Hk, DV = b.DV;
   const int64_t slot = blockIdx.x;
-  const int n = int(slot % NC);
-  const int64_t bh = slot / NC, h = bh % H, hk = h / (H / Hk);
+  const uint32_t bh = blockIdx.x / uint32_t(NC), batch = bh / uint32_t(H);
+  const int n = int(blockIdx.x - bh * uint32_t(NC)), h32 = int(bh - batch * uint32_t(H));
+  const int64_t h = h32, hk = h32 / (H / Hk);
   const int64_t left = b.L - int64_t(n) * C;
   const int valid = int(left < C ? left : C);
-  const int64_t tok0 = (bh / H) * b.L + int64_t(n) * C;
+  const int64_t tok0 = batch * b.L + int64_t(n) * C;
   const int64_t row0 = tok0 * H + h, krow0 = tok0 * Hk + hk;
   const int tid = threadIdx.x, lane0 = tid & 63, w = wave_id(), li0 = lane0 & 15, g0 = lane0 >> 4;
   const int64_t k_stride = int64_t(Hk) * DK, v_stride = int64_t(H) * DV;

@@ -35,9 +35,10 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(
   __shared__ __align__(16) float red_q[NRG * DVW];
   __shared__ float coef[3];
 
-  const int64_t unit = blockIdx.x / NVB;
-  const int v0 = int(blockIdx.x % NVB) * DVW;
-  const int n = int(unit / H), h = int(unit % H);
+  const uint32_t wg = blockIdx.x, unit32 = wg / uint32_t(NVB);  // 32-bit divisions: the 64-bit ones cost a microsecond
+  const int64_t unit = unit32;
+  const int v0 = int(wg % uint32_t(NVB)) * DVW;
+  const int n = int(unit32 / uint32_t(H)), h = int(unit32 % uint32_t(H));
   const int64_t row = state_row(slots, n, P);
   if (row < 0) return;
   const int64_t uk = int64_t(n) * Hk + h / (H / Hk);
@@ -183,10 +184,10 @@ __global__ __launch_bounds__(2 * kThreads) void gated_recurrent_kernel(GatedFwd 
   __shared__ float oS[2][TB * 17 + kThreads];  // behind the tile: where lanes without an output write
 
   const int NVB = a.DV / 16, H = a.H, DV = a.DV;
-  const int64_t unit = blockIdx.x / NVB;
-  const int v0 = int(blockIdx.x % NVB) * 16;
-  const int h = int(unit % H);
-  int seq = int(unit / H);
+  const uint32_t wg = blockIdx.x, unit = wg / uint32_t(NVB);
+  const int v0 = int(wg % uint32_t(NVB)) * 16;
+  const int h = int(unit % uint32_t(H));
+  int seq = int(unit / uint32_t(H));
   int64_t bos = int64_t(seq) * a.L, len = a.L;
   if (a.cu != nullptr) {
     if (a.order != nullptr) seq = seq_of_rank(a.order, seq, a.N);
@@ -343,8 +344,9 @@ __global__ __launch_bounds__(2 * kThreads) void gated_recurrent_kernel(GatedFwd 
   __syncthreads();
   for (int64_t t0 = 0; t0 < len; t0 += TB) {
     const int b = int(t0 / TB) & 1;
-    if (states != nullptr && t0 % C == 0) {
-      float* dst = states + (slot0 + t0 / C) * DK * DV + v0 + col;
+    const uint32_t blk = uint32_t(t0 / TB), per = uint32_t(C) / TB;
+    if (states != nullptr && blk % per == 0) {
+      float* dst = states + (slot0 + blk / per) * DK * DV + v0 + col;
 #pragma unroll
       for (int e = 0; e < NK; ++e) dst[int64_t(li * NK + e) * DV] = S[e];
     }

@@ -95,11 +95,13 @@ __global__ __launch_bounds__(256, BWD ? 2 : 4) void gated_ut_wave_kernel(const u
   if (id >= nchunks) return;  // no workgroup barriers below
   SeqSpan sp;
   int chunk;
-  const int64_t h = cu == nullptr ? (id / NC) % H : id / NC;
+  const uint32_t unit = uint32_t(id) / uint32_t(NC), at = uint32_t(id) - unit * uint32_t(NC);
+  const uint32_t batch = cu == nullptr ? unit / uint32_t(H) : 0u;
+  const int64_t h = unit - batch * uint32_t(H);
   if (cu == nullptr) {
-    chunk = int(id % NC);
-    sp = seq_span<C>(nullptr, int(id / NC / H), h, H, L, NC);
-  } else if (!slot_chunk<C>(cu, N, id % NC, h, H, L, NC, sp, chunk)) {
+    chunk = int(at);
+    sp = seq_span<C>(nullptr, int(batch), h, H, L, NC);
+  } else if (!gated_slot_chunk<C>(cu, N, at, h, H, L, NC, lane, sp, chunk)) {
     return;  // a slot no chunk of the packed batch uses
   }
   const int64_t t0 = int64_t(chunk) * C;

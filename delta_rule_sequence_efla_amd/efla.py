@@ -13,6 +13,7 @@ S_t = (I - alpha_t k_t k_t^T) S_{t-1} + alpha_t k_t v_t^T, o_t = S_t^T q_t.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import NamedTuple
 
@@ -562,12 +563,17 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# Without the check that torch is initialised: its tensors are.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_f32 = torch.float32
+
+
 def _call(fn, index: int, where: str, *args) -> None:
     """fn(*args, stream) on torch's current stream of device ``index``, with
     that device current.  A call of a decode step costs more on the host than
     on the GPU, so the device is switched only where it is another one."""
     stream = _raw_stream(index)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, stream)
     else:
         with torch.cuda.device(index):
@@ -577,15 +583,17 @@ def _call(fn, index: int, where: str, *args) -> None:
 
 
 def _gated_shapes(q, k, v, beta, g, lead: int):
-    """(device index, H, Hk, dk, dv) of a gated call's inputs, checked."""
+    """(device index, H, Hk, dk, dv) of a gated call's inputs, checked.  (A decode
+    call is bound by the host: its checks take the cheapest form of each test.)"""
     dt, ks, vs = q.dtype, k.shape, v.shape
-    if len(ks) != lead + 2 or len(vs) != lead + 2 or q.shape != ks or vs[:lead] != ks[:lead] \
-            or beta.shape != vs[:-1] or g.shape != vs[:-1] or k.dtype != dt or v.dtype != dt or beta.dtype != dt \
-            or g.dtype != torch.float32:
+    rows = vs[:-1]
+    if len(ks) != lead + 2 or len(vs) != lead + 2 or ks[:lead] != vs[:lead] or q.shape != ks or beta.shape != rows \
+            or g.shape != rows or k.dtype is not dt or v.dtype is not dt or beta.dtype is not dt \
+            or g.dtype is not _f32:
         dims = {1: "N", 2: "B,L"}[lead]
         raise ValueError(f"expected q, k [{dims},Hk,dk], v [{dims},H,dv], beta [{dims},H] of one type, "
                          f"g float32 [{dims},H]")
-    H, Hk = vs[-2], ks[-2]
+    H, Hk = rows[lead], ks[lead]
     if Hk < 1 or H % Hk:
         raise ValueError(f"the {H} value heads must be a multiple of the {Hk} query and key heads")
     index = q.get_device()
@@ -596,14 +604,24 @@ def _gated_shapes(q, k, v, beta, g, lead: int):
 def _same(index: int, *ts) -> None:
     """Every tensor given must be contiguous and live on GPU ``index``."""
     for t in ts:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError("EFLA tensors must live on the GPU")
-        if not t.is_contiguous():
-            raise ValueError("EFLA tensors must be contiguous")
-        if t.get_device() != index:
+        if t is not None and (index < 0 or t.get_device() != index or not t.is_contiguous()):
+            if not t.is_cuda:
+                raise ValueError("EFLA tensors must live on the GPU")
+            if not t.is_contiguous():
+                raise ValueError("EFLA tensors must be contiguous")
             raise ValueError("EFLA tensors must share one device")
+
+
+def _shaped(t, shape, name: str, dtype) -> None:
+    """_want for tensors that are given in most calls."""
+    if t is not None and (t.shape != shape or t.dtype is not dtype):
+        _want(t, shape, name, dtype)
+
+
+@functools.lru_cache(maxsize=1024)
+def _gated_workspace(name: str, *sizes) -> int:
+    """Bytes of workspace of entry point ``name``, a function of the sizes alone."""
+    return getattr(lib(), name + "_workspace_size")(*sizes)
 
 
 def _nbytes(t) -> int:
@@ -622,17 +640,17 @@ def efla_gated_chunk_fwd(q, k, v, beta, g, s0=None, chunk: int = 64, o=None, s_f
     index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
     B, L = k.shape[:2]
     _same(index, s0, o, s_final, workspace)
-    _want(s0, (B, H, dk, dv), "s0", torch.float32)
-    _want(o, v.shape, "o", q.dtype)
-    _want(s_final, (B, H, dk, dv), "s_final", torch.float32)
+    _shaped(s0, (B, H, dk, dv), "s0", _f32)
+    _shaped(o, v.shape, "o", q.dtype)
+    _shaped(s_final, (B, H, dk, dv), "s_final", _f32)
     if o is None:
         o = torch.empty_like(v)
     if s_final is None and want_final:
-        s_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device)
+        s_final = g.new_empty((B, H, dk, dv))
     code, r = _code(q.dtype), _rule(rule)
     if workspace is None:
-        n = lib().efla_gated_chunk_fwd_workspace_size(B, H, Hk, L, dk, dv, chunk, code)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        n = _gated_workspace("efla_gated_chunk_fwd", B, H, Hk, L, dk, dv, chunk, code)
+        workspace = q.new_empty(n, dtype=torch.uint8) if n else None
     _call(lib().efla_gated_chunk_fwd, index, "efla_gated_chunk_fwd", _at(q), _at(k), _at(v), _at(beta), _at(g), _at(s0),
           _at(o), _at(s_final), B, H, Hk, L, dk, dv, chunk, code, r, _at(workspace), _nbytes(workspace))
     return o, s_final
@@ -656,26 +674,26 @@ def efla_gated_chunk_fwd_varlen(q, k, v, beta, g, cu_seqlens, s0=None, chunk: in
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be a 1-D int32 tensor of N+1 offsets")
     N = cu_seqlens.numel() - 1
-    _want(slots, (N,), "slots", torch.int32)
-    _want(order, (N,), "order", torch.int32)
-    _want(o, v.shape, "o", q.dtype)
+    _shaped(slots, (N,), "slots", torch.int32)
+    _shaped(order, (N,), "order", torch.int32)
+    _shaped(o, v.shape, "o", q.dtype)
     P = N
     if slots is not None:
         if s0 is None and s_final is None:
             raise ValueError("slots need a pool: s0, s_final or both")
         P = (s0 if s0 is not None else s_final).shape[0]
-    _want(s0, (P, H, dk, dv), "s0", torch.float32)
-    _want(s_final, (P, H, dk, dv), "s_final", torch.float32)
+    _shaped(s0, (P, H, dk, dv), "s0", _f32)
+    _shaped(s_final, (P, H, dk, dv), "s_final", _f32)
     if o is None:
         o = torch.empty_like(v)
     if s_final is None and want_final:
         if slots is not None:
             raise ValueError("with slots the final states need a pool: pass s_final (it may be s0), or want_final=False")
-        s_final = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+        s_final = g.new_empty((N, H, dk, dv))
     code, r = _code(q.dtype), _rule(rule)
     if workspace is None:
-        n = lib().efla_gated_chunk_fwd_varlen_workspace_size(N, H, Hk, T, dk, dv, chunk, code)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        n = _gated_workspace("efla_gated_chunk_fwd_varlen", N, H, Hk, T, dk, dv, chunk, code)
+        workspace = q.new_empty(n, dtype=torch.uint8) if n else None
     _call(lib().efla_gated_chunk_fwd_varlen, index, "efla_gated_chunk_fwd_varlen", _at(q), _at(k), _at(v), _at(beta),
           _at(g), _at(cu_seqlens), _at(slots), _at(order), N, P, _at(s0), _at(o), _at(s_final), H, Hk, T, dk, dv, chunk,
           code, r, _at(workspace), _nbytes(workspace))
@@ -695,15 +713,15 @@ def efla_gated_chunk_bwd(q, k, v, beta, g, d_o, s0=None, ds_final=None, chunk: i
     index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
     B, L = k.shape[:2]
     _same(index, d_o, s0, ds_final, workspace)
-    _want(d_o, v.shape, "d_o", q.dtype)
-    _want(s0, (B, H, dk, dv), "s0", torch.float32)
-    _want(ds_final, (B, H, dk, dv), "ds_final", torch.float32)
+    _shaped(d_o, v.shape, "d_o", q.dtype)
+    _shaped(s0, (B, H, dk, dv), "s0", _f32)
+    _shaped(ds_final, (B, H, dk, dv), "ds_final", _f32)
     gq, gk, gv, gb, gg = (torch.empty_like(x) for x in (q, k, v, beta, beta))
-    gs0 = torch.empty((B, H, dk, dv), dtype=torch.float32, device=q.device) if want_ds0 else None
+    gs0 = g.new_empty((B, H, dk, dv)) if want_ds0 else None
     code, r = _code(q.dtype), _rule(rule)
     if workspace is None:
-        n = lib().efla_gated_chunk_bwd_workspace_size(B, H, Hk, L, dk, dv, chunk, code)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        n = _gated_workspace("efla_gated_chunk_bwd", B, H, Hk, L, dk, dv, chunk, code)
+        workspace = q.new_empty(n, dtype=torch.uint8) if n else None
     _call(lib().efla_gated_chunk_bwd, index, "efla_gated_chunk_bwd", _at(q), _at(k), _at(v), _at(beta), _at(g), _at(s0),
           _at(d_o), _at(ds_final), _at(gq), _at(gk), _at(gv), _at(gb), _at(gg), _at(gs0), B, H, Hk, L, dk, dv, chunk,
           code, r, _at(workspace), _nbytes(workspace))
@@ -718,15 +736,15 @@ def efla_gated_step(q, k, v, beta, g, state, slots=None, o=None, rule: str = "ex
     index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1)
     N = k.shape[0]
     _same(index, state, slots, o)
-    if state.dim() != 4 or state.shape[1:] != (H, dk, dv) or state.dtype != torch.float32 \
-            or (slots is None and state.shape[0] != N):
+    P = N if slots is None or state.dim() != 4 else state.shape[0]
+    if state.shape != (P, H, dk, dv) or state.dtype is not _f32:
         raise ValueError("state must be float32 [P,H,dk,dv], with P = N where no slots are given")
-    _want(slots, (N,), "slots", torch.int32)
-    _want(o, v.shape, "o", q.dtype)
+    _shaped(slots, (N,), "slots", torch.int32)
+    _shaped(o, v.shape, "o", q.dtype)
     if o is None:
         o = torch.empty_like(v)
     _call(lib().efla_gated_step, index, "efla_gated_step", _at(q), _at(k), _at(v), _at(beta), _at(g), _at(state),
-          _at(slots), _at(o), N, state.shape[0], H, Hk, dk, dv, _code(q.dtype), _rule(rule))
+          _at(slots), _at(o), N, P, H, Hk, dk, dv, _code(q.dtype), _rule(rule))
     return o
 
 
@@ -747,10 +765,10 @@ def efla_pack_plan(lengths, tokens: int, starts=None, chunk: int = 64) -> PackPl
     if lengths.dim() != 1 or lengths.dtype != torch.int32:
         raise ValueError("lengths must be a 1-D int32 tensor")
     N, T = lengths.numel(), int(tokens)
-    _want(starts, (N,), "starts", torch.int32)
+    _shaped(starts, (N,), "starts", torch.int32)
     if not 0 <= T < 2 ** 31:
         raise ValueError("tokens must be in [0, 2^31)")
-    cu, order, seq, pos = torch.empty(2 * N + 1 + 2 * T, dtype=torch.int32, device=lengths.device).split([N + 1, N, T, T])
+    cu, order, seq, pos = lengths.new_empty(2 * N + 1 + 2 * T).split_with_sizes((N + 1, N, T, T))
     at = cu.data_ptr()
     _call(lib().efla_pack_plan, index, "efla_pack_plan", _at(lengths), _at(starts), N, T, chunk, at, at + 4 * (N + 1),
           at + 4 * (2 * N + 1), at + 4 * (2 * N + 1 + T))

@@ -110,6 +110,9 @@ class _NoLaunch:
 def host(monkeypatch):
     monkeypatch.setattr(efla, "_same", lambda *a: None)
     monkeypatch.setattr(efla, "lib", lambda: _NoLaunch())
+    efla._gated_workspace.cache_clear()
+    yield
+    efla._gated_workspace.cache_clear()
 
 
 def inputs(lead, H=4, Hk=2, dk=16, dv=32, dt=BF):
