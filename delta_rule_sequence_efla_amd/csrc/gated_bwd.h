@@ -34,7 +34,7 @@
 namespace efla {
 
 struct GatedBwdLayout {
-  size_t t, x, p, a, gc, s, ds, dqh, dkh, tfr, qe, total;
+  size_t t, x, p, a, gc, s, ds, dqh, dkh, xfr, qe, total;
 };
 
 // Inclusive sum over the 64 lanes of a wavefront.

@@ -4,8 +4,8 @@
 //     T, X, P [C][C]; a [C], G [C] in 64 bits; S, dS [d_k][d_v]
 //   bf16 matrix cores (bf16 inputs, d_k 64 or 128, d_v % 32 == 0; chunks of 64
 //   whatever chunk the caller names):
-//     T fragments (12 KiB) and gate block (1 KiB) as the forward's, X fp32,
-//     T and P bf16 [C][C], Qe bf16 [C][d_k], S and dS bf16 [d_v][d_k]
+//     X fragments (12 KiB) and gate block (1 KiB) as the forward's, P fragments
+//     (6 KiB), Qe bf16 [C][d_k], S and dS bf16 [d_v][d_k]
 // and for both, where key heads are shared, dq and dk per value head in fp32,
 // [B L][H][d_k].
 #include "gated_bwd.h"
@@ -40,16 +40,17 @@ static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, 
   };
   GatedBwdLayout w{};
   const size_t e = fast ? 2 : 4;
-  w.x = region(slots * C * C * 4);
-  w.t = region(slots * C * C * e);
-  w.p = region(slots * C * C * e);
   w.s = region(slots * size_t(DK) * DV * e);
   w.ds = region(slots * size_t(DK) * DV * e);
   if (fast) {
-    w.tfr = region(slots * 12 * 1024);
+    w.xfr = region(slots * 12 * 1024);
+    w.p = region(slots * 6 * 1024);
     w.gc = region(slots * 1024);
     w.qe = region(slots * size_t(C) * DK * 2);
   } else {
+    w.x = region(slots * C * C * 4);
+    w.t = region(slots * C * C * 4);
+    w.p = region(slots * C * C * 4);
     w.a = region(slots * C * 4);
     w.gc = region(slots * C * 8);
   }
@@ -99,11 +100,11 @@ static hipError_t gated_bwd_bf16(const GatedBwd& b, unsigned char* ws, hipStream
   auto u = [&](size_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
   const GatedFwd a = forward_of(b);
   const bool shared = b.Hk < b.H;
-  hipError_t e = launch_gated_ut_bwd(a, u(lay.tfr), f(lay.gc), f(lay.x), u(lay.t), u(lay.p), u(lay.qe), s);
-  if (e == hipSuccess) e = launch_gated_states(a, u(lay.tfr), f(lay.gc), u(lay.s), s);
-  if (e == hipSuccess) e = launch_gated_reverse(b, u(lay.t), u(lay.qe), f(lay.gc), u(lay.ds), s);
+  hipError_t e = launch_gated_ut_bwd(a, u(lay.xfr), f(lay.gc), u(lay.p), u(lay.qe), s);
+  if (e == hipSuccess) e = launch_gated_states(a, u(lay.xfr), f(lay.gc), u(lay.s), s);
+  if (e == hipSuccess) e = launch_gated_reverse(b, u(lay.xfr), u(lay.qe), f(lay.gc), u(lay.ds), s);
   if (e == hipSuccess)
-    e = launch_gated_bwd_chunk(b, u(lay.t), u(lay.p), f(lay.x), f(lay.gc), u(lay.s), u(lay.ds),
+    e = launch_gated_bwd_chunk(b, u(lay.xfr), u(lay.p), f(lay.gc), u(lay.s), u(lay.ds),
                                shared ? f(lay.dqh) : nullptr, shared ? f(lay.dkh) : nullptr, s);
   if (e == hipSuccess && shared) e = sum_heads<uint16_t>(b, f(lay.dqh), f(lay.dkh), s);
   return e;

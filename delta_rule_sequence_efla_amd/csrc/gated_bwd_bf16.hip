@@ -8,37 +8,37 @@
 namespace efla {
 
 template <int DK>
-static hipError_t reverse_impl(const GatedBwd& b, const uint16_t* t, const uint16_t* qe, const float* gws,
+static hipError_t reverse_impl(const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe, const float* gws,
                                uint16_t* dstatesT, hipStream_t s) {
   const int NC = int((b.L + 63) / 64), NVB = b.DV / 32;
   const int64_t bh = int64_t(b.B) * b.H;
   hipLaunchKernelGGL((gated_reverse_kernel<DK>), dim3(unsigned(bh * NVB)), dim3(GatedReverseShape<DK>::THREADS), 0, s, b,
-                     qe, t, gws, dstatesT, NC, NVB, bh % 8 == 0 ? 1 : 0);
+                     qe, xfr, gws, dstatesT, NC, NVB, bh % 8 == 0 ? 1 : 0);
   return hipGetLastError();
 }
 
-hipError_t launch_gated_reverse(const GatedBwd& b, const uint16_t* t, const uint16_t* qe, const float* gws,
+hipError_t launch_gated_reverse(const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe, const float* gws,
                                 uint16_t* dstatesT, hipStream_t s) {
-  return b.DK == 64 ? reverse_impl<64>(b, t, qe, gws, dstatesT, s) : reverse_impl<128>(b, t, qe, gws, dstatesT, s);
+  return b.DK == 64 ? reverse_impl<64>(b, xfr, qe, gws, dstatesT, s) : reverse_impl<128>(b, xfr, qe, gws, dstatesT, s);
 }
 
 template <int DK, bool SHARED>
-static hipError_t chunk_impl(const GatedBwd& b, const uint16_t* t, const uint16_t* p, const float* x, const float* gws,
+static hipError_t chunk_impl(const GatedBwd& b, const uint16_t* xfr, const uint16_t* p, const float* gws,
                              const uint16_t* statesT, const uint16_t* dstatesT, float* dqh, float* dkh, hipStream_t s) {
   const int NC = int((b.L + 63) / 64);
   hipLaunchKernelGGL((gated_bwd_tr_kernel<DK, SHARED>), dim3(unsigned(int64_t(b.B) * b.H * NC)),
-                     dim3(GatedTrShape<DK>::NTH), 0, s, b, t, p, x, gws, statesT, dstatesT, dqh, dkh, NC);
+                     dim3(GatedTrShape<DK>::NTH), 0, s, b, xfr, p, gws, statesT, dstatesT, dqh, dkh, NC);
   return hipGetLastError();
 }
 
-hipError_t launch_gated_bwd_chunk(const GatedBwd& b, const uint16_t* t, const uint16_t* p, const float* x,
-                                  const float* gws, const uint16_t* statesT, const uint16_t* dstatesT, float* dqh,
+hipError_t launch_gated_bwd_chunk(const GatedBwd& b, const uint16_t* xfr, const uint16_t* p, const float* gws,
+                                  const uint16_t* statesT, const uint16_t* dstatesT, float* dqh,
                                   float* dkh, hipStream_t s) {
   if (b.DK == 64)
-    return dqh != nullptr ? chunk_impl<64, true>(b, t, p, x, gws, statesT, dstatesT, dqh, dkh, s)
-                          : chunk_impl<64, false>(b, t, p, x, gws, statesT, dstatesT, dqh, dkh, s);
-  return dqh != nullptr ? chunk_impl<128, true>(b, t, p, x, gws, statesT, dstatesT, dqh, dkh, s)
-                        : chunk_impl<128, false>(b, t, p, x, gws, statesT, dstatesT, dqh, dkh, s);
+    return dqh != nullptr ? chunk_impl<64, true>(b, xfr, p, gws, statesT, dstatesT, dqh, dkh, s)
+                          : chunk_impl<64, false>(b, xfr, p, gws, statesT, dstatesT, dqh, dkh, s);
+  return dqh != nullptr ? chunk_impl<128, true>(b, xfr, p, gws, statesT, dstatesT, dqh, dkh, s)
+                        : chunk_impl<128, false>(b, xfr, p, gws, statesT, dstatesT, dqh, dkh, s);
 }
 
 }  // namespace efla

@@ -24,7 +24,7 @@
 // two lane exchanges.
 // Shared key heads (SHARED): dq and dk of every value head leave in fp32, and
 // gated_head_sum_kernel adds them up.
-// 79 KiB of LDS; bound as bwd_chunk_tr_kernel by the latency of its loads.
+// 80 KiB of LDS; bound as bwd_chunk_tr_kernel by the latency of its loads.
 #pragma once
 
 #include <type_traits>
@@ -41,6 +41,8 @@ struct GatedTrShape : BwdTrShape<DK, 64> {
   static constexpr int C = 64;
   static constexpr int EDT = B::LOOP_END;               // diag(e) dD (negated) [C][BV]
   static constexpr int LOOP_END = EDT + C * B::BV * 2;
+  // tail: Q, later W, over X and P; dX, later Gam dA, behind Q and dP
+  static constexpr int WH = B::TT, WL = WH + C * C * 2, DXH = B::A0, DXL = DXH + C * C * 2, DAF = B::A0;
   // row and column sums of M: behind dA in the region that held Q and dX, or
   // (d_k 64) behind the tail's arrays
   static constexpr int MSUM_BYTES = 2 * B::NRT * C * 4;
@@ -52,20 +54,20 @@ struct GatedTrShape : BwdTrShape<DK, 64> {
 
 template <int DK, bool SHARED>
 __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_waves_per_eu(4, 4))) void gated_bwd_tr_kernel(
-    GatedBwd b, const uint16_t* __restrict__ tws, const uint16_t* __restrict__ pws, const float* __restrict__ xws,
-    const float* __restrict__ gws, const uint16_t* __restrict__ states, const uint16_t* __restrict__ dstates,
+    GatedBwd b, const uint16_t* __restrict__ xfr, const uint16_t* __restrict__ pfr, const float* __restrict__ gws, const uint16_t* __restrict__ states, const uint16_t* __restrict__ dstates,
     float* __restrict__ dqh, float* __restrict__ dkh, int NC) {
   using S = GatedTrShape<DK>;
   constexpr int C = 64, BV = S::BV, NRT = S::NRT, NDT = S::NDT, NKU_D = S::NKU_D, NKU_C = S::NKU_C, NWV = S::NWV;
   constexpr int NTH = S::NTH, NQ = S::NQ, NP = S::NP, CPF = S::CPF;
   __shared__ __align__(1024) unsigned char lds[S::BYTES];
-  __shared__ __align__(16) float as[C], das[C], dls[C], lam[C];
+  __shared__ __align__(16) float as[C], dls[C], lam[C];
   __shared__ __align__(16) float gs[C], es[C], ws[C], ys[C];
-  __shared__ __align__(16) float xw[4][C];  // row sums: dD.(e K S) and U.(w K dS'), by tile column of the block
+  // row sums: dD.(e K S), U.(w K dS') and (X^T dU).D, by tile column of the block
+  __shared__ __align__(16) float xw[6][C];
   __shared__ float c0s[NWV];
   auto b16 = [&](int off) { return reinterpret_cast<uint16_t*>(lds + off); };
   auto f32p = [&](int off) { return reinterpret_cast<float*>(lds + off); };
-  uint16_t *Kt = b16(S::KT), *Tt = b16(S::TT), *Pt = b16(S::PT), *St = b16(S::ST), *dSt = b16(S::DST);
+  uint16_t *Kt = b16(S::KT), *Xt = b16(S::TT), *Pt = b16(S::PT), *St = b16(S::ST), *dSt = b16(S::DST);
   uint16_t *Vt = b16(S::VT), *dOt = b16(S::DOT), *Dt = b16(S::DT), *dUt = b16(S::DUT), *Ut = b16(S::UT);
   uint16_t *dDt = b16(S::DDT), *eDt = b16(S::EDT), *Wt = Vt;
 
@@ -88,35 +90,31 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
   auto st16 = [](uint16_t* p, const u32x4& x) { *reinterpret_cast<u32x4*>(p) = x; };
   constexpr u32x4 Z{0u, 0u, 0u, 0u};
 
-  // the chunk's K, T, P: direct transfers (rows of K past the end re-read row 0
+  // the chunk's K, X (high parts) and P: direct transfers (rows of K past the end re-read row 0
   // and are cleared with the first block's)
   constexpr int UK = C * DK / 8;
   static_assert(UK % NTH == 0, "whole units per thread");
   typename S::TK dma_k;
-  typename S::TC dma_c;
   dma_k.init(k_stride, lane0, w);
-  dma_c.init(C, lane0, w);
   {
     const auto* ks = static_cast<const uint16_t*>(uniform_ptr(k + krow0 * DK));
-    const auto* ts = static_cast<const uint16_t*>(uniform_ptr(tws + slot * C * C));
-    const auto* ps = static_cast<const uint16_t*>(uniform_ptr(pws + slot * C * C));
 #pragma unroll
     for (int i = 0; i < S::TK::PER_WAVE; ++i) {
       if (valid == C) dma_k.template issue<false>(i, lds_addr_of(Kt), ks, C);
       else dma_k.template issue<true>(i, lds_addr_of(Kt), ks, valid);
     }
-#pragma unroll
-    for (int i = 0; i < S::TC::PER_WAVE; ++i) {
-      dma_c.template issue<false>(i, lds_addr_of(Tt), ts, C);
-      dma_c.template issue<false>(i, lds_addr_of(Pt), ps, C);
+    if (w < 6) {  // 6 KiB each, in fragment order
+      const uint32_t at = 1024u * uint32_t(w);
+      dma16(uniform_ptr(xfr + slot * kGatedX), at + 16u * uint32_t(lane0), lds_addr_of(Xt) + at);
+      dma16(uniform_ptr(pfr + slot * kGatedP), at + 16u * uint32_t(lane0), lds_addr_of(Pt) + at);
     }
   }
   if (tid < 4 * C) {
     const float x = gws[slot * kGatedG + tid];
     float* const to = tid < C ? gs : tid < 2 * C ? es : tid < 3 * C ? ws : as;
     to[tid & (C - 1)] = x;
-    xw[tid >> 6][tid & 63] = 0.0f;
   }
+  if (tid < 6 * C) xw[tid >> 6][tid & 63] = 0.0f;
 
   typename S::TS dma_s;
   typename S::TV dma_v;
@@ -157,16 +155,15 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
   // that fragments serve two products; reading them is what the LDS is busiest with.
   auto q_row = [&](int i) { return 2 * (w >> 2) + (i & 1); };
   auto q_col = [&](int i) { return NQ / 2 * (w & 3) + (i >> 1); };
-  f32x4 dQa[NQ], dKa[NQ], dPa[NP], dTa[NP];
+  f32x4 dQa[NQ], dKa[NQ], dPa[NP], dXa[NP];
 #pragma unroll
   for (int i = 0; i < NQ; ++i) dQa[i] = dKa[i] = zero4();
 #pragma unroll
-  for (int i = 0; i < NP; ++i) dPa[i] = dTa[i] = zero4();
+  for (int i = 0; i < NP; ++i) dPa[i] = dXa[i] = zero4();
   float c0 = 0.0f;  // this thread's part of <dS', S>
 
-  constexpr int UX = C * C / 4;  // 16-byte units of fp32 X
-  u32x4 rx[UX / NTH];
-  static_assert(UX % NTH == 0, "whole units per thread");
+  constexpr int UX = kGatedX / 8;  // 16-byte units of X, both parts
+  u32x4 rx[cdiv(UX, NTH)];
 
   dma_block(0);
   auto block = [&](const int v0, auto lastc) {
@@ -190,6 +187,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     const int rt = w >> 1, c = w & 1;  // this wavefront's tile of the [C][BV] products
     // D = V - diag(e) K S and dU = P^T dO + diag(w) K dS'
     f32x4 d = zero4(), du = zero4(), eks, wkd;
+    const float ar = as[16 * rt + li];
     {
 #pragma unroll
       for (int ku = 0; ku < NKU_D; ++ku) {
@@ -202,11 +200,11 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       du = wkd;
 #pragma unroll
       for (int ku = 0; ku < NKU_C; ++ku)
-        if (32 * ku + 31 >= 16 * rt) mma(du, sw_frag_tr<BV>(dOt, 16 * c, ku, lane), sw_frag_tr<C>(Pt, 16 * rt, ku, lane));
+        if (32 * ku + 31 >= 16 * rt) mma(du, sw_frag_tr<BV>(dOt, 16 * c, ku, lane), tri_frag_tr(Pt, rt, ku, lane));
       const bf16x4 vv = *reinterpret_cast<const bf16x4*>(Vt + swz_off<BV>(16 * rt + li, 16 * c + 4 * g));
 #pragma unroll
       for (int qq = 0; qq < 4; ++qq) d[qq] = static_cast<float>(vv[qq]) - eks[qq];
-      put(Dt, d, rt, c, li, g);
+      put(Dt, ar * d, rt, c, li, g);
       put(dUt, du, rt, c, li, g);
       // <dS', S>: both tiles have one layout, eight elements a thread
       if (tidv < BV * DK / 8) {
@@ -218,20 +216,20 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     __syncthreads();
     if constexpr (LAST) {
 #pragma unroll
-      for (int i = 0; i < UX / NTH; ++i) {
-        const int u = tidv + NTH * i, r = u / (C / 4), ch = u % (C / 4);
-        rx[i] = *reinterpret_cast<const u32x4*>(xws + slot * C * C + r * C + 4 * ch);
-      }
+      for (int i = 0; i < cdiv(UX, NTH); ++i)
+        if (tidv + NTH * i < UX) rx[i] = *reinterpret_cast<const u32x4*>(xfr + slot * kGatedX + 8 * (tidv + NTH * i));
     }
-    // U = T D and dD = T^T dU (= dV), and both scaled for dK
+    // U = X (a D) and dD = a X^T dU (= dV), and both scaled for dK
     {
       f32x4 u = zero4(), dd = zero4();
 #pragma unroll
       for (int ku = 0; ku < NKU_C; ++ku) {
-        if (32 * ku <= 16 * rt + 15) mma(u, sw_frag_tr<BV>(Dt, 16 * c, ku, lane), sw_frag<C>(Tt, 16 * rt + li, ku, g));
+        if (32 * ku <= 16 * rt + 15) mma(u, sw_frag_tr<BV>(Dt, 16 * c, ku, lane), tri_frag(Xt, rt, ku, lane));
         if (32 * ku + 31 >= 16 * rt)
-          mma(dd, sw_frag_tr<BV>(dUt, 16 * c, ku, lane), sw_frag_tr<C>(Tt, 16 * rt, ku, lane));
+          mma(dd, sw_frag_tr<BV>(dUt, 16 * c, ku, lane), tri_frag_tr(Xt, rt, ku, lane));
       }
+      const float da = rows4(sum4(dd, d));
+      dd *= ar;
       put(Ut, u, rt, c, li, g);
       put(dDt, dd, rt, c, li, g);
       const float xs = rows4(sum4(dd, eks)), wk = rows4(sum4(u, wkd));
@@ -240,6 +238,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       if (g == 0) {  // one lane per row and tile column: its own place
         xw[c][16 * rt + li] += xs;
         xw[2 + c][16 * rt + li] += wk;
+        xw[4 + c][16 * rt + li] += da;
       }
     }
     __syncthreads();
@@ -251,7 +250,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
         __builtin_nontemporal_store(x, reinterpret_cast<u32x4*>(dv + row0 * DV + r * v_stride + v0 + 8 * p));
       }
     }
-    if (v0 + BV >= DV) {  // the tail's Q, during the last block (over T and P, done with)
+    if (v0 + BV >= DV) {  // the tail's Q, during the last block (over X and P, done with)
       const auto* qs = static_cast<const uint16_t*>(uniform_ptr(q + krow0 * DK));
 #pragma unroll
       for (int i = 0; i < S::TK::PER_WAVE; ++i) {
@@ -259,7 +258,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
         else dma_k.template issue<true>(i, lds_addr_of(b16(S::QT)), qs, valid);
       }
     }
-    // dQ += dO S^T (unscaled);  dK += (w U) dS'^T + (-e dD) S^T;  dP0 += dO U^T;  dT += dU D^T
+    // dQ += dO S^T (unscaled);  dK += (w U) dS'^T + (-e dD) S^T;  dP0 += dO U^T;  dX += dU (a D)^T
 #pragma unroll
     for (int i = 0; i < NQ; ++i) {
       const int rr = q_row(i), dt = q_col(i);
@@ -273,7 +272,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       const int t = w + NWV * i, rr = t / NRT, jt = t % NRT;
       if (jt <= rr) {
         mma(dPa[i], sw_frag<BV>(Ut, 16 * jt + li, 0, g), sw_frag<BV>(dOt, 16 * rr + li, 0, g));
-        mma(dTa[i], sw_frag<BV>(Dt, 16 * jt + li, 0, g), sw_frag<BV>(dUt, 16 * rr + li, 0, g));
+        mma(dXa[i], sw_frag<BV>(Dt, 16 * jt + li, 0, g), sw_frag<BV>(dUt, 16 * rr + li, 0, g));
       }
     }
     if (v0 + BV < DV) {
@@ -293,12 +292,10 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
   // took 10,000 of a chunk's 95,000 cycles)
   auto fresh = [&]() { asm volatile("" : "+v"(li), "+v"(g), "+v"(lane)); };
   uint16_t *Qt = b16(S::QT), *dPt = b16(S::DPT), *dXh = b16(S::DXH), *dXl = b16(S::DXL);
-  uint16_t *Wh = b16(S::WH), *Wl = b16(S::WL), *Xh = b16(S::XH), *Xl = b16(S::XL), *Eb = b16(S::EB);
+  uint16_t *Wh = b16(S::WH), *Wl = b16(S::WL), *Xh = b16(S::XF), *Xl = Xh + kGatedX / 2, *Eb = b16(S::EB);
   uint16_t *dQs = b16(S::DQS), *dKs = b16(S::DKS);
-  float *A0 = f32p(S::A0), *dAf = f32p(S::DAF), *red = f32p(S::RED), *msum = f32p(S::MSUM);
+  float *dAf = f32p(S::DAF), *red = f32p(S::RED), *msum = f32p(S::MSUM);
   constexpr int CPG = S::CPG;
-  constexpr int NPART = NTH / C, RPP = C / NPART;
-  const int cr = tid % C, prt = tid / C;
   auto split = [](float x, uint16_t& hi, uint16_t& lo) {
     hi = from_f32<uint16_t>(x);
     lo = from_f32<uint16_t>(x - to_f32(hi));
@@ -341,7 +338,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     if (g == 0) red[dt * C + r] = s;
   }
   fresh();
-  // dP = Gam * dP0 as bf16, dT fp32, X as high and low parts; the first part of
+  // dP = Gam * dP0 as bf16, dX and X as high and low parts; the first part of
   // M (strictly lower), dP * Q K^T, stays in registers
   f32x4 M[NP];
 #pragma unroll
@@ -356,21 +353,19 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     }
     const float gr = gs[r];
     const f32x4 gj = *reinterpret_cast<const f32x4*>(gs + c);
-    f32x4 p, dt_;
+    f32x4 p, dx;
 #pragma unroll
     for (int qq = 0; qq < 4; ++qq) {
       p[qq] = c + qq <= r ? dPa[i][qq] * exp2_gate(gr - gj[qq]) : 0.0f;
       M[i][qq] = c + qq < r ? p[qq] * qk[qq] : 0.0f;
-      dt_[qq] = c + qq <= r ? dTa[i][qq] : 0.0f;
+      dx[qq] = c + qq <= r ? dXa[i][qq] : 0.0f;
     }
     st4(dPt + swz_off<C>(r, c), p);
-    st4(A0 + r * CPF + c, dt_);
+    split4(dx, dXh + swz_off<C>(r, c), dXl + swz_off<C>(r, c));
   }
 #pragma unroll
-  for (int i = 0; i < UX / NTH; ++i) {
-    const int u = tid + NTH * i, r = u / (C / 4), ch = u % (C / 4);
-    split4(__builtin_bit_cast(f32x4, rx[i]), Xh + swz_off<C>(r, 4 * ch), Xl + swz_off<C>(r, 4 * ch));
-  }
+  for (int i = 0; i < cdiv(UX, NTH); ++i)
+    if (tid + NTH * i < UX) st16(Xh + 8 * (tid + NTH * i), rx[i]);
   __syncthreads();
   if (tid < C) {  // y_i so far
     float s = -(xw[0][tid] + xw[1][tid]);
@@ -409,29 +404,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     }
   }
   __syncthreads();  // red is read, Q and dP are done with
-  // da_j = sum_i dT_ij X_ij (partial sums);  dX = dT diag(a), as high and low parts (over Q)
-  {
-    float s = 0.0f;
-#pragma unroll
-    for (int r = prt * RPP; r < (prt + 1) * RPP; ++r)
-      s = fmaf(A0[r * CPF + cr], to_f32(Xh[swz_off<C>(r, cr)]) + to_f32(Xl[swz_off<C>(r, cr)]), s);
-    red[prt * C + cr] = s;
-  }
-#pragma unroll
-  for (int i = 0; i < C * C / 4 / NTH; ++i) {
-    const int u = tid + NTH * i, r = u / (C / 4), c = 4 * (u % (C / 4));
-    split4(*reinterpret_cast<const f32x4*>(A0 + r * CPF + c) * *reinterpret_cast<const f32x4*>(as + c),
-           dXh + swz_off<C>(r, c), dXl + swz_off<C>(r, c));
-  }
-  __syncthreads();
-  if (tid < C) {
-    float s = 0.0f;
-#pragma unroll
-    for (int p = 0; p < NPART; ++p) s += red[p * C + tid];
-    das[tid] = s;
-  }
-  fresh();
-  // W = X^T dX, as high and low parts (over dT)
+  // W = X^T dX, as high and low parts (over Q)
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
     const int t = w + NWV * i, rr = t / NRT, jt = t % NRT;
@@ -440,7 +413,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     for (int ku = 0; ku < NKU_C; ++ku)
       if (32 * ku + 31 >= 16 * rr && 32 * ku + 31 >= 16 * jt)  // X and dT are lower triangular
         mma3(acc, sw_frag_tr<C>(dXh, 16 * jt, ku, lane), sw_frag_tr<C>(dXl, 16 * jt, ku, lane),
-             sw_frag_tr<C>(Xh, 16 * rr, ku, lane), sw_frag_tr<C>(Xl, 16 * rr, ku, lane));
+             tri_frag_tr(Xh, rr, ku, lane), tri_frag_tr(Xl, rr, ku, lane));
     const int at = swz_off<C>(16 * rr + li, 16 * jt + 4 * g);
     split4(acc, Wh + at, Wl + at);
   }
@@ -456,7 +429,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
 #pragma unroll
       for (int ku = 0; ku < NKU_C; ++ku)
         if (32 * ku <= 16 * jt + 15)  // X^T's rows of this tile are zero past column 16 jt + 15
-          mma3(acc, sw_frag<C>(Xh, 16 * jt + li, ku, g), sw_frag<C>(Xl, 16 * jt + li, ku, g),
+          mma3(acc, tri_frag(Xh, jt, ku, lane), tri_frag(Xl, jt, ku, lane),
                sw_frag<C>(Wh, 16 * rr + li, ku, g), sw_frag<C>(Wl, 16 * rr + li, ku, g));
 #pragma unroll
       for (int ku = 0; ku < NKU_D; ++ku)
@@ -488,7 +461,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
   __syncthreads();
   // da_i += sum_j N_ij, then dbeta and dlambda;  dg;  dG + dG^T as bf16 (over X)
   if (tid < C) {
-    float s = das[tid], y = ys[tid];
+    float s = xw[4][tid] + xw[5][tid], y = ys[tid];
 #pragma unroll
     for (int jt = 0; jt < NRT; ++jt) {
       s += red[jt * C + tid];

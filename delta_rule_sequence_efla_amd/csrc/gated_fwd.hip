@@ -14,7 +14,7 @@ constexpr int kGatedChunk = 64;
 constexpr int kGatedOrderedSeqs = 4096;
 
 template <int DK, bool BWD>
-hipError_t ut_impl(const GatedFwd& a, uint16_t* tfr, float* gws, const GatedUtBwd& b, int32_t* order, hipStream_t s) {
+hipError_t ut_impl(const GatedFwd& a, uint16_t* xfr, float* gws, const GatedUtBwd& b, int32_t* order, hipStream_t s) {
   const int NC = a.cu == nullptr ? int((a.L + kGatedChunk - 1) / kGatedChunk) : int(a.L / kGatedChunk) + a.N;
   const int64_t nchunks = int64_t(a.cu == nullptr ? a.B : 1) * a.H * NC;
   constexpr int W = UtWaveShape<DK, kGatedChunk>::WAVES;
@@ -24,19 +24,19 @@ hipError_t ut_impl(const GatedFwd& a, uint16_t* tfr, float* gws, const GatedUtBw
   const int64_t nrank = order != nullptr ? (a.N + kRankSeqs - 1) / kRankSeqs : 0;
   if (nwg + nrank == 0) return hipSuccess;
   hipLaunchKernelGGL((gated_ut_wave_kernel<DK, BWD>), dim3(unsigned(nwg + nrank)), dim3(kThreads), 0, s,
-                     static_cast<const uint16_t*>(a.k), static_cast<const uint16_t*>(a.beta), a.g, tfr, gws, a.H, a.Hk,
+                     static_cast<const uint16_t*>(a.k), static_cast<const uint16_t*>(a.beta), a.g, xfr, gws, a.H, a.Hk,
                      a.L, NC, nchunks, a.rule, a.cu, a.N, nwg, order, b);
   return hipGetLastError();
 }
 
 template <int DK, bool OUT>
-hipError_t split_impl(const GatedFwd& a, const uint16_t* tfr, const float* gws, const int32_t* order,
+hipError_t split_impl(const GatedFwd& a, const uint16_t* xfr, const float* gws, const int32_t* order,
                       uint16_t* statesT, hipStream_t s) {
   const int NC = a.cu == nullptr ? int((a.L + kGatedChunk - 1) / kGatedChunk) : int(a.L / kGatedChunk) + a.N;
   const int64_t bh = int64_t(a.cu == nullptr ? a.B : a.N) * a.H;
   const int NVB = a.DV / 32;
   hipLaunchKernelGGL((gated_split_kernel<DK, OUT>), dim3(unsigned(bh * NVB)), dim3(OUT ? GatedSplitShape<DK>::THREADS : GatedSplitShape<DK>::STATE_THREADS), 0, s,
-                     a, tfr, gws, order, NC, NVB, bh % 8 == 0 ? 1 : 0, statesT);
+                     a, xfr, gws, order, NC, NVB, bh % 8 == 0 ? 1 : 0, statesT);
   return hipGetLastError();
 }
 }  // namespace
@@ -46,38 +46,37 @@ bool gated_chunk_supported(int DK, int DV) { return (DK == 64 || DK == 128) && D
 GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed) {
   const size_t slots = packed ? size_t(H) * (L / kGatedChunk + N) : size_t(B) * H * ((L + kGatedChunk - 1) / kGatedChunk);
   GatedFwdLayout w{};
-  w.t = 0;
-  w.g = align256(slots * kGatedT * 2);
+  w.x = 0;
+  w.g = align256(slots * kGatedX * 2);
   w.order = w.g + align256(slots * kGatedG * 4);
   w.total = w.order + (packed ? align256(size_t(N) * 4) : 0);
   return w;
 }
 
-hipError_t launch_gated_ut_bwd(const GatedFwd& a, uint16_t* tfr, float* gws, float* x, uint16_t* t, uint16_t* p,
-                               uint16_t* qe, hipStream_t s) {
-  const GatedUtBwd b{static_cast<const uint16_t*>(a.q), x, t, p, qe};
-  return a.DK == 64 ? ut_impl<64, true>(a, tfr, gws, b, nullptr, s) : ut_impl<128, true>(a, tfr, gws, b, nullptr, s);
+hipError_t launch_gated_ut_bwd(const GatedFwd& a, uint16_t* xfr, float* gws, uint16_t* p, uint16_t* qe, hipStream_t s) {
+  const GatedUtBwd b{static_cast<const uint16_t*>(a.q), p, qe};
+  return a.DK == 64 ? ut_impl<64, true>(a, xfr, gws, b, nullptr, s) : ut_impl<128, true>(a, xfr, gws, b, nullptr, s);
 }
 
-hipError_t launch_gated_states(const GatedFwd& a, const uint16_t* tfr, const float* gws, uint16_t* statesT,
+hipError_t launch_gated_states(const GatedFwd& a, const uint16_t* xfr, const float* gws, uint16_t* statesT,
                                hipStream_t s) {
-  return a.DK == 64 ? split_impl<64, false>(a, tfr, gws, nullptr, statesT, s)
-                    : split_impl<128, false>(a, tfr, gws, nullptr, statesT, s);
+  return a.DK == 64 ? split_impl<64, false>(a, xfr, gws, nullptr, statesT, s)
+                    : split_impl<128, false>(a, xfr, gws, nullptr, statesT, s);
 }
 
 hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s) {
   const bool packed = a.cu != nullptr;
   const GatedFwdLayout lay = gated_fwd_layout(a.B, a.N, a.H, a.L, packed);
   auto* ws = static_cast<unsigned char*>(workspace);
-  auto* tfr = reinterpret_cast<uint16_t*>(ws + lay.t);
+  auto* xfr = reinterpret_cast<uint16_t*>(ws + lay.x);
   auto* gws = reinterpret_cast<float*>(ws + lay.g);
   // packed: the caller's schedule, or one ranked by workgroups of the UT launch
   int32_t* mine = packed && a.order == nullptr && a.N <= kGatedOrderedSeqs ? reinterpret_cast<int32_t*>(ws + lay.order) : nullptr;
   const GatedUtBwd none{};
-  const hipError_t e = a.DK == 64 ? ut_impl<64, false>(a, tfr, gws, none, mine, s) : ut_impl<128, false>(a, tfr, gws, none, mine, s);
+  const hipError_t e = a.DK == 64 ? ut_impl<64, false>(a, xfr, gws, none, mine, s) : ut_impl<128, false>(a, xfr, gws, none, mine, s);
   if (e != hipSuccess) return e;
   const int32_t* order = mine != nullptr ? mine : a.order;
-  return a.DK == 64 ? split_impl<64, true>(a, tfr, gws, order, nullptr, s) : split_impl<128, true>(a, tfr, gws, order, nullptr, s);
+  return a.DK == 64 ? split_impl<64, true>(a, xfr, gws, order, nullptr, s) : split_impl<128, true>(a, xfr, gws, order, nullptr, s);
 }
 
 }  // namespace efla

@@ -4,7 +4,7 @@
 // Per chunk, last to first, with dS' the loss gradient at the chunk's end, e =
 // e^G, w = e^{G_C - G} and Qe = diag(e) Q - P T diag(e) K (gated_ut.h):
 //     dstates[n] = dS'
-//     E = diag(w) K dS',   F = diag(e) T^T E
+//     E = diag(w) K dS',   F = diag(e) T^T E = diag(e a) X^T E
 //     dS = e^{G_C} dS' + Qe^T dO - K^T F
 // dS is held and summed in float32; as an operand it is rounded to bf16 once (it
 // is read by products that end in bf16 gradients), as are E and F.
@@ -30,21 +30,20 @@ struct GatedReverseShape {
   static constexpr int NT = BV / 16;  // dS tiles per workgroup
   static constexpr int NRT = C / 16, NKU_D = DK / 32, NKU_C = C / 32;
   static constexpr int NSW = NKU_D;  // S waves, 32 key dims each
-  static constexpr int KOFF = 0, QOFF = C * DK, TOFF = 2 * C * DK, OOFF = 2 * C * DK + C * C;
+  static constexpr int KOFF = 0, QOFF = C * DK, XOFF = 2 * C * DK, OOFF = 2 * C * DK + kGatedX / 2;
   static constexpr int GOFF = OOFF + C * BV;
   static constexpr int SLOT = GOFF + kGatedG * 2;  // in bf16 elements
   using TK = DmaTile<C, DK, 1, true>;  // K and Qe: 16-byte-fragment swizzle
-  using TT = DmaTile<C, C, 1>;
   using TO = DmaTile<C, BV, 1>;
-  static constexpr int PK = TK::PER_WAVE, PT = TT::PER_WAVE, PO = TO::PER_WAVE;
-  static constexpr int COUNT = 2 * PK + PT + PO + 1;  // transfers per chunk
+  static constexpr int PK = TK::PER_WAVE, PX = kGatedX / 2 * 2 / 1024, PO = TO::PER_WAVE;
+  static constexpr int COUNT = 2 * PK + PX + PO + 1;  // transfers per chunk
   static constexpr int kY0 = 0, kS0 = 2, kDma = 2 + NSW, NWAVES = 3 + NSW, THREADS = NWAVES * kWave;
 };
 
 // dense batch; NVB = DV / BV workgroups per (b, h).
 template <int DK>
 __global__ __launch_bounds__((GatedReverseShape<DK>::THREADS)) void gated_reverse_kernel(
-    GatedBwd b, const uint16_t* __restrict__ qe, const uint16_t* __restrict__ tws, const float* __restrict__ gws,
+    GatedBwd b, const uint16_t* __restrict__ qe, const uint16_t* __restrict__ xfr, const float* __restrict__ gws,
     uint16_t* __restrict__ dstatesT, int NC, int NVB, int remap) {
   using S = GatedReverseShape<DK>;
   constexpr int C = S::C, BV = S::BV, NT = S::NT, NRT = S::NRT, NKU_D = S::NKU_D, NKU_C = S::NKU_C;
@@ -99,17 +98,15 @@ __global__ __launch_bounds__((GatedReverseShape<DK>::THREADS)) void gated_revers
     constexpr int D = S::COUNT;
     static_assert(D < 64, "one chunk's transfers fit the vmcnt counter");
     typename S::TK tk, tq;
-    typename S::TT tt;
-    typename S::TO to;
+      typename S::TO to;
     tk.init(int64_t(b.Hk) * DK, lane, 0);
     tq.init(DK, lane, 0);
-    tt.init(C, lane, 0);
-    to.init(int64_t(H) * DV, lane, 0);
+      to.init(int64_t(H) * DV, lane, 0);
     auto issue = [&](int n, int part, int parts) {
       const int m = chunk_of(n);
       const auto* ks = static_cast<const uint16_t*>(uniform_ptr(k + (tok_of(m) * b.Hk + hk) * DK));
       const auto* qs = static_cast<const uint16_t*>(uniform_ptr(qe + (sp.slot0 + m) * C * DK));
-      const auto* ts = static_cast<const uint16_t*>(uniform_ptr(tws + (sp.slot0 + m) * C * C));
+      const void* xs = uniform_ptr(xfr + (sp.slot0 + m) * kGatedX);  // the high parts
       const auto* os = static_cast<const uint16_t*>(uniform_ptr(dout + (tok_of(m) * H + h) * DV + v0));
       const void* gsrc = uniform_ptr(gws + (sp.slot0 + m) * kGatedG);
       const int valid = chunk_valid(m);
@@ -121,8 +118,8 @@ __global__ __launch_bounds__((GatedReverseShape<DK>::THREADS)) void gated_revers
           if (j < part * D / parts || j >= (part + 1) * D / parts) continue;
           if (j < S::PK) tk.template issue<R>(j, addr + 2 * S::KOFF, ks, valid);
           else if (j < 2 * S::PK) tq.template issue<false>(j - S::PK, addr + 2 * S::QOFF, qs, C);
-          else if (j < 2 * S::PK + S::PT) tt.template issue<false>(j - 2 * S::PK, addr + 2 * S::TOFF, ts, C);
-          else if (j < D - 1) to.template issue<R>(j - 2 * S::PK - S::PT, addr + 2 * S::OOFF, os, valid);
+          else if (j < 2 * S::PK + S::PX) dma16(xs, uint32_t(j - 2 * S::PK) * 1024u + uint32_t(lane) * 16u, addr + 2 * S::XOFF + 1024 * (j - 2 * S::PK));
+          else if (j < D - 1) to.template issue<R>(j - 2 * S::PK - S::PX, addr + 2 * S::OOFF, os, valid);
           else dma16(gsrc, uint32_t(lane) * 16u, addr + 2 * S::GOFF);
         }
       };
@@ -150,21 +147,22 @@ __global__ __launch_bounds__((GatedReverseShape<DK>::THREADS)) void gated_revers
     // ----------------------------------------------------------------- Y
     const int ct = role - S::kY0;
     Frag<uint16_t> Kf[NRT][NKU_D];
-    Frag<uint16_t> Tf[NRT][NKU_C];  // T^T: row tile rt, k-unit ku (T^T is upper triangular: ku >= rt / 2)
+    Frag<uint16_t> Xf[NRT][NKU_C];  // X^T: row tile rt, k-unit ku (X^T is upper triangular: ku >= rt / 2)
     f32x4 eg[NRT], wg[NRT];
     auto load = [&](const uint16_t* __restrict__ cur) {
       const uint16_t* Ks = cur + S::KOFF;
-      const uint16_t* Ts = cur + S::TOFF;
+      const uint16_t* Xs = cur + S::XOFF;
 #pragma unroll
       for (int rt = 0; rt < NRT; ++rt) {
-        eg[rt] = *reinterpret_cast<const f32x4*>(gates(cur) + 64 + 16 * rt + 4 * g);
+        eg[rt] = *reinterpret_cast<const f32x4*>(gates(cur) + 64 + 16 * rt + 4 * g) *
+                 *reinterpret_cast<const f32x4*>(gates(cur) + 192 + 16 * rt + 4 * g);
         wg[rt] = *reinterpret_cast<const f32x4*>(gates(cur) + 128 + 16 * rt + 4 * g);
       }
 #pragma unroll
       for (int rt = 0; rt < NRT; ++rt)
 #pragma unroll
         for (int ku = 0; ku < NKU_C; ++ku)
-          if (32 * ku + 31 >= 16 * rt) Tf[rt][ku] = sw_frag_tr<C>(Ts, 16 * rt, ku, lane);
+          if (32 * ku + 31 >= 16 * rt) Xf[rt][ku] = tri_frag_tr(Xs, rt, ku, lane);
 #pragma unroll
       for (int ku = 0; ku < NKU_D; ++ku)
 #pragma unroll
@@ -196,8 +194,8 @@ __global__ __launch_bounds__((GatedReverseShape<DK>::THREADS)) void gated_revers
         f32x4 F0 = zero4(), F1 = zero4();
 #pragma unroll
         for (int kk = ku; kk < NKU_C; ++kk) {
-          mma(F0, Tf[2 * ku][kk], bE[kk]);
-          mma(F1, Tf[2 * ku + 1][kk], bE[kk]);
+          mma(F0, Xf[2 * ku][kk], bE[kk]);
+          mma(F1, Xf[2 * ku + 1][kk], bE[kk]);
         }
 #pragma unroll
         for (int qq = 0; qq < 4; ++qq) {

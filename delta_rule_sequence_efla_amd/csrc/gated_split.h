@@ -67,7 +67,7 @@ struct GatedSplitShape {
 // transposed, [slots][DV][DK] (the layout of recurrence_split.h), without the O
 // and P waves and Q.
 template <int DK, bool OUT>
-__global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitShape<DK>::STATE_THREADS)) void gated_split_kernel(GatedFwd a, const uint16_t* __restrict__ tfr,
+__global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitShape<DK>::STATE_THREADS)) void gated_split_kernel(GatedFwd a, const uint16_t* __restrict__ xfr,
                                                           const float* __restrict__ gws,
                                                           const int32_t* __restrict__ order, int NC, int NVB, int remap,
                                                           uint16_t* __restrict__ statesT) {
@@ -193,16 +193,16 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
     const int ct = role & 1;  // the later half's waves, with twice the products after M, on SIMDs 2 and 3
     auto y_role = [&](auto halfc) {
       constexpr int Y = decltype(halfc)::value, RT0 = 2 * Y;
-      Frag<uint16_t> Kf[2][NKU_D], Th[2][Y + 1], Tl[2][Y + 1];
+      Frag<uint16_t> Kf[2][NKU_D], Xh[2][Y + 1], Xl[2][Y + 1];
       bf16x4 Vt[2];
-      auto load_t = [&](int m) {
-        const bf16x8* src = reinterpret_cast<const bf16x8*>(tfr + (sp.slot0 + (m < nc ? m : nc - 1)) * kGatedT) + lane;
+      auto load_x = [&](int m) {
+        const bf16x8* src = reinterpret_cast<const bf16x8*>(xfr + (sp.slot0 + (m < nc ? m : nc - 1)) * kGatedX) + lane;
 #pragma unroll
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int kk = 0; kk <= Y; ++kk) {
-            Th[r][kk].v = src[pf_index(RT0 + r, kk) * 64];
-            Tl[r][kk].v = src[(6 + pf_index(RT0 + r, kk)) * 64];
+            Xh[r][kk].v = src[pf_index(RT0 + r, kk) * 64];
+            Xl[r][kk].v = src[(6 + pf_index(RT0 + r, kk)) * 64];
           }
       };
       auto load = [&](const uint16_t* __restrict__ cur) {  // this chunk's K and this tile's V
@@ -224,12 +224,13 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
           sh[ku].v = bS_buf[0][ct][ku][lane];
           sl[ku].v = bS_buf[1][ct][ku][lane];
         }
-        f32x4 D[2], lo[2], eg[2], wg[2];
+        f32x4 D[2], lo[2], eg[2], wg[2], ag[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           D[r] = lo[r] = zero4();
           eg[r] = *reinterpret_cast<const f32x4*>(gt + 64 + 16 * r);
           wg[r] = *reinterpret_cast<const f32x4*>(gt + 128 + 16 * r);
+          ag[r] = *reinterpret_cast<const f32x4*>(gt + 192 + 16 * r);
         }
 #pragma unroll
         for (int ku = 0; ku < NKU_D; ++ku) {  // high and low parts in sums of their own: four chains
@@ -242,7 +243,7 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int qq = 0; qq < 4; ++qq)
-            D[r][qq] = fmaf(-eg[r][qq], D[r][qq] + lo[r][qq], static_cast<float>(Vt[r][qq]));
+            D[r][qq] = ag[r][qq] * fmaf(-eg[r][qq], D[r][qq] + lo[r][qq], static_cast<float>(Vt[r][qq]));
         Frag<uint16_t> dh[Y + 1], dl[Y + 1];
         split_frag(D[0], D[1], dh[Y], dl[Y]);
         if constexpr (Y == 0) {
@@ -260,11 +261,11 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
 #pragma unroll
         for (int kk = Y; kk >= 0; --kk) {  // this wave's own D first, while the other half's arrives
 #pragma unroll
-          for (int r = 0; r < 2; ++r) mma(U[r], Tl[r][kk], dh[kk]);
+          for (int r = 0; r < 2; ++r) mma(U[r], Xl[r][kk], dh[kk]);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) mma(U[r], Th[r][kk], dl[kk]);
+          for (int r = 0; r < 2; ++r) mma(U[r], Xh[r][kk], dl[kk]);
 #pragma unroll
-          for (int r = 0; r < 2; ++r) mma(U[r], Th[r][kk], dh[kk]);
+          for (int r = 0; r < 2; ++r) mma(U[r], Xh[r][kk], dh[kk]);
         }
         if constexpr (OUT) bU_buf[ct][Y][lane] = acc_frag<uint16_t>(U[0], U[1]).v;
 #pragma unroll
@@ -280,10 +281,10 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
         // whatever the ring holds, and nothing reads what they bring: behind a
         // branch, the loaded registers would be merged with the old ones, with
         // a wait there.
-        load_t(n + 1);
+        load_x(n + 1);
         load(ring + ((n + 1) % 3) * S::SLOT);
       };
-      if (nc > 0) load_t(0);
+      if (nc > 0) load_x(0);
       for (int n = 0; n < nc; ++n) step(n);
     };
     if (role < 2) y_role(std::integral_constant<int, 0>{});
@@ -329,9 +330,9 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
       sync();  // A
       seen |= warm;
       {
-        constexpr int LINES = kGatedT * 2 / 128 / S::NSW;
+        constexpr int LINES = kGatedX * 2 / 128 / S::NSW;
         const int m = n + 3 < nc ? n + 3 : nc - 1;
-        const auto* line = reinterpret_cast<const uint32_t*>(tfr + (sp.slot0 + m) * kGatedT) + 32 * (LINES * sw + (lane < LINES ? lane : LINES - 1));
+        const auto* line = reinterpret_cast<const uint32_t*>(xfr + (sp.slot0 + m) * kGatedX) + 32 * (LINES * sw + (lane < LINES ? lane : LINES - 1));
         warm = *line;
       }
       Frag<uint16_t> KT[2][NKU_C];

@@ -12,19 +12,20 @@
 // v_exp_f32.
 //
 // Written per chunk slot:
-//   tfr  T as the recurrence's operand fragments, in two bf16 parts (T = hi +
+//   xfr  X as the recurrence's operand fragments, in two bf16 parts (X = hi +
 //        lo to 2^-16): [12][64 lanes][8], fragments (rt, ku) of the lower
 //        triangle as pf_index numbers them, high parts first.  A lane's tile
-//        of X_ij^T is half a fragment of row tile i, so T leaves the registers
-//        in that order, 1 KiB coalesced, and the recurrence loads it the same
-//        way, past the LDS.
+//        of X_ij^T is half a fragment of row tile i, so X leaves the registers
+//        in that order, 1 KiB coalesced, and is loaded the same way.  T itself
+//        is not stored: where it is a factor, the other operand's rows are
+//        scaled by a (T D = X (a D), T^T dU = a (X^T dU)).
 //   gws  [4][64] fp32: G log2(e), e^{G_i}, e^{G_C - G_i}, a.  Tokens past the
 //        end have a = 0 and G = G_C.
-//   BWD: also what the backward's passes read, as rows: X fp32 and T bf16
-//        ([64][64], zeros above the diagonal), P = Gam * tril(Q K^T) bf16, and
-//        the effective queries Qe = diag(e^G) Q - P T diag(e^G) K, bf16
-//        [64][d_k], through which the output reads the chunk's start state
-//        (O = Qe S + P T V), formed from registers as in ut_wave.h.
+//   BWD: also what the backward's passes read: P = Gam * tril(Q K^T) as six
+//        bf16 fragments in the same order, and the effective queries Qe =
+//        diag(e^G) Q - P T diag(e^G) K, bf16 [64][d_k], through which the output
+//        reads the chunk's start state (O = Qe S + P T V), formed from registers
+//        as in ut_wave.h.
 // Bound by HBM like ut_wave_kernel: 16 KiB of K read and 13 KiB written a chunk
 // at d_k 128.
 #pragma once
@@ -39,12 +40,12 @@ namespace efla {
 // What the backward instance reads and writes besides (null otherwise).
 struct GatedUtBwd {
   const uint16_t* q;
-  float* x;
-  uint16_t *t, *p, *qe;
+  uint16_t *p, *qe;
 };
 
 constexpr double kLog2e = 1.4426950408889634;
-constexpr int kGatedT = 12 * 64 * 8;  // bf16 values of T per chunk slot
+constexpr int kGatedX = 12 * 64 * 8;  // bf16 values of X per chunk slot
+constexpr int kGatedP = 6 * 64 * 8;   // and of P
 constexpr int kGatedG = 4 * 64;       // floats of the gate block per chunk slot
 
 // e^{x} for x in base-2 logarithms
@@ -71,10 +72,28 @@ __device__ __forceinline__ void split_frag(const f32x4& lo4, const f32x4& hi4, F
   l.v = __builtin_bit_cast(bf16x8, lp);
 }
 
+// Fragments of a lower-triangular [64][64] array held in fragment order in the
+// LDS: of rows 16 rt .., one 16-byte read, ...
+__device__ __forceinline__ Frag<uint16_t> tri_frag(const uint16_t* X, int rt, int ku, int lane) {
+  Frag<uint16_t> f;
+  f.v = *reinterpret_cast<const bf16x8*>(X + (pf_index(rt, ku) * 64 + lane) * 8);
+  return f;
+}
+// ... and of its transpose, rows 16 ct .. of X^T (ku >= ct / 2), as sw_frag_tr
+__device__ __forceinline__ Frag<uint16_t> tri_frag_tr(const uint16_t* X, int ct, int ku, int lane) {
+  const int j = lane & 15, g = lane >> 4;
+  const int at = ((j & 3) * 16 + 4 * g + (j >> 2)) * 8 + 4 * (ct & 1);
+  const bf16x4 lo = lds_read_tr(X + pf_index(2 * ku, ct >> 1) * 512 + at);
+  const bf16x4 hi = lds_read_tr(X + pf_index(2 * ku + 1, ct >> 1) * 512 + at);
+  Frag<uint16_t> f;
+  f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return f;
+}
+
 template <int DK, bool BWD = false>
 __global__ __launch_bounds__(256, BWD ? 2 : 4) void gated_ut_wave_kernel(const uint16_t* __restrict__ k,
                                                             const uint16_t* __restrict__ beta,
-                                                            const float* __restrict__ gate, uint16_t* __restrict__ tfr,
+                                                            const float* __restrict__ gate, uint16_t* __restrict__ xfr,
                                                             float* __restrict__ gws, int H, int Hk, int64_t L, int NC,
                                                             int64_t nchunks, int rule, const int32_t* __restrict__ cu,
                                                             int N, int64_t nwg_ut, int32_t* __restrict__ order,
@@ -246,7 +265,7 @@ __global__ __launch_bounds__(256, BWD ? 2 : 4) void gated_ut_wave_kernel(const u
         XTo[i][j][qq] = -YT[qq];
       }
     }
-  bf16x8* tdst = reinterpret_cast<bf16x8*>(tfr + id * kGatedT) + lane;
+  bf16x8* xdst = reinterpret_cast<bf16x8*>(xfr + id * kGatedX) + lane;
 #pragma unroll
   for (int i = 0; i < NRT; ++i)
 #pragma unroll
@@ -257,46 +276,19 @@ __global__ __launch_bounds__(256, BWD ? 2 : 4) void gated_ut_wave_kernel(const u
         const int j = 2 * ku + p;
 #pragma unroll
         for (int qq = 0; qq < 4; ++qq)
-          t[p][qq] = (j < i || (j == i && 4 * g + qq <= li)) ? XTo[i][j < i ? j : i][qq] * arow[j][qq] : 0.0f;
+          t[p][qq] = (j < i || (j == i && 4 * g + qq <= li)) ? XTo[i][j < i ? j : i][qq] : 0.0f;
       }
       Frag<uint16_t> hi, lo;
       split_frag(t[0], t[1], hi, lo);
-      tdst[pf_index(i, ku) * 64] = hi.v;
-      tdst[(6 + pf_index(i, ku)) * 64] = lo.v;
+      xdst[pf_index(i, ku) * 64] = hi.v;
+      xdst[(6 + pf_index(i, ku)) * 64] = lo.v;
     }
   if constexpr (BWD) {
     constexpr int TP = S::TP, NKC = C / 32;
     uint16_t* Ts = reinterpret_cast<uint16_t*>(scratch_all[w]);  // [C][TP] staging
-    float* xdst = b.x + id * int64_t(C) * C;
     float e_row[NRT];
 #pragma unroll
     for (int i = 0; i < NRT; ++i) e_row[i] = exp2_gate(gr[i]);
-    // X as rows, a lane's four columns a piece; T staged as bf16 rows
-#pragma unroll
-    for (int i = 0; i < NRT; ++i)
-#pragma unroll
-      for (int j = 0; j < NRT; ++j) {
-        f32x4 x;
-        bf16x4 tv;
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq) {
-          x[qq] = (j < i || (j == i && 4 * g + qq <= li)) ? XTo[i][j < i ? j : i][qq] : 0.0f;
-          tv[qq] = static_cast<__bf16>(x[qq] * arow[j][qq]);
-        }
-        __builtin_nontemporal_store(x, reinterpret_cast<f32x4*>(xdst + (16 * i + li) * C + 16 * j + 4 * g));
-        *reinterpret_cast<bf16x4*>(Ts + (16 * i + li) * TP + 16 * j + 4 * g) = tv;
-      }
-    auto store_rows = [&](uint16_t* dst) {  // the staging tile as 16-byte row pieces
-      wave_lds_order();
-#pragma unroll
-      for (int idx = lane; idx < C * (C / 8); idx += 64) {
-        const int r = idx / (C / 8), c0 = (idx % (C / 8)) * 8;
-        __builtin_nontemporal_store(*reinterpret_cast<const u32x4*>(Ts + r * TP + c0),
-                                    reinterpret_cast<u32x4*>(dst + r * C + c0));
-      }
-      wave_lds_order();
-    };
-    store_rows(b.t + id * int64_t(C) * C);
     Frag<uint16_t> Qr[NRT][NKU];
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt) {
@@ -323,8 +315,9 @@ __global__ __launch_bounds__(256, BWD ? 2 : 4) void gated_ut_wave_kernel(const u
           Ts[ii * TP + jj] = from_f32<uint16_t>(jj <= ii ? acc[qq] * exp2_gate(gc[r][qq] - gr[c]) : 0.0f);
         }
       }
-    store_rows(b.p + id * int64_t(C) * C);
-    // P^T as B operand fragments, ku <= rt / 2 (P is lower triangular)
+    wave_lds_order();
+    // P^T as B operand fragments, ku <= rt / 2 (P is lower triangular), stored as such
+    bf16x8* pdst = reinterpret_cast<bf16x8*>(b.p + id * kGatedP) + lane;
     Frag<uint16_t> PtB[NRT][NKC];
 #pragma unroll
     for (int rt = 0; rt < NRT; ++rt)
@@ -334,6 +327,7 @@ __global__ __launch_bounds__(256, BWD ? 2 : 4) void gated_ut_wave_kernel(const u
           const bf16x4 lo = *reinterpret_cast<const bf16x4*>(Ts + (16 * rt + li) * TP + 32 * ku + 4 * g);
           const bf16x4 hi = *reinterpret_cast<const bf16x4*>(Ts + (16 * rt + li) * TP + 32 * ku + 16 + 4 * g);
           PtB[rt][ku].v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+          __builtin_nontemporal_store(PtB[rt][ku].v, pdst + pf_index(rt, ku) * 64);
         }
     float acol[NRT];
 #pragma unroll

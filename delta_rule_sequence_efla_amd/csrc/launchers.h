@@ -167,17 +167,16 @@ hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipSt
 // Chunked forward of bf16 inputs (gated_ut.h, gated_split.h): d_k 64 or 128, d_v
 // a multiple of 32, in chunks of 64.
 struct GatedFwdLayout {
-  size_t t, g, order, total;
+  size_t x, g, order, total;
 };
 bool gated_chunk_supported(int DK, int DV);
 GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed);
 hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s);
-// Its two launches as the backward runs them over a dense batch: T fragments and
-// gate blocks as the forward's, X (fp32), T, P and Qe as rows; then every
-// chunk's start state, [slots][DV][DK] bf16.
-hipError_t launch_gated_ut_bwd(const GatedFwd& a, uint16_t* tfr, float* gws, float* x, uint16_t* t, uint16_t* p,
-                               uint16_t* qe, hipStream_t s);
-hipError_t launch_gated_states(const GatedFwd& a, const uint16_t* tfr, const float* gws, uint16_t* statesT,
+// Its two launches as the backward runs them over a dense batch: X fragments and
+// gate blocks as the forward's, P fragments, Qe as rows; then every chunk's start
+// state, [slots][DV][DK] bf16.
+hipError_t launch_gated_ut_bwd(const GatedFwd& a, uint16_t* xfr, float* gws, uint16_t* p, uint16_t* qe, hipStream_t s);
+hipError_t launch_gated_states(const GatedFwd& a, const uint16_t* xfr, const float* gws, uint16_t* statesT,
                                hipStream_t s);
 
 struct GatedBwd {
@@ -195,10 +194,10 @@ hipError_t launch_gated_bwd(const GatedBwd& b, int C, void* ws, hipStream_t s);
 // reverse pass over the chunks (gated_reverse.h), dS' of every chunk as
 // [slots][DV][DK] bf16, and the per-chunk gradients (gated_bwd_chunk.h); dqh,
 // dkh as in gated_bwd.h.
-hipError_t launch_gated_reverse(const GatedBwd& b, const uint16_t* t, const uint16_t* qe, const float* gws,
+hipError_t launch_gated_reverse(const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe, const float* gws,
                                 uint16_t* dstatesT, hipStream_t s);
-hipError_t launch_gated_bwd_chunk(const GatedBwd& b, const uint16_t* t, const uint16_t* p, const float* x,
-                                  const float* gws, const uint16_t* statesT, const uint16_t* dstatesT, float* dqh,
+hipError_t launch_gated_bwd_chunk(const GatedBwd& b, const uint16_t* xfr, const uint16_t* p, const float* gws,
+                                  const uint16_t* statesT, const uint16_t* dstatesT, float* dqh,
                                   float* dkh, hipStream_t s);
 
 // Tables of a packed batch (plan.hip); order, seq, pos and starts nullable.
