@@ -194,7 +194,7 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
     auto y_role = [&](auto halfc) {
       constexpr int Y = decltype(halfc)::value, RT0 = 2 * Y;
       Frag<uint16_t> Kf[2][NKU_D], Xh[2][Y + 1], Xl[2][Y + 1];
-      bf16x4 Vt[2];
+      f32x4 aV[2];  // diag(a) V
       auto load_x = [&](int m) {
         const bf16x8* src = reinterpret_cast<const bf16x8*>(xfr + (sp.slot0 + (m < nc ? m : nc - 1)) * kGatedX) + lane;
 #pragma unroll
@@ -207,8 +207,12 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
       };
       auto load = [&](const uint16_t* __restrict__ cur) {  // this chunk's K and this tile's V
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          Vt[r] = lds_read_tr(cur + S::VOFF + swz_off<BV>(16 * (RT0 + r) + 4 * g + (li >> 2), 16 * ct + 4 * (li & 3)));
+        for (int r = 0; r < 2; ++r) {
+          const bf16x4 v = lds_read_tr(cur + S::VOFF + swz_off<BV>(16 * (RT0 + r) + 4 * g + (li >> 2), 16 * ct + 4 * (li & 3)));
+          const f32x4 ag = *reinterpret_cast<const f32x4*>(gates(cur) + 192 + 16 * (RT0 + r) + 4 * g);
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq) aV[r][qq] = ag[qq] * static_cast<float>(v[qq]);
+        }
 #pragma unroll
         for (int ku = 0; ku < NKU_D; ++ku)
 #pragma unroll
@@ -224,13 +228,12 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
           sh[ku].v = bS_buf[0][ct][ku][lane];
           sl[ku].v = bS_buf[1][ct][ku][lane];
         }
-        f32x4 D[2], lo[2], eg[2], wg[2], ag[2];
+        f32x4 D[2], lo[2], eg[2], wg[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           D[r] = lo[r] = zero4();
-          eg[r] = *reinterpret_cast<const f32x4*>(gt + 64 + 16 * r);
+          eg[r] = -*reinterpret_cast<const f32x4*>(gt + 64 + 16 * r) * *reinterpret_cast<const f32x4*>(gt + 192 + 16 * r);
           wg[r] = *reinterpret_cast<const f32x4*>(gt + 128 + 16 * r);
-          ag[r] = *reinterpret_cast<const f32x4*>(gt + 192 + 16 * r);
         }
 #pragma unroll
         for (int ku = 0; ku < NKU_D; ++ku) {  // high and low parts in sums of their own: four chains
@@ -243,7 +246,7 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
         for (int r = 0; r < 2; ++r)
 #pragma unroll
           for (int qq = 0; qq < 4; ++qq)
-            D[r][qq] = ag[r][qq] * fmaf(-eg[r][qq], D[r][qq] + lo[r][qq], static_cast<float>(Vt[r][qq]));
+            D[r][qq] = fmaf(eg[r][qq], D[r][qq] + lo[r][qq], aV[r][qq]);
         Frag<uint16_t> dh[Y + 1], dl[Y + 1];
         split_frag(D[0], D[1], dh[Y], dl[Y]);
         if constexpr (Y == 0) {
