@@ -14,6 +14,8 @@
 // and key head h / (H / Hk).
 #pragma once
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace efla {
@@ -43,6 +45,32 @@ __device__ __forceinline__ float row_sum16(float s) {
   s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x124, 0xF, 0xF, false));
   s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x122, 0xF, 0xF, false));
   s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), 0x121, 0xF, 0xF, false));
+  return s;
+}
+
+// Sum over the four lanes li, li + 16, li + 32, li + 48, in each of them: by the
+// row and half exchanges of the vector unit, no LDS round trips.
+__device__ __forceinline__ float row_sum4(float s) {
+  const uint32_t a = __float_as_uint(s);
+  const auto x = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+  const float t = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+  const uint32_t b = __float_as_uint(t);
+  const auto y = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  return __uint_as_float(y[0]) + __uint_as_float(y[1]);
+}
+
+// Inclusive sum over the lanes, by DPP: within rows of 16, then the rows' ends.
+__device__ __forceinline__ float wave_scan_dpp(float s) {
+  auto add = [&](auto ctrl, auto rows) {  // lanes without a source, and rows not named, add zero
+    s += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, s), decltype(ctrl)::value,
+                                                               decltype(rows)::value, 0xF, false));
+  };
+  add(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});  // row_shr:1, 2, 4, 8
+  add(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});
+  add(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});
+  add(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});
+  add(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});  // row_bcast:15 into rows 1, 3
+  add(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});  // row_bcast:31 into rows 2, 3
   return s;
 }
 

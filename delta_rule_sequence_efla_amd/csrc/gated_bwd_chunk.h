@@ -143,10 +143,6 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
   auto put = [&](uint16_t* X, const f32x4& a, int rt, int c, int li, int g) {
     st4(X + swz_off<BV>(16 * rt + li, 16 * c + 4 * g), a);
   };
-  auto rows4 = [](float s) {  // sum over the four lanes of a row
-    s += __shfl_xor(s, 16);
-    return s + __shfl_xor(s, 32);
-  };
   auto sum4 = [](const f32x4& a, const f32x4& b_) {
     return fmaf(a[0], b_[0], fmaf(a[1], b_[1], fmaf(a[2], b_[2], a[3] * b_[3])));
   };
@@ -228,11 +224,11 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
         if (32 * ku + 31 >= 16 * rt)
           mma(dd, sw_frag_tr<BV>(dUt, 16 * c, ku, lane), tri_frag_tr(Xt, rt, ku, lane));
       }
-      const float da = rows4(sum4(dd, d));
+      const float da = row_sum4(sum4(dd, d));
       dd *= ar;
       put(Ut, u, rt, c, li, g);
       put(dDt, dd, rt, c, li, g);
-      const float xs = rows4(sum4(dd, eks)), wk = rows4(sum4(u, wkd));
+      const float xs = row_sum4(sum4(dd, eks)), wk = row_sum4(sum4(u, wkd));
       put(Wt, ws[16 * rt + li] * u, rt, c, li, g);
       put(eDt, -es[16 * rt + li] * dd, rt, c, li, g);
       if (g == 0) {  // one lane per row and tile column: its own place
@@ -315,8 +311,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     mma(acc, ah, bl);
     mma(acc, al, bh_);
   };
-#pragma unroll
-  for (int d = 32; d > 0; d >>= 1) c0 += __shfl_xor(c0, d);
+  c0 = row_sum4(row_sum16(c0));
   if (lane == 0) c0s[w] = c0;
   // rows of Q past the end re-read row 0: cleared before they are read
   if (valid < C) {
@@ -334,7 +329,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     f32x4 qf;
 #pragma unroll
     for (int qq = 0; qq < 4; ++qq) qf[qq] = static_cast<float>(qv[qq]);
-    const float s = rows4(sum4(dQa[i], qf));
+    const float s = row_sum4(sum4(dQa[i], qf));
     if (g == 0) red[dt * C + r] = s;
   }
   fresh();
@@ -451,22 +446,20 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       if (li == 0) msum[(NRT + rr) * C + c + qq] = cs;
     }
     *reinterpret_cast<f32x4*>(dAf + r * CPF + c) = da;
-    s = rows4(s);
-    sm = rows4(sm);
+    s = row_sum4(s);
+    sm = row_sum4(sm);
     if (g == 0) {
       red[jt * C + r] = s;
       msum[jt * C + r] = sm;
     }
   }
   __syncthreads();
-  // da_i += sum_j N_ij, then dbeta and dlambda;  dg;  dG + dG^T as bf16 (over X)
+  // da_i += sum_j N_ij, then dbeta and dlambda, by one wavefront;  dg by another;
+  // dG + dG^T as bf16 (over X)
   if (tid < C) {
-    float s = xw[4][tid] + xw[5][tid], y = ys[tid];
+    float s = xw[4][tid] + xw[5][tid];
 #pragma unroll
-    for (int jt = 0; jt < NRT; ++jt) {
-      s += red[jt * C + tid];
-      y += msum[jt * C + tid] - msum[(NRT + jt) * C + tid];
-    }
+    for (int jt = 0; jt < NRT; ++jt) s += red[jt * C + tid];
     float dl = 0.0f;
     if (tid < valid) {
       const float bt = to_f32(static_cast<const uint16_t*>(b.beta)[row0 + int64_t(tid) * H]);
@@ -476,19 +469,21 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
       static_cast<uint16_t*>(b.dbeta)[row0 + int64_t(tid) * H] = from_f32<uint16_t>(s * da_db);
     }
     dls[tid] = dl;
-    // dg_t = e^{G_C} <dS', S> + sum_{j<t} k_j . Y2_j + sum_{i>=t} y_i  (tid < C: one wavefront)
-    const float wj = xw[2][tid] + xw[3][tid];
-    float before = wj, after = y, all = 0.0f;
+  } else if (tid < 2 * C) {
+    // dg_t = e^{G_C} <dS', S> + sum_{j<t} k_j . Y2_j + sum_{i>=t} y_i: sums of the
+    // tokens before, and, with the tokens in reverse order, from here on
+    const int t = lane, rev = C - 1 - lane;
+    float y = ys[rev];
 #pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const float p = __shfl_up(before, d), z = __shfl_down(after, d);
-      if (tid >= d) before += p;
-      if (tid + d < kWave) after += z;
-    }
+    for (int jt = 0; jt < NRT; ++jt) y += msum[jt * C + rev] - msum[(NRT + jt) * C + rev];
+    const float wj = xw[2][t] + xw[3][t];
+    const float before = wave_scan_dpp(wj), from = wave_scan_dpp(y);
+    float all = 0.0f;
 #pragma unroll
     for (int j = 0; j < NWV; ++j) all += c0s[j];
-    if (tid < valid)
-      static_cast<uint16_t*>(b.dg)[row0 + int64_t(tid) * H] = from_f32<uint16_t>(fmaf(es[C - 1], all, before - wj + after));
+    const float after = __shfl(from, rev);
+    if (t < valid)
+      static_cast<uint16_t*>(b.dg)[row0 + int64_t(t) * H] = from_f32<uint16_t>(fmaf(es[C - 1], all, before - wj + after));
   }
 #pragma unroll
   for (int i = 0; i < C * C / 4 / NTH; ++i) {
