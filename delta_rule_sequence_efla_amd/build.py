@@ -17,7 +17,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libefla.so")
 SOURCES = ["api.hip", "step_kernels.hip", "chunk_bf16.hip", "chunk_bf16_roles.hip", "chunk_bf16_split.hip",
            "chunk_bf16_states.hip", "ut_bf16.hip", "chunk_f32.hip", "bwd.hip", "bwd_bf16_chunk.hip", "seg.hip",
-           "gated_api.hip", "gated_fwd.hip", "gated_step.hip", "gated_bwd.hip", "gated_bwd_bf16.hip", "plan.hip"]
+           "gated_api.hip", "gated_fwd.hip", "gated_step.hip", "gated_blocks.hip", "gated_bwd.hip", "gated_bwd_bf16.hip", "plan.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 CFLAGS = [
@@ -37,6 +37,7 @@ SOURCE_FLAGS = {"chunk_bf16_roles.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "chunk_bf16_states.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "ut_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "bwd_bf16_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+                "gated_blocks.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "gated_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "gated_bwd_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 

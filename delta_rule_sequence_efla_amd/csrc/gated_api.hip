@@ -19,16 +19,18 @@ efla_status check_gated_shape(int B, int H, int Hk, int64_t L, int d_k, int d_v,
 // chunked matrix-core passes for bf16 at their shapes (whatever chunk the caller
 // names: it does not change the result), else the fp32 recurrence.  The latter
 // also where it is the faster of the two, short sequences and few workgroups:
-// one launch against two, but time per token.  Measured (bf16, us, recurrence /
-// chunks; workgroups = seqs H d_v / 16):
-//   d 128,  128 workgroups: L 16  7.3 / 12.4, 48 12.4 / 13.2, 64 14.8 / 13.6
-//   d 128, 1024:            L 8  15.5 / 18.2, 16 19.2 / 18.2, 24 24.1 / 18.5
-//   d 64,   512:            L 16  7.0 / 12.7, 48 12.3 / 13.1, 64 15.1 / 13.4
-//   d 64,  4096:            L 8  31.7 / 46.0, 24 51.2 / 45.8
+// one launch against two, but a longer chain.  Measured (bf16, us, chunks /
+// recurrence; workgroups = seqs H d_v / 16):
+//   d 64,  32 .. 256 workgroups: L 48 13.0 / 7.9, 128 14.3 / 12.5, 160 15.2 / 14.7, 192 15.3 / 16.5
+//   d 64,        512:            L 16 13.6 / 7.2, 48 14.0 / 12.8, 64 14.3 / 15.7
+//   d 128, 64 .. 256:            L 48 14.0 / 9.3, 96 15.8 / 13.4, 128 16.0 / 16.3
+//   d 128,       512:            L 16 14.0 / 10.4, 32 14.3 / 14.3, 48 14.8 / 18.8
+//   d 128,      1024:            L 8 19.1 / 15.6, 16 19.2 / 19.2, 32 19.6 / 27.4
 bool gated_chunked(int64_t seqs, int H, int64_t L, int d_k, int d_v, efla_dtype dt) {
   if (dt != EFLA_BF16 || !efla::gated_chunk_supported(d_k, d_v)) return false;
   const int64_t wgs = seqs * H * (d_v / 16);
-  return L > 48 || wgs > 4096 || L * wgs * d_k > 1500000;
+  if (wgs <= 256) return L > (d_k == 64 ? 176 : 112);
+  return L > 48 || wgs > 4096 || L * wgs * d_k > 2000000;
 }
 
 template <typename F>

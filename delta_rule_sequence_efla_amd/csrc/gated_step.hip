@@ -164,8 +164,9 @@ template hipError_t launch_gated_step<uint16_t>(const GatedStep&, hipStream_t);
 // threads a token: they load two blocks ahead into registers, form a, e and the
 // products of keys and queries among themselves, widen into one of two LDS
 // buffers, and store the outputs of the block before.
-// 777 tokens, 16 heads, d 64, fp32: 142 us token by token with the staging in
-// the same wavefronts, 111 us by pairs, 82 us with wavefronts for each.
+// 2 x 777 tokens, 8 heads, d 64, fp32: 142 us token by token with the staging in
+// the same wavefronts, 111 us by pairs, 82 us with wavefronts for each (and 52
+// by 16 tokens, gated_blocks.hip, which takes the longer sequences).
 // With `states`, the state before every C-th token is stored, [chunk
 // slot][d_k][d_v] fp32 (the backward's chunk starts; C % 16 == 0).
 template <typename T, int N> struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Piece { T e[N]; };
@@ -371,6 +372,16 @@ hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipSt
   const int64_t units = int64_t(a.cu == nullptr ? a.B : a.N) * a.H;
   const int64_t nwg = units * (a.DV / 16);
   if (nwg == 0) return hipSuccess;
+  // By 16 tokens (gated_blocks.hip) the chain is shorter, but it starts four
+  // blocks late and fewer of its workgroups share a compute unit.  Measured (fp32,
+  // us, pairs / blocks):
+  //   d 64,   256 workgroups: 16 tokens 5.8 / 6.0, 32 7.5 / 7.1, 128 17.7 / 13.0, 512 57 / 38
+  //   d 64,  1024:            32 18.3 / 24.7, 128 49.1 / 50.4, 512 160 / 142
+  //   d 128,   64:            16 7.2 / 6.5, 32 9.6 / 8.0, 128 23.6 / 16.8, 512 80 / 52
+  //   d 128,  512:            32 14.7 / 16.1, 64 24.1 / 25.1, 128 38.8 / 36.6, 512 126 / 105
+  //   d 128, 8192:            32 155 / 231, 128 508 / 525, 512 1963 / 1613
+  const int64_t tokens = a.cu == nullptr ? a.L : a.L / a.N;
+  if (a.DK >= 64 && tokens >= (nwg <= 256 ? 32 : 160)) return launch_gated_blocks<T>(a, states, C, s);
   const int NC = int((a.L + C - 1) / C);
   const dim3 grid{unsigned(nwg)}, wg{2 * kThreads};
   switch (a.DK) {

@@ -161,6 +161,10 @@ struct GatedFwd {
 };
 // Token by token in fp32, any d_k / d_v; o may be null; states (dense batches):
 // the state before every C-th token, [chunk slot][d_k][d_v].
+// launch_gated_blocks (gated_blocks.hip): 16 tokens at a time, d_k 64 or 128; the
+// recurrence hands long sequences of those on to it.
+template <typename T>
+hipError_t launch_gated_blocks(const GatedFwd& a, float* states, int C, hipStream_t s);
 template <typename T>
 hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipStream_t s);
 

@@ -67,7 +67,9 @@ def test_step_reset_takes_a_finite_state_to_zero(dt):
 
 # L at which the forward changes kernels (d 64 and 128, few and many workgroups), and the backward
 @pytest.mark.parametrize("d", [64, 128])
-@pytest.mark.parametrize("B,L", [(1, 15), (1, 16), (1, 17), (1, 48), (1, 49), (1, 64), (1, 65), (70, 8), (70, 24), (130, 3)])
+@pytest.mark.parametrize("B,L", [(1, 15), (1, 16), (1, 17), (1, 31), (1, 32), (1, 33), (1, 48), (1, 65),
+                                 (1, 112), (1, 113), (1, 176), (1, 177), (20, 1), (20, 47), (20, 49), (20, 64), (20, 65), (20, 127),
+                                 (70, 8), (70, 24), (130, 3)])
 def test_where_kernels_change(B, L, d):
     x = G.make(B, L, 4, 2, d, d, BF, seed=L)
     a = dev(x)
@@ -81,6 +83,22 @@ def test_where_kernels_change(B, L, d):
     got = efla.efla_gated_chunk_bwd(*args, do.cuda(), a["s0"])
     for name, p, r in zip(GRADS, got, grads_ref(x, do, None, "exact")):
         assert G.rel(p, r) <= G.tol_grad(BF, L, d), name
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,L", [(1, 31), (1, 32), (2, 47), (1, 333), (30, 100), (30, 161), (12, 200)])
+def test_fp32_where_kernels_change(B, L, d):
+    x = G.make(B, L, 6, 3, d, d, F32, seed=L)
+    a = dev(x)
+    args = [a[n] for n in G.NAMES]
+    o, S = efla.efla_gated_chunk_fwd(*args, a["s0"], rule="euler")
+    wo, wS = G.forward_ref(*G.wide(x), x["s0"].double(), "euler")
+    assert G.rel(o, wo) <= G.tol_o(F32, L, d) and G.rel(S, wS) <= G.tol_s(F32, L, d)
+    if B == 1:
+        do = torch.randn(B, L, 6, d, generator=torch.Generator().manual_seed(1))
+        got = efla.efla_gated_chunk_bwd(*args, do.cuda(), a["s0"], chunk=16, rule="euler")
+        for name, p, r in zip(GRADS, got, grads_ref(x, do, None, "euler")):
+            assert G.rel(p, r) <= G.tol_grad(F32, L, d), name
 
 
 @pytest.mark.parametrize("chunk", [16, 32, 64])
