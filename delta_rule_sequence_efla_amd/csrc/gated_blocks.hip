@@ -154,10 +154,11 @@ __global__ __launch_bounds__(13 * kWave) void gated_blocks_kernel(GatedFwd a, fl
     // Loads and stores to the LDS run whether the block exists or not, tokens past
     // the end reading the last one: behind a branch the compiler could not count
     // the loads in flight and would wait for all of them in every period.
+    const int64_t k_stride = int64_t(a.Hk) * DK, k_block = TB * k_stride, h_block = int64_t(TB) * H;
     auto load = [&](Regs& x, int m) {
       const int left = int(len - int64_t(m) * TB) - 1;  // the block's last token
       const int t = tok < left ? tok : left;            // may lie before the block
-      const int64_t kt = int64_t(m) * (TB * a.Hk * DK) + t * (a.Hk * DK), ht = int64_t(m) * (TB * H) + t * H;
+      const int64_t kt = m * k_block + t * k_stride, ht = m * h_block + int64_t(t) * H;
       x.k = *reinterpret_cast<const Row<T, NK>*>(k + kt);
       x.q = *reinterpret_cast<const Row<T, NK>*>(q + kt);
       x.v = v[ht * DV];

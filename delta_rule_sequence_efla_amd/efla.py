@@ -582,8 +582,9 @@ def _call(fn, index: int, where: str, *args) -> None:
         raise EflaError(status, where)
 
 
-def _gated_shapes(q, k, v, beta, g, lead: int):
-    """(device index, H, Hk, dk, dv) of a gated call's inputs, checked.  (A decode
+def _gated_shapes(q, k, v, beta, g, lead: int, *others):
+    """(device index, H, Hk, dk, dv) of a gated call's inputs, checked; others:
+    the call's further tensors, of which only the place is checked.  (A decode
     call is bound by the host: its checks take the cheapest form of each test.)"""
     dt, ks, vs = q.dtype, k.shape, v.shape
     rows = vs[:-1]
@@ -597,7 +598,7 @@ def _gated_shapes(q, k, v, beta, g, lead: int):
     if Hk < 1 or H % Hk:
         raise ValueError(f"the {H} value heads must be a multiple of the {Hk} query and key heads")
     index = q.get_device()
-    _same(index, q, k, v, beta, g)
+    _same(index, q, k, v, beta, g, *others)
     return index, H, Hk, ks[-1], vs[-1]
 
 
@@ -637,9 +638,8 @@ def efla_gated_chunk_fwd(q, k, v, beta, g, s0=None, chunk: int = 64, o=None, s_f
     """Gated forward pass over a dense batch: q, k [B,L,Hk,dk], v [B,L,H,dv],
     beta [B,L,H] in one type, g float32 [B,L,H].  Returns (o [B,L,H,dv] in q's
     dtype, S_L float32 [B,H,dk,dv] or None)."""
-    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
+    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2, s0, o, s_final, workspace)
     B, L = k.shape[:2]
-    _same(index, s0, o, s_final, workspace)
     _shaped(s0, (B, H, dk, dv), "s0", _f32)
     _shaped(o, v.shape, "o", q.dtype)
     _shaped(s_final, (B, H, dk, dv), "s_final", _f32)
@@ -651,8 +651,9 @@ def efla_gated_chunk_fwd(q, k, v, beta, g, s0=None, chunk: int = 64, o=None, s_f
     if workspace is None:
         n = _gated_workspace("efla_gated_chunk_fwd", B, H, Hk, L, dk, dv, chunk, code)
         workspace = q.new_empty(n, dtype=torch.uint8) if n else None
-    _call(lib().efla_gated_chunk_fwd, index, "efla_gated_chunk_fwd", _at(q), _at(k), _at(v), _at(beta), _at(g), _at(s0),
-          _at(o), _at(s_final), B, H, Hk, L, dk, dv, chunk, code, r, _at(workspace), _nbytes(workspace))
+    _call(lib().efla_gated_chunk_fwd, index, "efla_gated_chunk_fwd", q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          beta.data_ptr(), g.data_ptr(), _at(s0), _at(o), _at(s_final), B, H, Hk, L, dk, dv, chunk, code, r,
+          _at(workspace), _nbytes(workspace))
     return o, s_final
 
 
@@ -668,9 +669,8 @@ def efla_gated_chunk_fwd_varlen(q, k, v, beta, g, cu_seqlens, s0=None, chunk: in
     sequence i starts from and ends in (an entry outside the pool: from zero,
     final state not written).  order: a schedule as efla_pack_plan returns it.
     Returns (o shaped like v, s_final)."""
-    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1)
+    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1, s0, o, s_final, workspace, cu_seqlens, slots, order)
     T = k.shape[0]
-    _same(index, s0, o, s_final, workspace, cu_seqlens, slots, order)
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
         raise ValueError("cu_seqlens must be a 1-D int32 tensor of N+1 offsets")
     N = cu_seqlens.numel() - 1
@@ -694,9 +694,9 @@ def efla_gated_chunk_fwd_varlen(q, k, v, beta, g, cu_seqlens, s0=None, chunk: in
     if workspace is None:
         n = _gated_workspace("efla_gated_chunk_fwd_varlen", N, H, Hk, T, dk, dv, chunk, code)
         workspace = q.new_empty(n, dtype=torch.uint8) if n else None
-    _call(lib().efla_gated_chunk_fwd_varlen, index, "efla_gated_chunk_fwd_varlen", _at(q), _at(k), _at(v), _at(beta),
-          _at(g), _at(cu_seqlens), _at(slots), _at(order), N, P, _at(s0), _at(o), _at(s_final), H, Hk, T, dk, dv, chunk,
-          code, r, _at(workspace), _nbytes(workspace))
+    _call(lib().efla_gated_chunk_fwd_varlen, index, "efla_gated_chunk_fwd_varlen", q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          beta.data_ptr(), g.data_ptr(), _at(cu_seqlens), _at(slots), _at(order), N, P, _at(s0), _at(o), _at(s_final), H,
+          Hk, T, dk, dv, chunk, code, r, _at(workspace), _nbytes(workspace))
     return o, s_final
 
 
@@ -710,9 +710,8 @@ def efla_gated_chunk_bwd(q, k, v, beta, g, d_o, s0=None, ds_final=None, chunk: i
     = ds_final (None: zero).  Returns (dq, dk, dv, dbeta, dg, ds0): the first
     five in q's dtype (dq and dk summed over the value heads that share a
     head), ds0 float32 [B,H,dk,dv] or None when want_ds0 is False."""
-    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2)
+    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2, d_o, s0, ds_final, workspace)
     B, L = k.shape[:2]
-    _same(index, d_o, s0, ds_final, workspace)
     _shaped(d_o, v.shape, "d_o", q.dtype)
     _shaped(s0, (B, H, dk, dv), "s0", _f32)
     _shaped(ds_final, (B, H, dk, dv), "ds_final", _f32)
@@ -722,9 +721,9 @@ def efla_gated_chunk_bwd(q, k, v, beta, g, d_o, s0=None, ds_final=None, chunk: i
     if workspace is None:
         n = _gated_workspace("efla_gated_chunk_bwd", B, H, Hk, L, dk, dv, chunk, code)
         workspace = q.new_empty(n, dtype=torch.uint8) if n else None
-    _call(lib().efla_gated_chunk_bwd, index, "efla_gated_chunk_bwd", _at(q), _at(k), _at(v), _at(beta), _at(g), _at(s0),
-          _at(d_o), _at(ds_final), _at(gq), _at(gk), _at(gv), _at(gb), _at(gg), _at(gs0), B, H, Hk, L, dk, dv, chunk,
-          code, r, _at(workspace), _nbytes(workspace))
+    _call(lib().efla_gated_chunk_bwd, index, "efla_gated_chunk_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(),
+          beta.data_ptr(), g.data_ptr(), _at(s0), _at(d_o), _at(ds_final), _at(gq), _at(gk), _at(gv), _at(gb), _at(gg),
+          _at(gs0), B, H, Hk, L, dk, dv, chunk, code, r, _at(workspace), _nbytes(workspace))
     return gq, gk, gv, gb, gg, gs0
 
 
@@ -733,18 +732,18 @@ def efla_gated_step(q, k, v, beta, g, state, slots=None, o=None, rule: str = "ex
     q, k [N,Hk,dk], v [N,H,dv], beta [N,H] in one type, g float32 [N,H].  Row n
     updates state slots[n] (int32 [N]; None: state n); a slot outside the pool
     skips the row and leaves its row of o as it was.  Returns o [N,H,dv]."""
-    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1)
+    index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1, state, slots, o)
     N = k.shape[0]
-    _same(index, state, slots, o)
     P = N if slots is None or state.dim() != 4 else state.shape[0]
     if state.shape != (P, H, dk, dv) or state.dtype is not _f32:
         raise ValueError("state must be float32 [P,H,dk,dv], with P = N where no slots are given")
     _shaped(slots, (N,), "slots", torch.int32)
-    _shaped(o, v.shape, "o", q.dtype)
     if o is None:
         o = torch.empty_like(v)
-    _call(lib().efla_gated_step, index, "efla_gated_step", _at(q), _at(k), _at(v), _at(beta), _at(g), _at(state),
-          _at(slots), _at(o), N, P, H, Hk, dk, dv, _code(q.dtype), _rule(rule))
+    else:
+        _shaped(o, v.shape, "o", q.dtype)
+    _call(lib().efla_gated_step, index, "efla_gated_step", q.data_ptr(), k.data_ptr(), v.data_ptr(), beta.data_ptr(),
+          g.data_ptr(), state.data_ptr(), _at(slots), o.data_ptr(), N, P, H, Hk, dk, dv, _code(q.dtype), _rule(rule))
     return o
 
 

@@ -351,6 +351,13 @@ efla_status efla_step_rule(const void *q, const void *k, const void *v, const vo
  *     that feed a state take each float32 operand as the sum of two bf16
  *     values (16 significant bits), so a state is good to about 1e-5 whatever
  *     the inputs' type; products that only feed o round such operands once.
+ *   - chunk is checked as above and bounds nothing else: the kernels take the
+ *     chunks that suit them (64 tokens for bf16, 16 in float32), and results
+ *     agree for every value.  Small forwards and float32 ones need no workspace.
+ *   - A NaN or an infinity in a token's row reaches its sequence's outputs from
+ *     the start of its chunk on, not only from the token on; never another
+ *     sequence's.
+ *   - Sequences of at most 16 tokens are differentiated in float32 throughout.
  *   - Layouts, alignment, streams, workspaces and errors as above otherwise.
  *
  * efla_gated_chunk_fwd -- dense batch.  q, k [B, L, Hk, d_k], v, o
