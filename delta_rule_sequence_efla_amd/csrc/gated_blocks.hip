@@ -19,11 +19,11 @@
 // Products use the accumulator layout on both sides: of the 16x16x4 products that
 // sum over 16 values, step r takes values 4 g + r, so rows 4 g .. 4 g + 3 of an
 // accumulator are an operand as they stand.
-// 2 x 777 tokens of 8 heads, d 64: 52 us, 1.0 us a block (token pairs,
+// 2 x 777 tokens of 8 heads, d 64: 49 us, 0.95 us a block (token pairs,
 // gated_step.hip: 83 us).  Bound by issue and latency about evenly: the chain, X's
 // two halves, P's first and O each take 2000 to 2400 cycles of a block's 2450,
 // thirteen wavefronts on four SIMDs.  X by all 16 rows of substitution and the
-// gates' factors in the same wavefront: 81 us; factors moved to P's: 65 to 52.
+// gates' factors in the same wavefront: 81 us; factors moved to P's: 65 to 53.
 #include "gated.h"
 #include "launchers.h"
 #include "lds_ring.h"
@@ -65,6 +65,11 @@ __global__ __launch_bounds__(13 * kWave) void gated_blocks_kernel(GatedFwd a, fl
   const int hk = h / (H / a.Hk);
   const int role = wave_id(), lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
   const int nb = int((len + TB - 1) / TB);
+  // Three or four wavefronts share a SIMD; the longest path issues first: X, then
+  // S, then P and O, the loads last (all alike: 52.8 us for 49.0).
+  if (role == 8 || role == 9) __builtin_amdgcn_s_setprio(3);
+  else if (role < 4) __builtin_amdgcn_s_setprio(2);
+  else if (role >= 10) __builtin_amdgcn_s_setprio(1);
   auto sync = [&]() {
     wait_lgkm0();
     barrier_nowait();

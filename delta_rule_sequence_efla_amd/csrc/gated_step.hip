@@ -165,7 +165,7 @@ template hipError_t launch_gated_step<uint16_t>(const GatedStep&, hipStream_t);
 // products of keys and queries among themselves, widen into one of two LDS
 // buffers, and store the outputs of the block before.
 // 2 x 777 tokens, 8 heads, d 64, fp32: 142 us token by token with the staging in
-// the same wavefronts, 111 us by pairs, 82 us with wavefronts for each (and 52
+// the same wavefronts, 111 us by pairs, 82 us with wavefronts for each (and 49
 // by 16 tokens, gated_blocks.hip, which takes the longer sequences).
 // With `states`, the state before every C-th token is stored, [chunk
 // slot][d_k][d_v] fp32 (the backward's chunk starts; C % 16 == 0).
