@@ -108,7 +108,7 @@ efla_status efla_gated_chunk_fwd_varlen(const void* q, const void* k, const void
 size_t efla_gated_chunk_bwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
                                            efla_dtype dtype) {
   if (check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || L == 0) return 0;
-  return efla::gated_bwd_workspace(B, H, Hk, L, d_k, d_v, chunk, elem_bytes(dtype));
+  return efla::gated_bwd_workspace(B, H, Hk, L, d_k, d_v, elem_bytes(dtype));
 }
 
 efla_status efla_gated_chunk_bwd(const void* q, const void* k, const void* v, const void* beta, const float* g,
@@ -133,7 +133,7 @@ efla_status efla_gated_chunk_bwd(const void* q, const void* k, const void* v, co
   const efla::GatedBwd b{q, k, v, beta, d_o, g, s0, ds_final, dq, dk, dv, dbeta, dg, ds0, B, H, Hk, d_k, d_v,
                          int(rule), L};
   return by_type(dtype, [&](auto t) {
-    return efla::launch_gated_bwd<decltype(t)>(b, chunk, workspace, static_cast<hipStream_t>(stream));
+    return efla::launch_gated_bwd<decltype(t)>(b, workspace, static_cast<hipStream_t>(stream));
   });
 }
 

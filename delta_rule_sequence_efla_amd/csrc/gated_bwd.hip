@@ -25,12 +25,16 @@ constexpr int64_t kShort = 16;
 static bool gated_bwd_fast(int64_t L, int DK, int DV, size_t esz) {
   return esz == 2 && L > kShort && gated_chunk_supported(DK, DV);
 }
-// chunk of the fp32 kernels (the result does not depend on it)
-static int fp32_chunk(int64_t L, int C) { return L <= kShort ? 16 : C; }
+// Chunk of the fp32 kernels: 32 tokens.  A workgroup's products with S cost as
+// much a token at any chunk, so half the chunk is twice the workgroups at half the
+// time each; at 16 the chains over the chunks outweigh it.  Measured, 16 / 32 / 64
+// (us, float32): 8 heads d 64, 200 tokens 75 / 61 / 91, 3 x 1100 323 / 210 / 246;
+// d 128, 200 tokens 118 / 97 / 156, 3 x 1100 633 / 392 / 421.
+static int fp32_chunk(int64_t L) { return L <= kShort ? 16 : 32; }
 
-static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t esz) {
+static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, int DV, size_t esz) {
   const bool fast = gated_bwd_fast(L, DK, DV, esz);
-  C = fast ? 64 : fp32_chunk(L, C);
+  const int C = fast ? 64 : fp32_chunk(L);
   const size_t slots = size_t(B) * H * ((L + C - 1) / C);
   size_t at = 0;
   auto region = [&](size_t bytes) {
@@ -61,8 +65,8 @@ static GatedBwdLayout gated_bwd_layout(int B, int H, int Hk, int64_t L, int DK, 
   return w;
 }
 
-size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t esz) {
-  return gated_bwd_layout(B, H, Hk, L, DK, DV, C, esz).total;
+size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, size_t esz) {
+  return gated_bwd_layout(B, H, Hk, L, DK, DV, esz).total;
 }
 
 // The forward's inputs, for the backward's recomputation.
@@ -95,7 +99,7 @@ static hipError_t sum_heads(const GatedBwd& b, const float* dqh, const float* dk
 }
 
 static hipError_t gated_bwd_bf16(const GatedBwd& b, unsigned char* ws, hipStream_t s) {
-  const GatedBwdLayout lay = gated_bwd_layout(b.B, b.H, b.Hk, b.L, b.DK, b.DV, 64, 2);
+  const GatedBwdLayout lay = gated_bwd_layout(b.B, b.H, b.Hk, b.L, b.DK, b.DV, 2);
   auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
   auto u = [&](size_t off) { return reinterpret_cast<uint16_t*>(ws + off); };
   const GatedFwd a = forward_of(b);
@@ -114,7 +118,7 @@ template <typename T, int DK, int C>
 static hipError_t gated_bwd_impl(const GatedBwd& b, unsigned char* ws, hipStream_t s) {
   const int NC = int((b.L + C - 1) / C);
   const int64_t bh = int64_t(b.B) * b.H, slots = bh * NC;
-  const GatedBwdLayout lay = gated_bwd_layout(b.B, b.H, b.Hk, b.L, DK, b.DV, C, sizeof(T));
+  const GatedBwdLayout lay = gated_bwd_layout(b.B, b.H, b.Hk, b.L, DK, b.DV, sizeof(T));
   auto f = [&](size_t off) { return reinterpret_cast<float*>(ws + off); };
   if (slots > 0) {
     hipLaunchKernelGGL((gated_ut_kernel<T, DK, C>), dim3(unsigned(slots)), dim3(kThreads), 0, s, b, f(lay.t), f(lay.x),
@@ -135,29 +139,23 @@ static hipError_t gated_bwd_impl(const GatedBwd& b, unsigned char* ws, hipStream
 }
 
 template <typename T, int DK>
-static hipError_t gated_bwd_c(const GatedBwd& b, int C, unsigned char* ws, hipStream_t s) {
-  switch (C) {
-    case 16: return gated_bwd_impl<T, DK, 16>(b, ws, s);
-    case 32: return gated_bwd_impl<T, DK, 32>(b, ws, s);
-    case 64: return gated_bwd_impl<T, DK, 64>(b, ws, s);
-  }
-  return hipErrorInvalidValue;
+static hipError_t gated_bwd_c(const GatedBwd& b, unsigned char* ws, hipStream_t s) {
+  return fp32_chunk(b.L) == 16 ? gated_bwd_impl<T, DK, 16>(b, ws, s) : gated_bwd_impl<T, DK, 32>(b, ws, s);
 }
 
 template <typename T>
-hipError_t launch_gated_bwd(const GatedBwd& b, int C, void* workspace, hipStream_t s) {
+hipError_t launch_gated_bwd(const GatedBwd& b, void* workspace, hipStream_t s) {
   auto* ws = static_cast<unsigned char*>(workspace);
   if (gated_bwd_fast(b.L, b.DK, b.DV, sizeof(T))) return gated_bwd_bf16(b, ws, s);
-  C = fp32_chunk(b.L, C);
   switch (b.DK) {
-    case 16: return gated_bwd_c<T, 16>(b, C, ws, s);
-    case 32: return gated_bwd_c<T, 32>(b, C, ws, s);
-    case 64: return gated_bwd_c<T, 64>(b, C, ws, s);
-    case 128: return gated_bwd_c<T, 128>(b, C, ws, s);
+    case 16: return gated_bwd_c<T, 16>(b, ws, s);
+    case 32: return gated_bwd_c<T, 32>(b, ws, s);
+    case 64: return gated_bwd_c<T, 64>(b, ws, s);
+    case 128: return gated_bwd_c<T, 128>(b, ws, s);
   }
   return hipErrorInvalidValue;
 }
-template hipError_t launch_gated_bwd<float>(const GatedBwd&, int, void*, hipStream_t);
-template hipError_t launch_gated_bwd<uint16_t>(const GatedBwd&, int, void*, hipStream_t);
+template hipError_t launch_gated_bwd<float>(const GatedBwd&, void*, hipStream_t);
+template hipError_t launch_gated_bwd<uint16_t>(const GatedBwd&, void*, hipStream_t);
 
 }  // namespace efla

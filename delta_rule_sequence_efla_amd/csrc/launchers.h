@@ -191,9 +191,9 @@ struct GatedBwd {
   int B, H, Hk, DK, DV, rule;
   int64_t L;
 };
-size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, int C, size_t esz);
+size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, size_t esz);
 template <typename T>
-hipError_t launch_gated_bwd(const GatedBwd& b, int C, void* ws, hipStream_t s);
+hipError_t launch_gated_bwd(const GatedBwd& b, void* ws, hipStream_t s);
 // The backward's passes for bf16 inputs at the chunked forward's shapes: the
 // reverse pass over the chunks (gated_reverse.h), dS' of every chunk as
 // [slots][DV][DK] bf16, and the per-chunk gradients (gated_bwd_chunk.h); dqh,

@@ -352,8 +352,8 @@ efla_status efla_step_rule(const void *q, const void *k, const void *v, const vo
  *     values (16 significant bits), so a state is good to about 1e-5 whatever
  *     the inputs' type; products that only feed o round such operands once.
  *   - chunk is checked as above and bounds nothing else: the kernels take the
- *     chunks that suit them (64 tokens for bf16, 16 in float32), and results
- *     agree for every value.  Small forwards and float32 ones need no workspace.
+ *     chunks that suit them (64 tokens for bf16, 16 or 32 in float32), and
+ *     results agree for every value.  Small forwards and float32 ones need no workspace.
  *   - A NaN or an infinity in a token's row reaches its sequence's outputs from
  *     the start of its chunk on, not only from the token on; never another
  *     sequence's.
