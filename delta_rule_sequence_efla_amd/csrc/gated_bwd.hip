@@ -105,8 +105,7 @@ static hipError_t gated_bwd_bf16(const GatedBwd& b, unsigned char* ws, hipStream
   const GatedFwd a = forward_of(b);
   const bool shared = b.Hk < b.H;
   hipError_t e = launch_gated_ut_bwd(a, u(lay.xfr), f(lay.gc), u(lay.p), u(lay.qe), s);
-  if (e == hipSuccess) e = launch_gated_states(a, u(lay.xfr), f(lay.gc), u(lay.s), s);
-  if (e == hipSuccess) e = launch_gated_reverse(b, u(lay.xfr), u(lay.qe), f(lay.gc), u(lay.ds), s);
+  if (e == hipSuccess) e = launch_gated_chains(a, b, u(lay.xfr), u(lay.qe), f(lay.gc), u(lay.s), u(lay.ds), s);
   if (e == hipSuccess)
     e = launch_gated_bwd_chunk(b, u(lay.xfr), u(lay.p), f(lay.gc), u(lay.s), u(lay.ds),
                                shared ? f(lay.dqh) : nullptr, shared ? f(lay.dkh) : nullptr, s);

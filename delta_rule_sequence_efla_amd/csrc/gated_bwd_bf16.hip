@@ -8,18 +8,19 @@
 namespace efla {
 
 template <int DK>
-static hipError_t reverse_impl(const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe, const float* gws,
-                               uint16_t* dstatesT, hipStream_t s) {
+static hipError_t chains_impl(const GatedFwd& a, const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe,
+                              const float* gws, uint16_t* statesT, uint16_t* dstatesT, hipStream_t s) {
   const int NC = int((b.L + 63) / 64), NVB = b.DV / 32;
   const int64_t bh = int64_t(b.B) * b.H;
-  hipLaunchKernelGGL((gated_reverse_kernel<DK>), dim3(unsigned(bh * NVB)), dim3(GatedReverseShape<DK>::THREADS), 0, s, b,
-                     qe, xfr, gws, dstatesT, NC, NVB, bh % 8 == 0 ? 1 : 0);
+  hipLaunchKernelGGL((gated_chains_kernel<DK>), dim3(unsigned(2 * bh * NVB)), dim3(GatedSplitShape<DK>::STATE_THREADS),
+                     0, s, a, b, qe, xfr, gws, statesT, dstatesT, NC, NVB, bh % 8 == 0 ? 1 : 0);
   return hipGetLastError();
 }
 
-hipError_t launch_gated_reverse(const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe, const float* gws,
-                                uint16_t* dstatesT, hipStream_t s) {
-  return b.DK == 64 ? reverse_impl<64>(b, xfr, qe, gws, dstatesT, s) : reverse_impl<128>(b, xfr, qe, gws, dstatesT, s);
+hipError_t launch_gated_chains(const GatedFwd& a, const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe,
+                               const float* gws, uint16_t* statesT, uint16_t* dstatesT, hipStream_t s) {
+  return b.DK == 64 ? chains_impl<64>(a, b, xfr, qe, gws, statesT, dstatesT, s)
+                    : chains_impl<128>(a, b, xfr, qe, gws, statesT, dstatesT, s);
 }
 
 template <int DK, bool SHARED>

@@ -29,14 +29,13 @@ hipError_t ut_impl(const GatedFwd& a, uint16_t* xfr, float* gws, const GatedUtBw
   return hipGetLastError();
 }
 
-template <int DK, bool OUT>
-hipError_t split_impl(const GatedFwd& a, const uint16_t* xfr, const float* gws, const int32_t* order,
-                      uint16_t* statesT, hipStream_t s) {
+template <int DK>
+hipError_t split_impl(const GatedFwd& a, const uint16_t* xfr, const float* gws, const int32_t* order, hipStream_t s) {
   const int NC = a.cu == nullptr ? int((a.L + kGatedChunk - 1) / kGatedChunk) : int(a.L / kGatedChunk) + a.N;
   const int64_t bh = int64_t(a.cu == nullptr ? a.B : a.N) * a.H;
   const int NVB = a.DV / 32;
-  hipLaunchKernelGGL((gated_split_kernel<DK, OUT>), dim3(unsigned(bh * NVB)), dim3(OUT ? GatedSplitShape<DK>::THREADS : GatedSplitShape<DK>::STATE_THREADS), 0, s,
-                     a, xfr, gws, order, NC, NVB, bh % 8 == 0 ? 1 : 0, statesT);
+  hipLaunchKernelGGL((gated_split_kernel<DK>), dim3(unsigned(bh * NVB)), dim3(GatedSplitShape<DK>::THREADS), 0, s, a,
+                     xfr, gws, order, NC, NVB, bh % 8 == 0 ? 1 : 0);
   return hipGetLastError();
 }
 }  // namespace
@@ -58,12 +57,6 @@ hipError_t launch_gated_ut_bwd(const GatedFwd& a, uint16_t* xfr, float* gws, uin
   return a.DK == 64 ? ut_impl<64, true>(a, xfr, gws, b, nullptr, s) : ut_impl<128, true>(a, xfr, gws, b, nullptr, s);
 }
 
-hipError_t launch_gated_states(const GatedFwd& a, const uint16_t* xfr, const float* gws, uint16_t* statesT,
-                               hipStream_t s) {
-  return a.DK == 64 ? split_impl<64, false>(a, xfr, gws, nullptr, statesT, s)
-                    : split_impl<128, false>(a, xfr, gws, nullptr, statesT, s);
-}
-
 hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s) {
   const bool packed = a.cu != nullptr;
   const GatedFwdLayout lay = gated_fwd_layout(a.B, a.N, a.H, a.L, packed);
@@ -76,7 +69,7 @@ hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s)
   const hipError_t e = a.DK == 64 ? ut_impl<64, false>(a, xfr, gws, none, mine, s) : ut_impl<128, false>(a, xfr, gws, none, mine, s);
   if (e != hipSuccess) return e;
   const int32_t* order = mine != nullptr ? mine : a.order;
-  return a.DK == 64 ? split_impl<64, true>(a, xfr, gws, order, nullptr, s) : split_impl<128, true>(a, xfr, gws, order, nullptr, s);
+  return a.DK == 64 ? split_impl<64>(a, xfr, gws, order, s) : split_impl<128>(a, xfr, gws, order, s);
 }
 
 }  // namespace efla

@@ -21,6 +21,7 @@
 
 #include "gated.h"
 #include "gated_ut.h"
+#include "gated_split.h"
 #include "lds_ring.h"
 
 namespace efla {
@@ -42,23 +43,31 @@ struct GatedReverseShape {
   static constexpr int kY0 = 0, kS0 = 2, kDma = 2 + NSW, NWAVES = 3 + NSW, THREADS = NWAVES * kWave;
 };
 
-// dense batch; NVB = DV / BV workgroups per (b, h).
 template <int DK>
-__global__ __launch_bounds__((GatedReverseShape<DK>::THREADS)) void gated_reverse_kernel(
-    GatedBwd b, const uint16_t* __restrict__ qe, const uint16_t* __restrict__ xfr, const float* __restrict__ gws,
-    uint16_t* __restrict__ dstatesT, int NC, int NVB, int remap) {
+struct GatedReverseLds {
+  using S = GatedReverseShape<DK>;
+  alignas(1024) uint16_t ring[3 * S::SLOT];
+  alignas(16) bf16x8 bS_buf[S::NT][S::NKU_D][kWave];  // dS' as operand fragments
+  alignas(16) bf16x8 bF_buf[S::NT][S::NKU_C][kWave];  // -F as operand fragments
+};
+
+// dense batch; workgroup x of NVB = DV / BV per (b, h).
+template <int DK>
+__device__ __forceinline__ void gated_reverse_run(GatedReverseLds<DK>& lds, const GatedBwd& b, const int x,
+                                                  const uint16_t* __restrict__ qe, const uint16_t* __restrict__ xfr,
+                                                  const float* __restrict__ gws, uint16_t* __restrict__ dstatesT,
+                                                  int NC, int NVB, int remap) {
   using S = GatedReverseShape<DK>;
   constexpr int C = S::C, BV = S::BV, NT = S::NT, NRT = S::NRT, NKU_D = S::NKU_D, NKU_C = S::NKU_C;
-  __shared__ __align__(1024) uint16_t ring[3 * S::SLOT];
+  uint16_t* const ring = lds.ring;
   uint16_t* const slot0 = ring;
   uint16_t* const slot1 = ring + S::SLOT;
   uint16_t* const slot2 = ring + 2 * S::SLOT;
-  __shared__ __align__(16) bf16x8 bS_buf[NT][NKU_D][kWave];  // dS' as operand fragments
-  __shared__ __align__(16) bf16x8 bF_buf[NT][NKU_C][kWave];  // -F as operand fragments
+  auto& bS_buf = lds.bS_buf;
+  auto& bF_buf = lds.bF_buf;
 
   const auto* k = static_cast<const uint16_t*>(b.k);
   const auto* dout = static_cast<const uint16_t*>(b.d_o);
-  const int x = blockIdx.x;
   int bh, vb;
   if (remap) {  // all value blocks of one (b, h) on one XCD (same blockIdx % 8)
     const int slot = x >> 3;
@@ -298,6 +307,31 @@ __global__ __launch_bounds__((GatedReverseShape<DK>::THREADS)) void gated_revers
             b.ds0[(int64_t(bh) * DK + key_phys(16 * (2 * sw + d) + 4 * g + qq)) * DV + col0 + 16 * c + li] =
                 St[d][c][qq];
     }
+  }
+}
+
+// The reverse pass and the chunks' start states (gated_split.h), which do not need
+// each other, in one launch: the first half of the workgroups runs the one, the
+// second the other.  Where neither fills the GPU they run side by side (8 heads
+// of 515 tokens, d 64: two launches took 11.0 and 8.7 us); where both do (256
+// workgroups each at the 340M layer) they follow each other as before.
+template <int DK>
+union GatedChainsLds {
+  GatedSplitLds<DK> states;
+  GatedReverseLds<DK> reverse;
+};
+template <int DK>
+__global__ __launch_bounds__((GatedSplitShape<DK>::STATE_THREADS)) void gated_chains_kernel(
+    GatedFwd a, GatedBwd b, const uint16_t* __restrict__ qe, const uint16_t* __restrict__ xfr,
+    const float* __restrict__ gws, uint16_t* __restrict__ statesT, uint16_t* __restrict__ dstatesT, int NC, int NVB,
+    int remap) {
+  static_assert(GatedReverseShape<DK>::THREADS <= GatedSplitShape<DK>::STATE_THREADS, "one shape for both");
+  __shared__ GatedChainsLds<DK> lds;
+  const int half = int(gridDim.x >> 1), x = int(blockIdx.x);
+  if (x >= half) {
+    gated_split_run<DK, false>(lds.states, a, x - half, xfr, gws, nullptr, NC, NVB, remap, statesT);
+  } else if (wave_id() < GatedReverseShape<DK>::NWAVES) {  // the others end here and leave its barriers
+    gated_reverse_run<DK>(lds.reverse, b, x, qe, xfr, gws, dstatesT, NC, NVB, remap);
   }
 }
 

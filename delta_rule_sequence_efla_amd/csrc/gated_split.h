@@ -68,30 +68,52 @@ struct GatedSplitShape {
   static constexpr int THREADS = (kO + 2) * kWave, STATE_THREADS = (kDma + 1) * kWave;
 };
 
+template <int DK>
+struct GatedSplitLds {
+  using S = GatedSplitShape<DK>;
+  alignas(1024) uint16_t ring[3 * S::SLOT];
+  alignas(16) bf16x8 bS_buf[2][S::NT][S::NKU_D][kWave];  // S_n, high and low parts
+  alignas(16) bf16x8 bU_buf[S::NT][S::NKU_C][kWave];     // U_n, high parts
+  alignas(16) bf16x8 bW_buf[2][S::NT][S::NKU_C][kWave];  // diag(w) U_n, high and low parts
+  alignas(16) bf16x8 bD_buf[2][S::NT][kWave];            // D_n of tokens 0-31, high and low parts
+  alignas(16) bf16x8 P_buf[S::NPF][kWave];
+  alignas(16) uint16_t O_st[S::C][S::OP];
+};
+template <int DK>
+struct GatedSplitRefs {
+  using L = GatedSplitLds<DK>;
+  uint16_t* ring;
+  decltype(L::bS_buf)& bS_buf;
+  decltype(L::bU_buf)& bU_buf;
+  decltype(L::bW_buf)& bW_buf;
+  decltype(L::bD_buf)& bD_buf;
+  decltype(L::P_buf)& P_buf;
+  decltype(L::O_st)& O_st;
+};
+
 // OUT: writes o and the final state.  Else (the backward's recomputation) the
 // state at the start of every chunk instead, as the high operand parts,
 // transposed, [slots][DV][DK] (the layout of recurrence_split.h), without the O
 // and P waves and Q.
-template <int DK, bool OUT>
-__global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitShape<DK>::STATE_THREADS)) void gated_split_kernel(GatedFwd a, const uint16_t* __restrict__ xfr,
-                                                          const float* __restrict__ gws,
-                                                          const int32_t* __restrict__ order, int NC, int NVB, int remap,
-                                                          uint16_t* __restrict__ statesT) {
+template <int DK, bool OUT, typename Lds>
+__device__ __forceinline__ void gated_split_run(Lds& lds, const GatedFwd& a, const int x,
+                                                const uint16_t* __restrict__ xfr, const float* __restrict__ gws,
+                                                const int32_t* __restrict__ order, int NC, int NVB, int remap,
+                                                uint16_t* __restrict__ statesT) {
   using S = GatedSplitShape<DK>;
   constexpr int C = S::C, BV = S::BV, NT = S::NT, NRT = S::NRT, NKU_D = S::NKU_D, NKU_C = S::NKU_C, KH = S::KH;
-  __shared__ __align__(1024) uint16_t ring[3 * S::SLOT];
+  uint16_t* const ring = lds.ring;
   uint16_t* const slot0 = ring;
   uint16_t* const slot1 = ring + S::SLOT;
   uint16_t* const slot2 = ring + 2 * S::SLOT;
-  __shared__ __align__(16) bf16x8 bS_buf[2][NT][NKU_D][kWave];  // S_n, high and low parts
-  __shared__ __align__(16) bf16x8 bU_buf[NT][NKU_C][kWave];     // U_n, high parts
-  __shared__ __align__(16) bf16x8 bW_buf[2][NT][NKU_C][kWave];  // diag(w) U_n, high and low parts
-  __shared__ __align__(16) bf16x8 bD_buf[2][NT][kWave];         // D_n of tokens 0-31, high and low parts
-  __shared__ __align__(16) bf16x8 P_buf[S::NPF][kWave];
-  __shared__ __align__(16) uint16_t O_st[C][S::OP];
+  auto& bS_buf = lds.bS_buf;
+  auto& bW_buf = lds.bW_buf;
+  auto &bU_buf = lds.bU_buf;
+  auto& bD_buf = lds.bD_buf;
+  auto& P_buf = lds.P_buf;
+  auto& O_st = lds.O_st;
 
   const int H = a.H, DV = a.DV;
-  const int x = blockIdx.x;
   int bh, vb;
   if (remap) {  // all value blocks of one (b, h) on one XCD (same blockIdx % 8)
     const int slot = x >> 3;
@@ -519,6 +541,24 @@ __global__ __launch_bounds__((OUT ? GatedSplitShape<DK>::THREADS : GatedSplitSha
     else p_role(integral_constant<int, 3>{}, integral_constant<int, 4>{});
   }
   sync();  // with the output waves' last barrier
+}
+
+template <int DK>
+__global__ __launch_bounds__((GatedSplitShape<DK>::THREADS)) void gated_split_kernel(
+    GatedFwd a, const uint16_t* __restrict__ xfr, const float* __restrict__ gws, const int32_t* __restrict__ order,
+    int NC, int NVB, int remap) {
+  // arrays of their own: in one struct, where an exchange buffer's writes may be
+  // writes to the ring for all the compiler knows, the forward is 2 us longer
+  using S = GatedSplitShape<DK>;
+  __shared__ __align__(1024) uint16_t ring[3 * S::SLOT];
+  __shared__ __align__(16) bf16x8 bS_buf[2][S::NT][S::NKU_D][kWave];
+  __shared__ __align__(16) bf16x8 bU_buf[S::NT][S::NKU_C][kWave];
+  __shared__ __align__(16) bf16x8 bW_buf[2][S::NT][S::NKU_C][kWave];
+  __shared__ __align__(16) bf16x8 bD_buf[2][S::NT][kWave];
+  __shared__ __align__(16) bf16x8 P_buf[S::NPF][kWave];
+  __shared__ __align__(16) uint16_t O_st[S::C][S::OP];
+  const GatedSplitRefs<DK> lds{ring, bS_buf, bU_buf, bW_buf, bD_buf, P_buf, O_st};
+  gated_split_run<DK, true>(lds, a, blockIdx.x, xfr, gws, order, NC, NVB, remap, nullptr);
 }
 
 }  // namespace efla

@@ -176,12 +176,9 @@ struct GatedFwdLayout {
 bool gated_chunk_supported(int DK, int DV);
 GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed);
 hipError_t launch_gated_chunk(const GatedFwd& a, void* workspace, hipStream_t s);
-// Its two launches as the backward runs them over a dense batch: X fragments and
-// gate blocks as the forward's, P fragments, Qe as rows; then every chunk's start
-// state, [slots][DV][DK] bf16.
+// Its UT transform as the backward runs it over a dense batch: X fragments and
+// gate blocks as the forward's, P fragments, Qe as rows.
 hipError_t launch_gated_ut_bwd(const GatedFwd& a, uint16_t* xfr, float* gws, uint16_t* p, uint16_t* qe, hipStream_t s);
-hipError_t launch_gated_states(const GatedFwd& a, const uint16_t* xfr, const float* gws, uint16_t* statesT,
-                               hipStream_t s);
 
 struct GatedBwd {
   const void *q, *k, *v, *beta, *d_o;
@@ -195,11 +192,11 @@ size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, size
 template <typename T>
 hipError_t launch_gated_bwd(const GatedBwd& b, void* ws, hipStream_t s);
 // The backward's passes for bf16 inputs at the chunked forward's shapes: the
-// reverse pass over the chunks (gated_reverse.h), dS' of every chunk as
+// chunks' start states and the reverse pass over them (gated_reverse.h), both as
 // [slots][DV][DK] bf16, and the per-chunk gradients (gated_bwd_chunk.h); dqh,
 // dkh as in gated_bwd.h.
-hipError_t launch_gated_reverse(const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe, const float* gws,
-                                uint16_t* dstatesT, hipStream_t s);
+hipError_t launch_gated_chains(const GatedFwd& a, const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe,
+                               const float* gws, uint16_t* statesT, uint16_t* dstatesT, hipStream_t s);
 hipError_t launch_gated_bwd_chunk(const GatedBwd& b, const uint16_t* xfr, const uint16_t* p, const float* gws,
                                   const uint16_t* statesT, const uint16_t* dstatesT, float* dqh,
                                   float* dkh, hipStream_t s);
