@@ -37,9 +37,9 @@
 //     Y: X D -> publish U | P: gates -> publish
 //   B (U and P published, chunk n+1 in LDS)
 //     Y: load K, V, X of n+1 | S: update -> publish | O: O^T | P: start n+1 | DMA
-// Bound by that chain: 4 x 4096 tokens of 16 heads, d 128, take 107 us, 1.65 us a
-// chunk on every compute unit: 220 MB counted (2 TB/s), 345 TFLOP/s of products.
-// Eight wavefronts took 117 us, eleven 109; without P and O (their outputs wrong)
+// Bound by that chain: 4 x 4096 tokens of 16 heads, d 128, take 109 us, 1.7 us a
+// chunk on every compute unit: 220 MB counted (2 TB/s), 338 TFLOP/s of products.
+// Eight wavefronts took 117 us, eleven 109 for 107; without P and O (outputs wrong)
 // 100; wave priorities, sleeps before contended reads and interleave hints were
 // no faster.  The backward's instance, states only, takes 49 us for 8 x 2048
 // tokens of 8 heads.
