@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kThreads) void plan_kernel(const int32_t* __restric
   // chunk counts, padded with -1 (below every count) to whole steps of 64
   const int padded = (N + 63) / 64 * 64;
   for (int u = tid; u < padded; u += kThreads)
-    chunks[u] = u < N ? (end[u] - (u > 0 ? end[u - 1] : 0) + (1 << shift) - 1) >> shift : -1;
+    chunks[u] = u < N ? chunk_count(end[u] - (u > 0 ? end[u - 1] : 0), shift) : -1;
   __syncthreads();
   // rank(u) = #{v : n(v) > n(u)} + #{v < u : n(v) = n(u)}, 16 lanes a sequence, four v a step
   typedef int i32x4 __attribute__((ext_vector_type(4)));

@@ -1,0 +1,44 @@
+"""Sizes at the ends of what the gated entry points and the plan accept, on the GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from delta_rule_sequence_efla_amd import efla
+from tests import _gated as G
+
+pytestmark = pytest.mark.gpu
+TOP = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("chunk", [16, 32, 64])
+@pytest.mark.parametrize("lens", [[TOP], [TOP - 15], [3, TOP - 63], [0, 5, TOP, 7], [2 ** 30] * 3], ids=str)
+def test_plan_of_the_longest_requests(lens, chunk):
+    """Offsets and order alone, by the C entry point: tables of their own size inside guarded arrays."""
+    N, T, pad = len(lens), TOP, 128
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    cu = torch.full((pad + N + 1 + pad,), 77, dtype=torch.int32).cuda()
+    order = torch.full((pad + N + pad,), 77, dtype=torch.int32).cuda()
+    at = lambda t: ctypes.c_void_p(t.data_ptr() + 4 * pad)
+    assert efla.lib().efla_pack_plan(ctypes.c_void_p(ln.data_ptr()), None, N, T, chunk, at(cu), at(order), None, None,
+                                     ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == 0
+    want = [0]
+    for x in lens:
+        want.append(min(want[-1] + x, T))
+    n = [-(-(b - a) // chunk) for a, b in zip(want, want[1:])]
+    assert cu[pad:-pad].tolist() == want
+    assert order[pad:-pad].tolist() == sorted(range(N), key=lambda u: (-n[u], u))
+    for t in (cu, order):
+        assert bool((t[:pad] == 77).all()) and bool((t[-pad:] == 77).all())
+
+
+def test_plan_of_the_largest_batch():
+    """Through the binding, with the tables of 2^31 - 1 rows."""
+    lens, starts = [9, TOP - 100], [4, 1000]
+    p = efla.efla_pack_plan(torch.tensor(lens, dtype=torch.int32).cuda(), TOP, torch.tensor(starts, dtype=torch.int32).cuda())
+    end = sum(lens)
+    assert p.cu_seqlens.tolist() == [0, 9, end] and p.order.tolist() == [1, 0]
+    rows = [0, 8, 9, 2 ** 30, end - 1, end, TOP - 1]
+    assert p.token_seq[rows].tolist() == [0, 0, 1, 1, 1, -1, -1]
+    wrap = lambda x: (x + 2 ** 31) % 2 ** 32 - 2 ** 31
+    assert p.token_pos[rows].tolist() == [4, 12, 1000, wrap(2 ** 30 - 9 + 1000), wrap(end - 10 + 1000), -1, -1]
