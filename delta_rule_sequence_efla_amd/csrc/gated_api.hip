@@ -15,6 +15,18 @@ efla_status check_gated_shape(int B, int H, int Hk, int64_t L, int d_k, int d_v,
   return H % Hk == 0 ? EFLA_OK : EFLA_ERR_INVALID_ARG;
 }
 
+// Shapes of a gated call over N sequences packed into T tokens: what bounds it is
+// the workgroups of the recurrence and the chunk slots of the whole batch (gated_fwd.hip:
+// T / 64 + N a head), not N sequences of T tokens each, and not the chunk named.
+efla_status check_gated_packed(int N, int H, int Hk, int64_t T, int d_k, int d_v, int chunk, efla_dtype dt,
+                               efla_rule rule) {
+  if (!valid_rule(rule) || !valid_dtype(dt) || N < 0 || T < 0 || T > INT32_MAX || H < 1 || Hk < 1)
+    return EFLA_ERR_INVALID_ARG;
+  if (!valid_dim(d_k) || !valid_dim(d_v) || !valid_chunk(chunk)) return EFLA_ERR_UNSUPPORTED;
+  if (int64_t(N) * H * (d_v / 16) > kMaxGrid || int64_t(H) * (T / 64 + N) > kMaxGrid) return EFLA_ERR_UNSUPPORTED;
+  return H % Hk == 0 ? EFLA_OK : EFLA_ERR_INVALID_ARG;
+}
+
 // Which forward kernels run over `seqs` sequences of at most L tokens: the
 // chunked matrix-core passes for bf16 at their shapes (whatever chunk the caller
 // names: it does not change the result), else the fp32 recurrence.  The latter
@@ -75,7 +87,7 @@ efla_status efla_gated_chunk_fwd(const void* q, const void* k, const void* v, co
 
 size_t efla_gated_chunk_fwd_varlen_workspace_size(int N, int H, int Hk, int64_t T, int d_k, int d_v, int chunk,
                                                   efla_dtype dtype) {
-  if (check_gated_shape(N, H, Hk, T, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || T == 0) return 0;
+  if (check_gated_packed(N, H, Hk, T, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || N == 0 || T == 0) return 0;
   return gated_chunked(N, H, T, d_k, d_v, dtype) ? efla::gated_fwd_layout(0, N, H, T, true).total : 0;
 }
 
@@ -84,12 +96,11 @@ efla_status efla_gated_chunk_fwd_varlen(const void* q, const void* k, const void
                                         int P, const float* s0, void* o, float* s_final, int H, int Hk, int64_t T,
                                         int d_k, int d_v, int chunk, efla_dtype dtype, efla_rule rule,
                                         void* workspace, size_t workspace_bytes, void* stream) {
-  if (N < 0 || P < 0 || T > INT32_MAX) return EFLA_ERR_INVALID_ARG;
-  const efla_status st = check_gated_shape(N < 1 ? 1 : N, H, Hk, T, d_k, d_v, chunk, dtype, rule);
+  if (P < 0) return EFLA_ERR_INVALID_ARG;
+  const efla_status st = check_gated_packed(N, H, Hk, T, d_k, d_v, chunk, dtype, rule);
   if (st != EFLA_OK) return st;
   if (slots == nullptr && P < N) return EFLA_ERR_INVALID_ARG;
   if (N == 0) return EFLA_OK;
-  if (int64_t(H) * (T / 16 + N) > kMaxGrid) return EFLA_ERR_UNSUPPORTED;
   if (cu_seqlens == nullptr) return EFLA_ERR_INVALID_ARG;
   if (T > 0) {
     if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || o == nullptr)

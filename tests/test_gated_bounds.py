@@ -1,10 +1,12 @@
 """Sizes at the ends of what the gated entry points and the plan accept, on the CPU."""
+import ctypes
 import os
 import subprocess
 
 import pytest
+import torch
 
-from delta_rule_sequence_efla_amd import build
+from delta_rule_sequence_efla_amd import build, efla
 
 COUNTS = r"""
 #include "common.h"
@@ -32,3 +34,37 @@ def test_chunk_counts_up_to_the_last_length(tmp_path, shift):
     # and it is what the plan's kernel counts with
     with open(os.path.join(build.CSRC, "plan.hip")) as f:
         assert "chunk_count(end[u]" in f.read()
+
+
+# ---------------------------------------------------- packed batches of many sequences and tokens
+INVALID, UNSUPPORTED, WORKSPACE = 1, 2, 3
+NUL, FAKE = None, ctypes.c_void_p(4096)
+
+
+def varlen(N, H, T, chunk=64, Hk=1, d=128, dt=1):
+    """Status of a packed call whose workspace is missing: WORKSPACE once the shape is accepted."""
+    return efla.lib().efla_gated_chunk_fwd_varlen(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, NUL, NUL, N, N, NUL, FAKE, NUL, H, Hk, T,
+                                                  d, d, chunk, dt, 0, NUL, 0, NUL)
+
+
+def test_packed_batches_are_bounded_by_what_runs():
+    """2048 and 4096 sequences in 2^20 tokens: T / 64 + N chunk slots a head whatever chunk is named, 12 KiB of X
+    and 1 KiB of gates each, and 4 bytes a sequence for the schedule."""
+    size = efla.efla_gated_chunk_fwd_varlen_workspace_size
+    for N, H in ((2048, 16), (4095, 32), (4096, 32), (4097, 32), (65536, 16)):
+        want = H * (2 ** 20 // 64 + N) * 13 * 1024 + (4 * N + 255) // 256 * 256
+        for chunk in (16, 32, 64):
+            assert size(N, H, 1, 2 ** 20, 128, 128, chunk, torch.bfloat16) == want
+            assert varlen(N, H, 2 ** 20, chunk) == WORKSPACE
+    # the largest T, in one sequence and in many
+    assert size(1, 1, 1, 2 ** 31 - 1, 64, 64, 16, torch.bfloat16) == (2 ** 25 - 1 + 1) * 13 * 1024 + 256
+    assert varlen(1, 1, 2 ** 31 - 1, 16, d=64) == WORKSPACE
+
+
+def test_packed_batches_beyond_the_grid_are_refused():
+    size = efla.efla_gated_chunk_fwd_varlen_workspace_size
+    for N, H, T in ((2 ** 28, 1, 640), (2 ** 20, 2 ** 8, 640), (1, 2 ** 7, 2 ** 31 - 1)):  # workgroups, workgroups, slots
+        assert size(N, H, 1, T, 128, 128, 64, torch.bfloat16) == 0 and varlen(N, H, T) == UNSUPPORTED
+    for bad in (dict(N=-1), dict(T=-1), dict(T=2 ** 31), dict(H=0), dict(Hk=0), dict(H=4, Hk=3), dict(dt=5)):
+        assert varlen(**{**dict(N=2, H=4, T=640), **bad}) == INVALID
+    assert size(0, 4, 2, 640, 64, 64, 64, torch.bfloat16) == 0

@@ -42,3 +42,20 @@ def test_plan_of_the_largest_batch():
     assert p.token_seq[rows].tolist() == [0, 0, 1, 1, 1, -1, -1]
     wrap = lambda x: (x + 2 ** 31) % 2 ** 32 - 2 ** 31
     assert p.token_pos[rows].tolist() == [4, 12, 1000, wrap(2 ** 30 - 9 + 1000), wrap(end - 10 + 1000), -1, -1]
+
+
+@pytest.mark.parametrize("N,H,chunk", [(4096, 32, 64), (2048, 16, 16)])
+def test_packed_batch_of_many_long_requests(N, H, chunk):
+    """2^20 tokens in thousands of sequences: each gives, bit for bit, what it gives alone."""
+    T, d, n = 2 ** 20, 128, 2 ** 20 // N
+    gen = torch.Generator(device="cuda").manual_seed(N)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    k = r(T, 1, d)
+    x = [r(T, 1, d).to(torch.bfloat16), (k / k.norm(dim=-1, keepdim=True)).to(torch.bfloat16),
+         torch.empty(T, H, d, dtype=torch.bfloat16, device="cuda").normal_(generator=gen),
+         torch.sigmoid(r(T, H)).to(torch.bfloat16), -0.02 * r(T, H).exp()]
+    cu = torch.arange(0, T + 1, n, dtype=torch.int32).cuda()
+    o, S = efla.efla_gated_chunk_fwd_varlen(*x, cu, chunk=chunk)
+    for u in (0, 1, N // 2, N - 1):
+        o1, S1 = efla.efla_gated_chunk_fwd(*(t[None, u * n:(u + 1) * n].contiguous() for t in x), chunk=chunk)
+        assert torch.equal(o[u * n:(u + 1) * n], o1[0]) and torch.equal(S[u], S1[0])
