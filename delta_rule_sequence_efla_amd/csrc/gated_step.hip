@@ -30,7 +30,8 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(
   constexpr int NCQ = DVW / 4;
   constexpr int NRG = kThreads / NCQ < DK ? kThreads / NCQ : DK;  // rows in flight
   constexpr int RPT = DK / NRG;
-  __shared__ float ks[DK], qs[DK], us[DVW];
+  __shared__ float ks[DK], qs[DK];
+  __shared__ __align__(16) float us[DVW];
   __shared__ __align__(16) float red_k[NRG * DVW];
   __shared__ __align__(16) float red_q[NRG * DVW];
   __shared__ float coef[3];
