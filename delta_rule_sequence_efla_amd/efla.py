@@ -668,7 +668,8 @@ def efla_gated_chunk_fwd_varlen(q, k, v, beta, g, cu_seqlens, s0=None, chunk: in
     [N,H,dk,dv], or with int32 slots [N] pools [P,H,dk,dv] whose row slots[i]
     sequence i starts from and ends in (an entry outside the pool: from zero,
     final state not written).  order: a schedule as efla_pack_plan returns it.
-    Returns (o shaped like v, s_final)."""
+    Returns (o shaped like v, s_final); rows of no sequence are left as they
+    were in an ``o`` that is given, and are zero in one that is made here."""
     index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1, s0, o, s_final, workspace, cu_seqlens, slots, order)
     T = k.shape[0]
     if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
@@ -685,7 +686,7 @@ def efla_gated_chunk_fwd_varlen(q, k, v, beta, g, cu_seqlens, s0=None, chunk: in
     _shaped(s0, (P, H, dk, dv), "s0", _f32)
     _shaped(s_final, (P, H, dk, dv), "s_final", _f32)
     if o is None:
-        o = torch.empty_like(v)
+        o = torch.zeros_like(v)  # the offsets are on the device: whether they cover every row is not known here
     if s_final is None and want_final:
         if slots is not None:
             raise ValueError("with slots the final states need a pool: pass s_final (it may be s0), or want_final=False")
@@ -731,7 +732,8 @@ def efla_gated_step(q, k, v, beta, g, state, slots=None, o=None, rule: str = "ex
     """One gated decode step, in place on a pool of states [P,H,dk,dv] (fp32):
     q, k [N,Hk,dk], v [N,H,dv], beta [N,H] in one type, g float32 [N,H].  Row n
     updates state slots[n] (int32 [N]; None: state n); a slot outside the pool
-    skips the row and leaves its row of o as it was.  Returns o [N,H,dv]."""
+    skips the row: its row of an ``o`` that is given is left as it was, that of
+    one that is made here is zero.  Returns o [N,H,dv]."""
     index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 1, state, slots, o)
     N = k.shape[0]
     P = N if slots is None or state.dim() != 4 else state.shape[0]
@@ -739,7 +741,7 @@ def efla_gated_step(q, k, v, beta, g, state, slots=None, o=None, rule: str = "ex
         raise ValueError("state must be float32 [P,H,dk,dv], with P = N where no slots are given")
     _shaped(slots, (N,), "slots", torch.int32)
     if o is None:
-        o = torch.empty_like(v)
+        o = torch.empty_like(v) if slots is None else torch.zeros_like(v)
     else:
         _shaped(o, v.shape, "o", q.dtype)
     _call(lib().efla_gated_step, index, "efla_gated_step", q.data_ptr(), k.data_ptr(), v.data_ptr(), beta.data_ptr(),
