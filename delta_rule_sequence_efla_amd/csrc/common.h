@@ -39,13 +39,6 @@ __device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane
 __host__ __device__ constexpr int round_up(int x, int m) { return (x + m - 1) / m * m; }
 __host__ __device__ constexpr int cdiv(int x, int m) { return (x + m - 1) / m; }
 
-// Chunks of 2^shift tokens in a sequence of `tokens` >= 0, up to 2^31 - 1 of them:
-// the sum is formed unsigned, since a signed one is negative in the last chunk
-// below 2^31.
-__host__ __device__ constexpr int chunk_count(int tokens, int shift) {
-  return int((uint32_t(tokens) + (1u << shift) - 1u) >> shift);
-}
-
 // ---- element types: float, or bf16 carried as its 16-bit pattern ----------
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(uint16_t h) { return __uint_as_float(uint32_t(h) << 16); }

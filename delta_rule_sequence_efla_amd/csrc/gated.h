@@ -20,6 +20,13 @@
 
 namespace efla {
 
+// Chunks of 2^shift tokens in a sequence of `tokens` >= 0, up to 2^31 - 1 of them:
+// the sum is formed unsigned, since a signed one is negative in the last chunk
+// below 2^31.
+__host__ __device__ constexpr int chunk_count(int tokens, int shift) {
+  return int((uint32_t(tokens) + (1u << shift) - 1u) >> shift);
+}
+
 // Log-decays below -128 act as -128: e^{-128} is zero in fp32 already, and
 // sums of a chunk's gates stay finite (G_i - G_j of two infinities would be
 // NaN), so g = -inf resets the state.  NaN passes through.

@@ -9,7 +9,7 @@ import torch
 from delta_rule_sequence_efla_amd import build, efla
 
 COUNTS = r"""
-#include "common.h"
+#include "gated.h"
 #include <stdio.h>
 #include <stdlib.h>
 int main(int n, char** a) {
