@@ -110,4 +110,11 @@ __device__ __forceinline__ int64_t state_row(const int32_t* __restrict__ slots, 
   return s >= 0 && s < P ? s : -1;
 }
 
+// dg of a token: float32, or rounded to the inputs' type.
+template <typename T>
+__device__ __forceinline__ void store_gate_grad(void* dg, int64_t at, float x, int dg32) {
+  if (dg32) static_cast<float*>(dg)[at] = x;
+  else static_cast<T*>(dg)[at] = from_f32<T>(x);
+}
+
 }  // namespace efla

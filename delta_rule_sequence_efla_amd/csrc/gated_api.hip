@@ -127,8 +127,18 @@ efla_status efla_gated_chunk_bwd(const void* q, const void* k, const void* v, co
                                  void* dbeta, void* dg, float* ds0, int B, int H, int Hk, int64_t L, int d_k, int d_v,
                                  int chunk, efla_dtype dtype, efla_rule rule, void* workspace, size_t workspace_bytes,
                                  void* stream) {
+  return efla_gated_chunk_bwd_typed(q, k, v, beta, g, s0, d_o, ds_final, dq, dk, dv, dbeta, dg, ds0, B, H, Hk, L, d_k,
+                                    d_v, chunk, dtype, dtype, rule, workspace, workspace_bytes, stream);
+}
+
+efla_status efla_gated_chunk_bwd_typed(const void* q, const void* k, const void* v, const void* beta, const float* g,
+                                       const float* s0, const void* d_o, const float* ds_final, void* dq, void* dk,
+                                       void* dv, void* dbeta, void* dg, float* ds0, int B, int H, int Hk, int64_t L,
+                                       int d_k, int d_v, int chunk, efla_dtype dtype, efla_dtype dg_dtype,
+                                       efla_rule rule, void* workspace, size_t workspace_bytes, void* stream) {
   const efla_status st = check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, rule);
   if (st != EFLA_OK) return st;
+  if (dg_dtype != dtype && dg_dtype != EFLA_F32) return EFLA_ERR_INVALID_ARG;
   if (L == 0 && ds0 == nullptr) return EFLA_OK;
   if (L > 0) {
     if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || d_o == nullptr ||
@@ -142,7 +152,7 @@ efla_status efla_gated_chunk_bwd(const void* q, const void* k, const void* v, co
     if (!aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
   }
   const efla::GatedBwd b{q, k, v, beta, d_o, g, s0, ds_final, dq, dk, dv, dbeta, dg, ds0, B, H, Hk, d_k, d_v,
-                         int(rule), L};
+                         int(rule), L, dg_dtype == EFLA_F32 ? 1 : 0};
   return by_type(dtype, [&](auto t) {
     return efla::launch_gated_bwd<decltype(t)>(b, workspace, static_cast<hipStream_t>(stream));
   });

@@ -547,7 +547,7 @@ __global__ __launch_bounds__(kThreads) void gated_bwd_chunk_kernel(
       if (lane + d < kWave) after += z;
     }
     const float cc = end * (c0s[0] + c0s[1] + c0s[2] + c0s[3]);
-    if (lane < valid) static_cast<T*>(b.dg)[row0 + int64_t(lane) * H] = from_f32<T>(cc + before + after);
+    if (lane < valid) store_gate_grad<T>(b.dg, row0 + int64_t(lane) * H, cc + before + after, b.dg32);
   }
   __syncthreads();
   // dK += (dG + dG^T) K + 2 diag(dlambda) K;  write dq, dk

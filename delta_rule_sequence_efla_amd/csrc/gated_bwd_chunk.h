@@ -491,7 +491,7 @@ __global__ __launch_bounds__((GatedTrShape<DK>::NTH)) __attribute__((amdgpu_wave
     for (int j = 0; j < NWV; ++j) all += c0s[j];
     const float after = __shfl(from, rev);
     if (t < valid)
-      static_cast<uint16_t*>(b.dg)[row0 + int64_t(t) * H] = from_f32<uint16_t>(fmaf(es[C - 1], all, before - wj + after));
+      store_gate_grad<uint16_t>(b.dg, row0 + int64_t(t) * H, fmaf(es[C - 1], all, before - wj + after), b.dg32);
   }
 #pragma unroll
   for (int i = 0; i < C * C / 4 / NTH; ++i) {

@@ -187,6 +187,7 @@ struct GatedBwd {
   float* ds0;
   int B, H, Hk, DK, DV, rule;
   int64_t L;
+  int dg32;  // dg in float32 whatever the inputs' type
 };
 size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, size_t esz);
 template <typename T>

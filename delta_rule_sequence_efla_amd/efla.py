@@ -108,6 +108,8 @@ def lib() -> ctypes.CDLL:
         L.efla_gated_chunk_bwd_workspace_size.argtypes = [_i, _i, _i, _i64, _i, _i, _i, _i]
         L.efla_gated_chunk_bwd.restype = _i
         L.efla_gated_chunk_bwd.argtypes = [_vp] * 14 + [_i, _i, _i, _i64, _i, _i, _i, _i, _i, _vp, _sz, _vp]
+        L.efla_gated_chunk_bwd_typed.restype = _i
+        L.efla_gated_chunk_bwd_typed.argtypes = [_vp] * 14 + [_i, _i, _i, _i64, _i, _i, _i, _i, _i, _i, _vp, _sz, _vp]
         L.efla_gated_step.restype = _i
         L.efla_gated_step.argtypes = [_vp] * 8 + [_i, _i, _i, _i, _i, _i, _i, _i, _vp]
         L.efla_pack_plan.restype = _i
@@ -706,25 +708,28 @@ def efla_gated_chunk_bwd_workspace_size(B, H, Hk, L, d_k, d_v, chunk, dtype) -> 
 
 
 def efla_gated_chunk_bwd(q, k, v, beta, g, d_o, s0=None, ds_final=None, chunk: int = 64, rule: str = "exact",
-                         want_ds0: bool = True, workspace=None):
+                         want_ds0: bool = True, workspace=None, dg_dtype=None):
     """Gradients through efla_gated_chunk_fwd for dLoss/do = d_o and dLoss/dS_L
     = ds_final (None: zero).  Returns (dq, dk, dv, dbeta, dg, ds0): the first
     five in q's dtype (dq and dk summed over the value heads that share a
-    head), ds0 float32 [B,H,dk,dv] or None when want_ds0 is False."""
+    head; dg in float32, as g is, with dg_dtype=torch.float32), ds0 float32
+    [B,H,dk,dv] or None when want_ds0 is False."""
     index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2, d_o, s0, ds_final, workspace)
     B, L = k.shape[:2]
     _shaped(d_o, v.shape, "d_o", q.dtype)
     _shaped(s0, (B, H, dk, dv), "s0", _f32)
     _shaped(ds_final, (B, H, dk, dv), "ds_final", _f32)
-    gq, gk, gv, gb, gg = (torch.empty_like(x) for x in (q, k, v, beta, beta))
+    if dg_dtype is not None and dg_dtype not in (q.dtype, _f32):
+        raise ValueError("dg_dtype must be q's dtype or float32")
+    gq, gk, gv, gb, gg = (torch.empty_like(x) for x in (q, k, v, beta, g if dg_dtype is _f32 else beta))
     gs0 = g.new_empty((B, H, dk, dv)) if want_ds0 else None
     code, r = _code(q.dtype), _rule(rule)
     if workspace is None:
         n = _gated_workspace("efla_gated_chunk_bwd", B, H, Hk, L, dk, dv, chunk, code)
         workspace = q.new_empty(n, dtype=torch.uint8) if n else None
-    _call(lib().efla_gated_chunk_bwd, index, "efla_gated_chunk_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(),
+    _call(lib().efla_gated_chunk_bwd_typed, index, "efla_gated_chunk_bwd", q.data_ptr(), k.data_ptr(), v.data_ptr(),
           beta.data_ptr(), g.data_ptr(), _at(s0), _at(d_o), _at(ds_final), _at(gq), _at(gk), _at(gv), _at(gb), _at(gg),
-          _at(gs0), B, H, Hk, L, dk, dv, chunk, code, r, _at(workspace), _nbytes(workspace))
+          _at(gs0), B, H, Hk, L, dk, dv, chunk, code, _code(gg.dtype), r, _at(workspace), _nbytes(workspace))
     return gq, gk, gv, gb, gg, gs0
 
 

@@ -405,6 +405,9 @@ efla_status efla_gated_chunk_fwd_varlen(const void *q, const void *k, const void
  * (summed over the value heads that share a head, in a fixed order), dv
  * [B, L, H, d_v], dbeta and dg [B, L, H], all in dtype, and ds0 float32
  * (NULL: not written).  Results do not depend on timing.
+ * efla_gated_chunk_bwd_typed -- the same with dg in a type of its own: dtype, or
+ * EFLA_F32 as g is (dg is summed in float32 either way; anything else is
+ * EFLA_ERR_INVALID_ARG).
  */
 size_t efla_gated_chunk_bwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
                                            efla_dtype dtype);
@@ -413,6 +416,12 @@ efla_status efla_gated_chunk_bwd(const void *q, const void *k, const void *v, co
                                  void *dq, void *dk, void *dv, void *dbeta, void *dg, float *ds0, int B,
                                  int H, int Hk, int64_t L, int d_k, int d_v, int chunk, efla_dtype dtype,
                                  efla_rule rule, void *workspace, size_t workspace_bytes, void *stream);
+efla_status efla_gated_chunk_bwd_typed(const void *q, const void *k, const void *v, const void *beta,
+                                       const float *g, const float *s0, const void *d_o, const float *ds_final,
+                                       void *dq, void *dk, void *dv, void *dbeta, void *dg, float *ds0, int B,
+                                       int H, int Hk, int64_t L, int d_k, int d_v, int chunk, efla_dtype dtype,
+                                       efla_dtype dg_dtype, efla_rule rule, void *workspace,
+                                       size_t workspace_bytes, void *stream);
 
 /*
  * efla_gated_step -- one token per request, its state updated in place in a
