@@ -713,7 +713,8 @@ def efla_gated_chunk_bwd(q, k, v, beta, g, d_o, s0=None, ds_final=None, chunk: i
     = ds_final (None: zero).  Returns (dq, dk, dv, dbeta, dg, ds0): the first
     five in q's dtype (dq and dk summed over the value heads that share a
     head; dg in float32, as g is, with dg_dtype=torch.float32), ds0 float32
-    [B,H,dk,dv] or None when want_ds0 is False."""
+    [B,H,dk,dv] or None when want_ds0 is False.  bf16 inputs: ds0 too is good
+    to bf16 only."""
     index, H, Hk, dk, dv = _gated_shapes(q, k, v, beta, g, 2, d_o, s0, ds_final, workspace)
     B, L = k.shape[:2]
     _shaped(d_o, v.shape, "d_o", q.dtype)

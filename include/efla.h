@@ -405,6 +405,11 @@ efla_status efla_gated_chunk_fwd_varlen(const void *q, const void *k, const void
  * (summed over the value heads that share a head, in a fixed order), dv
  * [B, L, H, d_v], dbeta and dg [B, L, H], all in dtype, and ds0 float32
  * (NULL: not written).  Results do not depend on timing.
+ *   - Where the bf16 matrix-core passes run (bf16, d_k 64 or 128, d_v % 32 == 0,
+ *     more than 16 tokens), gradients are good to bf16, about 4e-3 of their
+ *     norm, and so is ds0, whatever its type: the state gradient is summed in
+ *     float32 but rounded to bf16 once a chunk where it is an operand.  Chains of
+ *     segments through ds0 and ds_final add that up once a segment.
  * efla_gated_chunk_bwd_typed -- the same with dg in a type of its own: dtype, or
  * EFLA_F32 as g is (dg is summed in float32 either way; anything else is
  * EFLA_ERR_INVALID_ARG).
