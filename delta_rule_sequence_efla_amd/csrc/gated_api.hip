@@ -38,6 +38,13 @@ efla_status check_gated_packed(int N, int H, int Hk, int64_t T, int d_k, int d_v
 //   d 128, 64 .. 256:            L 48 14.0 / 9.3, 96 15.8 / 13.4, 128 16.0 / 16.3
 //   d 128,       512:            L 16 14.0 / 10.4, 32 14.3 / 14.3, 48 14.8 / 18.8
 //   d 128,      1024:            L 8 19.1 / 15.6, 16 19.2 / 19.2, 32 19.6 / 27.4
+// Packed batches give T for L: the lengths are on the device, and T is the only
+// bound on the longest of them, which sets the recurrence's time.  Measured
+// (sequences x tokens, same units):
+//   d 64, 8 heads:   16 x 128 16.8 / 26.6, 300 and 15 x 1 19.3 / 35.1, 600, 2, 3, 4 24.0 / 38.5
+//                    but 64 x 8 29.5 / 18.7, 200 x 1 73.6 / 44.3, 256 x 4 91.9 / 61.0
+//   d 128, 16 heads: 4 x 100 17.9 / 32.2, 64 x 8 88.9 / 106, 200 x 1 260 / 289, 600, 2, 3, 4 30.1 / 93.6
+// so batches of many short requests at d 64 are where it takes the slower one.
 bool gated_chunked(int64_t seqs, int H, int64_t L, int d_k, int d_v, efla_dtype dt) {
   if (dt != EFLA_BF16 || !efla::gated_chunk_supported(d_k, d_v)) return false;
   const int64_t wgs = seqs * H * (d_v / 16);
