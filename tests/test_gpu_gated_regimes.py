@@ -115,3 +115,47 @@ def test_step_with_long_and_zero_keys(dt, lam):
     wo, wS = G.forward_ref(*G.wide(x), x["s0"].double())
     assert G.rel(torch.stack(outs, 1), wo) <= G.tol32(6, 64) + (0 if dt == F32 else 2.0 ** -8)
     assert G.rel(st, wS) <= G.tol32(6, 64)
+
+
+@pytest.mark.parametrize("d,dt", [(64, BF), (128, BF), (32, F32), (64, F32)], ids=str)
+def test_growing_gates(d, dt):
+    """Positive gates: a state that grows by e^40 over the sequence, e^19 a chunk.  Exponents of gate differences are
+    then positive, up to 0.3 x 63 = 19: a float32 exponential of it is off by 19 x 2^-24 more, which each token's
+    factor passes on once; gradients pass two such factors."""
+    L = 130
+    x = G.make(1, L, 4, 2, d, d, dt, seed=d)
+    gen = torch.Generator().manual_seed(2)
+    x["g"] = 0.3 + 0.01 * torch.randn(x["g"].shape, generator=gen)
+    do, dsf = torch.randn(1, L, 4, d, generator=gen).to(dt), torch.randn(1, 4, d, d, generator=gen)
+    a = dev(x)
+    args = [a[n] for n in G.NAMES]
+    o, S = efla.efla_gated_chunk_fwd(*args, a["s0"])
+    wo, wS = G.forward_ref(*G.wide(x), x["s0"].double())
+    more = 20 * 2.0 ** -24 * L ** 0.5
+    errs = {"o": (G.rel(o, wo), G.tol_o(dt, L, d) + more), "S": (G.rel(S, wS), G.tol_s(dt, L, d) + more)}
+    got = efla.efla_gated_chunk_bwd(*args, do.cuda(), a["s0"], dsf.cuda())
+    for n, g, w in zip(GRADS, got, grads_ref(x, do, dsf, "exact")):
+        errs[n] = (G.rel(g, w), G.tol_grad(dt, L, d) + 2 * more)
+    print(f"growth d {d} {dt}: " + ", ".join(f"{n} {e:.2e}/{t:.1e}" for n, (e, t) in errs.items()), flush=True)
+    assert all(e <= t for e, t in errs.values()), errs
+
+
+@pytest.mark.parametrize("d,dt", [(128, BF), (64, BF), (64, F32)], ids=str)
+def test_long_sequences_of_slow_heads(d, dt):
+    """2048 tokens, the first head without any decay (the 64-bit form on the GPU)."""
+    L, H = 2048, 2
+    x = R.slow(1, L, H, 1, d, d, dt, seed=d)
+    gen = torch.Generator().manual_seed(2)
+    do, dsf = torch.randn(1, L, H, d, generator=gen).to(dt).cuda(), torch.randn(1, H, d, d, generator=gen).cuda()
+    a = dev(x)
+    args = [a[n] for n in G.NAMES]
+    o, S = efla.efla_gated_chunk_fwd(*args, a["s0"])
+    leaves = [t.requires_grad_() for t in (*G.wide(a), a["s0"].double())]
+    wo, wS = G.forward_ref(*leaves)
+    errs = {"o": (G.rel(o, wo), G.tol_o(dt, L, d)), "S": (G.rel(S, wS), G.tol_s(dt, L, d))}
+    want = torch.autograd.grad((wo * do.double()).sum() + (wS * dsf.double()).sum(), leaves)
+    got = efla.efla_gated_chunk_bwd(*args, do, a["s0"], dsf)
+    for n, g, w in zip(GRADS, got, want):
+        errs[n] = (G.rel(g, w), G.tol_grad(dt, L, d))
+    print(f"long d {d} {dt}: " + ", ".join(f"{n} {e:.2e}/{t:.1e}" for n, (e, t) in errs.items()), flush=True)
+    assert all(e <= t for e, t in errs.values()), errs
