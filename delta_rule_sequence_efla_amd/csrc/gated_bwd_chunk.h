@@ -17,6 +17,10 @@
 //     accumulators before dP K is added.  <dS', S> is summed from the tiles.
 //   * M = dP0 * P + diag(a) N of gated_bwd.h: Q K^T is formed once more in fp32
 //     at the end (P itself was rounded to bf16), on the tiles that hold dP.
+//   * Gam is formed from G as one float (gated_ut.h), not two: behind 48 resets in a
+//     chunk its entries are off by up to 7e-4, below the 2^-8 of the roundings to
+//     bf16 around it.  Measured behind 0 / 48 resets: dq 3.3e-3 / 3.5e-3, dk 3.4e-3 /
+//     3.5e-3, dv 3.0e-3 / 2.8e-3, dbeta 2.7e-3 / 3.3e-3, dg 2.5e-3 / 1.6e-3.
 // Every product is formed transposed: an accumulator tile then holds, in one lane,
 // four consecutive columns of one row (token), so tiles are written to the LDS
 // and rows of K and Q read beside them as 8-byte pieces (4 elements) instead of
@@ -27,12 +31,13 @@
 // X and P stay in fragment order in the LDS (gated_ut.h); T is not held: a scales
 // D's and dV's rows instead, so the sum over D and dU is dX itself, and da needs
 // the row sums of (X^T dU) D alone, both in registers.
-// 80 KiB of LDS.  8 x 2048 tokens of 8 heads, d 128: 134 us, 37 us a workgroup at
-// two to a compute unit.  Bound by latency: between its 18 barriers four
-// wavefronts a SIMD keep the vector unit busy 0.5, the LDS 0.58 (a third of it
-// conflicts of transposing reads) and the matrix unit 0.13 of the time.  In
-// LDS places without those conflicts X and P cost more address arithmetic than
-// they save (267 us of the whole backward for 260).
+// 80 KiB of LDS.  8 x 2048 tokens of 8 heads, d 128: 121 us (133 to 160 in a process's
+// first launches), four rounds of 30 us at two workgroups to a compute unit.  Bound
+// by latency: between its 18 barriers four wavefronts a SIMD keep the vector unit
+// busy 0.55, the LDS 0.57 (a third of it conflicts of transposing reads) and the matrix unit 0.14
+// of the time; an accumulator tile spills in the loop (24 bytes a lane; 2 registers
+// of it where key heads are shared).  In LDS places without those conflicts X and P
+// cost more address arithmetic than they save (267 us of the whole backward for 260).
 #pragma once
 
 #include <type_traits>

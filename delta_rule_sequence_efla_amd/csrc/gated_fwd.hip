@@ -1,6 +1,6 @@
 // gated_fwd.hip -- launches of the chunked gated forward pass for bf16 inputs:
 // the UT transform (gated_ut.h), then the recurrence (gated_split.h).
-// Workspace, regions 256-byte aligned: T fragments [slots][12 KiB], gate blocks
+// Workspace, regions 256-byte aligned: X fragments [slots][12 KiB], gate blocks
 // [slots][1 KiB], and for packed batches the schedule (int32 per sequence).
 #include "gated_split.h"
 

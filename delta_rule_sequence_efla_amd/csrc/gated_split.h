@@ -37,12 +37,14 @@
 //     Y: X D -> publish U | P: gates -> publish
 //   B (U and P published, chunk n+1 in LDS)
 //     Y: load K, V, X of n+1 | S: update -> publish | O: O^T | P: start n+1 | DMA
-// Bound by that chain: 4 x 4096 tokens of 16 heads, d 128, take 109 us, 1.7 us a
-// chunk on every compute unit: 220 MB counted (2 TB/s), 338 TFLOP/s of products.
-// Eight wavefronts took 117 us, eleven 109 for 107; without P and O (outputs wrong)
-// 100; wave priorities, sleeps before contended reads and interleave hints were
-// no faster.  The backward's instance, states only, takes 49 us for 8 x 2048
-// tokens of 8 heads.
+// Bound by that chain: 4 x 4096 tokens of 16 heads, d 128, take 111 us, 1.7 us a chunk
+// on every compute unit: 222 MB counted (2 TB/s), 332 TFLOP/s of products.  Eight
+// wavefronts took 117 us where these took 107, eleven 109; without P and O (outputs
+// wrong) 100; wave priorities, sleeps before contended reads and interleave hints
+// were no faster.  The backward's instance, states only, took 49 us for 8 x 2048
+// tokens of 8 heads as a launch of its own (gated_reverse.h has both chains' time).
+// It keeps this kernel's LDS layout, of which it leaves 63 of 154 KiB (d_k 128)
+// unused: Q's third of the ring, bU, P and O_st.
 #pragma once
 
 #include <type_traits>
@@ -354,7 +356,7 @@ __device__ __forceinline__ void gated_split_run(Lds& lds, const GatedFwd& a, con
       }
     };
     publish();
-    // T of a later chunk touched line by line, a share by each S wave in its idle
+    // X of a later chunk touched line by line, a share by each S wave in its idle
     // phase, so that the Y waves' loads half a chunk ahead find it in L2
     uint32_t warm = 0, seen = 0;
     run([&](const uint16_t* __restrict__ cur, const uint16_t*, int n) {

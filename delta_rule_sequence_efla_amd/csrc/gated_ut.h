@@ -28,7 +28,7 @@
 //        as in ut_wave.h.
 // Bound by HBM like ut_wave_kernel: 16 KiB of K read and 13 KiB written a chunk
 // at d_k 128, 28 us for 4 x 4096 tokens of 16 heads (4.3 TB/s); the backward's
-// instance reads 32 and writes 35 KiB, 38 us for 8 x 2048 tokens of 8 heads (3.7
+// instance reads 32 and writes 35 KiB, 36 us for 8 x 2048 tokens of 8 heads (3.9
 // TB/s; 47 us when it wrote T and X in float32 as well).  A few chunks alone take
 // 10 us, a launch and 6 us of one wavefront's chain.
 #pragma once
@@ -153,7 +153,9 @@ __global__ __launch_bounds__(256, BWD ? 2 : 4) void gated_ut_wave_kernel(const u
     gt = gate_floor(gate[row0 + int64_t(lane) * H]);
   }
   // G in two floats, so that differences behind a reset are as good as before
-  // it.  The block in gws holds the first: it serves P, which is rounded to bf16.
+  // it.  The block in gws holds the first: it serves P, which is rounded to bf16
+  // (behind 48 resets in a chunk o is off by 3.0e-3, without any by 2.9e-3), and
+  // the backward's Gam (gated_bwd_chunk.h).
   // Against float sums: 0.3 us of a 135 us forward (4 x 4096 tokens, 16 heads, d 128).
   const double Gd64 = wave_scan_gate(gt, lane) * kLog2e;
   const float G = float(Gd64);
