@@ -15,18 +15,6 @@ efla_status check_gated_shape(int B, int H, int Hk, int64_t L, int d_k, int d_v,
   return H % Hk == 0 ? EFLA_OK : EFLA_ERR_INVALID_ARG;
 }
 
-// Shapes of a gated call over N sequences packed into T tokens: what bounds it is
-// the workgroups of the recurrence and the chunk slots of the whole batch (gated_fwd.hip:
-// T / 64 + N a head), not N sequences of T tokens each, and not the chunk named.
-efla_status check_gated_packed(int N, int H, int Hk, int64_t T, int d_k, int d_v, int chunk, efla_dtype dt,
-                               efla_rule rule) {
-  if (!valid_rule(rule) || !valid_dtype(dt) || N < 0 || T < 0 || T > INT32_MAX || H < 1 || Hk < 1)
-    return EFLA_ERR_INVALID_ARG;
-  if (!valid_dim(d_k) || !valid_dim(d_v) || !valid_chunk(chunk)) return EFLA_ERR_UNSUPPORTED;
-  if (int64_t(N) * H * (d_v / 16) > kMaxGrid || int64_t(H) * (T / 64 + N) > kMaxGrid) return EFLA_ERR_UNSUPPORTED;
-  return H % Hk == 0 ? EFLA_OK : EFLA_ERR_INVALID_ARG;
-}
-
 // Which forward kernels run over `seqs` sequences of at most L tokens: the
 // chunked matrix-core passes for bf16 at their shapes (whatever chunk the caller
 // names: it does not change the result), else the fp32 recurrence.  The latter
@@ -52,6 +40,27 @@ bool gated_chunked(int64_t seqs, int H, int64_t L, int d_k, int d_v, efla_dtype 
   return L > 48 || wgs > 4096 || L * wgs * d_k > 2000000;
 }
 
+// Whether the forward's largest launch over these sequences has fewer threads than
+// the runtime takes (seqs > 0; L = 0 launches the recurrence, which copies states).
+bool gated_fwd_fits(int64_t seqs, int H, int64_t L, bool packed, int d_k, int d_v, efla_dtype dt) {
+  return (L > 0 && gated_chunked(seqs, H, L, d_k, d_v, dt) ? efla::gated_chunk_threads(seqs, H, L, packed, d_k, d_v)
+                                                           : efla::gated_recurrent_threads(seqs, H, L, packed, d_k, d_v)) <=
+         efla::kMaxLaunchThreads;
+}
+
+// Shapes of a gated call over N sequences packed into T tokens: what bounds it is
+// the workgroups of the recurrence and the chunk slots of the whole batch (gated_fwd.hip:
+// T / 64 + N a head), not N sequences of T tokens each, and not the chunk named.
+efla_status check_gated_packed(int N, int H, int Hk, int64_t T, int d_k, int d_v, int chunk, efla_dtype dt,
+                               efla_rule rule) {
+  if (!valid_rule(rule) || !valid_dtype(dt) || N < 0 || T < 0 || T > INT32_MAX || H < 1 || Hk < 1)
+    return EFLA_ERR_INVALID_ARG;
+  if (!valid_dim(d_k) || !valid_dim(d_v) || !valid_chunk(chunk)) return EFLA_ERR_UNSUPPORTED;
+  if (int64_t(N) * H * (d_v / 16) > kMaxGrid || int64_t(H) * (T / 64 + N) > kMaxGrid) return EFLA_ERR_UNSUPPORTED;
+  if (N > 0 && !gated_fwd_fits(N, H, T, true, d_k, d_v, dt)) return EFLA_ERR_UNSUPPORTED;
+  return H % Hk == 0 ? EFLA_OK : EFLA_ERR_INVALID_ARG;
+}
+
 template <typename F>
 efla_status by_type(efla_dtype dt, F&& f) {
   return from_hip(dt == EFLA_BF16 ? f(uint16_t{}) : f(float{}));
@@ -69,6 +78,7 @@ extern "C" {
 size_t efla_gated_chunk_fwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
                                            efla_dtype dtype) {
   if (check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || L == 0) return 0;
+  if (!gated_fwd_fits(B, H, L, false, d_k, d_v, dtype)) return 0;
   return gated_chunked(B, H, L, d_k, d_v, dtype) ? efla::gated_fwd_layout(B, 0, H, L, false).total : 0;
 }
 
@@ -78,6 +88,7 @@ efla_status efla_gated_chunk_fwd(const void* q, const void* k, const void* v, co
                                  size_t workspace_bytes, void* stream) {
   const efla_status st = check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, rule);
   if (st != EFLA_OK) return st;
+  if (!gated_fwd_fits(B, H, L, false, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
   if (L > 0) {
     if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || o == nullptr)
       return EFLA_ERR_INVALID_ARG;
@@ -126,6 +137,7 @@ efla_status efla_gated_chunk_fwd_varlen(const void* q, const void* k, const void
 size_t efla_gated_chunk_bwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, int chunk,
                                            efla_dtype dtype) {
   if (check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, EFLA_RULE_EXACT) != EFLA_OK || L == 0) return 0;
+  if (efla::gated_bwd_threads(B, H, Hk, L, d_k, d_v, elem_bytes(dtype)) > efla::kMaxLaunchThreads) return 0;
   return efla::gated_bwd_workspace(B, H, Hk, L, d_k, d_v, elem_bytes(dtype));
 }
 
@@ -146,6 +158,8 @@ efla_status efla_gated_chunk_bwd_typed(const void* q, const void* k, const void*
   const efla_status st = check_gated_shape(B, H, Hk, L, d_k, d_v, chunk, dtype, rule);
   if (st != EFLA_OK) return st;
   if (dg_dtype != dtype && dg_dtype != EFLA_F32) return EFLA_ERR_INVALID_ARG;
+  if (efla::gated_bwd_threads(B, H, Hk, L, d_k, d_v, elem_bytes(dtype)) > efla::kMaxLaunchThreads)
+    return EFLA_ERR_UNSUPPORTED;
   if (L == 0 && ds0 == nullptr) return EFLA_OK;
   if (L > 0) {
     if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || d_o == nullptr ||
@@ -170,7 +184,9 @@ efla_status efla_gated_step(const void* q, const void* k, const void* v, const v
                             efla_dtype dtype, efla_rule rule, void* stream) {
   if (!valid_rule(rule) || !valid_dtype(dtype) || N < 0 || P < 0 || H < 1 || Hk < 1 || H % Hk != 0)
     return EFLA_ERR_INVALID_ARG;
-  if (!valid_dim(d_k) || !valid_dim(d_v) || int64_t(N) * H * (d_v / 16) > kMaxGrid) return EFLA_ERR_UNSUPPORTED;
+  if (!valid_dim(d_k) || !valid_dim(d_v) || int64_t(N) * H * (d_v / 16) > kMaxGrid ||
+      efla::gated_step_threads(N, H, d_v) > efla::kMaxLaunchThreads)
+    return EFLA_ERR_UNSUPPORTED;
   if (slots == nullptr && P < N) return EFLA_ERR_INVALID_ARG;
   if (N == 0 || P == 0) return EFLA_OK;
   if (q == nullptr || k == nullptr || v == nullptr || beta == nullptr || g == nullptr || state == nullptr ||

@@ -38,7 +38,7 @@ template <typename T, int N> struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) :
 // With `states`, the state before every C-th token is stored, [chunk
 // slot][d_k][d_v] fp32 (dense batches; C % 16 == 0).
 template <typename T, int DK>
-__global__ __launch_bounds__(13 * kWave) void gated_blocks_kernel(GatedFwd a, float* __restrict__ states, int C, int NC) {
+__global__ __launch_bounds__(kGatedBlocksThreads) void gated_blocks_kernel(GatedFwd a, float* __restrict__ states, int C, int NC) {
   constexpr int TB = 16, NK = DK / 16, NT = DK / 64, KP = DK + 4;  // tokens a block, ...; key tiles a wave; row pitch
   constexpr int RING = 4;                                          // blocks of q, k, v, gates and P in the LDS
   __shared__ __align__(16) float kS[RING][TB * KP], qS[RING][TB * KP];
@@ -347,7 +347,7 @@ hipError_t launch_gated_blocks(const GatedFwd& a, float* states, int C, hipStrea
   const int64_t nwg = int64_t(a.cu == nullptr ? a.B : a.N) * a.H * (a.DV / 16);
   if (nwg == 0) return hipSuccess;
   const int NC = int((a.L + C - 1) / C);
-  const dim3 grid{unsigned(nwg)}, wg{13 * kWave};
+  const dim3 grid{unsigned(nwg)}, wg{kGatedBlocksThreads};
   if (a.DK == 64) hipLaunchKernelGGL((gated_blocks_kernel<T, 64>), grid, wg, 0, s, a, states, C, NC);
   else hipLaunchKernelGGL((gated_blocks_kernel<T, 128>), grid, wg, 0, s, a, states, C, NC);
   return hipGetLastError();

@@ -69,6 +69,17 @@ size_t gated_bwd_workspace(int B, int H, int Hk, int64_t L, int DK, int DV, size
   return gated_bwd_layout(B, H, Hk, L, DK, DV, esz).total;
 }
 
+int64_t gated_bwd_threads(int B, int H, int Hk, int64_t L, int DK, int DV, size_t esz) {
+  const bool fast = gated_bwd_fast(L, DK, DV, esz);
+  const int C = fast ? 64 : fp32_chunk(L);
+  const int64_t bh = int64_t(B) * H, slots = bh * ((L + C - 1) / C);
+  const int64_t chains = fast ? 2 * bh * (DV / 32) * gated_chains_threads(DK) : gated_recurrent_threads(B, H, L, false, DK, DV);
+  const int64_t chunks = slots * (fast ? gated_bwd_chunk_threads(DK) : kThreads);
+  const int64_t heads = Hk < H ? int64_t(B) * L * Hk * (DK / 4) : 0;
+  const int64_t most = chains > chunks ? chains : chunks;
+  return most > heads ? most : heads;
+}
+
 // The forward's inputs, for the backward's recomputation.
 static GatedFwd forward_of(const GatedBwd& b) {
   GatedFwd a{};

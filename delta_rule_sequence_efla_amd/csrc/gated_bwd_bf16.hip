@@ -7,6 +7,9 @@
 
 namespace efla {
 
+int gated_chains_threads(int DK) { return DK == 64 ? GatedSplitShape<64>::STATE_THREADS : GatedSplitShape<128>::STATE_THREADS; }
+int gated_bwd_chunk_threads(int DK) { return DK == 64 ? GatedTrShape<64>::NTH : GatedTrShape<128>::NTH; }
+
 template <int DK>
 static hipError_t chains_impl(const GatedFwd& a, const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe,
                               const float* gws, uint16_t* statesT, uint16_t* dstatesT, hipStream_t s) {

@@ -52,6 +52,12 @@ GatedFwdLayout gated_fwd_layout(int B, int N, int H, int64_t L, bool packed) {
   return w;
 }
 
+int64_t gated_chunk_threads(int64_t seqs, int H, int64_t L, bool packed, int DK, int DV) {
+  const int64_t slots = packed ? H * (L / kGatedChunk + seqs) : seqs * H * ((L + kGatedChunk - 1) / kGatedChunk);
+  const int64_t split = seqs * H * (DV / 32) * (DK == 64 ? GatedSplitShape<64>::THREADS : GatedSplitShape<128>::THREADS);
+  return split > slots * kWave ? split : slots * kWave;
+}
+
 hipError_t launch_gated_ut_bwd(const GatedFwd& a, uint16_t* xfr, float* gws, uint16_t* p, uint16_t* qe, hipStream_t s) {
   const GatedUtBwd b{static_cast<const uint16_t*>(a.q), p, qe};
   return a.DK == 64 ? ut_impl<64, true>(a, xfr, gws, b, nullptr, s) : ut_impl<128, true>(a, xfr, gws, b, nullptr, s);

@@ -121,11 +121,17 @@ static hipError_t gated_step_impl(const GatedStep& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// 64 value columns a workgroup (above); where that gives the compute units
+// less than four workgroups each, 32, so that more of them share the loads.
+static bool cut_columns(int N, int H, int DV) { return int64_t(N) * H * (DV / 64) < 1024; }
+
+int64_t gated_step_threads(int N, int H, int DV) {
+  return int64_t(N) * H * (DV < 64 ? 1 : DV / (cut_columns(N, H, DV) ? 32 : 64)) * kThreads;
+}
+
 template <typename T, int DK>
 static hipError_t gated_step_dv(const GatedStep& a, hipStream_t s) {
-  // 64 value columns a workgroup (above); where that gives the compute units
-  // less than four workgroups each, 32, so that more of them share the loads.
-  const bool cut = int64_t(a.N) * a.H * (a.DV / 64) < 1024;
+  const bool cut = cut_columns(a.N, a.H, a.DV);
   switch (a.DV) {
     case 16: return gated_step_impl<T, DK, 16>(a, s);
     case 32: return gated_step_impl<T, DK, 32>(a, s);
@@ -368,26 +374,32 @@ __global__ __launch_bounds__(2 * kThreads) void gated_recurrent_kernel(GatedFwd 
   finish();
 }
 
+// By 16 tokens (gated_blocks.hip) the chain is shorter, but it starts four
+// blocks late and fewer of its workgroups share a compute unit.  Measured (fp32,
+// us, pairs / blocks):
+//   d 64,   256 workgroups: 16 tokens 5.8 / 6.0, 32 7.5 / 7.1, 128 17.7 / 13.0, 512 57 / 38
+//   d 64,  1024:            32 18.3 / 24.7, 128 49.1 / 50.4, 512 160 / 142
+//   d 128,   64:            16 7.2 / 6.5, 32 9.6 / 8.0, 128 23.6 / 16.8, 512 80 / 52
+//   d 128,  512:            32 14.7 / 16.1, 64 24.1 / 25.1, 128 38.8 / 36.6, 512 126 / 105
+//   d 128, 8192:            32 155 / 231, 128 508 / 525, 512 1963 / 1613
+// Packed batches go by their mean length: most of their workgroups are about that
+// long, and both forms take any length.  Measured (sequences x tokens, same units):
+//   d 64, 8 heads:   64 x 8 18.4 / 37.5, 200 x 1 43 / 112, 4 x 100 15.0 / 11.3
+//   d 128, 16 heads: 64 x 8 92 / 169, 32 x 32 85 / 115, 8 x 64 41.5 / 45.1
+//   and one long among short ones: 300 and 15 x 1 at d 64 35 / 22, at d 128 51 / 58
+static bool by_blocks(int64_t nwg, int64_t tokens, int DK) { return DK >= 64 && tokens >= (nwg <= 256 ? 32 : 160); }
+
+int64_t gated_recurrent_threads(int64_t seqs, int H, int64_t L, bool packed, int DK, int DV) {
+  const int64_t nwg = seqs * H * (DV / 16);
+  return nwg * (by_blocks(nwg, packed ? L / seqs : L, DK) ? kGatedBlocksThreads : 2 * kThreads);
+}
+
 template <typename T>
 hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipStream_t s) {
   const int64_t units = int64_t(a.cu == nullptr ? a.B : a.N) * a.H;
   const int64_t nwg = units * (a.DV / 16);
   if (nwg == 0) return hipSuccess;
-  // By 16 tokens (gated_blocks.hip) the chain is shorter, but it starts four
-  // blocks late and fewer of its workgroups share a compute unit.  Measured (fp32,
-  // us, pairs / blocks):
-  //   d 64,   256 workgroups: 16 tokens 5.8 / 6.0, 32 7.5 / 7.1, 128 17.7 / 13.0, 512 57 / 38
-  //   d 64,  1024:            32 18.3 / 24.7, 128 49.1 / 50.4, 512 160 / 142
-  //   d 128,   64:            16 7.2 / 6.5, 32 9.6 / 8.0, 128 23.6 / 16.8, 512 80 / 52
-  //   d 128,  512:            32 14.7 / 16.1, 64 24.1 / 25.1, 128 38.8 / 36.6, 512 126 / 105
-  //   d 128, 8192:            32 155 / 231, 128 508 / 525, 512 1963 / 1613
-  // Packed batches go by their mean length: most of their workgroups are about that
-  // long, and both forms take any length.  Measured (sequences x tokens, same units):
-  //   d 64, 8 heads:   64 x 8 18.4 / 37.5, 200 x 1 43 / 112, 4 x 100 15.0 / 11.3
-  //   d 128, 16 heads: 64 x 8 92 / 169, 32 x 32 85 / 115, 8 x 64 41.5 / 45.1
-  //   and one long among short ones: 300 and 15 x 1 at d 64 35 / 22, at d 128 51 / 58
-  const int64_t tokens = a.cu == nullptr ? a.L : a.L / a.N;
-  if (a.DK >= 64 && tokens >= (nwg <= 256 ? 32 : 160)) return launch_gated_blocks<T>(a, states, C, s);
+  if (by_blocks(nwg, a.cu == nullptr ? a.L : a.L / a.N, a.DK)) return launch_gated_blocks<T>(a, states, C, s);
   const int NC = int((a.L + C - 1) / C);
   const dim3 grid{unsigned(nwg)}, wg{2 * kThreads};
   switch (a.DK) {

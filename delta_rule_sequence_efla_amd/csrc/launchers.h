@@ -167,6 +167,16 @@ template <typename T>
 hipError_t launch_gated_blocks(const GatedFwd& a, float* states, int C, hipStream_t s);
 template <typename T>
 hipError_t launch_gated_recurrent(const GatedFwd& a, float* states, int C, hipStream_t s);
+constexpr int kGatedBlocksThreads = 13 * kWave;  // a workgroup of launch_gated_blocks
+
+// Threads of the largest launch of the recurrence, of the chunked forward, of the
+// backward and of the step; the runtime takes fewer than 2^32 in one.  L: tokens a
+// sequence, or of the packed batch; esz: bytes of an input value.
+constexpr int64_t kMaxLaunchThreads = (int64_t(1) << 32) - 1;
+int64_t gated_recurrent_threads(int64_t seqs, int H, int64_t L, bool packed, int DK, int DV);
+int64_t gated_chunk_threads(int64_t seqs, int H, int64_t L, bool packed, int DK, int DV);
+int64_t gated_bwd_threads(int B, int H, int Hk, int64_t L, int DK, int DV, size_t esz);
+int64_t gated_step_threads(int N, int H, int DV);
 
 // Chunked forward of bf16 inputs (gated_ut.h, gated_split.h): d_k 64 or 128, d_v
 // a multiple of 32, in chunks of 64.
@@ -196,6 +206,9 @@ hipError_t launch_gated_bwd(const GatedBwd& b, void* ws, hipStream_t s);
 // chunks' start states and the reverse pass over them (gated_reverse.h), both as
 // [slots][DV][DK] bf16, and the per-chunk gradients (gated_bwd_chunk.h); dqh,
 // dkh as in gated_bwd.h.
+// gated_chains_threads, gated_bwd_chunk_threads: threads of their workgroups.
+int gated_chains_threads(int DK);
+int gated_bwd_chunk_threads(int DK);
 hipError_t launch_gated_chains(const GatedFwd& a, const GatedBwd& b, const uint16_t* xfr, const uint16_t* qe,
                                const float* gws, uint16_t* statesT, uint16_t* dstatesT, hipStream_t s);
 hipError_t launch_gated_bwd_chunk(const GatedBwd& b, const uint16_t* xfr, const uint16_t* p, const float* gws,

@@ -358,6 +358,9 @@ efla_status efla_step_rule(const void *q, const void *k, const void *v, const vo
  *     the start of its chunk on, not only from the token on; never another
  *     sequence's.
  *   - Sequences of at most 16 tokens are differentiated in float32 throughout.
+ *   - A call whose largest launch would have 2^32 threads or more is
+ *     EFLA_ERR_UNSUPPORTED (bf16, d_v 128: above 1.19 million sequences times heads,
+ *     so 65536 sequences of 16 heads run; a step at d_v 128: 2^23 rows times heads).
  *   - Layouts, alignment, streams, workspaces and errors as above otherwise.
  *
  * efla_gated_chunk_fwd -- dense batch.  q, k [B, L, Hk, d_k], v, o

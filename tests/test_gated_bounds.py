@@ -68,3 +68,35 @@ def test_packed_batches_beyond_the_grid_are_refused():
     for bad in (dict(N=-1), dict(T=-1), dict(T=2 ** 31), dict(H=0), dict(Hk=0), dict(H=4, Hk=3), dict(dt=5)):
         assert varlen(**{**dict(N=2, H=4, T=640), **bad}) == INVALID
     assert size(0, 4, 2, 640, 64, 64, 64, torch.bfloat16) == 0
+
+
+# ----------------------------------------------------------- launches of 2^32 threads and more
+def dense(B, H, L, dt=1, d=128, bwd=False):
+    """Status of a dense call without pointers: INVALID once the sizes are accepted."""
+    n = [NUL] * (14 if bwd else 8)
+    if bwd:
+        n[-1] = FAKE  # ds0
+    f = efla.lib().efla_gated_chunk_bwd if bwd else efla.lib().efla_gated_chunk_fwd
+    return f(*n, B, H, 1, L, d, d, 64, dt, 0, NUL, 0, NUL)
+
+
+def step(N, H, d=128):
+    return efla.lib().efla_gated_step(NUL, NUL, NUL, NUL, NUL, NUL, NUL, NUL, N, N, H, 1, d, d, 1, 0, NUL)
+
+
+def test_launches_of_2_to_32_threads_are_refused():
+    """A workgroup has 896 threads per 32 value columns in the chunked forward at d_k 128, 512 or 832 per 16 in the
+    recurrence, 576 per 32 for each of the backward's two chains, 256 per 64 in the step."""
+    bf, f32 = 1, 0
+    top = (2 ** 32 - 1) // (4 * 896)
+    assert dense(top, 1, 500) == INVALID and dense(top + 1, 1, 500) == UNSUPPORTED
+    assert varlen(top, 1, 2 ** 24) == WORKSPACE and varlen(top + 1, 1, 2 ** 24) == UNSUPPORTED
+    for L, threads in ((1, 512), (300, 832)):
+        top = (2 ** 32 - 1) // (8 * threads)
+        assert dense(top, 1, L, f32) == INVALID and dense(top + 1, 1, L, f32) == UNSUPPORTED
+    top = (2 ** 32 - 1) // (2 * 4 * 576)
+    assert dense(top, 1, 20, bwd=True) == INVALID and dense(top + 1, 1, 20, bwd=True) == UNSUPPORTED
+    assert step(2 ** 20 - 1, 8) == INVALID and step(2 ** 20, 8) == UNSUPPORTED
+    size, sizeb = efla.efla_gated_chunk_fwd_workspace_size, efla.efla_gated_chunk_bwd_workspace_size
+    assert size(65536, 32, 1, 500, 128, 128, 64, torch.bfloat16) == sizeb(65536, 32, 1, 500, 128, 128, 64, torch.bfloat16) == 0
+    assert size(65536, 16, 1, 500, 128, 128, 64, torch.bfloat16) > 0

@@ -59,3 +59,27 @@ def test_packed_batch_of_many_long_requests(N, H, chunk):
     for u in (0, 1, N // 2, N - 1):
         o1, S1 = efla.efla_gated_chunk_fwd(*(t[None, u * n:(u + 1) * n].contiguous() for t in x), chunk=chunk)
         assert torch.equal(o[u * n:(u + 1) * n], o1[0]) and torch.equal(S[u], S1[0])
+
+
+def test_largest_batches_that_run():
+    """65536 requests of 16 heads (64 GiB of states): one token each through the packed forward, 3.8e9 threads in one
+    launch, then a decode step; some of them against themselves alone."""
+    N, H, d = 65536, 16, 128
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    r = lambda *s: torch.randn(*s, generator=gen, device="cuda")
+    k = r(2, N, 1, d)
+    x = [r(2, N, 1, d).bfloat16(), (k / k.norm(dim=-1, keepdim=True)).bfloat16(), r(2, N, H, d).bfloat16(),
+         torch.sigmoid(r(2, N, H)).bfloat16(), -0.02 * r(2, N, H).exp()]
+    cu = torch.arange(N + 1, dtype=torch.int32).cuda()
+    o, S = efla.efla_gated_chunk_fwd_varlen(*(t[0] for t in x), cu)
+    rows = [0, 1, 9, 4097, 40000, N - 2, N - 1]
+    few = [t[:, rows].contiguous() for t in x]
+    # at d_k 128 a batch this small takes the float32 recurrence: the two agree to the chunked passes' tolerance
+    o1, S1 = efla.efla_gated_chunk_fwd_varlen(*(t[0] for t in few), torch.arange(len(rows) + 1, dtype=torch.int32).cuda())
+    assert G.rel(o[rows], o1) <= 2 * G.tol_o(torch.bfloat16, 1, d) and G.rel(S[rows], S1) <= 2 * G.tol_s(torch.bfloat16, 1, d)
+    S1 = S[rows].clone()
+    y = efla.efla_gated_step(*(t[1] for t in x), S)
+    y1 = efla.efla_gated_step(*(t[1] for t in few), S1)
+    # The few rows take value blocks of 32 columns, the many of 64: a column's d_k products are then summed in 32 parts
+    # of 4 and in 16 of 8, so the sums round differently; each is within tol32 of the exact one, y one rounding more.
+    assert G.rel(y[rows], y1) <= 2 * (2.0 ** -8 + G.tol32(1, d)) and G.rel(S[rows], S1) <= 2 * G.tol32(1, d)
