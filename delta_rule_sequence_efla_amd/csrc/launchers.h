@@ -219,4 +219,101 @@ hipError_t launch_gated_bwd_chunk(const GatedBwd& b, const uint16_t* xfr, const 
 hipError_t launch_plan(const int32_t* lengths, const int32_t* starts, int N, int T, int C, int32_t* cu,
                        int32_t* order, int32_t* seq, int32_t* pos, hipStream_t s);
 
+// The short causal convolution (conv.hip).  Pointers as in include/efla.h; *_row:
+// elements from one token's row to the next; element type by template argument.
+struct ConvFwd {
+  const void *x, *w, *bias, *s0;
+  void *y, *sfin;
+  const int32_t *cu, *slots;  // packed batch: offsets, rows of the states
+  int64_t x_row, y_row;
+  int64_t N;  // sequences
+  int P, D, W, silu;
+  int64_t L;  // tokens a sequence, or of the packed batch
+};
+struct ConvStep {
+  const void *x, *w, *bias;
+  void *state, *y;
+  const int32_t* slots;
+  int64_t x_row, y_row;
+  int64_t N;
+  int P, D, W, silu;
+};
+struct ConvBwd {
+  const void *x, *w, *bias, *s0, *dy, *dsf;
+  void *dx, *ds0;
+  float *dw, *db;
+  int64_t x_row, dy_row, dx_row;
+  int B, D, W, silu;
+  int64_t L;
+};
+template <typename T>
+hipError_t launch_conv_fwd(const ConvFwd& a, hipStream_t s);
+template <typename T>
+hipError_t launch_conv_step(const ConvStep& a, hipStream_t s);
+template <typename T>
+hipError_t launch_conv_bwd(const ConvBwd& a, float* part, hipStream_t s);
+size_t conv_bwd_workspace(int B, int64_t L, int D, int W);
+// Threads of the largest launch over `seqs` dense sequences of L tokens (a packed
+// batch: one of T) and N states.
+int64_t conv_threads(int64_t seqs, int64_t L, int64_t N, int D);
+
+// Moves of state-pool rows (pool.hip).
+constexpr int kPoolsPerLaunch = 64;
+struct PoolSet {
+  void* base[kPoolsPerLaunch];
+  uint64_t bytes[kPoolsPerLaunch];  // of a row
+  uint32_t first[kPoolsPerLaunch + 1];  // pieces of a row in the pools before
+  int count;
+};
+int64_t pool_pieces(uint64_t row_bytes);
+// Row i: pool row src[i] (outside [0, P): zeros) to dst[i] (outside: nothing);
+// share: rows with one source are served by one read.
+hipError_t launch_pool_copy(const PoolSet& set, const int32_t* src, const int32_t* dst, int N, int P, bool share,
+                            hipStream_t s);
+constexpr int kMaxCompactRows = 1 << 17;  // a bit and a count a row in the LDS
+hipError_t launch_pool_plan(const int32_t* slots, int N, int P, int32_t* out, int32_t* live, int32_t* src, int32_t* dst,
+                            hipStream_t s);
+
+// The selective state space scan (ssm.h).
+struct SsmStep {
+  const void *q, *k, *v, *dt;
+  const float *a, *d, *bias;
+  float* state;
+  const int32_t* slots;
+  void* o;
+  int64_t q_row, k_row, v_row, dt_row, o_row;
+  int N, P, H, Hk, DK, DV;
+};
+template <typename T>
+hipError_t launch_ssm_step(const SsmStep& a, hipStream_t s);
+int64_t ssm_step_threads(int N, int H, int DV);
+
+struct SsmFwd {
+  const void *q, *k, *v, *dt;
+  const float *a, *d, *bias, *s0;
+  void* o;
+  float* sfin;
+  const int32_t *cu, *slots, *order;  // packed batch: offsets, rows of the states, schedule
+  int64_t q_row, k_row, v_row, dt_row, o_row;
+  int N, P, H, Hk, DK, DV;  // N: sequences; P: rows of s0 and sfin
+  int64_t L;                // tokens a sequence, or of the packed batch
+};
+struct SsmBwd {
+  const void *q, *k, *v, *dt, *d_o;
+  const float *a, *d, *bias, *s0, *dsf;
+  void *dq, *dk, *dv, *ddt;
+  float *da, *dd, *dbias, *ds0;
+  int64_t q_row, k_row, v_row, dt_row, do_row, dq_row, dk_row, dv_row, ddt_row;
+  int B, H, Hk, DK, DV;
+  int64_t L;
+};
+// In float32 throughout, every size and type, 32 tokens at a time (ssm_f32.hip).
+template <typename T>
+hipError_t launch_ssm_f32(const SsmFwd& a, hipStream_t s);
+int64_t ssm_f32_threads(int64_t seqs, int H, int DV);
+template <typename T>
+hipError_t launch_ssm_bwd_f32(const SsmBwd& b, void* ws, hipStream_t s);
+size_t ssm_bwd_f32_workspace(int B, int H, int64_t L, int DK, int DV);
+int64_t ssm_bwd_f32_threads(int B, int H, int64_t L, int DV);
+
 }  // namespace efla

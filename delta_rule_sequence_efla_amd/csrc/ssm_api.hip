@@ -1,0 +1,330 @@
+// ssm_api.hip -- the C entry points of the short causal convolution, of the
+// selective state space scan and of the moves of state-pool rows
+// (include/efla.h): validation, workspace sizing, launches on the caller's
+// stream.  Nothing here allocates device memory or synchronizes.
+#include <initializer_list>
+
+#include "checks.h"
+#include "launchers.h"
+
+namespace {
+
+constexpr int64_t kMaxRow = int64_t(1) << 24;  // elements from one token's row to the next
+
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+template <typename F>
+efla_status by_type(efla_dtype dt, F&& f) {
+  return from_hip(dt == EFLA_BF16 ? f(uint16_t{}) : f(float{}));
+}
+
+bool all_given(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (p == nullptr) return false;
+  return true;
+}
+
+// ---------------------------------------------------------------- convolution
+efla_status check_conv(int64_t N, int64_t L, int D, int W, int silu, efla_dtype dt, std::initializer_list<int64_t> rows) {
+  if (N < 0 || L < 0 || D < 1 || !valid_dtype(dt) || (silu != 0 && silu != 1)) return EFLA_ERR_INVALID_ARG;
+  if (W < 2 || W > 4 || D >= kMaxRow) return EFLA_ERR_UNSUPPORTED;
+  for (int64_t r : rows) {
+    if (r < D) return EFLA_ERR_INVALID_ARG;
+    if (r >= kMaxRow) return EFLA_ERR_UNSUPPORTED;
+  }
+  return EFLA_OK;
+}
+
+bool conv_aligned(efla_dtype dt, std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (!aligned_to(p, elem_bytes(dt))) return false;
+  return true;
+}
+
+bool conv_fits(int64_t seqs, int64_t L, int64_t N, int D) {
+  return L <= kMaxGrid && seqs * D <= kMaxGrid && N * int64_t(D) <= (int64_t(1) << 40) &&
+         efla::conv_threads(seqs, L, N, D) <= efla::kMaxLaunchThreads;
+}
+
+// ---------------------------------------------------------------- scan
+// Shapes of a scan over `seqs` sequences (dense: of L tokens each; packed: L in all).
+efla_status check_ssm(int64_t seqs, int H, int Hk, int64_t L, int d_k, int d_v, efla_dtype dt) {
+  if (seqs < 0 || H < 1 || Hk < 1 || L < 0 || !valid_dtype(dt) || H % Hk != 0) return EFLA_ERR_INVALID_ARG;
+  if (!valid_dim(d_k) || !valid_dim(d_v)) return EFLA_ERR_UNSUPPORTED;
+  if (int64_t(H) * d_v >= kMaxRow || int64_t(Hk) * d_k >= kMaxRow || L > kMaxGrid || seqs * H > kMaxGrid)
+    return EFLA_ERR_UNSUPPORTED;
+  return EFLA_OK;
+}
+
+struct Rows {
+  int64_t row, width;
+  bool wide;  // moved in 16-byte pieces
+};
+efla_status check_rows(efla_dtype dt, std::initializer_list<Rows> rows) {
+  for (const Rows& r : rows) {
+    if (r.row < r.width || (r.wide && r.row * int64_t(elem_bytes(dt)) % 16 != 0)) return EFLA_ERR_INVALID_ARG;
+    if (r.row >= kMaxRow) return EFLA_ERR_UNSUPPORTED;
+  }
+  return EFLA_OK;
+}
+
+bool all_aligned16(std::initializer_list<const void*> ptrs) {
+  for (const void* p : ptrs)
+    if (!aligned16(p)) return false;
+  return true;
+}
+
+// Whether the forward's launches over these sequences have fewer threads than the
+// runtime takes.
+bool ssm_fwd_fits(int64_t seqs, int H, int64_t, int d_v) {
+  return efla::ssm_f32_threads(seqs, H, d_v) <= efla::kMaxLaunchThreads;
+}
+
+efla_status ssm_forward(const efla::SsmFwd& a, efla_dtype dt, void*, hipStream_t s) {
+  return by_type(dt, [&](auto t) { return efla::launch_ssm_f32<decltype(t)>(a, s); });
+}
+
+bool ssm_bwd_fits(int B, int H, int64_t L, int d_v) {
+  return int64_t(B) * H * ((L + 31) / 32) <= kMaxGrid && efla::ssm_bwd_f32_threads(B, H, L, d_v) <= efla::kMaxLaunchThreads;
+}
+
+}  // namespace
+
+extern "C" {
+
+efla_status efla_conv_fwd(const void* x, int64_t x_row, const void* w, const void* bias, const void* s0, void* y,
+                          int64_t y_row, void* s_final, int B, int64_t L, int D, int W, int silu, efla_dtype dtype,
+                          void* stream) {
+  const efla_status st = check_conv(B, L, D, W, silu, dtype, {x_row, y_row});
+  if (st != EFLA_OK) return st;
+  if (B < 1) return EFLA_ERR_INVALID_ARG;
+  if (!conv_fits(B, L, B, D)) return EFLA_ERR_UNSUPPORTED;
+  if (L > 0 && !all_given({x, w, y})) return EFLA_ERR_INVALID_ARG;
+  if (!conv_aligned(dtype, {x, w, bias, s0, y, s_final})) return EFLA_ERR_INVALID_ARG;
+  if (L == 0 && s_final == nullptr) return EFLA_OK;
+  const efla::ConvFwd a{x, w, bias, s0, y, s_final, nullptr, nullptr, x_row, y_row, B, B, D, W, silu, L};
+  return by_type(dtype, [&](auto t) { return efla::launch_conv_fwd<decltype(t)>(a, static_cast<hipStream_t>(stream)); });
+}
+
+efla_status efla_conv_fwd_varlen(const void* x, int64_t x_row, const void* w, const void* bias,
+                                 const int32_t* cu_seqlens, const int32_t* slots, int N, int P, const void* s0, void* y,
+                                 int64_t y_row, void* s_final, int64_t T, int D, int W, int silu, efla_dtype dtype,
+                                 void* stream) {
+  const efla_status st = check_conv(N, T, D, W, silu, dtype, {x_row, y_row});
+  if (st != EFLA_OK) return st;
+  if (P < 0 || T > INT32_MAX || (slots == nullptr && P < N)) return EFLA_ERR_INVALID_ARG;
+  if (!conv_fits(1, T, N, D)) return EFLA_ERR_UNSUPPORTED;
+  if (N == 0) return EFLA_OK;
+  if (cu_seqlens == nullptr || (T > 0 && !all_given({x, w, y}))) return EFLA_ERR_INVALID_ARG;
+  if (!conv_aligned(dtype, {x, w, bias, s0, y, s_final})) return EFLA_ERR_INVALID_ARG;
+  if (T == 0 && s_final == nullptr) return EFLA_OK;
+  const efla::ConvFwd a{x, w, bias, s0, y, s_final, cu_seqlens, slots, x_row, y_row, N, P, D, W, silu, T};
+  return by_type(dtype, [&](auto t) { return efla::launch_conv_fwd<decltype(t)>(a, static_cast<hipStream_t>(stream)); });
+}
+
+efla_status efla_conv_step(const void* x, int64_t x_row, const void* w, const void* bias, void* state,
+                           const int32_t* slots, void* y, int64_t y_row, int N, int P, int D, int W, int silu,
+                           efla_dtype dtype, void* stream) {
+  const efla_status st = check_conv(N, 1, D, W, silu, dtype, {x_row, y_row});
+  if (st != EFLA_OK) return st;
+  if (P < 0 || (slots == nullptr && P < N)) return EFLA_ERR_INVALID_ARG;
+  if (!conv_fits(1, 1, N, D)) return EFLA_ERR_UNSUPPORTED;
+  if (N == 0 || P == 0) return EFLA_OK;
+  if (!all_given({x, w, state, y}) || !conv_aligned(dtype, {x, w, bias, state, y})) return EFLA_ERR_INVALID_ARG;
+  const efla::ConvStep a{x, w, bias, state, y, slots, x_row, y_row, N, P, D, W, silu};
+  return by_type(dtype, [&](auto t) { return efla::launch_conv_step<decltype(t)>(a, static_cast<hipStream_t>(stream)); });
+}
+
+size_t efla_conv_bwd_workspace_size(int B, int64_t L, int D, int W) {
+  if (B < 1 || check_conv(B, L, D, W, 0, EFLA_F32, {}) != EFLA_OK || !conv_fits(B, L, B, D) || L == 0) return 0;
+  return efla::conv_bwd_workspace(B, L, D, W);
+}
+
+efla_status efla_conv_bwd(const void* x, int64_t x_row, const void* w, const void* bias, const void* s0, const void* dy,
+                          int64_t dy_row, const void* ds_final, void* dx, int64_t dx_row, float* dw, float* dbias,
+                          void* ds0, int B, int64_t L, int D, int W, int silu, efla_dtype dtype, void* workspace,
+                          size_t workspace_bytes, void* stream) {
+  const efla_status st = check_conv(B, L, D, W, silu, dtype, {x_row, dy_row, dx_row});
+  if (st != EFLA_OK) return st;
+  if (B < 1) return EFLA_ERR_INVALID_ARG;
+  if (!conv_fits(B, L, B, D)) return EFLA_ERR_UNSUPPORTED;
+  if (dw == nullptr || (L > 0 && !all_given({x, w, dy, dx}))) return EFLA_ERR_INVALID_ARG;
+  if (!conv_aligned(dtype, {x, w, bias, s0, dy, ds_final, dx, ds0}) || !aligned_to(dw, 4) || !aligned_to(dbias, 4))
+    return EFLA_ERR_INVALID_ARG;
+  const size_t need = efla_conv_bwd_workspace_size(B, L, D, W);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
+  const efla::ConvBwd a{x, w, bias, s0, dy, ds_final, dx, ds0, dw, dbias, x_row, dy_row, dx_row, B, D, W, silu, L};
+  return by_type(dtype, [&](auto t) {
+    return efla::launch_conv_bwd<decltype(t)>(a, static_cast<float*>(workspace), static_cast<hipStream_t>(stream));
+  });
+}
+
+size_t efla_ssm_fwd_workspace_size(int, int, int, int64_t, int, int, efla_dtype) { return 0; }
+
+efla_status efla_ssm_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
+                         const void* dt, int64_t dt_row, const float* a, const float* d, const float* dt_bias,
+                         const float* s0, void* o, int64_t o_row, float* s_final, int B, int H, int Hk, int64_t L,
+                         int d_k, int d_v, efla_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  efla_status st = check_ssm(B, H, Hk, L, d_k, d_v, dtype);
+  if (st != EFLA_OK) return st;
+  if (B < 1) return EFLA_ERR_INVALID_ARG;
+  const int64_t kw = int64_t(Hk) * d_k, vw = int64_t(H) * d_v;
+  st = check_rows(dtype, {{q_row, kw, true}, {k_row, kw, true}, {v_row, vw, true}, {dt_row, H, false}, {o_row, vw, true}});
+  if (st != EFLA_OK) return st;
+  if (!ssm_fwd_fits(B, H, L, d_v)) return EFLA_ERR_UNSUPPORTED;
+  if (a == nullptr || (L > 0 && !all_given({q, k, v, dt, o}))) return EFLA_ERR_INVALID_ARG;
+  if (!all_aligned16({q, k, v, o})) return EFLA_ERR_INVALID_ARG;
+  const size_t need = efla_ssm_fwd_workspace_size(B, H, Hk, L, d_k, d_v, dtype);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
+  if (L == 0 && s_final == nullptr) return EFLA_OK;
+  const efla::SsmFwd x{q,     k,     v,     dt,     a,     d, dt_bias, s0, o,  s_final, nullptr, nullptr, nullptr,
+                       q_row, k_row, v_row, dt_row, o_row, B, B,       H,  Hk, d_k,     d_v,     L};
+  return ssm_forward(x, dtype, workspace, static_cast<hipStream_t>(stream));
+}
+
+size_t efla_ssm_fwd_varlen_workspace_size(int, int, int, int64_t, int, int, efla_dtype) { return 0; }
+
+efla_status efla_ssm_fwd_varlen(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
+                                const void* dt, int64_t dt_row, const float* a, const float* d, const float* dt_bias,
+                                const int32_t* cu_seqlens, const int32_t* slots, const int32_t* order, int N, int P,
+                                const float* s0, void* o, int64_t o_row, float* s_final, int H, int Hk, int64_t T,
+                                int d_k, int d_v, efla_dtype dtype, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  efla_status st = check_ssm(N, H, Hk, T, d_k, d_v, dtype);
+  if (st != EFLA_OK) return st;
+  if (P < 0 || T > INT32_MAX || (slots == nullptr && P < N)) return EFLA_ERR_INVALID_ARG;
+  const int64_t kw = int64_t(Hk) * d_k, vw = int64_t(H) * d_v;
+  st = check_rows(dtype, {{q_row, kw, true}, {k_row, kw, true}, {v_row, vw, true}, {dt_row, H, false}, {o_row, vw, true}});
+  if (st != EFLA_OK) return st;
+  if (!ssm_fwd_fits(N, H, T, d_v)) return EFLA_ERR_UNSUPPORTED;
+  if (N == 0) return EFLA_OK;
+  if (a == nullptr || cu_seqlens == nullptr || (T > 0 && !all_given({q, k, v, dt, o}))) return EFLA_ERR_INVALID_ARG;
+  if (!all_aligned16({q, k, v, o})) return EFLA_ERR_INVALID_ARG;
+  const size_t need = efla_ssm_fwd_varlen_workspace_size(N, H, Hk, T, d_k, d_v, dtype);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
+  if (T == 0 && s_final == nullptr) return EFLA_OK;
+  const efla::SsmFwd x{q,     k,     v,     dt,     a,     d, dt_bias, s0, o,  s_final, cu_seqlens, slots, order,
+                       q_row, k_row, v_row, dt_row, o_row, N, P,       H,  Hk, d_k,     d_v,        T};
+  return ssm_forward(x, dtype, workspace, static_cast<hipStream_t>(stream));
+}
+
+efla_status efla_ssm_step(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
+                          const void* dt, int64_t dt_row, const float* a, const float* d, const float* dt_bias,
+                          float* state, const int32_t* slots, void* o, int64_t o_row, int N, int P, int H, int Hk,
+                          int d_k, int d_v, efla_dtype dtype, void* stream) {
+  efla_status st = check_ssm(N, H, Hk, 1, d_k, d_v, dtype);
+  if (st != EFLA_OK) return st;
+  if (P < 0 || (slots == nullptr && P < N)) return EFLA_ERR_INVALID_ARG;
+  const int64_t kw = int64_t(Hk) * d_k, vw = int64_t(H) * d_v;
+  st = check_rows(dtype, {{q_row, kw, false}, {k_row, kw, false}, {v_row, vw, false}, {dt_row, H, false}, {o_row, vw, false}});
+  if (st != EFLA_OK) return st;
+  if (efla::ssm_step_threads(N, H, d_v) > efla::kMaxLaunchThreads) return EFLA_ERR_UNSUPPORTED;
+  if (N == 0 || P == 0) return EFLA_OK;
+  if (!all_given({q, k, v, dt, a, state, o}) || !aligned16(state)) return EFLA_ERR_INVALID_ARG;
+  const efla::SsmStep x{q, k, v, dt, a, d, dt_bias, state, slots, o, q_row, k_row, v_row, dt_row, o_row, N, P, H, Hk, d_k, d_v};
+  return by_type(dtype, [&](auto t) { return efla::launch_ssm_step<decltype(t)>(x, static_cast<hipStream_t>(stream)); });
+}
+
+size_t efla_ssm_bwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, efla_dtype dtype) {
+  if (B < 1 || check_ssm(B, H, Hk, L, d_k, d_v, dtype) != EFLA_OK || L == 0 || !ssm_bwd_fits(B, H, L, d_v)) return 0;
+  return efla::ssm_bwd_f32_workspace(B, H, L, d_k, d_v);
+}
+
+efla_status efla_ssm_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
+                         const void* dt, int64_t dt_row, const float* a, const float* d, const float* dt_bias,
+                         const float* s0, const void* d_o, int64_t do_row, const float* ds_final, void* dq,
+                         int64_t dq_row, void* dk, int64_t dk_row, void* dv, int64_t dv_row, void* ddt, int64_t ddt_row,
+                         float* da, float* dd, float* dbias, float* ds0, int B, int H, int Hk, int64_t L, int d_k,
+                         int d_v, efla_dtype dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  efla_status st = check_ssm(B, H, Hk, L, d_k, d_v, dtype);
+  if (st != EFLA_OK) return st;
+  if (B < 1) return EFLA_ERR_INVALID_ARG;
+  const int64_t kw = int64_t(Hk) * d_k, vw = int64_t(H) * d_v;
+  st = check_rows(dtype, {{q_row, kw, true}, {k_row, kw, true}, {v_row, vw, true}, {dt_row, H, false}, {do_row, vw, true},
+                          {dq_row, kw, true}, {dk_row, kw, true}, {dv_row, vw, true}, {ddt_row, H, false}});
+  if (st != EFLA_OK) return st;
+  if (!ssm_bwd_fits(B, H, L, d_v)) return EFLA_ERR_UNSUPPORTED;
+  if (a == nullptr || (L > 0 && !all_given({q, k, v, dt, d_o, dq, dk, dv, ddt}))) return EFLA_ERR_INVALID_ARG;
+  if (!all_aligned16({q, k, v, d_o, dq, dk, dv})) return EFLA_ERR_INVALID_ARG;
+  const size_t need = efla_ssm_bwd_workspace_size(B, H, Hk, L, d_k, d_v, dtype);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
+  const efla::SsmBwd x{q,     k,     v,      dt,     d_o,    a,      d,      dt_bias, s0,      ds_final, dq, dk, dv, ddt, da,
+                       dd,    dbias, ds0,    q_row,  k_row,  v_row,  dt_row, do_row,  dq_row,  dk_row,   dv_row, ddt_row,
+                       B,     H,     Hk,     d_k,    d_v,    L};
+  return by_type(dtype, [&](auto t) {
+    return efla::launch_ssm_bwd_f32<decltype(t)>(x, workspace, static_cast<hipStream_t>(stream));
+  });
+}
+
+}  // extern "C"
+
+namespace {
+
+efla_status check_pools(void* const* pools, const size_t* row_bytes, int count, int N, int P) {
+  if (count < 0 || N < 0 || P < 0 || (count > 0 && (pools == nullptr || row_bytes == nullptr))) return EFLA_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    if (pools[i] == nullptr || row_bytes[i] == 0 || row_bytes[i] % 2 != 0 || !aligned_to(pools[i], 2))
+      return EFLA_ERR_INVALID_ARG;
+    if (row_bytes[i] > (size_t(1) << 40)) return EFLA_ERR_UNSUPPORTED;
+  }
+  for (int i = 0; i < count; i += efla::kPoolsPerLaunch) {
+    int64_t pieces = 0;
+    for (int j = i; j < count && j < i + efla::kPoolsPerLaunch; ++j) pieces += efla::pool_pieces(row_bytes[j]);
+    if (pieces > kMaxGrid || pieces * N * efla::kThreads > efla::kMaxLaunchThreads) return EFLA_ERR_UNSUPPORTED;
+  }
+  return EFLA_OK;
+}
+
+efla_status copy_rows(void* const* pools, const size_t* row_bytes, int count, const int32_t* src, const int32_t* dst, int N,
+                      int P, bool share, hipStream_t s) {
+  for (int i = 0; i < count; i += efla::kPoolsPerLaunch) {
+    efla::PoolSet set{};
+    set.count = count - i < efla::kPoolsPerLaunch ? count - i : efla::kPoolsPerLaunch;
+    for (int j = 0; j < set.count; ++j) {
+      set.base[j] = pools[i + j];
+      set.bytes[j] = row_bytes[i + j];
+      set.first[j + 1] = set.first[j] + uint32_t(efla::pool_pieces(row_bytes[i + j]));
+    }
+    const efla_status st = from_hip(efla::launch_pool_copy(set, src, dst, N, P, share, s));
+    if (st != EFLA_OK) return st;
+  }
+  return EFLA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+efla_status efla_pool_copy(void* const* pools, const size_t* row_bytes, int count, const int32_t* src, const int32_t* dst,
+                           int N, int P, void* stream) {
+  const efla_status st = check_pools(pools, row_bytes, count, N, P);
+  if (st != EFLA_OK) return st;
+  if (N == 0 || P == 0 || count == 0) return EFLA_OK;
+  if (!all_given({src, dst})) return EFLA_ERR_INVALID_ARG;
+  return copy_rows(pools, row_bytes, count, src, dst, N, P, true, static_cast<hipStream_t>(stream));
+}
+
+size_t efla_pool_compact_workspace_size(int N) { return N > 0 ? 8 * size_t(N) : 0; }
+
+efla_status efla_pool_compact(void* const* pools, const size_t* row_bytes, int count, const int32_t* slots, int N, int P,
+                              int32_t* new_slots, int32_t* live, void* workspace, size_t workspace_bytes, void* stream) {
+  const efla_status st = check_pools(pools, row_bytes, count, N, P);
+  if (st != EFLA_OK) return st;
+  if (P > efla::kMaxCompactRows) return EFLA_ERR_UNSUPPORTED;
+  if (live == nullptr || (N > 0 && !all_given({slots, new_slots}))) return EFLA_ERR_INVALID_ARG;
+  const size_t need = efla_pool_compact_workspace_size(N);
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
+  if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
+  auto* src = static_cast<int32_t*>(workspace);
+  int32_t* dst = src + N;
+  const auto s = static_cast<hipStream_t>(stream);
+  const efla_status plan = from_hip(efla::launch_pool_plan(slots, N, P, new_slots, live, src, dst, s));
+  if (plan != EFLA_OK || N == 0 || P == 0) return plan;
+  return copy_rows(pools, row_bytes, count, src, dst, N, P, false, s);
+}
+
+}  // extern "C"

@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from typing import NamedTuple
 
@@ -114,6 +115,41 @@ def lib() -> ctypes.CDLL:
         L.efla_gated_step.argtypes = [_vp] * 8 + [_i, _i, _i, _i, _i, _i, _i, _i, _vp]
         L.efla_pack_plan.restype = _i
         L.efla_pack_plan.argtypes = [_vp, _vp, _i, _i64, _i, _vp, _vp, _vp, _vp, _vp]
+        conv_tail = [_i, _i64, _i, _i, _i, _i]
+        L.efla_conv_fwd.restype = _i
+        L.efla_conv_fwd.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, *conv_tail, _vp]
+        L.efla_conv_fwd_varlen.restype = _i
+        L.efla_conv_fwd_varlen.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _i, _i, _vp, _vp, _i64, _vp, _i64, _i, _i, _i,
+                                           _i, _vp]
+        L.efla_conv_step.restype = _i
+        L.efla_conv_step.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _i64, _i, _i, _i, _i, _i, _i, _vp]
+        L.efla_conv_bwd_workspace_size.restype = _sz
+        L.efla_conv_bwd_workspace_size.argtypes = [_i, _i64, _i, _i]
+        L.efla_conv_bwd.restype = _i
+        L.efla_conv_bwd.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, *conv_tail, _vp,
+                                    _sz, _vp]
+        rows = [_vp, _i64]
+        ssm_in = [*rows * 4, _vp, _vp, _vp]  # q, k, v, dt with their rows; a, d, dt_bias
+        ssm_sizes = [_i, _i, _i, _i64, _i, _i, _i]
+        L.efla_ssm_fwd_workspace_size.restype = L.efla_ssm_fwd_varlen_workspace_size.restype = _sz
+        L.efla_ssm_fwd_workspace_size.argtypes = L.efla_ssm_fwd_varlen_workspace_size.argtypes = ssm_sizes
+        L.efla_ssm_fwd.restype = _i
+        L.efla_ssm_fwd.argtypes = [*ssm_in, _vp, *rows, _vp, *ssm_sizes, _vp, _sz, _vp]
+        L.efla_ssm_fwd_varlen.restype = _i
+        L.efla_ssm_fwd_varlen.argtypes = [*ssm_in, _vp, _vp, _vp, _i, _i, _vp, *rows, _vp, _i, _i, _i64, _i, _i, _i, _vp,
+                                          _sz, _vp]
+        L.efla_ssm_step.restype = _i
+        L.efla_ssm_step.argtypes = [*ssm_in, _vp, _vp, *rows, _i, _i, _i, _i, _i, _i, _i, _vp]
+        L.efla_ssm_bwd_workspace_size.restype = _sz
+        L.efla_ssm_bwd_workspace_size.argtypes = ssm_sizes
+        L.efla_ssm_bwd.restype = _i
+        L.efla_ssm_bwd.argtypes = [*ssm_in, _vp, *rows, _vp, *rows * 4, _vp, _vp, _vp, _vp, *ssm_sizes, _vp, _sz, _vp]
+        L.efla_pool_copy.restype = _i
+        L.efla_pool_copy.argtypes = [_vp, _vp, _i, _vp, _vp, _i, _i, _vp]
+        L.efla_pool_compact_workspace_size.restype = _sz
+        L.efla_pool_compact_workspace_size.argtypes = [_i]
+        L.efla_pool_compact.restype = _i
+        L.efla_pool_compact.argtypes = [_vp, _vp, _i, _vp, _i, _i, _vp, _vp, _vp, _sz, _vp]
         _lib = L
     return _lib
 
@@ -780,6 +816,364 @@ def efla_pack_plan(lengths, tokens: int, starts=None, chunk: int = 64) -> PackPl
     _call(lib().efla_pack_plan, index, "efla_pack_plan", _at(lengths), _at(starts), N, T, chunk, at, at + 4 * (N + 1),
           at + 4 * (2 * N + 1), at + 4 * (2 * N + 1 + T))
     return PackPlan(cu, order, seq, pos)
+
+
+# ---------------------------------------------------------------------------
+# The short causal convolution, the selective state space scan, and the moves of
+# state pools.  Token tensors may be parts of wider rows (slices of a fused
+# projection): only a row's own values must be adjacent, and the rows evenly
+# spaced.
+
+def _placed(index: int, *ts) -> None:
+    """Every tensor given must live on GPU ``index``."""
+    for t in ts:
+        if t is not None and (index < 0 or t.get_device() != index):
+            if not t.is_cuda:
+                raise ValueError("EFLA tensors must live on the GPU")
+            raise ValueError("EFLA tensors must share one device")
+
+
+def _row(t, lead: int, name: str) -> int:
+    """Elements from one token's row to the next of ``t`` [*tokens, ...], its
+    first ``lead`` dimensions the tokens."""
+    sh, st = t.shape, t.stride()
+    if t.numel() == 0:
+        return math.prod(sh[lead:])
+    width = 1
+    for i in range(len(sh) - 1, lead - 1, -1):
+        if sh[i] != 1 and st[i] != width:
+            raise ValueError(f"{name}: the values of a token must be adjacent")
+        width *= sh[i]
+    row, count = width, 1
+    for i in range(lead - 1, -1, -1):  # the innermost token dimension that has a stride sets it
+        if sh[i] == 1:
+            continue
+        if count == 1:
+            row, count = st[i], sh[i]
+        elif st[i] != row * count:
+            raise ValueError(f"{name}: the tokens' rows must be evenly spaced")
+        else:
+            count *= sh[i]
+    if 1 < count and row < width:
+        raise ValueError(f"{name}: the tokens' rows overlap")
+    return row
+
+
+def _offsets(cu_seqlens) -> int:
+    if cu_seqlens.dtype != torch.int32 or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a 1-D int32 tensor of N+1 offsets")
+    return cu_seqlens.numel() - 1
+
+
+def _conv_args(x, w, bias, lead: int, activation, *others):
+    """(device index, D, W, silu) of a convolution's inputs, checked."""
+    if activation not in ("silu", None):
+        raise ValueError(f"unknown activation {activation!r}; use 'silu' or None")
+    if x.dim() != lead + 1 or w.dim() != 2 or w.shape[0] != x.shape[-1] or w.dtype is not x.dtype:
+        dims = {1: "T", 2: "B,L"}[lead]
+        raise ValueError(f"expected x [{dims},D] and w [D,W] of one type")
+    D, W = w.shape
+    _shaped(bias, (D,), "bias", x.dtype)
+    index = x.get_device()
+    _same(index, w, bias, *others)
+    _placed(index, x)
+    return index, D, W, 1 if activation else 0
+
+
+def _out_rows(t, like, lead: int, name: str) -> int:
+    """Row length of an output that is given, checked against ``like``."""
+    _shaped(t, like.shape, name, like.dtype)
+    _placed(like.get_device(), t)
+    return _row(t, lead, name)
+
+
+def efla_conv_fwd(x, w, bias=None, s0=None, activation="silu", y=None, s_final=None, want_final: bool = True):
+    """Short causal convolution over a dense batch: x [B,L,D] (rows evenly
+    spaced), w [D,W] with W 2, 3 or 4, bias [D], s0 [B,W-1,D] the inputs before
+    the first token (None: zeros).  activation: 'silu' or None.  Returns
+    (y [B,L,D], the last W-1 inputs [B,W-1,D] or None)."""
+    index, D, W, silu = _conv_args(x, w, bias, 2, activation, s0, s_final)
+    B, L = x.shape[:2]
+    _shaped(s0, (B, W - 1, D), "s0", x.dtype)
+    _shaped(s_final, (B, W - 1, D), "s_final", x.dtype)
+    if y is None:
+        y = x.new_empty(x.shape)
+    if s_final is None and want_final:
+        s_final = x.new_empty((B, W - 1, D))
+    _call(lib().efla_conv_fwd, index, "efla_conv_fwd", x.data_ptr(), _row(x, 2, "x"), w.data_ptr(), _at(bias), _at(s0),
+          y.data_ptr(), _out_rows(y, x, 2, "y"), _at(s_final), B, L, D, W, silu, _code(x.dtype))
+    return y, s_final
+
+
+def _pool_rows(slots, s0, s_final, N: int, want_final: bool) -> int:
+    """Rows of the state tensors of a packed call."""
+    _shaped(slots, (N,), "slots", torch.int32)
+    if slots is None:
+        return N
+    if s0 is None and s_final is None:
+        raise ValueError("slots need a pool: s0, s_final or both")
+    if s_final is None and want_final:
+        raise ValueError("with slots the final states need a pool: pass s_final (it may be s0), or want_final=False")
+    return (s0 if s0 is not None else s_final).shape[0]
+
+
+def efla_conv_fwd_varlen(x, w, cu_seqlens, bias=None, s0=None, slots=None, activation="silu", y=None, s_final=None,
+                         want_final: bool = True):
+    """Short causal convolution over a packed batch: x [T,D], int32 device
+    offsets cu_seqlens [N+1]; s0 and s_final [N,W-1,D], or with int32 slots [N]
+    pools [P,W-1,D] whose row slots[i] sequence i starts from and ends in (an
+    entry outside the pool: from zeros, final state not written).  Returns
+    (y [T,D], s_final); rows of no sequence are left as they were in a ``y`` that
+    is given, and are zero in one that is made here."""
+    index, D, W, silu = _conv_args(x, w, bias, 1, activation, s0, s_final, cu_seqlens, slots)
+    T, N = x.shape[0], _offsets(cu_seqlens)
+    P = _pool_rows(slots, s0, s_final, N, want_final)
+    _shaped(s0, (P, W - 1, D), "s0", x.dtype)
+    _shaped(s_final, (P, W - 1, D), "s_final", x.dtype)
+    if y is None:
+        y = x.new_zeros(x.shape)
+    if s_final is None and want_final:
+        s_final = x.new_empty((N, W - 1, D))
+    _call(lib().efla_conv_fwd_varlen, index, "efla_conv_fwd_varlen", x.data_ptr(), _row(x, 1, "x"), w.data_ptr(), _at(bias),
+          cu_seqlens.data_ptr(), _at(slots), N, P, _at(s0), y.data_ptr(), _out_rows(y, x, 1, "y"), _at(s_final), T, D, W,
+          silu, _code(x.dtype))
+    return y, s_final
+
+
+def efla_conv_step(x, w, state, bias=None, slots=None, activation="silu", y=None):
+    """One token a request: x [N,D]; the last inputs in ``state`` [P,W-1,D] move up
+    by one in place.  Row n uses state slots[n] (int32 [N]; None: state n); a slot
+    outside the pool skips the row: its row of a ``y`` that is given is left as it
+    was, that of one that is made here is zero.  Returns y [N,D]."""
+    index, D, W, silu = _conv_args(x, w, bias, 1, activation, state, slots)
+    N = x.shape[0]
+    P = N if slots is None or state.dim() != 3 else state.shape[0]
+    if state.shape != (P, W - 1, D) or state.dtype is not x.dtype:
+        raise ValueError("state must be [P,W-1,D] in x's dtype, with P = N where no slots are given")
+    _shaped(slots, (N,), "slots", torch.int32)
+    if y is None:
+        y = x.new_empty(x.shape) if slots is None else x.new_zeros(x.shape)
+    _call(lib().efla_conv_step, index, "efla_conv_step", x.data_ptr(), _row(x, 1, "x"), w.data_ptr(), _at(bias),
+          state.data_ptr(), _at(slots), y.data_ptr(), _out_rows(y, x, 1, "y"), N, P, D, W, silu, _code(x.dtype))
+    return y
+
+
+def efla_conv_bwd_workspace_size(B, L, D, W) -> int:
+    return int(lib().efla_conv_bwd_workspace_size(B, L, D, W))
+
+
+def efla_conv_bwd(x, w, dy, bias=None, s0=None, ds_final=None, activation="silu", want_ds0: bool = True, dx=None,
+                  workspace=None):
+    """Gradients through efla_conv_fwd for dLoss/dy = dy [B,L,D] and
+    dLoss/ds_final = ds_final (None: zero).  Returns (dx, dw, dbias, ds0): dx
+    [B,L,D] and ds0 [B,W-1,D] in x's dtype (ds0 None when want_ds0 is False), dw
+    [D,W] and dbias [D] float32 (dbias None without a bias)."""
+    index, D, W, silu = _conv_args(x, w, bias, 2, activation, s0, ds_final, workspace)
+    B, L = x.shape[:2]
+    _shaped(s0, (B, W - 1, D), "s0", x.dtype)
+    _shaped(ds_final, (B, W - 1, D), "ds_final", x.dtype)
+    if dx is None:
+        dx = x.new_empty(x.shape)
+    dw = x.new_empty((D, W), dtype=_f32)
+    db = None if bias is None else x.new_empty((D,), dtype=_f32)
+    ds0 = x.new_empty((B, W - 1, D)) if want_ds0 else None
+    if workspace is None:
+        n = _gated_workspace("efla_conv_bwd", B, L, D, W)
+        workspace = x.new_empty(n, dtype=torch.uint8) if n else None
+    _call(lib().efla_conv_bwd, index, "efla_conv_bwd", x.data_ptr(), _row(x, 2, "x"), w.data_ptr(), _at(bias), _at(s0),
+          dy.data_ptr(), _out_rows(dy, x, 2, "dy"), _at(ds_final), dx.data_ptr(), _out_rows(dx, x, 2, "dx"), dw.data_ptr(),
+          _at(db), _at(ds0), B, L, D, W, silu, _code(x.dtype), _at(workspace), _nbytes(workspace))
+    return dx, dw, db, ds0
+
+
+def _ssm_args(q, k, v, dt, a, d, dt_bias, lead: int, *others):
+    """(device index, H, Hk, dk, dv, the inputs' addresses and rows) of a scan's
+    inputs, checked."""
+    ty, ks, vs = q.dtype, k.shape, v.shape
+    if len(ks) != lead + 2 or len(vs) != lead + 2 or ks[:lead] != vs[:lead] or q.shape != ks or dt.shape != vs[:-1] \
+            or k.dtype is not ty or v.dtype is not ty or dt.dtype is not ty:
+        dims = {1: "N", 2: "B,L"}[lead]
+        raise ValueError(f"expected q, k [{dims},Hk,dk], v [{dims},H,dv], dt [{dims},H] of one type")
+    H, Hk = vs[lead], ks[lead]
+    if Hk < 1 or H % Hk:
+        raise ValueError(f"the {H} value heads must be a multiple of the {Hk} query and key heads")
+    if a.shape != (H,) or a.dtype is not _f32:
+        raise ValueError("a must be float32 [H]")
+    _shaped(d, (H,), "d", _f32)
+    _shaped(dt_bias, (H,), "dt_bias", _f32)
+    index = q.get_device()
+    _placed(index, q, k, v, dt)
+    _same(index, a, d, dt_bias, *others)
+    ins = (q.data_ptr(), _row(q, lead, "q"), k.data_ptr(), _row(k, lead, "k"), v.data_ptr(), _row(v, lead, "v"),
+           dt.data_ptr(), _row(dt, lead, "dt"), a.data_ptr(), _at(d), _at(dt_bias))
+    return index, H, Hk, ks[-1], vs[-1], ins
+
+
+def efla_ssm_fwd_workspace_size(B, H, Hk, L, d_k, d_v, dtype) -> int:
+    return int(lib().efla_ssm_fwd_workspace_size(B, H, Hk, L, d_k, d_v, _code(dtype)))
+
+
+def efla_ssm_fwd(q, k, v, dt, a, d=None, dt_bias=None, s0=None, o=None, s_final=None, workspace=None,
+                 want_final: bool = True):
+    """Selective state space scan over a dense batch: S_t = e^{a D_t} S_{t-1} +
+    D_t k_t v_t^T, o_t = S_t^T q_t + d v_t with D_t = softplus(dt_t + dt_bias).
+    q, k [B,L,Hk,dk], v [B,L,H,dv], dt [B,L,H] in one type, rows evenly spaced;
+    a, d, dt_bias float32 [H].  Returns (o [B,L,H,dv] in q's dtype, S_L float32
+    [B,H,dk,dv] or None)."""
+    index, H, Hk, dk, dv, ins = _ssm_args(q, k, v, dt, a, d, dt_bias, 2, s0, s_final, workspace)
+    B, L = k.shape[:2]
+    _shaped(s0, (B, H, dk, dv), "s0", _f32)
+    _shaped(s_final, (B, H, dk, dv), "s_final", _f32)
+    if o is None:
+        o = v.new_empty(v.shape)
+    if s_final is None and want_final:
+        s_final = a.new_empty((B, H, dk, dv))
+    code = _code(q.dtype)
+    if workspace is None:
+        n = _gated_workspace("efla_ssm_fwd", B, H, Hk, L, dk, dv, code)
+        workspace = q.new_empty(n, dtype=torch.uint8) if n else None
+    _call(lib().efla_ssm_fwd, index, "efla_ssm_fwd", *ins, _at(s0), o.data_ptr(), _out_rows(o, v, 2, "o"), _at(s_final), B,
+          H, Hk, L, dk, dv, code, _at(workspace), _nbytes(workspace))
+    return o, s_final
+
+
+def efla_ssm_fwd_varlen_workspace_size(N, H, Hk, T, d_k, d_v, dtype) -> int:
+    return int(lib().efla_ssm_fwd_varlen_workspace_size(N, H, Hk, T, d_k, d_v, _code(dtype)))
+
+
+def efla_ssm_fwd_varlen(q, k, v, dt, a, cu_seqlens, d=None, dt_bias=None, s0=None, slots=None, order=None, o=None,
+                        s_final=None, workspace=None, want_final: bool = True):
+    """Selective state space scan over a packed batch: q, k [T,Hk,dk], v [T,H,dv],
+    dt [T,H], int32 device offsets cu_seqlens [N+1]; s0, s_final, slots and order
+    as in efla_gated_chunk_fwd_varlen.  Returns (o shaped like v, s_final); rows of
+    no sequence are left as they were in an ``o`` that is given, and are zero in
+    one that is made here."""
+    index, H, Hk, dk, dv, ins = _ssm_args(q, k, v, dt, a, d, dt_bias, 1, s0, s_final, workspace, cu_seqlens, slots, order)
+    T, N = k.shape[0], _offsets(cu_seqlens)
+    _shaped(order, (N,), "order", torch.int32)
+    P = _pool_rows(slots, s0, s_final, N, want_final)
+    _shaped(s0, (P, H, dk, dv), "s0", _f32)
+    _shaped(s_final, (P, H, dk, dv), "s_final", _f32)
+    if o is None:
+        o = v.new_zeros(v.shape)
+    if s_final is None and want_final:
+        s_final = a.new_empty((N, H, dk, dv))
+    code = _code(q.dtype)
+    if workspace is None:
+        n = _gated_workspace("efla_ssm_fwd_varlen", N, H, Hk, T, dk, dv, code)
+        workspace = q.new_empty(n, dtype=torch.uint8) if n else None
+    _call(lib().efla_ssm_fwd_varlen, index, "efla_ssm_fwd_varlen", *ins, cu_seqlens.data_ptr(), _at(slots), _at(order), N, P,
+          _at(s0), o.data_ptr(), _out_rows(o, v, 1, "o"), _at(s_final), H, Hk, T, dk, dv, code, _at(workspace),
+          _nbytes(workspace))
+    return o, s_final
+
+
+def efla_ssm_step(q, k, v, dt, a, state, d=None, dt_bias=None, slots=None, o=None):
+    """One token a request, in place on a pool of states [P,H,dk,dv] (fp32): q, k
+    [N,Hk,dk], v [N,H,dv], dt [N,H] in one type.  Row n updates state slots[n]
+    (int32 [N]; None: state n); a slot outside the pool skips the row: its row of
+    an ``o`` that is given is left as it was, that of one that is made here is
+    zero.  Returns o [N,H,dv]."""
+    index, H, Hk, dk, dv, ins = _ssm_args(q, k, v, dt, a, d, dt_bias, 1, state, slots)
+    N = k.shape[0]
+    P = N if slots is None or state.dim() != 4 else state.shape[0]
+    if state.shape != (P, H, dk, dv) or state.dtype is not _f32:
+        raise ValueError("state must be float32 [P,H,dk,dv], with P = N where no slots are given")
+    _shaped(slots, (N,), "slots", torch.int32)
+    if o is None:
+        o = v.new_empty(v.shape) if slots is None else v.new_zeros(v.shape)
+    _call(lib().efla_ssm_step, index, "efla_ssm_step", *ins, state.data_ptr(), _at(slots), o.data_ptr(),
+          _out_rows(o, v, 1, "o"), N, P, H, Hk, dk, dv, _code(q.dtype))
+    return o
+
+
+def efla_ssm_bwd_workspace_size(B, H, Hk, L, d_k, d_v, dtype) -> int:
+    return int(lib().efla_ssm_bwd_workspace_size(B, H, Hk, L, d_k, d_v, _code(dtype)))
+
+
+def efla_ssm_bwd(q, k, v, dt, a, d_o, d=None, dt_bias=None, s0=None, ds_final=None, want_ds0: bool = True, dq=None, dk=None,
+                 dv=None, ddt=None, workspace=None):
+    """Gradients through efla_ssm_fwd for dLoss/do = d_o and dLoss/dS_L = ds_final
+    (None: zero).  Returns (dq, dk, dv, ddt, da, dd, ddt_bias, ds0): the first
+    four in q's dtype (dq and dk summed over the value heads that share a head;
+    each may be given, a part of wider rows), the others float32 (dd and ddt_bias
+    None without d and dt_bias, ds0 None when want_ds0 is False)."""
+    index, H, Hk, K, V, ins = _ssm_args(q, k, v, dt, a, d, dt_bias, 2, s0, ds_final, workspace)
+    B, L = k.shape[:2]
+    _shaped(s0, (B, H, K, V), "s0", _f32)
+    _shaped(ds_final, (B, H, K, V), "ds_final", _f32)
+    outs, at = [], []
+    for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv"), (ddt, dt, "ddt")):
+        t = like.new_empty(like.shape) if t is None else t
+        outs.append(t)
+        at += [t.data_ptr(), _out_rows(t, like, 2, name)]
+    da = a.new_empty((H,))
+    dd, db = (None if t is None else a.new_empty((H,)) for t in (d, dt_bias))
+    ds0 = a.new_empty((B, H, K, V)) if want_ds0 else None
+    code = _code(q.dtype)
+    if workspace is None:
+        n = _gated_workspace("efla_ssm_bwd", B, H, Hk, L, K, V, code)
+        workspace = q.new_empty(n, dtype=torch.uint8) if n else None
+    _call(lib().efla_ssm_bwd, index, "efla_ssm_bwd", *ins, _at(s0), d_o.data_ptr(), _out_rows(d_o, v, 2, "d_o"),
+          _at(ds_final), *at, da.data_ptr(), _at(dd), _at(db), _at(ds0), B, H, Hk, L, K, V, code, _at(workspace),
+          _nbytes(workspace))
+    return (*outs, da, dd, db, ds0)
+
+
+def _pool_set(pools, index: int):
+    """(P, pointer array, row size array, count) of pools [P, ...] on one GPU."""
+    if not pools:
+        raise ValueError("no pools given")
+    P = pools[0].shape[0] if pools[0].dim() else 0
+    for t in pools:
+        if t.dim() < 2 or t.shape[0] != P:
+            raise ValueError("every pool must be [P, ...] with the same number of rows")
+        if not t.is_floating_point() or t.numel() == 0:
+            raise ValueError("pools must hold floating-point rows")
+    _same(index, *pools)
+    n = len(pools)
+    at = (_vp * n)(*(t.data_ptr() for t in pools))
+    size = (_sz * n)(*(t.stride(0) * t.element_size() if t.shape[0] > 1 else _nbytes(t) for t in pools))
+    return P, at, size, n
+
+
+def _entries(t, name: str) -> None:
+    if t.dim() != 1 or t.dtype != torch.int32:
+        raise ValueError(f"{name} must be a 1-D int32 tensor")
+
+
+def efla_pool_copy(pools, src, dst) -> None:
+    """In every pool [P, ...] of ``pools`` (all layers' states), row src[i] to row
+    dst[i] (int32 [N] on the device): forks where a source is named often; a src
+    outside the pool clears row dst[i], a dst outside it does nothing.  A row may
+    not be named twice in dst, nor in both."""
+    _entries(src, "src")
+    _shaped(dst, src.shape, "dst", torch.int32)
+    index = src.get_device()
+    P, at, size, n = _pool_set(pools, index)
+    _same(index, src, dst)
+    _call(lib().efla_pool_copy, index, "efla_pool_copy", at, size, n, src.data_ptr(), dst.data_ptr(), src.numel(), P)
+
+
+def efla_pool_compact(pools, slots, new_slots=None):
+    """Moves the rows in use, the K distinct rows that ``slots`` (int32 [N] on the
+    device) names, to rows 0 .. K-1 of every pool: those at K or above go, in
+    ascending order, into the unused ones below.  Returns (new_slots, live): each
+    entry's row afterwards (entries outside the pool stay; new_slots may be slots)
+    and K as an int32 [1], both on the device."""
+    _entries(slots, "slots")
+    _shaped(new_slots, slots.shape, "new_slots", torch.int32)
+    index = slots.get_device()
+    P, at, size, n = _pool_set(pools, index)
+    _same(index, slots, new_slots)
+    N = slots.numel()
+    if new_slots is None:
+        new_slots = torch.empty_like(slots)
+    live = slots.new_empty(1)
+    workspace = slots.new_empty(2 * N) if N else None
+    _call(lib().efla_pool_compact, index, "efla_pool_compact", at, size, n, slots.data_ptr(), N, P, new_slots.data_ptr(),
+          live.data_ptr(), _at(workspace), _nbytes(workspace))
+    return new_slots, live
 
 
 class PreparedCall:

@@ -460,6 +460,153 @@ efla_status efla_pack_plan(const int32_t *lengths, const int32_t *starts, int N,
                            int32_t *cu_seqlens, int32_t *order, int32_t *token_seq, int32_t *token_pos,
                            void *stream);
 
+/*
+ * The short causal convolution of a layer's projections: depthwise over the
+ * last W tokens, with bias and SiLU, per channel
+ *     u_t = bias + sum_{i < W} w_i x_{t-W+1+i},     y_t = u_t / (1 + e^{-u_t})
+ * (y_t = u_t with silu = 0).  W is 2, 3 or 4 (else EFLA_ERR_UNSUPPORTED), the
+ * number of channels D any from 1 on.
+ *   - x, y (and their gradients) [B, L, D] or packed [T, D] or, for one token a
+ *     request, [N, D] in dtype, whose rows need not be adjacent: *_row is the
+ *     number of elements from one token's row to the next (>= D, < 2^24), the
+ *     same over all B * L rows; a row's channels are adjacent.  w [D, W] and
+ *     bias [D] (nullable) in dtype.
+ *   - A state is the last W - 1 inputs, [W - 1, D] in dtype, oldest first.  s0
+ *     and s_final hold one for each sequence (NULL: zeros, and not written) or,
+ *     with slots, are pools of P of them, as in efla_gated_chunk_fwd_varlen;
+ *     s_final may be s0.  y may not overlap x or a state.
+ *   - Arithmetic is float32, rounded once.  Where every tensor and row starts on
+ *     16 bytes (D and the row lengths a multiple of 8 in bf16, of 4 in float32)
+ *     memory moves in 16-byte pieces, else in single elements, several times
+ *     slower; only alignment to the element is required.
+ *   - A call whose largest launch would have 2^32 threads or more is
+ *     EFLA_ERR_UNSUPPORTED.
+ *
+ * efla_conv_fwd -- dense batch.  L may be 0: the state is copied.
+ * efla_conv_fwd_varlen -- packed batch: sequence i is rows cu_seqlens[i] ..
+ *     cu_seqlens[i + 1] - 1 (offsets int32 [N + 1], DEVICE memory, not
+ *     decreasing, clamped into [0, T]); rows of no sequence are left as they
+ *     were.  slots as in efla_gated_chunk_fwd_varlen (P >= N where NULL); T < 2^31.
+ * efla_conv_step -- one token a request: state [P, W - 1, D] is moved up by one
+ *     token in place; slots as in efla_gated_step (a slot outside the pool skips
+ *     the row; a slot named twice is unspecified).
+ * efla_conv_bwd -- gradients through efla_conv_fwd: dx [B, L, D] in dtype, dw
+ *     [D, W] and dbias [D] float32 (dbias nullable), ds0 [B, W - 1, D] in dtype
+ *     (nullable), for dLoss/dy = dy and dLoss/ds_final = ds_final (nullable:
+ *     zero).  dw and dbias are summed in float32 in a fixed order.
+ */
+efla_status efla_conv_fwd(const void *x, int64_t x_row, const void *w, const void *bias, const void *s0, void *y,
+                          int64_t y_row, void *s_final, int B, int64_t L, int D, int W, int silu,
+                          efla_dtype dtype, void *stream);
+efla_status efla_conv_fwd_varlen(const void *x, int64_t x_row, const void *w, const void *bias,
+                                 const int32_t *cu_seqlens, const int32_t *slots, int N, int P, const void *s0,
+                                 void *y, int64_t y_row, void *s_final, int64_t T, int D, int W, int silu,
+                                 efla_dtype dtype, void *stream);
+efla_status efla_conv_step(const void *x, int64_t x_row, const void *w, const void *bias, void *state,
+                           const int32_t *slots, void *y, int64_t y_row, int N, int P, int D, int W, int silu,
+                           efla_dtype dtype, void *stream);
+size_t efla_conv_bwd_workspace_size(int B, int64_t L, int D, int W);
+efla_status efla_conv_bwd(const void *x, int64_t x_row, const void *w, const void *bias, const void *s0,
+                          const void *dy, int64_t dy_row, const void *ds_final, void *dx, int64_t dx_row,
+                          float *dw, float *dbias, void *ds0, int B, int64_t L, int D, int W, int silu,
+                          efla_dtype dtype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The selective state space scan: the associative state without the delta
+ * rule's correction, decayed by a step size of each token's own,
+ *     D_t = softplus(dt_t + dt_bias),
+ *     S_t = exp(a D_t) S_{t-1} + D_t k_t v_t^T,     o_t = S_t^T q_t + d v_t,
+ * with k and q a state space model's input and output projections, v its
+ * inputs, a its rate (negative; the parameter itself, not its logarithm) and d
+ * its skip.
+ *   - q, k [.., Hk, d_k], v, o [.., H, d_v], dt [.., H] in dtype; a, d, dt_bias
+ *     [H] float32 (d and dt_bias nullable: zero); states [.., H, d_k, d_v]
+ *     float32.  H a multiple of Hk: value head h reads head h / (H / Hk).  Head
+ *     sizes 16, 32, 64 or 128.
+ *   - The rows of q, k, v, dt and o (and their gradients) need not be adjacent,
+ *     so that they may be parts of one projection's rows: *_row is the number of
+ *     elements from one token's row to the next (at least the row's own length,
+ *     < 2^24), the same over all rows.  q, k, v, o, their gradients and their rows
+ *     start on 16 bytes (EFLA_ERR_INVALID_ARG otherwise); dt is free.
+ *   - A decay below e^{-128} is zero in float32, and so it acts.  A token's step
+ *     size may be zero (dt of -inf): it leaves the state as it was.
+ *   - States are carried in float32.  For bf16 inputs, matrix-core products that
+ *     feed a state or a float32 gradient take each float32 operand as the sum of
+ *     two bf16 values (16 significant bits), so these are good to about 1e-5;
+ *     products that only feed bf16 outputs round such operands once.
+ *   - A NaN or an infinity in a token's row reaches its sequence's outputs from
+ *     the start of its chunk of 64 tokens on, not only from the token on; never
+ *     another sequence's.
+ *   - A call whose largest launch would have 2^32 threads or more is
+ *     EFLA_ERR_UNSUPPORTED.
+ *
+ * efla_ssm_fwd -- dense batch [B, L, ..]; s0, s_final [B, H, d_k, d_v] (each
+ *     nullable; s_final may be s0).  L may be 0: the state is copied.
+ * efla_ssm_fwd_varlen -- packed batch [T, ..] with cu_seqlens, slots, P and order
+ *     as in efla_gated_chunk_fwd_varlen.
+ * efla_ssm_step -- one token a request, in place on a pool, as efla_gated_step.
+ * efla_ssm_bwd -- gradients through efla_ssm_fwd for dLoss/do = d_o and
+ *     dLoss/ds_final = ds_final (nullable: zero): dq, dk (summed over the value
+ *     heads that share a head), dv, ddt in dtype, da, dd, dbias [H] and ds0
+ *     [B, H, d_k, d_v] float32 (these four nullable: not written).  Every sum has
+ *     a fixed order.  Outputs may be parts of one tensor's rows.
+ */
+size_t efla_ssm_fwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, efla_dtype dtype);
+efla_status efla_ssm_fwd(const void *q, int64_t q_row, const void *k, int64_t k_row, const void *v, int64_t v_row,
+                         const void *dt, int64_t dt_row, const float *a, const float *d, const float *dt_bias,
+                         const float *s0, void *o, int64_t o_row, float *s_final, int B, int H, int Hk, int64_t L,
+                         int d_k, int d_v, efla_dtype dtype, void *workspace, size_t workspace_bytes,
+                         void *stream);
+size_t efla_ssm_fwd_varlen_workspace_size(int N, int H, int Hk, int64_t T, int d_k, int d_v, efla_dtype dtype);
+efla_status efla_ssm_fwd_varlen(const void *q, int64_t q_row, const void *k, int64_t k_row, const void *v,
+                                int64_t v_row, const void *dt, int64_t dt_row, const float *a, const float *d,
+                                const float *dt_bias, const int32_t *cu_seqlens, const int32_t *slots,
+                                const int32_t *order, int N, int P, const float *s0, void *o, int64_t o_row,
+                                float *s_final, int H, int Hk, int64_t T, int d_k, int d_v, efla_dtype dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+efla_status efla_ssm_step(const void *q, int64_t q_row, const void *k, int64_t k_row, const void *v, int64_t v_row,
+                          const void *dt, int64_t dt_row, const float *a, const float *d, const float *dt_bias,
+                          float *state, const int32_t *slots, void *o, int64_t o_row, int N, int P, int H, int Hk,
+                          int d_k, int d_v, efla_dtype dtype, void *stream);
+size_t efla_ssm_bwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, efla_dtype dtype);
+efla_status efla_ssm_bwd(const void *q, int64_t q_row, const void *k, int64_t k_row, const void *v, int64_t v_row,
+                         const void *dt, int64_t dt_row, const float *a, const float *d, const float *dt_bias,
+                         const float *s0, const void *d_o, int64_t do_row, const float *ds_final, void *dq,
+                         int64_t dq_row, void *dk, int64_t dk_row, void *dv, int64_t dv_row, void *ddt,
+                         int64_t ddt_row, float *da, float *dd, float *dbias, float *ds0, int B, int H, int Hk,
+                         int64_t L, int d_k, int d_v, efla_dtype dtype, void *workspace, size_t workspace_bytes,
+                         void *stream);
+
+/*
+ * Moves of whole rows of state pools.  A serving program keeps one pool a layer
+ * and kind of state, all with P rows and row i of each that of one request; these
+ * calls move the rows of all of them in one launch (64 pools a launch).
+ *   pools, row_bytes -- HOST arrays of `count` DEVICE pointers and row sizes
+ *       (even, any size otherwise; 16-byte aligned pools with rows of a multiple
+ *       of 16 bytes move in 16-byte pieces).  Pools may not overlap.
+ *
+ * efla_pool_copy -- row src[i] of every pool to its row dst[i], i < N (int32,
+ *     DEVICE memory): src[i] outside [0, P) clears row dst[i] to zero bytes, dst[i]
+ *     outside [0, P) does nothing.  A source may be named often (a request forked
+ *     into several: it is read once).  The entries cannot be checked here: a row
+ *     that is the destination of two entries, or a destination and a source, holds
+ *     unspecified bytes afterwards, as does what is copied from it; no access
+ *     leaves the pools.
+ * efla_pool_compact -- with K distinct rows in [0, P) named by slots [N] (int32,
+ *     DEVICE memory), moves those at K or above, in ascending order, into the rows
+ *     below K that slots does not name, in ascending order, so that rows 0 .. K-1
+ *     are the ones in use, and writes each entry's new row into new_slots [N] (which
+ *     may be slots; entries outside [0, P) stay) and K into live [1].  Rows at K
+ *     and above keep their bytes.  P <= 131072 (EFLA_ERR_UNSUPPORTED above).
+ *     Workspace: 8 N bytes, aligned to 16.
+ */
+efla_status efla_pool_copy(void *const *pools, const size_t *row_bytes, int count, const int32_t *src,
+                           const int32_t *dst, int N, int P, void *stream);
+size_t efla_pool_compact_workspace_size(int N);
+efla_status efla_pool_compact(void *const *pools, const size_t *row_bytes, int count, const int32_t *slots, int N,
+                              int P, int32_t *new_slots, int32_t *live, void *workspace, size_t workspace_bytes,
+                              void *stream);
+
 #ifdef __cplusplus
 }
 #endif
