@@ -311,6 +311,10 @@ struct SsmBwd {
 template <typename T>
 hipError_t launch_ssm_f32(const SsmFwd& a, hipStream_t s);
 int64_t ssm_f32_threads(int64_t seqs, int H, int DV);
+// bf16, d_k 64 or 128, d_v a multiple of 32, 64 tokens at a time (ssm_chunk.h).
+bool ssm_chunk_supported(int DK, int DV);
+hipError_t launch_ssm_chunk(const SsmFwd& a, hipStream_t s);
+int64_t ssm_chunk_threads(int64_t seqs, int H, int DV);
 template <typename T>
 hipError_t launch_ssm_bwd_f32(const SsmBwd& b, void* ws, hipStream_t s);
 size_t ssm_bwd_f32_workspace(int B, int H, int64_t L, int DK, int DV);

@@ -76,11 +76,15 @@ bool all_aligned16(std::initializer_list<const void*> ptrs) {
 
 // Whether the forward's launches over these sequences have fewer threads than the
 // runtime takes.
-bool ssm_fwd_fits(int64_t seqs, int H, int64_t, int d_v) {
-  return efla::ssm_f32_threads(seqs, H, d_v) <= efla::kMaxLaunchThreads;
+bool ssm_chunked(int d_k, int d_v, efla_dtype dt) { return dt == EFLA_BF16 && efla::ssm_chunk_supported(d_k, d_v); }
+
+bool ssm_fwd_fits(int64_t seqs, int H, int d_k, int d_v, efla_dtype dt) {
+  return (ssm_chunked(d_k, d_v, dt) ? efla::ssm_chunk_threads(seqs, H, d_v) : efla::ssm_f32_threads(seqs, H, d_v)) <=
+         efla::kMaxLaunchThreads;
 }
 
 efla_status ssm_forward(const efla::SsmFwd& a, efla_dtype dt, void*, hipStream_t s) {
+  if (ssm_chunked(a.DK, a.DV, dt)) return from_hip(efla::launch_ssm_chunk(a, s));
   return by_type(dt, [&](auto t) { return efla::launch_ssm_f32<decltype(t)>(a, s); });
 }
 
@@ -172,7 +176,7 @@ efla_status efla_ssm_fwd(const void* q, int64_t q_row, const void* k, int64_t k_
   const int64_t kw = int64_t(Hk) * d_k, vw = int64_t(H) * d_v;
   st = check_rows(dtype, {{q_row, kw, true}, {k_row, kw, true}, {v_row, vw, true}, {dt_row, H, false}, {o_row, vw, true}});
   if (st != EFLA_OK) return st;
-  if (!ssm_fwd_fits(B, H, L, d_v)) return EFLA_ERR_UNSUPPORTED;
+  if (!ssm_fwd_fits(B, H, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
   if (a == nullptr || (L > 0 && !all_given({q, k, v, dt, o}))) return EFLA_ERR_INVALID_ARG;
   if (!all_aligned16({q, k, v, o})) return EFLA_ERR_INVALID_ARG;
   const size_t need = efla_ssm_fwd_workspace_size(B, H, Hk, L, d_k, d_v, dtype);
@@ -198,7 +202,7 @@ efla_status efla_ssm_fwd_varlen(const void* q, int64_t q_row, const void* k, int
   const int64_t kw = int64_t(Hk) * d_k, vw = int64_t(H) * d_v;
   st = check_rows(dtype, {{q_row, kw, true}, {k_row, kw, true}, {v_row, vw, true}, {dt_row, H, false}, {o_row, vw, true}});
   if (st != EFLA_OK) return st;
-  if (!ssm_fwd_fits(N, H, T, d_v)) return EFLA_ERR_UNSUPPORTED;
+  if (!ssm_fwd_fits(N, H, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
   if (N == 0) return EFLA_OK;
   if (a == nullptr || cu_seqlens == nullptr || (T > 0 && !all_given({q, k, v, dt, o}))) return EFLA_ERR_INVALID_ARG;
   if (!all_aligned16({q, k, v, o})) return EFLA_ERR_INVALID_ARG;

@@ -1,0 +1,25 @@
+// ssm_chunk.hip -- launches of the chunked scan for bf16 inputs (ssm_chunk.h).
+#include "launchers.h"
+#include "ssm_chunk.h"
+
+namespace efla {
+
+bool ssm_chunk_supported(int DK, int DV) { return (DK == 64 || DK == 128) && DV % 32 == 0; }
+
+int64_t ssm_chunk_threads(int64_t seqs, int H, int DV) { return seqs * H * (DV / 32) * SsmShape<64>::THREADS; }
+
+template <int DK>
+static hipError_t chunk_impl(const SsmFwd& a, hipStream_t s) {
+  const int NVB = a.DV / 32;
+  const int64_t bh = int64_t(a.N) * a.H;
+  const int r = a.H / a.Hk;
+  // heads that share their queries and keys on one XCD, whose L2 then serves them;
+  // packed sequences differ in length, so there only a head's own value blocks
+  const int remap = a.cu == nullptr && bh / r % 8 == 0 ? r : bh % 8 == 0 ? 1 : 0;
+  hipLaunchKernelGGL((ssm_chunk_kernel<DK>), dim3(unsigned(bh * NVB)), dim3(SsmShape<DK>::THREADS), 0, s, a, NVB, remap);
+  return hipGetLastError();
+}
+
+hipError_t launch_ssm_chunk(const SsmFwd& a, hipStream_t s) { return a.DK == 64 ? chunk_impl<64>(a, s) : chunk_impl<128>(a, s); }
+
+}  // namespace efla
