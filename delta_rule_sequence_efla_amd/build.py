@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(HERE, "libefla.so")
 SOURCES = ["api.hip", "step_kernels.hip", "chunk_bf16.hip", "chunk_bf16_roles.hip", "chunk_bf16_split.hip",
            "chunk_bf16_states.hip", "ut_bf16.hip", "chunk_f32.hip", "bwd.hip", "bwd_bf16_chunk.hip", "seg.hip",
            "gated_api.hip", "gated_fwd.hip", "gated_step.hip", "gated_blocks.hip", "gated_bwd.hip", "gated_bwd_bf16.hip", "plan.hip",
-           "ssm_api.hip", "conv.hip", "pool.hip", "ssm_step.hip", "ssm_f32.hip", "ssm_chunk.hip"]
+           "ssm_api.hip", "conv.hip", "pool.hip", "ssm_step.hip", "ssm_f32.hip", "ssm_chunk.hip", "ssm_bwd_chunk.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 CFLAGS = [
@@ -41,7 +41,8 @@ SOURCE_FLAGS = {"chunk_bf16_roles.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "gated_blocks.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "gated_fwd.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
                 "gated_bwd_bf16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
-                "ssm_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+                "ssm_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+                "ssm_bwd_chunk.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str) -> str:

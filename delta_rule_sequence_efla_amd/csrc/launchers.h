@@ -317,6 +317,12 @@ hipError_t launch_ssm_chunk(const SsmFwd& a, hipStream_t s);
 int64_t ssm_chunk_threads(int64_t seqs, int H, int DV);
 template <typename T>
 hipError_t launch_ssm_bwd_f32(const SsmBwd& b, void* ws, hipStream_t s);
+// da, dbias and dd (each nullable) of every head from the partial sums [3][H][M].
+hipError_t launch_ssm_sums(const float* part, float* da, float* dbias, float* dd, int64_t M, int H, hipStream_t s);
+// For the shapes of the chunked forward (ssm_bwd_chunk.h), L > 0.
+size_t ssm_bwd_chunk_workspace(int B, int H, int64_t L, int DK, int DV);
+int64_t ssm_bwd_chunk_threads(int B, int H, int64_t L, int DV);
+hipError_t launch_ssm_bwd_chunk(const SsmBwd& b, void* ws, hipStream_t s);
 size_t ssm_bwd_f32_workspace(int B, int H, int64_t L, int DK, int DV);
 int64_t ssm_bwd_f32_threads(int B, int H, int64_t L, int DV);
 

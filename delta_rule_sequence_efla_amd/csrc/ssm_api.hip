@@ -88,8 +88,12 @@ efla_status ssm_forward(const efla::SsmFwd& a, efla_dtype dt, void*, hipStream_t
   return by_type(dt, [&](auto t) { return efla::launch_ssm_f32<decltype(t)>(a, s); });
 }
 
-bool ssm_bwd_fits(int B, int H, int64_t L, int d_v) {
-  return int64_t(B) * H * ((L + 31) / 32) <= kMaxGrid && efla::ssm_bwd_f32_threads(B, H, L, d_v) <= efla::kMaxLaunchThreads;
+bool ssm_bwd_chunked(int64_t L, int d_k, int d_v, efla_dtype dt) { return L > 0 && ssm_chunked(d_k, d_v, dt); }
+
+bool ssm_bwd_fits(int B, int H, int64_t L, int d_k, int d_v, efla_dtype dt) {
+  if (int64_t(B) * H * ((L + 31) / 32) > kMaxGrid) return false;
+  return (ssm_bwd_chunked(L, d_k, d_v, dt) ? efla::ssm_bwd_chunk_threads(B, H, L, d_v)
+                                           : efla::ssm_bwd_f32_threads(B, H, L, d_v)) <= efla::kMaxLaunchThreads;
 }
 
 }  // namespace
@@ -233,8 +237,9 @@ efla_status efla_ssm_step(const void* q, int64_t q_row, const void* k, int64_t k
 }
 
 size_t efla_ssm_bwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, efla_dtype dtype) {
-  if (B < 1 || check_ssm(B, H, Hk, L, d_k, d_v, dtype) != EFLA_OK || L == 0 || !ssm_bwd_fits(B, H, L, d_v)) return 0;
-  return efla::ssm_bwd_f32_workspace(B, H, L, d_k, d_v);
+  if (B < 1 || check_ssm(B, H, Hk, L, d_k, d_v, dtype) != EFLA_OK || L == 0 || !ssm_bwd_fits(B, H, L, d_k, d_v, dtype)) return 0;
+  return ssm_bwd_chunked(L, d_k, d_v, dtype) ? efla::ssm_bwd_chunk_workspace(B, H, L, d_k, d_v)
+                                             : efla::ssm_bwd_f32_workspace(B, H, L, d_k, d_v);
 }
 
 efla_status efla_ssm_bwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
@@ -250,7 +255,7 @@ efla_status efla_ssm_bwd(const void* q, int64_t q_row, const void* k, int64_t k_
   st = check_rows(dtype, {{q_row, kw, true}, {k_row, kw, true}, {v_row, vw, true}, {dt_row, H, false}, {do_row, vw, true},
                           {dq_row, kw, true}, {dk_row, kw, true}, {dv_row, vw, true}, {ddt_row, H, false}});
   if (st != EFLA_OK) return st;
-  if (!ssm_bwd_fits(B, H, L, d_v)) return EFLA_ERR_UNSUPPORTED;
+  if (!ssm_bwd_fits(B, H, L, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
   if (a == nullptr || (L > 0 && !all_given({q, k, v, dt, d_o, dq, dk, dv, ddt}))) return EFLA_ERR_INVALID_ARG;
   if (!all_aligned16({q, k, v, d_o, dq, dk, dv})) return EFLA_ERR_INVALID_ARG;
   const size_t need = efla_ssm_bwd_workspace_size(B, H, Hk, L, d_k, d_v, dtype);
@@ -259,6 +264,7 @@ efla_status efla_ssm_bwd(const void* q, int64_t q_row, const void* k, int64_t k_
   const efla::SsmBwd x{q,     k,     v,      dt,     d_o,    a,      d,      dt_bias, s0,      ds_final, dq, dk, dv, ddt, da,
                        dd,    dbias, ds0,    q_row,  k_row,  v_row,  dt_row, do_row,  dq_row,  dk_row,   dv_row, ddt_row,
                        B,     H,     Hk,     d_k,    d_v,    L};
+  if (ssm_bwd_chunked(L, d_k, d_v, dtype)) return from_hip(efla::launch_ssm_bwd_chunk(x, workspace, static_cast<hipStream_t>(stream)));
   return by_type(dtype, [&](auto t) {
     return efla::launch_ssm_bwd_f32<decltype(t)>(x, workspace, static_cast<hipStream_t>(stream));
   });

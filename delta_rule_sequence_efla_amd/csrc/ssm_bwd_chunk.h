@@ -1,0 +1,608 @@
+// ssm_bwd_chunk.h -- the backward pass of the selective state space scan (ssm.h)
+// for bf16 inputs on the matrix cores: the chains of states and of their
+// gradients, and the gradients chunk by chunk, 64 tokens each.
+//
+// Precision.  dq, dk and dv are rounded to bf16, and the operands that lead to
+// them alone (P, dP and the gradient of the state where it meets a key) once.  The gradients
+// of the decays are sums of products r, p and M (ssm.h) over all tokens, which
+// end in float32: M comes from exact products in float32, and in r and p the
+// states go in as two bf16 parts (16 bits); so do the float32 operands that feed a
+// state.
+#pragma once
+
+#include <type_traits>
+
+#include "ssm_chunk.h"
+
+namespace efla {
+
+// What the chains leave for every (sequence, head, chunk): the state S before it
+// and the gradient X of the state behind it, [d_k][d_v], each as two bf16 parts,
+// X's first also transposed, and the chunk's gates.
+template <int DK>
+struct SsmStates {
+  uint16_t *sh, *sl, *xh, *xl, *xt;
+  ChunkGates* gates;
+};
+
+template <int DK>
+struct SsmChainShape {
+  static constexpr int C = 64, BV = 32, NDT = DK / 16, ND = NDT / 4;  // state tiles of key dims, of an S wave
+  static constexpr int KOFF = 0, VOFF = C * DK, SLOT = C * DK + C * BV;
+  using TK = DmaTile<C, DK, 1, true>;
+  using TV = DmaTile<C, BV, 1, true>;
+  static constexpr int PK = TK::PER_WAVE, PV = TV::PER_WAVE;
+  static constexpr int kW = 4, kGate = 8, kDma = 9, THREADS = 10 * kWave;
+};
+
+// One chain: S <- e^{G_C} S + A^T diag(w) B over the chunks, storing S before each.
+//   forward   A = k, B = v, w = e^{G_C - G} D
+//   REV       the chunks from last to first, A = q, B = dO, w = e^G
+// A workgroup owns 32 value columns of one (sequence, head).  Four S waves keep a
+// quarter of the key dims each, transposed (a lane's rows are value columns, so that the
+// states leave in whole 16-byte pieces), and for REV the other way round as well, for
+// the transposed copy; four W waves form the parts of diag(w) B of the next chunk; one wavefront the gates, one the transfers.  One
+// barrier a chunk; two workgroups share a compute unit and cover each other's waits.
+template <int DK, bool REV, typename Lds>
+__device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, int NVB, const SsmStates<DK>& out) {
+  using S = SsmChainShape<DK>;
+  constexpr int C = S::C, BV = S::BV, ND = S::ND;
+  const int H = b.H, DV = b.DV, bh = x / NVB, vb = x % NVB, h = bh % H, hk = h / (H / b.Hk);
+  const int64_t seq = bh / H;
+  const int nc = int((b.L + C - 1) / C), v0 = vb * BV;
+  const int lane = threadIdx.x & 63, role = wave_id(), li = lane & 15, g = lane >> 4;
+  auto chunk_of = [&](int n) { return REV ? nc - 1 - n : n; };  // n in the chain's order
+  auto valid_of = [&](int n) {
+    const int64_t t = int64_t(chunk_of(n)) * C;
+    return int(b.L - t < C ? b.L - t : C);
+  };
+  auto tok_of = [&](int n) { return seq * b.L + int64_t(chunk_of(n)) * C; };
+  auto sync = [&]() {
+    wait_lgkm0();
+    barrier_nowait();
+  };
+  const int64_t krow = REV ? b.q_row : b.k_row, vrow = REV ? b.do_row : b.v_row;
+
+  // Barriers: one before chunk 0's W, one before every chunk n (its K is in the
+  // ring and its W in the LDS; chunk n + 1's V and gates are there).
+  if (role == S::kDma) {
+    using U = const uint16_t*;
+    const U k = static_cast<U>(REV ? b.q : b.k) + hk * DK;
+    const U v = static_cast<U>(REV ? b.d_o : b.v) + int64_t(h) * DV + v0;
+    typename S::TK tk;
+    typename S::TV tv;
+    tk.init(krow, lane, 0);
+    tv.init(vrow, lane, 0);
+    auto issue = [&](int m) {
+      const int64_t t = tok_of(m);
+      const U ks = (U)uniform_ptr(k + t * krow), vs = (U)uniform_ptr(v + t * vrow);
+      const int valid = valid_of(m);
+      const uint32_t addr = lds_addr_of(lds.ring + (m % 3) * S::SLOT);
+      auto body = [&](auto ragged) {
+        constexpr bool R = decltype(ragged)::value;
+#pragma unroll
+        for (int j = 0; j < S::PV; ++j) tv.template issue<R>(j, addr + 2 * S::VOFF, vs, valid);
+#pragma unroll
+        for (int j = 0; j < S::PK; ++j) tk.template issue<R>(j, addr + 2 * S::KOFF, ks, valid);
+      };
+      if (valid == C) body(std::false_type{});
+      else body(std::true_type{});
+    };
+    auto wait_for = [&](bool more) {  // all but the K transfers issued last, where there are such
+      if (more) wait_vmcnt<S::PK>();
+      else wait_vmcnt<0>();
+    };
+    if (nc > 0) issue(0);
+    wait_vmcnt<0>();
+    barrier_nowait();  // chunk 0
+    if (nc > 1) issue(1);
+    wait_for(nc > 1);
+    for (int n = 0; n < nc; ++n) {
+      barrier_nowait();
+      if (n + 2 < nc) issue(n + 2);  // into chunk n - 1's slot
+      wait_for(n + 2 < nc);
+    }
+  } else if (role == S::kGate) {
+    const auto* dt = static_cast<const uint16_t*>(b.dt) + h;
+    const float rate = b.a[h], bias = b.bias != nullptr ? b.bias[h] : 0.0f;
+    auto load = [&](int n) {
+      if (n >= nc) return 0.0f;
+      return lane < valid_of(n) ? to_f32(dt[(tok_of(n) + lane) * b.dt_row]) : 0.0f;
+    };
+    float now = load(0), next = load(1), then = load(2);
+    auto put = [&](int n) {
+      ChunkGates& gt = lds.gates[n % 3];
+      put_chunk_gates(gt, now + bias, rate, n < nc && lane < valid_of(n), lane);
+      if (!REV && vb == 0 && n < nc) {  // for the gradients, chunk by chunk
+        ChunkGates& dst = out.gates[int64_t(bh) * nc + n];
+        dst.hi[lane] = gt.hi[lane];
+        dst.lo[lane] = gt.lo[lane];
+        dst.D[lane] = gt.D[lane];
+        dst.e[lane] = gt.e[lane];
+        dst.w[lane] = gt.w[lane];
+      }
+      now = next;
+      next = then;
+      then = load(n + 3);
+    };
+    put(0);
+    sync();
+    put(1);
+    for (int n = 0; n < nc; ++n) {
+      sync();
+      put(n + 2);
+    }
+  } else if (role >= S::kW) {
+    const int c = role & 1, ku = (role >> 1) & 1;
+    auto weigh = [&](int n) {
+      const Frag<uint16_t> v = value_frag<BV>(lds.ring + (n % 3) * S::SLOT + S::VOFF, c, ku, lane);
+      const float* gw = REV ? lds.gates[n % 3].e : lds.gates[n % 3].w;
+      f32x4 y[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const f32x4 w = *reinterpret_cast<const f32x4*>(gw + 32 * ku + 16 * e + 4 * g);
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) y[e][qq] = w[qq] * static_cast<float>(v.v[4 * e + qq]);
+      }
+      Frag<uint16_t> hi, lo;
+      split_parts(y[0], y[1], hi, lo);
+      if (REV) {  // rows past the end repeat row 0, and e is not zero there
+        const int valid = n < nc ? valid_of(n) : C;
+        if (valid < C) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (32 * ku + 16 * (e / 4) + 4 * g + e % 4 >= valid) hi.v[e] = lo.v[e] = static_cast<__bf16>(0.0f);
+        }
+      }
+      lds.bW[n & 1][0][c][ku][lane] = hi.v;
+      lds.bW[n & 1][1][c][ku][lane] = lo.v;
+    };
+    sync();
+    weigh(0);
+    for (int n = 0; n < nc; ++n) {
+      sync();
+      weigh(n + 1);  // past the last chunk: stale values that nothing uses
+    }
+  } else {
+    const int sw = role;
+    // T[d][c][qq]: key dim key_phys(16 (ND sw + d) + li), value column v0 + 8 g + 4 c + qq; N: rows and columns exchanged
+    f32x4 T[ND][2], N[ND][2];
+    const float* s0 = REV ? b.dsf : b.s0;
+    const int64_t st = (seq * H + h) * DK;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int t0 = 16 * (ND * sw + d);
+        T[d][c] = zero4();
+        if (s0 != nullptr) T[d][c] = *reinterpret_cast<const f32x4*>(s0 + (st + key_phys(t0 + li)) * DV + v0 + 8 * g + 4 * c);
+        if (REV) {
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq)
+            N[d][c][qq] = s0 != nullptr ? s0[(st + key_phys(t0 + 4 * g + qq)) * DV + v0 + value_phys(c, li)] : 0.0f;
+        }
+      }
+    uint16_t* hi_out = REV ? out.xh : out.sh;
+    uint16_t* lo_out = REV ? out.xl : out.sl;
+    sync();
+    for (int n = 0; n < nc; ++n) {
+      sync();
+      const uint16_t* cur = lds.ring + (n % 3) * S::SLOT + S::KOFF;
+      Frag<uint16_t> KT[ND][2];
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int ku = 0; ku < 2; ++ku) KT[d][ku] = wide_frag_tr<DK>(cur, ND * sw + d, ku, lane);
+      const int64_t slot = int64_t(bh) * nc + chunk_of(n);
+#pragma unroll
+      for (int d = 0; d < ND; ++d) {
+        Frag<uint16_t> hi, lo;
+        split_parts(T[d][0], T[d][1], hi, lo);
+        const int64_t at = (slot * DK + key_phys(16 * (ND * sw + d) + li)) * DV + v0 + 8 * g;
+        *reinterpret_cast<bf16x8*>(hi_out + at) = hi.v;
+        *reinterpret_cast<bf16x8*>(lo_out + at) = lo.v;
+        if (REV) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            st4(out.xt + (slot * DV + v0 + value_phys(c, li)) * DK + key_phys(16 * (ND * sw + d) + 4 * g), N[d][c]);
+        }
+      }
+      const float all = lds.gates[n % 3].e[63];
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          T[d][c] = all * T[d][c];
+          if (REV) N[d][c] = all * N[d][c];
+        }
+#pragma unroll
+      for (int ku = 0; ku < 2; ++ku)
+#pragma unroll
+        for (int part = 1; part >= 0; --part)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            Frag<uint16_t> W;
+            W.v = lds.bW[n & 1][part][c][ku][lane];
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+              mma(T[d][c], W, KT[d][ku]);
+              if (REV) mma(N[d][c], KT[d][ku], W);
+            }
+          }
+    }
+    if (REV && b.ds0 != nullptr) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          *reinterpret_cast<f32x4*>(b.ds0 + (st + key_phys(16 * (ND * sw + d) + li)) * DV + v0 + 8 * g + 4 * c) = T[d][c];
+    }
+  }
+}
+
+template <int DK>
+__global__ __launch_bounds__((SsmChainShape<DK>::THREADS), 5) void ssm_chain_kernel(SsmBwd b, int NVB, int half,
+                                                                                    SsmStates<DK> out) {
+  using S = SsmChainShape<DK>;
+  __shared__ __align__(1024) uint16_t ring[3 * S::SLOT];
+  __shared__ __align__(16) bf16x8 bW[2][2][2][2][kWave];  // [buffer][part][column tile][k-unit]
+  __shared__ __align__(16) ChunkGates gates[3];
+  struct Refs {
+    uint16_t* ring;
+    decltype(bW)& bW;
+    decltype(gates)& gates;
+  };
+  Refs lds{ring, bW, gates};
+  if (int(blockIdx.x) < half) ssm_chain_run<DK, true>(lds, b, blockIdx.x, NVB, out);
+  else ssm_chain_run<DK, false>(lds, b, blockIdx.x - half, NVB, out);
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of one chunk for one query and key head: its value heads one after
+// the other, dQ and dK summed over them in registers, in order.  Eight wavefronts:
+//   the 10 tiles of the lower triangle of Q K^T and dO V^T, spread over them: P
+//   and dP with their decays and D into the LDS, row and column sums of M
+//   then each wavefront key dims 16 w .. of dQ^T and dK^T (all tokens), states as
+//   operands straight from memory, and value columns of dV^T
+//   then one of them the gradients of the 64 steps
+// All products have tokens as columns, so a lane's four rows are adjacent values
+// of one token.
+template <int DK, int DV>
+struct SsmGradShape {
+  static constexpr int C = 64, KU = DK / 32, VU = DV / 32, NW = 8, THREADS = NW * kWave;
+  static constexpr int DT = DK / 16, VT = DV / 16;
+  static constexpr int VSPLIT = NW / VT;           // wavefronts a tile of value columns, a share of the tokens each
+  static constexpr int VTOK = 4 / (VSPLIT > 4 ? 4 : VSPLIT);
+  using TK = DmaTile<C, DK, NW, true>;
+  using TV = DmaTile<C, DV, NW, true>;
+};
+
+// Tile t (0 .. 9) of the lower triangle: row tile, column tile.
+__host__ __device__ constexpr int tri_row(int t) { return t < 1 ? 0 : t < 3 ? 1 : t < 6 ? 2 : 3; }
+__host__ __device__ constexpr int tri_at(int r, int c) { return r * (r + 1) / 2 + c; }
+
+// P and dP live tile by tile, [tile][16][16] row-major with rows i and columns j.
+// Operand row i (k index j) ...
+__device__ __forceinline__ Frag<uint16_t> tri_rows(const uint16_t* X, int rt, int ku, int lane) {
+  const int li = lane & 15, g = lane >> 4;
+  Frag<uint16_t> f;
+  const bf16x4 lo = *reinterpret_cast<const bf16x4*>(X + (tri_at(rt, 2 * ku) * 16 + li) * 16 + 4 * g);
+  bf16x4 hi{};
+  if (2 * ku + 1 <= rt) hi = *reinterpret_cast<const bf16x4*>(X + (tri_at(rt, 2 * ku + 1) * 16 + li) * 16 + 4 * g);
+  f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return f;
+}
+// ... and operand row j (k index i).
+__device__ __forceinline__ Frag<uint16_t> tri_cols(const uint16_t* X, int ct, int ku, int lane) {
+  const int j = lane & 15, g = lane >> 4, at = (4 * g + (j >> 2)) * 16 + 4 * (j & 3);
+  Frag<uint16_t> f;
+  bf16x4 lo{};
+  if (2 * ku >= ct) lo = lds_read_tr(X + tri_at(2 * ku, ct) * 256 + at);
+  const bf16x4 hi = lds_read_tr(X + tri_at(2 * ku + 1, ct) * 256 + at);
+  f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return f;
+}
+
+// Operand row m0 + li of the transpose of a tile in the 16-byte layout, k index
+// over its rows.
+template <int ROWE>
+__device__ __forceinline__ Frag<uint16_t> sw_frag_tr_wide(const uint16_t* X, int m0, int ku, int lane) {
+  const int j = lane & 15, g = lane >> 4;
+  const int r = 32 * ku + 4 * g + (j >> 2), c = m0 + 4 * (j & 3);
+  const bf16x4 lo = lds_read_tr(X + swzw_off<ROWE>(r, c));
+  const bf16x4 hi = lds_read_tr(X + swzw_off<ROWE>(r + 16, c));
+  Frag<uint16_t> f;
+  f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return f;
+}
+
+template <int DK, int DV>
+__global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kernel(SsmBwd b, SsmStates<DK> st,
+                                                                                   float* __restrict__ part, int NC) {
+  using S = SsmGradShape<DK, DV>;
+  constexpr int C = S::C, KU = S::KU, VU = S::VU, DT = S::DT, VT = S::VT, VTOK = S::VTOK;
+  __shared__ __align__(1024) uint16_t Qs[C * DK], Ks[C * DK], Vs[C * DV], Os[C * DV];
+  __shared__ __align__(16) uint16_t Pm[10 * 256], Dm[10 * 256];
+  __shared__ __align__(16) ChunkGates gt;
+  __shared__ float rowM[10][16], colM[10][16], rin[8][C], pin[8][C], dots[2][8];
+
+  const int r = b.H / b.Hk;
+  const uint32_t wg = blockIdx.x;
+  const int n = int(wg % uint32_t(NC));
+  const uint32_t bk = wg / uint32_t(NC);
+  const int hk = int(bk % uint32_t(b.Hk));
+  const int64_t bb = bk / uint32_t(b.Hk);
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), li = lane & 15, g = lane >> 4;
+  const int64_t t0 = int64_t(n) * C, tok = bb * b.L + t0;
+  const int valid = int(b.L - t0 < C ? b.L - t0 : C);
+  auto sync = [&]() {
+    wait_lgkm0();
+    barrier_nowait();
+  };
+  using U = const uint16_t*;
+  typename S::TK tk;
+  typename S::TV tv;
+  auto fetch_qk = [&]() {
+    const U qs = (U)uniform_ptr(static_cast<U>(b.q) + tok * b.q_row + hk * DK);
+    const U ks = (U)uniform_ptr(static_cast<U>(b.k) + tok * b.k_row + hk * DK);
+    tk.init(b.q_row, lane, w);
+#pragma unroll
+    for (int i = 0; i < S::TK::PER_WAVE; ++i) tk.template issue<true>(i, lds_addr_of(Qs), qs, valid);
+    tk.init(b.k_row, lane, w);
+#pragma unroll
+    for (int i = 0; i < S::TK::PER_WAVE; ++i) tk.template issue<true>(i, lds_addr_of(Ks), ks, valid);
+  };
+  auto fetch_head = [&](int h) {
+    const U vs = (U)uniform_ptr(static_cast<U>(b.v) + tok * b.v_row + int64_t(h) * DV);
+    const U os = (U)uniform_ptr(static_cast<U>(b.d_o) + tok * b.do_row + int64_t(h) * DV);
+    tv.init(b.v_row, lane, w);
+#pragma unroll
+    for (int i = 0; i < S::TV::PER_WAVE; ++i) tv.template issue<true>(i, lds_addr_of(Vs), vs, valid);
+    tv.init(b.do_row, lane, w);
+#pragma unroll
+    for (int i = 0; i < S::TV::PER_WAVE; ++i) tv.template issue<true>(i, lds_addr_of(Os), os, valid);
+  };
+  fetch_qk();
+  fetch_head(hk * r);
+
+  // which of dQ and dK this wavefront forms, and their key dims: with 128 of them both, with 64 one
+  const int dt = DT == 8 ? w : w & 3;
+  const bool do_q = DT == 8 || w < 4, do_k = DT == 8 || w >= 4;
+  const int vt = w % VT, vtok = (w / VT) * VTOK;  // value tile, first token tile of dV
+  f32x4 dQ[4], dK[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) dQ[t] = dK[t] = zero4();
+  f32x4 raw[2] = {zero4(), zero4()};  // of tiles w and w + 8: raw[.][qq] = k_j . q_i, j = 16 c + 4 g + qq, i = 16 r + li
+
+  for (int hh = 0; hh < r; ++hh) {
+    const int h = hk * r + hh;
+    const int64_t slot = (bb * b.H + h) * NC + n;
+    const float skip = b.d != nullptr ? b.d[h] : 0.0f;
+    // states as operands: row dt, all value columns (k index in the order of wide_frag)
+    const int64_t srow = (slot * DK + 16 * dt + li) * DV + 8 * g;
+    Frag<uint16_t> Sh[VU], Sl[VU], Xh[VU], Xl[VU], XT[KU];
+#pragma unroll
+    for (int ku = 0; ku < VU; ++ku) {
+      Sh[ku].v = *reinterpret_cast<const bf16x8*>(st.sh + srow + 32 * ku);
+      Sl[ku].v = *reinterpret_cast<const bf16x8*>(st.sl + srow + 32 * ku);
+      Xh[ku].v = *reinterpret_cast<const bf16x8*>(st.xh + srow + 32 * ku);
+      Xl[ku].v = *reinterpret_cast<const bf16x8*>(st.xl + srow + 32 * ku);
+    }
+#pragma unroll
+    for (int ku = 0; ku < KU; ++ku)
+      XT[ku].v = *reinterpret_cast<const bf16x8*>(st.xt + (slot * DV + 16 * vt + li) * DK + 32 * ku + 8 * g);
+    if (w == 7) {
+      const ChunkGates& src = st.gates[slot];
+      gt.hi[lane] = src.hi[lane];
+      gt.lo[lane] = src.lo[lane];
+      gt.D[lane] = src.D[lane];
+      gt.e[lane] = src.e[lane];
+      gt.w[lane] = src.w[lane];
+    }
+    wait_vmcnt<0>();
+    sync();  // this head's V, dO and gates are there
+    if (hh == 0) {
+      if (valid < C) {  // rows past the end repeat row 0: zeros
+        for (int at = tid; at < (C - valid) * DK / 8; at += S::THREADS)
+          reinterpret_cast<u32x4*>(Qs)[valid * DK / 8 + at] = reinterpret_cast<u32x4*>(Ks)[valid * DK / 8 + at] = u32x4{};
+      }
+    }
+    if (valid < C) {
+      for (int at = tid; at < (C - valid) * DV / 8; at += S::THREADS)
+        reinterpret_cast<u32x4*>(Vs)[valid * DV / 8 + at] = reinterpret_cast<u32x4*>(Os)[valid * DV / 8 + at] = u32x4{};
+      sync();
+    }
+    float skips = 0.0f, dot = 0.0f;  // v . dO of this chunk; <X, S>
+    for (int at = tid; at < C * DV / 8; at += S::THREADS) {
+      const bf16x8 x = reinterpret_cast<const bf16x8*>(Vs)[at], y = reinterpret_cast<const bf16x8*>(Os)[at];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) skips = fmaf(float(x[e]), float(y[e]), skips);
+    }
+    if (do_q) {
+#pragma unroll
+      for (int ku = 0; ku < VU; ++ku)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          dot = fmaf(float(Sh[ku].v[e]) + float(Sl[ku].v[e]), float(Xh[ku].v[e]) + float(Xl[ku].v[e]), dot);
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      skips += __shfl_xor(skips, off);
+      dot += __shfl_xor(dot, off);
+    }
+    if (lane == 0) {
+      dots[0][w] = skips;
+      dots[1][w] = dot;
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int tile = w + 8 * u;
+      if (tile >= 10) break;
+      const int rt = tri_row(tile), ct = tile - tri_at(rt, 0), i = 16 * rt + li;
+      if (hh == 0) {
+#pragma unroll
+        for (int ku = 0; ku < KU; ++ku)
+          mma(raw[u], wide_frag<DK>(Ks, 16 * ct + li, ku, g), wide_frag<DK>(Qs, i, ku, g));
+      }
+      f32x4 dp = zero4();
+#pragma unroll
+      for (int ku = 0; ku < VU; ++ku) mma(dp, wide_frag<DV>(Vs, 16 * ct + li, ku, g), wide_frag<DV>(Os, i, ku, g));
+      const float hi = gt.hi[i], lo = gt.lo[i];
+      const f32x4 ch = *reinterpret_cast<const f32x4*>(gt.hi + 16 * ct + 4 * g);
+      const f32x4 cl = *reinterpret_cast<const f32x4*>(gt.lo + 16 * ct + 4 * g);
+      const f32x4 D = *reinterpret_cast<const f32x4*>(gt.D + 16 * ct + 4 * g);
+      f32x4 p, d;
+      float rs = 0.0f;
+#pragma unroll
+      for (int qq = 0; qq < 4; ++qq) {
+        const bool in = ct < rt || 4 * g + qq <= li;
+        const float f = in ? __builtin_amdgcn_exp2f((hi - ch[qq]) + (lo - cl[qq])) : 0.0f;
+        const float m = in ? dp[qq] * (raw[u][qq] * f) : 0.0f;
+        p[qq] = in ? raw[u][qq] * f * D[qq] : 0.0f;
+        d[qq] = in ? dp[qq] * f * D[qq] : 0.0f;
+        rs = fmaf(m, D[qq], rs);
+        const float cs = row_sum16(m);
+        if (li == 0) colM[tile][4 * g + qq] = cs;
+      }
+      rs = row_sum4(rs);
+      if (g == 0) rowM[tile][li] = rs;
+      st4(Pm + (tile * 16 + li) * 16 + 4 * g, p);
+      st4(Dm + (tile * 16 + li) * 16 + 4 * g, d);
+    }
+    sync();
+    float rp[4] = {}, pp[4] = {};  // this wavefront's share of r and of p / D, token 16 t + li
+    if (do_q) {
+      Frag<uint16_t> KT[2];
+#pragma unroll
+      for (int ku = 0; ku < 2; ++ku) KT[ku] = sw_frag_tr_wide<DK>(Ks, 16 * dt, ku, lane);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        f32x4 x = zero4(), y = zero4();
+#pragma unroll
+        for (int ku = 0; ku < VU; ++ku) {
+          const Frag<uint16_t> o = wide_frag<DV>(Os, 16 * t + li, ku, g);
+          mma(y, Sl[ku], o);
+          mma(x, Sh[ku], o);
+        }
+        x = gt.e[16 * t + li] * (x + y);
+        const bf16x4 q = *reinterpret_cast<const bf16x4*>(Qs + swzw_off<DK>(16 * t + li, 16 * dt + 4 * g));
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) rp[t] = fmaf(x[qq], float(q[qq]), rp[t]);
+#pragma unroll
+        for (int ku = 0; ku < 2; ++ku)
+          if (2 * ku <= t) mma(x, KT[ku], tri_rows(Dm, t, ku, lane));
+        dQ[t] += x;
+      }
+    }
+    if (do_k) {
+      Frag<uint16_t> QT[2];
+#pragma unroll
+      for (int ku = 0; ku < 2; ++ku) QT[ku] = sw_frag_tr_wide<DK>(Qs, 16 * dt, ku, lane);
+      const float hi_end = gt.hi[63], lo_end = gt.lo[63];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        f32x4 x = zero4(), y = zero4();
+#pragma unroll
+        for (int ku = 0; ku < VU; ++ku) {
+          const Frag<uint16_t> v = wide_frag<DV>(Vs, 16 * t + li, ku, g);
+          mma(y, Xl[ku], v);
+          mma(x, Xh[ku], v);
+        }
+        const int j = 16 * t + li;
+        x = __builtin_amdgcn_exp2f((hi_end - gt.hi[j]) + (lo_end - gt.lo[j])) * (x + y);
+        const bf16x4 k = *reinterpret_cast<const bf16x4*>(Ks + swzw_off<DK>(j, 16 * dt + 4 * g));
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) pp[t] = fmaf(x[qq], float(k[qq]), pp[t]);
+        x = gt.D[j] * x;
+#pragma unroll
+        for (int ku = 0; ku < 2; ++ku)
+          if (2 * ku + 1 >= t) mma(x, QT[ku], tri_cols(Dm, t, ku, lane));
+        dK[t] += x;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float x = row_sum4(rp[t]), y = row_sum4(pp[t]);
+      if (g == 0) {
+        rin[w][16 * t + li] = x;
+        pin[w][16 * t + li] = y;
+      }
+    }
+    {
+      uint16_t* dv = static_cast<uint16_t*>(b.dv) + tok * b.dv_row + int64_t(h) * DV + 16 * vt + 4 * g;
+      Frag<uint16_t> OT[2];
+#pragma unroll
+      for (int ku = 0; ku < 2; ++ku) OT[ku] = sw_frag_tr_wide<DV>(Os, 16 * vt, ku, lane);
+#pragma unroll
+      for (int tt = 0; tt < VTOK; ++tt) {
+        const int t = vtok + tt, j = 16 * t + li;
+        f32x4 x = zero4();
+#pragma unroll
+        for (int ku = 0; ku < KU; ++ku) mma(x, XT[ku], wide_frag<DK>(Ks, j, ku, g));
+        x = gt.w[j] * x;
+#pragma unroll
+        for (int ku = 0; ku < 2; ++ku)
+          if (2 * ku + 1 >= t) mma(x, OT[ku], tri_cols(Pm, t, ku, lane));
+        const bf16x4 o = *reinterpret_cast<const bf16x4*>(Os + swzw_off<DV>(j, 16 * vt + 4 * g));
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) x[qq] = fmaf(skip, float(o[qq]), x[qq]);
+        if (j < valid) st4(dv + j * b.dv_row, x);
+      }
+    }
+    sync();
+    if (hh + 1 < r) fetch_head(h + 1);
+    if (w == 0) {
+      const int l = lane, rt = l >> 4, i = l & 15;
+      float ri = 0.0f, ci = 0.0f, rr = 0.0f, pj = 0.0f, xs = 0.0f, vo = 0.0f;
+      for (int c = 0; c <= rt; ++c) ri += rowM[tri_at(rt, c)][i];
+      for (int t = rt; t < 4; ++t) ci += colM[tri_at(t, rt)][i];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        rr += rin[u][l];
+        pj += pin[u][l];
+        vo += dots[0][u];
+        xs += dots[1][u];
+      }
+      const float D = gt.D[l], rate = b.a[h];
+      const bool real = l < valid;
+      float suf = real ? ri - D * ci + rr : 0.0f, pre = real ? D * pj : 0.0f;
+      const float own = pre;
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) {
+        const float y = __shfl_down(suf, d), z = __shfl_up(pre, d);
+        if (l + d < kWave) suf += y;
+        if (l >= d) pre += z;
+      }
+      const float gd = suf + (pre - own) + gt.e[63] * xs;
+      const float dD = ci + pj + rate * gd;
+      float ddt = 0.0f;
+      if (real) {
+        const float x = to_f32(static_cast<U>(b.dt)[(tok + l) * b.dt_row + h]) + (b.bias != nullptr ? b.bias[h] : 0.0f);
+        ddt = dD * (1.0f / (1.0f + expf(-x)));
+        static_cast<uint16_t*>(b.ddt)[(tok + l) * b.ddt_row + h] = from_f32<uint16_t>(ddt);
+      }
+      float sa = real ? D * gd : 0.0f, sb = ddt;
+#pragma unroll
+      for (int off = 32; off > 0; off >>= 1) {
+        sa += __shfl_xor(sa, off);
+        sb += __shfl_xor(sb, off);
+      }
+      if (lane == 0) {
+        const int64_t M = int64_t(b.B) * NC, at = int64_t(h) * M + bb * NC + n, all = int64_t(b.H) * M;
+        part[at] = sa;
+        part[all + at] = sb;
+        part[2 * all + at] = vo;
+      }
+    }
+    if (hh + 1 < r) sync();  // wavefront 0 is done with the gates and the sums
+  }
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const int j = 16 * t + li;
+    if (j >= valid) continue;
+    if (do_q) st4(static_cast<uint16_t*>(b.dq) + (tok + j) * b.dq_row + hk * DK + 16 * dt + 4 * g, dQ[t]);
+    if (do_k) st4(static_cast<uint16_t*>(b.dk) + (tok + j) * b.dk_row + hk * DK + 16 * dt + 4 * g, dK[t]);
+  }
+}
+
+}  // namespace efla

@@ -1,0 +1,59 @@
+// ssm_bwd_chunk.hip -- launches of the scan's backward pass for bf16 inputs
+// (ssm_bwd_chunk.h).
+#include "launchers.h"
+#include "ssm_bwd_chunk.h"
+
+namespace efla {
+
+namespace {
+
+struct Layout {
+  size_t state, gates, part, total;  // bytes of one of the five state arrays; offsets behind them
+};
+Layout layout(int B, int H, int64_t L, int DK, int DV) {
+  const size_t slots = size_t(B) * H * size_t((L + 63) / 64);
+  Layout w{};
+  w.state = slots * DK * DV * 2;
+  w.gates = 5 * w.state;
+  w.part = w.gates + slots * sizeof(ChunkGates);
+  w.total = w.part + slots * 3 * sizeof(float);
+  return w;
+}
+
+template <int DK>
+hipError_t bwd_impl(const SsmBwd& b, void* ws, hipStream_t s) {
+  const Layout w = layout(b.B, b.H, b.L, DK, b.DV);
+  auto* at = static_cast<unsigned char*>(ws);
+  auto arr = [&](int i) { return reinterpret_cast<uint16_t*>(at + i * w.state); };
+  const SsmStates<DK> st{arr(0), arr(1), arr(2), arr(3), arr(4), reinterpret_cast<ChunkGates*>(at + w.gates)};
+  float* part = reinterpret_cast<float*>(at + w.part);
+  const int NC = int((b.L + 63) / 64), NVB = b.DV / 32, half = b.B * b.H * NVB;
+  hipLaunchKernelGGL((ssm_chain_kernel<DK>), dim3(unsigned(2 * half)), dim3(SsmChainShape<DK>::THREADS), 0, s, b, NVB, half, st);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 grid(unsigned(int64_t(b.B) * b.Hk * NC)), wg(SsmGradShape<DK, 64>::THREADS);
+  switch (b.DV) {
+    case 32: hipLaunchKernelGGL((ssm_grad_kernel<DK, 32>), grid, wg, 0, s, b, st, part, NC); break;
+    case 64: hipLaunchKernelGGL((ssm_grad_kernel<DK, 64>), grid, wg, 0, s, b, st, part, NC); break;
+    case 128: hipLaunchKernelGGL((ssm_grad_kernel<DK, 128>), grid, wg, 0, s, b, st, part, NC); break;
+    default: return hipErrorInvalidValue;
+  }
+  e = hipGetLastError();
+  return e != hipSuccess ? e : launch_ssm_sums(part, b.da, b.dbias, b.dd, int64_t(b.B) * NC, b.H, s);
+}
+
+}  // namespace
+
+size_t ssm_bwd_chunk_workspace(int B, int H, int64_t L, int DK, int DV) { return layout(B, H, L, DK, DV).total; }
+
+int64_t ssm_bwd_chunk_threads(int B, int H, int64_t L, int DV) {
+  const int64_t chains = 2 * int64_t(B) * H * (DV / 32) * SsmChainShape<64>::THREADS;
+  const int64_t grads = int64_t(B) * H * ((L + 63) / 64) * SsmGradShape<64, 64>::THREADS;
+  return chains > grads ? chains : grads;
+}
+
+hipError_t launch_ssm_bwd_chunk(const SsmBwd& b, void* ws, hipStream_t s) {
+  return b.DK == 64 ? bwd_impl<64>(b, ws, s) : bwd_impl<128>(b, ws, s);
+}
+
+}  // namespace efla

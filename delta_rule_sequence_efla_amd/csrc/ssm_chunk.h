@@ -92,6 +92,14 @@ __device__ __forceinline__ void split3_frag(const f32x4& lo4, const f32x4& hi4, 
   for (int i = 0; i < 3; ++i) p[i].v = __builtin_bit_cast(bf16x8, part[i]);
 }
 
+// As a sum of two.
+__device__ __forceinline__ void split_parts(const f32x4& lo4, const f32x4& hi4, Frag<uint16_t>& hi, Frag<uint16_t>& lo) {
+  Frag<uint16_t> p[3];
+  split3_frag(lo4, hi4, p);
+  hi = p[0];
+  lo = p[1];
+}
+
 template <int DK>
 struct SsmShape {
   static_assert(DK == 64 || DK == 128, "shapes of the chunked scan");

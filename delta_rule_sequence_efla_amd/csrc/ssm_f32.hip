@@ -506,6 +506,11 @@ hipError_t launch_ssm_f32(const SsmFwd& a, hipStream_t s) {
 template hipError_t launch_ssm_f32<float>(const SsmFwd&, hipStream_t);
 template hipError_t launch_ssm_f32<uint16_t>(const SsmFwd&, hipStream_t);
 
+hipError_t launch_ssm_sums(const float* part, float* da, float* dbias, float* dd, int64_t M, int H, hipStream_t s) {
+  hipLaunchKernelGGL(ssm_sum_kernel, dim3(unsigned(3 * H)), dim3(kThreads), 0, s, part, da, dbias, dd, M, H);
+  return hipGetLastError();
+}
+
 int64_t ssm_bwd_f32_threads(int B, int H, int64_t L, int DV) {
   const int64_t chains = ssm_f32_threads(B, H, DV), grads = int64_t(B) * H * ((L + kC - 1) / kC) * kThreads;
   return chains > grads ? chains : grads;
@@ -549,9 +554,7 @@ hipError_t launch_ssm_bwd_f32(const SsmBwd& b, void* ws, hipStream_t s) {
     });
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(ssm_sum_kernel, dim3(unsigned(3 * b.H)), dim3(kThreads), 0, s, part, b.da, b.dbias, b.dd,
-                     int64_t(b.B) * NC, b.H);
-  return hipGetLastError();
+  return launch_ssm_sums(part, b.da, b.dbias, b.dd, int64_t(b.B) * NC, b.H, s);
 }
 template hipError_t launch_ssm_bwd_f32<float>(const SsmBwd&, void*, hipStream_t);
 template hipError_t launch_ssm_bwd_f32<uint16_t>(const SsmBwd&, void*, hipStream_t);
