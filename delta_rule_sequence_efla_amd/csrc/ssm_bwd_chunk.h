@@ -17,8 +17,13 @@
 namespace efla {
 
 // What the chains leave for every (sequence, head, chunk): the state S before it
-// and the gradient X of the state behind it, [d_k][d_v], each as two bf16 parts,
-// X's first also transposed, and the chunk's gates.
+// and the gradient X of the state behind it, each as two bf16 parts, X's first also
+// transposed, and the chunk's gates.  The arrays are cut into k-units of 32,
+// [slot][d_v / 32][d_k][32] and [slot][d_k / 32][d_v][32], so that what one
+// workgroup of the chains writes of a chunk is one piece of memory, and so is the
+// operand fragment that a wavefront of the gradients reads.  (Rows of d_v values, of
+// which four workgroups on four dies write 64 bytes each: 188 us instead of CHAINUS for
+// the chains of 8 x 2048 tokens, 8 heads, d 128.)
 template <int DK>
 struct SsmStates {
   uint16_t *sh, *sl, *xh, *xl, *xt;
@@ -198,13 +203,17 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
       for (int d = 0; d < ND; ++d) {
         Frag<uint16_t> hi, lo;
         split_parts(T[d][0], T[d][1], hi, lo);
-        const int64_t at = (slot * DK + key_phys(16 * (ND * sw + d) + li)) * DV + v0 + 8 * g;
+        const int64_t at = ((slot * (DV / 32) + vb) * DK + key_phys(16 * (ND * sw + d) + li)) * 32 + 8 * g;
         *reinterpret_cast<bf16x8*>(hi_out + at) = hi.v;
         *reinterpret_cast<bf16x8*>(lo_out + at) = lo.v;
-        if (REV) {
+      }
+      if constexpr (REV) {
+        const int u = ND * sw / 2;  // k-unit of these key dims
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-            st4(out.xt + (slot * DV + v0 + value_phys(c, li)) * DK + key_phys(16 * (ND * sw + d) + 4 * g), N[d][c]);
+        for (int c = 0; c < 2; ++c) {
+          uint16_t* row = out.xt + ((slot * (DK / 32) + u) * DV + v0 + value_phys(c, li)) * 32 + 8 * g;
+          if constexpr (ND == 2) *reinterpret_cast<bf16x8*>(row) = acc_frag<uint16_t>(N[0][c], N[1][c]).v;
+          else st4(row + 4 * (sw & 1), N[0][c]);
         }
       }
       const float all = lds.gates[n % 3].e[63];
@@ -259,20 +268,20 @@ __global__ __launch_bounds__((SsmChainShape<DK>::THREADS), 5) void ssm_chain_ker
 
 // ---------------------------------------------------------------------------
 // Gradients of one chunk for one query and key head: its value heads one after
-// the other, dQ and dK summed over them in registers, in order.  Eight wavefronts:
-//   the 10 tiles of the lower triangle of Q K^T and dO V^T, spread over them: P
-//   and dP with their decays and D into the LDS, row and column sums of M
-//   then each wavefront key dims 16 w .. of dQ^T and dK^T (all tokens), states as
-//   operands straight from memory, and value columns of dV^T
-//   then one of them the gradients of the 64 steps
+// the other, dQ and dK summed over them in registers, in order.  Sixteen wavefronts:
+//   ten of them a tile each of the lower triangle of Q K^T and dO V^T: P and dP with
+//   their decays and D into the LDS, row and column sums of M
+//   then the first half key dims of dQ^T each (all tokens), the other half of dK^T,
+//   states as operands straight from memory, and all of them a share of dV^T
+//   then one of them the gradients of the 64 steps, beside the next head
 // All products have tokens as columns, so a lane's four rows are adjacent values
 // of one token.
 template <int DK, int DV>
 struct SsmGradShape {
-  static constexpr int C = 64, KU = DK / 32, VU = DV / 32, NW = 8, THREADS = NW * kWave;
+  static constexpr int C = 64, KU = DK / 32, VU = DV / 32, NW = 16, THREADS = NW * kWave;
   static constexpr int DT = DK / 16, VT = DV / 16;
-  static constexpr int VSPLIT = NW / VT;           // wavefronts a tile of value columns, a share of the tokens each
-  static constexpr int VTOK = 4 / (VSPLIT > 4 ? 4 : VSPLIT);
+  static constexpr int KTOK = DT / 2;              // token tiles of dQ or dK a wavefront: 8 wavefronts, DT x 4 tiles
+  static constexpr int VSPLIT = NW / VT > 4 ? 4 : NW / VT, VTOK = 4 / VSPLIT;  // of dV: VT VSPLIT wavefronts
   using TK = DmaTile<C, DK, NW, true>;
   using TV = DmaTile<C, DV, NW, true>;
 };
@@ -320,11 +329,12 @@ template <int DK, int DV>
 __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kernel(SsmBwd b, SsmStates<DK> st,
                                                                                    float* __restrict__ part, int NC) {
   using S = SsmGradShape<DK, DV>;
-  constexpr int C = S::C, KU = S::KU, VU = S::VU, DT = S::DT, VT = S::VT, VTOK = S::VTOK;
-  __shared__ __align__(1024) uint16_t Qs[C * DK], Ks[C * DK], Vs[C * DV], Os[C * DV];
+  constexpr int C = S::C, KU = S::KU, VU = S::VU, VT = S::VT, KTOK = S::KTOK, VTOK = S::VTOK;
+  __shared__ __align__(1024) uint16_t Qs[C * DK], Ks[C * DK], VO[2][2][C * DV];  // V and dO of this head and the next
   __shared__ __align__(16) uint16_t Pm[10 * 256], Dm[10 * 256];
-  __shared__ __align__(16) ChunkGates gt;
-  __shared__ float rowM[10][16], colM[10][16], rin[8][C], pin[8][C], dots[2][8];
+  // of this head and the next: the step gradients of a head are formed beside the next head's products
+  __shared__ __align__(16) ChunkGates gates[2];
+  __shared__ float rowM[2][10][16], colM[2][10][16], rsum[2][S::DT][C], psum[2][S::DT][C], dots[2][2][S::NW];
 
   const int r = b.H / b.Hk;
   const uint32_t wg = blockIdx.x;
@@ -332,7 +342,15 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
   const uint32_t bk = wg / uint32_t(NC);
   const int hk = int(bk % uint32_t(b.Hk));
   const int64_t bb = bk / uint32_t(b.Hk);
-  const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), li = lane & 15, g = lane >> 4;
+  const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
+  // The lane's index afresh, so that addresses formed from it belong to one stage:
+  // kept over the heads, they were 43 registers a lane of scratch memory, 180 MB
+  // of writes in all and three times the time.
+  auto lane_now = [&]() {
+    int x = lane;
+    asm volatile("" : "+v"(x));
+    return x;
+  };
   const int64_t t0 = int64_t(n) * C, tok = bb * b.L + t0;
   const int valid = int(b.L - t0 < C ? b.L - t0 : C);
   auto sync = [&]() {
@@ -340,9 +358,8 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     barrier_nowait();
   };
   using U = const uint16_t*;
-  typename S::TK tk;
-  typename S::TV tv;
-  auto fetch_qk = [&]() {
+  {
+    typename S::TK tk;
     const U qs = (U)uniform_ptr(static_cast<U>(b.q) + tok * b.q_row + hk * DK);
     const U ks = (U)uniform_ptr(static_cast<U>(b.k) + tok * b.k_row + hk * DK);
     tk.init(b.q_row, lane, w);
@@ -351,47 +368,104 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     tk.init(b.k_row, lane, w);
 #pragma unroll
     for (int i = 0; i < S::TK::PER_WAVE; ++i) tk.template issue<true>(i, lds_addr_of(Ks), ks, valid);
-  };
-  auto fetch_head = [&](int h) {
+  }
+  auto fetch_head = [&](int hh) {
+    const int h = hk * r + hh;
+    typename S::TV tv;
     const U vs = (U)uniform_ptr(static_cast<U>(b.v) + tok * b.v_row + int64_t(h) * DV);
     const U os = (U)uniform_ptr(static_cast<U>(b.d_o) + tok * b.do_row + int64_t(h) * DV);
     tv.init(b.v_row, lane, w);
 #pragma unroll
-    for (int i = 0; i < S::TV::PER_WAVE; ++i) tv.template issue<true>(i, lds_addr_of(Vs), vs, valid);
+    for (int i = 0; i < S::TV::PER_WAVE; ++i) tv.template issue<true>(i, lds_addr_of(VO[hh & 1][0]), vs, valid);
     tv.init(b.do_row, lane, w);
 #pragma unroll
-    for (int i = 0; i < S::TV::PER_WAVE; ++i) tv.template issue<true>(i, lds_addr_of(Os), os, valid);
+    for (int i = 0; i < S::TV::PER_WAVE; ++i) tv.template issue<true>(i, lds_addr_of(VO[hh & 1][1]), os, valid);
   };
-  fetch_qk();
-  fetch_head(hk * r);
+  fetch_head(0);
 
-  // which of dQ and dK this wavefront forms, and their key dims: with 128 of them both, with 64 one
-  const int dt = DT == 8 ? w : w & 3;
-  const bool do_q = DT == 8 || w < 4, do_k = DT == 8 || w >= 4;
-  const int vt = w % VT, vtok = (w / VT) * VTOK;  // value tile, first token tile of dV
-  f32x4 dQ[4], dK[4];
+  const bool is_q = w < 8;                                                  // dQ, or dK
+  const int dt = (w & 7) / (4 / KTOK), ktok = (w & 7) % (4 / KTOK) * KTOK;  // its key dims 16 dt .., token tiles from ktok on
+  const int vt = w % VT, vtok = w / VT * VTOK;                              // the same of dV
+  const bool do_v = vtok < 4;
+  f32x4 dA[KTOK];  // dQ^T or dK^T
 #pragma unroll
-  for (int t = 0; t < 4; ++t) dQ[t] = dK[t] = zero4();
-  f32x4 raw[2] = {zero4(), zero4()};  // of tiles w and w + 8: raw[.][qq] = k_j . q_i, j = 16 c + 4 g + qq, i = 16 r + li
+  for (int t = 0; t < KTOK; ++t) dA[t] = zero4();
+  f32x4 raw = zero4();  // of tile w: raw[qq] = k_j . q_i, j = 16 ct + 4 g + qq, i = 16 rt + li
+  const int tile = w < 10 ? w : 9, rt = tri_row(tile), ct = tile - tri_at(rt, 0);
+
+  // The gradients of head hh's steps from the sums in buffer hh & 1, a lane a token.
+  auto step_grads = [&](int hh) {
+    const int h = hk * r + hh, u = hh & 1, l = lane, lt = l >> 4, i = l & 15;
+    const ChunkGates& gt = gates[u];
+    float ri = 0.0f, ci = 0.0f, rr = 0.0f, pj = 0.0f, xs = 0.0f, vo = 0.0f;
+#pragma unroll 1
+    for (int c = 0; c <= lt; ++c) ri += rowM[u][tri_at(lt, c)][i];
+#pragma unroll 1
+    for (int t = lt; t < 4; ++t) ci += colM[u][tri_at(t, lt)][i];
+#pragma unroll 1
+    for (int x = 0; x < S::DT; ++x) {
+      rr += rsum[u][x][l];
+      pj += psum[u][x][l];
+    }
+#pragma unroll 1
+    for (int x = 0; x < S::NW; ++x) {
+      vo += dots[u][0][x];
+      xs += dots[u][1][x];
+    }
+    const float D = gt.D[l], rate = b.a[h];
+    const bool real = l < valid;
+    float suf = real ? ri - D * ci + rr : 0.0f, pre = real ? D * pj : 0.0f;
+    const float own = pre;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const float y = __shfl_down(suf, d), z = __shfl_up(pre, d);
+      if (l + d < kWave) suf += y;
+      if (l >= d) pre += z;
+    }
+    const float gd = suf + (pre - own) + gt.e[63] * xs;
+    const float dD = ci + pj + rate * gd;
+    float ddt = 0.0f;
+    if (real) {
+      const float x = to_f32(static_cast<U>(b.dt)[(tok + l) * b.dt_row + h]) + (b.bias != nullptr ? b.bias[h] : 0.0f);
+      ddt = dD * (1.0f / (1.0f + expf(-x)));
+      static_cast<uint16_t*>(b.ddt)[(tok + l) * b.ddt_row + h] = from_f32<uint16_t>(ddt);
+    }
+    float sa = real ? D * gd : 0.0f, sb = ddt;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) {
+      sa += __shfl_xor(sa, off);
+      sb += __shfl_xor(sb, off);
+    }
+    if (lane == 0) {
+      const int64_t M = int64_t(b.B) * NC, at = int64_t(h) * M + bb * NC + n, all = int64_t(b.H) * M;
+      part[at] = sa;
+      part[all + at] = sb;
+      part[2 * all + at] = vo;
+    }
+  };
 
   for (int hh = 0; hh < r; ++hh) {
-    const int h = hk * r + hh;
+    const int h = hk * r + hh, u = hh & 1;
     const int64_t slot = (bb * b.H + h) * NC + n;
     const float skip = b.d != nullptr ? b.d[h] : 0.0f;
-    // states as operands: row dt, all value columns (k index in the order of wide_frag)
-    const int64_t srow = (slot * DK + 16 * dt + li) * DV + 8 * g;
-    Frag<uint16_t> Sh[VU], Sl[VU], Xh[VU], Xl[VU], XT[KU];
+    uint16_t* const Vs = VO[u][0];
+    uint16_t* const Os = VO[u][1];
+    ChunkGates& gt = gates[u];
+    // this wavefront's state rows as operands (k index over the value columns, in wide_frag's order): S for dQ, X for dK
+    Frag<uint16_t> Ah[VU], Al[VU];
+    const int64_t sbase = (slot * VU * DK + 16 * dt) * 32;
+    {
+      const int ln = lane_now();
+      const int64_t srow = sbase + (ln & 15) * 32 + 8 * (ln >> 4);
+      const uint16_t* h0 = (is_q ? st.sh : st.xh) + srow;
+      const uint16_t* l0 = (is_q ? st.sl : st.xl) + srow;
 #pragma unroll
-    for (int ku = 0; ku < VU; ++ku) {
-      Sh[ku].v = *reinterpret_cast<const bf16x8*>(st.sh + srow + 32 * ku);
-      Sl[ku].v = *reinterpret_cast<const bf16x8*>(st.sl + srow + 32 * ku);
-      Xh[ku].v = *reinterpret_cast<const bf16x8*>(st.xh + srow + 32 * ku);
-      Xl[ku].v = *reinterpret_cast<const bf16x8*>(st.xl + srow + 32 * ku);
+      for (int ku = 0; ku < VU; ++ku) {
+        Ah[ku].v = *reinterpret_cast<const bf16x8*>(h0 + ku * DK * 32);
+        Al[ku].v = *reinterpret_cast<const bf16x8*>(l0 + ku * DK * 32);
+      }
     }
-#pragma unroll
-    for (int ku = 0; ku < KU; ++ku)
-      XT[ku].v = *reinterpret_cast<const bf16x8*>(st.xt + (slot * DV + 16 * vt + li) * DK + 32 * ku + 8 * g);
-    if (w == 7) {
+    if (w == 14) {  // which reads a head's gates last, in step_grads
       const ChunkGates& src = st.gates[slot];
       gt.hi[lane] = src.hi[lane];
       gt.lo[lane] = src.lo[lane];
@@ -400,49 +474,22 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       gt.w[lane] = src.w[lane];
     }
     wait_vmcnt<0>();
-    sync();  // this head's V, dO and gates are there
-    if (hh == 0) {
-      if (valid < C) {  // rows past the end repeat row 0: zeros
+    sync();  // this head's V, dO and gates are there, the one before is done with the LDS
+    if (valid < C) {  // rows past the end repeat row 0: zeros
+      if (hh == 0) {
         for (int at = tid; at < (C - valid) * DK / 8; at += S::THREADS)
           reinterpret_cast<u32x4*>(Qs)[valid * DK / 8 + at] = reinterpret_cast<u32x4*>(Ks)[valid * DK / 8 + at] = u32x4{};
       }
-    }
-    if (valid < C) {
       for (int at = tid; at < (C - valid) * DV / 8; at += S::THREADS)
         reinterpret_cast<u32x4*>(Vs)[valid * DV / 8 + at] = reinterpret_cast<u32x4*>(Os)[valid * DV / 8 + at] = u32x4{};
       sync();
     }
-    float skips = 0.0f, dot = 0.0f;  // v . dO of this chunk; <X, S>
-    for (int at = tid; at < C * DV / 8; at += S::THREADS) {
-      const bf16x8 x = reinterpret_cast<const bf16x8*>(Vs)[at], y = reinterpret_cast<const bf16x8*>(Os)[at];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) skips = fmaf(float(x[e]), float(y[e]), skips);
-    }
-    if (do_q) {
-#pragma unroll
-      for (int ku = 0; ku < VU; ++ku)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          dot = fmaf(float(Sh[ku].v[e]) + float(Sl[ku].v[e]), float(Xh[ku].v[e]) + float(Xl[ku].v[e]), dot);
-    }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-      skips += __shfl_xor(skips, off);
-      dot += __shfl_xor(dot, off);
-    }
-    if (lane == 0) {
-      dots[0][w] = skips;
-      dots[1][w] = dot;
-    }
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int tile = w + 8 * u;
-      if (tile >= 10) break;
-      const int rt = tri_row(tile), ct = tile - tri_at(rt, 0), i = 16 * rt + li;
+    if (hh + 1 < r) fetch_head(hh + 1);
+    if (w < 10) {
+      const int ln = lane_now(), li = ln & 15, g = ln >> 4, i = 16 * rt + li;
       if (hh == 0) {
 #pragma unroll
-        for (int ku = 0; ku < KU; ++ku)
-          mma(raw[u], wide_frag<DK>(Ks, 16 * ct + li, ku, g), wide_frag<DK>(Qs, i, ku, g));
+        for (int ku = 0; ku < KU; ++ku) mma(raw, wide_frag<DK>(Ks, 16 * ct + li, ku, g), wide_frag<DK>(Qs, i, ku, g));
       }
       f32x4 dp = zero4();
 #pragma unroll
@@ -457,82 +504,101 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       for (int qq = 0; qq < 4; ++qq) {
         const bool in = ct < rt || 4 * g + qq <= li;
         const float f = in ? __builtin_amdgcn_exp2f((hi - ch[qq]) + (lo - cl[qq])) : 0.0f;
-        const float m = in ? dp[qq] * (raw[u][qq] * f) : 0.0f;
-        p[qq] = in ? raw[u][qq] * f * D[qq] : 0.0f;
+        const float m = in ? dp[qq] * (raw[qq] * f) : 0.0f;
+        p[qq] = in ? raw[qq] * f * D[qq] : 0.0f;
         d[qq] = in ? dp[qq] * f * D[qq] : 0.0f;
         rs = fmaf(m, D[qq], rs);
         const float cs = row_sum16(m);
-        if (li == 0) colM[tile][4 * g + qq] = cs;
+        if (li == 0) colM[u][tile][4 * g + qq] = cs;
       }
       rs = row_sum4(rs);
-      if (g == 0) rowM[tile][li] = rs;
+      if (g == 0) rowM[u][tile][li] = rs;
       st4(Pm + (tile * 16 + li) * 16 + 4 * g, p);
       st4(Dm + (tile * 16 + li) * 16 + 4 * g, d);
     }
-    sync();
-    float rp[4] = {}, pp[4] = {};  // this wavefront's share of r and of p / D, token 16 t + li
-    if (do_q) {
-      Frag<uint16_t> KT[2];
+    __builtin_amdgcn_sched_barrier(0);
+    // v . dO of this chunk, and <X, S>: half of the value columns of both by the
+    // wavefronts that hold S, the others by those that hold X (one of each key tile)
+    float skips = 0.0f, dot = 0.0f;
+    for (int at = tid; at < C * DV / 8; at += S::THREADS) {
+      const bf16x8 x = reinterpret_cast<const bf16x8*>(Vs)[at], y = reinterpret_cast<const bf16x8*>(Os)[at];
 #pragma unroll
-      for (int ku = 0; ku < 2; ++ku) KT[ku] = sw_frag_tr_wide<DK>(Ks, 16 * dt, ku, lane);
+      for (int e = 0; e < 8; ++e) skips = fmaf(float(x[e]), float(y[e]), skips);
+    }
+    if (ktok == 0) {
+      const int ln = lane_now();
+      const int64_t srow = sbase + (ln & 15) * 32 + 8 * (ln >> 4);
+      const uint16_t* h0 = (is_q ? st.xh : st.sh) + srow;
+      const uint16_t* l0 = (is_q ? st.xl : st.sl) + srow;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        f32x4 x = zero4(), y = zero4();
+      for (int ku = 0; ku < VU; ++ku) {
+        if (VU > 1 ? (ku < VU / 2) != is_q : !is_q) continue;
+        const bf16x8 bh = *reinterpret_cast<const bf16x8*>(h0 + ku * DK * 32), bl = *reinterpret_cast<const bf16x8*>(l0 + ku * DK * 32);
 #pragma unroll
-        for (int ku = 0; ku < VU; ++ku) {
-          const Frag<uint16_t> o = wide_frag<DV>(Os, 16 * t + li, ku, g);
-          mma(y, Sl[ku], o);
-          mma(x, Sh[ku], o);
-        }
-        x = gt.e[16 * t + li] * (x + y);
-        const bf16x4 q = *reinterpret_cast<const bf16x4*>(Qs + swzw_off<DK>(16 * t + li, 16 * dt + 4 * g));
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq) rp[t] = fmaf(x[qq], float(q[qq]), rp[t]);
-#pragma unroll
-        for (int ku = 0; ku < 2; ++ku)
-          if (2 * ku <= t) mma(x, KT[ku], tri_rows(Dm, t, ku, lane));
-        dQ[t] += x;
+        for (int e = 0; e < 8; ++e) dot = fmaf(float(Ah[ku].v[e]) + float(Al[ku].v[e]), float(bh[e]) + float(bl[e]), dot);
       }
     }
-    if (do_k) {
-      Frag<uint16_t> QT[2];
 #pragma unroll
-      for (int ku = 0; ku < 2; ++ku) QT[ku] = sw_frag_tr_wide<DK>(Qs, 16 * dt, ku, lane);
+    for (int off = 32; off > 0; off >>= 1) {
+      skips += __shfl_xor(skips, off);
+      dot += __shfl_xor(dot, off);
+    }
+    if (lane == 0) {
+      dots[u][0][w] = skips;
+      dots[u][1][w] = dot;
+    }
+    __builtin_amdgcn_sched_barrier(0);
+    sync();  // P and dP
+    if (w == 14 && hh > 0) step_grads(hh - 1);
+    // dQ^T = S (dO diag(e))^T + K^T dP, dK^T = X (V diag(w))^T + Q^T dP^T: tokens in columns
+    auto key_grads = [&](auto qc) {
+      constexpr bool Q = decltype(qc)::value;
+      const int ln = lane_now(), li = ln & 15, g = ln >> 4;
+      const uint16_t* rows = Q ? Os : Vs;
+      const uint16_t* mine = Q ? Qs : Ks;
+      Frag<uint16_t> T[2];
+#pragma unroll
+      for (int ku = 0; ku < 2; ++ku) T[ku] = sw_frag_tr_wide<DK>(Q ? Ks : Qs, 16 * dt, ku, ln);
       const float hi_end = gt.hi[63], lo_end = gt.lo[63];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
+      for (int tt = 0; tt < KTOK; ++tt) {
+        const int t = ktok + tt, j = 16 * t + li;
         f32x4 x = zero4(), y = zero4();
 #pragma unroll
         for (int ku = 0; ku < VU; ++ku) {
-          const Frag<uint16_t> v = wide_frag<DV>(Vs, 16 * t + li, ku, g);
-          mma(y, Xl[ku], v);
-          mma(x, Xh[ku], v);
+          const Frag<uint16_t> f = wide_frag<DV>(rows, j, ku, g);
+          mma(y, Al[ku], f);
+          mma(x, Ah[ku], f);
         }
-        const int j = 16 * t + li;
-        x = __builtin_amdgcn_exp2f((hi_end - gt.hi[j]) + (lo_end - gt.lo[j])) * (x + y);
-        const bf16x4 k = *reinterpret_cast<const bf16x4*>(Ks + swzw_off<DK>(j, 16 * dt + 4 * g));
+        x = (Q ? gt.e[j] : __builtin_amdgcn_exp2f((hi_end - gt.hi[j]) + (lo_end - gt.lo[j]))) * (x + y);
+        const bf16x4 o = *reinterpret_cast<const bf16x4*>(mine + swzw_off<DK>(j, 16 * dt + 4 * g));
+        float sum = 0.0f;
 #pragma unroll
-        for (int qq = 0; qq < 4; ++qq) pp[t] = fmaf(x[qq], float(k[qq]), pp[t]);
-        x = gt.D[j] * x;
+        for (int qq = 0; qq < 4; ++qq) sum = fmaf(x[qq], float(o[qq]), sum);
+        sum = row_sum4(sum);
+        if (g == 0) (Q ? rsum : psum)[u][dt][j] = sum;
+        if (!Q) x = gt.D[j] * x;
 #pragma unroll
-        for (int ku = 0; ku < 2; ++ku)
-          if (2 * ku + 1 >= t) mma(x, QT[ku], tri_cols(Dm, t, ku, lane));
-        dK[t] += x;
+        for (int ku = 0; ku < 2; ++ku) {
+          if (Q && 2 * ku <= t) mma(x, T[ku], tri_rows(Dm, t, ku, ln));
+          if (!Q && 2 * ku + 1 >= t) mma(x, T[ku], tri_cols(Dm, t, ku, ln));
+        }
+        dA[tt] += x;
       }
-    }
+    };
+    if (is_q) key_grads(std::true_type{});
+    else key_grads(std::false_type{});
+    __builtin_amdgcn_sched_barrier(0);
+    if (do_v) {
+      const int ln = lane_now(), li = ln & 15, g = ln >> 4;
+      Frag<uint16_t> XT[KU];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const float x = row_sum4(rp[t]), y = row_sum4(pp[t]);
-      if (g == 0) {
-        rin[w][16 * t + li] = x;
-        pin[w][16 * t + li] = y;
-      }
-    }
-    {
+      for (int ku = 0; ku < KU; ++ku)
+        XT[ku].v = *reinterpret_cast<const bf16x8*>(st.xt + ((slot * KU + ku) * DV + 16 * vt + li) * 32 + 8 * g);
       uint16_t* dv = static_cast<uint16_t*>(b.dv) + tok * b.dv_row + int64_t(h) * DV + 16 * vt + 4 * g;
       Frag<uint16_t> OT[2];
 #pragma unroll
-      for (int ku = 0; ku < 2; ++ku) OT[ku] = sw_frag_tr_wide<DV>(Os, 16 * vt, ku, lane);
+      for (int ku = 0; ku < 2; ++ku) OT[ku] = sw_frag_tr_wide<DV>(Os, 16 * vt, ku, ln);
 #pragma unroll
       for (int tt = 0; tt < VTOK; ++tt) {
         const int t = vtok + tt, j = 16 * t + li;
@@ -542,66 +608,23 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
         x = gt.w[j] * x;
 #pragma unroll
         for (int ku = 0; ku < 2; ++ku)
-          if (2 * ku + 1 >= t) mma(x, OT[ku], tri_cols(Pm, t, ku, lane));
+          if (2 * ku + 1 >= t) mma(x, OT[ku], tri_cols(Pm, t, ku, ln));
         const bf16x4 o = *reinterpret_cast<const bf16x4*>(Os + swzw_off<DV>(j, 16 * vt + 4 * g));
 #pragma unroll
         for (int qq = 0; qq < 4; ++qq) x[qq] = fmaf(skip, float(o[qq]), x[qq]);
         if (j < valid) st4(dv + j * b.dv_row, x);
       }
     }
-    sync();
-    if (hh + 1 < r) fetch_head(h + 1);
-    if (w == 0) {
-      const int l = lane, rt = l >> 4, i = l & 15;
-      float ri = 0.0f, ci = 0.0f, rr = 0.0f, pj = 0.0f, xs = 0.0f, vo = 0.0f;
-      for (int c = 0; c <= rt; ++c) ri += rowM[tri_at(rt, c)][i];
-      for (int t = rt; t < 4; ++t) ci += colM[tri_at(t, rt)][i];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        rr += rin[u][l];
-        pj += pin[u][l];
-        vo += dots[0][u];
-        xs += dots[1][u];
-      }
-      const float D = gt.D[l], rate = b.a[h];
-      const bool real = l < valid;
-      float suf = real ? ri - D * ci + rr : 0.0f, pre = real ? D * pj : 0.0f;
-      const float own = pre;
-#pragma unroll
-      for (int d = 1; d < kWave; d <<= 1) {
-        const float y = __shfl_down(suf, d), z = __shfl_up(pre, d);
-        if (l + d < kWave) suf += y;
-        if (l >= d) pre += z;
-      }
-      const float gd = suf + (pre - own) + gt.e[63] * xs;
-      const float dD = ci + pj + rate * gd;
-      float ddt = 0.0f;
-      if (real) {
-        const float x = to_f32(static_cast<U>(b.dt)[(tok + l) * b.dt_row + h]) + (b.bias != nullptr ? b.bias[h] : 0.0f);
-        ddt = dD * (1.0f / (1.0f + expf(-x)));
-        static_cast<uint16_t*>(b.ddt)[(tok + l) * b.ddt_row + h] = from_f32<uint16_t>(ddt);
-      }
-      float sa = real ? D * gd : 0.0f, sb = ddt;
-#pragma unroll
-      for (int off = 32; off > 0; off >>= 1) {
-        sa += __shfl_xor(sa, off);
-        sb += __shfl_xor(sb, off);
-      }
-      if (lane == 0) {
-        const int64_t M = int64_t(b.B) * NC, at = int64_t(h) * M + bb * NC + n, all = int64_t(b.H) * M;
-        part[at] = sa;
-        part[all + at] = sb;
-        part[2 * all + at] = vo;
-      }
-    }
-    if (hh + 1 < r) sync();  // wavefront 0 is done with the gates and the sums
   }
+  sync();
+  if (w == 14) step_grads(r - 1);
+  const int li = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    const int j = 16 * t + li;
+  for (int tt = 0; tt < KTOK; ++tt) {
+    const int j = 16 * (ktok + tt) + li;
     if (j >= valid) continue;
-    if (do_q) st4(static_cast<uint16_t*>(b.dq) + (tok + j) * b.dq_row + hk * DK + 16 * dt + 4 * g, dQ[t]);
-    if (do_k) st4(static_cast<uint16_t*>(b.dk) + (tok + j) * b.dk_row + hk * DK + 16 * dt + 4 * g, dK[t]);
+    uint16_t* out = is_q ? static_cast<uint16_t*>(b.dq) + (tok + j) * b.dq_row : static_cast<uint16_t*>(b.dk) + (tok + j) * b.dk_row;
+    st4(out + hk * DK + 16 * dt + 4 * g, dA[tt]);
   }
 }
 
