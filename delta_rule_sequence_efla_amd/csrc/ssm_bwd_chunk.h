@@ -16,28 +16,41 @@
 
 namespace efla {
 
-// What the chains leave for every (sequence, head, chunk): the state S before it
-// and the gradient X of the state behind it, each as two bf16 parts, X's first also
-// transposed, and the chunk's gates.  The arrays are cut into k-units of 32,
-// [slot][d_v / 32][d_k][32] and [slot][d_k / 32][d_v][32], so that what one
-// workgroup of the chains writes of a chunk is one piece of memory, and so is the
-// operand fragment that a wavefront of the gradients reads.  (Rows of d_v values, of
+// What is kept of every (sequence, head, chunk): its gates, formed by a launch of
+// their own (a wavefront a chunk: formed along the chains, they were half of the
+// chains' time), the state S before it and the gradient X of the state behind it,
+// each as two bf16 parts.  The arrays are cut into k-units of 32,
+// [slot][d_v / 32][d_k][32], so that what one workgroup of the chains writes of a
+// chunk is one piece of memory, and so is the operand fragment that a wavefront of
+// the gradients reads.  (Rows of d_v values, of
 // which four workgroups on four dies write 64 bytes each: 188 us instead of CHAINUS for
 // the chains of 8 x 2048 tokens, 8 heads, d 128.)
-template <int DK>
 struct SsmStates {
-  uint16_t *sh, *sl, *xh, *xl, *xt;
+  uint16_t *sh, *sl, *xh, *xl;
   ChunkGates* gates;
 };
+
+// The gates of every chunk, a wavefront each; slot (b H + h) NC + n.
+__global__ __launch_bounds__(kThreads) void ssm_gates_kernel(SsmBwd b, ChunkGates* __restrict__ gates, int NC, int64_t slots) {
+  const int64_t slot = int64_t(blockIdx.x) * 4 + wave_id();
+  if (slot >= slots) return;
+  const int lane = threadIdx.x & 63, n = int(slot % NC), h = int(slot / NC % b.H);
+  const int64_t t = int64_t(n) * 64 + lane;
+  const bool real = t < b.L;
+  float raw = b.bias != nullptr ? b.bias[h] : 0.0f;
+  if (real) raw += to_f32(static_cast<const uint16_t*>(b.dt)[(slot / NC / b.H * b.L + t) * b.dt_row + h]);
+  put_chunk_gates(gates[slot], raw, b.a[h], real, lane);
+}
 
 template <int DK>
 struct SsmChainShape {
   static constexpr int C = 64, BV = 32, NDT = DK / 16, ND = NDT / 4;  // state tiles of key dims, of an S wave
-  static constexpr int KOFF = 0, VOFF = C * DK, SLOT = C * DK + C * BV;
+  // lo, D, e and w of the gates (1 KiB) behind K and V
+  static constexpr int KOFF = 0, VOFF = C * DK, GOFF = VOFF + C * BV, SLOT = GOFF + 512;
   using TK = DmaTile<C, DK, 1, true>;
   using TV = DmaTile<C, BV, 1, true>;
   static constexpr int PK = TK::PER_WAVE, PV = TV::PER_WAVE;
-  static constexpr int kW = 4, kGate = 8, kDma = 9, THREADS = 10 * kWave;
+  static constexpr int kW = 4, kDma = 8, THREADS = 9 * kWave;
 };
 
 // One chain: S <- e^{G_C} S + A^T diag(w) B over the chunks, storing S before each.
@@ -45,11 +58,11 @@ struct SsmChainShape {
 //   REV       the chunks from last to first, A = q, B = dO, w = e^G
 // A workgroup owns 32 value columns of one (sequence, head).  Four S waves keep a
 // quarter of the key dims each, transposed (a lane's rows are value columns, so that the
-// states leave in whole 16-byte pieces), and for REV the other way round as well, for
-// the transposed copy; four W waves form the parts of diag(w) B of the next chunk; one wavefront the gates, one the transfers.  One
-// barrier a chunk; two workgroups share a compute unit and cover each other's waits.
+// states leave in whole 16-byte pieces); four W waves form the parts of diag(w) B of
+// the next chunk; one wavefront the transfers.  One barrier a chunk; two workgroups
+// share a compute unit and cover each other's waits.
 template <int DK, bool REV, typename Lds>
-__device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, int NVB, const SsmStates<DK>& out) {
+__device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, int NVB, const SsmStates& st) {
   using S = SsmChainShape<DK>;
   constexpr int C = S::C, BV = S::BV, ND = S::ND;
   const int H = b.H, DV = b.DV, bh = x / NVB, vb = x % NVB, h = bh % H, hk = h / (H / b.Hk);
@@ -83,6 +96,8 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
       const U ks = (U)uniform_ptr(k + t * krow), vs = (U)uniform_ptr(v + t * vrow);
       const int valid = valid_of(m);
       const uint32_t addr = lds_addr_of(lds.ring + (m % 3) * S::SLOT);
+      const void* gs = uniform_ptr(st.gates[int64_t(bh) * nc + chunk_of(m)].lo);
+      dma16(gs, uint32_t(lane) * 16u, addr + 2 * S::GOFF);
       auto body = [&](auto ragged) {
         constexpr bool R = decltype(ragged)::value;
 #pragma unroll
@@ -107,41 +122,11 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
       if (n + 2 < nc) issue(n + 2);  // into chunk n - 1's slot
       wait_for(n + 2 < nc);
     }
-  } else if (role == S::kGate) {
-    const auto* dt = static_cast<const uint16_t*>(b.dt) + h;
-    const float rate = b.a[h], bias = b.bias != nullptr ? b.bias[h] : 0.0f;
-    auto load = [&](int n) {
-      if (n >= nc) return 0.0f;
-      return lane < valid_of(n) ? to_f32(dt[(tok_of(n) + lane) * b.dt_row]) : 0.0f;
-    };
-    float now = load(0), next = load(1), then = load(2);
-    auto put = [&](int n) {
-      ChunkGates& gt = lds.gates[n % 3];
-      put_chunk_gates(gt, now + bias, rate, n < nc && lane < valid_of(n), lane);
-      if (!REV && vb == 0 && n < nc) {  // for the gradients, chunk by chunk
-        ChunkGates& dst = out.gates[int64_t(bh) * nc + n];
-        dst.hi[lane] = gt.hi[lane];
-        dst.lo[lane] = gt.lo[lane];
-        dst.D[lane] = gt.D[lane];
-        dst.e[lane] = gt.e[lane];
-        dst.w[lane] = gt.w[lane];
-      }
-      now = next;
-      next = then;
-      then = load(n + 3);
-    };
-    put(0);
-    sync();
-    put(1);
-    for (int n = 0; n < nc; ++n) {
-      sync();
-      put(n + 2);
-    }
   } else if (role >= S::kW) {
     const int c = role & 1, ku = (role >> 1) & 1;
     auto weigh = [&](int n) {
       const Frag<uint16_t> v = value_frag<BV>(lds.ring + (n % 3) * S::SLOT + S::VOFF, c, ku, lane);
-      const float* gw = REV ? lds.gates[n % 3].e : lds.gates[n % 3].w;
+      const float* gw = reinterpret_cast<const float*>(lds.ring + (n % 3) * S::SLOT + S::GOFF) + (REV ? 128 : 192);  // e or w
       f32x4 y[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -170,25 +155,19 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
     }
   } else {
     const int sw = role;
-    // T[d][c][qq]: key dim key_phys(16 (ND sw + d) + li), value column v0 + 8 g + 4 c + qq; N: rows and columns exchanged
-    f32x4 T[ND][2], N[ND][2];
+    f32x4 T[ND][2];  // T[d][c][qq]: key dim key_phys(16 (ND sw + d) + li), value column v0 + 8 g + 4 c + qq
     const float* s0 = REV ? b.dsf : b.s0;
-    const int64_t st = (seq * H + h) * DK;
+    const int64_t row0 = (seq * H + h) * DK;
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
-        const int t0 = 16 * (ND * sw + d);
         T[d][c] = zero4();
-        if (s0 != nullptr) T[d][c] = *reinterpret_cast<const f32x4*>(s0 + (st + key_phys(t0 + li)) * DV + v0 + 8 * g + 4 * c);
-        if (REV) {
-#pragma unroll
-          for (int qq = 0; qq < 4; ++qq)
-            N[d][c][qq] = s0 != nullptr ? s0[(st + key_phys(t0 + 4 * g + qq)) * DV + v0 + value_phys(c, li)] : 0.0f;
-        }
+        if (s0 != nullptr)
+          T[d][c] = *reinterpret_cast<const f32x4*>(s0 + (row0 + key_phys(16 * (ND * sw + d) + li)) * DV + v0 + 8 * g + 4 * c);
       }
-    uint16_t* hi_out = REV ? out.xh : out.sh;
-    uint16_t* lo_out = REV ? out.xl : out.sl;
+    uint16_t* hi_out = REV ? st.xh : st.sh;
+    uint16_t* lo_out = REV ? st.xl : st.sl;
     sync();
     for (int n = 0; n < nc; ++n) {
       sync();
@@ -207,23 +186,11 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
         *reinterpret_cast<bf16x8*>(hi_out + at) = hi.v;
         *reinterpret_cast<bf16x8*>(lo_out + at) = lo.v;
       }
-      if constexpr (REV) {
-        const int u = ND * sw / 2;  // k-unit of these key dims
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint16_t* row = out.xt + ((slot * (DK / 32) + u) * DV + v0 + value_phys(c, li)) * 32 + 8 * g;
-          if constexpr (ND == 2) *reinterpret_cast<bf16x8*>(row) = acc_frag<uint16_t>(N[0][c], N[1][c]).v;
-          else st4(row + 4 * (sw & 1), N[0][c]);
-        }
-      }
-      const float all = lds.gates[n % 3].e[63];
+      const float all = reinterpret_cast<const float*>(lds.ring + (n % 3) * S::SLOT + S::GOFF)[128 + 63];
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          T[d][c] = all * T[d][c];
-          if (REV) N[d][c] = all * N[d][c];
-        }
+        for (int c = 0; c < 2; ++c) T[d][c] = all * T[d][c];
 #pragma unroll
       for (int ku = 0; ku < 2; ++ku)
 #pragma unroll
@@ -233,10 +200,7 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
             Frag<uint16_t> W;
             W.v = lds.bW[n & 1][part][c][ku][lane];
 #pragma unroll
-            for (int d = 0; d < ND; ++d) {
-              mma(T[d][c], W, KT[d][ku]);
-              if (REV) mma(N[d][c], KT[d][ku], W);
-            }
+            for (int d = 0; d < ND; ++d) mma(T[d][c], W, KT[d][ku]);
           }
     }
     if (REV && b.ds0 != nullptr) {
@@ -244,26 +208,24 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
       for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          *reinterpret_cast<f32x4*>(b.ds0 + (st + key_phys(16 * (ND * sw + d) + li)) * DV + v0 + 8 * g + 4 * c) = T[d][c];
+          *reinterpret_cast<f32x4*>(b.ds0 + (row0 + key_phys(16 * (ND * sw + d) + li)) * DV + v0 + 8 * g + 4 * c) = T[d][c];
     }
   }
 }
 
 template <int DK>
 __global__ __launch_bounds__((SsmChainShape<DK>::THREADS), 5) void ssm_chain_kernel(SsmBwd b, int NVB, int half,
-                                                                                    SsmStates<DK> out) {
+                                                                                    SsmStates st) {
   using S = SsmChainShape<DK>;
   __shared__ __align__(1024) uint16_t ring[3 * S::SLOT];
   __shared__ __align__(16) bf16x8 bW[2][2][2][2][kWave];  // [buffer][part][column tile][k-unit]
-  __shared__ __align__(16) ChunkGates gates[3];
   struct Refs {
     uint16_t* ring;
     decltype(bW)& bW;
-    decltype(gates)& gates;
   };
-  Refs lds{ring, bW, gates};
-  if (int(blockIdx.x) < half) ssm_chain_run<DK, true>(lds, b, blockIdx.x, NVB, out);
-  else ssm_chain_run<DK, false>(lds, b, blockIdx.x - half, NVB, out);
+  Refs lds{ring, bW};
+  if (int(blockIdx.x) < half) ssm_chain_run<DK, true>(lds, b, blockIdx.x, NVB, st);
+  else ssm_chain_run<DK, false>(lds, b, blockIdx.x - half, NVB, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -325,12 +287,24 @@ __device__ __forceinline__ Frag<uint16_t> sw_frag_tr_wide(const uint16_t* X, int
   return f;
 }
 
+// Operand row `row` of a tile in the 16-byte layout with the k index in the plain
+// order of common.h, as a transposing read's rows are.
+template <int ROWE>
+__device__ __forceinline__ Frag<uint16_t> key_frag(const uint16_t* X, int row, int ku, int g) {
+  const bf16x4 lo = *reinterpret_cast<const bf16x4*>(X + swzw_off<ROWE>(row, 32 * ku + 4 * g));
+  const bf16x4 hi = *reinterpret_cast<const bf16x4*>(X + swzw_off<ROWE>(row, 32 * ku + 16 + 4 * g));
+  Frag<uint16_t> f;
+  f.v = __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+  return f;
+}
+
 template <int DK, int DV>
-__global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kernel(SsmBwd b, SsmStates<DK> st,
+__global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kernel(SsmBwd b, SsmStates st,
                                                                                    float* __restrict__ part, int NC) {
   using S = SsmGradShape<DK, DV>;
   constexpr int C = S::C, KU = S::KU, VU = S::VU, VT = S::VT, KTOK = S::KTOK, VTOK = S::VTOK;
   __shared__ __align__(1024) uint16_t Qs[C * DK], Ks[C * DK], VO[2][2][C * DV];  // V and dO of this head and the next
+  __shared__ __align__(1024) uint16_t Xs[DK * DV];  // X's first part, from the wavefronts that hold it
   __shared__ __align__(16) uint16_t Pm[10 * 256], Dm[10 * 256];
   // of this head and the next: the step gradients of a head are formed beside the next head's products
   __shared__ __align__(16) ChunkGates gates[2];
@@ -342,13 +316,13 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
   const uint32_t bk = wg / uint32_t(NC);
   const int hk = int(bk % uint32_t(b.Hk));
   const int64_t bb = bk / uint32_t(b.Hk);
-  const int tid = threadIdx.x, lane = tid & 63, w = wave_id();
+  const int w = wave_id();
   // The lane's index afresh, so that addresses formed from it belong to one stage:
   // kept over the heads, they were 43 registers a lane of scratch memory, 180 MB
-  // of writes in all and three times the time.
+  // of writes in all and half of the time.
   auto lane_now = [&]() {
-    int x = lane;
-    asm volatile("" : "+v"(x));
+    int x;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(x));
     return x;
   };
   const int64_t t0 = int64_t(n) * C, tok = bb * b.L + t0;
@@ -362,10 +336,11 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     typename S::TK tk;
     const U qs = (U)uniform_ptr(static_cast<U>(b.q) + tok * b.q_row + hk * DK);
     const U ks = (U)uniform_ptr(static_cast<U>(b.k) + tok * b.k_row + hk * DK);
-    tk.init(b.q_row, lane, w);
+    const int ln = lane_now();
+    tk.init(b.q_row, ln, w);
 #pragma unroll
     for (int i = 0; i < S::TK::PER_WAVE; ++i) tk.template issue<true>(i, lds_addr_of(Qs), qs, valid);
-    tk.init(b.k_row, lane, w);
+    tk.init(b.k_row, ln, w);
 #pragma unroll
     for (int i = 0; i < S::TK::PER_WAVE; ++i) tk.template issue<true>(i, lds_addr_of(Ks), ks, valid);
   }
@@ -374,10 +349,11 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     typename S::TV tv;
     const U vs = (U)uniform_ptr(static_cast<U>(b.v) + tok * b.v_row + int64_t(h) * DV);
     const U os = (U)uniform_ptr(static_cast<U>(b.d_o) + tok * b.do_row + int64_t(h) * DV);
-    tv.init(b.v_row, lane, w);
+    const int ln = lane_now();
+    tv.init(b.v_row, ln, w);
 #pragma unroll
     for (int i = 0; i < S::TV::PER_WAVE; ++i) tv.template issue<true>(i, lds_addr_of(VO[hh & 1][0]), vs, valid);
-    tv.init(b.do_row, lane, w);
+    tv.init(b.do_row, ln, w);
 #pragma unroll
     for (int i = 0; i < S::TV::PER_WAVE; ++i) tv.template issue<true>(i, lds_addr_of(VO[hh & 1][1]), os, valid);
   };
@@ -395,7 +371,7 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
 
   // The gradients of head hh's steps from the sums in buffer hh & 1, a lane a token.
   auto step_grads = [&](int hh) {
-    const int h = hk * r + hh, u = hh & 1, l = lane, lt = l >> 4, i = l & 15;
+    const int h = hk * r + hh, u = hh & 1, l = lane_now(), lt = l >> 4, i = l & 15;
     const ChunkGates& gt = gates[u];
     float ri = 0.0f, ci = 0.0f, rr = 0.0f, pj = 0.0f, xs = 0.0f, vo = 0.0f;
 #pragma unroll 1
@@ -436,13 +412,41 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       sa += __shfl_xor(sa, off);
       sb += __shfl_xor(sb, off);
     }
-    if (lane == 0) {
+    if (l == 0) {
       const int64_t M = int64_t(b.B) * NC, at = int64_t(h) * M + bb * NC + n, all = int64_t(b.H) * M;
       part[at] = sa;
       part[all + at] = sb;
       part[2 * all + at] = vo;
     }
   };
+
+  // This wavefront's state rows as operands (k index over the value columns, in
+  // wide_frag's order), S for dQ, X for dK, and a head's gates.  They are asked for
+  // as soon as the head before has used its own.
+  Frag<uint16_t> Ah[VU], Al[VU];
+  auto fetch_state = [&](int hh) {
+    const int64_t slot = (bb * b.H + hk * r + hh) * NC + n;
+    const int ln = lane_now();
+    const int64_t row = ((slot * VU) * DK + 16 * dt + (ln & 15)) * 32 + 8 * (ln >> 4);
+    const uint16_t* h0 = (is_q ? st.sh : st.xh) + row;
+    const uint16_t* l0 = (is_q ? st.sl : st.xl) + row;
+#pragma unroll
+    for (int ku = 0; ku < VU; ++ku) {
+      Ah[ku].v = *reinterpret_cast<const bf16x8*>(h0 + ku * DK * 32);
+      Al[ku].v = *reinterpret_cast<const bf16x8*>(l0 + ku * DK * 32);
+    }
+    if (w == 14) {  // which reads a head's gates last, in step_grads
+      const ChunkGates& src = st.gates[slot];
+      ChunkGates& gt = gates[hh & 1];
+      gt.hi[ln] = src.hi[ln];
+      gt.lo[ln] = src.lo[ln];
+      gt.D[ln] = src.D[ln];
+      gt.e[ln] = src.e[ln];
+      gt.w[ln] = src.w[ln];
+    }
+  };
+  wait_vmcnt<0>();  // Q, K and the first head's V and dO
+  fetch_state(0);
 
   for (int hh = 0; hh < r; ++hh) {
     const int h = hk * r + hh, u = hh & 1;
@@ -451,36 +455,14 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     uint16_t* const Vs = VO[u][0];
     uint16_t* const Os = VO[u][1];
     ChunkGates& gt = gates[u];
-    // this wavefront's state rows as operands (k index over the value columns, in wide_frag's order): S for dQ, X for dK
-    Frag<uint16_t> Ah[VU], Al[VU];
     const int64_t sbase = (slot * VU * DK + 16 * dt) * 32;
-    {
-      const int ln = lane_now();
-      const int64_t srow = sbase + (ln & 15) * 32 + 8 * (ln >> 4);
-      const uint16_t* h0 = (is_q ? st.sh : st.xh) + srow;
-      const uint16_t* l0 = (is_q ? st.sl : st.xl) + srow;
-#pragma unroll
-      for (int ku = 0; ku < VU; ++ku) {
-        Ah[ku].v = *reinterpret_cast<const bf16x8*>(h0 + ku * DK * 32);
-        Al[ku].v = *reinterpret_cast<const bf16x8*>(l0 + ku * DK * 32);
-      }
-    }
-    if (w == 14) {  // which reads a head's gates last, in step_grads
-      const ChunkGates& src = st.gates[slot];
-      gt.hi[lane] = src.hi[lane];
-      gt.lo[lane] = src.lo[lane];
-      gt.D[lane] = src.D[lane];
-      gt.e[lane] = src.e[lane];
-      gt.w[lane] = src.w[lane];
-    }
-    wait_vmcnt<0>();
     sync();  // this head's V, dO and gates are there, the one before is done with the LDS
     if (valid < C) {  // rows past the end repeat row 0: zeros
       if (hh == 0) {
-        for (int at = tid; at < (C - valid) * DK / 8; at += S::THREADS)
+        for (int at = w * kWave + lane_now(); at < (C - valid) * DK / 8; at += S::THREADS)
           reinterpret_cast<u32x4*>(Qs)[valid * DK / 8 + at] = reinterpret_cast<u32x4*>(Ks)[valid * DK / 8 + at] = u32x4{};
       }
-      for (int at = tid; at < (C - valid) * DV / 8; at += S::THREADS)
+      for (int at = w * kWave + lane_now(); at < (C - valid) * DV / 8; at += S::THREADS)
         reinterpret_cast<u32x4*>(Vs)[valid * DV / 8 + at] = reinterpret_cast<u32x4*>(Os)[valid * DV / 8 + at] = u32x4{};
       sync();
     }
@@ -516,11 +498,17 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       st4(Pm + (tile * 16 + li) * 16 + 4 * g, p);
       st4(Dm + (tile * 16 + li) * 16 + 4 * g, d);
     }
+    if (!is_q && ktok == 0) {
+      const int ln = lane_now();
+#pragma unroll
+      for (int ku = 0; ku < VU; ++ku)
+        *reinterpret_cast<bf16x8*>(Xs + swzw_off<DV>(16 * dt + (ln & 15), 32 * ku + 8 * (ln >> 4))) = Ah[ku].v;
+    }
     __builtin_amdgcn_sched_barrier(0);
     // v . dO of this chunk, and <X, S>: half of the value columns of both by the
     // wavefronts that hold S, the others by those that hold X (one of each key tile)
     float skips = 0.0f, dot = 0.0f;
-    for (int at = tid; at < C * DV / 8; at += S::THREADS) {
+    for (int at = w * kWave + lane_now(); at < C * DV / 8; at += S::THREADS) {
       const bf16x8 x = reinterpret_cast<const bf16x8*>(Vs)[at], y = reinterpret_cast<const bf16x8*>(Os)[at];
 #pragma unroll
       for (int e = 0; e < 8; ++e) skips = fmaf(float(x[e]), float(y[e]), skips);
@@ -543,12 +531,12 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       skips += __shfl_xor(skips, off);
       dot += __shfl_xor(dot, off);
     }
-    if (lane == 0) {
+    if (lane_now() == 0) {
       dots[u][0][w] = skips;
       dots[u][1][w] = dot;
     }
     __builtin_amdgcn_sched_barrier(0);
-    sync();  // P and dP
+    sync();  // P, dP and X
     if (w == 14 && hh > 0) step_grads(hh - 1);
     // dQ^T = S (dO diag(e))^T + K^T dP, dK^T = X (V diag(w))^T + Q^T dP^T: tokens in columns
     auto key_grads = [&](auto qc) {
@@ -588,13 +576,16 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     };
     if (is_q) key_grads(std::true_type{});
     else key_grads(std::false_type{});
+    if (hh + 1 < r) {
+      wait_vmcnt<0>();  // the next head's V and dO
+      fetch_state(hh + 1);
+    }
     __builtin_amdgcn_sched_barrier(0);
     if (do_v) {
       const int ln = lane_now(), li = ln & 15, g = ln >> 4;
-      Frag<uint16_t> XT[KU];
+      Frag<uint16_t> XT[KU];  // X^T: row 16 vt + li, k index over the key dims in the order of key_frag
 #pragma unroll
-      for (int ku = 0; ku < KU; ++ku)
-        XT[ku].v = *reinterpret_cast<const bf16x8*>(st.xt + ((slot * KU + ku) * DV + 16 * vt + li) * 32 + 8 * g);
+      for (int ku = 0; ku < KU; ++ku) XT[ku] = sw_frag_tr_wide<DV>(Xs, 16 * vt, ku, ln);
       uint16_t* dv = static_cast<uint16_t*>(b.dv) + tok * b.dv_row + int64_t(h) * DV + 16 * vt + 4 * g;
       Frag<uint16_t> OT[2];
 #pragma unroll
@@ -604,7 +595,7 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
         const int t = vtok + tt, j = 16 * t + li;
         f32x4 x = zero4();
 #pragma unroll
-        for (int ku = 0; ku < KU; ++ku) mma(x, XT[ku], wide_frag<DK>(Ks, j, ku, g));
+        for (int ku = 0; ku < KU; ++ku) mma(x, XT[ku], key_frag<DK>(Ks, j, ku, g));
         x = gt.w[j] * x;
 #pragma unroll
         for (int ku = 0; ku < 2; ++ku)
@@ -618,7 +609,7 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
   }
   sync();
   if (w == 14) step_grads(r - 1);
-  const int li = lane & 15, g = lane >> 4;
+  const int ln = lane_now(), li = ln & 15, g = ln >> 4;
 #pragma unroll
   for (int tt = 0; tt < KTOK; ++tt) {
     const int j = 16 * (ktok + tt) + li;

@@ -8,13 +8,13 @@ namespace efla {
 namespace {
 
 struct Layout {
-  size_t state, gates, part, total;  // bytes of one of the five state arrays; offsets behind them
+  size_t state, gates, part, total;  // bytes of one of the four state arrays; offsets behind them
 };
 Layout layout(int B, int H, int64_t L, int DK, int DV) {
   const size_t slots = size_t(B) * H * size_t((L + 63) / 64);
   Layout w{};
   w.state = slots * DK * DV * 2;
-  w.gates = 5 * w.state;
+  w.gates = 4 * w.state;
   w.part = w.gates + slots * sizeof(ChunkGates);
   w.total = w.part + slots * 3 * sizeof(float);
   return w;
@@ -25,11 +25,15 @@ hipError_t bwd_impl(const SsmBwd& b, void* ws, hipStream_t s) {
   const Layout w = layout(b.B, b.H, b.L, DK, b.DV);
   auto* at = static_cast<unsigned char*>(ws);
   auto arr = [&](int i) { return reinterpret_cast<uint16_t*>(at + i * w.state); };
-  const SsmStates<DK> st{arr(0), arr(1), arr(2), arr(3), arr(4), reinterpret_cast<ChunkGates*>(at + w.gates)};
+  const SsmStates st{arr(0), arr(1), arr(2), arr(3), reinterpret_cast<ChunkGates*>(at + w.gates)};
   float* part = reinterpret_cast<float*>(at + w.part);
   const int NC = int((b.L + 63) / 64), NVB = b.DV / 32, half = b.B * b.H * NVB;
-  hipLaunchKernelGGL((ssm_chain_kernel<DK>), dim3(unsigned(2 * half)), dim3(SsmChainShape<DK>::THREADS), 0, s, b, NVB, half, st);
+  const int64_t slots = int64_t(b.B) * b.H * NC;
+  hipLaunchKernelGGL(ssm_gates_kernel, dim3(unsigned((slots + 3) / 4)), dim3(kThreads), 0, s, b, st.gates, NC, slots);
   hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((ssm_chain_kernel<DK>), dim3(unsigned(2 * half)), dim3(SsmChainShape<DK>::THREADS), 0, s, b, NVB, half, st);
+  e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid(unsigned(int64_t(b.B) * b.Hk * NC)), wg(SsmGradShape<DK, 64>::THREADS);
   switch (b.DV) {
