@@ -28,6 +28,14 @@ namespace efla {
 struct SsmStates {
   uint16_t *sh, *sl, *xh, *xl;
   ChunkGates* gates;
+  struct ChunkSums* sums;
+};
+
+// What the gradients of a chunk's steps are formed from (ssm_steps_kernel), each
+// written by the wavefront that has it: row sums of M and its column sums by D, a
+// tile each; r and p / D by 16 key dims; <X, S> and v . dO by wavefront.
+struct ChunkSums {
+  float row[10][16], col[10][16], r[8][64], p[8][64], xs[16], vo[16];
 };
 
 // The gates of every chunk, a wavefront each; slot (b H + h) NC + n.
@@ -235,7 +243,7 @@ __global__ __launch_bounds__((SsmChainShape<DK>::THREADS), 5) void ssm_chain_ker
 //   their decays and D into the LDS, row and column sums of M
 //   then the first half key dims of dQ^T each (all tokens), the other half of dK^T,
 //   states as operands straight from memory, and all of them a share of dV^T
-//   then one of them the gradients of the 64 steps, beside the next head
+// The gradients of the 64 steps follow in a launch of their own.
 // All products have tokens as columns, so a lane's four rows are adjacent values
 // of one token.
 template <int DK, int DV>
@@ -298,17 +306,23 @@ __device__ __forceinline__ Frag<uint16_t> key_frag(const uint16_t* X, int row, i
   return f;
 }
 
+// Sum of the products of eight pairs of bf16 values, added to c.
+__device__ __forceinline__ float dot8(const u32x4& x, const u32x4& y, float c) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    c = __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, uint32_t(x[e])), __builtin_bit_cast(bf16x2, uint32_t(y[e])), c, false);
+  return c;
+}
+
 template <int DK, int DV>
-__global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kernel(SsmBwd b, SsmStates st,
-                                                                                   float* __restrict__ part, int NC) {
+__global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kernel(SsmBwd b, SsmStates st, int NC) {
   using S = SsmGradShape<DK, DV>;
   constexpr int C = S::C, KU = S::KU, VU = S::VU, VT = S::VT, KTOK = S::KTOK, VTOK = S::VTOK;
   __shared__ __align__(1024) uint16_t Qs[C * DK], Ks[C * DK], VO[2][2][C * DV];  // V and dO of this head and the next
   __shared__ __align__(1024) uint16_t Xs[DK * DV];  // X's first part, from the wavefronts that hold it
   __shared__ __align__(16) uint16_t Pm[10 * 256], Dm[10 * 256];
-  // of this head and the next: the step gradients of a head are formed beside the next head's products
-  __shared__ __align__(16) ChunkGates gates[2];
-  __shared__ float rowM[2][10][16], colM[2][10][16], rsum[2][S::DT][C], psum[2][S::DT][C], dots[2][2][S::NW];
+  __shared__ __align__(16) ChunkGates gates[2];  // of this head and the next
 
   const int r = b.H / b.Hk;
   const uint32_t wg = blockIdx.x;
@@ -369,57 +383,6 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
   f32x4 raw = zero4();  // of tile w: raw[qq] = k_j . q_i, j = 16 ct + 4 g + qq, i = 16 rt + li
   const int tile = w < 10 ? w : 9, rt = tri_row(tile), ct = tile - tri_at(rt, 0);
 
-  // The gradients of head hh's steps from the sums in buffer hh & 1, a lane a token.
-  auto step_grads = [&](int hh) {
-    const int h = hk * r + hh, u = hh & 1, l = lane_now(), lt = l >> 4, i = l & 15;
-    const ChunkGates& gt = gates[u];
-    float ri = 0.0f, ci = 0.0f, rr = 0.0f, pj = 0.0f, xs = 0.0f, vo = 0.0f;
-#pragma unroll 1
-    for (int c = 0; c <= lt; ++c) ri += rowM[u][tri_at(lt, c)][i];
-#pragma unroll 1
-    for (int t = lt; t < 4; ++t) ci += colM[u][tri_at(t, lt)][i];
-#pragma unroll 1
-    for (int x = 0; x < S::DT; ++x) {
-      rr += rsum[u][x][l];
-      pj += psum[u][x][l];
-    }
-#pragma unroll 1
-    for (int x = 0; x < S::NW; ++x) {
-      vo += dots[u][0][x];
-      xs += dots[u][1][x];
-    }
-    const float D = gt.D[l], rate = b.a[h];
-    const bool real = l < valid;
-    float suf = real ? ri - D * ci + rr : 0.0f, pre = real ? D * pj : 0.0f;
-    const float own = pre;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const float y = __shfl_down(suf, d), z = __shfl_up(pre, d);
-      if (l + d < kWave) suf += y;
-      if (l >= d) pre += z;
-    }
-    const float gd = suf + (pre - own) + gt.e[63] * xs;
-    const float dD = ci + pj + rate * gd;
-    float ddt = 0.0f;
-    if (real) {
-      const float x = to_f32(static_cast<U>(b.dt)[(tok + l) * b.dt_row + h]) + (b.bias != nullptr ? b.bias[h] : 0.0f);
-      ddt = dD * (1.0f / (1.0f + expf(-x)));
-      static_cast<uint16_t*>(b.ddt)[(tok + l) * b.ddt_row + h] = from_f32<uint16_t>(ddt);
-    }
-    float sa = real ? D * gd : 0.0f, sb = ddt;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-      sa += __shfl_xor(sa, off);
-      sb += __shfl_xor(sb, off);
-    }
-    if (l == 0) {
-      const int64_t M = int64_t(b.B) * NC, at = int64_t(h) * M + bb * NC + n, all = int64_t(b.H) * M;
-      part[at] = sa;
-      part[all + at] = sb;
-      part[2 * all + at] = vo;
-    }
-  };
-
   // This wavefront's state rows as operands (k index over the value columns, in
   // wide_frag's order), S for dQ, X for dK, and a head's gates.  They are asked for
   // as soon as the head before has used its own.
@@ -435,7 +398,7 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       Ah[ku].v = *reinterpret_cast<const bf16x8*>(h0 + ku * DK * 32);
       Al[ku].v = *reinterpret_cast<const bf16x8*>(l0 + ku * DK * 32);
     }
-    if (w == 14) {  // which reads a head's gates last, in step_grads
+    if (w == 14) {
       const ChunkGates& src = st.gates[slot];
       ChunkGates& gt = gates[hh & 1];
       gt.hi[ln] = src.hi[ln];
@@ -445,8 +408,8 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       gt.w[ln] = src.w[ln];
     }
   };
-  wait_vmcnt<0>();  // Q, K and the first head's V and dO
   fetch_state(0);
+  wait_vmcnt<0>();  // Q, K and the first head's V and dO
 
   for (int hh = 0; hh < r; ++hh) {
     const int h = hk * r + hh, u = hh & 1;
@@ -454,7 +417,8 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     const float skip = b.d != nullptr ? b.d[h] : 0.0f;
     uint16_t* const Vs = VO[u][0];
     uint16_t* const Os = VO[u][1];
-    ChunkGates& gt = gates[u];
+    const ChunkGates& gt = gates[u];
+    ChunkSums& sums = st.sums[slot];
     const int64_t sbase = (slot * VU * DK + 16 * dt) * 32;
     sync();  // this head's V, dO and gates are there, the one before is done with the LDS
     if (valid < C) {  // rows past the end repeat row 0: zeros
@@ -491,10 +455,10 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
         d[qq] = in ? dp[qq] * f * D[qq] : 0.0f;
         rs = fmaf(m, D[qq], rs);
         const float cs = row_sum16(m);
-        if (li == 0) colM[u][tile][4 * g + qq] = cs;
+        if (li == 0) sums.col[tile][4 * g + qq] = cs;
       }
       rs = row_sum4(rs);
-      if (g == 0) rowM[u][tile][li] = rs;
+      if (g == 0) sums.row[tile][li] = rs;
       st4(Pm + (tile * 16 + li) * 16 + 4 * g, p);
       st4(Dm + (tile * 16 + li) * 16 + 4 * g, d);
     }
@@ -508,11 +472,8 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     // v . dO of this chunk, and <X, S>: half of the value columns of both by the
     // wavefronts that hold S, the others by those that hold X (one of each key tile)
     float skips = 0.0f, dot = 0.0f;
-    for (int at = w * kWave + lane_now(); at < C * DV / 8; at += S::THREADS) {
-      const bf16x8 x = reinterpret_cast<const bf16x8*>(Vs)[at], y = reinterpret_cast<const bf16x8*>(Os)[at];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) skips = fmaf(float(x[e]), float(y[e]), skips);
-    }
+    for (int at = w * kWave + lane_now(); at < C * DV / 8; at += S::THREADS)
+      skips = dot8(reinterpret_cast<const u32x4*>(Vs)[at], reinterpret_cast<const u32x4*>(Os)[at], skips);
     if (ktok == 0) {
       const int ln = lane_now();
       const int64_t srow = sbase + (ln & 15) * 32 + 8 * (ln >> 4);
@@ -521,23 +482,21 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
 #pragma unroll
       for (int ku = 0; ku < VU; ++ku) {
         if (VU > 1 ? (ku < VU / 2) != is_q : !is_q) continue;
-        const bf16x8 bh = *reinterpret_cast<const bf16x8*>(h0 + ku * DK * 32), bl = *reinterpret_cast<const bf16x8*>(l0 + ku * DK * 32);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) dot = fmaf(float(Ah[ku].v[e]) + float(Al[ku].v[e]), float(bh[e]) + float(bl[e]), dot);
+        const u32x4 bh = *reinterpret_cast<const u32x4*>(h0 + ku * DK * 32), bl = *reinterpret_cast<const u32x4*>(l0 + ku * DK * 32);
+        const u32x4 ah = __builtin_bit_cast(u32x4, Ah[ku].v), al = __builtin_bit_cast(u32x4, Al[ku].v);
+        dot = dot8(al, bh, dot);  // the product of the two low parts is 2^-18 of the whole, dropped
+        dot = dot8(ah, bl, dot);
+        dot = dot8(ah, bh, dot);
       }
     }
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) {
-      skips += __shfl_xor(skips, off);
-      dot += __shfl_xor(dot, off);
-    }
+    skips = row_sum4(row_sum16(skips));
+    dot = row_sum4(row_sum16(dot));
     if (lane_now() == 0) {
-      dots[u][0][w] = skips;
-      dots[u][1][w] = dot;
+      sums.vo[w] = skips;
+      sums.xs[w] = dot;
     }
     __builtin_amdgcn_sched_barrier(0);
     sync();  // P, dP and X
-    if (w == 14 && hh > 0) step_grads(hh - 1);
     // dQ^T = S (dO diag(e))^T + K^T dP, dK^T = X (V diag(w))^T + Q^T dP^T: tokens in columns
     auto key_grads = [&](auto qc) {
       constexpr bool Q = decltype(qc)::value;
@@ -564,7 +523,7 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
 #pragma unroll
         for (int qq = 0; qq < 4; ++qq) sum = fmaf(x[qq], float(o[qq]), sum);
         sum = row_sum4(sum);
-        if (g == 0) (Q ? rsum : psum)[u][dt][j] = sum;
+        if (g == 0) (Q ? sums.r : sums.p)[dt][j] = sum;
         if (!Q) x = gt.D[j] * x;
 #pragma unroll
         for (int ku = 0; ku < 2; ++ku) {
@@ -607,8 +566,6 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       }
     }
   }
-  sync();
-  if (w == 14) step_grads(r - 1);
   const int ln = lane_now(), li = ln & 15, g = ln >> 4;
 #pragma unroll
   for (int tt = 0; tt < KTOK; ++tt) {
@@ -616,6 +573,65 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     if (j >= valid) continue;
     uint16_t* out = is_q ? static_cast<uint16_t*>(b.dq) + (tok + j) * b.dq_row : static_cast<uint16_t*>(b.dk) + (tok + j) * b.dk_row;
     st4(out + hk * DK + 16 * dt + 4 * g, dA[tt]);
+  }
+}
+
+// ddt of every token and the chunks' shares of da, dbias and dd from their sums
+// (ssm.h), a wavefront a chunk, a lane a token.  DT: key tiles of 16.
+__global__ __launch_bounds__(kThreads) void ssm_steps_kernel(SsmBwd b, SsmStates st, float* __restrict__ part, int NC,
+                                                             int64_t slots, int DT) {
+  const int64_t slot = int64_t(blockIdx.x) * 4 + wave_id();
+  if (slot >= slots) return;
+  const int l = threadIdx.x & 63, lt = l >> 4, i = l & 15;
+  const int n = int(slot % NC), h = int(slot / NC % b.H);
+  const int64_t bb = slot / NC / b.H, t = int64_t(n) * 64 + l, tok = bb * b.L + t;
+  const bool real = t < b.L;
+  const ChunkSums& s = st.sums[slot];
+  const ChunkGates& gt = st.gates[slot];
+  float ri = 0.0f, ci = 0.0f, rr = 0.0f, pj = 0.0f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    const float x = s.row[tri_at(lt, c <= lt ? c : lt)][i], y = s.col[tri_at(c >= lt ? c : lt, lt)][i];
+    ri += c <= lt ? x : 0.0f;
+    ci += c >= lt ? y : 0.0f;
+  }
+#pragma unroll
+  for (int x = 0; x < 8; ++x) {
+    if (x >= DT) break;
+    rr += s.r[x][l];
+    pj += s.p[x][l];
+  }
+  float xs = l < 16 ? s.xs[l] : 0.0f, vo = l < 16 ? s.vo[l] : 0.0f;
+  const float D = gt.D[l], rate = b.a[h];
+  float x = b.bias != nullptr ? b.bias[h] : 0.0f;
+  if (real) x += to_f32(static_cast<const uint16_t*>(b.dt)[tok * b.dt_row + h]);
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    xs += __shfl_xor(xs, off);
+    vo += __shfl_xor(vo, off);
+  }
+  float suf = real ? ri - D * ci + rr : 0.0f, pre = real ? D * pj : 0.0f;
+  const float own = pre;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const float y = __shfl_down(suf, d), z = __shfl_up(pre, d);
+    if (l + d < kWave) suf += y;
+    if (l >= d) pre += z;
+  }
+  const float gd = suf + (pre - own) + gt.e[63] * xs;
+  const float ddt = real ? (ci + pj + rate * gd) * (1.0f / (1.0f + expf(-x))) : 0.0f;
+  if (real) static_cast<uint16_t*>(b.ddt)[tok * b.ddt_row + h] = from_f32<uint16_t>(ddt);
+  float sa = real ? D * gd : 0.0f, sb = ddt;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) {
+    sa += __shfl_xor(sa, off);
+    sb += __shfl_xor(sb, off);
+  }
+  if (l == 0) {
+    const int64_t M = int64_t(b.B) * NC, at = int64_t(h) * M + bb * NC + n, all = int64_t(b.H) * M;
+    part[at] = sa;
+    part[all + at] = sb;
+    part[2 * all + at] = vo;
   }
 }
 

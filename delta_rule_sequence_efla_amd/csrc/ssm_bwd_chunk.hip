@@ -8,14 +8,15 @@ namespace efla {
 namespace {
 
 struct Layout {
-  size_t state, gates, part, total;  // bytes of one of the four state arrays; offsets behind them
+  size_t state, gates, sums, part, total;  // bytes of one of the four state arrays; offsets behind them
 };
 Layout layout(int B, int H, int64_t L, int DK, int DV) {
   const size_t slots = size_t(B) * H * size_t((L + 63) / 64);
   Layout w{};
   w.state = slots * DK * DV * 2;
   w.gates = 4 * w.state;
-  w.part = w.gates + slots * sizeof(ChunkGates);
+  w.sums = w.gates + slots * sizeof(ChunkGates);
+  w.part = w.sums + slots * sizeof(ChunkSums);
   w.total = w.part + slots * 3 * sizeof(float);
   return w;
 }
@@ -25,7 +26,8 @@ hipError_t bwd_impl(const SsmBwd& b, void* ws, hipStream_t s) {
   const Layout w = layout(b.B, b.H, b.L, DK, b.DV);
   auto* at = static_cast<unsigned char*>(ws);
   auto arr = [&](int i) { return reinterpret_cast<uint16_t*>(at + i * w.state); };
-  const SsmStates st{arr(0), arr(1), arr(2), arr(3), reinterpret_cast<ChunkGates*>(at + w.gates)};
+  const SsmStates st{arr(0), arr(1), arr(2), arr(3), reinterpret_cast<ChunkGates*>(at + w.gates),
+                     reinterpret_cast<ChunkSums*>(at + w.sums)};
   float* part = reinterpret_cast<float*>(at + w.part);
   const int NC = int((b.L + 63) / 64), NVB = b.DV / 32, half = b.B * b.H * NVB;
   const int64_t slots = int64_t(b.B) * b.H * NC;
@@ -37,11 +39,14 @@ hipError_t bwd_impl(const SsmBwd& b, void* ws, hipStream_t s) {
   if (e != hipSuccess) return e;
   const dim3 grid(unsigned(int64_t(b.B) * b.Hk * NC)), wg(SsmGradShape<DK, 64>::THREADS);
   switch (b.DV) {
-    case 32: hipLaunchKernelGGL((ssm_grad_kernel<DK, 32>), grid, wg, 0, s, b, st, part, NC); break;
-    case 64: hipLaunchKernelGGL((ssm_grad_kernel<DK, 64>), grid, wg, 0, s, b, st, part, NC); break;
-    case 128: hipLaunchKernelGGL((ssm_grad_kernel<DK, 128>), grid, wg, 0, s, b, st, part, NC); break;
+    case 32: hipLaunchKernelGGL((ssm_grad_kernel<DK, 32>), grid, wg, 0, s, b, st, NC); break;
+    case 64: hipLaunchKernelGGL((ssm_grad_kernel<DK, 64>), grid, wg, 0, s, b, st, NC); break;
+    case 128: hipLaunchKernelGGL((ssm_grad_kernel<DK, 128>), grid, wg, 0, s, b, st, NC); break;
     default: return hipErrorInvalidValue;
   }
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(ssm_steps_kernel, dim3(unsigned((slots + 3) / 4)), dim3(kThreads), 0, s, b, st, part, NC, slots, DK / 16);
   e = hipGetLastError();
   return e != hipSuccess ? e : launch_ssm_sums(part, b.da, b.dbias, b.dd, int64_t(b.B) * NC, b.H, s);
 }
