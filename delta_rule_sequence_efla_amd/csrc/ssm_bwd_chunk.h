@@ -53,11 +53,9 @@ __global__ __launch_bounds__(kThreads) void ssm_gates_kernel(SsmBwd b, ChunkGate
 template <int DK>
 struct SsmChainShape {
   static constexpr int C = 64, BV = 32, NDT = DK / 16, ND = NDT / 4;  // state tiles of key dims, of an S wave
-  // lo, D, e and w of the gates (1 KiB) behind K and V
-  static constexpr int KOFF = 0, VOFF = C * DK, GOFF = VOFF + C * BV, SLOT = GOFF + 512;
+  static constexpr int SLOT = C * DK;
   using TK = DmaTile<C, DK, 1, true>;
-  using TV = DmaTile<C, BV, 1, true>;
-  static constexpr int PK = TK::PER_WAVE, PV = TV::PER_WAVE;
+  static constexpr int PK = TK::PER_WAVE;
   static constexpr int kW = 4, kDma = 8, THREADS = 9 * kWave;
 };
 
@@ -67,13 +65,18 @@ struct SsmChainShape {
 // A workgroup owns 32 value columns of one (sequence, head).  Four S waves keep a
 // quarter of the key dims each, transposed (a lane's rows are value columns, so that the
 // states leave in whole 16-byte pieces); four W waves form the parts of diag(w) B of
-// the next chunk; one wavefront the transfers.  One barrier a chunk; two workgroups
-// share a compute unit and cover each other's waits.
+// the next chunk, from rows they have asked for three chunks before; one wavefront
+// fetches A into a ring of three slots.  One barrier a chunk; two workgroups share a
+// compute unit and cover each other's waits.  (With B through the ring as well, one
+// chunk ahead, the chains waited for it: 110 us.)
 template <int DK, bool REV, typename Lds>
-__device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, int NVB, const SsmStates& st) {
+__device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, int NVB, int remap,
+                                              const SsmStates& st) {
   using S = SsmChainShape<DK>;
   constexpr int C = S::C, BV = S::BV, ND = S::ND;
-  const int H = b.H, DV = b.DV, bh = x / NVB, vb = x % NVB, h = bh % H, hk = h / (H / b.Hk);
+  int bh, vb;
+  ssm_block(x, NVB, remap, bh, vb);
+  const int H = b.H, DV = b.DV, h = bh % H, hk = h / (H / b.Hk);
   const int64_t seq = bh / H;
   const int nc = int((b.L + C - 1) / C), v0 = vb * BV;
   const int lane = threadIdx.x & 63, role = wave_id(), li = lane & 15, g = lane >> 4;
@@ -89,77 +92,90 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
   };
   const int64_t krow = REV ? b.q_row : b.k_row, vrow = REV ? b.do_row : b.v_row;
 
-  // Barriers: one before chunk 0's W, one before every chunk n (its K is in the
-  // ring and its W in the LDS; chunk n + 1's V and gates are there).
+  // A barrier before every chunk n: its A is in the ring and its W in the LDS.
   if (role == S::kDma) {
     using U = const uint16_t*;
     const U k = static_cast<U>(REV ? b.q : b.k) + hk * DK;
-    const U v = static_cast<U>(REV ? b.d_o : b.v) + int64_t(h) * DV + v0;
     typename S::TK tk;
-    typename S::TV tv;
     tk.init(krow, lane, 0);
-    tv.init(vrow, lane, 0);
     auto issue = [&](int m) {
-      const int64_t t = tok_of(m);
-      const U ks = (U)uniform_ptr(k + t * krow), vs = (U)uniform_ptr(v + t * vrow);
+      const U ks = (U)uniform_ptr(k + tok_of(m) * krow);
       const int valid = valid_of(m);
       const uint32_t addr = lds_addr_of(lds.ring + (m % 3) * S::SLOT);
-      const void* gs = uniform_ptr(st.gates[int64_t(bh) * nc + chunk_of(m)].lo);
-      dma16(gs, uint32_t(lane) * 16u, addr + 2 * S::GOFF);
       auto body = [&](auto ragged) {
-        constexpr bool R = decltype(ragged)::value;
 #pragma unroll
-        for (int j = 0; j < S::PV; ++j) tv.template issue<R>(j, addr + 2 * S::VOFF, vs, valid);
-#pragma unroll
-        for (int j = 0; j < S::PK; ++j) tk.template issue<R>(j, addr + 2 * S::KOFF, ks, valid);
+        for (int j = 0; j < S::PK; ++j) tk.template issue<decltype(ragged)::value>(j, addr, ks, valid);
       };
       if (valid == C) body(std::false_type{});
       else body(std::true_type{});
     };
-    auto wait_for = [&](bool more) {  // all but the K transfers issued last, where there are such
+    auto wait_for = [&](bool more) {  // all but the transfers issued last, where there are such
       if (more) wait_vmcnt<S::PK>();
       else wait_vmcnt<0>();
     };
-    if (nc > 0) issue(0);
-    wait_vmcnt<0>();
-    barrier_nowait();  // chunk 0
+    issue(0);
     if (nc > 1) issue(1);
     wait_for(nc > 1);
     for (int n = 0; n < nc; ++n) {
-      barrier_nowait();
+      barrier_nowait();  // chunk n is there
       if (n + 2 < nc) issue(n + 2);  // into chunk n - 1's slot
       wait_for(n + 2 < nc);
     }
   } else if (role >= S::kW) {
     const int c = role & 1, ku = (role >> 1) & 1;
-    auto weigh = [&](int n) {
-      const Frag<uint16_t> v = value_frag<BV>(lds.ring + (n % 3) * S::SLOT + S::VOFF, c, ku, lane);
-      const float* gw = reinterpret_cast<const float*>(lds.ring + (n % 3) * S::SLOT + S::GOFF) + (REV ? 128 : 192);  // e or w
+    // rows (tokens) 32 ku + lane / 4 and 16 further on, the columns 8 (lane % 4) + 4 c .. of the block
+    const auto* v = static_cast<const uint16_t*>(REV ? b.d_o : b.v) + int64_t(h) * DV + v0 + 8 * (lane & 3) + 4 * c;
+    uint16_t* const tile = lds.tile[role & 3];
+    struct Rows {
+      bf16x4 v[2];
+      f32x4 w[2];  // weights of tokens 32 ku + 16 e + 4 g ..
+      float all;
+    } at[3];
+    auto load = [&](Rows& x, int n) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) x.v[e] = bf16x4{};
+      if (n >= nc) return;
+      const int valid = valid_of(n);
+      const uint16_t* rows = v + tok_of(n) * vrow;
+      const ChunkGates& gt = st.gates[int64_t(bh) * nc + chunk_of(n)];
+      x.all = gt.e[63];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = 32 * ku + 16 * e + (lane >> 2);
+        if (t < valid) x.v[e] = *reinterpret_cast<const bf16x4*>(rows + t * vrow);
+        x.w[e] = *reinterpret_cast<const f32x4*>((REV ? gt.e : gt.w) + 32 * ku + 16 * e + 4 * g);
+      }
+    };
+    auto weigh = [&](Rows& x, int n) {  // into W of chunk n
+#pragma unroll
+      for (int e = 0; e < 2; ++e) *reinterpret_cast<bf16x4*>(tile + (16 * e + (lane >> 2)) * 16 + 4 * (lane & 3)) = x.v[e];
+      wait_lgkm0();
       f32x4 y[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const f32x4 w = *reinterpret_cast<const f32x4*>(gw + 32 * ku + 16 * e + 4 * g);
+        const bf16x4 t = lds_read_tr(tile + (16 * e + 4 * g + (li >> 2)) * 16 + 4 * (li & 3));
 #pragma unroll
-        for (int qq = 0; qq < 4; ++qq) y[e][qq] = w[qq] * static_cast<float>(v.v[4 * e + qq]);
+        for (int qq = 0; qq < 4; ++qq) y[e][qq] = x.w[e][qq] * static_cast<float>(t[qq]);
       }
       Frag<uint16_t> hi, lo;
       split_parts(y[0], y[1], hi, lo);
-      if (REV) {  // rows past the end repeat row 0, and e is not zero there
-        const int valid = n < nc ? valid_of(n) : C;
-        if (valid < C) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (32 * ku + 16 * (e / 4) + 4 * g + e % 4 >= valid) hi.v[e] = lo.v[e] = static_cast<__bf16>(0.0f);
-        }
-      }
       lds.bW[n & 1][0][c][ku][lane] = hi.v;
       lds.bW[n & 1][1][c][ku][lane] = lo.v;
+      if (role == S::kW && lane == 0) lds.all[n & 1] = x.all;
+      load(x, n + 3);
     };
-    sync();
-    weigh(0);
-    for (int n = 0; n < nc; ++n) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) load(at[i], i);
+    weigh(at[0], 0);
+    for (int n = 0; n < nc; n += 3) {
       sync();
-      weigh(n + 1);  // past the last chunk: stale values that nothing uses
+      weigh(at[1], n + 1);  // past the last chunk: zeros or stale values that nothing uses
+      if (n + 1 >= nc) break;
+      sync();
+      weigh(at[2], n + 2);
+      if (n + 2 >= nc) break;
+      sync();
+      weigh(at[0], n + 3);
     }
   } else {
     const int sw = role;
@@ -176,10 +192,9 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
       }
     uint16_t* hi_out = REV ? st.xh : st.sh;
     uint16_t* lo_out = REV ? st.xl : st.sl;
-    sync();
     for (int n = 0; n < nc; ++n) {
       sync();
-      const uint16_t* cur = lds.ring + (n % 3) * S::SLOT + S::KOFF;
+      const uint16_t* cur = lds.ring + (n % 3) * S::SLOT;
       Frag<uint16_t> KT[ND][2];
 #pragma unroll
       for (int d = 0; d < ND; ++d)
@@ -194,7 +209,7 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
         *reinterpret_cast<bf16x8*>(hi_out + at) = hi.v;
         *reinterpret_cast<bf16x8*>(lo_out + at) = lo.v;
       }
-      const float all = reinterpret_cast<const float*>(lds.ring + (n % 3) * S::SLOT + S::GOFF)[128 + 63];
+      const float all = lds.all[n & 1];
 #pragma unroll
       for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -222,18 +237,22 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
 }
 
 template <int DK>
-__global__ __launch_bounds__((SsmChainShape<DK>::THREADS), 5) void ssm_chain_kernel(SsmBwd b, int NVB, int half,
+__global__ __launch_bounds__((SsmChainShape<DK>::THREADS), 5) void ssm_chain_kernel(SsmBwd b, int NVB, int half, int remap,
                                                                                     SsmStates st) {
   using S = SsmChainShape<DK>;
   __shared__ __align__(1024) uint16_t ring[3 * S::SLOT];
   __shared__ __align__(16) bf16x8 bW[2][2][2][2][kWave];  // [buffer][part][column tile][k-unit]
+  __shared__ __align__(16) uint16_t tile[4][32 * 16];     // a W wave's rows on their way to its operands
+  __shared__ float all[2];                                // e^{G_C} of the chunk in bW
   struct Refs {
     uint16_t* ring;
     decltype(bW)& bW;
+    decltype(tile)& tile;
+    decltype(all)& all;
   };
-  Refs lds{ring, bW};
-  if (int(blockIdx.x) < half) ssm_chain_run<DK, true>(lds, b, blockIdx.x, NVB, st);
-  else ssm_chain_run<DK, false>(lds, b, blockIdx.x - half, NVB, st);
+  Refs lds{ring, bW, tile, all};
+  if (int(blockIdx.x) < half) ssm_chain_run<DK, true>(lds, b, blockIdx.x, NVB, remap, st);
+  else ssm_chain_run<DK, false>(lds, b, blockIdx.x - half, NVB, remap, st);
 }
 
 // ---------------------------------------------------------------------------

@@ -34,7 +34,8 @@ hipError_t bwd_impl(const SsmBwd& b, void* ws, hipStream_t s) {
   hipLaunchKernelGGL(ssm_gates_kernel, dim3(unsigned((slots + 3) / 4)), dim3(kThreads), 0, s, b, st.gates, NC, slots);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((ssm_chain_kernel<DK>), dim3(unsigned(2 * half)), dim3(SsmChainShape<DK>::THREADS), 0, s, b, NVB, half, st);
+  hipLaunchKernelGGL((ssm_chain_kernel<DK>), dim3(unsigned(2 * half)), dim3(SsmChainShape<DK>::THREADS), 0, s, b, NVB, half,
+                     ssm_remap(int64_t(b.B) * b.H, b.H / b.Hk), st);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 grid(unsigned(int64_t(b.B) * b.Hk * NC)), wg(SsmGradShape<DK, 64>::THREADS);

@@ -100,6 +100,23 @@ __device__ __forceinline__ void split_parts(const f32x4& lo4, const f32x4& hi4, 
   lo = p[1];
 }
 
+// (Sequence, head) and value block of workgroup x.  remap > 0: all value blocks of
+// `remap` adjacent heads on one XCD (same x % 8), whose L2 then serves what they
+// share; the (sequence, head)s are a multiple of 8 remap.
+__device__ __forceinline__ void ssm_block(int x, int NVB, int remap, int& bh, int& vb) {
+  if (remap > 0) {
+    const int slot = x >> 3, in = slot % (remap * NVB);
+    vb = in % NVB;
+    bh = ((slot / (remap * NVB)) * 8 + (x & 7)) * remap + in / NVB;
+  } else {
+    bh = x / NVB;
+    vb = x % NVB;
+  }
+}
+// Heads that share their queries and keys together where that comes out even, else
+// a head's own value blocks, else none.
+inline int ssm_remap(int64_t bh, int r) { return bh / r % 8 == 0 ? r : bh % 8 == 0 ? 1 : 0; }
+
 template <int DK>
 struct SsmShape {
   static_assert(DK == 64 || DK == 128, "shapes of the chunked scan");
@@ -138,14 +155,7 @@ __global__ __launch_bounds__((SsmShape<DK>::THREADS)) void ssm_chunk_kernel(SsmF
 
   const int H = a.H, DV = a.DV;
   int bh, vb;
-  if (remap > 0) {  // all value blocks of `remap` adjacent heads on one XCD (same blockIdx % 8)
-    const int slot = int(blockIdx.x) >> 3, in = slot % (remap * NVB);
-    vb = in % NVB;
-    bh = ((slot / (remap * NVB)) * 8 + (int(blockIdx.x) & 7)) * remap + in / NVB;
-  } else {
-    bh = int(blockIdx.x) / NVB;
-    vb = int(blockIdx.x) % NVB;
-  }
+  ssm_block(int(blockIdx.x), NVB, remap, bh, vb);
   int seq = bh / H;
   const int h = bh % H, hk = h / (H / a.Hk);
   if (a.cu != nullptr && a.order != nullptr) seq = seq_of_rank(a.order, seq, a.N);

@@ -13,9 +13,8 @@ static hipError_t chunk_impl(const SsmFwd& a, hipStream_t s) {
   const int NVB = a.DV / 32;
   const int64_t bh = int64_t(a.N) * a.H;
   const int r = a.H / a.Hk;
-  // heads that share their queries and keys on one XCD, whose L2 then serves them;
-  // packed sequences differ in length, so there only a head's own value blocks
-  const int remap = a.cu == nullptr && bh / r % 8 == 0 ? r : bh % 8 == 0 ? 1 : 0;
+  // packed sequences differ in length: there only a head's own value blocks go together
+  const int remap = ssm_remap(bh, a.cu == nullptr ? r : 1);
   hipLaunchKernelGGL((ssm_chunk_kernel<DK>), dim3(unsigned(bh * NVB)), dim3(SsmShape<DK>::THREADS), 0, s, a, NVB, remap);
   return hipGetLastError();
 }
