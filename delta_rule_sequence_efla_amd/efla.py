@@ -837,6 +837,26 @@ def _row(t, lead: int, name: str) -> int:
     """Elements from one token's row to the next of ``t`` [*tokens, ...], its
     first ``lead`` dimensions the tokens."""
     sh, st = t.shape, t.stride()
+    # the common forms first: a call for single tokens is bound by the host
+    if lead == 1:
+        if len(sh) == 3:
+            n, h, d = sh
+            if st[2] == 1 and (st[1] == d or h == 1):
+                if n == 1:
+                    return h * d
+                if n > 1 and st[0] >= h * d:
+                    return st[0]
+        elif st[1] == 1:
+            n, d = sh
+            if n == 1:
+                return d
+            if n > 1 and st[0] >= d:
+                return st[0]
+    return _any_row(t, lead, name)
+
+
+def _any_row(t, lead: int, name: str) -> int:
+    sh, st = t.shape, t.stride()
     if t.numel() == 0:
         return math.prod(sh[lead:])
     width = 1
@@ -867,23 +887,28 @@ def _offsets(cu_seqlens) -> int:
 
 def _conv_args(x, w, bias, lead: int, activation, *others):
     """(device index, D, W, silu) of a convolution's inputs, checked."""
-    if activation not in ("silu", None):
+    if activation != "silu" and activation is not None:
         raise ValueError(f"unknown activation {activation!r}; use 'silu' or None")
-    if x.dim() != lead + 1 or w.dim() != 2 or w.shape[0] != x.shape[-1] or w.dtype is not x.dtype:
+    xs, ws, ty = x.shape, w.shape, x.dtype
+    if len(xs) != lead + 1 or len(ws) != 2 or ws[0] != xs[lead] or w.dtype is not ty:
         dims = {1: "T", 2: "B,L"}[lead]
         raise ValueError(f"expected x [{dims},D] and w [D,W] of one type")
-    D, W = w.shape
-    _shaped(bias, (D,), "bias", x.dtype)
+    D, W = ws
+    if bias is not None and (bias.shape != (D,) or bias.dtype is not ty):
+        _want(bias, (D,), "bias", ty)
     index = x.get_device()
     _same(index, w, bias, *others)
-    _placed(index, x)
+    if index < 0:
+        _placed(index, x)
     return index, D, W, 1 if activation else 0
 
 
-def _out_rows(t, like, lead: int, name: str) -> int:
+def _out_rows(t, like, lead: int, name: str, index: int) -> int:
     """Row length of an output that is given, checked against ``like``."""
-    _shaped(t, like.shape, name, like.dtype)
-    _placed(like.get_device(), t)
+    if t.shape != like.shape or t.dtype is not like.dtype:
+        _want(t, like.shape, name, like.dtype)
+    if t.get_device() != index:
+        _placed(index, t)
     return _row(t, lead, name)
 
 
@@ -901,7 +926,7 @@ def efla_conv_fwd(x, w, bias=None, s0=None, activation="silu", y=None, s_final=N
     if s_final is None and want_final:
         s_final = x.new_empty((B, W - 1, D))
     _call(lib().efla_conv_fwd, index, "efla_conv_fwd", x.data_ptr(), _row(x, 2, "x"), w.data_ptr(), _at(bias), _at(s0),
-          y.data_ptr(), _out_rows(y, x, 2, "y"), _at(s_final), B, L, D, W, silu, _code(x.dtype))
+          y.data_ptr(), _out_rows(y, x, 2, "y", index), _at(s_final), B, L, D, W, silu, _code(x.dtype))
     return y, s_final
 
 
@@ -935,7 +960,7 @@ def efla_conv_fwd_varlen(x, w, cu_seqlens, bias=None, s0=None, slots=None, activ
     if s_final is None and want_final:
         s_final = x.new_empty((N, W - 1, D))
     _call(lib().efla_conv_fwd_varlen, index, "efla_conv_fwd_varlen", x.data_ptr(), _row(x, 1, "x"), w.data_ptr(), _at(bias),
-          cu_seqlens.data_ptr(), _at(slots), N, P, _at(s0), y.data_ptr(), _out_rows(y, x, 1, "y"), _at(s_final), T, D, W,
+          cu_seqlens.data_ptr(), _at(slots), N, P, _at(s0), y.data_ptr(), _out_rows(y, x, 1, "y", index), _at(s_final), T, D, W,
           silu, _code(x.dtype))
     return y, s_final
 
@@ -954,7 +979,7 @@ def efla_conv_step(x, w, state, bias=None, slots=None, activation="silu", y=None
     if y is None:
         y = x.new_empty(x.shape) if slots is None else x.new_zeros(x.shape)
     _call(lib().efla_conv_step, index, "efla_conv_step", x.data_ptr(), _row(x, 1, "x"), w.data_ptr(), _at(bias),
-          state.data_ptr(), _at(slots), y.data_ptr(), _out_rows(y, x, 1, "y"), N, P, D, W, silu, _code(x.dtype))
+          state.data_ptr(), _at(slots), y.data_ptr(), _out_rows(y, x, 1, "y", index), N, P, D, W, silu, _code(x.dtype))
     return y
 
 
@@ -981,7 +1006,7 @@ def efla_conv_bwd(x, w, dy, bias=None, s0=None, ds_final=None, activation="silu"
         n = _gated_workspace("efla_conv_bwd", B, L, D, W)
         workspace = x.new_empty(n, dtype=torch.uint8) if n else None
     _call(lib().efla_conv_bwd, index, "efla_conv_bwd", x.data_ptr(), _row(x, 2, "x"), w.data_ptr(), _at(bias), _at(s0),
-          dy.data_ptr(), _out_rows(dy, x, 2, "dy"), _at(ds_final), dx.data_ptr(), _out_rows(dx, x, 2, "dx"), dw.data_ptr(),
+          dy.data_ptr(), _out_rows(dy, x, 2, "dy", index), _at(ds_final), dx.data_ptr(), _out_rows(dx, x, 2, "dx", index), dw.data_ptr(),
           _at(db), _at(ds0), B, L, D, W, silu, _code(x.dtype), _at(workspace), _nbytes(workspace))
     return dx, dw, db, ds0
 
@@ -990,8 +1015,8 @@ def _ssm_args(q, k, v, dt, a, d, dt_bias, lead: int, *others):
     """(device index, H, Hk, dk, dv, the inputs' addresses and rows) of a scan's
     inputs, checked."""
     ty, ks, vs = q.dtype, k.shape, v.shape
-    if len(ks) != lead + 2 or len(vs) != lead + 2 or ks[:lead] != vs[:lead] or q.shape != ks or dt.shape != vs[:-1] \
-            or k.dtype is not ty or v.dtype is not ty or dt.dtype is not ty:
+    if len(ks) != lead + 2 or len(vs) != lead + 2 or q.shape != ks or ks[0] != vs[0] or ks[lead - 1] != vs[lead - 1] \
+            or dt.shape != vs[:-1] or k.dtype is not ty or v.dtype is not ty or dt.dtype is not ty:
         dims = {1: "N", 2: "B,L"}[lead]
         raise ValueError(f"expected q, k [{dims},Hk,dk], v [{dims},H,dv], dt [{dims},H] of one type")
     H, Hk = vs[lead], ks[lead]
@@ -999,13 +1024,17 @@ def _ssm_args(q, k, v, dt, a, d, dt_bias, lead: int, *others):
         raise ValueError(f"the {H} value heads must be a multiple of the {Hk} query and key heads")
     if a.shape != (H,) or a.dtype is not _f32:
         raise ValueError("a must be float32 [H]")
-    _shaped(d, (H,), "d", _f32)
-    _shaped(dt_bias, (H,), "dt_bias", _f32)
+    if d is not None and (d.shape != (H,) or d.dtype is not _f32):
+        _want(d, (H,), "d", _f32)
+    if dt_bias is not None and (dt_bias.shape != (H,) or dt_bias.dtype is not _f32):
+        _want(dt_bias, (H,), "dt_bias", _f32)
     index = q.get_device()
-    _placed(index, q, k, v, dt)
+    if index < 0 or k.get_device() != index or v.get_device() != index or dt.get_device() != index:
+        _placed(index, q, k, v, dt)
     _same(index, a, d, dt_bias, *others)
     ins = (q.data_ptr(), _row(q, lead, "q"), k.data_ptr(), _row(k, lead, "k"), v.data_ptr(), _row(v, lead, "v"),
-           dt.data_ptr(), _row(dt, lead, "dt"), a.data_ptr(), _at(d), _at(dt_bias))
+           dt.data_ptr(), _row(dt, lead, "dt"), a.data_ptr(), 0 if d is None else d.data_ptr(),
+           0 if dt_bias is None else dt_bias.data_ptr())
     return index, H, Hk, ks[-1], vs[-1], ins
 
 
@@ -1032,7 +1061,7 @@ def efla_ssm_fwd(q, k, v, dt, a, d=None, dt_bias=None, s0=None, o=None, s_final=
     if workspace is None:
         n = _gated_workspace("efla_ssm_fwd", B, H, Hk, L, dk, dv, code)
         workspace = q.new_empty(n, dtype=torch.uint8) if n else None
-    _call(lib().efla_ssm_fwd, index, "efla_ssm_fwd", *ins, _at(s0), o.data_ptr(), _out_rows(o, v, 2, "o"), _at(s_final), B,
+    _call(lib().efla_ssm_fwd, index, "efla_ssm_fwd", *ins, _at(s0), o.data_ptr(), _out_rows(o, v, 2, "o", index), _at(s_final), B,
           H, Hk, L, dk, dv, code, _at(workspace), _nbytes(workspace))
     return o, s_final
 
@@ -1063,7 +1092,7 @@ def efla_ssm_fwd_varlen(q, k, v, dt, a, cu_seqlens, d=None, dt_bias=None, s0=Non
         n = _gated_workspace("efla_ssm_fwd_varlen", N, H, Hk, T, dk, dv, code)
         workspace = q.new_empty(n, dtype=torch.uint8) if n else None
     _call(lib().efla_ssm_fwd_varlen, index, "efla_ssm_fwd_varlen", *ins, cu_seqlens.data_ptr(), _at(slots), _at(order), N, P,
-          _at(s0), o.data_ptr(), _out_rows(o, v, 1, "o"), _at(s_final), H, Hk, T, dk, dv, code, _at(workspace),
+          _at(s0), o.data_ptr(), _out_rows(o, v, 1, "o", index), _at(s_final), H, Hk, T, dk, dv, code, _at(workspace),
           _nbytes(workspace))
     return o, s_final
 
@@ -1083,7 +1112,7 @@ def efla_ssm_step(q, k, v, dt, a, state, d=None, dt_bias=None, slots=None, o=Non
     if o is None:
         o = v.new_empty(v.shape) if slots is None else v.new_zeros(v.shape)
     _call(lib().efla_ssm_step, index, "efla_ssm_step", *ins, state.data_ptr(), _at(slots), o.data_ptr(),
-          _out_rows(o, v, 1, "o"), N, P, H, Hk, dk, dv, _code(q.dtype))
+          _out_rows(o, v, 1, "o", index), N, P, H, Hk, dk, dv, _code(q.dtype))
     return o
 
 
@@ -1106,7 +1135,7 @@ def efla_ssm_bwd(q, k, v, dt, a, d_o, d=None, dt_bias=None, s0=None, ds_final=No
     for t, like, name in ((dq, q, "dq"), (dk, k, "dk"), (dv, v, "dv"), (ddt, dt, "ddt")):
         t = like.new_empty(like.shape) if t is None else t
         outs.append(t)
-        at += [t.data_ptr(), _out_rows(t, like, 2, name)]
+        at += [t.data_ptr(), _out_rows(t, like, 2, name, index)]
     da = a.new_empty((H,))
     dd, db = (None if t is None else a.new_empty((H,)) for t in (d, dt_bias))
     ds0 = a.new_empty((B, H, K, V)) if want_ds0 else None
@@ -1114,7 +1143,7 @@ def efla_ssm_bwd(q, k, v, dt, a, d_o, d=None, dt_bias=None, s0=None, ds_final=No
     if workspace is None:
         n = _gated_workspace("efla_ssm_bwd", B, H, Hk, L, K, V, code)
         workspace = q.new_empty(n, dtype=torch.uint8) if n else None
-    _call(lib().efla_ssm_bwd, index, "efla_ssm_bwd", *ins, _at(s0), d_o.data_ptr(), _out_rows(d_o, v, 2, "d_o"),
+    _call(lib().efla_ssm_bwd, index, "efla_ssm_bwd", *ins, _at(s0), d_o.data_ptr(), _out_rows(d_o, v, 2, "d_o", index),
           _at(ds_final), *at, da.data_ptr(), _at(dd), _at(db), _at(ds0), B, H, Hk, L, K, V, code, _at(workspace),
           _nbytes(workspace))
     return (*outs, da, dd, db, ds0)
