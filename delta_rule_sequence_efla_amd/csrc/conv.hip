@@ -102,7 +102,7 @@ __device__ __forceinline__ int conv_seq_of(const int32_t* __restrict__ cu, int N
   return __builtin_amdgcn_readfirstlane(lo);
 }
 
-constexpr int kConvGroup = 8;  // rows in flight
+constexpr int kConvGroup = 4;  // rows asked for at once
 
 // Forward.  The first W - 1 tokens of a sequence and its final state belong to
 // one wavefront a sequence and channel block (the launch's first workgroups),
@@ -199,10 +199,17 @@ __global__ __launch_bounds__(kThreads) void conv_fwd_kernel(ConvFwd a, int block
     const int64_t t = t0 - (W - 1) + i;
     conv_push<T, V, W>(win, row_of(t < 0 ? 0 : t));  // rows before a sequence's W - 1st feed no row that is stored
   }
+  ConvVec<T, V> next[kConvGroup];  // the next rows, asked for a group ahead
+  auto fetch = [&](int64_t t) {
+#pragma unroll
+    for (int i = 0; i < kConvGroup; ++i) next[i] = row_of(t + i < t1 ? t + i : t1 - 1);
+  };
+  fetch(t0);
   for (int64_t t = t0; t < t1; t += kConvGroup) {
     ConvVec<T, V> in[kConvGroup];
 #pragma unroll
-    for (int i = 0; i < kConvGroup; ++i) in[i] = row_of(t + i < t1 ? t + i : t1 - 1);
+    for (int i = 0; i < kConvGroup; ++i) in[i] = next[i];
+    if (t + kConvGroup < t1) fetch(t + kConvGroup);
 #pragma unroll
     for (int i = 0; i < kConvGroup; ++i) {
       const int64_t at = t + i;
@@ -275,15 +282,25 @@ __global__ __launch_bounds__(kThreads) void conv_bwd_kernel(ConvBwd a, int block
         in = *reinterpret_cast<const ConvVec<T, V>*>(static_cast<const T*>(a.s0) + srow + (t + W - 1) * a.D);
       conv_push<T, V, W>(win, in);
     }
-    constexpr int G = kConvGroup / 2;
+    constexpr int G = kConvGroup;
+    ConvVec<T, V> xn[G], yn[G];  // the next rows, asked for a group ahead
+    auto fetch = [&](int64_t t) {
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        const int64_t at = t + i < a.L ? t + i : a.L - 1;
+        xn[i] = *reinterpret_cast<const ConvVec<T, V>*>(x + at * a.x_row);
+        yn[i] = *reinterpret_cast<const ConvVec<T, V>*>(dy + at * a.dy_row);
+      }
+    };
+    fetch(t0);
     for (int64_t t = t0; t < t1 + W - 1; t += G) {
       ConvVec<T, V> xi[G], yi[G];
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        const int64_t at = t + i < a.L ? t + i : a.L - 1;
-        xi[i] = *reinterpret_cast<const ConvVec<T, V>*>(x + at * a.x_row);
-        yi[i] = *reinterpret_cast<const ConvVec<T, V>*>(dy + at * a.dy_row);
+        xi[i] = xn[i];
+        yi[i] = yn[i];
       }
+      if (t + G < t1 + W - 1) fetch(t + G);
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         const int64_t at = t + i;
@@ -412,11 +429,14 @@ static hipError_t conv_by_vector(bool aligned, F&& f) {
 
 static int64_t conv_blocks(int D, int V) { return (int64_t(D) + kWave * V - 1) / (kWave * V); }
 
-// Tokens a run: as long as there are 4096 wavefronts (sixteen a compute unit), up
-// to 64, where the W - 1 rows that a run reads before its own cost little.
-static int conv_run(int64_t seqs, int64_t L, int64_t blocks) {
+// Tokens a run: as long as there are `waves` wavefronts, up to 64, where the W - 1
+// rows that a run reads before its own cost little.  The gradient, whose registers
+// leave two wavefronts a SIMD, takes 2048 (8 x 2048 tokens of 2048 channels: runs of
+// 32 49 us, of 16 62 us), the forward pass 16384 (4 x 4096 tokens of 6144 channels: runs
+// of 8 75 us, of 16 81 us, of 32 86 us).
+static int conv_run(int64_t seqs, int64_t L, int64_t blocks, int64_t waves) {
   for (int run = 64; run > 8; run /= 2)
-    if (seqs * ((L + run - 1) / run) * blocks >= 4096) return run;
+    if (seqs * ((L + run - 1) / run) * blocks >= waves) return run;
   return 8;
 }
 
@@ -427,7 +447,7 @@ hipError_t launch_conv_fwd(const ConvFwd& a, hipStream_t s) {
     return conv_by_vector<T>(aligned, [&](auto vc) {
       constexpr int W = decltype(wc)::value, V = decltype(vc)::value;
       const int64_t blocks = conv_blocks(a.D, V), seqs = a.cu != nullptr ? 1 : a.N;
-      const int run = conv_run(seqs, a.L, blocks);
+      const int run = conv_run(seqs, a.L, blocks, 16384);
       const int64_t seq_wgs = (a.N * blocks + 3) / 4;
       const int64_t wgs = seq_wgs + (a.y == nullptr || a.L == 0 ? 0 : seqs * ((a.L + 4 * run - 1) / (4 * run)) * blocks);
       if (wgs == 0) return hipSuccess;
@@ -455,9 +475,9 @@ hipError_t launch_conv_step(const ConvStep& a, hipStream_t s) {
 template hipError_t launch_conv_step<float>(const ConvStep&, hipStream_t);
 template hipError_t launch_conv_step<uint16_t>(const ConvStep&, hipStream_t);
 
-// Runs of the gradient by the scalar path's block count, so that the workspace
-// does not depend on how the tensors are aligned.
-static int conv_bwd_run(int B, int64_t L, int D) { return conv_run(B, L, conv_blocks(D, 8)); }
+// Runs of the gradient, by one block count whatever the alignment, so that the
+// workspace does not depend on it.
+static int conv_bwd_run(int B, int64_t L, int D) { return conv_run(B, L, conv_blocks(D, 8), 2048); }
 size_t conv_bwd_workspace(int B, int64_t L, int D, int W) {
   const int run = conv_bwd_run(B, L, D);
   return size_t(B) * size_t((L + 4 * run - 1) / (4 * run)) * size_t(W + 1) * size_t(D) * sizeof(float);
@@ -465,7 +485,7 @@ size_t conv_bwd_workspace(int B, int64_t L, int D, int W) {
 // Threads of the largest launch over these sizes (one element a lane).
 int64_t conv_threads(int64_t seqs, int64_t L, int64_t N, int D) {
   const int64_t blocks = conv_blocks(D, 1);
-  const int run = conv_run(seqs, L, conv_blocks(D, 8));
+  const int run = conv_run(seqs, L, conv_blocks(D, 8), 16384);  // the shortest any of them takes
   return ((N * blocks + 3) / 4 + seqs * ((L + 4 * run - 1) / (4 * run)) * blocks) * kThreads;
 }
 
