@@ -35,4 +35,22 @@ __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log
 // difference is exact to float32, and so is the decay.
 __device__ __forceinline__ float decay_between(double hi, double lo) { return expf(float(hi - lo)); }
 
+// Sequence handled in rank r of a packed batch: by the caller's order, or, for up
+// to 64 sequences without one, the r-th longest by chunks of C tokens (ties by
+// index), found by every wavefront for itself; larger batches go by index.
+// Workgroups start in index order, so the longest chains start first.
+template <int C>
+__device__ __forceinline__ int ranked_seq(const int32_t* __restrict__ cu, const int32_t* __restrict__ order, int r, int N,
+                                          int64_t T) {
+  if (order != nullptr) return seq_of_rank(order, r, N);
+  if (N > kWave) return r;
+  const int lane = threadIdx.x & 63, mine = lane < N ? seq_chunks<C>(cu, lane, T) : -1;
+  int rank = 0;
+  for (int u = 0; u < N; ++u) {
+    const int n = __builtin_amdgcn_readlane(mine, u);
+    rank += n > mine || (n == mine && u < lane) ? 1 : 0;
+  }
+  return __builtin_amdgcn_readfirstlane(__builtin_ctzll(__ballot(lane < N && rank == r)));
+}
+
 }  // namespace efla

@@ -158,7 +158,7 @@ __global__ __launch_bounds__((SsmShape<DK>::THREADS)) void ssm_chunk_kernel(SsmF
   ssm_block(int(blockIdx.x), NVB, remap, bh, vb);
   int seq = bh / H;
   const int h = bh % H, hk = h / (H / a.Hk);
-  if (a.cu != nullptr && a.order != nullptr) seq = seq_of_rank(a.order, seq, a.N);
+  if (a.cu != nullptr) seq = ranked_seq<C>(a.cu, a.order, seq, a.N, a.L);
   const SeqSpan sp = seq_span<C>(a.cu, seq, h, H, a.L, int((a.L + C - 1) / C));
   const int64_t srow = state_row(a.slots, seq, a.P);
   const int nc = sp.nc, v0 = vb * BV;

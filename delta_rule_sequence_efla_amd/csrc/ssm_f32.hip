@@ -91,7 +91,7 @@ __global__ __launch_bounds__(kThreads) void ssm_f32_kernel(SsmFwd a, float* __re
   int seq = int(unit / uint32_t(H));
   int64_t bos = int64_t(seq) * a.L, len = a.L;
   if (a.cu != nullptr) {
-    if (a.order != nullptr) seq = seq_of_rank(a.order, seq, a.N);
+    seq = ranked_seq<kC>(a.cu, a.order, seq, a.N, a.L);
     bos = clamp_offset(a.cu[seq], 0, a.L);
     len = clamp_offset(a.cu[seq + 1], bos, a.L) - bos;
   }

@@ -852,6 +852,12 @@ def _row(t, lead: int, name: str) -> int:
                 return d
             if n > 1 and st[0] >= d:
                 return st[0]
+    elif len(sh) == 4:
+        b, n, h, d = sh
+        if b > 0 and n > 1 and st[3] == 1 and (st[2] == d or h == 1) and st[1] >= h * d and (b == 1 or st[0] == n * st[1]):
+            return st[1]
+    elif sh[0] > 0 and sh[1] > 1 and st[2] == 1 and st[1] >= sh[2] and (sh[0] == 1 or st[0] == sh[1] * st[1]):
+        return st[1]
     return _any_row(t, lead, name)
 
 
