@@ -31,9 +31,52 @@ namespace efla {
 
 __device__ __forceinline__ float softplus(float x) { return fmaxf(x, 0.0f) + log1pf(expf(-fabsf(x))); }
 
-// e^x for differences of the log-decay's sums, which are held in 64 bits: their
-// difference is exact to float32, and so is the decay.
-__device__ __forceinline__ float decay_between(double hi, double lo) { return expf(float(hi - lo)); }
+// Inclusive sums over the lanes in 64 bits, by DPP (wave_scan_dpp for doubles).
+__device__ __forceinline__ double wave_scan_dpp64(double s) {
+  auto add = [&](auto ctrl, auto rows) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, s);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(u >> 32)), decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+    s += __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
+  };
+  add(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});
+  add(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});
+  add(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});
+  add(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});
+  add(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
+  add(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
+  return s;
+}
+
+// The gates of a chunk of C tokens, in log2 units: G as the sum of two floats (what
+// is needed of it are differences, and e^{G_i - G_j} is then good to float32 however
+// far G has fallen), D, e^{G}, w.
+template <int C>
+struct GatesOf {
+  float hi[C], lo[C], D[C], e[C], w[C];
+  // e^{G_i - G_j}, by token i's own hi and lo
+  __device__ __forceinline__ float between(float hi_i, float lo_i, int j) const {
+    return __builtin_amdgcn_exp2f((hi_i - hi[j]) + (lo_i - lo[j]));
+  }
+};
+using ChunkGates = GatesOf<64>;
+
+// By one wavefront, a lane a token; raw: dt + bias.
+template <int C>
+__device__ __forceinline__ void put_chunk_gates(GatesOf<C>& gt, float raw, float rate, bool real, int lane) {
+  constexpr double kLog2E = 1.4426950408889634;
+  const float D = real ? softplus(raw) : 0.0f;
+  const double G = wave_scan_dpp64(real ? double(gate_floor(rate * D)) * kLog2E : 0.0);
+  const uint64_t u = __builtin_bit_cast(uint64_t, G);
+  const uint32_t el = __builtin_amdgcn_readlane(int(uint32_t(u)), 63), eh = __builtin_amdgcn_readlane(int(uint32_t(u >> 32)), 63);
+  const double end = __builtin_bit_cast(double, (uint64_t(eh) << 32) | el);
+  if (lane >= C) return;
+  gt.hi[lane] = float(G);
+  gt.lo[lane] = float(G - double(float(G)));
+  gt.D[lane] = D;
+  gt.e[lane] = __builtin_amdgcn_exp2f(float(G));
+  gt.w[lane] = __builtin_amdgcn_exp2f(float(end - G)) * D;
+}
 
 // Sequence handled in rank r of a packed batch: by the caller's order, or, for up
 // to 64 sequences without one, the r-th longest by chunks of C tokens (ties by

@@ -33,45 +33,6 @@
 
 namespace efla {
 
-// Inclusive sums over the lanes in 64 bits, by DPP (wave_scan_dpp for doubles).
-__device__ __forceinline__ double wave_scan_dpp64(double s) {
-  auto add = [&](auto ctrl, auto rows) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, s);
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(u)), decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(u >> 32)), decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
-    s += __builtin_bit_cast(double, (uint64_t(hi) << 32) | lo);
-  };
-  add(std::integral_constant<int, 0x111>{}, std::integral_constant<int, 0xF>{});
-  add(std::integral_constant<int, 0x112>{}, std::integral_constant<int, 0xF>{});
-  add(std::integral_constant<int, 0x114>{}, std::integral_constant<int, 0xF>{});
-  add(std::integral_constant<int, 0x118>{}, std::integral_constant<int, 0xF>{});
-  add(std::integral_constant<int, 0x142>{}, std::integral_constant<int, 0xA>{});
-  add(std::integral_constant<int, 0x143>{}, std::integral_constant<int, 0xC>{});
-  return s;
-}
-
-// A chunk's gates in the LDS, in log2 units: G as the sum of two floats (what is
-// needed of it are differences, and e^{G_i - G_j} is then good to float32 however
-// far G has fallen), D, e^{G}, w.
-struct ChunkGates {
-  float hi[64], lo[64], D[64], e[64], w[64];
-};
-
-// By one wavefront, a lane a token; raw: dt + bias.
-__device__ __forceinline__ void put_chunk_gates(ChunkGates& gt, float raw, float rate, bool real, int lane) {
-  constexpr double kLog2E = 1.4426950408889634;
-  const float D = real ? softplus(raw) : 0.0f;
-  const double G = wave_scan_dpp64(real ? double(gate_floor(rate * D)) * kLog2E : 0.0);
-  const uint64_t u = __builtin_bit_cast(uint64_t, G);
-  const uint32_t el = __builtin_amdgcn_readlane(int(uint32_t(u)), 63), eh = __builtin_amdgcn_readlane(int(uint32_t(u >> 32)), 63);
-  const double end = __builtin_bit_cast(double, (uint64_t(eh) << 32) | el);
-  gt.hi[lane] = float(G);
-  gt.lo[lane] = float(G - double(float(G)));
-  gt.D[lane] = D;
-  gt.e[lane] = __builtin_amdgcn_exp2f(float(G));
-  gt.w[lane] = __builtin_amdgcn_exp2f(float(end - G)) * D;
-}
-
 // Eight values (k-unit halves lo4, hi4) as a sum of three bf16 fragments.
 __device__ __forceinline__ void split3_frag(const f32x4& lo4, const f32x4& hi4, Frag<uint16_t> (&p)[3]) {
   typedef float f32x2 __attribute__((ext_vector_type(2)));

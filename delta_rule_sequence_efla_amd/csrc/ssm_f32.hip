@@ -14,13 +14,14 @@ namespace {
 
 constexpr int kC = 32, kBV = 16;  // tokens a chunk, value columns a workgroup of a chain
 constexpr int kFwd = 0, kStates = 1, kReverse = 2;
+constexpr int kChain = 2 * kThreads;  // threads of a workgroup of a chain
 
 // ROWS x COLS values of T (row t at src + t * stride) on their way to the LDS:
 // fetched into registers, widened and stored with a pitch; rows at or past
 // `valid` are zero, and so are columns COLS .. PITCH's multiple of 32.
-template <typename T, int COLS>
+template <typename T, int COLS, int THREADS = kThreads>
 struct Tile {
-  static constexpr int VE = 16 / sizeof(T), VPR = COLS / VE, N = kC * VPR, PER = cdiv(N, kThreads);
+  static constexpr int VE = 16 / sizeof(T), VPR = COLS / VE, N = kC * VPR, PER = cdiv(N, THREADS);
   struct alignas(16) Vec {
     T e[VE];
   };
@@ -28,7 +29,7 @@ struct Tile {
   __device__ __forceinline__ void fetch(const T* __restrict__ src, int64_t stride, int valid, int tid) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int at = tid + i * kThreads, r = at / VPR, c = at % VPR;
+      const int at = tid + i * THREADS, r = at / VPR, c = at % VPR;
 #pragma unroll
       for (int e = 0; e < VE; ++e) x[i].e[e] = T(0);
       if (at < N && r < valid) x[i] = *reinterpret_cast<const Vec*>(src + r * stride + c * VE);
@@ -37,7 +38,7 @@ struct Tile {
   __device__ __forceinline__ void put(float* dst, int pitch, int tid) const {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int at = tid + i * kThreads, r = at / VPR, c = at % VPR;
+      const int at = tid + i * THREADS, r = at / VPR, c = at % VPR;
       if (at < N) {
 #pragma unroll
         for (int e = 0; e < VE; e += 4)
@@ -48,42 +49,33 @@ struct Tile {
   }
 };
 
-// A chunk's gates by one wavefront (lanes 0 .. 31; tokens at or past `valid` are
-// without a step): G in 64 bits and D.
-struct Gates {
-  double G[kC];
-  float D[kC];
-  float raw[kC];
-};
-template <typename T>
-__device__ __forceinline__ void chunk_gates(Gates& gt, float raw, float rate, int valid, int lane) {
-  const float delta = lane < valid ? softplus(raw) : 0.0f;
-  const double G = wave_scan_gate(lane < valid ? gate_floor(rate * delta) : 0.0f, lane);
-  if (lane < kC) {
-    gt.G[lane] = G;
-    gt.D[lane] = delta;
-    gt.raw[lane] = raw;
-  }
-}
+using Gates = GatesOf<kC>;
 
 // ---------------------------------------------------------------------------
 // One workgroup carries 16 value columns of one sequence and head through its
-// chunks.  The state tiles S[16 dt ..][16 columns] stay in the accumulators of
-// wavefront dt % 4 and pass the LDS once a chunk for the readout.
+// chunks.
 //   kFwd:     o and the final state
 //   kStates:  the state before every chunk, [slot][d_k][d_v]
 //   kReverse: the chunks from last to first, X <- e^{G_C} X + Q^T diag(e^G) dO,
 //             and X after every chunk (k = q, v = dO here)
+// A chunk takes two barriers.  Behind the first, side by side: three wavefronts the
+// tiles of P, two S^T Q^T for half of the tokens each, two (the chains: four) the
+// state's tiles, which stay in their accumulators, one the gates of the next chunk.
+// Behind the second: O = diag(e^G) S^T Q^T + V^T P^T and its store, the new state
+// into the LDS for the next readout, and the next chunk's tokens into the other
+// buffer.  Bound by that chain: 777 tokens, d 64, 25 chunks, F32US; one after the other
+// with three barriers and the gates in line, on four wavefronts, 77 us.
 template <typename T, int DK, int MODE>
-__global__ __launch_bounds__(kThreads) void ssm_f32_kernel(SsmFwd a, float* __restrict__ states, int NC) {
+__global__ __launch_bounds__(kChain) void ssm_f32_kernel(SsmFwd a, float* __restrict__ states, int NC) {
+  constexpr bool FWD = MODE == kFwd;
   constexpr int DKP = DK < 32 ? 32 : DK, KP = DKP + 4, VP = kBV + 4, PP = kC + 4;
-  constexpr int KU = DKP / 32, DT = DK / 16, OWN = cdiv(DT, 4);
-  __shared__ __align__(16) float Qs[MODE == kFwd ? kC : 1][KP];
-  __shared__ __align__(16) float Ks[kC][KP];
-  __shared__ __align__(16) float Vs[kC][VP];
+  constexpr int KU = DKP / 32, DT = DK / 16, SW = FWD ? 2 : 4, OWN = cdiv(DT, SW);  // S waves: the last SW
+  __shared__ __align__(16) float Qs[FWD ? 2 : 1][FWD ? kC : 1][KP];
+  __shared__ __align__(16) float Ks[2][kC][KP];
+  __shared__ __align__(16) float Vs[2][kC][VP];
   __shared__ __align__(16) float Ps[kC][PP];
   __shared__ __align__(16) float St[kBV][KP];  // S^T, for the readout
-  __shared__ Gates gt;
+  __shared__ Gates gates[2];
 
   const int NVB = a.DV / kBV, H = a.H;
   const uint32_t wg = blockIdx.x, unit = wg / uint32_t(NVB);
@@ -102,8 +94,9 @@ __global__ __launch_bounds__(kThreads) void ssm_f32_kernel(SsmFwd a, float* __re
   const T* v = static_cast<const T*>(a.v) + bos * a.v_row + int64_t(h) * a.DV + v0;
   const T* dt = static_cast<const T*>(a.dt) + bos * a.dt_row + h;
   T* o = static_cast<T*>(a.o) + bos * a.o_row + int64_t(h) * a.DV + v0;
-  const float rate = a.a[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f;
+  const float rate = a.a[h], bias = a.bias != nullptr ? a.bias[h] : 0.0f, skip = a.d != nullptr ? a.d[h] : 0.0f;
   const int tid = threadIdx.x, lane = tid & 63, w = wave_id(), li = lane & 15, g = lane >> 4;
+  const int sw = w - (8 - SW);  // >= 0: an S wave, tiles sw, sw + SW, ..
 
   f32x4 S[OWN];
   const float* s0 = a.s0 == nullptr || row < 0 ? nullptr : a.s0 + (row * H + h) * DK * a.DV + v0 + li;
@@ -111,104 +104,127 @@ __global__ __launch_bounds__(kThreads) void ssm_f32_kernel(SsmFwd a, float* __re
   for (int i = 0; i < OWN; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int r = 16 * (w + 4 * i) + 4 * g + e;
-      S[i][e] = s0 != nullptr && r < DK ? s0[int64_t(r) * a.DV] : 0.0f;
+      const int r = 16 * (sw + SW * i) + 4 * g + e;
+      S[i][e] = sw >= 0 && s0 != nullptr && r < DK ? s0[int64_t(r) * a.DV] : 0.0f;
     }
   auto store = [&](float* dst) {
 #pragma unroll
     for (int i = 0; i < OWN; ++i)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int r = 16 * (w + 4 * i) + 4 * g + e;
+        const int r = 16 * (sw + SW * i) + 4 * g + e;
         if (r < DK) dst[int64_t(r) * a.DV + v0 + li] = S[i][e];
       }
   };
+  auto publish = [&]() {
+#pragma unroll
+    for (int i = 0; i < OWN; ++i)
+      if (sw + SW * i < DT) st4(&St[li][16 * (sw + SW * i) + 4 * g], S[i]);
+  };
 
   const int chunks = int((len + kC - 1) / kC);
-  for (int at = tid; at < kC * KP; at += kThreads) {  // columns past d_k
-    Ks[at / KP][at % KP] = 0.0f;
-    if (MODE == kFwd) Qs[at / KP][at % KP] = 0.0f;
+  for (int at = tid; at < kC * KP; at += kChain) {  // columns past d_k
+    Ks[0][at / KP][at % KP] = Ks[1][at / KP][at % KP] = 0.0f;
+    if constexpr (FWD) Qs[0][at / KP][at % KP] = Qs[1][at / KP][at % KP] = 0.0f;
     if (at < kBV * KP) St[at / KP][at % KP] = 0.0f;
     if (at < kC * PP) Ps[at / PP][at % PP] = 0.0f;  // above the diagonal
   }
-  Tile<T, DK> tk, tq;
-  Tile<T, kBV> tv;
+  Tile<T, DK, kChain> tk, tq;
+  Tile<T, kBV, kChain> tv;
   float raw = 0.0f;
   auto chunk_at = [&](int n) { return MODE == kReverse ? chunks - 1 - n : n; };
+  auto valid_of = [&](int n) {
+    const int64_t t = int64_t(chunk_at(n)) * kC;
+    return int(len - t < kC ? len - t : kC);
+  };
   auto fetch = [&](int n) {
     const int64_t t = int64_t(chunk_at(n)) * kC;
-    const int valid = int(len - t < kC ? len - t : kC);
+    const int valid = valid_of(n);
     tk.fetch(k + t * a.k_row, a.k_row, valid, tid);
-    if (MODE == kFwd) tq.fetch(q + t * a.q_row, a.q_row, valid, tid);
+    if constexpr (FWD) tq.fetch(q + t * a.q_row, a.q_row, valid, tid);
     tv.fetch(v + t * a.v_row, a.v_row, valid, tid);
-    if (w == 3) raw = lane < valid ? to_f32(dt[(t + lane) * a.dt_row]) + bias : 0.0f;
   };
-  if (chunks > 0) fetch(0);
+  auto stage = [&](int b) {
+    tk.put(Ks[b][0], KP, tid);
+    if constexpr (FWD) tq.put(Qs[b][0], KP, tid);
+    tv.put(Vs[b][0], VP, tid);
+  };
+  auto fetch_dt = [&](int n) {
+    raw = n < chunks && lane < valid_of(n) ? to_f32(dt[(int64_t(chunk_at(n)) * kC + lane) * a.dt_row]) + bias : 0.0f;
+  };
+  if (chunks > 0) {
+    fetch(0);
+    __syncthreads();  // the zeros
+    stage(0);
+    if (chunks > 1) fetch(1);
+    if (w == 3) {
+      fetch_dt(0);
+      put_chunk_gates(gates[0], raw, rate, lane < valid_of(0), lane);
+      fetch_dt(1);
+    }
+    if (FWD && sw >= 0) publish();
+    __syncthreads();
+  }
   for (int n = 0; n < chunks; ++n) {
-    const int c = chunk_at(n);
-    const int64_t t = int64_t(c) * kC;
-    const int valid = int(len - t < kC ? len - t : kC);
-    __syncthreads();  // the chunk before is done with the LDS
-    tk.put(Ks[0], KP, tid);
-    if (MODE == kFwd) tq.put(Qs[0], KP, tid);
-    tv.put(Vs[0], VP, tid);
-    if (w == 3) chunk_gates<T>(gt, raw, rate, valid, lane);
-    if (MODE == kFwd) {
+    const int b = n & 1;
+    const int64_t t = int64_t(chunk_at(n)) * kC;
+    const int valid = valid_of(n);
+    const Gates& gt = gates[b];
+    f32x4 x = zero4();  // of the Z waves: diag(e^G) S^T Q^T, 16 tokens
+    if (FWD && w < 3) {  // P, lower triangle: tiles (0, 0), (1, 0), (1, 1)
+      const int it = (w + 1) / 2, jt = w / 2, i = 16 * it + li;
+      f32x4 p = zero4();
+#pragma unroll
+      for (int ku = 0; ku < KU; ++ku)
+        mma(p, lds_frag(Ks[b][0], KP, 16 * jt + li, ku, g), lds_frag(Qs[b][0], KP, i, ku, g));
+      const float hi = gt.hi[i], lo = gt.lo[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = 16 * jt + 4 * g + e;
+        p[e] = i >= j ? p[e] * (gt.between(hi, lo, j) * gt.D[j]) : 0.0f;
+      }
+      st4(&Ps[i][16 * jt + 4 * g], p);
+    } else if (w == 3) {
+      put_chunk_gates(gates[b ^ 1], raw, rate, n + 1 < chunks && lane < valid_of(n + 1), lane);
+      fetch_dt(n + 2);
+    } else if (FWD && sw < 0) {  // wavefronts 4 and 5
+      const int i = 16 * (w - 4) + li;
+#pragma unroll
+      for (int ku = 0; ku < KU; ++ku) mma(x, lds_frag(St[0], KP, li, ku, g), lds_frag(Qs[b][0], KP, i, ku, g));
+      x = gt.e[i] * x;
+    } else if (sw >= 0) {  // S <- e^{G_C} S + K^T diag(w) V
+      if constexpr (!FWD) store(states + (int64_t(unit) * NC + chunk_at(n)) * DK * a.DV);
+      Frag<float> wv = lds_frag_t(Vs[b][0], VP, li, 0, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wv.v[e] *= (MODE == kReverse ? gt.e : gt.w)[16 * (e / 4) + 4 * g + e % 4];
+      const float all = gt.e[kC - 1];
 #pragma unroll
       for (int i = 0; i < OWN; ++i)
-        if (w + 4 * i < DT) st4(&St[li][16 * (w + 4 * i) + 4 * g], S[i]);
-    } else {
-      store(states + (int64_t(unit) * NC + c) * DK * a.DV);
+        if (sw + SW * i < DT) {
+          S[i] = all * S[i];
+          mma(S[i], lds_frag_t(Ks[b][0], KP, 16 * (sw + SW * i) + li, 0, g), wv);
+        }
     }
     __syncthreads();
-    if (n + 1 < chunks) fetch(n + 1);
-    if constexpr (MODE == kFwd) {
-      if (w < 3) {  // P, lower triangle: tiles (0, 0), (1, 0), (1, 1)
-        const int it = (w + 1) / 2, jt = w / 2, i = 16 * it + li;
-        f32x4 p = zero4();
-#pragma unroll
-        for (int ku = 0; ku < KU; ++ku)
-          mma(p, lds_frag(Ks[0], KP, 16 * jt + li, ku, g), lds_frag(Qs[0], KP, i, ku, g));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = 16 * jt + 4 * g + e;
-          p[e] = i >= j ? p[e] * (decay_between(gt.G[i], gt.G[j]) * gt.D[j]) : 0.0f;
-        }
-        st4(&Ps[i][16 * jt + 4 * g], p);
-      }
-      __syncthreads();
-      if (w < 2) {  // O^T = S^T Q^T diag(e^G) + V^T P^T + d V^T, 16 tokens a wavefront
-        const int i = 16 * w + li;
-        f32x4 x = zero4();
-#pragma unroll
-        for (int ku = 0; ku < KU; ++ku) mma(x, lds_frag(St[0], KP, li, ku, g), lds_frag(Qs[0], KP, i, ku, g));
-        x = expf(float(gt.G[i])) * x;
-        mma(x, lds_frag_t(Vs[0], VP, li, 0, g), lds_frag(Ps[0], PP, i, 0, g));
+    if (n + 1 < chunks) {
+      stage(b ^ 1);
+      if (n + 2 < chunks) fetch(n + 2);
+    }
+    if constexpr (FWD) {
+      if (w == 4 || w == 5) {
+        const int i = 16 * (w - 4) + li;
+        mma(x, lds_frag_t(Vs[b][0], VP, li, 0, g), lds_frag(Ps[0], PP, i, 0, g));
         if (a.d != nullptr) {
-          const float skip = a.d[h];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = fmaf(skip, Vs[i][4 * g + e], x[e]);
+          for (int e = 0; e < 4; ++e) x[e] = fmaf(skip, Vs[b][i][4 * g + e], x[e]);
         }
         if (i < valid) st4(o + (t + i) * a.o_row + 4 * g, x);
       }
+      if (sw >= 0) publish();
     }
-    // S <- e^{G_C} S + K^T diag(w) V
-    const double end = gt.G[kC - 1];
-    Frag<float> wv = lds_frag_t(Vs[0], VP, li, 0, g);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int j = 16 * (e / 4) + 4 * g + e % 4;
-      wv.v[e] *= MODE == kReverse ? expf(float(gt.G[j])) : decay_between(end, gt.G[j]) * gt.D[j];
-    }
-    const float all = expf(float(end));
-#pragma unroll
-    for (int i = 0; i < OWN; ++i)
-      if (w + 4 * i < DT) {
-        S[i] = all * S[i];
-        mma(S[i], lds_frag_t(Ks[0], KP, 16 * (w + 4 * i) + li, 0, g), wv);
-      }
+    __syncthreads();
   }
-  if (a.sfin != nullptr && row >= 0) store(a.sfin + (row * H + h) * DK * a.DV);
+  if (a.sfin != nullptr && row >= 0 && sw >= 0) store(a.sfin + (row * H + h) * DK * a.DV);
 }
 
 // ---------------------------------------------------------------------------
@@ -295,10 +311,10 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
       red[1][w] = dot;
     }
     if (w == 3)
-      chunk_gates<T>(gt, lane < valid ? to_f32(static_cast<const T*>(b.dt)[(tok + lane) * b.dt_row + h]) +
-                                            (b.bias != nullptr ? b.bias[h] : 0.0f)
-                                      : 0.0f,
-                     rate, valid, lane);
+      put_chunk_gates(gt, lane < valid ? to_f32(static_cast<const T*>(b.dt)[(tok + lane) * b.dt_row + h]) +
+                                             (b.bias != nullptr ? b.bias[h] : 0.0f)
+                                       : 0.0f,
+                      rate, lane < valid, lane);
     __syncthreads();
     if (w < 3) {
       f32x4 p = zero4();
@@ -310,7 +326,7 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * it + 4 * g + e;
-        const float f = i >= j ? decay_between(gt.G[i], gt.G[j]) : 0.0f;
+        const float f = i >= j ? gt.between(gt.hi[i], gt.lo[i], j) : 0.0f;
         p[e] = i >= j ? p[e] * f : 0.0f;
         Pm[i][j] = i >= j ? raw[e] * f : 0.0f;
         Dm[i][j] = p[e];
@@ -323,7 +339,7 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
       if (g == 0) colM[w][li] = col;
     }
     __syncthreads();
-    const double end = gt.G[kC - 1];
+    const float end_hi = gt.hi[kC - 1], end_lo = gt.lo[kC - 1];
     auto del = [&](int ku, Frag<float>& f) {  // times D of the k index
 #pragma unroll
       for (int e = 0; e < 8; ++e) f.v[e] *= gt.D[32 * ku + 16 * (e / 4) + 4 * g + e % 4];
@@ -360,8 +376,8 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int tk = 16 * half + 4 * g + e, c = 16 * dt + li;
-          x[e] *= expf(float(gt.G[tk]));
-          y[e] *= decay_between(end, gt.G[tk]);
+          x[e] *= gt.e[tk];
+          y[e] *= gt.between(end_hi, end_lo, tk);
           rsum[half][e] += x[e] * Qs[tk][c];
           psum[half][e] += y[e] * Ks[tk][c];
         }
@@ -394,7 +410,7 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
         for (int ku = 0; ku < KU; ++ku)
           mma(x, lds_frag(Ks[0], KP, 16 * half + li, ku, g), state_cols(X, 16 * vt + li, ku));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] *= decay_between(end, gt.G[16 * half + 4 * g + e]);
+        for (int e = 0; e < 4; ++e) x[e] *= gt.between(end_hi, end_lo, 16 * half + 4 * g + e);
         mma(x, lds_frag_t(Pm[0], PP, 16 * half + li, 0, g), lds_frag_t(Os[0], VP, 16 * vt + li, 0, g));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -420,10 +436,12 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
         if (lane + d < kC) suf += y;
         if (lane >= d) pre += z;
       }
-      const float xs = expf(float(end)) * (red[1][0] + red[1][1] + red[1][2] + red[1][3]);
+      const float xs = gt.e[kC - 1] * (red[1][0] + red[1][1] + red[1][2] + red[1][3]);
       const float gd = suf + (pre - D * pp) + xs;
       const float dD = ci + pp + rate * gd;
-      const float ddt = dD * (1.0f / (1.0f + expf(-gt.raw[l])));
+      float raw_dt = b.bias != nullptr ? b.bias[h] : 0.0f;
+      if (real) raw_dt += to_f32(static_cast<const T*>(b.dt)[(tok + lane) * b.dt_row + h]);
+      const float ddt = dD * (1.0f / (1.0f + expf(-raw_dt)));
       if (real) static_cast<T*>(b.ddt)[(tok + lane) * b.ddt_row + h] = from_f32<T>(ddt);
       float sa = real ? D * gd : 0.0f, sb = real ? ddt : 0.0f;
 #pragma unroll
@@ -489,7 +507,7 @@ template <typename T, int MODE>
 hipError_t launch_chain(const SsmFwd& a, float* states, int NC, hipStream_t s) {
   const int64_t wgs = int64_t(a.N) * a.H * (a.DV / kBV);
   return by_dim(a.DK, [&](auto dk) {
-    hipLaunchKernelGGL((ssm_f32_kernel<T, decltype(dk)::value, MODE>), dim3(unsigned(wgs)), dim3(kThreads), 0, s, a,
+    hipLaunchKernelGGL((ssm_f32_kernel<T, decltype(dk)::value, MODE>), dim3(unsigned(wgs)), dim3(kChain), 0, s, a,
                        states, NC);
     return hipGetLastError();
   });
@@ -497,7 +515,7 @@ hipError_t launch_chain(const SsmFwd& a, float* states, int NC, hipStream_t s) {
 
 }  // namespace
 
-int64_t ssm_f32_threads(int64_t seqs, int H, int DV) { return seqs * H * (DV / kBV) * kThreads; }
+int64_t ssm_f32_threads(int64_t seqs, int H, int DV) { return seqs * H * (DV / kBV) * kChain; }
 
 template <typename T>
 hipError_t launch_ssm_f32(const SsmFwd& a, hipStream_t s) {
