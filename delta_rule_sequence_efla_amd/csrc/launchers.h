@@ -297,6 +297,11 @@ struct SsmFwd {
   int64_t q_row, k_row, v_row, dt_row, o_row;
   int N, P, H, Hk, DK, DV;  // N: sequences; P: rows of s0 and sfin
   int64_t L;                // tokens a sequence, or of the packed batch
+  // Sequences cut into segments of `seg` tokens (0: not), seg_slots of them a head;
+  // seg_s [seg_slots H][d_k][d_v] and seg_e [seg_slots H]: a segment's end state (the
+  // first's from s0, the others' from zero; the last's place holds s0) and its decay.
+  int64_t seg = 0, seg_slots = 0;
+  float *seg_s = nullptr, *seg_e = nullptr;
 };
 struct SsmBwd {
   const void *q, *k, *v, *dt, *d_o;
@@ -308,12 +313,13 @@ struct SsmBwd {
   int64_t L;
 };
 // In float32 throughout, every size and type, 32 tokens at a time (ssm_f32.hip).
+// local: the segments' end states and decays alone.
 template <typename T>
-hipError_t launch_ssm_f32(const SsmFwd& a, hipStream_t s);
+hipError_t launch_ssm_f32(const SsmFwd& a, bool local, hipStream_t s);
 int64_t ssm_f32_threads(int64_t seqs, int H, int DV);
 // bf16, d_k 64 or 128, d_v a multiple of 32, 64 tokens at a time (ssm_chunk.h).
 bool ssm_chunk_supported(int DK, int DV);
-hipError_t launch_ssm_chunk(const SsmFwd& a, hipStream_t s);
+hipError_t launch_ssm_chunk(const SsmFwd& a, bool local, hipStream_t s);
 int64_t ssm_chunk_threads(int64_t seqs, int H, int DV);
 template <typename T>
 hipError_t launch_ssm_bwd_f32(const SsmBwd& b, void* ws, hipStream_t s);

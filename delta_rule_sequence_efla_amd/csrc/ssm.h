@@ -96,4 +96,71 @@ __device__ __forceinline__ int ranked_seq(const int32_t* __restrict__ cu, const 
   return __builtin_amdgcn_readfirstlane(__builtin_ctzll(__ballot(lane < N && rank == r)));
 }
 
+// What workgroup unit x (of the sequences' or their segments') has to do for head h.
+struct SsmUnit {
+  int seq;            // sequence; < 0: nothing to do
+  int64_t bos, len;   // its tokens
+  int64_t slot;       // its segment's place in seg_s and seg_e; those of the sequence are H apart
+  int64_t first, end; // the places of the sequence's first and last segment
+  int before;         // segments before it
+  bool last;          // the sequence ends in it
+  // Where the unit's first state comes from.  The launch that brings the segments' ends
+  // (local) starts a sequence's first segment from s0, and keeps s0 at the place of the
+  // last, which it has no use for: the final state may be written over s0, and in the
+  // second launch the last segment may end before the first one begins.
+  __device__ __forceinline__ const float* start(bool local, const float* s0, const float* seg_s, int64_t state) const {
+    if (before == 0 && (local || last)) return s0;
+    return local ? nullptr : seg_s + (before == 0 ? end : first) * state;
+  }
+};
+template <int C, typename Args>
+__device__ __forceinline__ SsmUnit ssm_unit(const Args& a, int x, int h, int lane) {
+  SsmUnit u{x, 0, 0, 0, 0, 0, 0, true};
+  if (a.seg == 0) {
+    u.bos = int64_t(x) * a.L;
+    u.len = a.L;
+    if (a.cu != nullptr) {
+      u.seq = ranked_seq<C>(a.cu, a.order, x, a.N, a.L);
+      u.bos = clamp_offset(a.cu[u.seq], 0, a.L);
+      u.len = clamp_offset(a.cu[u.seq + 1], u.bos, a.L) - u.bos;
+    }
+    return u;
+  }
+  int64_t end;
+  if (a.cu == nullptr) {
+    const int per = int((a.L + a.seg - 1) / a.seg);
+    u.seq = x / per;
+    u.before = x % per;
+    u.bos = int64_t(u.seq) * a.L;
+    end = u.bos + a.L;
+  } else {
+    // slots floor(offset / seg) + u, as those of chunks (common.h); a sequence
+    // without tokens has one, to copy its state
+    int lo = 0, left = a.N;
+    while (left > 1) {
+      const int step = (left + kWave - 1) / kWave, at = lane * step;
+      const bool before = at < left && clamp_offset(a.cu[lo + at], 0, a.L) / a.seg + lo + at <= x;
+      const int cnt = __popcll(__ballot(before)), by = cnt > 1 ? (cnt - 1) * step : 0;
+      lo += by;
+      left = left - by < step ? left - by : step;
+    }
+    u.seq = __builtin_amdgcn_readfirstlane(lo);
+    u.bos = clamp_offset(a.cu[u.seq], 0, a.L);
+    end = clamp_offset(a.cu[u.seq + 1], u.bos, a.L);
+    const int64_t n = x - (u.bos / a.seg + u.seq);
+    if (n < 0 || n * a.seg >= (end > u.bos ? end - u.bos : 1)) {
+      u.seq = -1;
+      return u;
+    }
+    u.before = int(n);
+  }
+  u.slot = int64_t(x) * a.H + h;
+  u.first = u.slot - int64_t(u.before) * a.H;
+  u.end = u.first + (end > u.bos ? (end - u.bos - 1) / a.seg : 0) * a.H;
+  u.bos += u.before * a.seg;
+  u.last = u.bos + a.seg >= end;
+  u.len = u.last ? end - u.bos : a.seg;
+  return u;
+}
+
 }  // namespace efla

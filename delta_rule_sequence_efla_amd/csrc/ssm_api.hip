@@ -74,18 +74,62 @@ bool all_aligned16(std::initializer_list<const void*> ptrs) {
   return true;
 }
 
-// Whether the forward's launches over these sequences have fewer threads than the
-// runtime takes.
 bool ssm_chunked(int d_k, int d_v, efla_dtype dt) { return dt == EFLA_BF16 && efla::ssm_chunk_supported(d_k, d_v); }
 
-bool ssm_fwd_fits(int64_t seqs, int H, int d_k, int d_v, efla_dtype dt) {
-  return (ssm_chunked(d_k, d_v, dt) ? efla::ssm_chunk_threads(seqs, H, d_v) : efla::ssm_f32_threads(seqs, H, d_v)) <=
+// How the forward cuts its sequences: where sequences, heads and value blocks leave
+// most compute units without work, long ones are cut into segments of whole chunks.  A
+// first launch brings each segment's end state (from zero, the first's from s0) and its
+// decay, the second folds those before it into each segment's own first state and runs
+// all side by side.
+// Measured (us, whole / cut into segments for 256 workgroups):
+//   bf16, workgroups 4-16:  1 x 3500 4 heads d 64 53 / 19, 1 x 800 16.2 / 12.4, packed 2 in 12000 tokens 133 / 37
+//   bf16, 64, 16 heads d 128: 1 x 2048 44 / 32, 1 x 512 15.4 / 16.1;  128: 2 x 4096 83 / 90;  1024: packed 16 in 16384 130 / 181
+//   float32, 32-64:  2 x 777 8 heads d 64 52 / 35, 1 x 1200 4 heads d 128 110 / 57;  512: packed 4 in 3000 167 / 192
+struct Segments {
+  int64_t seg = 0, slots = 0;  // tokens a segment (0: not cut), segments a head
+};
+Segments ssm_segments(int64_t seqs, bool packed, int H, int64_t L, int d_k, int d_v, efla_dtype dt) {
+  const bool chunked = ssm_chunked(d_k, d_v, dt);
+  const int64_t chunk = chunked ? 64 : 32, wgs = seqs * H * (d_v / (chunked ? 32 : 16));
+  if (wgs <= 0 || wgs > 64) return {};
+  // segments of the longest sequence there may be: a packed batch may be one sequence and empty ones
+  const int64_t chunks = (L + chunk - 1) / chunk, want = 256 / (packed ? wgs / seqs : wgs);
+  const int64_t even = (chunks + want - 1) / want, per = even < 2 ? 2 : even;  // chunks a segment
+  if (chunks < 2 * per + 6) return {};
+  Segments r;
+  r.seg = per * chunk;
+  r.slots = packed ? L / r.seg + seqs : seqs * ((L + r.seg - 1) / r.seg);
+  return r;
+}
+
+size_t ssm_fwd_workspace(const Segments& g, int H, int d_k, int d_v) {
+  return al256(size_t(g.slots) * H * d_k * d_v * sizeof(float)) + al256(size_t(g.slots) * H * sizeof(float));
+}
+
+// Whether the forward's launches over these sequences have fewer threads than the
+// runtime takes.
+bool ssm_fwd_fits(int64_t seqs, bool packed, int H, int64_t L, int d_k, int d_v, efla_dtype dt) {
+  const Segments g = ssm_segments(seqs, packed, H, L, d_k, d_v, dt);
+  const int64_t units = g.seg > 0 ? g.slots : seqs;
+  return (ssm_chunked(d_k, d_v, dt) ? efla::ssm_chunk_threads(units, H, d_v) : efla::ssm_f32_threads(units, H, d_v)) <=
          efla::kMaxLaunchThreads;
 }
 
-efla_status ssm_forward(const efla::SsmFwd& a, efla_dtype dt, void*, hipStream_t s) {
-  if (ssm_chunked(a.DK, a.DV, dt)) return from_hip(efla::launch_ssm_chunk(a, s));
-  return by_type(dt, [&](auto t) { return efla::launch_ssm_f32<decltype(t)>(a, s); });
+efla_status ssm_forward(efla::SsmFwd a, efla_dtype dt, void* workspace, hipStream_t s) {
+  const Segments g = ssm_segments(a.N, a.cu != nullptr, a.H, a.L, a.DK, a.DV, dt);
+  auto launch = [&](bool local) {
+    if (ssm_chunked(a.DK, a.DV, dt)) return from_hip(efla::launch_ssm_chunk(a, local, s));
+    return by_type(dt, [&](auto t) { return efla::launch_ssm_f32<decltype(t)>(a, local, s); });
+  };
+  if (g.seg > 0) {
+    a.seg = g.seg;
+    a.seg_slots = g.slots;
+    a.seg_s = static_cast<float*>(workspace);
+    a.seg_e = a.seg_s + al256(size_t(g.slots) * a.H * a.DK * a.DV * sizeof(float)) / sizeof(float);
+    const efla_status st = launch(true);
+    if (st != EFLA_OK) return st;
+  }
+  return launch(false);
 }
 
 bool ssm_bwd_chunked(int64_t L, int d_k, int d_v, efla_dtype dt) { return L > 0 && ssm_chunked(d_k, d_v, dt); }
@@ -168,7 +212,10 @@ efla_status efla_conv_bwd(const void* x, int64_t x_row, const void* w, const voi
   });
 }
 
-size_t efla_ssm_fwd_workspace_size(int, int, int, int64_t, int, int, efla_dtype) { return 0; }
+size_t efla_ssm_fwd_workspace_size(int B, int H, int Hk, int64_t L, int d_k, int d_v, efla_dtype dtype) {
+  if (B < 1 || check_ssm(B, H, Hk, L, d_k, d_v, dtype) != EFLA_OK) return 0;
+  return ssm_fwd_workspace(ssm_segments(B, false, H, L, d_k, d_v, dtype), H, d_k, d_v);
+}
 
 efla_status efla_ssm_fwd(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
                          const void* dt, int64_t dt_row, const float* a, const float* d, const float* dt_bias,
@@ -180,7 +227,7 @@ efla_status efla_ssm_fwd(const void* q, int64_t q_row, const void* k, int64_t k_
   const int64_t kw = int64_t(Hk) * d_k, vw = int64_t(H) * d_v;
   st = check_rows(dtype, {{q_row, kw, true}, {k_row, kw, true}, {v_row, vw, true}, {dt_row, H, false}, {o_row, vw, true}});
   if (st != EFLA_OK) return st;
-  if (!ssm_fwd_fits(B, H, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
+  if (!ssm_fwd_fits(B, false, H, L, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
   if (a == nullptr || (L > 0 && !all_given({q, k, v, dt, o}))) return EFLA_ERR_INVALID_ARG;
   if (!all_aligned16({q, k, v, o})) return EFLA_ERR_INVALID_ARG;
   const size_t need = efla_ssm_fwd_workspace_size(B, H, Hk, L, d_k, d_v, dtype);
@@ -192,7 +239,10 @@ efla_status efla_ssm_fwd(const void* q, int64_t q_row, const void* k, int64_t k_
   return ssm_forward(x, dtype, workspace, static_cast<hipStream_t>(stream));
 }
 
-size_t efla_ssm_fwd_varlen_workspace_size(int, int, int, int64_t, int, int, efla_dtype) { return 0; }
+size_t efla_ssm_fwd_varlen_workspace_size(int N, int H, int Hk, int64_t T, int d_k, int d_v, efla_dtype dtype) {
+  if (check_ssm(N, H, Hk, T, d_k, d_v, dtype) != EFLA_OK) return 0;
+  return ssm_fwd_workspace(ssm_segments(N, true, H, T, d_k, d_v, dtype), H, d_k, d_v);
+}
 
 efla_status efla_ssm_fwd_varlen(const void* q, int64_t q_row, const void* k, int64_t k_row, const void* v, int64_t v_row,
                                 const void* dt, int64_t dt_row, const float* a, const float* d, const float* dt_bias,
@@ -206,7 +256,7 @@ efla_status efla_ssm_fwd_varlen(const void* q, int64_t q_row, const void* k, int
   const int64_t kw = int64_t(Hk) * d_k, vw = int64_t(H) * d_v;
   st = check_rows(dtype, {{q_row, kw, true}, {k_row, kw, true}, {v_row, vw, true}, {dt_row, H, false}, {o_row, vw, true}});
   if (st != EFLA_OK) return st;
-  if (!ssm_fwd_fits(N, H, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
+  if (!ssm_fwd_fits(N, true, H, T, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
   if (N == 0) return EFLA_OK;
   if (a == nullptr || cu_seqlens == nullptr || (T > 0 && !all_given({q, k, v, dt, o}))) return EFLA_ERR_INVALID_ARG;
   if (!all_aligned16({q, k, v, o})) return EFLA_ERR_INVALID_ARG;

@@ -88,6 +88,7 @@ struct SsmShape {
   static constexpr int PQ = TQ::PER_WAVE, PV = TV::PER_WAVE, COUNT = 2 * PQ + PV;
   // wavefronts by index (SIMD = index % 4)
   static constexpr int kO = 4, kP = 8, kGate = 9, kP3 = 10, kP2 = 11, kDma = 12, THREADS = 13 * kWave;
+  static constexpr int LOCAL_THREADS = 6 * kWave;  // S, gates, DMA
 };
 
 // Value columns of a block: row l of column tile c is column 8 (l / 4) + 4 c + l % 4,
@@ -105,8 +106,11 @@ __device__ __forceinline__ Frag<uint16_t> value_frag(const uint16_t* X, int c, i
   return f;
 }
 
-template <int DK>
-__global__ __launch_bounds__((SsmShape<DK>::THREADS)) void ssm_chunk_kernel(SsmFwd a, int NVB, int remap) {
+// LOCAL: a segment's end state (the first's from s0, the others' from zero) and its
+// decay alone, with the S, gate and DMA waves and neither Q nor o.
+template <int DK, bool LOCAL>
+__global__ __launch_bounds__((LOCAL ? SsmShape<DK>::LOCAL_THREADS : SsmShape<DK>::THREADS)) void ssm_chunk_kernel(
+    SsmFwd a, int NVB, int remap) {
   using S = SsmShape<DK>;
   constexpr int C = S::C, BV = S::BV, NKU = S::NKU, NDT = S::NDT;
   __shared__ __align__(1024) uint16_t ring[3 * S::SLOT];
@@ -117,13 +121,14 @@ __global__ __launch_bounds__((SsmShape<DK>::THREADS)) void ssm_chunk_kernel(SsmF
   const int H = a.H, DV = a.DV;
   int bh, vb;
   ssm_block(int(blockIdx.x), NVB, remap, bh, vb);
-  int seq = bh / H;
   const int h = bh % H, hk = h / (H / a.Hk);
-  if (a.cu != nullptr) seq = ranked_seq<C>(a.cu, a.order, seq, a.N, a.L);
-  const SeqSpan sp = seq_span<C>(a.cu, seq, h, H, a.L, int((a.L + C - 1) / C));
-  const int64_t srow = state_row(a.slots, seq, a.P);
-  const int nc = sp.nc, v0 = vb * BV;
-  const int lane = threadIdx.x & 63, role = wave_id(), li = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, li = lane & 15, g = lane >> 4;
+  const SsmUnit sp = ssm_unit<C>(a, bh / H, h, lane);
+  if (sp.seq < 0 || (LOCAL && sp.last)) return;
+  const int64_t srow = state_row(a.slots, sp.seq, a.P);
+  const int nc = int((sp.len + C - 1) / C), v0 = vb * BV;
+  int role = wave_id();
+  if (LOCAL && role >= S::kO) role = role == S::kO ? S::kGate : S::kDma;
   auto valid_of = [&](int n) { return int(sp.len - int64_t(n) * C < C ? sp.len - int64_t(n) * C : C); };
   auto tok_of = [&](int n) { return sp.bos + int64_t(n) * C; };
   // Barriers: one before chunk 0's operands are read, one before every chunk n
@@ -154,15 +159,18 @@ __global__ __launch_bounds__((SsmShape<DK>::THREADS)) void ssm_chunk_kernel(SsmF
         for (int j = 0; j < S::PV; ++j) tv.template issue<R>(j, addr + 2 * S::VOFF, vs, valid);
 #pragma unroll
         for (int j = 0; j < S::PQ; ++j) tk.template issue<R>(j, addr + 2 * S::KOFF, ks, valid);
+        if constexpr (!LOCAL) {
 #pragma unroll
-        for (int j = 0; j < S::PQ; ++j) tq.template issue<R>(j, addr + 2 * S::QOFF, qs, valid);
+          for (int j = 0; j < S::PQ; ++j) tq.template issue<R>(j, addr + 2 * S::QOFF, qs, valid);
+        }
       };
       if (valid == C) body(std::false_type{});
       else body(std::true_type{});
     };
-    static_assert(S::COUNT < 64, "one chunk's transfers fit the vmcnt counter");
+    constexpr int COUNT = LOCAL ? S::COUNT - S::PQ : S::COUNT;
+    static_assert(COUNT < 64, "one chunk's transfers fit the vmcnt counter");
     auto wait_for = [&](bool more) {  // all but the transfers issued last, where there are such
-      if (more) wait_vmcnt<S::COUNT>();
+      if (more) wait_vmcnt<COUNT>();
       else wait_vmcnt<0>();
     };
     if (nc > 0) issue(0);
@@ -206,11 +214,32 @@ __global__ __launch_bounds__((SsmShape<DK>::THREADS)) void ssm_chunk_kernel(SsmF
     const int c = role & 1, d0 = ND * (role >> 1);
     const int col = v0 + value_phys(c, li);
     f32x4 St[ND];  // St[d][qq] = S[key_phys(16 (d0 + d) + 4 g + qq)][col]
-    const float* s0 = a.s0 == nullptr || srow < 0 ? nullptr : a.s0 + (srow * H + h) * DK * DV + col;
+    auto at = [&](int d, int qq) { return int64_t(key_phys(16 * (d0 + d) + 4 * g + qq)) * DV; };
+    auto put_state = [&](float* dst) {
+#pragma unroll
+      for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int qq = 0; qq < 4; ++qq) dst[at(d, qq)] = St[d][qq];
+    };
+    const float* s0 = a.s0 == nullptr || srow < 0 ? nullptr : a.s0 + (srow * H + h) * DK * DV;
+    s0 = sp.start(LOCAL, s0, a.seg_s, int64_t(DK) * DV);
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int qq = 0; qq < 4; ++qq) St[d][qq] = s0 != nullptr ? s0[int64_t(key_phys(16 * (d0 + d) + 4 * g + qq)) * DV] : 0.0f;
+      for (int qq = 0; qq < 4; ++qq) St[d][qq] = s0 != nullptr ? s0[at(d, qq) + col] : 0.0f;
+    if constexpr (LOCAL) {
+      if (sp.before == 0) put_state(a.seg_s + sp.end * DK * DV + col);
+    } else {
+      for (int64_t slot = sp.first + H; slot < sp.slot; slot += H) {  // the segments before, in order
+        const float e = a.seg_e[slot];
+        const float* src = a.seg_s + slot * DK * DV + col;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq) St[d][qq] = fmaf(e, St[d][qq], src[at(d, qq)]);
+      }
+    }
+    float decay = 1.0f;  // of all chunks
     auto publish = [&](int buf) {
 #pragma unroll
       for (int d = 0; d < ND; d += 2) bS[buf][c][(d0 + d) / 2][lane] = acc_frag<uint16_t>(St[d], St[d + 1]).v;
@@ -242,11 +271,12 @@ __global__ __launch_bounds__((SsmShape<DK>::THREADS)) void ssm_chunk_kernel(SsmF
     };
     sync();
     load(0);
-    publish(0);
+    if constexpr (!LOCAL) publish(0);
     weigh(0);
     for (int n = 0; n < nc; ++n) {
       sync();
       const float all = gates[n % 3].e[63];
+      if constexpr (LOCAL) decay *= all;
 #pragma unroll
       for (int d = 0; d < ND; ++d) St[d] = all * St[d];
 #pragma unroll
@@ -256,17 +286,14 @@ __global__ __launch_bounds__((SsmShape<DK>::THREADS)) void ssm_chunk_kernel(SsmF
 #pragma unroll
           for (int d = 0; d < ND; ++d) mma(St[d], KT[ku][d], W[ku][part]);
       load(n + 1);  // past the last chunk: stale values that nothing uses
-      publish((n + 1) & 1);
+      if constexpr (!LOCAL) publish((n + 1) & 1);
       weigh(n + 1);
     }
     sync();
-    if (a.sfin != nullptr && srow >= 0) {
-      float* sf = a.sfin + (srow * H + h) * DK * DV + col;
-#pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int qq = 0; qq < 4; ++qq) sf[int64_t(key_phys(16 * (d0 + d) + 4 * g + qq)) * DV] = St[d][qq];
-    }
+    float* sf = LOCAL ? a.seg_s + sp.slot * DK * DV + col
+                      : a.sfin == nullptr || srow < 0 || !sp.last ? nullptr : a.sfin + (srow * H + h) * DK * DV + col;
+    if (sf != nullptr) put_state(sf);
+    if (LOCAL && vb == 0 && threadIdx.x == 0) a.seg_e[sp.slot] = decay;
   } else if (role >= S::kP) {
     // ------------------------------------------------------------------- P
     auto p_role = [&](auto r0c, auto r1c) {

@@ -13,7 +13,7 @@ namespace efla {
 namespace {
 
 constexpr int kC = 32, kBV = 16;  // tokens a chunk, value columns a workgroup of a chain
-constexpr int kFwd = 0, kStates = 1, kReverse = 2;
+constexpr int kFwd = 0, kStates = 1, kReverse = 2, kLocal = 3;
 constexpr int kChain = 2 * kThreads;  // threads of a workgroup of a chain
 
 // ROWS x COLS values of T (row t at src + t * stride) on their way to the LDS:
@@ -58,12 +58,14 @@ using Gates = GatesOf<kC>;
 //   kStates:  the state before every chunk, [slot][d_k][d_v]
 //   kReverse: the chunks from last to first, X <- e^{G_C} X + Q^T diag(e^G) dO,
 //             and X after every chunk (k = q, v = dO here)
+//   kLocal:   a segment's end state (the first's from s0, the others' from zero) and
+//             its decay
 // A chunk takes two barriers.  Behind the first, side by side: three wavefronts the
 // tiles of P, two S^T Q^T for half of the tokens each, two (the chains: four) the
 // state's tiles, which stay in their accumulators, one the gates of the next chunk.
 // Behind the second: O = diag(e^G) S^T Q^T + V^T P^T and its store, the new state
 // into the LDS for the next readout, and the next chunk's tokens into the other
-// buffer.  Bound by that chain: 777 tokens, d 64, 25 chunks, F32US; one after the other
+// buffer.  Bound by that chain: 777 tokens, d 64, 25 chunks in one go, 52 us; one after the other
 // with three barriers and the gates in line, on four wavefronts, 77 us.
 template <typename T, int DK, int MODE>
 __global__ __launch_bounds__(kChain) void ssm_f32_kernel(SsmFwd a, float* __restrict__ states, int NC) {
@@ -80,14 +82,9 @@ __global__ __launch_bounds__(kChain) void ssm_f32_kernel(SsmFwd a, float* __rest
   const int NVB = a.DV / kBV, H = a.H;
   const uint32_t wg = blockIdx.x, unit = wg / uint32_t(NVB);
   const int v0 = int(wg % uint32_t(NVB)) * kBV, h = int(unit % uint32_t(H));
-  int seq = int(unit / uint32_t(H));
-  int64_t bos = int64_t(seq) * a.L, len = a.L;
-  if (a.cu != nullptr) {
-    seq = ranked_seq<kC>(a.cu, a.order, seq, a.N, a.L);
-    bos = clamp_offset(a.cu[seq], 0, a.L);
-    len = clamp_offset(a.cu[seq + 1], bos, a.L) - bos;
-  }
-  const int64_t row = state_row(a.slots, seq, a.P);
+  const SsmUnit sp = ssm_unit<kC>(a, int(unit / uint32_t(H)), h, int(threadIdx.x) & 63);
+  if (sp.seq < 0 || (MODE == kLocal && sp.last)) return;
+  const int64_t bos = sp.bos, len = sp.len, row = state_row(a.slots, sp.seq, a.P);
   const int hk = h / (H / a.Hk);
   const T* q = static_cast<const T*>(a.q) + bos * a.q_row + hk * DK;
   const T* k = static_cast<const T*>(a.k) + bos * a.k_row + hk * DK;
@@ -99,13 +96,14 @@ __global__ __launch_bounds__(kChain) void ssm_f32_kernel(SsmFwd a, float* __rest
   const int sw = w - (8 - SW);  // >= 0: an S wave, tiles sw, sw + SW, ..
 
   f32x4 S[OWN];
-  const float* s0 = a.s0 == nullptr || row < 0 ? nullptr : a.s0 + (row * H + h) * DK * a.DV + v0 + li;
+  const float* s0 = a.s0 == nullptr || row < 0 ? nullptr : a.s0 + (row * H + h) * DK * a.DV;
+  s0 = sp.start(MODE == kLocal, s0, a.seg_s, int64_t(DK) * a.DV);
 #pragma unroll
   for (int i = 0; i < OWN; ++i)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int r = 16 * (sw + SW * i) + 4 * g + e;
-      S[i][e] = sw >= 0 && s0 != nullptr && r < DK ? s0[int64_t(r) * a.DV] : 0.0f;
+      S[i][e] = sw >= 0 && s0 != nullptr && r < DK ? s0[int64_t(r) * a.DV + v0 + li] : 0.0f;
     }
   auto store = [&](float* dst) {
 #pragma unroll
@@ -116,6 +114,21 @@ __global__ __launch_bounds__(kChain) void ssm_f32_kernel(SsmFwd a, float* __rest
         if (r < DK) dst[int64_t(r) * a.DV + v0 + li] = S[i][e];
       }
   };
+  if (MODE == kLocal && sw >= 0 && sp.before == 0) store(a.seg_s + sp.end * DK * a.DV);
+  if (FWD && sw >= 0) {
+    for (int64_t slot = sp.first + H; slot < sp.slot; slot += H) {  // the segments before, in order
+      const float d = a.seg_e[slot];
+      const float* src = a.seg_s + slot * DK * a.DV + v0 + li;
+#pragma unroll
+      for (int i = 0; i < OWN; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int r = 16 * (sw + SW * i) + 4 * g + e;
+          if (r < DK) S[i][e] = fmaf(d, S[i][e], src[int64_t(r) * a.DV]);
+        }
+    }
+  }
+  float decay = 1.0f;  // of all chunks
   auto publish = [&]() {
 #pragma unroll
     for (int i = 0; i < OWN; ++i)
@@ -193,11 +206,12 @@ __global__ __launch_bounds__(kChain) void ssm_f32_kernel(SsmFwd a, float* __rest
       for (int ku = 0; ku < KU; ++ku) mma(x, lds_frag(St[0], KP, li, ku, g), lds_frag(Qs[b][0], KP, i, ku, g));
       x = gt.e[i] * x;
     } else if (sw >= 0) {  // S <- e^{G_C} S + K^T diag(w) V
-      if constexpr (!FWD) store(states + (int64_t(unit) * NC + chunk_at(n)) * DK * a.DV);
+      if constexpr (MODE == kStates || MODE == kReverse) store(states + (int64_t(unit) * NC + chunk_at(n)) * DK * a.DV);
       Frag<float> wv = lds_frag_t(Vs[b][0], VP, li, 0, g);
 #pragma unroll
       for (int e = 0; e < 8; ++e) wv.v[e] *= (MODE == kReverse ? gt.e : gt.w)[16 * (e / 4) + 4 * g + e % 4];
       const float all = gt.e[kC - 1];
+      decay *= all;
 #pragma unroll
       for (int i = 0; i < OWN; ++i)
         if (sw + SW * i < DT) {
@@ -224,7 +238,12 @@ __global__ __launch_bounds__(kChain) void ssm_f32_kernel(SsmFwd a, float* __rest
     }
     __syncthreads();
   }
-  if (a.sfin != nullptr && row >= 0 && sw >= 0) store(a.sfin + (row * H + h) * DK * a.DV);
+  if constexpr (MODE == kLocal) {
+    if (sw >= 0) store(a.seg_s + sp.slot * DK * a.DV);
+    if (v0 == 0 && sw == 0 && lane == 0) a.seg_e[sp.slot] = decay;
+  } else {
+    if (a.sfin != nullptr && row >= 0 && sw >= 0 && sp.last) store(a.sfin + (row * H + h) * DK * a.DV);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -505,7 +524,7 @@ hipError_t by_dim(int d, F&& f) {
 
 template <typename T, int MODE>
 hipError_t launch_chain(const SsmFwd& a, float* states, int NC, hipStream_t s) {
-  const int64_t wgs = int64_t(a.N) * a.H * (a.DV / kBV);
+  const int64_t wgs = (a.seg > 0 ? a.seg_slots : a.N) * a.H * (a.DV / kBV);
   return by_dim(a.DK, [&](auto dk) {
     hipLaunchKernelGGL((ssm_f32_kernel<T, decltype(dk)::value, MODE>), dim3(unsigned(wgs)), dim3(kChain), 0, s, a,
                        states, NC);
@@ -518,11 +537,11 @@ hipError_t launch_chain(const SsmFwd& a, float* states, int NC, hipStream_t s) {
 int64_t ssm_f32_threads(int64_t seqs, int H, int DV) { return seqs * H * (DV / kBV) * kChain; }
 
 template <typename T>
-hipError_t launch_ssm_f32(const SsmFwd& a, hipStream_t s) {
-  return launch_chain<T, kFwd>(a, nullptr, 0, s);
+hipError_t launch_ssm_f32(const SsmFwd& a, bool local, hipStream_t s) {
+  return local ? launch_chain<T, kLocal>(a, nullptr, 0, s) : launch_chain<T, kFwd>(a, nullptr, 0, s);
 }
-template hipError_t launch_ssm_f32<float>(const SsmFwd&, hipStream_t);
-template hipError_t launch_ssm_f32<uint16_t>(const SsmFwd&, hipStream_t);
+template hipError_t launch_ssm_f32<float>(const SsmFwd&, bool, hipStream_t);
+template hipError_t launch_ssm_f32<uint16_t>(const SsmFwd&, bool, hipStream_t);
 
 hipError_t launch_ssm_sums(const float* part, float* da, float* dbias, float* dd, int64_t M, int H, hipStream_t s) {
   hipLaunchKernelGGL(ssm_sum_kernel, dim3(unsigned(3 * H)), dim3(kThreads), 0, s, part, da, dbias, dd, M, H);

@@ -531,14 +531,18 @@ efla_status efla_conv_bwd(const void *x, int64_t x_row, const void *w, const voi
  *   - A decay below e^{-128} is zero in float32, and so it acts.  A token's step
  *     size may be zero (dt of -inf): it leaves the state as it was.
  *   - States are carried in float32.  For bf16 inputs, matrix-core products that
- *     feed a state or a float32 gradient take each float32 operand as the sum of
- *     two bf16 values (16 significant bits), so these are good to about 1e-5;
- *     products that only feed bf16 outputs round such operands once.
+ *     feed the forward's state take each float32 operand as the sum of three bf16
+ *     values (24 significant bits); those that feed a float32 gradient, as the sum
+ *     of two (16 bits), so da, dd, dbias and ds0 are good to about 1e-5; products
+ *     that only feed bf16 outputs round such operands once.
  *   - A NaN or an infinity in a token's row reaches its sequence's outputs from
  *     the start of its chunk of 64 tokens on, not only from the token on; never
  *     another sequence's.
  *   - A call whose largest launch would have 2^32 threads or more is
  *     EFLA_ERR_UNSUPPORTED.
+ *   - The forward needs a workspace where it cuts few, long sequences into segments
+ *     that run side by side; its size is a function of the sizes alone, not of the
+ *     offsets.
  *
  * efla_ssm_fwd -- dense batch [B, L, ..]; s0, s_final [B, H, d_k, d_v] (each
  *     nullable; s_final may be s0).  L may be 0: the state is copied.

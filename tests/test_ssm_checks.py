@@ -100,6 +100,16 @@ def test_ssm_alignment(call):
     assert call(row=260) == INVALID and call(krow=129) == INVALID  # rows that do not start on 16 bytes
 
 
+def test_ssm_workspace_of_cut_sequences():
+    size, packed = efla.efla_ssm_fwd_workspace_size, efla.efla_ssm_fwd_varlen_workspace_size
+    n = size(1, 4, 4, 3500, 64, 64, BF)  # segments of two chunks of 64 tokens, 28 of them a head
+    assert n >= 28 * 4 * (64 * 64 + 1) * 4
+    assert size(4, 16, 16, 4096, 128, 128, BF) == 0 and size(1, 4, 4, 300, 64, 64, BF) == 0 and size(1, 4, 3, 3500, 64, 64, BF) == 0
+    assert packed(3, 4, 4, 3500, 64, 64, BF) > n and packed(100, 4, 4, 3500, 64, 64, BF) == 0
+    assert ssm(L=3500, H=4, Hk=4, ws=NUL, row=256) == WORKSPACE and ssm(L=3500, Hk=4, n=64) == WORKSPACE
+    assert ssm(L=3500, Hk=4, ws=ODD) == INVALID and ssm_varlen(L=3500, Hk=4, ws=NUL) == WORKSPACE
+
+
 def test_ssm_counts():
     assert ssm(B=0) == INVALID and ssm(L=-1) == INVALID and ssm_bwd(B=0) == INVALID and ssm_bwd(L=-1) == INVALID
     assert ssm_varlen(N=-1) == INVALID and ssm_varlen(L=-1) == INVALID and ssm_varlen(L=1 << 31) != OK
