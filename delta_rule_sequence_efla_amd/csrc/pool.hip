@@ -9,7 +9,12 @@ namespace efla {
 
 constexpr int kPieceVecs = 8;                              // 16-byte vectors a thread
 constexpr int kPieceBytes = kThreads * kPieceVecs * 16;    // of a row, a workgroup
-constexpr int kMaxShare = 8192;
+// Entries up to which a shared source is looked for: every workgroup runs over the
+// list.  us without / with it, rows of 1 MiB each copied to 1, 2 or 8 others:
+//   64 entries  25 / 26, 18 / 17, 17 / 15     256  98 / 108, 83 / 76, 88 / 51
+//   512  187 / 220, 159 / 154, 174 / 113      1024 of 512 KiB  183 / 313, 159 / 273, 183 / 179
+//   8192 of 64 KiB  181 / 1395, 166 / 1425, 181 / 1475
+constexpr int kMaxShare = 512;
 
 int64_t pool_pieces(uint64_t row_bytes) { return int64_t((row_bytes + kPieceBytes - 1) / kPieceBytes); }
 

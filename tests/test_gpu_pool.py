@@ -104,3 +104,18 @@ def test_no_entries_and_a_captured_graph():
             row = w[want_new[2]].clone()
             w[order[0]] = row
             assert torch.equal(p, w)
+
+
+@pytest.mark.parametrize("N", [512, 513, 3000])
+def test_forks_of_long_lists(N):
+    """Lists on both sides of the length up to which one read serves all copies of a row."""
+    P = N + 40
+    pool = torch.randn(P, 24, device="cuda")
+    gen = torch.Generator().manual_seed(N)
+    src = torch.randint(-1, 40, (N,), generator=gen)
+    src[src >= 0] += N  # the last 40 rows, or none: cleared
+    dst = torch.randperm(N, generator=gen)
+    want = pool.clone()
+    want[dst.cuda()] = torch.where((src >= 0).cuda()[:, None], pool[src.clamp(min=0).cuda()], torch.zeros((), device="cuda"))
+    efla.efla_pool_copy([pool], src.to(**I32), dst.to(**I32))
+    assert torch.equal(pool, want)
