@@ -13,6 +13,12 @@ constexpr int64_t kMaxRow = int64_t(1) << 24;  // elements from one token's row 
 
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
+bool all_aligned_to(std::initializer_list<const void*> ptrs, size_t n) {
+  for (const void* p : ptrs)
+    if (!aligned_to(p, n)) return false;
+  return true;
+}
+
 template <typename F>
 efla_status by_type(efla_dtype dt, F&& f) {
   return from_hip(dt == EFLA_BF16 ? f(uint16_t{}) : f(float{}));
@@ -35,11 +41,7 @@ efla_status check_conv(int64_t N, int64_t L, int D, int W, int silu, efla_dtype 
   return EFLA_OK;
 }
 
-bool conv_aligned(efla_dtype dt, std::initializer_list<const void*> ptrs) {
-  for (const void* p : ptrs)
-    if (!aligned_to(p, elem_bytes(dt))) return false;
-  return true;
-}
+bool conv_aligned(efla_dtype dt, std::initializer_list<const void*> ptrs) { return all_aligned_to(ptrs, elem_bytes(dt)); }
 
 bool conv_fits(int64_t seqs, int64_t L, int64_t N, int D) {
   return L <= kMaxGrid && seqs * D <= kMaxGrid && N * int64_t(D) <= (int64_t(1) << 40) &&
@@ -68,10 +70,9 @@ efla_status check_rows(efla_dtype dt, std::initializer_list<Rows> rows) {
   return EFLA_OK;
 }
 
-bool all_aligned16(std::initializer_list<const void*> ptrs) {
-  for (const void* p : ptrs)
-    if (!aligned16(p)) return false;
-  return true;
+bool all_aligned16(std::initializer_list<const void*> ptrs) { return all_aligned_to(ptrs, 16); }
+bool ssm_aligned(efla_dtype dt, std::initializer_list<const void*> elems, std::initializer_list<const void*> floats) {
+  return all_aligned_to(elems, elem_bytes(dt)) && all_aligned_to(floats, sizeof(float));
 }
 
 bool ssm_chunked(int d_k, int d_v, efla_dtype dt) { return dt == EFLA_BF16 && efla::ssm_chunk_supported(d_k, d_v); }
@@ -229,7 +230,7 @@ efla_status efla_ssm_fwd(const void* q, int64_t q_row, const void* k, int64_t k_
   if (st != EFLA_OK) return st;
   if (!ssm_fwd_fits(B, false, H, L, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
   if (a == nullptr || (L > 0 && !all_given({q, k, v, dt, o}))) return EFLA_ERR_INVALID_ARG;
-  if (!all_aligned16({q, k, v, o})) return EFLA_ERR_INVALID_ARG;
+  if (!all_aligned16({q, k, v, o, s0, s_final}) || !ssm_aligned(dtype, {dt}, {a, d, dt_bias})) return EFLA_ERR_INVALID_ARG;
   const size_t need = efla_ssm_fwd_workspace_size(B, H, Hk, L, d_k, d_v, dtype);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
@@ -259,7 +260,7 @@ efla_status efla_ssm_fwd_varlen(const void* q, int64_t q_row, const void* k, int
   if (!ssm_fwd_fits(N, true, H, T, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
   if (N == 0) return EFLA_OK;
   if (a == nullptr || cu_seqlens == nullptr || (T > 0 && !all_given({q, k, v, dt, o}))) return EFLA_ERR_INVALID_ARG;
-  if (!all_aligned16({q, k, v, o})) return EFLA_ERR_INVALID_ARG;
+  if (!all_aligned16({q, k, v, o, s0, s_final}) || !ssm_aligned(dtype, {dt}, {a, d, dt_bias})) return EFLA_ERR_INVALID_ARG;
   const size_t need = efla_ssm_fwd_varlen_workspace_size(N, H, Hk, T, d_k, d_v, dtype);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
@@ -282,6 +283,7 @@ efla_status efla_ssm_step(const void* q, int64_t q_row, const void* k, int64_t k
   if (efla::ssm_step_threads(N, H, d_v) > efla::kMaxLaunchThreads) return EFLA_ERR_UNSUPPORTED;
   if (N == 0 || P == 0) return EFLA_OK;
   if (!all_given({q, k, v, dt, a, state, o}) || !aligned16(state)) return EFLA_ERR_INVALID_ARG;
+  if (!ssm_aligned(dtype, {q, k, v, dt, o}, {a, d, dt_bias})) return EFLA_ERR_INVALID_ARG;
   const efla::SsmStep x{q, k, v, dt, a, d, dt_bias, state, slots, o, q_row, k_row, v_row, dt_row, o_row, N, P, H, Hk, d_k, d_v};
   return by_type(dtype, [&](auto t) { return efla::launch_ssm_step<decltype(t)>(x, static_cast<hipStream_t>(stream)); });
 }
@@ -307,7 +309,9 @@ efla_status efla_ssm_bwd(const void* q, int64_t q_row, const void* k, int64_t k_
   if (st != EFLA_OK) return st;
   if (!ssm_bwd_fits(B, H, L, d_k, d_v, dtype)) return EFLA_ERR_UNSUPPORTED;
   if (a == nullptr || (L > 0 && !all_given({q, k, v, dt, d_o, dq, dk, dv, ddt}))) return EFLA_ERR_INVALID_ARG;
-  if (!all_aligned16({q, k, v, d_o, dq, dk, dv})) return EFLA_ERR_INVALID_ARG;
+  if (!all_aligned16({q, k, v, d_o, dq, dk, dv, s0, ds_final, ds0}) ||
+      !ssm_aligned(dtype, {dt, ddt}, {a, d, dt_bias, da, dd, dbias}))
+    return EFLA_ERR_INVALID_ARG;
   const size_t need = efla_ssm_bwd_workspace_size(B, H, Hk, L, d_k, d_v, dtype);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;

@@ -527,7 +527,9 @@ efla_status efla_conv_bwd(const void *x, int64_t x_row, const void *w, const voi
  *     so that they may be parts of one projection's rows: *_row is the number of
  *     elements from one token's row to the next (at least the row's own length,
  *     < 2^24), the same over all rows.  q, k, v, o, their gradients and their rows
- *     start on 16 bytes (EFLA_ERR_INVALID_ARG otherwise); dt is free.
+ *     start on 16 bytes, and so do states (EFLA_ERR_INVALID_ARG otherwise); dt
+ *     needs its element's alignment alone, and so do q, k, v and o of efla_ssm_step.
+ *     Outputs may not overlap inputs, but that s_final may be s0.
  *   - A decay below e^{-128} is zero in float32, and so it acts.  A token's step
  *     size may be zero (dt of -inf): it leaves the state as it was.
  *   - States are carried in float32.  For bf16 inputs, matrix-core products that

@@ -207,3 +207,43 @@ def test_results_do_not_change_between_runs():
     for _ in range(3):
         again = efla.efla_conv_bwd(x["x"], x["w"], dy, x["bias"])
         assert all(torch.equal(a, b) for a, b in zip(first[:3], again[:3]))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_another_stream_and_a_captured_graph(dtype):
+    x = dev(R.make_conv(2, 300, 72, 4, dtype))
+    dy = torch.randn(2, 300, 72, device="cuda").to(dtype)
+    pool = torch.randn(4, 3, 72, device="cuda").to(dtype)
+    slots = torch.tensor([2, -1, 0], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 5, 5, 290], dtype=torch.int32, device="cuda")
+
+    def run():
+        st = pool.clone()
+        y, sf = efla.efla_conv_fwd(x["x"], x["w"], x["bias"], x["s0"])
+        z = torch.zeros(300, 72, dtype=dtype, device="cuda")
+        efla.efla_conv_fwd_varlen(x["x"][0], x["w"], cu, x["bias"], s0=st, slots=slots, y=z, s_final=st)
+        t = torch.zeros(3, 72, dtype=dtype, device="cuda")
+        efla.efla_conv_step(x["x"][0, :3], x["w"], st, x["bias"], slots=slots, y=t)
+        return (y, sf, z, t, st) + tuple(efla.efla_conv_bwd(x["x"], x["w"], dy, x["bias"], s0=x["s0"]))
+
+    def same(a, b):
+        return all(p is r is None or torch.equal(p, r) for p, r in zip(a, b, strict=True))
+    want = run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run()
+    torch.cuda.current_stream().wait_stream(side)
+    assert same(want, got)
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    outs = []
+    for graph in graphs:
+        with torch.cuda.graph(graph):
+            outs.append(run())
+    for i in range(3):
+        x["x"].copy_(torch.randn(2, 300, 72, device="cuda"))
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        want = run()
+        assert all(same(want, got) for got in outs), i

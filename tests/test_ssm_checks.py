@@ -100,6 +100,22 @@ def test_ssm_alignment(call):
     assert call(row=260) == INVALID and call(krow=129) == INVALID  # rows that do not start on 16 bytes
 
 
+def test_ssm_alignment_of_states_and_parameters():
+    off, run = ctypes.c_void_p(4104), efla.lib()
+    x = ssm_in(FAKE, 256)
+    for args in ((off, NUL, NUL, NUL), (NUL, NUL, NUL, off), (NUL, NUL, ctypes.c_void_p(4102), NUL), (NUL, ODD, NUL, NUL)):
+        s0, d, bias, sf = args
+        assert run.efla_ssm_fwd(*x, FAKE, d, bias, s0, FAKE, 256, sf, 1, 4, 2, 640, 64, 64, 1, FAKE, 1 << 34, NUL) == INVALID
+        assert run.efla_ssm_fwd_varlen(*x, FAKE, d, bias, FAKE, NUL, NUL, 2, 2, s0, FAKE, 256, sf, 4, 2, 640, 64, 64, 1, FAKE,
+                                       1 << 34, NUL) == INVALID
+    for which in range(7):  # s0, ds_final, da, dd, dbias, ds0, ddt
+        s0, dsf, da, dd, dbias, ds0, ddt = (((off, off, ODD, ODD, ODD, off, ctypes.c_void_p(4097))[i] if i == which else
+                                             (NUL if i < 6 else FAKE)) for i in range(7))
+        assert run.efla_ssm_bwd(*x, FAKE, NUL, NUL, s0, FAKE, 256, dsf, FAKE, 256, FAKE, 256, FAKE, 256, ddt, 256, da, dd, dbias,
+                                ds0, 1, 4, 2, 640, 64, 64, 1, FAKE, 1 << 34, NUL) == INVALID
+    assert ssm_step(p=ctypes.c_void_p(4097)) == INVALID and ssm_step(a=ODD) == INVALID
+
+
 def test_ssm_workspace_of_cut_sequences():
     size, packed = efla.efla_ssm_fwd_workspace_size, efla.efla_ssm_fwd_varlen_workspace_size
     n = size(1, 4, 4, 3500, 64, 64, BF)  # segments of two chunks of 64 tokens, 28 of them a head
