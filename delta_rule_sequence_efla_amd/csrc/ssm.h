@@ -18,7 +18,9 @@
 // stands between: with M_ij = dP_ij (q_i . k_j) D_j, r_i = e^{G_i} q_i . (S dO_i)
 // and p_j = w_j k_j . (X v_j),
 //     gd_t = sum_{i >= t > j} M_ij + sum_{i >= t} r_i + sum_{j < t} p_j + e^{G_C} <X, S>,
-// whose first term is sum_{i >= t} (row sum - column sum) of M.  Then
+// whose first term is taken tile by tile (16 x 16): of t's own diagonal tile the pairs
+// around t, of the tiles left of it row sums, of those below it column sums, of those
+// between whole tiles.  Then
 //     dD_t = (column sum of M + p)_t / D_t + a gd_t,   ddt = dD sigmoid(dt + bias),
 //     da = sum D_t gd_t,   dbias = sum ddt,   dd = sum v . dO.
 // Query and key heads may be fewer than value heads: value head h reads query
@@ -161,6 +163,64 @@ __device__ __forceinline__ SsmUnit ssm_unit(const Args& a, int x, int h, int lan
   u.last = u.bos + a.seg >= end;
   u.len = u.last ? end - u.bos : a.seg;
   return u;
+}
+
+// Of a diagonal tile with x[qq] = M_ij D_j at row i = li and column j = 4 g + qq: in
+// lanes li = 0, out[qq] = sum_{i >= t > j} M_ij D_j for t = 4 g + qq, the tile's own share
+// of gd_t.  Formed from the pairs around t alone: as differences of row and column
+// sums, whose diagonals and whose pairs on one side of t cancel, da was off by 1e-5.
+__device__ __forceinline__ f32x4 tile_between(const f32x4& x, int li, int g) {
+  float sum = (x[0] + x[1]) + (x[2] + x[3]);
+  const float one = __shfl_up(sum, 16);
+  sum += g >= 1 ? one : 0.0f;
+  const float two = __shfl_up(sum, 32);
+  sum += g >= 2 ? two : 0.0f;
+  const float left = __shfl_up(sum, 16);
+  float before = g >= 1 ? left : 0.0f;  // of the row's columns below t
+  f32x4 out;
+#pragma unroll
+  for (int qq = 0; qq < 4; ++qq) {
+    out[qq] = row_sum16(li >= 4 * g + qq ? before : 0.0f);
+    before += x[qq];
+  }
+  return out;
+}
+
+// The same with the tile the other way round: x[qq] at row i = 4 g + qq, column j = li.
+__device__ __forceinline__ f32x4 tile_between_tr(const f32x4& x, int li, int g) {
+  float sum = (x[0] + x[1]) + (x[2] + x[3]);
+  const float one = __shfl_down(sum, 16);
+  sum += g <= 2 ? one : 0.0f;
+  const float two = __shfl_down(sum, 32);
+  sum += g <= 1 ? two : 0.0f;
+  const float right = __shfl_down(sum, 16);
+  float from = g <= 2 ? right : 0.0f;  // of the column's rows from t on
+  f32x4 out;
+#pragma unroll
+  for (int qq = 3; qq >= 0; --qq) {
+    from += x[qq];
+    out[qq] = row_sum16(li < 4 * g + qq ? from : 0.0f);
+  }
+  return out;
+}
+
+// Sums over the lane's row of 16: of itself and the lanes above, and of the lanes below.
+__device__ __forceinline__ float row_suffix16(float x, int li) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    const float y = __shfl_down(x, d, 16);
+    x += li + d < 16 ? y : 0.0f;
+  }
+  return x;
+}
+__device__ __forceinline__ float row_before16(float x, int li) {
+#pragma unroll
+  for (int d = 1; d < 16; d <<= 1) {
+    const float y = __shfl_up(x, d, 16);
+    x += li >= d ? y : 0.0f;
+  }
+  const float y = __shfl_up(x, 1, 16);
+  return li > 0 ? y : 0.0f;
 }
 
 }  // namespace efla

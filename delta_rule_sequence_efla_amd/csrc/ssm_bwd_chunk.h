@@ -18,22 +18,24 @@ namespace efla {
 
 // What is kept of every (sequence, head, chunk): its gates, formed by a launch of
 // their own (a wavefront a chunk: formed along the chains, they were half of the
-// chains' time), the state S before it and the gradient X of the state behind it,
-// each as two bf16 parts.  The arrays are cut into k-units of 32,
-// [slot][d_v / 32][d_k][32], so that what one workgroup of the chains writes of a
-// chunk is one piece of memory, and so is the operand fragment that a wavefront of
-// the gradients reads.  (Rows of d_v values, of
-// which four workgroups on four dies write 64 bytes each: 188 us instead of 151 for
-// the chains of 8 x 2048 tokens, 8 heads, d 128.)
+// chains' time), the state S before it and the gradient X of the state behind it.
+// The arrays are cut into k-units of 32, [slot][d_v / 32][d_k][32], so that what one
+// workgroup of the chains writes of a chunk is one piece of memory, and so is the
+// operand fragment that a wavefront of the gradients reads.  (Rows of d_v values, of
+// which four workgroups on four dies write a part each: 188 us instead of 151 for
+// the chains of 8 x 2048 tokens, 8 heads, d 128.)  Both are float32, and three bf16 parts
+// where they become operands of sums that da and dbias are formed from: these are off
+// by up to 2e-6, with two parts in the same bytes by 5e-6 (whole pass 272 us, 253).
 struct SsmStates {
-  uint16_t *sh, *sl, *xh, *xl;
+  float *s, *x;
   ChunkGates* gates;
   struct ChunkSums* sums;
 };
 
 // What the gradients of a chunk's steps are formed from (ssm_steps_kernel), each
-// written by the wavefront that has it: row sums of M and its column sums by D, a
-// tile each; r and p / D by 16 key dims; <X, S> and v . dO by wavefront.
+// written by the wavefront that has it: row sums of M (of a diagonal tile the sums
+// of tile_between) and its column sums by D, a tile each; r and p / D by 16 key dims;
+// <X, S> and v . dO by wavefront.
 struct ChunkSums {
   float row[10][16], col[10][16], r[8][64], p[8][64], xs[16], vo[16];
 };
@@ -157,10 +159,10 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
 #pragma unroll
         for (int qq = 0; qq < 4; ++qq) y[e][qq] = x.w[e][qq] * static_cast<float>(t[qq]);
       }
-      Frag<uint16_t> hi, lo;
-      split_parts(y[0], y[1], hi, lo);
-      lds.bW[n & 1][0][c][ku][lane] = hi.v;
-      lds.bW[n & 1][1][c][ku][lane] = lo.v;
+      Frag<uint16_t> p[3];
+      split3_frag(y[0], y[1], p);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) lds.bW[n & 1][i][c][ku][lane] = p[i].v;
       if (role == S::kW && lane == 0) lds.all[n & 1] = x.all;
       load(x, n + 3);
     };
@@ -190,8 +192,7 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
         if (s0 != nullptr)
           T[d][c] = *reinterpret_cast<const f32x4*>(s0 + (row0 + key_phys(16 * (ND * sw + d) + li)) * DV + v0 + 8 * g + 4 * c);
       }
-    uint16_t* hi_out = REV ? st.xh : st.sh;
-    uint16_t* lo_out = REV ? st.xl : st.sl;
+    float* const out = REV ? st.x : st.s;
     for (int n = 0; n < nc; ++n) {
       sync();
       const uint16_t* cur = lds.ring + (n % 3) * S::SLOT;
@@ -203,11 +204,9 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
       const int64_t slot = int64_t(bh) * nc + chunk_of(n);
 #pragma unroll
       for (int d = 0; d < ND; ++d) {
-        Frag<uint16_t> hi, lo;
-        split_parts(T[d][0], T[d][1], hi, lo);
-        const int64_t at = ((slot * (DV / 32) + vb) * DK + key_phys(16 * (ND * sw + d) + li)) * 32 + 8 * g;
-        *reinterpret_cast<bf16x8*>(hi_out + at) = hi.v;
-        *reinterpret_cast<bf16x8*>(lo_out + at) = lo.v;
+        float* const to = out + ((slot * (DV / 32) + vb) * DK + key_phys(16 * (ND * sw + d) + li)) * 32 + 8 * g;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) *reinterpret_cast<f32x4*>(to + 4 * c) = T[d][c];
       }
       const float all = lds.all[n & 1];
 #pragma unroll
@@ -217,7 +216,7 @@ __device__ __forceinline__ void ssm_chain_run(Lds& lds, const SsmBwd& b, int x, 
 #pragma unroll
       for (int ku = 0; ku < 2; ++ku)
 #pragma unroll
-        for (int part = 1; part >= 0; --part)
+        for (int part = 2; part >= 0; --part)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             Frag<uint16_t> W;
@@ -241,7 +240,7 @@ __global__ __launch_bounds__((SsmChainShape<DK>::THREADS), 5) void ssm_chain_ker
                                                                                     SsmStates st) {
   using S = SsmChainShape<DK>;
   __shared__ __align__(1024) uint16_t ring[3 * S::SLOT];
-  __shared__ __align__(16) bf16x8 bW[2][2][2][2][kWave];  // [buffer][part][column tile][k-unit]
+  __shared__ __align__(16) bf16x8 bW[2][3][2][2][kWave];  // [buffer][part][column tile][k-unit]
   __shared__ __align__(16) uint16_t tile[4][32 * 16];     // a W wave's rows on their way to its operands
   __shared__ float all[2];                                // e^{G_C} of the chunk in bW
   struct Refs {
@@ -402,21 +401,19 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
   f32x4 raw = zero4();  // of tile w: raw[qq] = k_j . q_i, j = 16 ct + 4 g + qq, i = 16 rt + li
   const int tile = w < 10 ? w : 9, rt = tri_row(tile), ct = tile - tri_at(rt, 0);
 
-  // This wavefront's state rows as operands (k index over the value columns, in
-  // wide_frag's order), S for dQ, X for dK, and a head's gates.  They are asked for
-  // as soon as the head before has used its own.
-  Frag<uint16_t> Ah[VU], Al[VU];
+  // This wavefront's state rows (values 8 g .. of every k-unit, as in wide_frag's
+  // operands), S for dQ, X for dK, and a head's gates.  They are asked for as soon as
+  // the head before has used its own.
+  f32x4 A[VU][2];
   auto fetch_state = [&](int hh) {
     const int64_t slot = (bb * b.H + hk * r + hh) * NC + n;
     const int ln = lane_now();
     const int64_t row = ((slot * VU) * DK + 16 * dt + (ln & 15)) * 32 + 8 * (ln >> 4);
-    const uint16_t* h0 = (is_q ? st.sh : st.xh) + row;
-    const uint16_t* l0 = (is_q ? st.sl : st.xl) + row;
+    const float* const src = (is_q ? st.s : st.x) + row;
 #pragma unroll
-    for (int ku = 0; ku < VU; ++ku) {
-      Ah[ku].v = *reinterpret_cast<const bf16x8*>(h0 + ku * DK * 32);
-      Al[ku].v = *reinterpret_cast<const bf16x8*>(l0 + ku * DK * 32);
-    }
+    for (int ku = 0; ku < VU; ++ku)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) A[ku][e] = *reinterpret_cast<const f32x4*>(src + ku * DK * 32 + 4 * e);
     if (w == 14) {
       const ChunkGates& src = st.gates[slot];
       ChunkGates& gt = gates[hh & 1];
@@ -463,8 +460,7 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       const f32x4 ch = *reinterpret_cast<const f32x4*>(gt.hi + 16 * ct + 4 * g);
       const f32x4 cl = *reinterpret_cast<const f32x4*>(gt.lo + 16 * ct + 4 * g);
       const f32x4 D = *reinterpret_cast<const f32x4*>(gt.D + 16 * ct + 4 * g);
-      f32x4 p, d;
-      float rs = 0.0f;
+      f32x4 p, d, md;
 #pragma unroll
       for (int qq = 0; qq < 4; ++qq) {
         const bool in = ct < rt || 4 * g + qq <= li;
@@ -472,12 +468,17 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
         const float m = in ? dp[qq] * (raw[qq] * f) : 0.0f;
         p[qq] = in ? raw[qq] * f * D[qq] : 0.0f;
         d[qq] = in ? dp[qq] * f * D[qq] : 0.0f;
-        rs = fmaf(m, D[qq], rs);
+        md[qq] = m * D[qq];
         const float cs = row_sum16(m);
         if (li == 0) sums.col[tile][4 * g + qq] = cs;
       }
-      rs = row_sum4(rs);
-      if (g == 0) sums.row[tile][li] = rs;
+      if (rt == ct) {
+        const f32x4 own = tile_between(md, li, g);
+        if (li == 0) *reinterpret_cast<f32x4*>(sums.row[tile] + 4 * g) = own;
+      } else {
+        const float rs = row_sum4((md[0] + md[1]) + (md[2] + md[3]));
+        if (g == 0) sums.row[tile][li] = rs;
+      }
       st4(Pm + (tile * 16 + li) * 16 + 4 * g, p);
       st4(Dm + (tile * 16 + li) * 16 + 4 * g, d);
     }
@@ -485,7 +486,8 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
       const int ln = lane_now();
 #pragma unroll
       for (int ku = 0; ku < VU; ++ku)
-        *reinterpret_cast<bf16x8*>(Xs + swzw_off<DV>(16 * dt + (ln & 15), 32 * ku + 8 * (ln >> 4))) = Ah[ku].v;
+        *reinterpret_cast<bf16x8*>(Xs + swzw_off<DV>(16 * dt + (ln & 15), 32 * ku + 8 * (ln >> 4))) =
+            acc_frag<uint16_t>(A[ku][0], A[ku][1]).v;
     }
     __builtin_amdgcn_sched_barrier(0);
     // v . dO of this chunk, and <X, S>: half of the value columns of both by the
@@ -496,16 +498,16 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
     if (ktok == 0) {
       const int ln = lane_now();
       const int64_t srow = sbase + (ln & 15) * 32 + 8 * (ln >> 4);
-      const uint16_t* h0 = (is_q ? st.xh : st.sh) + srow;
-      const uint16_t* l0 = (is_q ? st.xl : st.sl) + srow;
+      const float* const other = (is_q ? st.x : st.s) + srow;
 #pragma unroll
       for (int ku = 0; ku < VU; ++ku) {
         if (VU > 1 ? (ku < VU / 2) != is_q : !is_q) continue;
-        const u32x4 bh = *reinterpret_cast<const u32x4*>(h0 + ku * DK * 32), bl = *reinterpret_cast<const u32x4*>(l0 + ku * DK * 32);
-        const u32x4 ah = __builtin_bit_cast(u32x4, Ah[ku].v), al = __builtin_bit_cast(u32x4, Al[ku].v);
-        dot = dot8(al, bh, dot);  // the product of the two low parts is 2^-18 of the whole, dropped
-        dot = dot8(ah, bl, dot);
-        dot = dot8(ah, bh, dot);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const f32x4 y = *reinterpret_cast<const f32x4*>(other + ku * DK * 32 + 4 * e);
+#pragma unroll
+          for (int qq = 0; qq < 4; ++qq) dot = fmaf(A[ku][e][qq], y[qq], dot);
+        }
       }
     }
     skips = row_sum4(row_sum16(skips));
@@ -526,17 +528,24 @@ __global__ __launch_bounds__((SsmGradShape<DK, DV>::THREADS)) void ssm_grad_kern
 #pragma unroll
       for (int ku = 0; ku < 2; ++ku) T[ku] = sw_frag_tr_wide<DK>(Q ? Ks : Qs, 16 * dt, ku, ln);
       const float hi_end = gt.hi[63], lo_end = gt.lo[63];
+      f32x4 xs[KTOK];
+#pragma unroll
+      for (int tt = 0; tt < KTOK; ++tt) xs[tt] = zero4();
+#pragma unroll
+      for (int ku = 0; ku < VU; ++ku) {  // the state in three parts: r and p go into sums that cancel
+        Frag<uint16_t> p[3];
+        split3_frag(A[ku][0], A[ku][1], p);
+#pragma unroll
+        for (int tt = 0; tt < KTOK; ++tt) {
+          const Frag<uint16_t> f = wide_frag<DV>(rows, 16 * (ktok + tt) + li, ku, g);
+#pragma unroll
+          for (int i = 2; i >= 0; --i) mma(xs[tt], p[i], f);
+        }
+      }
 #pragma unroll
       for (int tt = 0; tt < KTOK; ++tt) {
         const int t = ktok + tt, j = 16 * t + li;
-        f32x4 x = zero4(), y = zero4();
-#pragma unroll
-        for (int ku = 0; ku < VU; ++ku) {
-          const Frag<uint16_t> f = wide_frag<DV>(rows, j, ku, g);
-          mma(y, Al[ku], f);
-          mma(x, Ah[ku], f);
-        }
-        x = (Q ? gt.e[j] : __builtin_amdgcn_exp2f((hi_end - gt.hi[j]) + (lo_end - gt.lo[j]))) * (x + y);
+        f32x4 x = (Q ? gt.e[j] : __builtin_amdgcn_exp2f((hi_end - gt.hi[j]) + (lo_end - gt.lo[j]))) * xs[tt];
         const bf16x4 o = *reinterpret_cast<const bf16x4*>(mine + swzw_off<DK>(j, 16 * dt + 4 * g));
         float sum = 0.0f;
 #pragma unroll
@@ -607,13 +616,18 @@ __global__ __launch_bounds__(kThreads) void ssm_steps_kernel(SsmBwd b, SsmStates
   const bool real = t < b.L;
   const ChunkSums& s = st.sums[slot];
   const ChunkGates& gt = st.gates[slot];
-  float ri = 0.0f, ci = 0.0f, rr = 0.0f, pj = 0.0f;
+  // of M: t's own tile; rows and columns of the tiles left of it and below it; the tiles
+  // between them; all columns by D
+  float own = s.row[tri_at(lt, lt)][i], ri = 0.0f, cb = 0.0f, mid = 0.0f, ci = s.col[tri_at(lt, lt)][i], rr = 0.0f, pj = 0.0f;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    const float x = s.row[tri_at(lt, c <= lt ? c : lt)][i], y = s.col[tri_at(c >= lt ? c : lt, lt)][i];
-    ri += c <= lt ? x : 0.0f;
-    ci += c >= lt ? y : 0.0f;
+    if (c < lt) ri += s.row[tri_at(lt, c)][i];
+    if (c > lt) cb += s.col[tri_at(c, lt)][i];
+#pragma unroll
+    for (int r = c + 2; r < 4; ++r)
+      if (c < lt && lt < r) mid += s.row[tri_at(r, c)][i];
   }
+  ci += cb;
 #pragma unroll
   for (int x = 0; x < 8; ++x) {
     if (x >= DT) break;
@@ -629,15 +643,16 @@ __global__ __launch_bounds__(kThreads) void ssm_steps_kernel(SsmBwd b, SsmStates
     xs += __shfl_xor(xs, off);
     vo += __shfl_xor(vo, off);
   }
-  float suf = real ? ri - D * ci + rr : 0.0f, pre = real ? D * pj : 0.0f;
-  const float own = pre;
+  own += row_suffix16(ri, i) + row_before16(D * cb, i) + row_sum16(mid);
+  float suf = real ? rr : 0.0f, pre = real ? D * pj : 0.0f;
+  const float last = pre;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
     const float y = __shfl_down(suf, d), z = __shfl_up(pre, d);
     if (l + d < kWave) suf += y;
     if (l >= d) pre += z;
   }
-  const float gd = suf + (pre - own) + gt.e[63] * xs;
+  const float gd = own + (suf + (pre - last) + gt.e[63] * xs);
   const float ddt = real ? (ci + pj + rate * gd) * (1.0f / (1.0f + expf(-x))) : 0.0f;
   if (real) static_cast<uint16_t*>(b.ddt)[tok * b.ddt_row + h] = from_f32<uint16_t>(ddt);
   float sa = real ? D * gd : 0.0f, sb = ddt;

@@ -8,13 +8,13 @@ namespace efla {
 namespace {
 
 struct Layout {
-  size_t state, gates, sums, part, total;  // bytes of one of the four state arrays; offsets behind them
+  size_t state, gates, sums, part, total;  // bytes of one of the two state arrays; offsets behind them
 };
 Layout layout(int B, int H, int64_t L, int DK, int DV) {
   const size_t slots = size_t(B) * H * size_t((L + 63) / 64);
   Layout w{};
-  w.state = slots * DK * DV * 2;
-  w.gates = 4 * w.state;
+  w.state = slots * DK * DV * sizeof(float);
+  w.gates = 2 * w.state;
   w.sums = w.gates + slots * sizeof(ChunkGates);
   w.part = w.sums + slots * sizeof(ChunkSums);
   w.total = w.part + slots * 3 * sizeof(float);
@@ -25,8 +25,7 @@ template <int DK>
 hipError_t bwd_impl(const SsmBwd& b, void* ws, hipStream_t s) {
   const Layout w = layout(b.B, b.H, b.L, DK, b.DV);
   auto* at = static_cast<unsigned char*>(ws);
-  auto arr = [&](int i) { return reinterpret_cast<uint16_t*>(at + i * w.state); };
-  const SsmStates st{arr(0), arr(1), arr(2), arr(3), reinterpret_cast<ChunkGates*>(at + w.gates),
+  const SsmStates st{reinterpret_cast<float*>(at), reinterpret_cast<float*>(at + w.state), reinterpret_cast<ChunkGates*>(at + w.gates),
                      reinterpret_cast<ChunkSums*>(at + w.sums)};
   float* part = reinterpret_cast<float*>(at + w.part);
   const int NC = int((b.L + 63) / 64), NVB = b.DV / 32, half = b.B * b.H * NVB;

@@ -53,14 +53,6 @@ __device__ __forceinline__ void split3_frag(const f32x4& lo4, const f32x4& hi4, 
   for (int i = 0; i < 3; ++i) p[i].v = __builtin_bit_cast(bf16x8, part[i]);
 }
 
-// As a sum of two.
-__device__ __forceinline__ void split_parts(const f32x4& lo4, const f32x4& hi4, Frag<uint16_t>& hi, Frag<uint16_t>& lo) {
-  Frag<uint16_t> p[3];
-  split3_frag(lo4, hi4, p);
-  hi = p[0];
-  lo = p[1];
-}
-
 // (Sequence, head) and value block of workgroup x.  remap > 0: all value blocks of
 // `remap` adjacent heads on one XCD (same x % 8), whose L2 then serves what they
 // share; the (sequence, head)s are a multiple of 8 remap.

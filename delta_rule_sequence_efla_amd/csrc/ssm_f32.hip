@@ -259,7 +259,9 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
   constexpr int KOWN = cdiv(2 * DT, 4), VOWN = cdiv(2 * VT, 4);  // tiles (token half, column tile) a wavefront
   __shared__ __align__(16) float Qs[kC][KP], Ks[kC][KP], Vs[kC][VP], Os[kC][VP];
   __shared__ __align__(16) float Pm[kC][PP], Dm[kC][PP];  // e^{G_i - G_j} times q_i . k_j and dO_i . v_j
-  __shared__ float rowM[3][16], colM[3][16], rin[4][kC], pin[4][kC], red[3][4];
+  // rowM: of the diagonal tiles what tile_between has
+  __shared__ __align__(16) float rowM[3][16];
+  __shared__ float colM[3][16], rin[4][kC], pin[4][kC], red[3][4];
   __shared__ Gates gt;
 
   const int r = b.H / b.Hk;
@@ -342,6 +344,7 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
         mma(p, lds_frag(Os[0], VP, 16 * it + li, ku, g), lds_frag(Vs[0], VP, 16 * jt + li, ku, g));
       const int j = 16 * jt + li;
       float col = 0.0f;
+      f32x4 md;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 16 * it + 4 * g + e;
@@ -351,9 +354,15 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
         Dm[i][j] = p[e];
         const float m = i >= j ? p[e] * raw[e] : 0.0f;
         col += m;
-        const float rs = row_sum16(m * gt.D[j]);
-        if (li == 0) rowM[w][4 * g + e] = rs;
+        md[e] = m * gt.D[j];
       }
+      if (it == jt) {
+        md = tile_between_tr(md, li, g);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) md[e] = row_sum16(md[e]);
+      }
+      if (li == 0) st4(&rowM[w][4 * g], md);
       col = row_sum4(col);
       if (g == 0) colM[w][li] = col;
     }
@@ -444,11 +453,13 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
       const bool real = lane < valid;
       const int l = lane < kC ? lane : kC - 1, half = l >> 4, i = l & 15;
       // tiles: 0 (0, 0), 1 (1, 0), 2 (1, 1)
-      float ri = half ? rowM[1][i] + rowM[2][i] : rowM[0][i], ci = half ? colM[2][i] : colM[0][i] + colM[1][i];
+      const float ci = !real ? 0.0f : half ? colM[2][i] : colM[0][i] + colM[1][i];
       float rr = rin[0][l] + rin[1][l] + rin[2][l] + rin[3][l], pp = pin[0][l] + pin[1][l] + pin[2][l] + pin[3][l];
-      if (!real) ri = ci = rr = pp = 0.0f;
+      if (!real) rr = pp = 0.0f;
       const float D = gt.D[l];
-      float suf = ri - D * ci + rr, pre = D * pp;  // to be summed over i >= t, and over j < t
+      const float left = row_suffix16(rowM[1][i], i), below = row_before16(D * colM[1][i], i);
+      const float own = half ? rowM[2][i] + left : rowM[0][i] + below;
+      float suf = rr, pre = D * pp;  // to be summed over i >= t, and over j < t
 #pragma unroll
       for (int d = 1; d < kC; d <<= 1) {
         const float y = __shfl_down(suf, d), z = __shfl_up(pre, d);
@@ -456,7 +467,7 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
         if (lane >= d) pre += z;
       }
       const float xs = gt.e[kC - 1] * (red[1][0] + red[1][1] + red[1][2] + red[1][3]);
-      const float gd = suf + (pre - D * pp) + xs;
+      const float gd = own + (suf + (pre - D * pp) + xs);
       const float dD = ci + pp + rate * gd;
       float raw_dt = b.bias != nullptr ? b.bias[h] : 0.0f;
       if (real) raw_dt += to_f32(static_cast<const T*>(b.dt)[(tok + lane) * b.dt_row + h]);

@@ -533,10 +533,9 @@ efla_status efla_conv_bwd(const void *x, int64_t x_row, const void *w, const voi
  *   - A decay below e^{-128} is zero in float32, and so it acts.  A token's step
  *     size may be zero (dt of -inf): it leaves the state as it was.
  *   - States are carried in float32.  For bf16 inputs, matrix-core products that
- *     feed the forward's state take each float32 operand as the sum of three bf16
- *     values (24 significant bits); those that feed a float32 gradient, as the sum
- *     of two (16 bits), so da, dd, dbias and ds0 are good to about 1e-5; products
- *     that only feed bf16 outputs round such operands once.
+ *     feed a state or a float32 gradient take each float32 operand as the sum of
+ *     three bf16 values (24 significant bits); products that only feed bf16 outputs
+ *     round such operands once.
  *   - A NaN or an infinity in a token's row reaches its sequence's outputs from
  *     the start of its chunk of 64 tokens on, not only from the token on; never
  *     another sequence's.
@@ -594,10 +593,10 @@ efla_status efla_ssm_bwd(const void *q, int64_t q_row, const void *k, int64_t k_
  * efla_pool_copy -- row src[i] of every pool to its row dst[i], i < N (int32,
  *     DEVICE memory): src[i] outside [0, P) clears row dst[i] to zero bytes, dst[i]
  *     outside [0, P) does nothing.  A source may be named often (a request forked
- *     into several: in lists of up to 512 entries it is read once).  The entries cannot be checked here: a row
- *     that is the destination of two entries, or a destination and a source, holds
- *     unspecified bytes afterwards, as does what is copied from it; no access
- *     leaves the pools.
+ *     into several: in lists of up to 512 entries it is read once).  The entries
+ *     cannot be checked here: a row that is the destination of two entries, or a
+ *     destination and a source, holds unspecified bytes afterwards, as does what is
+ *     copied from it; no access leaves the pools.
  * efla_pool_compact -- with K distinct rows in [0, P) named by slots [N] (int32,
  *     DEVICE memory), moves those at K or above, in ascending order, into the rows
  *     below K that slots does not name, in ascending order, so that rows 0 .. K-1

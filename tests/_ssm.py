@@ -189,3 +189,19 @@ def in_wider_rows(t, lead, extra, gen=None):
     rows = torch.full((*t.shape[:lead], flat.shape[-1] + extra), float("nan"), dtype=t.dtype, device=t.device)
     rows[..., :flat.shape[-1]] = flat
     return rows[..., :flat.shape[-1]].unflatten(-1, t.shape[lead:])
+
+
+def rate_gradient_ref(x, d_o):
+    """da of a scan from no state in float64, and the root of the summed squares of the terms that its rounding errors
+    scale: over all pairs i > j of every head, with T_ij = (dO_i . v_j) (q_i . k_j) e^{G_i - G_j} D_j,
+    (D_{j+1} + .. + D_i) T_ij, the dot product dO_i . v_j by the norm of its terms."""
+    q, k, v, dt, a, d, bias, _ = wide(x)
+    r = v.shape[2] // k.shape[2]
+    q, k = (t.repeat_interleave(r, 2).transpose(1, 2) for t in (q, k))  # [B, H, L, *]
+    v, w = v.transpose(1, 2), d_o.double().transpose(1, 2)
+    D = softplus(dt + (0 if bias is None else bias)).transpose(1, 2)
+    C = D.cumsum(-1)
+    apart = (C[..., :, None] - C[..., None, :]).tril(-1)
+    f = torch.exp(a[:, None, None] * apart).tril(-1) * D[..., None, :] * (q @ k.transpose(-1, -2)) * apart
+    da = (f * (w @ v.transpose(-1, -2))).sum((0, 2, 3))
+    return da, (f * f * ((w * w) @ (v * v).transpose(-1, -2))).sum((0, 2, 3)).sqrt()

@@ -221,6 +221,23 @@ def test_gradient_of_shared_heads(dtype, H, Hk):
         assert all(torch.equal(p, r) for p, r in zip(got, again))
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("L", [16, 64, 100, 300])
+@pytest.mark.parametrize("rate", [-16.0, -1.0])
+def test_rate_gradient_of_neighbours(dtype, L, rate):
+    """Of a head that forgets within a few tokens only near pairs carry da; the errors of the others' products, which
+    cancel on each side of a token, may not.  A term has the roundings of two products over 64 and the factors,
+    sqrt(64) + 8 half steps; states and their gradients another 3 parts' worth, the same again."""
+    x = dev(R.make_scan(2, L, 8, 2, 64, 64, dtype, seed=L, s0=False, steps=(0.05, 0.1)))
+    x["q"], x["k"] = x["q"].abs(), x["k"].abs()
+    x["a"].fill_(rate)
+    a, kw = ins(x)
+    d_o = torch.randn(2, L, 8, 64, generator=torch.Generator().manual_seed(L)).to(dtype).cuda()
+    da = efla.efla_ssm_bwd(*a, d_o, **kw)[4].double().cpu()
+    want, scale = R.rate_gradient_ref({n: None if t is None else t.cpu() for n, t in x.items()}, d_o.cpu())
+    assert bool(((da - want).abs() <= 32 * 2.0 ** -24 * scale).all()), ((da - want) / scale * 2.0 ** 24).tolist()
+
+
 def test_gradient_against_differences():
     x = R.make_scan(1, 40, 2, 1, 16, 16, F32)
     gen = torch.Generator().manual_seed(3)
