@@ -6,8 +6,8 @@
 // them alone (P, dP and the gradient of the state where it meets a key) once.  The gradients
 // of the decays are sums of products r, p and M (ssm.h) over all tokens, which
 // end in float32: M comes from exact products in float32, and in r and p the
-// states go in as two bf16 parts (16 bits); so do the float32 operands that feed a
-// state.
+// states go in as three bf16 parts (24 bits); so do the float32 operands that feed
+// a state.
 #pragma once
 
 #include <type_traits>

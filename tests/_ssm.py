@@ -18,12 +18,11 @@ the state's norm (decays <= 1 do not expand it); 4 times that is allowed, 16 for
 gradients, whose sums run over d_v and the chunk as well.
 
 Scan, bf16.  o: P, the state as an operand and o itself, three roundings of 2^-8.
-States and ds0: each float32 operand as two bf16 parts, off by 2^-16 at most, once
-a chunk, independent from chunk to chunk.  dq, dk, dv: the longest path rounds the
-state (or its gradient) or P (or dP), and the result: three.  ddt: inputs as two
-parts or exact, then one rounding of the result; its sum of decay terms cancels,
-which the float32 factor covers.  da, dbias, dd: sums over all tokens of float32
-terms good to 2^-16 per operand, held to the sum of the terms' absolute values.
+States and ds0: each float32 operand as three bf16 parts, off by 2^-24, which the
+float32 bound covers.  dq, dk, dv: the longest path rounds the
+state (or its gradient) or P (or dP), and the result: three.  ddt: one rounding of
+the result.  da, dbias, dd: sums over all tokens of float32
+terms, held to the sum of the terms' absolute values.
 """
 import math
 
@@ -52,23 +51,17 @@ def tol32(L, dk, what="out"):
     return {"out": 4, "grad": 16}[what] * 2.0 ** -24 * math.sqrt(max(L, 1) * (dk + 8))
 
 
-def _parts(L):
-    return 4 * 2.0 ** -16 * math.sqrt(max(1, -(-L // 64)))
-
-
 def tol_o(dtype, L, dk):
     return tol32(L, dk) + (3 * 2.0 ** -8 if dtype == BF else 0.0)
 
 
 def tol_s(dtype, L, dk):
-    return tol32(L, dk) + (_parts(L) if dtype == BF else 0.0)
+    return tol32(L, dk)
 
 
 def tol_grad(dtype, L, dk, name):
-    t = tol32(L, dk, "grad")
-    if dtype == F32:
-        return t
-    return t + {"dq": 3 * 2.0 ** -8, "dk": 3 * 2.0 ** -8, "dv": 3 * 2.0 ** -8, "ddt": 2.0 ** -8 + 4 * _parts(L)}.get(name, 4 * _parts(L))
+    rounded = {"dq": 3 * 2.0 ** -8, "dk": 3 * 2.0 ** -8, "dv": 3 * 2.0 ** -8, "ddt": 2.0 ** -8}
+    return tol32(L, dk, "grad") + (rounded.get(name, 0.0) if dtype == BF else 0.0)
 
 
 def softplus(x):
