@@ -538,7 +538,8 @@ efla_status efla_conv_bwd(const void *x, int64_t x_row, const void *w, const voi
  *     round such operands once.
  *   - A NaN or an infinity in a token's row reaches its sequence's outputs from
  *     the start of its chunk of 64 tokens on, not only from the token on; never
- *     another sequence's.
+ *     another sequence's.  In the gradients it reaches its whole sequence, and da,
+ *     dd and dbias of its heads.
  *   - A call whose largest launch would have 2^32 threads or more is
  *     EFLA_ERR_UNSUPPORTED.
  *   - The forward needs a workspace where it cuts few, long sequences into segments
