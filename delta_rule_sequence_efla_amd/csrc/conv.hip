@@ -489,13 +489,16 @@ int64_t conv_threads(int64_t seqs, int64_t L, int64_t N, int D) {
   return ((N * blocks + 3) / 4 + seqs * ((L + 4 * run - 1) / (4 * run)) * blocks) * kThreads;
 }
 
+int64_t conv_copy_threads(int64_t B, int D, int W) {
+  return (B * (W - 1) * D + kThreads - 1) / kThreads * kThreads;
+}
+
 template <typename T>
 hipError_t launch_conv_bwd(const ConvBwd& a, float* part, hipStream_t s) {
   if (a.L == 0) {
     if (a.ds0 != nullptr) {
-      const int64_t n = int64_t(a.B) * (a.W - 1) * a.D;
-      hipLaunchKernelGGL((conv_copy_kernel<T>), dim3(unsigned((n + kThreads - 1) / kThreads)), dim3(kThreads), 0, s,
-                         static_cast<const T*>(a.dsf), static_cast<T*>(a.ds0), n);
+      hipLaunchKernelGGL((conv_copy_kernel<T>), dim3(unsigned(conv_copy_threads(a.B, a.D, a.W) / kThreads)), dim3(kThreads), 0,
+                         s, static_cast<const T*>(a.dsf), static_cast<T*>(a.ds0), int64_t(a.B) * (a.W - 1) * a.D);
     }
   } else {
     const bool aligned = conv_rows_aligned({a.x, a.w, a.bias, a.s0, a.dy, a.dsf, a.dx, a.ds0},

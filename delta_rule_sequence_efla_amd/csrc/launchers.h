@@ -256,6 +256,8 @@ size_t conv_bwd_workspace(int B, int64_t L, int D, int W);
 // Threads of the largest launch over `seqs` dense sequences of L tokens (a packed
 // batch: one of T) and N states.
 int64_t conv_threads(int64_t seqs, int64_t L, int64_t N, int D);
+// Threads of the copy of ds_final that sequences without tokens take.
+int64_t conv_copy_threads(int64_t B, int D, int W);
 
 // Moves of state-pool rows (pool.hip).
 constexpr int kPoolsPerLaunch = 64;

@@ -201,6 +201,7 @@ efla_status efla_conv_bwd(const void* x, int64_t x_row, const void* w, const voi
   if (st != EFLA_OK) return st;
   if (B < 1) return EFLA_ERR_INVALID_ARG;
   if (!conv_fits(B, L, B, D)) return EFLA_ERR_UNSUPPORTED;
+  if (L == 0 && ds0 != nullptr && efla::conv_copy_threads(B, D, W) > efla::kMaxLaunchThreads) return EFLA_ERR_UNSUPPORTED;
   if (dw == nullptr || (L > 0 && !all_given({x, w, dy, dx}))) return EFLA_ERR_INVALID_ARG;
   if (!conv_aligned(dtype, {x, w, bias, s0, dy, ds_final, dx, ds0}) || !aligned_to(dw, 4) || !aligned_to(dbias, 4))
     return EFLA_ERR_INVALID_ARG;
