@@ -48,6 +48,25 @@ bool conv_fits(int64_t seqs, int64_t L, int64_t N, int D) {
          efla::conv_threads(seqs, L, N, D) <= efla::kMaxLaunchThreads;
 }
 
+// Whether an output written row by row, width bytes every out_row, shares a byte with
+// rows of an input that other wavefronts still read.  Rows of one length may lie side
+// by side in a wider tensor's; of two lengths only disjoint stretches are told apart,
+// and the rest is the caller's to keep.
+bool rows_meet(const void* out, int64_t out_row, const void* in, int64_t in_row, int64_t rows, int64_t width) {
+  if (out == nullptr || in == nullptr || rows == 0) return false;
+  const auto x = reinterpret_cast<uintptr_t>(out), y = reinterpret_cast<uintptr_t>(in);
+  if (y < x ? x - y >= uint64_t((rows - 1) * in_row + width) : y - x >= uint64_t((rows - 1) * out_row + width)) return false;
+  if (rows == 1) return true;
+  if (out_row != in_row) return false;
+  const int64_t by = int64_t(y < x ? x - y : y - x) % out_row;  // of one row of the later from the one before it
+  return by < width || out_row - by < width;
+}
+
+bool conv_meet(efla_dtype dt, const void* out, int64_t out_row, const void* in, int64_t in_row, int64_t rows, int64_t D) {
+  const auto e = int64_t(elem_bytes(dt));
+  return rows_meet(out, out_row * e, in, in_row * e, rows, D * e);
+}
+
 // ---------------------------------------------------------------- scan
 // Shapes of a scan over `seqs` sequences (dense: of L tokens each; packed: L in all).
 efla_status check_ssm(int64_t seqs, int H, int Hk, int64_t L, int d_k, int d_v, efla_dtype dt) {
@@ -154,6 +173,7 @@ efla_status efla_conv_fwd(const void* x, int64_t x_row, const void* w, const voi
   if (!conv_fits(B, L, B, D)) return EFLA_ERR_UNSUPPORTED;
   if (L > 0 && !all_given({x, w, y})) return EFLA_ERR_INVALID_ARG;
   if (!conv_aligned(dtype, {x, w, bias, s0, y, s_final})) return EFLA_ERR_INVALID_ARG;
+  if (conv_meet(dtype, y, y_row, x, x_row, B * L, D)) return EFLA_ERR_INVALID_ARG;
   if (L == 0 && s_final == nullptr) return EFLA_OK;
   const efla::ConvFwd a{x, w, bias, s0, y, s_final, nullptr, nullptr, x_row, y_row, B, B, D, W, silu, L};
   return by_type(dtype, [&](auto t) { return efla::launch_conv_fwd<decltype(t)>(a, static_cast<hipStream_t>(stream)); });
@@ -170,6 +190,7 @@ efla_status efla_conv_fwd_varlen(const void* x, int64_t x_row, const void* w, co
   if (N == 0) return EFLA_OK;
   if (cu_seqlens == nullptr || (T > 0 && !all_given({x, w, y}))) return EFLA_ERR_INVALID_ARG;
   if (!conv_aligned(dtype, {x, w, bias, s0, y, s_final})) return EFLA_ERR_INVALID_ARG;
+  if (conv_meet(dtype, y, y_row, x, x_row, T, D)) return EFLA_ERR_INVALID_ARG;
   if (T == 0 && s_final == nullptr) return EFLA_OK;
   const efla::ConvFwd a{x, w, bias, s0, y, s_final, cu_seqlens, slots, x_row, y_row, N, P, D, W, silu, T};
   return by_type(dtype, [&](auto t) { return efla::launch_conv_fwd<decltype(t)>(a, static_cast<hipStream_t>(stream)); });
@@ -208,6 +229,10 @@ efla_status efla_conv_bwd(const void* x, int64_t x_row, const void* w, const voi
   const size_t need = efla_conv_bwd_workspace_size(B, L, D, W);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EFLA_ERR_WORKSPACE;
   if (need > 0 && !aligned16(workspace)) return EFLA_ERR_INVALID_ARG;
+  const int64_t states = int64_t(W - 1) * D;
+  if (conv_meet(dtype, dx, dx_row, x, x_row, B * L, D) || conv_meet(dtype, dx, dx_row, dy, dy_row, B * L, D) ||
+      (L > 0 && (conv_meet(dtype, ds0, states, ds_final, states, B, states) || conv_meet(dtype, ds0, states, s0, states, B, states))))
+    return EFLA_ERR_INVALID_ARG;
   const efla::ConvBwd a{x, w, bias, s0, dy, ds_final, dx, ds0, dw, dbias, x_row, dy_row, dx_row, B, D, W, silu, L};
   return by_type(dtype, [&](auto t) {
     return efla::launch_conv_bwd<decltype(t)>(a, static_cast<float*>(workspace), static_cast<hipStream_t>(stream));

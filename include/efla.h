@@ -473,8 +473,11 @@ efla_status efla_pack_plan(const int32_t *lengths, const int32_t *starts, int N,
  *     bias [D] (nullable) in dtype.
  *   - A state is the last W - 1 inputs, [W - 1, D] in dtype, oldest first.  s0
  *     and s_final hold one for each sequence (NULL: zeros, and not written) or,
- *     with slots, are pools of P of them, as in efla_gated_chunk_fwd_varlen;
- *     s_final may be s0.  y may not overlap x or a state.
+ *     with slots, are pools of P of them, as in efla_gated_chunk_fwd_varlen.
+ *   - Outputs may not overlap inputs, for other wavefronts still read them, but that
+ *     s_final may be s0, and y of efla_conv_step may be x.  Rows of one length that do
+ *     (y over x, dx over x or dy), and ds0 over ds_final or s0, are
+ *     EFLA_ERR_INVALID_ARG; rows that lie side by side in a wider tensor's do not.
  *   - Arithmetic is float32, rounded once.  Where every tensor and row starts on
  *     16 bytes (D and the row lengths a multiple of 8 in bf16, of 4 in float32)
  *     memory moves in 16-byte pieces, else in single elements, several times
