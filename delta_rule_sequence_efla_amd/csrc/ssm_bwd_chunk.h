@@ -645,14 +645,15 @@ __global__ __launch_bounds__(kThreads) void ssm_steps_kernel(SsmBwd b, SsmStates
   }
   own += row_suffix16(ri, i) + row_before16(D * cb, i) + row_sum16(mid);
   float suf = real ? rr : 0.0f, pre = real ? D * pj : 0.0f;
-  const float last = pre;
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
     const float y = __shfl_down(suf, d), z = __shfl_up(pre, d);
     if (l + d < kWave) suf += y;
     if (l >= d) pre += z;
   }
-  const float gd = own + (suf + (pre - last) + gt.e[63] * xs);
+  // the lane before's, not the lane's own less its term: a large last one would round the others away
+  const float before = __shfl_up(pre, 1);
+  const float gd = own + (suf + (l > 0 ? before : 0.0f) + gt.e[63] * xs);
   const float ddt = real ? (ci + pj + rate * gd) * (1.0f / (1.0f + expf(-x))) : 0.0f;
   if (real) static_cast<uint16_t*>(b.ddt)[tok * b.ddt_row + h] = from_f32<uint16_t>(ddt);
   float sa = real ? D * gd : 0.0f, sb = ddt;

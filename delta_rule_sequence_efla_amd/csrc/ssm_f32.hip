@@ -467,7 +467,8 @@ __global__ __launch_bounds__(kThreads) void ssm_bwd_f32_kernel(SsmBwd b, const f
         if (lane >= d) pre += z;
       }
       const float xs = gt.e[kC - 1] * (red[1][0] + red[1][1] + red[1][2] + red[1][3]);
-      const float gd = own + (suf + (pre - D * pp) + xs);
+      const float before = __shfl_up(pre, 1);  // not pre less its own term, which may be far larger than the others
+      const float gd = own + (suf + (lane > 0 ? before : 0.0f) + xs);
       const float dD = ci + pp + rate * gd;
       float raw_dt = b.bias != nullptr ? b.bias[h] : 0.0f;
       if (real) raw_dt += to_f32(static_cast<const T*>(b.dt)[(tok + lane) * b.dt_row + h]);
