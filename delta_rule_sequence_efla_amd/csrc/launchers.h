@@ -269,7 +269,7 @@ struct PoolSet {
 };
 int64_t pool_pieces(uint64_t row_bytes);
 // Row i: pool row src[i] (outside [0, P): zeros) to dst[i] (outside: nothing);
-// share: rows with one source are served by one read (lists of up to 512).
+// share: rows with one source may be served by one read (pool.hip has the rule).
 hipError_t launch_pool_copy(const PoolSet& set, const int32_t* src, const int32_t* dst, int N, int P, bool share,
                             hipStream_t s);
 constexpr int kMaxCompactRows = 1 << 17;  // a bit and a count a row in the LDS

@@ -9,22 +9,37 @@ namespace efla {
 
 constexpr int kPieceVecs = 8;                              // 16-byte vectors a thread
 constexpr int kPieceBytes = kThreads * kPieceVecs * 16;    // of a row, a workgroup
-// Entries up to which a shared source is looked for: every workgroup runs over the
-// list.  us without / with it, rows of 1 MiB each copied to 1, 2 or 8 others:
-//   64 entries  25 / 26, 18 / 17, 17 / 15     256  98 / 108, 83 / 76, 88 / 51
-//   512  187 / 220, 159 / 154, 174 / 113      1024 of 512 KiB  183 / 313, 159 / 273, 183 / 179
-//   8192 of 64 KiB  181 / 1395, 166 / 1425, 181 / 1475
+// Whether entries that name one source share a read of it.  A workgroup that reads for
+// others saves reads from memory and makes their writes wait for one another, and
+// every one runs over the list.  us without / with it, rows copied to 1, 2, 8, 32 or
+// 500 others (500: to all of a list of 500), from 32 MiB written and up to 512 entries:
+//   500 x 4 KiB (below it)   3.5 / 5.2, 3.6 / 5.2, 3.6 / 6.5, 3.6 / 10, 3.5 / 16
+//   500 x 64 KiB (below it)  14 / 16.5, 14 / 12.4, 11 / 11.8, 10 / 18, 10 / 33
+//   64 x 1 MiB   25 / 25.5, 25 / 19, 15.7 / 15.4, 15.5 / 16.1
+//   256 x 1 MiB  103 / 111, 87 / 85, 82 / 53, 45 / 49
+//   500 x 1 MiB  201 / 220, 201 / 171, 167 / 129, 129 / 115, 120 / 107
+//   1024 x 512 KiB (above)  183 / 313, 159 / 273, 183 / 179;  8192 x 64 KiB  181 / 1395, 166 / 1425, 181 / 1475
+constexpr uint64_t kMinShareBytes = uint64_t(32) << 20;
 constexpr int kMaxShare = 512;
+// Destinations a workgroup writes, of those in 64 entries: with all of them one piece of
+// a row that goes to 500 was 500 writes one after the other (500 x 64 KiB: 132 us).
+constexpr int kShared = 8;
+
+// The lowest n of the bits set in m.
+__device__ __forceinline__ uint64_t lowest(uint64_t m, int n) {
+  while (__popcll(m) > n) m &= ~(uint64_t(1) << (63 - __builtin_clzll(m)));
+  return m;
+}
 
 int64_t pool_pieces(uint64_t row_bytes) { return int64_t((row_bytes + kPieceBytes - 1) / kPieceBytes); }
 
-// One workgroup moves one 32 KiB piece of one row.  With `share`, the first of
-// the rows that name one source reads it once and writes it to all their
-// destinations, and the others' workgroups have nothing to do: a fork into eight
-// costs nine row moves, not sixteen.
+// One workgroup moves one 32 KiB piece of one row, entry i's.  With `share` it writes the
+// piece to the destinations of the first `served` entries with the same source in
+// every 64 from i + 1 on, up to `end`, as well.
 template <typename V>
 __device__ __forceinline__ void pool_piece(const PoolSet& set, int p, uint32_t piece, const int32_t* __restrict__ src,
-                                           const int32_t* __restrict__ dst, int i, int N, int P, bool share) {
+                                           const int32_t* __restrict__ dst, int i, int P, bool share, int served,
+                                           int end) {
   const uint64_t bytes = set.bytes[p], at = uint64_t(piece) * kPieceBytes;
   const int from = src[i];
   const bool clear = from < 0 || from >= P;
@@ -50,11 +65,13 @@ __device__ __forceinline__ void pool_piece(const PoolSet& set, int p, uint32_t p
   if (to >= 0 && to < P) put(to);
   if (!share || clear) return;
   const int lane = threadIdx.x & 63;
-  for (int j0 = i + 1; j0 < N; j0 += kWave) {
+  for (int j0 = i + 1; j0 < end; j0 += kWave) {
     const int j = j0 + lane;
-    const bool same = j < N && src[j] == from;
+    const bool same = j < end && src[j] == from;
     const int tj = same ? dst[j] : -1;
     uint64_t todo = __ballot(tj >= 0 && tj < P);
+    const uint64_t all = __ballot(same);
+    if (__popcll(all) > served) todo &= lowest(all, served);
     while (todo != 0) {
       const int l = __builtin_ctzll(todo);
       todo &= todo - 1;
@@ -70,26 +87,40 @@ __global__ __launch_bounds__(kThreads) void pool_copy_kernel(PoolSet set, const 
   const uint32_t at = blockIdx.x % pieces;
   const int from = src[i], to = dst[i], lane = threadIdx.x & 63;
   const bool clear = from < 0 || from >= P;
-  if (share && !clear) {  // the first row with this source does the work for all
-    for (int j0 = 0; j0 < i; j0 += kWave)
-      if (__ballot(j0 + lane < i && src[j0 + lane] == from) != 0) return;
+  int served = kShared, end = N;
+  if (share && !clear) {
+    // The first entry f with a source writes for the first kShared others in every 64
+    // entries behind it, and of the rest of those 64 every kShared-th for the ones up to
+    // the next: a fork into eight costs nine row moves, not sixteen.
+    for (int j0 = 0; j0 < i; j0 += kWave) {
+      const uint64_t same = __ballot(j0 + lane < i && src[j0 + lane] == from);
+      if (same == 0) continue;
+      const int f = j0 + __builtin_ctzll(same), first = i - (i - f - 1) % kWave;  // of i's 64
+      const int rank = __popcll(__ballot(first + lane < i && src[first + lane] == from));
+      if (rank == 0 || rank % kShared != 0) return;
+      served = kShared - 1;
+      end = first + kWave < N ? first + kWave : N;
+      break;
+    }
   } else if (to < 0 || to >= P) {
     return;
   }
   int p = 0;
   while (set.first[p + 1] <= at) ++p;
   const uint64_t odd = set.bytes[p] | reinterpret_cast<uintptr_t>(set.base[p]);
-  if ((odd & 15) == 0) pool_piece<u32x4>(set, p, at - set.first[p], src, dst, i, N, P, share);
-  else if ((odd & 3) == 0) pool_piece<uint32_t>(set, p, at - set.first[p], src, dst, i, N, P, share);
-  else pool_piece<uint16_t>(set, p, at - set.first[p], src, dst, i, N, P, share);
+  if ((odd & 15) == 0) pool_piece<u32x4>(set, p, at - set.first[p], src, dst, i, P, share, served, end);
+  else if ((odd & 3) == 0) pool_piece<uint32_t>(set, p, at - set.first[p], src, dst, i, P, share, served, end);
+  else pool_piece<uint16_t>(set, p, at - set.first[p], src, dst, i, P, share, served, end);
 }
 
 hipError_t launch_pool_copy(const PoolSet& set, const int32_t* src, const int32_t* dst, int N, int P, bool share,
                             hipStream_t s) {
   const int64_t wgs = int64_t(set.first[set.count]) * N;
+  uint64_t row = 0;  // bytes in all pools
+  for (int p = 0; p < set.count; ++p) row += set.bytes[p];
   if (wgs == 0) return hipSuccess;
   hipLaunchKernelGGL(pool_copy_kernel, dim3(unsigned(wgs)), dim3(kThreads), 0, s, set, src, dst, N, P,
-                     share && N <= kMaxShare ? 1 : 0);
+                     share && N <= kMaxShare && row * uint64_t(N) >= kMinShareBytes ? 1 : 0);
   return hipGetLastError();
 }
 

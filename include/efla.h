@@ -597,7 +597,7 @@ efla_status efla_ssm_bwd(const void *q, int64_t q_row, const void *k, int64_t k_
  * efla_pool_copy -- row src[i] of every pool to its row dst[i], i < N (int32,
  *     DEVICE memory): src[i] outside [0, P) clears row dst[i] to zero bytes, dst[i]
  *     outside [0, P) does nothing.  A source may be named often (a request forked
- *     into several: in lists of up to 512 entries it is read once).  The entries
+ *     into several: where much is written, eight or nine copies share a read).  The entries
  *     cannot be checked here: a row that is the destination of two entries, or a
  *     destination and a source, holds unspecified bytes afterwards, as does what is
  *     copied from it; no access leaves the pools.
