@@ -215,8 +215,10 @@ __global__ __launch_bounds__(kChain) void ssm_f32_kernel(SsmFwd a, float* __rest
 #pragma unroll
       for (int i = 0; i < OWN; ++i)
         if (sw + SW * i < DT) {
-          S[i] = all * S[i];
-          mma(S[i], lds_frag_t(Ks[b][0], KP, 16 * (sw + SW * i) + li, 0, g), wv);
+          f32x4 own = zero4();  // added once: eight steps onto S would round it eight times
+          mma(own, lds_frag_t(Ks[b][0], KP, 16 * (sw + SW * i) + li, 0, g), wv);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) S[i][e] = fmaf(all, S[i][e], own[e]);
         }
     }
     __syncthreads();
