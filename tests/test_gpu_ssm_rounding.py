@@ -10,7 +10,7 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 
 
-@pytest.mark.parametrize("dtype", [F32])
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("L,dk,dv", [(256, 64, 64), (1024, 128, 128), (2048, 128, 128), (2048, 64, 32), (2048, 128, 64)])
 @pytest.mark.parametrize("rates", [(-16.0, -1.0), (-2.0, -0.1)])
 def test_rate_gradient_of_positive_inputs(dtype, L, dk, dv, rates):
