@@ -429,15 +429,20 @@ static hipError_t conv_by_vector(bool aligned, F&& f) {
 
 static int64_t conv_blocks(int D, int V) { return (int64_t(D) + kWave * V - 1) / (kWave * V); }
 
-// Tokens a run: as long as there are `waves` wavefronts, up to 64, where the W - 1
-// rows that a run reads before its own cost little.  The gradient, whose registers
-// leave two wavefronts a SIMD, takes 2048 (8 x 2048 tokens of 2048 channels: runs of
-// 32 49 us, of 16 62 us), the forward pass 16384 (4 x 4096 tokens of 6144 channels: runs
-// of 8 75 us, of 16 81 us, of 32 86 us).
-static int conv_run(int64_t seqs, int64_t L, int64_t blocks, int64_t waves) {
-  for (int run = 64; run > 8; run /= 2)
-    if (seqs * ((L + run - 1) / run) * blocks >= waves) return run;
-  return 8;
+// Tokens a run of the forward pass: 8, whose windows overlap in the caches, and more only
+// where the launch would have more threads than the runtime takes.  us with runs of 8 /
+// 16 / 32 / 64, bf16, W = 4:
+//   1 x 2048 tokens, 2048 channels  8.3 / 10.1 / 14.7 / 26    8 x 2048, 2048  26.0 / 29.4 / 25.1 / 27.8
+//   4 x 4096, 6144  76 / 81 / 86 / 88                         8 x 4096, 6144  143 / 154 / 162 / 170
+//   16 x 8192, 4096  369 / 393 / 407 / 413                    1 x 65536, 1024  48.8 / 53.0 / 49.0 / 47.8
+// and float32:  4 x 4096, 6144  150 / 159 / 168 / 169         8 x 4096, 6144  288 / 305 / 326 / 329
+static int64_t conv_fwd_wgs(int64_t seqs, int64_t L, int64_t N, int64_t blocks, int run) {
+  return (N * blocks + 3) / 4 + seqs * ((L + 4 * run - 1) / (4 * run)) * blocks;
+}
+static int conv_fwd_run(int64_t seqs, int64_t L, int64_t N, int64_t blocks) {
+  int run = 8;
+  while (run < 64 && conv_fwd_wgs(seqs, L, N, blocks, run) * kThreads > kMaxLaunchThreads) run *= 2;
+  return run;
 }
 
 template <typename T>
@@ -447,9 +452,9 @@ hipError_t launch_conv_fwd(const ConvFwd& a, hipStream_t s) {
     return conv_by_vector<T>(aligned, [&](auto vc) {
       constexpr int W = decltype(wc)::value, V = decltype(vc)::value;
       const int64_t blocks = conv_blocks(a.D, V), seqs = a.cu != nullptr ? 1 : a.N;
-      const int run = conv_run(seqs, a.L, blocks, 16384);
+      const int run = conv_fwd_run(seqs, a.L, a.N, blocks);
       const int64_t seq_wgs = (a.N * blocks + 3) / 4;
-      const int64_t wgs = seq_wgs + (a.y == nullptr || a.L == 0 ? 0 : seqs * ((a.L + 4 * run - 1) / (4 * run)) * blocks);
+      const int64_t wgs = a.y == nullptr ? seq_wgs : conv_fwd_wgs(seqs, a.L, a.N, blocks, run);
       if (wgs == 0) return hipSuccess;
       hipLaunchKernelGGL((conv_fwd_kernel<T, V, W>), dim3(unsigned(wgs)), dim3(kThreads), 0, s, a, int(blocks),
                          int(seq_wgs), run);
@@ -475,9 +480,19 @@ hipError_t launch_conv_step(const ConvStep& a, hipStream_t s) {
 template hipError_t launch_conv_step<float>(const ConvStep&, hipStream_t);
 template hipError_t launch_conv_step<uint16_t>(const ConvStep&, hipStream_t);
 
-// Runs of the gradient, by one block count whatever the alignment, so that the
-// workspace does not depend on it.
-static int conv_bwd_run(int B, int64_t L, int D) { return conv_run(B, L, conv_blocks(D, 8), 2048); }
+// Tokens a run of the gradient, whose windows are longer and whose partial sums are one
+// row a workgroup: as long as there are 2048 wavefronts (its registers leave two a SIMD),
+// up to 64.  us with runs of 8 / 16 / 32 / 64, bf16, W = 4:
+//   1 x 2048 tokens, 2048 channels  18 / 24 / 34 / 59         8 x 2048, 2048  76 / 69 / 50 / 62
+//   1 x 4096, 6144  53 / 47 / 45 / 60 (takes 16)              4 x 4096, 6144  196 / 162 / 147 / 154 (64)
+//   8 x 4096, 6144  378 / 308 / 277 / 272                     1 x 65536, 1024  166 / 126 / 106 / 100
+// and float32:  8 x 2048, 2048  100 / 98 / 98 / 89 (32)       8 x 4096, 6144  502 / 489 / 498 / 507 (64)
+// By one block count whatever the alignment, so that the workspace does not depend on it.
+static int conv_bwd_run(int B, int64_t L, int D) {
+  for (int run = 64; run > 8; run /= 2)
+    if (B * ((L + run - 1) / run) * conv_blocks(D, 8) >= 2048) return run;
+  return 8;
+}
 size_t conv_bwd_workspace(int B, int64_t L, int D, int W) {
   const int run = conv_bwd_run(B, L, D);
   return size_t(B) * size_t((L + 4 * run - 1) / (4 * run)) * size_t(W + 1) * size_t(D) * sizeof(float);
@@ -485,8 +500,7 @@ size_t conv_bwd_workspace(int B, int64_t L, int D, int W) {
 // Threads of the largest launch over these sizes (one element a lane).
 int64_t conv_threads(int64_t seqs, int64_t L, int64_t N, int D) {
   const int64_t blocks = conv_blocks(D, 1);
-  const int run = conv_run(seqs, L, conv_blocks(D, 8), 16384);  // the shortest any of them takes
-  return ((N * blocks + 3) / 4 + seqs * ((L + 4 * run - 1) / (4 * run)) * blocks) * kThreads;
+  return conv_fwd_wgs(seqs, L, N, blocks, conv_fwd_run(seqs, L, N, blocks)) * kThreads;
 }
 
 int64_t conv_copy_threads(int64_t B, int D, int W) {

@@ -1,6 +1,6 @@
-"""The convolution where a wavefront takes runs of 16, 32 and 64 tokens: the largest power of
-two that leaves 16384 wavefronts in the forward pass, 2048 in the gradient.  Against a form in 64 bits over all
-tokens at once."""
+"""The convolution over many tokens, forward, packed and gradient, against a form in 64 bits
+over all tokens at once.  The gradient takes runs of 8 to 64 tokens a wavefront, the longest that leave 2048
+wavefronts; the forward pass 8, and more where the launch would have 2^32 threads."""
 import pytest
 import torch
 
@@ -11,9 +11,8 @@ pytestmark = pytest.mark.gpu
 BF, F32 = torch.bfloat16, torch.float32
 
 
-def run_of(seqs, L, D, vec, waves):
-    blocks = -(-D // (64 * vec))
-    return next((r for r in (64, 32, 16) if seqs * -(-L // r) * blocks >= waves), 8)
+def run_of(B, L, D):
+    return next((r for r in (64, 32, 16) if B * -(-L // r) * -(-D // 512) >= 2048), 8)
 
 
 def make(lead, D, W, dtype, seed):
@@ -24,15 +23,12 @@ def make(lead, D, W, dtype, seed):
     return n(*lead, D).to(dtype), (0.5 * n(D, W)).to(dtype), (0.5 * n(D)).to(dtype), n
 
 
-FORWARD = [(1, 262161, 40, 16), (3, 87399, 24, 16), (2, 262201, 40, 32), (1, 1048641, 8, 64), (5, 209800, 16, 64),
-           (2, 8199, 4101, 64)]
+FORWARD = [(1, 262161, 40), (3, 87399, 24), (2, 262201, 40), (1, 1048641, 8), (5, 209800, 16), (2, 8199, 4101)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("B,L,D,run", FORWARD)
-def test_forward(dtype, B, L, D, run):
-    vec = 1 if D % 8 else 16 // (2 if dtype == BF else 4)
-    assert run_of(B, L, D, vec, 16384) == run
+@pytest.mark.parametrize("B,L,D", FORWARD)
+def test_forward(dtype, B, L, D):
     x, w, bias, n = make((B, L), D, 4, dtype, L)
     s0 = n(B, 3, D).to(dtype)
     y, fin = efla.efla_conv_fwd(x, w, bias, s0)
@@ -45,11 +41,10 @@ def test_forward(dtype, B, L, D, run):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("T,D,W,longest,run", [(262300, 40, 4, 9, 16), (262300, 40, 3, 200, 16), (524500, 24, 4, 100, 32),
-                                               (1048800, 8, 4, 40, 64), (1048800, 8, 2, 70000, 64)])
-def test_packed(dtype, T, D, W, longest, run):
-    """Many short and empty sequences inside one run, and rows of none behind the last."""
-    assert run_of(1, T, D, 16 // (2 if dtype == BF else 4), 16384) == run
+@pytest.mark.parametrize("T,D,W,longest", [(262300, 40, 4, 9), (262300, 40, 3, 200), (524500, 24, 4, 100), (1048800, 8, 4, 40),
+                                           (1048800, 8, 2, 70000)])
+def test_packed(dtype, T, D, W, longest):
+    """Short and empty sequences inside one run, and rows of none behind the last."""
     gen = torch.Generator().manual_seed(T + W)
     lens = torch.randint(0, longest + 1, (2 * T // longest + 8,), generator=gen)
     lens[torch.rand(len(lens), generator=gen) < 0.1] = 0
@@ -79,6 +74,36 @@ def test_packed(dtype, T, D, W, longest, run):
     assert bool((out[rest] == 7.0).all())
 
 
+@pytest.mark.parametrize("L,packed", [(2 ** 29 + 77, False), (2 ** 30 + 5, True), (2 ** 31 - 9, False)])
+def test_launches_of_2_32_threads(L, packed):
+    """One channel, whose rows a wavefront moves one by one: runs of 16, 32 and 64 tokens."""
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(L, 1, dtype=BF, device="cuda")
+    step = 1 << 27
+    for at in range(0, L, step):
+        x[at:at + step] = torch.randn(min(step, L - at), 1, generator=gen, device="cuda").to(BF)
+    w, bias = torch.tensor([[0.3, -0.5, 0.25, 0.75]], device="cuda").to(BF), torch.tensor([0.125], device="cuda").to(BF)
+    state = torch.randn(3, 3, 1, generator=gen, device="cuda").to(BF)
+    cuts = [0, 5 * step + 3, L - 4] if packed else [0, L]  # two sequences and rows of none
+    if packed:
+        y, fin = torch.full_like(x, 3.0), None
+        _, fin = efla.efla_conv_fwd_varlen(x, w, torch.tensor(cuts, dtype=torch.int32, device="cuda"), bias, state[:2].contiguous(), y=y)
+        assert bool((y[cuts[-1]:] == 3.0).all())
+    else:
+        y, fin = efla.efla_conv_fwd(x[None], w, bias, state[:1].contiguous())
+        y = y[0]
+    wd = w[0].double()
+    for i, (first, end) in enumerate(zip(cuts, cuts[1:])):
+        assert torch.equal(fin[i], x[end - 3:end])
+        for at in range(first, end, step):
+            n = min(step, end - at)
+            full = torch.cat([state[i] if at == first else x[at - 3:at], x[at:at + n]])[:, 0].double()
+            u = bias.double() + sum(wd[j] * full[j:j + n] for j in range(4))
+            ry = u / (1 + torch.exp(-u))
+            assert R.rel(y[at:at + n, 0], ry) <= R.tol_conv(BF), (i, at)
+            del full, u, ry
+
+
 GRADIENT = [(2, 17001, 72, 16), (1, 32771, 512, 16), (3, 11003, 37, 16), (2, 33333, 72, 32), (1, 65601, 40, 32),
             (2, 66001, 24, 64), (8, 2049, 4096, 64), (1, 131073, 33, 64)]
 
@@ -88,7 +113,7 @@ GRADIENT = [(2, 17001, 72, 16), (1, 32771, 512, 16), (3, 11003, 37, 16), (2, 333
 def test_gradient(dtype, B, L, D, run):
     """dx and ds0 as in the short gradients.  dw and dbias are sums of B L terms: each is off by half a step of the
     absolute sum for its factors' 32 roundings, and by sqrt(B L) of the terms' root of squares for the summation."""
-    assert run_of(B, L, D, 8, 2048) == run
+    assert run_of(B, L, D) == run
     W = 4
     x, w, bias, n = make((B, L), D, W, dtype, L)
     s0, dy, dsf = n(B, 3, D).to(dtype), n(B, L, D).to(dtype), n(B, 3, D).to(dtype)
