@@ -96,7 +96,8 @@ __global__ __launch_bounds__(kThreads) void pool_copy_kernel(PoolSet set, const 
       const uint64_t same = __ballot(j0 + lane < i && src[j0 + lane] == from);
       if (same == 0) continue;
       const int f = j0 + __builtin_ctzll(same), first = i - (i - f - 1) % kWave;  // of i's 64
-      const int rank = __popcll(__ballot(first + lane < i && src[first + lane] == from));
+      const int rank = i <= j0 + kWave ? __popcll(same) - 1
+                                       : __popcll(__ballot(first + lane < i && src[first + lane] == from));
       if (rank == 0 || rank % kShared != 0) return;
       served = kShared - 1;
       end = first + kWave < N ? first + kWave : N;
