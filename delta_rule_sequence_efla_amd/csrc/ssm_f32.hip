@@ -18,7 +18,8 @@ constexpr int kChain = 2 * kThreads;  // threads of a workgroup of a chain
 
 // ROWS x COLS values of T (row t at src + t * stride) on their way to the LDS:
 // fetched into registers, widened and stored with a pitch; rows at or past
-// `valid` are zero, and so are columns COLS .. PITCH's multiple of 32.
+// `valid` are zero.  Columns from COLS on, which products over a head size of 16 read,
+// are left as they are: a kernel zeroes them, behind a barrier, before the first put.
 template <typename T, int COLS, int THREADS = kThreads>
 struct Tile {
   static constexpr int VE = 16 / sizeof(T), VPR = COLS / VE, N = kC * VPR, PER = cdiv(N, THREADS);
